@@ -96,6 +96,7 @@ typedef enum {
 #define PA_DEV_ERR_METADATA 0x4u  /* seq_len / query_start_loc inconsistent */
 #define PA_DEV_ERR_TIMEOUT 0x8u   /* a bounded pipeline wait ran out
                                      (pa_set_wait_limit_ns)                   */
+#define PA_DEV_ERR_NO_BLOCKS 0x10u /* pa_build_step ran out of free blocks   */
 
 /* The only block size supported: 16 tokens per physical block, the default
  * block size named in [Anatomy], "PagedAttention: paging the KV cache", and
@@ -366,6 +367,219 @@ pa_status pa_attention_cascade_workspace_size(int64_t num_tokens,
                                               int head_dim, int num_seqs,
                                               int max_query_len, int max_seq_len,
                                               size_t* bytes);
+
+/*
+ * pa_build_step -- a step's metadata on the GPU, from request lengths: the
+ * block tables extended by blocks popped from a stack of free ids, and the
+ * arrays that the other entry points read.  A decode loop that calls it needs
+ * no host work between steps and can be captured into a CUDA graph.
+ *
+ * Defines: the model runner turns {request: number of tokens} into query
+ * offsets, lengths, block tables and slots ([V1arch], "Scheduler forms one
+ * round of work"; [V0vsV1], section 3.1); position j of a request lives in
+ * block block_table[j / 16] at offset j % 16, and a block is taken from the
+ * pool when a request's tokens reach it ([Anatomy], Figure 2).
+ *
+ * For request r with n = query_lens[r] new tokens after c = computed_lens[r]:
+ *   need_r = ceil((c + n) / 16) - ceil(c / 16) blocks, popped in request order
+ *            (id = free_blocks[free_count - 1 - j] for the j-th of the step)
+ *            into entries ceil(c / 16) .. of its block-table row
+ *   r runs   if the needs of requests 0 .. r fit the stack and their tokens
+ *            fit num_tokens; both sums only grow, so those that run are the
+ *            first ones.  The others get no token and no block in this step
+ *            (PA_DEV_ERR_NO_BLOCKS, or PA_DEV_ERR_METADATA for the tokens).
+ *   seq_lens[r] = c + n, query_start_loc = running sum of n (n = 0 where r
+ *            does not run)
+ *   token t = query_start_loc[r] + i:  positions[t] = c + i, slot_mapping[t] =
+ *            block * 16 + (c + i) % 16
+ *   tokens past the last request's: position 0, slot -1 (padding)
+ *   *free_count_out = free_count less the blocks popped
+ *
+ * query_lens, computed_lens : device int32 [num_seqs].  A negative length, or
+ *            c + n beyond 16 * max_blocks_per_seq, sets PA_DEV_ERR_METADATA;
+ *            that request gets no token (and a c out of range counts as 0).
+ * block_tables : device int32 [num_seqs][max_blocks_per_seq], in and out:
+ *            entries below ceil(c / 16) are the request's blocks; entries past
+ *            ceil((c + n) / 16) are left as they were.
+ * free_blocks : device int32 [free_capacity], a stack of free ids whose top is
+ *            its last used entry; not changed (the caller pushes released ids
+ *            on top and raises the count).
+ * free_count : device int32, used entries of free_blocks (outside [0,
+ *            free_capacity]: PA_DEV_ERR_METADATA, no block is popped).
+ * An id outside [0, num_blocks), popped or in the table, sets
+ * PA_DEV_ERR_BLOCK_ID; the slots in it are -1.
+ * seq_lens may be computed_lens and free_count_out may be free_count (a loop's
+ * state updated in place); no other buffers may overlap.
+ * num_seqs <= 16384 (else PA_ERR_UNSUPPORTED), num_tokens < 2^31.
+ */
+pa_status pa_build_step(const int32_t* query_lens, const int32_t* computed_lens,
+                        int num_seqs, int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* free_blocks,
+                        int64_t free_capacity, const int32_t* free_count,
+                        int32_t* free_count_out, int64_t num_blocks,
+                        int block_size, int64_t num_tokens, int32_t* seq_lens,
+                        int32_t* query_start_loc, int32_t* positions,
+                        int64_t* slot_mapping, pa_stream_t stream);
+
+/*
+ * pa_norm_rope_and_cache -- RMS norm of each query and key head, the position
+ * rotation, and the K/V cache write, in one pass over the projection's output
+ * (no counterpart on the pages: what a model runs between its QKV projection
+ * and pa_attention).
+ *
+ * For token t at position positions[t], each query head and each key head x:
+ *   y = x / sqrt(mean(x^2) + eps) * w     (w = q_weight / k_weight; NULL: y = x)
+ *   for the first rotary_dim channels, in pairs (i, i + rotary_dim / 2) or,
+ *   interleaved != 0, (2i, 2i + 1), with cos, sin = cos_sin[position][i] and
+ *   [rotary_dim / 2 + i]:  (a, b) -> (a cos - b sin, b cos + a sin)
+ * in fp32, rounded once to dtype.  Queries go to q_out, keys and the
+ * unchanged values into the cache as pa_reshape_and_cache writes them (the
+ * same bits as that call on the rounded keys, except that a NaN may become
+ * another NaN).
+ *
+ * q, k, v    : device, dtype (PA_F32 / PA_F16 / PA_BF16); token t's row starts
+ *              at element t * q_stride (k_stride, v_stride); within a row,
+ *              [heads][head_dim] is contiguous, so slices of one QKV row do.
+ * q_weight, k_weight : device [head_dim] of weight_dtype (dtype or PA_F32).
+ * cos_sin    : device fp32 [max_position][rotary_dim], 16-byte aligned; a
+ *              position outside [0, max_position) sets PA_DEV_ERR_METADATA
+ *              and the token is skipped.  Not used, like positions, with
+ *              rotary_dim = 0.
+ * rotary_dim : 0, or a multiple of 16 up to head_dim (else
+ *              PA_ERR_UNSUPPORTED).
+ * q_out      : device [num_tokens][num_q_heads][head_dim], 16-byte aligned; may
+ *              be q itself when q_stride is num_q_heads * head_dim, otherwise
+ *              overlaps nothing.
+ * slot_mapping, caches, cache_dtype, scales : as pa_reshape_and_cache (16-byte
+ *              aligned caches); a token with a negative slot is padding:
+ *              nothing of it is read or written, its q_out row included, and
+ *              a token whose slot is out of range (PA_DEV_ERR_SLOT) is
+ *              skipped as well.
+ */
+pa_status pa_norm_rope_and_cache(
+    const void* q, const void* k, const void* v, pa_dtype dtype,
+    int64_t num_tokens, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+    const void* q_weight, const void* k_weight, pa_dtype weight_dtype, float eps,
+    const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved,
+    const int32_t* positions, void* q_out, void* k_cache, void* v_cache,
+    pa_dtype cache_dtype, int64_t num_blocks, int block_size, int num_q_heads,
+    int num_kv_heads, int head_dim, const int64_t* slot_mapping, float k_scale,
+    float v_scale, pa_stream_t stream);
+
+/*
+ * Sparse attention over selected blocks: for long contexts, each query reads
+ * the blocks whose keys can matter most instead of all of them (no counterpart
+ * on the pages; the same paged cache, tables and lengths as pa_attention).
+ *
+ *   pa_summarise_blocks    after a step's cache write: bounds of the keys of
+ *                          the blocks it wrote to
+ *   pa_select_blocks       the blocks of highest bound for each query and KV head
+ *   pa_attention_selected  attention over them
+ *
+ * The bounds of block b and KV head h are a record of PA_BOUNDS_BYTES(head_dim)
+ * bytes at bounds[b][h] (uint8 [num_blocks][num_kv_heads][PA_BOUNDS_BYTES]):
+ * head_dim int8 codes of the largest key value per channel, head_dim of the
+ * smallest, an fp32 scale s, 12 zero bytes:
+ *   s = fl32(max over the channels of max(|hi_d|, |lo_d|) / 127),
+ *   codes ceil(fl32(hi_d / s)) and floor(fl32(lo_d / s)) in [-127, 127]
+ *   (s = 0: codes 0),
+ * with hi_d, lo_d over the block's tokens written so far, as the cache holds
+ * them (without k_scale, which changes no order).  NaN keys are passed over
+ * and infinite ones count as the largest fp32 number.
+ */
+#define PA_BOUNDS_BYTES(head_dim) (2 * (head_dim) + 16)
+
+/*
+ * pa_summarise_blocks -- the records of the blocks this step's tokens were
+ * written to: for each request, blocks (L_r - n_r) / 16 .. (L_r - 1) / 16,
+ * each over its tokens 0 .. min(16, L_r - 16 b) - 1.  A call whose
+ * query_start_loc names all of a request's tokens as new (n_r = L_r) builds
+ * all of its records.  Step arguments and their checks as pa_attention.  A
+ * block copied by pa_copy_blocks gets its record with the next token written
+ * to it; until then the source's record holds for it too.
+ * bounds : device, 16-byte aligned; other records are left as they were.
+ */
+pa_status pa_summarise_blocks(const void* k_cache, pa_dtype cache_dtype,
+                              int64_t num_blocks, int block_size,
+                              int num_kv_heads, int head_dim,
+                              const int32_t* block_tables,
+                              int max_blocks_per_seq, const int32_t* seq_lens,
+                              const int32_t* query_start_loc, int num_seqs,
+                              int64_t num_tokens, int max_query_len,
+                              int max_seq_len, void* bounds,
+                              pa_stream_t stream);
+
+/*
+ * pa_select_blocks -- for each token and KV head, up to max_selected blocks of
+ * its request.
+ *
+ * A token at position p sees blocks 0 .. p / 16.  If these are at most
+ * max_selected, all are selected.  Otherwise the first keep_first and the last
+ * keep_last are, and of the others those of the highest score, ties to the
+ * lower block:
+ *   qc_d  = nearest integer (ties to even) to fl32(q_d / sq), in [-127, 127],
+ *           sq = fl32(max |q| over the query heads of the KV head / 127)
+ *   score = fl32(s * max over these heads of
+ *                    sum_d qc_d * (qc_d >= 0 ? hi_d : lo_d))
+ * with the block's codes hi, lo and scale s.  The sum is one of whole numbers:
+ * equal inputs select equal blocks whatever the batch around them.
+ *
+ * q            : device [num_tokens][num_q_heads][head_dim] of q_dtype
+ *                (PA_F32 / PA_F16 / PA_BF16), 16-byte aligned.
+ * keep_first >= 0, keep_last >= 1, keep_first + keep_last <= max_selected.
+ * selected     : device int32 [num_tokens][num_kv_heads][max_selected], the
+ *                blocks' indices in the request's block table in ascending
+ *                order, then -1.
+ * num_selected : device int32 [num_tokens][num_kv_heads].
+ * Rows of tokens that belong to no request are left as they were.
+ * The step's arguments and their checks as pa_attention; workspace as there,
+ * of pa_select_blocks_workspace_size bytes (at most 48 MiB, or one token's
+ * scores if they are more).
+ */
+pa_status pa_select_blocks_workspace_size(int64_t num_tokens, int num_kv_heads,
+                                          int max_seq_len, size_t* bytes);
+pa_status pa_select_blocks(const void* q, pa_dtype q_dtype, const void* bounds,
+                           int64_t num_blocks, int block_size, int num_q_heads,
+                           int num_kv_heads, int head_dim,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* seq_lens,
+                           const int32_t* query_start_loc, int num_seqs,
+                           int64_t num_tokens, int max_query_len,
+                           int max_seq_len, int max_selected, int keep_first,
+                           int keep_last, int32_t* selected,
+                           int32_t* num_selected, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_attention_selected -- pa_attention over the listed blocks only: the query
+ * head h of token t at position p sees the keys 16 b .. min(16 b + 15, p) of
+ * the blocks b listed for (t, KV head of h).  An empty list gives zeros.
+ *
+ * selected, num_selected : as pa_select_blocks leaves them, or the caller's
+ * own: row (t, KV head) has num_selected entries in strictly ascending order,
+ * each at most p / 16.  An entry that is not above the one before it or lies
+ * past the token's block is skipped, and a count outside [0, max_selected]
+ * gives zeros; both set PA_DEV_ERR_METADATA.
+ * Other arguments, types, results and checks as pa_attention (every cache type
+ * it takes; an entry whose physical block id is out of range is skipped with
+ * PA_DEV_ERR_BLOCK_ID).  The workspace must hold
+ * pa_attention_selected_workspace_size bytes for the same sizes.
+ * Results are bitwise deterministic from run to run.
+ */
+pa_status pa_attention_selected_workspace_size(int64_t num_tokens,
+                                               int num_q_heads,
+                                               int num_kv_heads, int head_dim,
+                                               int max_selected, size_t* bytes);
+pa_status pa_attention_selected(
+    const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,
+    pa_dtype cache_dtype, int64_t num_blocks, int block_size, int num_q_heads,
+    int num_kv_heads, int head_dim, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* seq_lens,
+    const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+    int max_query_len, int max_seq_len, const int32_t* selected,
+    const int32_t* num_selected, int max_selected, float scale, float k_scale,
+    float v_scale, void* out, void* workspace, size_t workspace_bytes,
+    pa_stream_t stream);
 
 /*
  * pa_set_wait_limit_ns -- the longest one pipeline wait inside the attention

@@ -12,6 +12,10 @@ calls raise; nothing falls back.
     pa_copy_blocks        -- block-granular copy-on-write
     pa_attention          -- unified decode + chunked-prefill paged attention
     pa_attention_workspace_size, pa_get_device_error
+    pa_build_step         -- a step's metadata on the GPU, from request lengths
+    pa_norm_rope_and_cache -- q/k norm per head, position rotation, K/V write
+    pa_summarise_blocks, pa_select_blocks, pa_attention_selected -- attention
+                             over the blocks that a cheap score selects
 """
 from __future__ import annotations
 
@@ -30,7 +34,7 @@ PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_DEVICE = \
     range(5)
 PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT4, PA_NVFP4 = range(6)
 PA_DEV_ERR_SLOT, PA_DEV_ERR_BLOCK_ID, PA_DEV_ERR_METADATA, \
-    PA_DEV_ERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+    PA_DEV_ERR_TIMEOUT, PA_DEV_ERR_NO_BLOCKS = 0x1, 0x2, 0x4, 0x8, 0x10
 BLOCK_SIZE = 16
 
 EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_copy_blocks",
@@ -40,7 +44,10 @@ EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_copy_blocks",
             "pa_set_debug_bounds", "pa_attention_window",
             "pa_attention_window_workspace_size", "pa_set_wait_limit_ns",
             "pa_test_skip_copy", "pa_attention_cascade",
-            "pa_attention_cascade_workspace_size")
+            "pa_attention_cascade_workspace_size", "pa_build_step",
+            "pa_norm_rope_and_cache", "pa_summarise_blocks",
+            "pa_select_blocks_workspace_size", "pa_select_blocks",
+            "pa_attention_selected_workspace_size", "pa_attention_selected")
 
 _DT = {"f32": PA_F32, "f16": PA_F16, "bf16": PA_BF16, "e4m3": PA_FP8_E4M3,
        "int4": PA_INT4, "nvfp4": PA_NVFP4}
@@ -50,6 +57,12 @@ def page_bytes_4bit(cache_dtype: str, head_dim: int) -> int:
     """PA_PAGE_BYTES of pa.h: bytes of one (block, KV head) page of a 4-bit
     cache (int4: codes + 16 fp32 scales; nvfp4: codes + E4M3 block scales)."""
     return 8 * head_dim + (64 if cache_dtype == "int4" else head_dim)
+
+
+def bounds_bytes(head_dim: int) -> int:
+    """PA_BOUNDS_BYTES of pa.h: bytes of one (block, KV head) record of key
+    bounds; a bounds tensor is uint8 [num_blocks, Hkv, bounds_bytes(D)]."""
+    return 2 * head_dim + 16
 
 
 def _cache_geometry(cache: torch.Tensor, cache_dtype: Optional[str],
@@ -138,6 +151,30 @@ def load_library(path: str = LIB_PATH):
                                          i32, P, i32, P, P, i32, i64, i32, i32,
                                          f32, f32, f32, P, P]
     lib.pa_attention_noalloc.restype = i32
+    lib.pa_build_step.argtypes = [P, P, i32, P, i32, P, i64, P, P, i64, i32,
+                                  i64, P, P, P, P, P]
+    lib.pa_build_step.restype = i32
+    lib.pa_norm_rope_and_cache.argtypes = [
+        P, P, P, i32, i64, i64, i64, i64, P, P, i32, f32, P, i64, i32, i32, P,
+        P, P, P, i32, i64, i32, i32, i32, i32, P, f32, f32, P]
+    lib.pa_norm_rope_and_cache.restype = i32
+    lib.pa_summarise_blocks.argtypes = [P, i32, i64, i32, i32, i32, P, i32, P,
+                                        P, i32, i64, i32, i32, P, P]
+    lib.pa_summarise_blocks.restype = i32
+    lib.pa_select_blocks_workspace_size.argtypes = [i64, i32, i32,
+                                                    ctypes.POINTER(sz)]
+    lib.pa_select_blocks_workspace_size.restype = i32
+    lib.pa_select_blocks.argtypes = [P, i32, P, i64, i32, i32, i32, i32, P, i32,
+                                     P, P, i32, i64, i32, i32, i32, i32, i32, P,
+                                     P, P, sz, P]
+    lib.pa_select_blocks.restype = i32
+    lib.pa_attention_selected_workspace_size.argtypes = [
+        i64, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.pa_attention_selected_workspace_size.restype = i32
+    lib.pa_attention_selected.argtypes = [
+        P, i32, P, P, i32, i64, i32, i32, i32, i32, P, i32, P, P, i32, i64, i32,
+        i32, P, P, i32, f32, f32, f32, P, P, sz, P]
+    lib.pa_attention_selected.restype = i32
     _lib = lib
     return lib
 
@@ -466,4 +503,295 @@ def pa_attention_noalloc(q: torch.Tensor, k_cache: torch.Tensor,
            int(max_seq_len), float(scale), float(k_scale), float(v_scale),
            _dev(out, "out"), _stream(stream))
     _check(st, "pa_attention_noalloc")
+    return out
+
+
+def _here(**tensors) -> None:
+    """The tensors (None: absent) are on the current CUDA device, where the
+    library launches."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _ints(t: torch.Tensor, name: str, n: int, dtype=torch.int32) -> torch.Tensor:
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+    return t
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def pa_build_step(query_lens: torch.Tensor, computed_lens: torch.Tensor,
+                  block_tables: torch.Tensor, free_blocks: torch.Tensor,
+                  free_count: torch.Tensor, num_blocks: int, num_tokens: int,
+                  seq_lens: Optional[torch.Tensor] = None,
+                  query_start_loc: Optional[torch.Tensor] = None,
+                  positions: Optional[torch.Tensor] = None,
+                  slot_mapping: Optional[torch.Tensor] = None,
+                  free_count_out: Optional[torch.Tensor] = None, stream=None):
+    """query_lens, computed_lens int32 [B]; block_tables int32 [B, M] (extended
+    in place); free_blocks int32 [F], a stack of free ids; free_count int32
+    [1].  Returns (seq_lens int32 [B], query_start_loc int32 [B+1], positions
+    int32 [num_tokens], slot_mapping int64 [num_tokens], free_count_out int32
+    [1]), allocated where not given; seq_lens may be computed_lens and
+    free_count_out may be free_count (updated in place)."""
+    if block_tables.dim() != 2 or block_tables.dtype != torch.int32 \
+            or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [B, M] tensor")
+    B, M = block_tables.shape
+    T = int(num_tokens)
+    _ints(query_lens, "query_lens", B)
+    _ints(computed_lens, "computed_lens", B)
+    _ints(free_blocks, "free_blocks", free_blocks.numel())
+    _ints(free_count, "free_count", 1)
+    dev = block_tables.device
+
+    def out(t, name, n, dtype=torch.int32):
+        if t is None:
+            return torch.empty(n, dtype=dtype, device=dev)
+        return _ints(t, name, n, dtype)
+    seq_lens = out(seq_lens, "seq_lens", B)
+    query_start_loc = out(query_start_loc, "query_start_loc", B + 1)
+    positions = out(positions, "positions", T)
+    slot_mapping = out(slot_mapping, "slot_mapping", T, torch.int64)
+    free_count_out = out(free_count_out, "free_count_out", 1)
+    _here(query_lens=query_lens, computed_lens=computed_lens,
+          block_tables=block_tables, free_blocks=free_blocks,
+          free_count=free_count, seq_lens=seq_lens,
+          query_start_loc=query_start_loc, positions=positions,
+          slot_mapping=slot_mapping, free_count_out=free_count_out)
+    st = _load().pa_build_step(
+        query_lens.data_ptr(), computed_lens.data_ptr(), B,
+        block_tables.data_ptr(), M, free_blocks.data_ptr(), free_blocks.numel(),
+        free_count.data_ptr(), free_count_out.data_ptr(), int(num_blocks),
+        BLOCK_SIZE, T, seq_lens.data_ptr(), query_start_loc.data_ptr(),
+        positions.data_ptr(), slot_mapping.data_ptr(), _stream(stream))
+    _check(st, "pa_build_step")
+    return seq_lens, query_start_loc, positions, slot_mapping, free_count_out
+
+
+def pa_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor,
+                           value: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                           positions: Optional[torch.Tensor] = None,
+                           cos_sin: Optional[torch.Tensor] = None,
+                           q_weight: Optional[torch.Tensor] = None,
+                           k_weight: Optional[torch.Tensor] = None,
+                           eps: float = 1e-6, interleaved: bool = False,
+                           k_scale: float = 1.0, v_scale: float = 1.0,
+                           q_out: Optional[torch.Tensor] = None,
+                           cache_dtype: Optional[str] = None,
+                           stream=None) -> torch.Tensor:
+    """q [T, Hq, D], key/value [T, Hkv, D] (rows may be slices of one QKV row);
+    positions int32 [T] and cos_sin fp32 [max_position, rotary_dim] (cosines,
+    then sines; None: no rotation); q_weight / k_weight [D] (None: no norm).
+    Writes the caches and returns q_out [T, Hq, D] (q itself if given as such
+    and contiguous)."""
+    if q.dim() != 3 or key.dim() != 3 or value.shape != key.shape \
+            or q.shape[0] != key.shape[0] or q.shape[2] != key.shape[2]:
+        raise ValueError("q must be [T, Hq, D] and key/value [T, Hkv, D]")
+    T, Hq, D = q.shape
+    Hkv = key.shape[1]
+    if key.dtype != q.dtype or value.dtype != q.dtype:
+        raise ValueError("q, key and value must be of one type")
+    for t, n in ((q, "q"), (key, "key"), (value, "value")):
+        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+            raise ValueError(f"{n} must have contiguous rows")
+    _ints(slot_mapping, "slot_mapping", T, torch.int64)
+    NB, Hc, bs, Dc = _cache_geometry(k_cache, cache_dtype, D)
+    if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape \
+            or v_cache.dtype != k_cache.dtype:
+        raise ValueError("cache shape does not match key/value")
+    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("the caches must be contiguous")
+    span = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 \
+                or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous fp32 "
+                             "[max_position, rotary_dim] tensor")
+        span, rot = cos_sin.shape
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _ints(positions, "positions", T)
+    wdt = None
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is None:
+            continue
+        if t.numel() != D or not t.is_contiguous() or (wdt or t.dtype) != t.dtype:
+            raise ValueError(f"{n} must be a contiguous [D] tensor, both of one type")
+        wdt = t.dtype
+    wcode = PA_F32 if wdt is None else _dtype_code(q_weight if q_weight is not None
+                                                   else k_weight)
+    if q_out is None:
+        q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+        raise ValueError("q_out must be a contiguous tensor like q")
+    _here(q=q, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
+          slot_mapping=slot_mapping, positions=positions, cos_sin=cos_sin,
+          q_weight=q_weight, k_weight=k_weight, q_out=q_out)
+    st = _load().pa_norm_rope_and_cache(
+        q.data_ptr(), key.data_ptr(), value.data_ptr(), _dtype_code(q), T,
+        _row_stride(q), _row_stride(key), _row_stride(value), _ptr(q_weight),
+        _ptr(k_weight), wcode, float(eps), _ptr(cos_sin), span, rot,
+        1 if interleaved else 0, _ptr(positions), q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache, cache_dtype),
+        NB, bs, Hq, Hkv, D, slot_mapping.data_ptr(), float(k_scale),
+        float(v_scale), _stream(stream))
+    _check(st, "pa_norm_rope_and_cache")
+    return q_out
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from one token's row to the next (of a single token: any)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _bounds_shape(bounds: torch.Tensor, NB, Hkv: int, D: int) -> int:
+    if bounds.dtype != torch.uint8 or bounds.dim() != 3 or not bounds.is_contiguous() \
+            or tuple(bounds.shape[1:]) != (Hkv, bounds_bytes(D)) \
+            or (NB is not None and bounds.shape[0] != NB):
+        raise ValueError("bounds must be a contiguous uint8 [num_blocks, Hkv, "
+                         "bounds_bytes(D)] tensor")
+    return bounds.shape[0]
+
+
+def _step_ints(block_tables, seq_lens, query_start_loc) -> int:
+    B = seq_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("inconsistent number of sequences")
+    _ints(block_tables, "block_tables", block_tables.numel())
+    _ints(seq_lens, "seq_lens", B)
+    _ints(query_start_loc, "query_start_loc", B + 1)
+    return B
+
+
+def pa_summarise_blocks(k_cache: torch.Tensor, bounds: torch.Tensor,
+                        block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                        query_start_loc: torch.Tensor, num_tokens: int,
+                        max_query_len: int, max_seq_len: int,
+                        cache_dtype: Optional[str] = None, stream=None) -> None:
+    """Key bounds of the blocks this step's tokens were written to, into bounds
+    (uint8 [num_blocks, Hkv, bounds_bytes(D)])."""
+    NB, Hkv, bs, D = _cache_geometry(k_cache, cache_dtype)
+    if not k_cache.is_contiguous():
+        raise ValueError("k_cache must be contiguous")
+    _bounds_shape(bounds, NB, Hkv, D)
+    B = _step_ints(block_tables, seq_lens, query_start_loc)
+    _here(k_cache=k_cache, bounds=bounds, block_tables=block_tables,
+          seq_lens=seq_lens, query_start_loc=query_start_loc)
+    st = _load().pa_summarise_blocks(
+        k_cache.data_ptr(), _dtype_code(k_cache, cache_dtype), NB, bs, Hkv, D,
+        block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+        query_start_loc.data_ptr(), B, int(num_tokens), int(max_query_len),
+        int(max_seq_len), bounds.data_ptr(), _stream(stream))
+    _check(st, "pa_summarise_blocks")
+
+
+def pa_select_blocks_workspace_size(num_tokens: int, num_kv_heads: int,
+                                    max_seq_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    st = _load().pa_select_blocks_workspace_size(num_tokens, num_kv_heads,
+                                                 max_seq_len, ctypes.byref(out))
+    _check(st, "pa_select_blocks_workspace_size")
+    return int(out.value)
+
+
+def pa_select_blocks(q: torch.Tensor, bounds: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     query_start_loc: torch.Tensor, max_query_len: int,
+                     max_seq_len: int, max_selected: int, keep_first: int = 1,
+                     keep_last: int = 1,
+                     selected: Optional[torch.Tensor] = None,
+                     num_selected: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """q [T, Hq, D]; bounds as pa_summarise_blocks leaves them.  Returns
+    (selected int32 [T, Hkv, max_selected], num_selected int32 [T, Hkv])."""
+    if q.dim() != 3 or not q.is_contiguous() or bounds.dim() != 3:
+        raise ValueError("q must be a contiguous [T, Hq, D] tensor")
+    T, Hq, D = q.shape
+    Hkv, K = bounds.shape[1], int(max_selected)
+    NB = _bounds_shape(bounds, None, Hkv, D)
+    B = _step_ints(block_tables, seq_lens, query_start_loc)
+    if selected is None:
+        selected = torch.empty(T, Hkv, K, dtype=torch.int32, device=q.device)
+    if num_selected is None:
+        num_selected = torch.empty(T, Hkv, dtype=torch.int32, device=q.device)
+    _ints(selected, "selected", T * Hkv * K)
+    _ints(num_selected, "num_selected", T * Hkv)
+    if workspace is None:
+        n = pa_select_blocks_workspace_size(T, Hkv, int(max_seq_len))
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    _here(q=q, bounds=bounds, block_tables=block_tables, seq_lens=seq_lens,
+          query_start_loc=query_start_loc, selected=selected,
+          num_selected=num_selected, workspace=workspace)
+    st = _load().pa_select_blocks(
+        q.data_ptr(), _dtype_code(q), bounds.data_ptr(), NB, BLOCK_SIZE, Hq, Hkv,
+        D, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+        query_start_loc.data_ptr(), B, T, int(max_query_len), int(max_seq_len), K,
+        int(keep_first), int(keep_last), selected.data_ptr(),
+        num_selected.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_select_blocks")
+    return selected, num_selected
+
+
+def pa_attention_selected_workspace_size(num_tokens: int, num_q_heads: int,
+                                         num_kv_heads: int, head_dim: int,
+                                         max_selected: int) -> int:
+    out = ctypes.c_size_t(0)
+    st = _load().pa_attention_selected_workspace_size(
+        num_tokens, num_q_heads, num_kv_heads, head_dim, max_selected,
+        ctypes.byref(out))
+    _check(st, "pa_attention_selected_workspace_size")
+    return int(out.value)
+
+
+def pa_attention_selected(q: torch.Tensor, k_cache: torch.Tensor,
+                          v_cache: torch.Tensor, block_tables: torch.Tensor,
+                          seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                          max_query_len: int, max_seq_len: int, scale: float,
+                          selected: torch.Tensor, num_selected: torch.Tensor,
+                          k_scale: float = 1.0, v_scale: float = 1.0,
+                          out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None,
+                          cache_dtype: Optional[str] = None,
+                          stream=None) -> torch.Tensor:
+    """pa_attention over the listed blocks only: selected int32 [T, Hkv, K] in
+    ascending order per row, num_selected int32 [T, Hkv]."""
+    T, Hq, D, NB, Hkv, bs, B = _step_shapes(q, k_cache, v_cache, block_tables,
+                                            seq_lens, query_start_loc, out,
+                                            cache_dtype)
+    if selected.dim() != 3 or tuple(selected.shape[:2]) != (T, Hkv):
+        raise ValueError("selected must be [T, Hkv, K]")
+    K = selected.shape[2]
+    _ints(selected, "selected", T * Hkv * K)
+    _ints(num_selected, "num_selected", T * Hkv)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        n = pa_attention_selected_workspace_size(T, Hq, Hkv, D, K)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    _here(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+          seq_lens=seq_lens, query_start_loc=query_start_loc, selected=selected,
+          num_selected=num_selected, out=out, workspace=workspace)
+    st = _load().pa_attention_selected(
+        q.data_ptr(), _dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(),
+        _dtype_code(k_cache, cache_dtype), NB, bs, Hq, Hkv, D,
+        block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+        query_start_loc.data_ptr(), B, T, int(max_query_len), int(max_seq_len),
+        selected.data_ptr(), num_selected.data_ptr(), K, float(scale),
+        float(k_scale), float(v_scale), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_attention_selected")
     return out

@@ -605,3 +605,387 @@ pa_status pa_get_device_error(pa_stream_t stream, uint32_t* flags) {
 }
 
 }  // extern "C"
+
+// ---- sparse decode step: metadata, norm + rotation + write, selection --------
+
+namespace {
+
+// the checks that every call taking a step's metadata makes; done: nothing to do
+pa_status step_status(const StepView& s, bool* done) {
+  *done = false;
+  if (s.num_seqs < 0 || s.num_tokens < 0 || s.max_query_len < 0 ||
+      s.max_seq_len < 0 || s.max_blocks_per_seq < 0)
+    return PA_ERR_INVALID_ARG;
+  if (s.num_seqs == 0 || s.num_tokens == 0 || s.max_query_len == 0 ||
+      s.max_seq_len == 0) {
+    *done = true;
+    return PA_OK;
+  }
+  if ((int64_t)s.max_blocks_per_seq * PA_BLOCK_SIZE < s.max_seq_len)
+    return PA_ERR_INVALID_ARG;
+  if (!s.block_tables || !s.seq_lens || !s.query_start_loc ||
+      !aligned(s.block_tables, 4) || !aligned(s.seq_lens, 4) ||
+      !aligned(s.query_start_loc, 4))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+bool is_scale(float x) { return isfinite(x) && x > 0; }
+
+bool scaled_type(pa_dtype t) { return t == PA_FP8_E4M3 || t == PA_NVFP4; }
+
+bool plain_type(int t) { return t == PA_F32 || t == PA_F16 || t == PA_BF16; }
+
+// true if any of the `outs` overlaps another buffer of the list
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool any_overlap(const Span* outs, int n_outs, const Span* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+    for (int j = 0; j < n_ins; ++j)
+      if (overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_build_step(const int32_t* query_lens, const int32_t* computed_lens,
+                        int num_seqs, int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* free_blocks,
+                        int64_t free_capacity, const int32_t* free_count,
+                        int32_t* free_count_out, int64_t num_blocks,
+                        int block_size, int64_t num_tokens, int32_t* seq_lens,
+                        int32_t* query_start_loc, int32_t* positions,
+                        int64_t* slot_mapping, pa_stream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 0 || free_capacity < 0 ||
+      num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (block_size != PA_BLOCK_SIZE || num_seqs > kMaxBuildSeqs ||
+      num_tokens >= (1ll << 31) || num_blocks >= (1ll << 31) ||
+      free_capacity >= (1ll << 31) ||
+      (int64_t)max_blocks_per_seq * PA_BLOCK_SIZE >= (1ll << 31))
+    return PA_ERR_UNSUPPORTED;
+  const void* i32[] = {query_lens, computed_lens, block_tables, free_blocks, free_count,
+                       free_count_out, seq_lens, query_start_loc, positions};
+  for (const void* p : i32)
+    if (!aligned(p, 4)) return PA_ERR_INVALID_ARG;
+  if (!free_count || !free_count_out || !query_start_loc || !aligned(slot_mapping, 8) ||
+      (free_capacity > 0 && !free_blocks) ||
+      (num_tokens > 0 && (!positions || !slot_mapping)) ||
+      (num_seqs > 0 && (!query_lens || !computed_lens || !seq_lens ||
+                        (max_blocks_per_seq > 0 && !block_tables))))
+    return PA_ERR_INVALID_ARG;
+  const size_t b = (size_t)num_seqs * 4, t = (size_t)num_tokens;
+  const Span outs[] = {{block_tables, b * max_blocks_per_seq},
+                       {free_count_out, 4},
+                       {seq_lens, b},
+                       {query_start_loc, b + 4},
+                       {positions, t * 4},
+                       {slot_mapping, t * 8}};
+  const Span ins[] = {{query_lens, b},
+                      {free_blocks, (size_t)free_capacity * 4},
+                      {computed_lens == seq_lens ? nullptr : computed_lens, b},
+                      {free_count == free_count_out ? nullptr : free_count, 4}};
+  if (any_overlap(outs, 6, ins, 4)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  const cudaError_t e = launch_build_step(
+      query_lens, computed_lens, num_seqs, block_tables, max_blocks_per_seq, free_blocks,
+      free_capacity, free_count, free_count_out, num_blocks, num_tokens, seq_lens,
+      query_start_loc, positions, slot_mapping, di->err,
+      reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_norm_rope_and_cache(
+    const void* q, const void* k, const void* v, pa_dtype dtype,
+    int64_t num_tokens, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+    const void* q_weight, const void* k_weight, pa_dtype weight_dtype, float eps,
+    const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved,
+    const int32_t* positions, void* q_out, void* k_cache, void* v_cache,
+    pa_dtype cache_dtype, int64_t num_blocks, int block_size, int num_q_heads,
+    int num_kv_heads, int head_dim, const int64_t* slot_mapping, float k_scale,
+    float v_scale, pa_stream_t stream) {
+  if (!valid_dtype(dtype) || !valid_dtype(cache_dtype) || num_tokens < 0 ||
+      num_q_heads <= 0 || rotary_dim < 0 || max_position < 0)
+    return PA_ERR_INVALID_ARG;
+  if (pa_status st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim))
+    return st;
+  if (!plain_type(dtype)) return PA_ERR_UNSUPPORTED;
+  if (cache_dtype != dtype && cache_dtype != PA_FP8_E4M3 && !is_4bit(cache_dtype))
+    return PA_ERR_UNSUPPORTED;
+  if (scaled_type(cache_dtype) && !(is_scale(k_scale) && is_scale(v_scale)))
+    return PA_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0 || rotary_dim > head_dim) return PA_ERR_UNSUPPORTED;
+  if (q_weight || k_weight) {
+    if (!valid_dtype(weight_dtype) || !isfinite(eps) || eps < 0) return PA_ERR_INVALID_ARG;
+    if (weight_dtype != dtype && weight_dtype != PA_F32) return PA_ERR_UNSUPPORTED;
+  }
+  const int64_t q_row = (int64_t)num_q_heads * head_dim;
+  const int64_t kv_row = (int64_t)num_kv_heads * head_dim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
+    return PA_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !k || !v || !q_out || !slot_mapping) return PA_ERR_INVALID_ARG;
+  if (rotary_dim > 0 && (!cos_sin || !positions || !aligned(cos_sin, 16) ||
+                         !aligned(positions, 4)))
+    return PA_ERR_INVALID_ARG;
+  const size_t eb = (size_t)elem_bytes(dtype);
+  const size_t wb = plain_type(weight_dtype) ? (size_t)elem_bytes(weight_dtype) : 1;
+  if (!aligned(q, eb) || !aligned(k, eb) || !aligned(v, eb) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8) ||
+      !aligned(q_weight, wb) || !aligned(k_weight, wb))
+    return PA_ERR_INVALID_ARG;
+  const size_t n1 = (size_t)(num_tokens - 1);
+  const Span q_in{q, (n1 * q_stride + q_row) * eb};
+  const size_t cache_bytes =
+      (size_t)num_blocks * num_kv_heads * page_bytes(cache_dtype, head_dim);
+  const Span outs[] = {{q_out, (size_t)num_tokens * q_row * eb},
+                       {k_cache, cache_bytes},
+                       {v_cache, cache_bytes}};
+  // q itself may be the output; it then still has to be clear of the caches
+  const bool in_place = q_out == q && q_stride == q_row;
+  const Span ins[] = {{k, (n1 * k_stride + kv_row) * eb},
+                      {v, (n1 * v_stride + kv_row) * eb},
+                      {q_weight, (size_t)head_dim * wb},
+                      {k_weight, (size_t)head_dim * wb},
+                      {rotary_dim ? cos_sin : nullptr,
+                       (size_t)max_position * rotary_dim * 4},
+                      {rotary_dim ? positions : nullptr, (size_t)num_tokens * 4},
+                      {slot_mapping, (size_t)num_tokens * 8},
+                      {in_place ? nullptr : q, q_in.n}};
+  if (any_overlap(outs, 3, ins, 8)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  RopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.dtype = dtype;
+  a.num_tokens = num_tokens;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.weight_dtype = weight_dtype;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_position = max_position;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.positions = positions;
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.cache_dtype = cache_dtype;
+  a.num_blocks = num_blocks;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.slot_mapping = slot_mapping;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.vector_ok = aligned(q, 16) && aligned(k, 16) && aligned(v, 16) &&
+                q_stride * eb % 16 == 0 && k_stride * eb % 16 == 0 &&
+                v_stride * eb % 16 == 0;
+  const cudaError_t e =
+      launch_norm_rope_and_cache(a, di->err, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_summarise_blocks(const void* k_cache, pa_dtype cache_dtype,
+                              int64_t num_blocks, int block_size,
+                              int num_kv_heads, int head_dim,
+                              const int32_t* block_tables,
+                              int max_blocks_per_seq, const int32_t* seq_lens,
+                              const int32_t* query_start_loc, int num_seqs,
+                              int64_t num_tokens, int max_query_len,
+                              int max_seq_len, void* bounds,
+                              pa_stream_t stream) {
+  if (!valid_dtype(cache_dtype)) return PA_ERR_INVALID_ARG;
+  if (pa_status st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim))
+    return st;
+  StepView s{block_tables,  max_blocks_per_seq, seq_lens,    query_start_loc, num_seqs,
+             num_tokens,    max_query_len,      max_seq_len, num_blocks,      nullptr};
+  bool done;
+  if (pa_status st = step_status(s, &done)) return st;
+  if (done) return PA_OK;
+  if (!k_cache || !bounds || !aligned(k_cache, 16) || !aligned(bounds, 16))
+    return PA_ERR_INVALID_ARG;
+  const size_t pages = (size_t)num_blocks * num_kv_heads;
+  const Span outs[] = {{bounds, pages * PA_BOUNDS_BYTES(head_dim)}};
+  const Span ins[] = {{k_cache, pages * page_bytes(cache_dtype, head_dim)},
+                      {block_tables, (size_t)num_seqs * max_blocks_per_seq * 4},
+                      {seq_lens, (size_t)num_seqs * 4},
+                      {query_start_loc, (size_t)num_seqs * 4 + 4}};
+  if (any_overlap(outs, 1, ins, 4)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  s.err = di->err;
+  const cudaError_t e =
+      launch_summarise_blocks(s, k_cache, cache_dtype, num_kv_heads, head_dim, bounds,
+                              reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_select_blocks_workspace_size(int64_t num_tokens, int num_kv_heads,
+                                          int max_seq_len, size_t* bytes) {
+  if (!bytes || num_tokens < 0 || num_kv_heads <= 0 || max_seq_len < 0)
+    return PA_ERR_INVALID_ARG;
+  *bytes = (size_t)make_select_plan(num_tokens, num_kv_heads, max_seq_len).bytes;
+  return PA_OK;
+}
+
+pa_status pa_select_blocks(const void* q, pa_dtype q_dtype, const void* bounds,
+                           int64_t num_blocks, int block_size, int num_q_heads,
+                           int num_kv_heads, int head_dim,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* seq_lens,
+                           const int32_t* query_start_loc, int num_seqs,
+                           int64_t num_tokens, int max_query_len,
+                           int max_seq_len, int max_selected, int keep_first,
+                           int keep_last, int32_t* selected,
+                           int32_t* num_selected, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream) {
+  if (!valid_dtype(q_dtype)) return PA_ERR_INVALID_ARG;
+  if (pa_status st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim))
+    return st;
+  if (num_q_heads <= 0 || num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (!plain_type(q_dtype)) return PA_ERR_UNSUPPORTED;
+  if (keep_first < 0 || keep_last < 1 || max_selected < 1 ||
+      (int64_t)keep_first + keep_last > max_selected)
+    return PA_ERR_INVALID_ARG;
+  StepView s{block_tables,  max_blocks_per_seq, seq_lens,    query_start_loc, num_seqs,
+             num_tokens,    max_query_len,      max_seq_len, num_blocks,      nullptr};
+  bool done;
+  if (pa_status st = step_status(s, &done)) return st;
+  if (done) return PA_OK;
+  if (!q || !bounds || !selected || !num_selected || !aligned(q, 16) ||
+      !aligned(bounds, 16) || !aligned(selected, 4) || !aligned(num_selected, 4))
+    return PA_ERR_INVALID_ARG;
+  const SelectPlan plan = make_select_plan(num_tokens, num_kv_heads, max_seq_len);
+  if (workspace_bytes < (size_t)plan.bytes ||
+      (plan.bytes > 0 && (!workspace || !aligned(workspace, 256))))
+    return PA_ERR_INVALID_ARG;
+  const size_t rows = (size_t)num_tokens * num_kv_heads;
+  const Span outs[] = {{selected, rows * max_selected * 4},
+                       {num_selected, rows * 4},
+                       {workspace, (size_t)plan.bytes}};
+  const Span ins[] = {
+      {q, (size_t)num_tokens * num_q_heads * head_dim * elem_bytes(q_dtype)},
+      {bounds, (size_t)num_blocks * num_kv_heads * PA_BOUNDS_BYTES(head_dim)},
+      {block_tables, (size_t)num_seqs * max_blocks_per_seq * 4},
+      {seq_lens, (size_t)num_seqs * 4},
+      {query_start_loc, (size_t)num_seqs * 4 + 4}};
+  if (any_overlap(outs, 3, ins, 5)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  s.err = di->err;
+  const cudaError_t e = launch_select_blocks(
+      s, plan, q, q_dtype, num_q_heads, num_kv_heads, head_dim, bounds, max_selected,
+      keep_first, keep_last, selected, num_selected, workspace, di->num_sms,
+      reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_attention_selected_workspace_size(int64_t num_tokens,
+                                               int num_q_heads,
+                                               int num_kv_heads, int head_dim,
+                                               int max_selected,
+                                               size_t* bytes) {
+  if (!bytes || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      num_q_heads % num_kv_heads != 0 || max_selected < 1)
+    return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  *bytes = (size_t)make_selected_plan(num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                      max_selected, di->num_sms)
+               .bytes;
+  return PA_OK;
+}
+
+pa_status pa_attention_selected(
+    const void* q, pa_dtype q_dtype, const void* k_cache, const void* v_cache,
+    pa_dtype cache_dtype, int64_t num_blocks, int block_size, int num_q_heads,
+    int num_kv_heads, int head_dim, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* seq_lens,
+    const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+    int max_query_len, int max_seq_len, const int32_t* selected,
+    const int32_t* num_selected, int max_selected, float scale, float k_scale,
+    float v_scale, void* out, void* workspace, size_t workspace_bytes,
+    pa_stream_t stream) {
+  if (!valid_dtype(q_dtype) || !valid_dtype(cache_dtype)) return PA_ERR_INVALID_ARG;
+  if (pa_status st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim))
+    return st;
+  if (num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_selected < 1)
+    return PA_ERR_INVALID_ARG;
+  if (!plain_type(q_dtype)) return PA_ERR_UNSUPPORTED;
+  const bool quantised = cache_dtype == PA_FP8_E4M3 || is_4bit(cache_dtype);
+  if (!quantised && cache_dtype != q_dtype) return PA_ERR_UNSUPPORTED;
+  if (quantised && q_dtype == PA_F32) return PA_ERR_UNSUPPORTED;
+  if (!isfinite(scale)) return PA_ERR_INVALID_ARG;
+  if (scaled_type(cache_dtype) && !(is_scale(k_scale) && is_scale(v_scale)))
+    return PA_ERR_INVALID_ARG;
+  StepView s{block_tables,  max_blocks_per_seq, seq_lens,    query_start_loc, num_seqs,
+             num_tokens,    max_query_len,      max_seq_len, num_blocks,      nullptr};
+  bool done;
+  if (pa_status st = step_status(s, &done)) return st;
+  if (done) return PA_OK;
+  if (!q || !k_cache || !v_cache || !selected || !num_selected || !out ||
+      !aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 128) ||
+      !aligned(v_cache, 128) || !aligned(selected, 4) || !aligned(num_selected, 4))
+    return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  const SelectedPlan plan = make_selected_plan(num_tokens, num_q_heads, num_kv_heads,
+                                               head_dim, max_selected, di->num_sms);
+  if (workspace_bytes < (size_t)plan.bytes ||
+      (plan.bytes > 0 && (!workspace || !aligned(workspace, 256))))
+    return PA_ERR_INVALID_ARG;
+  const size_t qo = (size_t)num_tokens * num_q_heads * head_dim * elem_bytes(q_dtype);
+  const size_t cache_bytes =
+      (size_t)num_blocks * num_kv_heads * page_bytes(cache_dtype, head_dim);
+  const size_t rows = (size_t)num_tokens * num_kv_heads;
+  const Span outs[] = {{out, qo}, {workspace, (size_t)plan.bytes}};
+  const Span ins[] = {{q, qo},
+                      {k_cache, cache_bytes},
+                      {v_cache, cache_bytes},
+                      {selected, rows * max_selected * 4},
+                      {num_selected, rows * 4},
+                      {block_tables, (size_t)num_seqs * max_blocks_per_seq * 4},
+                      {seq_lens, (size_t)num_seqs * 4},
+                      {query_start_loc, (size_t)num_seqs * 4 + 4}};
+  if (any_overlap(outs, 2, ins, 8)) return PA_ERR_INVALID_ARG;
+  s.err = di->err;
+  SelectedArgs a{};
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.cache_dtype = cache_dtype;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.selected = selected;
+  a.num_selected = num_selected;
+  a.max_selected = max_selected;
+  a.scale = scale;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.out = out;
+  a.workspace = workspace;
+  const cudaError_t e =
+      launch_attention_selected(s, plan, a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"

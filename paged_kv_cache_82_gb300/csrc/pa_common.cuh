@@ -59,6 +59,25 @@ __device__ __forceinline__ ReqMeta load_req(const int32_t* __restrict__ qsl,
   return m;
 }
 
+// The request that token t belongs to: the largest r < num_seqs with qsl[r] <=
+// t (called by a whole warp; qsl is non-decreasing and starts at 0).  A 32-ary
+// search: one load per lane and round, two rounds up to 1024 requests.  The
+// caller checks that t really lies in [qsl[r], qsl[r + 1]).
+__device__ __forceinline__ int warp_find_request(const int32_t* __restrict__ qsl,
+                                                 int num_seqs, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = num_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int64_t i = lo + (int64_t)lane * step;
+    const unsigned below = __ballot_sync(~0u, i < hi && __ldg(qsl + i) <= t);
+    if (below == 0) break;
+    lo += (31 - __clz(below)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // ----------------------------------------------------------------------------
 // shared-memory address helpers
 // ----------------------------------------------------------------------------
