@@ -21,14 +21,26 @@
 #include <algorithm>
 #include <type_traits>
 
+#include <cooperative_groups.h>
+
 #include "pa_common.cuh"
 #include "pa_internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
+#ifndef PA_SEL_AHEAD
+#define PA_SEL_AHEAD 2
+#endif
+constexpr int kAhead = PA_SEL_AHEAD;  // pages asked into L2 before their loads
 constexpr int kThreads = kWarps * 32;
+#ifndef PA_SEL_WAVES
+#define PA_SEL_WAVES 2
+#endif
+constexpr int kSelWaves = PA_SEL_WAVES;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum : int { kB16 = 0, kH16 = 1, kF8 = 2 };  // bf16, f16, E4M3 pages
@@ -39,14 +51,14 @@ struct SelParams {
   const void* k_cache;
   const void* v_cache;
   int num_q_heads, num_kv_heads, group;
-  int head_parts, splits, per_split;
+  int head_parts, cluster, splits;  // ranges of a list: cluster x splits
   const int32_t* selected;
   const int32_t* num_selected;
   int max_selected;
   float scale, k_scale, v_scale;
   void* out;
-  float* part;  // [unit][split][head_rows][D], then [..][2]: m, l
-  float* part_ml;
+  float* part;     // [unit][split][head_rows][D]
+  float* part_ml;  // [unit][split][head_rows][2]: m, l
   int head_rows;
 };
 
@@ -224,14 +236,17 @@ selected_kernel(const SelParams p) {
   constexpr int kRows = 8 * kNT;  // query heads of the unit, at most
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
-  const int64_t unit = blockIdx.x / p.splits;
-  const int split = (int)(blockIdx.x - unit * p.splits);
-  const Unit u = find_unit(p, unit, split == 0 && threadIdx.x == 0);
-  if (u.count < 0) return;
+  // CTA (unit, split, rank): the ranks of one (unit, split) are a cluster
+  const int ranges = p.cluster * p.splits;
+  const int64_t unit = blockIdx.x / ranges;
+  const int range = (int)(blockIdx.x - unit * ranges);
+  pdl_launch_dependents();
+  const Unit u = find_unit(p, unit, range == 0 && threadIdx.x == 0);
+  if (u.count < 0) return;  // the whole cluster
   const int heads = min(p.group - u.part * kRows, kRows);
   const int head0 = u.h * p.group + u.part * kRows;
-  const int begin = min(u.count, split * p.per_split);
-  const int end = min(u.count, begin + p.per_split);
+  const int begin = (int)((int64_t)u.count * range / ranges);
+  const int end = (int)((int64_t)u.count * (range + 1) / ranges);
 
   // Q operand words, in the channel order of the lane's K words.  Over FP8
   // pages the products are in f16: a power of two brings the unit's largest
@@ -341,6 +356,11 @@ selected_kernel(const SelParams p) {
       const int at = begin + warp + (i + lane) * kWarps;
       held = Entry{0, -1};
       if (i + lane < mine) held = list_entry(p, u, at);
+    }
+    // one lane asks a later page into L2: loads in flight beyond the registers
+    if (kAhead > 0 && lane == ((i + kAhead) & 31) && lane >= kAhead && held.phys >= 0) {
+      bulk_prefetch_l2(kbase + held.phys * block_bytes, (uint32_t)kPageBytes);
+      bulk_prefetch_l2(vbase + held.phys * block_bytes, (uint32_t)kPageBytes);
     }
     return Entry{__shfl_sync(~0u, held.block, i & 31), __shfl_sync(~0u, held.phys, i & 31)};
   };
@@ -487,23 +507,54 @@ selected_kernel(const SelParams p) {
     }
   }
   __syncthreads();
+  // the CTA's result into the place of warp 0's (each thread reads and writes
+  // its own elements), then the cluster's from all of its CTAs
   for (int i = threadIdx.x; i < heads * kD; i += kThreads) {
     const int hd = i / kD, d = i - hd * kD;
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][hd]);
-    float a = 0.f, ls = 0.f;
+    float a = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx);
-      a += f * s_acc[w][hd][d];
-      ls += f * s_l[w][hd];
+    for (int w = 0; w < kWarps; ++w)
+      a += (s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx)) * s_acc[w][hd][d];
+    s_acc[0][hd][d] = a;
+  }
+  __shared__ float s_ml[kRows][2];
+  if (threadIdx.x < heads) {
+    const int hd = threadIdx.x;
+    float mx = -INFINITY, ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][hd]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      ls += (s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx)) * s_l[w][hd];
+    s_ml[hd][0] = mx;
+    s_ml[hd][1] = ls;
+  }
+  cg::cluster_group cl = cg::this_cluster();
+  if (p.cluster > 1) cl.sync(); else __syncthreads();
+  const int rank = p.cluster > 1 ? (int)cl.block_rank() : 0;
+  for (int i = rank * kThreads + threadIdx.x; i < heads * kD; i += p.cluster * kThreads) {
+    const int hd = i / kD, d = i - hd * kD;
+    float mx = s_ml[hd][0], ls = s_ml[hd][1], a = s_acc[0][hd][d];
+    if (p.cluster > 1) {
+      mx = -INFINITY;
+      for (int c2 = 0; c2 < p.cluster; ++c2)
+        mx = fmaxf(mx, *cl.map_shared_rank(&s_ml[hd][0], c2));
+      ls = a = 0.f;
+      for (int c2 = 0; c2 < p.cluster; ++c2) {
+        const float ms = *cl.map_shared_rank(&s_ml[hd][0], c2);
+        const float f = ms == -INFINITY ? 0.f : exp2f(ms - mx);
+        ls += f * *cl.map_shared_rank(&s_ml[hd][1], c2);
+        a += f * *cl.map_shared_rank(&s_acc[0][hd][d], c2);
+      }
     }
     if (p.splits == 1) {
       static_cast<TQ*>(p.out)[(u.t * p.num_q_heads + head0 + hd) * kD + d] =
           from_f32<TQ>(ls == 0.f ? 0.f : a / ls * p.v_scale);
     } else {
-      const int64_t row = (int64_t)blockIdx.x * p.head_rows + hd;
+      const int64_t row = (unit * p.splits + range / p.cluster) * p.head_rows + hd;
       p.part[row * kD + d] = a;
       if (d == 0) {
         p.part_ml[2 * row] = mx;
@@ -511,9 +562,10 @@ selected_kernel(const SelParams p) {
       }
     }
   }
+  if (p.cluster > 1) cl.sync();  // the others may still read this CTA's memory
 }
 
-// Join a unit's ranges in order: one warp per (unit, query head).
+// Join a unit's splits in order: one warp per (unit, query head).
 template <typename TQ, int kD>
 __global__ void __launch_bounds__(kThreads) selected_join_kernel(const SelParams p) {
   const int lane = threadIdx.x & 31;
@@ -523,6 +575,7 @@ __global__ void __launch_bounds__(kThreads) selected_join_kernel(const SelParams
   const int hd = (int)(item - unit * p.head_rows);
   if (unit >= units) return;
   const Unit u = find_unit(p, unit, false);
+  pdl_wait();  // the splits' results
   if (u.count < 0 || hd >= min(p.group - u.part * p.head_rows, p.head_rows)) return;
   const int64_t row0 = unit * p.splits * p.head_rows + hd;
   float mx = -INFINITY;
@@ -564,18 +617,32 @@ cudaError_t launch_generic(SelParams& p, int head_dim, cudaStream_t stream) {
 
 template <typename TQ, int kPg, int kD>
 cudaError_t launch_mma_d(const SelParams& p, int64_t units, cudaStream_t stream) {
-  const int64_t grid = units * p.splits;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (p.head_rows == 8)
-    selected_kernel<TQ, kPg, kD, 1><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-  else
-    selected_kernel<TQ, kPg, kD, 2><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-  cudaError_t e = launched();
-  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t grid = units * p.cluster * p.splits;
   const int64_t join = (units * p.head_rows + kWarps - 1) / kWarps;
-  if (join > 0x7fffffffll) return cudaErrorInvalidValue;
-  selected_join_kernel<TQ, kD><<<(unsigned)join, kThreads, 0, stream>>>(p);
-  return launched();
+  if (grid > 0x7fffffffll || join > 0x7fffffffll) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  cudaError_t e = p.head_rows == 8
+                      ? cudaLaunchKernelEx(&cfg, selected_kernel<TQ, kPg, kD, 1>, p)
+                      : cudaLaunchKernelEx(&cfg, selected_kernel<TQ, kPg, kD, 2>, p);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  if (p.splits == 1) return cudaSuccess;
+  cfg.gridDim = dim3((unsigned)join);
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, selected_join_kernel<TQ, kD>, p);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 template <typename TQ, int kPg>
@@ -594,15 +661,17 @@ SelectedPlan make_selected_plan(int64_t num_tokens, int num_q_heads, int num_kv_
   pl.head_rows = group <= 8 ? 8 : 16;
   pl.head_parts = (group + pl.head_rows - 1) / pl.head_rows;
   pl.units = num_tokens * num_kv_heads * pl.head_parts;
-  // few units: cut the lists until every SM has two CTAs, ranges of at least
-  // two pages per warp
-  const int64_t want = 2 * num_sms;
-  const int most = std::max(1, max_selected / (2 * kWarps));
-  int64_t splits = pl.units > 0 ? (want + pl.units - 1) / pl.units : 1;
-  splits = std::max<int64_t>(1, std::min<int64_t>(splits, most));
-  pl.per_split = (int)((max_selected + splits - 1) / splits);
-  pl.splits = (max_selected + pl.per_split - 1) / std::max(1, pl.per_split);
-  pl.splits = std::max(1, pl.splits);
+  // Ranges per list: until the grid is kSelWaves CTAs per SM, of two pages per
+  // warp at least.  Up to 8 (a portable cluster) are joined through the
+  // cluster's shared memory; beyond that, clusters through the workspace.
+  const int64_t want = (int64_t)kSelWaves * num_sms;
+  const int64_t most = std::max(1, max_selected / (2 * kWarps));
+  int64_t ranges = pl.units > 0 ? (want + pl.units - 1) / pl.units : 1;
+  ranges = std::max<int64_t>(1, std::min(ranges, most));
+  pl.cluster = 1;
+  while (pl.cluster < 8 && pl.cluster < ranges) pl.cluster *= 2;
+  if (pl.cluster > most) pl.cluster /= 2;
+  pl.splits = ranges > 8 ? (int)((ranges + 7) / 8) : 1;
   pl.bytes = pl.splits == 1 ? 0
                             : pl.units * pl.splits * pl.head_rows * (head_dim + 2) *
                                   (int64_t)sizeof(float);
@@ -621,8 +690,8 @@ cudaError_t launch_attention_selected(const StepView& s, const SelectedPlan& pla
   p.group = a.num_q_heads / a.num_kv_heads;
   p.head_parts = plan.head_parts;
   p.head_rows = plan.head_rows;
+  p.cluster = plan.cluster;
   p.splits = plan.splits;
-  p.per_split = plan.per_split;
   p.selected = a.selected;
   p.num_selected = a.num_selected;
   p.max_selected = a.max_selected;

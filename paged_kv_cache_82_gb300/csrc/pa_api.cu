@@ -795,9 +795,9 @@ pa_status pa_norm_rope_and_cache(
   a.v_scale = v_scale;
   a.vector_ok = aligned(q, 16) && aligned(k, 16) && aligned(v, 16) &&
                 q_stride * eb % 16 == 0 && k_stride * eb % 16 == 0 &&
-                v_stride * eb % 16 == 0;
+                v_stride * eb % 16 == 0 && aligned(q_weight, 16) && aligned(k_weight, 16);
   const cudaError_t e =
-      launch_norm_rope_and_cache(a, di->err, reinterpret_cast<cudaStream_t>(stream));
+      launch_norm_rope_and_cache(a, di->num_sms, di->err, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

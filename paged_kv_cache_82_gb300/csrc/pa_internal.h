@@ -83,9 +83,9 @@ struct RopeArgs {
   int num_q_heads, num_kv_heads, head_dim;
   const int64_t* slot_mapping;
   float k_scale, v_scale;
-  bool vector_ok;  // q, k, v rows allow 16-byte loads
+  bool vector_ok;  // q, k, v rows and the weights allow 16-byte loads
 };
-cudaError_t launch_norm_rope_and_cache(const RopeArgs& a, unsigned* err,
+cudaError_t launch_norm_rope_and_cache(const RopeArgs& a, int num_sms, unsigned* err,
                                        cudaStream_t stream);
 
 // ---- block bounds and selection (select_kernels.cu) -------------------------
@@ -124,8 +124,8 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
 struct SelectedPlan {
   int head_rows;   // query heads of one work unit (of one KV head's group)
   int head_parts;  // units per KV head
-  int splits;      // ranges a unit's list is cut into
-  int per_split;   // list entries of one range
+  int cluster;     // ranges of a unit's list that one cluster joins
+  int splits;      // clusters per unit, joined through the workspace
   int64_t units;
   int64_t bytes;
 };

@@ -22,6 +22,13 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
+#ifndef PA_ROPE_CTAS
+#define PA_ROPE_CTAS 3
+#endif
+#ifndef PA_ROPE_H
+#define PA_ROPE_H 4
+#endif
+constexpr int kHeads = PA_ROPE_H;  // rows per lane group of a large step
 
 enum : int { kSame = 0, kFp8 = 1, kInt4 = 2, kNvfp4 = 3 };
 
@@ -46,6 +53,8 @@ struct RopeParams {
   const int64_t* slot_mapping;
   float k_scale, v_scale;
   unsigned* err;
+  int num_sms;
+  int items, q_items, kv_items;  // warps of one token: all, per kind
 };
 
 // 8 consecutive elements as fp32
@@ -81,6 +90,35 @@ __device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
     *reinterpret_cast<float4*>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
   }
 }
+
+// 8 elements of a row as they are read, 16 or 32 bytes
+template <typename T>
+struct alignas(16) Row8 {
+  T e[8];
+  template <bool kVec>
+  __device__ __forceinline__ void load(const T* src) {
+    if constexpr (kVec) {
+      const uint4* s = reinterpret_cast<const uint4*>(src);
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(e)[i] = s[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = src[i];
+    }
+  }
+  __device__ __forceinline__ Row8 shuffled(int from) const {
+    Row8 o;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) * 2; ++i)
+      reinterpret_cast<uint32_t*>(o.e)[i] =
+          __shfl_sync(~0u, reinterpret_cast<const uint32_t*>(e)[i], from);
+    return o;
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
+  }
+};
 
 // One lane's 8 elements x (lane sub of the kD / 8 of a row) of token offset o
 // into the page of a cache, by pa_reshape_and_cache's rule.  Every lane of
@@ -135,115 +173,170 @@ __device__ __forceinline__ void cache_row(void* cache, int64_t page, int o, int 
   }
 }
 
-template <typename T, int kCache, int kD, bool kVec>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeParams p) {
-  constexpr int kLanes = kD / 8;        // lanes of one head's row
-  constexpr int kRows = 32 / kLanes;    // rows of one warp
+// One warp: kH rows per group of lanes, all query, all key or all value heads
+// of one token, so the rotation's row and the weights are read once for kH
+// heads; all rows are on their way before the first is used.  kVec: rows and
+// weights allow 16-byte loads.
+template <typename T, int kCache, int kD, bool kVec, int kH>
+__global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS) norm_rope_kernel(const RopeParams p) {
+  constexpr int kLanes = kD / 8;      // lanes of one head's row
+  constexpr int kRows = 32 / kLanes;  // rows of one warp at a time
   const int lane = threadIdx.x & 31, sub = lane % kLanes;
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  const int64_t row =
-      (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * kRows + lane / kLanes;
-  bool on = row < p.num_tokens * heads;
-  const int64_t t = on ? row / heads : 0;
-  const int hr = on ? (int)(row - t * heads) : 0;
-  const int which = hr < p.num_q_heads ? 0 : hr < p.num_q_heads + p.num_kv_heads ? 1 : 2;
-  const int h = hr - (which == 0 ? 0 : which == 1 ? p.num_q_heads
-                                                  : p.num_q_heads + p.num_kv_heads);
+  const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = warp / (uint32_t)p.items;
+  if (t >= p.num_tokens) return;
+  const int item = (int)(warp - (uint32_t)t * (uint32_t)p.items);
+  const int which = item < p.q_items ? 0 : item < p.q_items + p.kv_items ? 1 : 2;
+  const int heads = which == 0 ? p.num_q_heads : p.num_kv_heads;
+  const int h0 = (item - (which == 0 ? 0 : p.q_items + (which - 1) * p.kv_items)) *
+                     (kRows * kH) + lane / kLanes;
   const int64_t slot = __ldg(p.slot_mapping + t);
   const int64_t pos = p.rotary_dim ? __ldg(p.positions + t) : 0;
-  on = on && slot >= 0;  // a padding token: nothing read or written
-  if (on && (slot >= p.num_slots || (p.rotary_dim && (pos < 0 || pos >= p.max_position)))) {
-    if (hr == 0 && sub == 0)
+  const T* src = (which == 0   ? static_cast<const T*>(p.q) + t * p.q_stride
+                  : which == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
+                               : static_cast<const T*>(p.v) + t * p.v_stride) +
+                 sub * 8;
+  if (slot < 0) return;  // a padding token: nothing written
+  if (slot >= p.num_slots || (p.rotary_dim && (pos < 0 || pos >= p.max_position))) {
+    if (item == 0 && lane == 0)
       flag_error(p.err, slot >= p.num_slots ? PA_DEV_ERR_SLOT : PA_DEV_ERR_METADATA);
-    on = false;
+    return;
   }
-  float x[8] = {};
-  if (on) {
-    const T* src = which == 0   ? static_cast<const T*>(p.q) + t * p.q_stride
-                   : which == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
-                                : static_cast<const T*>(p.v) + t * p.v_stride;
-    load8<T, kVec>(src + (int64_t)h * kD + sub * 8, x);
+  Row8<T> raw[kH];
+#pragma unroll
+  for (int j = 0; j < kH; ++j) {
+    const int h = h0 + j * kRows;
+    if (h < heads) raw[j].template load<kVec>(src + (int64_t)h * kD);
   }
+  // The lane's rotation with the weights in it: element i of the result is
+  //   r (x_i own_i + x_partner other_i),  r = 1/sqrt(mean + eps),
+  //   own = w cos, other = -+ w_partner sin
+  // (no norm: w = r = 1; no rotation: cos = 1, sin = 0).  The partner's element
+  // comes as it was read: a shuffle of the packed row.
   const void* wp = which == 0 ? p.q_weight : which == 1 ? p.k_weight : nullptr;
-  float ss = 0.f;
+  const int half = p.rotary_dim / 2;
+  const bool turns = which < 2 && sub * 8 < p.rotary_dim;
+  const bool second = sub * 8 >= half;
+  const int away = p.rotary_dim / 16;  // lanes between the two of a pair
+  const int partner = !turns || p.interleaved ? sub : second ? sub - away : sub + away;
+  float own[8], other[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
-  if (wp) {
-    const float r = 1.0f / sqrtf(ss * (1.0f / kD) + p.eps);
-    float w[8];
-    if (p.weight_f32)
-      load8<float, false>(static_cast<const float*>(wp) + sub * 8, w);
-    else
-      load8<T, false>(static_cast<const T*>(wp) + sub * 8, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-  }
-  if (p.rotary_dim) {
-    const int half = p.rotary_dim / 2;
-    const bool turns = on && which < 2 && sub * 8 < p.rotary_dim;
-    const float* row_cs = p.cos_sin + pos * p.rotary_dim;
+  for (int i = 0; i < 8; ++i) own[i] = 1.f, other[i] = 0.f;
+  if (turns) {
+    const float* row = p.cos_sin + pos * p.rotary_dim;
     if (p.interleaved) {
-      if (turns) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(row_cs + sub * 4));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(row_cs + half + sub * 4));
-        const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = a * cc[i] - b * sn[i];
-          x[2 * i + 1] = b * cc[i] + a * sn[i];
-        }
-      }
+      const float4 c = __ldg(reinterpret_cast<const float4*>(row + sub * 4));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + sub * 4));
+      own[0] = own[1] = c.x, own[2] = own[3] = c.y;
+      own[4] = own[5] = c.z, own[6] = own[7] = c.w;
+      other[0] = -s.x, other[1] = s.x, other[2] = -s.y, other[3] = s.y;
+      other[4] = -s.z, other[5] = s.z, other[6] = -s.w, other[7] = s.w;
     } else {
-      const bool second = sub * 8 >= half;
-      const int away = p.rotary_dim / 16;  // lanes between the two of a pair
-      const int from = (lane - sub) + (turns ? (second ? sub - away : sub + away) : sub);
-      float y[8];
+      const int f = sub * 8 - (second ? half : 0);
+      const float4* cp = reinterpret_cast<const float4*>(row + f);
+      const float4* sp = reinterpret_cast<const float4*>(row + half + f);
+      *reinterpret_cast<float4*>(own) = __ldg(cp);
+      *reinterpret_cast<float4*>(own + 4) = __ldg(cp + 1);
+      *reinterpret_cast<float4*>(other) = __ldg(sp);
+      *reinterpret_cast<float4*>(other + 4) = __ldg(sp + 1);
+      if (!second)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(~0u, x[i], from);
-      if (turns) {
-        float c[8], s[8];
-        const int f = sub * 8 - (second ? half : 0);
-        const float4* cp = reinterpret_cast<const float4*>(row_cs + f);
-        const float4* sp = reinterpret_cast<const float4*>(row_cs + half + f);
-        *reinterpret_cast<float4*>(c) = __ldg(cp);
-        *reinterpret_cast<float4*>(c + 4) = __ldg(cp + 1);
-        *reinterpret_cast<float4*>(s) = __ldg(sp);
-        *reinterpret_cast<float4*>(s + 4) = __ldg(sp + 1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[i] = x[i] * c[i] + (second ? y[i] : -y[i]) * s[i];
-      }
+        for (int i = 0; i < 8; ++i) other[i] = -other[i];
     }
   }
-  if (which == 0) {
-    if (on)
-      store8(static_cast<T*>(p.q_out) + (t * p.num_q_heads + h) * kD + sub * 8, x);
-  }
-  // the stored key is that of the input type, whatever the cache's
+  if (wp) {
+    float w[8], v[8];
+    if (p.weight_f32) {
+      load8<float, kVec>(static_cast<const float*>(wp) + sub * 8, w);
+      load8<float, kVec>(static_cast<const float*>(wp) + partner * 8, v);
+    } else {
+      load8<T, kVec>(static_cast<const T*>(wp) + sub * 8, w);
+      load8<T, kVec>(static_cast<const T*>(wp) + partner * 8, v);
+    }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_f32(from_f32<T>(x[i]));
-  const int64_t b = on ? slot / kBS : 0;
-  const int o = on ? (int)(slot - b * kBS) : 0;
-  cache_row<T, kCache, kD>(which == 2 ? p.v_cache : p.k_cache, b * p.num_kv_heads + h, o,
-                           sub, x, which == 2 ? p.v_scale : p.k_scale, on && which > 0);
+    for (int i = 0; i < 8; ++i) {
+      own[i] *= w[i];
+      other[i] *= p.interleaved ? w[i ^ 1] : v[i];
+    }
+  }
+  const int from = (lane - sub) + partner;
+  const int64_t b = slot / kBS;
+  const int o = (int)(slot - b * kBS);
+#pragma unroll
+  for (int j = 0; j < kH; ++j) {
+    if (h0 - lane / kLanes + j * kRows >= heads) break;  // the whole warp is past
+    const int h = h0 + j * kRows;
+    const bool on = h < heads;
+    float x[8];
+    raw[j].values(x);
+    float r = 1.f;
+    if (wp) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
+      r = rsqrtf(ss * (1.0f / kD) + p.eps);
+    }
+    if (which < 2) {
+      if (p.interleaved) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = x[i] * own[i];
+          if (turns) y[i] = fmaf(x[i ^ 1], other[i], y[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = y[i] * r;
+      } else {
+        float y[8];
+        raw[j].shuffled(from).values(y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = x[i] * own[i];
+          if (turns) x[i] = fmaf(y[i], other[i], x[i]);
+          x[i] *= r;
+        }
+      }
+    }
+    if (which == 0) {
+      if (on) store8(static_cast<T*>(p.q_out) + (t * p.num_q_heads + h) * kD + sub * 8, x);
+    } else {
+      // the stored key is that of the input type, whatever the cache's
+      if constexpr (kCache != kSame) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f32(from_f32<T>(x[i]));
+      }
+      cache_row<T, kCache, kD>(which == 2 ? p.v_cache : p.k_cache,
+                               b * p.num_kv_heads + h, o, sub, x,
+                               which == 2 ? p.v_scale : p.k_scale, on);
+    }
+  }
+}
+
+template <typename T, int kCache, int kD, bool kVec, int kH>
+cudaError_t launch_h(RopeParams p, cudaStream_t stream) {
+  constexpr int kRows = 32 / (kD / 8) * kH;
+  p.q_items = (p.num_q_heads + kRows - 1) / kRows;
+  p.kv_items = (p.num_kv_heads + kRows - 1) / kRows;
+  p.items = p.q_items + 2 * p.kv_items;
+  const int64_t blocks =
+      (p.num_tokens * p.items + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks >= (1ll << 29)) return cudaErrorInvalidValue;  // warps: 32 bits
+  norm_rope_kernel<T, kCache, kD, kVec, kH><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 template <typename T, int kCache, int kD>
 cudaError_t launch_d(const RopeParams& p, bool vec, cudaStream_t stream) {
+  if (!vec) return launch_h<T, kCache, kD, false, 1>(p, stream);
+  // several heads per lane group once that still leaves every SM 16 warps
   const int64_t rows = p.num_tokens * (p.num_q_heads + 2 * p.num_kv_heads);
-  const int64_t per_block = kThreads / (kD / 8);
-  const int64_t blocks = (rows + per_block - 1) / per_block;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (vec)
-    norm_rope_kernel<T, kCache, kD, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-  else
-    norm_rope_kernel<T, kCache, kD, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) count_launch();
-  return e;
+  if (rows >= 16ll * p.num_sms * kHeads * (32 / (kD / 8)))
+    return launch_h<T, kCache, kD, true, kHeads>(p, stream);
+  return launch_h<T, kCache, kD, true, 1>(p, stream);
 }
 
 template <typename T, int kCache>
@@ -265,7 +358,7 @@ cudaError_t launch_c(const RopeParams& p, pa_dtype cache, int head_dim, bool vec
 
 }  // namespace
 
-cudaError_t launch_norm_rope_and_cache(const RopeArgs& a, unsigned* err,
+cudaError_t launch_norm_rope_and_cache(const RopeArgs& a, int num_sms, unsigned* err,
                                        cudaStream_t stream) {
   RopeParams p{};
   p.q = a.q;
@@ -294,6 +387,7 @@ cudaError_t launch_norm_rope_and_cache(const RopeArgs& a, unsigned* err,
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
   p.err = err;
+  p.num_sms = num_sms;
   switch (a.dtype) {
     case PA_F32: return launch_c<float>(p, a.cache_dtype, a.head_dim, a.vector_ok, stream);
     case PA_F16: return launch_c<__half>(p, a.cache_dtype, a.head_dim, a.vector_ok, stream);

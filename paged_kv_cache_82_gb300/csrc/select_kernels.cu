@@ -31,120 +31,226 @@ constexpr int bounds_bytes(int d) { return PA_BOUNDS_BYTES(d); }
 // ---------------------------------------------------------------------------
 enum : int { kPgF32 = 0, kPgF16, kPgBf16, kPgFp8, kPgInt4, kPgNvfp4 };
 
-// 8 consecutive channels (from 8 * c8) of the token at offset o of a page
+// A lane's 8 consecutive channels of one token of a page, as read
+template <int kPg>
+struct PageWords {
+  static constexpr int kWords = kPg == kPgF32                        ? 8
+                                : kPg == kPgF16 || kPg == kPgBf16 ? 4
+                                : kPg == kPgFp8                      ? 2
+                                                                     : 1;
+  uint32_t w[kWords];
+  float scale;  // 4-bit pages: the token's or the block's
+};
+
 template <int kPg, int kD>
-__device__ __forceinline__ void page_load8(const void* cache, int64_t page, int o,
-                                           int c8, float (&x)[8]) {
+__device__ __forceinline__ PageWords<kPg> page_words(const void* cache, int64_t page, int o,
+                                                     int c8) {
+  PageWords<kPg> v;
+  v.scale = 0.f;
   if constexpr (kPg == kPgF32) {
-    const float4* src = reinterpret_cast<const float4*>(
+    const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const float*>(cache) + (page * kBS + o) * kD + c8 * 8);
-    const float4 a = __ldg(src), b = __ldg(src + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    *reinterpret_cast<uint4*>(v.w) = __ldg(src);
+    *reinterpret_cast<uint4*>(v.w + 4) = __ldg(src + 1);
   } else if constexpr (kPg == kPgF16 || kPg == kPgBf16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(
+    *reinterpret_cast<uint4*>(v.w) = __ldg(reinterpret_cast<const uint4*>(
         static_cast<const uint16_t*>(cache) + (page * kBS + o) * kD + c8 * 8));
-    if constexpr (kPg == kPgF16) {
-      const __half* e = reinterpret_cast<const __half*>(&u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
-    } else {
-      const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
-    }
   } else if constexpr (kPg == kPgFp8) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(
+    *reinterpret_cast<uint2*>(v.w) = __ldg(reinterpret_cast<const uint2*>(
         static_cast<const uint8_t*>(cache) + (page * kBS + o) * kD + c8 * 8));
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = e4m3_to_f32((uint8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3))));
   } else {
     constexpr int kPage = kPg == kPgNvfp4 ? 9 * kD : 8 * kD + 64;
     const uint8_t* pg = static_cast<const uint8_t*>(cache) + page * kPage;
-    const uint32_t w =
-        __ldg(reinterpret_cast<const uint32_t*>(pg + o * (kD / 2) + c8 * 4));
-    if constexpr (kPg == kPgInt4) {
-      const float sc = __ldg(reinterpret_cast<const float*>(pg + kBS * (kD / 2) + 4 * o));
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = sc * (float)((int)(w << (28 - 4 * i)) >> 28);
-    } else {
-      const float sc =
-          e4m3_to_f32(__ldg(pg + kBS * (kD / 2) + o * (kD / 16) + c8 / 2));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = sc * e2m1_to_f32((w >> (4 * i)) & 15u);
-    }
+    v.w[0] = __ldg(reinterpret_cast<const uint32_t*>(pg + o * (kD / 2) + c8 * 4));
+    if constexpr (kPg == kPgInt4)
+      v.scale = __ldg(reinterpret_cast<const float*>(pg + kBS * (kD / 2) + 4 * o));
+    else
+      v.scale = e4m3_to_f32(__ldg(pg + kBS * (kD / 2) + o * (kD / 16) + c8 / 2));
   }
+  return v;
 }
 
-// One group of kD / 8 lanes per (written block, KV head): 8 channels per lane,
-// the block's tokens one after the other.
+// Running largest and smallest of 8 channels: packed pairs where the page's
+// values are 16-bit numbers (E4M3 as f16), fp32 elsewhere.  A NaN is passed
+// over, as fmaxf and the packed maximum do.
+template <int kPg>
+struct Range8 {
+  static constexpr bool kPair = kPg == kPgF16 || kPg == kPgBf16 || kPg == kPgFp8;
+  static constexpr bool kBF = kPg == kPgBf16;
+  static constexpr int kN = kPair ? 4 : 8;
+  uint32_t hi[kN], lo[kN];
+
+  __device__ __forceinline__ static uint32_t max_of(uint32_t a, uint32_t b) {
+    if constexpr (!kPair) {
+      return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    } else if constexpr (kBF) {
+      const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                       *reinterpret_cast<__nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+      const __half2 m =
+          __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    }
+  }
+  __device__ __forceinline__ static uint32_t min_of(uint32_t a, uint32_t b) {
+    if constexpr (!kPair) {
+      return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
+    } else if constexpr (kBF) {
+      const __nv_bfloat162 m = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                       *reinterpret_cast<__nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+      const __half2 m =
+          __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+    const uint32_t inf = !kPair ? 0x7F800000u : kBF ? 0x7F807F80u : 0x7C007C00u;
+    const uint32_t ninf = !kPair ? 0xFF800000u : kBF ? 0xFF80FF80u : 0xFC00FC00u;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) hi[i] = ninf, lo[i] = inf;
+  }
+  __device__ __forceinline__ void add(const PageWords<kPg>& v) {
+    uint32_t x[kN];
+    if constexpr (kPg == kPgFp8) {
+      e4m3x4_to_f16x2x2(v.w[0], x[0], x[1]);
+      e4m3x4_to_f16x2x2(v.w[1], x[2], x[3]);
+    } else if constexpr (kPair || kPg == kPgF32) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) x[i] = v.w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t nib = (v.w[0] >> (4 * i)) & 15u;
+        x[i] = __float_as_uint(v.scale * (kPg == kPgInt4 ? (float)((int)(nib ^ 8u) - 8)
+                                                         : e2m1_to_f32(nib)));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      hi[i] = max_of(hi[i], x[i]);
+      lo[i] = min_of(lo[i], x[i]);
+    }
+  }
+  // with the lane `mask` away
+  __device__ __forceinline__ void join(int mask) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      hi[i] = max_of(hi[i], __shfl_xor_sync(~0u, hi[i], mask));
+      lo[i] = min_of(lo[i], __shfl_xor_sync(~0u, lo[i], mask));
+    }
+  }
+  __device__ __forceinline__ static float value(const uint32_t (&w)[kN], int i) {
+    if constexpr (!kPair) {
+      return __uint_as_float(w[i]);
+    } else if constexpr (kBF) {
+      return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    } else {
+      const __half2 h = *reinterpret_cast<const __half2*>(&w[i / 2]);
+      return (i & 1) ? __high2float(h) : __low2float(h);
+    }
+  }
+};
+
+// One warp per (written block, KV head): kD / 8 lanes hold 8 channels each of
+// a token, the warp reads 256 / kD tokens at a time and all of the page's 16
+// before it uses the first.  The page is read once and a 1/32 to 1/8 of its
+// bytes written, so the kernel is bound by HBM when there are many pages, and
+// by the chain of loads (lengths, block id, page) when there are few.
 template <int kPg, int kD>
 __global__ void __launch_bounds__(kThreads)
 summarise_kernel(StepView s, const void* __restrict__ k_cache, int num_kv_heads,
-                 int groups_per_seq, uint8_t* __restrict__ bounds) {
-  constexpr int kLanes = kD / 8, kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31, sub = lane % kLanes;
-  const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int64_t item = warp * kRows + lane / kLanes;
-  const int64_t per_seq = (int64_t)groups_per_seq * num_kv_heads;
-  if (item >= per_seq * s.num_seqs) return;
-  const int r = (int)(item / per_seq);
-  const int rem = (int)(item - r * per_seq);
-  const int nth = rem / num_kv_heads, h = rem - nth * num_kv_heads;
+                 int ctas_per_seq, uint8_t* __restrict__ bounds) {
+  constexpr int kLanes = kD / 8, kRows = 32 / kLanes, kReads = kBS / kRows;
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, part = lane / kLanes;
+  const int r = blockIdx.x / ctas_per_seq;
+  const int item =
+      (blockIdx.x - r * ctas_per_seq) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int nth = item / num_kv_heads, h = item - nth * num_kv_heads;
   const ReqMeta m = load_req(s.query_start_loc, s.seq_lens, r, s.num_tokens,
                              s.max_query_len, s.max_seq_len, s.max_blocks_per_seq);
   if (!m.ok) {
-    if (rem == 0 && sub == 0) flag_error(s.err, PA_DEV_ERR_METADATA);
+    if (item == 0 && lane == 0) flag_error(s.err, PA_DEV_ERR_METADATA);
     return;
   }
   const int b = (m.L - m.n) / kBS + nth;  // the nth block this step wrote to
   if (m.n == 0 || b >= m.nb) return;
   const int blk = __ldg(s.block_tables + (int64_t)r * s.max_blocks_per_seq + b);
   if (blk < 0 || (int64_t)blk >= s.num_blocks) {
-    if (h == 0 && sub == 0) flag_error(s.err, PA_DEV_ERR_BLOCK_ID);
+    if (h == 0 && lane == 0) flag_error(s.err, PA_DEV_ERR_BLOCK_ID);
     return;
   }
   const int64_t page = (int64_t)blk * num_kv_heads + h;
   const int tokens = min(kBS, m.L - b * kBS);
-  float hi[8], lo[8];
+  // a place past the block's tokens reads its last token again
+  PageWords<kPg> words[kReads];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
-#pragma unroll 4
-  for (int o = 0; o < tokens; ++o) {
-    float x[8];
-    page_load8<kPg, kD>(k_cache, page, o, sub, x);
+  for (int i = 0; i < kReads; ++i)
+    words[i] = page_words<kPg, kD>(k_cache, page, min(i * kRows + part, tokens - 1), sub);
+  using Range = Range8<kPg>;
+  Range range;
+  range.clear();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // a NaN is passed over
-      hi[i] = fmaxf(hi[i], x[i]);
-      lo[i] = fminf(lo[i], x[i]);
-    }
-  }
+  for (int i = 0; i < kReads; ++i) range.add(words[i]);
+#pragma unroll
+  for (int d = kLanes; d < 32; d <<= 1) range.join(d);
   float big = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (lo[i] > hi[i]) lo[i] = hi[i] = 0.f;  // nothing but NaN in the channel
-    lo[i] = fminf(fmaxf(lo[i], -FLT_MAX), FLT_MAX);
-    hi[i] = fminf(fmaxf(hi[i], -FLT_MAX), FLT_MAX);
-    big = fmaxf(big, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
-  }
-  const unsigned mask = kLanes == 32 ? ~0u : ((1u << kLanes) - 1) << (lane - sub);
+  for (int i = 0; i < 8; ++i)
+    big = fmaxf(big, fmaxf(fabsf(Range::value(range.hi, i)), fabsf(Range::value(range.lo, i))));
+  // The first part of the warp has the codes of the largest values, the second
+  // those of the smallest, as floor(x) = -ceil(-x).
+  const bool low = part & 1;
+  float x[8];
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) big = fmaxf(big, __shfl_xor_sync(mask, big, d));
+  for (int i = 0; i < 8; ++i)
+    x[i] = low ? -Range::value(range.lo, i) : Range::value(range.hi, i);
+  // infinite: an infinite key, or a channel of nothing but NaN (hi -inf, lo inf)
+  if (big == INFINITY) {
+    big = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float hi = Range::value(range.hi, i), lo = Range::value(range.lo, i);
+      x[i] = lo > hi ? 0.f : fminf(fmaxf(x[i], -FLT_MAX), FLT_MAX);
+      if (lo <= hi)
+        big = fmaxf(big, fminf(fmaxf(fabsf(lo), fabsf(hi)), FLT_MAX));
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
   const float sc = __fdiv_rn(big, 127.0f);
-  uint32_t ch[2] = {0, 0}, cl[2] = {0, 0};
+  int c[8];
+  if (kPg != kPgF32 && sc >= 0x1p-100f && sc <= 0x1p+16f) {
+    // fl32(x / s) from the correctly rounded 1 / s in two of Markstein's
+    // corrections (IBM J. Res. Dev. 34, 1990): after the first the quotient is
+    // within one step, so the second rounds correctly.  Half the instructions
+    // of a division each.  The range of s keeps 1 / s normal and the quotient
+    // of any 16-bit (or narrower) key from vanishing; a remainder that
+    // underflows belongs to a quotient far below 1, whose ceiling is its
+    // sign's.
+    const float rcp = __frcp_rn(sc);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int a = sc > 0.f ? min(127, max(-127, __float2int_ru(__fdiv_rn(hi[i], sc)))) : 0;
-    const int c = sc > 0.f ? min(127, max(-127, __float2int_rd(__fdiv_rn(lo[i], sc)))) : 0;
-    ch[i >> 2] |= ((uint32_t)a & 0xFFu) << (8 * (i & 3));
-    cl[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) {
+      float y = x[i] * rcp;
+      y = fmaf(fmaf(-y, sc, x[i]), rcp, y);
+      y = fmaf(fmaf(-y, sc, x[i]), rcp, y);
+      c[i] = __float2int_ru(fminf(y, 127.0f));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      c[i] = sc > 0.f ? __float2int_ru(fminf(__fdiv_rn(x[i], sc), 127.0f)) : 0;
   }
+  uint32_t code[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    code[i >> 2] |= ((uint32_t)(low ? -c[i] : c[i]) & 0xFFu) << (8 * (i & 3));
   uint8_t* rec = bounds + page * bounds_bytes(kD);
-  *reinterpret_cast<uint2*>(rec + sub * 8) = make_uint2(ch[0], ch[1]);
-  *reinterpret_cast<uint2*>(rec + kD + sub * 8) = make_uint2(cl[0], cl[1]);
-  if (sub == 0)
+  if (part < 2)
+    *reinterpret_cast<uint2*>(rec + (low ? kD : 0) + sub * 8) = make_uint2(code[0], code[1]);
+  if (lane == 0)
     *reinterpret_cast<uint4*>(rec + 2 * kD) = make_uint4(__float_as_uint(sc), 0, 0, 0);
 }
 
@@ -157,6 +263,10 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 constexpr uint32_t kKeptKey = 0xFFFFFFFFu;  // above every score's key
+// a score's key; a NaN's (of a record that was never written) is the highest
+__device__ __forceinline__ uint32_t score_key(float x) {
+  return min(order_key(x), kKeptKey - 1);
+}
 
 struct ScoreParams {
   StepView s;
@@ -165,6 +275,7 @@ struct ScoreParams {
   int num_q_heads, num_kv_heads, group;
   const uint8_t* bounds;
   int max_selected, keep_first, keep_last;
+  int chunk;  // cache blocks of one CTA
   int64_t row_scores;
   uint32_t* keys;  // [token of the pass][KV head][row_scores]
 };
@@ -189,72 +300,188 @@ __device__ __forceinline__ TokenView token_view(const StepView& s, int64_t t, bo
   return v;
 }
 
-constexpr int kScoreWarps = 8;
-constexpr int kScoreBlocks = 64;  // cache blocks of one CTA
+// each byte's sign bit all over the byte
+__device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %1, 0xba98;" : "=r"(d) : "r"(x));
+  return d;
+}
 
-// One CTA: one token, kScoreBlocks cache blocks, all KV heads (a warp per
-// head in turn: the heads' records of a block are one contiguous range).
-// kD / 16 lanes hold a record's 16 channels each, so a warp reads 512 / kD
-// records at a time; the query's codes stay in registers.
+// 16 consecutive elements as fp32 (16-byte aligned)
+template <typename T>
+__device__ __forceinline__ void load16(const T* src, float (&x)[16]) {
+  constexpr int kV = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 16 / kV; ++i) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) x[i * kV + j] = to_f32(e[j]);
+  }
+}
+
+#ifndef PA_SCORE_FLIGHT
+#define PA_SCORE_FLIGHT 4
+#endif
+#ifndef PA_SCORE_CTAS
+#define PA_SCORE_CTAS 3
+#endif
+constexpr int kScoreWarps = 8;
+constexpr int kScoreChunkMax = 256;
+constexpr int kScoreGroup = 32;  // blocks a warp scores in a row: one id per lane
+
+// One CTA: one token, p.chunk cache blocks, all KV heads.  A warp takes one
+// KV head (the heads' records of a block are one contiguous range, read by the
+// CTA's warps at about the same time); with fewer heads than warps, several
+// warps share a head's blocks.
+//
+// kD / 16 lanes hold a record's 16 channels each, so that a warp reads 512 /
+// kD records with two 16-byte loads per lane, four such steps in flight.  The
+// codes of kG query heads stay in registers, with a byte mask of the negative
+// ones: the product's bound is picked by one logic operation per word, and a
+// word's four products are one dp4a -- 8 instructions per 16 channels and head,
+// 1/4 of the issue slots that the record's bytes leave at 4 heads.
 template <typename TQ, int kD, int kG>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : PA_SCORE_CTAS) score_kernel(const ScoreParams p) {
   constexpr int kLanes = kD / 16;
   constexpr int kRecs = 32 / kLanes;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % kLanes;
+  constexpr int kSteps = kScoreGroup / kRecs;
+  constexpr int kFlight = PA_SCORE_FLIGHT;  // steps whose loads are out together
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane % kLanes, rec = lane / kLanes;
   const int64_t t = p.t0 + blockIdx.y;
-  const int first = (int)blockIdx.x * kScoreBlocks;
+  const int first = (int)blockIdx.x * p.chunk;
+  const int sharing = max(1, kScoreWarps / p.num_kv_heads);  // warps of one head
   const TokenView tv = token_view(p.s, t, false);
   if (tv.blocks <= p.max_selected || first >= tv.blocks) return;  // all of them
-  const int last = min(first + kScoreBlocks, tv.blocks);
+  if (warp >= sharing * p.num_kv_heads) return;
+  const int last = min(first + p.chunk, tv.blocks);
+  const int kept_last = tv.blocks - p.keep_last;
   const int32_t* table = p.s.block_tables + (int64_t)tv.r * p.s.max_blocks_per_seq;
-  for (int h = warp; h < p.num_kv_heads; h += kScoreWarps) {
+  const int passes = (p.group + kG - 1) / kG;
+  for (int h = warp % p.num_kv_heads; h < p.num_kv_heads; h += kScoreWarps) {
     const TQ* qp = static_cast<const TQ*>(p.q) +
                    (t * p.num_q_heads + (int64_t)h * p.group) * kD + sub * 16;
-    // one scale for all heads of the group
-    float big = 0.f;
-    for (int g = 0; g < p.group; ++g)
+    // one scale for all heads of the group: each part of the warp looks at some
+    float x[16], big = 0.f;
+    for (int g = rec; g < p.group; g += kRecs) {
+      load16(qp + g * kD, x);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(to_f32(qp[g * kD + i])));
+      for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(x[i]));
+    }
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
+    for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
     const float sq = __fdiv_rn(big, 127.0f);
     uint32_t* keys = p.keys + ((int64_t)blockIdx.y * p.num_kv_heads + h) * p.row_scores;
-    for (int b0 = first; b0 < last; b0 += kRecs) {
-      const int b = b0 + lane / kLanes;
-      const bool kept = b < p.keep_first || b >= tv.blocks - p.keep_last;
-      int blk = b < last && !kept ? __ldg(table + b) : 0;
-      if (blk < 0 || (int64_t)blk >= p.s.num_blocks) {
-        if (sub == 0 && h == 0) flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
-        blk = 0;
-      }
-      const uint8_t* rec = p.bounds + ((int64_t)blk * p.num_kv_heads + h) * bounds_bytes(kD);
-      const uint4 hi = __ldg(reinterpret_cast<const uint4*>(rec + sub * 16));
-      const uint4 lo = __ldg(reinterpret_cast<const uint4*>(rec + kD + sub * 16));
-      const float sc = __ldg(reinterpret_cast<const float*>(rec + 2 * kD));
-      const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-      int best = INT_MIN;
-      for (int g = 0; g < p.group; ++g) {
-        int dot = 0;
+    for (int pass = 0; pass < passes; ++pass) {
+      // codes of the pass's heads (past the group's end: its last head again),
+      // each head's by one part of the warp
+      uint32_t code[kG][4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t code = 0, neg = 0;
+      for (int g0 = 0; g0 < kG; g0 += kRecs) {
+        uint32_t mine[4] = {0, 0, 0, 0};
+        if (g0 + rec < kG) {
+          load16(qp + min(pass * kG + g0 + rec, p.group - 1) * kD, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = to_f32(qp[g * kD + 4 * w + i]);
-            int c = sq > 0.f ? __float2int_rn(__fdiv_rn(x, sq)) : 0;
+          for (int i = 0; i < 16; ++i) {
+            int c = sq > 0.f ? __float2int_rn(__fdiv_rn(x[i], sq)) : 0;
             c = min(127, max(-127, c));
-            code |= ((uint32_t)c & 0xFFu) << (8 * i);
-            neg |= (c < 0 ? 0xFFu : 0u) << (8 * i);
+            mine[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
           }
-          dot = __dp4a((int)((hw[w] & ~neg) | (lw[w] & neg)), (int)code, dot);
         }
 #pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) dot += __shfl_xor_sync(~0u, dot, d);
-        best = max(best, dot);
+        for (int g = g0; g < g0 + kRecs && g < kG; ++g)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            code[g][w] = __shfl_sync(~0u, mine[w], (g - g0) * kLanes + sub);
       }
-      // + 0: a zero is a positive zero
-      if (sub == 0 && b < last)
-        keys[b] = kept ? kKeptKey : order_key(__fmul_rn((float)best, sc) + 0.0f);
+      for (int b0 = first + (warp / p.num_kv_heads) * kScoreGroup; b0 < last;
+           b0 += sharing * kScoreGroup) {
+        // the group's physical blocks, one per lane; kept blocks are not read
+        const int mb = b0 + lane;
+        const bool kept = mb < p.keep_first || mb >= kept_last;
+        int id = mb < last && !kept ? __ldg(table + mb) : -1;
+        if (id < -1 || (id == -1 && mb < last && !kept) || (int64_t)id >= p.s.num_blocks) {
+          flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
+          id = -1;
+        }
+        uint32_t mine = kKeptKey;  // lane l: the key of block b0 + l
+#pragma unroll
+        for (int s0 = 0; s0 < kSteps; s0 += kFlight) {
+          uint4 hi[kFlight], lo[kFlight];
+          float sc[kFlight];
+#pragma unroll
+          for (int f = 0; f < kFlight; ++f) {
+            const int blk = __shfl_sync(~0u, id, (s0 + f) * kRecs + rec);
+            hi[f] = lo[f] = make_uint4(0, 0, 0, 0);
+            sc[f] = 0.f;
+            if (blk >= 0) {
+              const uint8_t* r =
+                  p.bounds + ((int64_t)blk * p.num_kv_heads + h) * bounds_bytes(kD);
+              hi[f] = __ldg(reinterpret_cast<const uint4*>(r + sub * 16));
+              lo[f] = __ldg(reinterpret_cast<const uint4*>(r + kD + sub * 16));
+              sc[f] = __ldg(reinterpret_cast<const float*>(r + 2 * kD));
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < kFlight; ++f) {
+            const uint32_t hw[4] = {hi[f].x, hi[f].y, hi[f].z, hi[f].w};
+            const uint32_t lw[4] = {lo[f].x, lo[f].y, lo[f].z, lo[f].w};
+            int dot[kG];
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              dot[g] = 0;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t neg = sign_bytes(code[g][w]);
+                dot[g] = __dp4a((int)((hw[w] & ~neg) | (lw[w] & neg)), (int)code[g][w],
+                                dot[g]);
+              }
+            }
+            // sum over the record's lanes: while a lane holds several heads, it
+            // keeps one half of them and gives the other half away
+            int held = kG, bit = 1;
+#pragma unroll
+            for (; bit < kLanes; bit <<= 1) {
+              if (held > 1) {
+                held >>= 1;
+                const bool up = lane & bit;
+#pragma unroll
+                for (int g = 0; g < kG / 2; ++g)
+                  if (g < held) {
+                    const int give = up ? dot[g] : dot[g + held];
+                    const int keep = up ? dot[g + held] : dot[g];
+                    dot[g] = keep + __shfl_xor_sync(~0u, give, bit);
+                  }
+              } else {
+                dot[0] += __shfl_xor_sync(~0u, dot[0], bit);
+              }
+            }
+            int best = dot[0];
+#pragma unroll
+            for (int g = 1; g < kG; ++g)
+              if (g < held) best = max(best, dot[g]);
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1)
+              best = max(best, __shfl_xor_sync(~0u, best, d));
+            // to the lane of the block, as the score's key; with further passes
+            // over the group's heads, as the sum
+            const int from = (lane % kRecs) * kLanes;
+            const int b_best = __shfl_sync(~0u, best, from);
+            const float b_sc = __shfl_sync(~0u, sc[f], from);
+            if (lane / kRecs == s0 + f && id >= 0) {
+              int all = b_best;
+              if (pass > 0) all = max(all, (int)keys[mb]);
+              // + 0: a zero is a positive zero
+              mine = pass + 1 < passes
+                         ? (uint32_t)all
+                         : score_key(__fmul_rn((float)all, b_sc) + 0.0f);
+            }
+          }
+        }
+        if (mb < last) keys[mb] = id < 0 && !kept ? score_key(-INFINITY) : mine;
+      }
     }
   }
 }
@@ -272,17 +499,29 @@ struct TopkParams {
   int32_t* num_selected;
 };
 
-constexpr int kTopkThreads = 256;
+constexpr int kTopkThreads = 512;
+constexpr int kTopkWarps = kTopkThreads / 32;
+constexpr int kTopkBits = 10;  // of a key per round: two bins per thread
+constexpr int kTopkBins = 1 << kTopkBits;
 
-__global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p) {
-  __shared__ int hist[256];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  __shared__ int warp_above[kTopkThreads / 32], warp_equal[kTopkThreads / 32];
+// One CTA per (token, KV head).  The keys' range is cut into 1024 bins, the
+// bin that the K-th largest falls into becomes the next range, until a round
+// leaves only keys that are all taken (two or three rounds: the first range
+// is that of the row's own keys, so no round is spent on their common bits).
+// Then each warp writes the entries of its contiguous part of the row in
+// order.  kPer keys per lane are held in registers (up to 512 kPer blocks);
+// kPer = 0 reads them again each time.
+template <int kPer>
+__global__ void __launch_bounds__(kTopkThreads, 2) topk_kernel(const TopkParams p) {
+  __shared__ int hist[kTopkBins];
+  __shared__ uint32_t s_lo[kTopkWarps], s_hi[kTopkWarps];
+  __shared__ int s_warp[kTopkWarps], s_equal[kTopkWarps];
+  __shared__ int s_bin, s_need, s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = (int)(blockIdx.x % p.num_kv_heads);
   const int64_t tp = blockIdx.x / p.num_kv_heads, t = p.t0 + tp;
   const TokenView tv = token_view(p.s, t, h == 0 && tid == 0);
+  pdl_wait();  // the scores
   if (tv.blocks < 0) return;
   const int64_t row = t * p.num_kv_heads + h;
   int32_t* out = p.selected + row * p.max_selected;
@@ -293,77 +532,120 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p) 
     return;
   }
   const uint32_t* keys = p.keys + (tp * p.num_kv_heads + h) * p.row_scores;
-  // the K-th largest key, 8 bits at a time from the top
-  uint32_t prefix = 0;
-  int need = K;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kTopkThreads) {
-      const uint32_t k = keys[i];
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[(k >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // lane l owns bins 8 l .. 8 l + 7; keys in the lanes above it
-      int own = 0;
+  // the warp's part: part keys from begin on, 32 at a time
+  const int part = kPer ? 32 * kPer : ((n + kTopkWarps - 1) / kTopkWarps + 31) & ~31;
+  const int begin = min(n, warp * part), end = min(n, begin + part);
+  uint32_t held[kPer ? kPer : 1];
+  if constexpr (kPer > 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) own += hist[lane * 8 + i];
-      int above = own;
+    for (int j = 0; j < kPer; ++j) {
+      const int i = begin + 32 * j + lane;
+      held[j] = i < end ? keys[i] : 0u;
+    }
+  }
+  // f(key) for each of the lane's keys in order; every lane of the warp comes
+  // along (on: the key exists)
+  auto each = [&](auto&& f) {
+    if constexpr (kPer > 0) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (begin + 32 * j >= end) break;
+        const int i = begin + 32 * j + lane;
+        f(held[j], i, i < end);
+      }
+    } else {
+      for (int i0 = begin; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        f(i < end ? keys[i] : 0u, i, i < end);
+      }
+    }
+  };
+  // the range of the keys that are scores (the kept ones are above all)
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  int kept = 0;
+  each([&](uint32_t k, int, bool on) {
+    const bool score = on && k != kKeptKey;
+    kept += __popc(__ballot_sync(~0u, on && k == kKeptKey));
+    if (score) lo = min(lo, k), hi = max(hi, k);
+  });
+  lo = __reduce_min_sync(~0u, lo);
+  hi = __reduce_max_sync(~0u, hi);
+  if (lane == 0) s_lo[warp] = lo, s_hi[warp] = hi, s_warp[warp] = kept;
+  __syncthreads();
+  int need = K;
+#pragma unroll
+  for (int w = 0; w < kTopkWarps; ++w) {
+    lo = min(lo, s_lo[w]);
+    hi = max(hi, s_hi[w]);
+    need -= s_warp[w];
+  }
+  // Selected: the kept keys, those above the range [lo, lo + 2^bits), and the
+  // first `need` of those inside.  (need = 0, all kept: none inside.)
+  int bits = hi > lo ? 32 - __clz(hi - lo) : 0;
+  uint32_t top = hi;  // keys above are taken whole
+  if (need > 0) {
+    while (bits > 0) {
+      const int shift = max(0, bits - kTopkBits);
+      hist[tid] = hist[tid + kTopkThreads] = 0;
+      __syncthreads();
+      each([&](uint32_t k, int, bool on) {
+        if (on && k >= lo && k <= top) atomicAdd(&hist[(k - lo) >> shift], 1);
+      });
+      __syncthreads();
+      // keys in the bins above this thread's two
+      const int c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
+      int above = c0 + c1;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_down_sync(~0u, above, d);
         if (lane + d < 32) above += o;
       }
-      above -= own;
-      if (above < need && above + own >= need) {
-        for (int i = 7; i >= 0; --i) {
-          const int c = hist[lane * 8 + i];
-          if (above + c >= need) {
-            s_prefix = prefix | (uint32_t)(lane * 8 + i) << shift;
-            s_need = need - above;
-            break;
-          }
-          above += c;
-        }
+      if (lane == 0) s_warp[warp] = above;
+      __syncthreads();
+      above -= c0 + c1;
+      for (int w = warp + 1; w < kTopkWarps; ++w) above += s_warp[w];
+      if (above < need && above + c0 + c1 >= need) {
+        const bool second = above + c1 >= need;
+        s_bin = 2 * tid + (second ? 1 : 0);
+        s_need = need - above - (second ? 0 : c1);
+        s_count = second ? c1 : c0;
       }
+      __syncthreads();
+      lo += (uint32_t)s_bin << shift;
+      top = min(top, lo + (uint32_t)((1ull << shift) - 1));
+      need = s_need;
+      bits = shift;
+      if (s_count == need) break;  // all of the bin
+      __syncthreads();  // hist and s_* are written again
     }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
   }
-  // in order: the keys above, and the first `need` of the equal ones.  Each
-  // warp has a contiguous part of the row.
-  constexpr int kWarps = kTopkThreads / 32;
-  const int part = ((n + kWarps - 1) / kWarps + 31) & ~31;
-  const int lo = min(n, warp * part), hi = min(n, lo + part);
+  // in order: the keys above, and the first `need` of those inside
+  auto over = [&](uint32_t k) { return k > top; };
+  auto inside = [&](uint32_t k) { return k >= lo && k <= top; };
+  if (need == 0) lo = 0xFFFFFFFFu, top = 0xFFFFFFFEu;  // the kept keys alone
   int above = 0, equal = 0;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < hi ? keys[i] : 0u;
-    above += __popc(__ballot_sync(~0u, i < hi && k > prefix));
-    equal += __popc(__ballot_sync(~0u, i < hi && k == prefix));
-  }
-  if (lane == 0) warp_above[warp] = above, warp_equal[warp] = equal;
+  each([&](uint32_t k, int, bool on) {
+    above += __popc(__ballot_sync(~0u, on && over(k)));
+    equal += __popc(__ballot_sync(~0u, on && inside(k)));
+  });
+  __syncthreads();  // s_warp was read above
+  if (lane == 0) s_warp[warp] = above, s_equal[warp] = equal;
   __syncthreads();
   int at = 0, eq = 0;  // entries before this warp's part
   for (int w = 0; w < warp; ++w) {
-    at += warp_above[w];
-    eq += warp_equal[w];
+    at += s_warp[w];
+    eq += s_equal[w];
   }
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < hi ? keys[i] : 0u;
-    const unsigned gt = __ballot_sync(~0u, i < hi && k > prefix);
-    const unsigned ge = __ballot_sync(~0u, i < hi && k == prefix);
+  each([&](uint32_t k, int i, bool on) {
+    const unsigned gt = __ballot_sync(~0u, on && over(k));
+    const unsigned ge = __ballot_sync(~0u, on && inside(k));
     const unsigned below = (1u << lane) - 1;
-    const int e = eq + __popc(ge & below);  // equal keys before this one
+    const int e = eq + __popc(ge & below);  // keys inside before this one
     if ((gt >> lane & 1) || ((ge >> lane & 1) && e < need))
       out[at + __popc(gt & below) + min(e, need)] = i;
     at += __popc(gt);
     eq += __popc(ge);
-  }
+  });
 }
 
 template <int kPg, int kD>
@@ -372,12 +654,11 @@ cudaError_t launch_summarise_d(const StepView& s, const void* k_cache, int num_k
   // blocks a request of max_query_len tokens writes to, at most
   const int64_t wide = std::min<int64_t>((s.max_query_len + kBS - 2) / kBS + 1,
                                          (s.max_seq_len + kBS - 1) / kBS);
-  const int64_t items = wide * num_kv_heads * s.num_seqs;
-  const int64_t per_block = kThreads / (kD / 8);
-  const int64_t blocks = (items + per_block - 1) / per_block;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  summarise_kernel<kPg, kD><<<(unsigned)blocks, kThreads, 0, stream>>>(
-      s, k_cache, num_kv_heads, (int)wide, static_cast<uint8_t*>(bounds));
+  const int64_t per_seq = (wide * num_kv_heads + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t ctas = per_seq * s.num_seqs;
+  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  summarise_kernel<kPg, kD><<<(unsigned)ctas, kThreads, 0, stream>>>(
+      s, k_cache, num_kv_heads, (int)per_seq, static_cast<uint8_t*>(bounds));
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
@@ -391,16 +672,27 @@ cudaError_t launch_summarise_t(const StepView& s, const void* k_cache, int num_k
              : launch_summarise_d<kPg, 64>(s, k_cache, num_kv_heads, bounds, stream);
 }
 
-template <typename TQ>
-cudaError_t launch_score(const ScoreParams& p, int head_dim, dim3 grid,
-                         cudaStream_t stream) {
-  if (head_dim == 128)
-    score_kernel<TQ, 128, 1><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+template <typename TQ, int kD>
+cudaError_t launch_score_d(const ScoreParams& p, dim3 grid, cudaStream_t stream) {
+  // query heads held at once: the group's, up to 8 (more: in passes)
+  if (p.group == 1)
+    score_kernel<TQ, kD, 1><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+  else if (p.group == 2)
+    score_kernel<TQ, kD, 2><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+  else if (p.group <= 4)
+    score_kernel<TQ, kD, 4><<<grid, kScoreWarps * 32, 0, stream>>>(p);
   else
-    score_kernel<TQ, 64, 1><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+    score_kernel<TQ, kD, 8><<<grid, kScoreWarps * 32, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
+}
+
+template <typename TQ>
+cudaError_t launch_score(const ScoreParams& p, int head_dim, dim3 grid,
+                         cudaStream_t stream) {
+  return head_dim == 128 ? launch_score_d<TQ, 128>(p, grid, stream)
+                         : launch_score_d<TQ, 64>(p, grid, stream);
 }
 
 }  // namespace
@@ -461,8 +753,13 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
       p.keep_last = keep_last;
       p.row_scores = plan.row_scores;
       p.keys = static_cast<uint32_t*>(workspace);
-      const dim3 grid((unsigned)((max_blocks + kScoreBlocks - 1) / kScoreBlocks),
-                      (unsigned)nt);
+      // as many blocks per CTA as leave four CTAs per SM: a warp's work on the
+      // query (its codes) is then spread over more records
+      p.chunk = kScoreChunkMax;
+      while (p.chunk > kScoreGroup &&
+             nt * ((max_blocks + p.chunk - 1) / p.chunk) < 4ll * num_sms)
+        p.chunk /= 2;
+      const dim3 grid((unsigned)((max_blocks + p.chunk - 1) / p.chunk), (unsigned)nt);
       cudaError_t e;
       switch (q_dtype) {
         case PA_F32: e = launch_score<float>(p, head_dim, grid, stream); break;
@@ -481,8 +778,21 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
     tp.selected = selected;
     tp.num_selected = num_selected;
     if (nt * num_kv_heads > 0x7fffffffll) return cudaErrorInvalidValue;
-    topk_kernel<<<(unsigned)(nt * num_kv_heads), kTopkThreads, 0, stream>>>(tp);
-    const cudaError_t e = cudaGetLastError();
+    // starts while the scores are being made, waits for them
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(nt * num_kv_heads));
+    cfg.blockDim = dim3(kTopkThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = max_blocks > max_selected ? 1 : 0;
+    const cudaError_t e = max_blocks <= 4 * kTopkThreads
+                              ? cudaLaunchKernelEx(&cfg, topk_kernel<4>, tp)
+                          : max_blocks <= 16 * kTopkThreads
+                              ? cudaLaunchKernelEx(&cfg, topk_kernel<16>, tp)
+                              : cudaLaunchKernelEx(&cfg, topk_kernel<0>, tp);
     if (e != cudaSuccess) return e;
     count_launch();
   }
