@@ -4,11 +4,14 @@
 //   out = sum_j softmax(scale <q, k_j>)_j v_j  over the keys j of the listed
 //   blocks up to the token's own position; a list of no blocks gives zeros.
 //
-// A work unit is one (token, KV head, up to 16 of its query heads); its list
-// is cut into `splits` ranges when there are few units, and a second kernel
-// joins the ranges' partial results in order.
+// A row is one (token, KV head) with its list; all rows' list entries in a row,
+// end to end, are cut into equal shares, one CTA each, as many as are resident
+// (every CTA sums the rows' list lengths for itself).  A share holds whole
+// lists and, at its ends, parts of lists; a second kernel joins those, part by
+// part in order.  So a few long lists and many short ones both keep every SM
+// busy to the end.
 //
-// The unit reads each listed block's K and V page once and does 4 G multiply-
+// A row reads each listed block's K and V page once and does 4 G multiply-
 // adds per element read (G query heads): far below the tensor cores' rate, so
 // it is bound by HBM and the pages' latency.  Pages go from HBM straight into
 // the registers that feed the MMAs: with the keys as the rows of the first
@@ -21,26 +24,19 @@
 #include <algorithm>
 #include <type_traits>
 
-#include <cooperative_groups.h>
-
 #include "pa_common.cuh"
 #include "pa_internal.h"
-
-namespace cg = cooperative_groups;
 
 namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-#ifndef PA_SEL_AHEAD
-#define PA_SEL_AHEAD 2
-#endif
-constexpr int kAhead = PA_SEL_AHEAD;  // pages asked into L2 before their loads
 constexpr int kThreads = kWarps * 32;
-#ifndef PA_SEL_WAVES
-#define PA_SEL_WAVES 2
+constexpr int kJoinThreads = 256;  // 8 heads x 128 channels, four per thread
+#ifndef PA_SEL_SHARE
+#define PA_SEL_SHARE 8
 #endif
-constexpr int kSelWaves = PA_SEL_WAVES;
+constexpr int kMinShare = PA_SEL_SHARE;  // list entries of a CTA, at least
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum : int { kB16 = 0, kH16 = 1, kF8 = 2 };  // bf16, f16, E4M3 pages
@@ -51,36 +47,42 @@ struct SelParams {
   const void* k_cache;
   const void* v_cache;
   int num_q_heads, num_kv_heads, group;
-  int head_parts, cluster, splits;  // ranges of a list: cluster x splits
+  int head_rows;  // query heads of a KV head that one CTA takes (grid.y: parts)
   const int32_t* selected;
   const int32_t* num_selected;
   int max_selected;
   float scale, k_scale, v_scale;
   void* out;
-  float* part;     // [unit][split][head_rows][D]
-  float* part_ml;  // [unit][split][head_rows][2]: m, l
-  int head_rows;
+  // parts of lists, two per CTA: its first and its last (see write_part)
+  float* part;     // [CTA][2][head_rows][D]
+  float* part_ml;  // [CTA][2][head_rows][2]: m, l
+  int2* cut;       // [CTA]: the row whose list begins here and is cut (-1: none)
 };
 
-// Token t of a unit: its request, position and list length (-1: the token
-// belongs to no request, or its metadata is broken).
+// A row: its token, request, position and list length (-1: the token belongs
+// to no request, or its metadata is broken).
 struct Unit {
   int64_t t;
-  int h, part;  // KV head, part of its group
+  int h;
   int r, pos, count;
 };
 
-__device__ __forceinline__ Unit find_unit(const SelParams& p, int64_t unit, bool tell) {
+__device__ __forceinline__ Unit find_unit(const SelParams& p, int64_t row, bool tell) {
   Unit u;
-  u.part = (int)(unit % p.head_parts);
-  const int64_t th = unit / p.head_parts;
-  u.h = (int)(th % p.num_kv_heads);
-  u.t = th / p.num_kv_heads;
-  u.count = __ldg(p.num_selected + u.t * p.num_kv_heads + u.h);
-  u.r = warp_find_request(p.s.query_start_loc, p.s.num_seqs, u.t);
-  const ReqMeta m =
-      load_req(p.s.query_start_loc, p.s.seq_lens, u.r, p.s.num_tokens,
-               p.s.max_query_len, p.s.max_seq_len, p.s.max_blocks_per_seq);
+  u.t = row / p.num_kv_heads;
+  u.h = (int)(row - u.t * p.num_kv_heads);
+  u.count = __ldg(p.num_selected + row);
+  // requests of equally many tokens (a decode step's): t's place among the
+  // tokens names its request, one round of loads instead of a search's two or
+  // three before the request's own
+  u.r = (int)(u.t * p.s.num_seqs / p.s.num_tokens);
+  ReqMeta m = load_req(p.s.query_start_loc, p.s.seq_lens, u.r, p.s.num_tokens,
+                       p.s.max_query_len, p.s.max_seq_len, p.s.max_blocks_per_seq);
+  if (u.t < m.q0 || u.t >= (int64_t)m.q0 + m.n) {
+    u.r = warp_find_request(p.s.query_start_loc, p.s.num_seqs, u.t);
+    m = load_req(p.s.query_start_loc, p.s.seq_lens, u.r, p.s.num_tokens,
+                 p.s.max_query_len, p.s.max_seq_len, p.s.max_blocks_per_seq);
+  }
   u.pos = m.L - m.n + (int)(u.t - m.q0);
   if (u.t < m.q0 || u.t >= (int64_t)m.q0 + m.n) {
     u.count = -1;
@@ -154,8 +156,7 @@ __global__ void __launch_bounds__(kThreads) selected_generic_kernel(const SelPar
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x / p.num_q_heads;
   const int hq = (int)(blockIdx.x % p.num_q_heads);
-  Unit u = find_unit(p, (t * p.num_kv_heads + hq / p.group) * p.head_parts,
-                     threadIdx.x == 0);
+  const Unit u = find_unit(p, t * p.num_kv_heads + hq / p.group, threadIdx.x == 0);
   if (u.count < 0) return;
   const TQ* qp = static_cast<const TQ*>(p.q) + (t * p.num_q_heads + hq) * kD;
   float qv[kPer], acc[kPer], m = -INFINITY, l = 0.f;
@@ -226,27 +227,205 @@ struct PageTraits {
   static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8;
   static constexpr int kVChunks = kRowBytes / (8 * kVBytes);
   static constexpr int kTiles = kD / 16;  // m16 tiles of the output's channels
+  // Pages of one step: 8 KB of K and V in a warp's registers, whatever the
+  // type, are on their way while the step before is computed (one page of
+  // 8-bit types leaves half the bytes in flight: 57 instead of PLACEHOLDER us for 32 tokens'
+  // 256 blocks of 8 KV heads).
+  static constexpr int kPages = 4096 / (kBS * kRowBytes);
 };
 
+// CTAs per SM that the kernels are built for: what the accumulators of 8 (kNT
+// = 1) or 16 query heads leave of the registers
+constexpr int ctas_per_sm(int head_rows) { return head_rows == 8 ? 3 : 2; }
+
+// Entries of a row's list that count: none of a row past the last request.
+__device__ __forceinline__ int list_length(const SelParams& p, int64_t row) {
+  const int c = __ldg(p.num_selected + row);
+  return c > 0 && c <= p.max_selected ? c : 0;
+}
+
+// A CTA's share of all the rows' list entries.
+struct Share {
+  int64_t begin, end;  // entries
+  int64_t size;        // of every share
+  int64_t row;         // the row that `begin` lies in,
+  int64_t row_begin;   // and where its list begins
+};
+
+__device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// Every thread sums a contiguous part of the rows; the one whose part holds
+// the share's first entry walks it.
+__device__ __forceinline__ Share find_share(const SelParams& p, int64_t rows) {
+  __shared__ int64_t warp_sums[32], total, s_row, s_row_begin;
+  const int64_t part = (rows + kThreads - 1) / kThreads;
+  const int64_t lo = least(rows, threadIdx.x * part), hi = least(rows, lo + part);
+  int64_t sum = 0;
+  for (int64_t i = lo; i < hi; ++i) sum += list_length(p, i);
+  const int64_t before = block_scan_excl(sum, &total, warp_sums);
+  Share s;
+  s.size = (total + gridDim.x - 1) / gridDim.x;
+  if (s.size < kMinShare) s.size = kMinShare;
+  s.begin = least(total, blockIdx.x * s.size);
+  s.end = least(total, s.begin + s.size);
+  if (s.begin < s.end && s.begin >= before && s.begin < before + sum) {
+    int64_t at = before, i = lo;
+    for (int c; at + (c = list_length(p, i)) <= s.begin; ++i) at += c;
+    s_row = i;
+    s_row_begin = at;
+  }
+  __syncthreads();
+  s.row = s_row;
+  s.row_begin = s_row_begin;
+  return s;
+}
+
 template <typename TQ, int kPg, int kD, int kNT>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, int begin,
+                                            int end, int slot);
+
+template <typename TQ, int kPg, int kD, int kNT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * kNT))
 selected_kernel(const SelParams p) {
+  pdl_launch_dependents();
+  // rows of tokens up to the last request's
+  const int64_t last = __ldg(p.s.query_start_loc + p.s.num_seqs);
+  const int64_t tokens = last < 0 ? 0 : least(last, p.s.num_tokens);
+  const int64_t rows = tokens * p.num_kv_heads;
+  const Share sh = find_share(p, rows);
+  const int cta = blockIdx.y * gridDim.x + blockIdx.x;
+  int2 cut = make_int2(-1, 0);
+  int64_t at = sh.begin, row = sh.row, row_begin = sh.row_begin;
+  while (at < sh.end) {
+    const int64_t row_end = row_begin + list_length(p, row);
+    if (row_end > at) {
+      const int64_t end = least(row_end, sh.end);
+      const Unit u = find_unit(p, row, threadIdx.x == 0);
+      // -1: the whole list is here; else the CTA's place for a part: 0 for its
+      // first entry's row, 1 for the row that goes on in the next CTA
+      const int slot = at == row_begin && end == row_end ? -1 : at == sh.begin ? 0 : 1;
+      if (u.count > 0) {
+        attend_part<TQ, kPg, kD, kNT>(p, u, (int)(at - row_begin), (int)(end - row_begin),
+                                      slot);
+        if (at == row_begin && end < row_end)
+          // parts x 2 + the place of the first
+          cut = make_int2((int)row,
+                          (int)((row_end - 1) / sh.size - blockIdx.x + 1) * 2 + slot);
+      }
+      at = end;
+    }
+    row_begin = row_end;
+    ++row;
+  }
+  if (threadIdx.x == 0) p.cut[cta] = cut;
+}
+
+// Entries begin .. end - 1 of a row's list: to the output if that is all of it
+// (slot < 0), else to the CTA's place for a part.
+template <typename TQ, int kPg, int kD, int kNT>
+__device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, int begin,
+                                            int end, int slot) {
   using Tr = PageTraits<kPg, kD>;
   constexpr bool kBF = kPg == kB16;
-  constexpr int kRows = 8 * kNT;  // query heads of the unit, at most
+  constexpr int kRows = 8 * kNT;  // query heads, at most
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
-  // CTA (unit, split, rank): the ranks of one (unit, split) are a cluster
-  const int ranges = p.cluster * p.splits;
-  const int64_t unit = blockIdx.x / ranges;
-  const int range = (int)(blockIdx.x - unit * ranges);
-  pdl_launch_dependents();
-  const Unit u = find_unit(p, unit, range == 0 && threadIdx.x == 0);
-  if (u.count < 0) return;  // the whole cluster
-  const int heads = min(p.group - u.part * kRows, kRows);
-  const int head0 = u.h * p.group + u.part * kRows;
-  const int begin = (int)((int64_t)u.count * range / ranges);
-  const int end = (int)((int64_t)u.count * (range + 1) / ranges);
+  const int part = blockIdx.y;
+  const int heads = min(p.group - part * kRows, kRows);
+  const int head0 = u.h * p.group + part * kRows;
+
+  float acc[kNT][Tr::kTiles][4];
+  float m[kNT][2], l[kNT][2];
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < Tr::kTiles; ++i)
+      acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+
+  constexpr int kP = Tr::kPages;
+  uint4 kr[kP][2][Tr::kKChunks];
+  uint32_t vr[kP][4][Tr::kVChunks][Tr::kVBytes / 4];
+  constexpr int64_t kPageBytes = kBS * (int64_t)Tr::kRowBytes;
+  const uint8_t* kbase = static_cast<const uint8_t*>(p.k_cache) + (int64_t)u.h * kPageBytes;
+  const uint8_t* vbase = static_cast<const uint8_t*>(p.v_cache) + (int64_t)u.h * kPageBytes;
+  const int64_t block_bytes = kPageBytes * p.num_kv_heads;
+  const int koff = r * Tr::kRowBytes + c * 16;
+
+  // keys of a page up to the token's position
+  auto page_keys = [&](const Entry& e) {
+    return e.phys < 0 ? 0 : min(kBS, u.pos - e.block * kBS + 1);
+  };
+  auto load_k = [&](const Entry (&en)[kP]) {
+#pragma unroll
+    for (int g = 0; g < kP; ++g) {
+      const uint8_t* src = kbase + (int64_t)max(en[g].phys, 0) * block_bytes + koff;
+      const bool on = en[g].phys >= 0;
+#pragma unroll
+      for (int i = 0; i < Tr::kKChunks; ++i) {
+        kr[g][0][i] = kr[g][1][i] = make_uint4(0, 0, 0, 0);
+        if (on) {
+          kr[g][0][i] = __ldg(reinterpret_cast<const uint4*>(src + 64 * i));
+          kr[g][1][i] =
+              __ldg(reinterpret_cast<const uint4*>(src + 8 * Tr::kRowBytes + 64 * i));
+        }
+      }
+    }
+  };
+  // a row past the position holds nothing yet (its bits may be anything): 0
+  auto load_v = [&](const Entry (&en)[kP]) {
+#pragma unroll
+    for (int g = 0; g < kP; ++g) {
+      const uint8_t* src =
+          vbase + (int64_t)max(en[g].phys, 0) * block_bytes + r * Tr::kVBytes;
+      const int keys = page_keys(en[g]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = 2 * c + (j & 1) + 8 * (j >> 1);
+#pragma unroll
+        for (int i = 0; i < Tr::kVChunks; ++i) {
+          const uint8_t* at = src + key * Tr::kRowBytes + i * 8 * Tr::kVBytes;
+          if constexpr (Tr::kVBytes == 16) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (key < keys) v = __ldg(reinterpret_cast<const uint4*>(at));
+            vr[g][j][i][0] = v.x; vr[g][j][i][1] = v.y;
+            vr[g][j][i][2] = v.z; vr[g][j][i][3] = v.w;
+          } else {
+            uint2 v = make_uint2(0, 0);
+            if (key < keys) v = __ldg(reinterpret_cast<const uint2*>(at));
+            vr[g][j][i][0] = v.x; vr[g][j][i][1] = v.y;
+          }
+        }
+      }
+    }
+  };
+
+  // The warp's steps: kP entries in a row from begin + kP warp, then kP kWarps
+  // further on.  The lanes hold the next 32 of the warp's entries.
+  const int first = begin + kP * warp;
+  const int steps = end > first ? (end - first + kP * kWarps - 1) / (kP * kWarps) : 0;
+  Entry held{0, -1};
+  auto entries = [&](int step, Entry (&en)[kP]) {
+    const int i = step * kP;  // of the warp's entries
+    if ((i & 31) == 0) {
+      const int mine = i + lane;
+      const int at = first + (mine / kP) * (kP * kWarps) + mine % kP;
+      held = Entry{0, -1};
+      if (at < end) held = list_entry(p, u, at);
+    }
+#pragma unroll
+    for (int g = 0; g < kP; ++g)
+      en[g] = Entry{__shfl_sync(~0u, held.block, (i & 31) + g),
+                    __shfl_sync(~0u, held.phys, (i & 31) + g)};
+  };
+  Entry cur[kP];
+  if (steps > 0) {
+    entries(0, cur);
+    load_k(cur);
+    load_v(cur);
+  }
 
   // Q operand words, in the channel order of the lane's K words.  Over FP8
   // pages the products are in f16: a power of two brings the unit's largest
@@ -264,9 +443,14 @@ selected_kernel(const SelParams p) {
         const int hd = nt * 8 + r;
         const TQ* src = static_cast<const TQ*>(p.q) +
                         (u.t * p.num_q_heads + head0 + hd) * kD + (c + 4 * i) * kE;
+        uint4 w[kE / 8];
+#pragma unroll
+        for (int e = 0; e < kE / 8; ++e)
+          w[e] = hd < heads ? __ldg(reinterpret_cast<const uint4*>(src) + e)
+                            : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
-          x[nt][i][e] = hd < heads ? to_f32(src[e]) : 0.f;
+          x[nt][i][e] = to_f32(reinterpret_cast<const TQ*>(w)[e]);
           big = fmaxf(big, fabsf(x[nt][i][e]));
         }
       }
@@ -289,133 +473,60 @@ selected_kernel(const SelParams p) {
           qw[nt][i][w] = pack2<kBF>(x[nt][i][2 * w] * down, x[nt][i][2 * w + 1] * down);
   }
 
-  float acc[kNT][Tr::kTiles][4];
-  float m[kNT][2], l[kNT][2];
-#pragma unroll
-  for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < Tr::kTiles; ++i)
-      acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.f;
-  }
-
-  uint4 kr[2][Tr::kKChunks];
-  uint32_t vr[4][Tr::kVChunks][Tr::kVBytes / 4];
-  constexpr int64_t kPageBytes = kBS * (int64_t)Tr::kRowBytes;
-  const uint8_t* kbase = static_cast<const uint8_t*>(p.k_cache) + (int64_t)u.h * kPageBytes;
-  const uint8_t* vbase = static_cast<const uint8_t*>(p.v_cache) + (int64_t)u.h * kPageBytes;
-  const int64_t block_bytes = kPageBytes * p.num_kv_heads;
-  const int koff = r * Tr::kRowBytes + c * 16;
-
-  // keys of a page up to the token's position
-  auto page_keys = [&](const Entry& e) {
-    return e.phys < 0 ? 0 : min(kBS, u.pos - e.block * kBS + 1);
-  };
-  auto load_k = [&](const Entry& e) {
-    const uint8_t* src = kbase + (int64_t)max(e.phys, 0) * block_bytes + koff;
-    const bool on = e.phys >= 0;
-#pragma unroll
-    for (int i = 0; i < Tr::kKChunks; ++i) {
-      kr[0][i] = kr[1][i] = make_uint4(0, 0, 0, 0);
-      if (on) {
-        kr[0][i] = __ldg(reinterpret_cast<const uint4*>(src + 64 * i));
-        kr[1][i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * Tr::kRowBytes + 64 * i));
-      }
-    }
-  };
-  // a row past the position holds nothing yet (its bits may be anything): 0
-  auto load_v = [&](const Entry& e) {
-    const uint8_t* src =
-        vbase + (int64_t)max(e.phys, 0) * block_bytes + r * Tr::kVBytes;
-    const int keys = page_keys(e);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int key = 2 * c + (j & 1) + 8 * (j >> 1);
-#pragma unroll
-      for (int i = 0; i < Tr::kVChunks; ++i) {
-        const uint8_t* at = src + key * Tr::kRowBytes + i * 8 * Tr::kVBytes;
-        if constexpr (Tr::kVBytes == 16) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (key < keys) v = __ldg(reinterpret_cast<const uint4*>(at));
-          vr[j][i][0] = v.x; vr[j][i][1] = v.y; vr[j][i][2] = v.z; vr[j][i][3] = v.w;
-        } else {
-          uint2 v = make_uint2(0, 0);
-          if (key < keys) v = __ldg(reinterpret_cast<const uint2*>(at));
-          vr[j][i][0] = v.x; vr[j][i][1] = v.y;
-        }
-      }
-    }
-  };
-
-  // the warp's entries, 32 at a time: begin + warp, + kWarps, ...
-  const int mine = end - begin > warp ? (end - begin - warp + kWarps - 1) / kWarps : 0;
-  Entry held{0, -1};
-  auto entry = [&](int i) {  // the warp's entry i, in order
-    if ((i & 31) == 0) {
-      const int at = begin + warp + (i + lane) * kWarps;
-      held = Entry{0, -1};
-      if (i + lane < mine) held = list_entry(p, u, at);
-    }
-    // one lane asks a later page into L2: loads in flight beyond the registers
-    if (kAhead > 0 && lane == ((i + kAhead) & 31) && lane >= kAhead && held.phys >= 0) {
-      bulk_prefetch_l2(kbase + held.phys * block_bytes, (uint32_t)kPageBytes);
-      bulk_prefetch_l2(vbase + held.phys * block_bytes, (uint32_t)kPageBytes);
-    }
-    return Entry{__shfl_sync(~0u, held.block, i & 31), __shfl_sync(~0u, held.phys, i & 31)};
-  };
-  Entry cur{0, -1};
-  if (mine > 0) {
-    cur = entry(0);
-    load_k(cur);
-    load_v(cur);
-  }
-  for (int i = 0; i < mine; ++i) {
-    const int keys = page_keys(cur);
+  for (int i = 0; i < steps; ++i) {
     // S^T = K Q^T: keys r and r + 8, heads 2c and 2c + 1
-    float s[kNT][4];
+    float s[kP][kNT][4];
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    for (int g = 0; g < kP; ++g) {
 #pragma unroll
-    for (int ch = 0; ch < Tr::kKChunks; ++ch) {
-      const uint32_t w0[4] = {kr[0][ch].x, kr[0][ch].y, kr[0][ch].z, kr[0][ch].w};
-      const uint32_t w1[4] = {kr[1][ch].x, kr[1][ch].y, kr[1][ch].z, kr[1][ch].w};
-      if constexpr (kPg == kF8) {
+      for (int nt = 0; nt < kNT; ++nt)
+        s[g][nt][0] = s[g][nt][1] = s[g][nt][2] = s[g][nt][3] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a[4];
-          e4m3x4_to_f16x2x2(w0[w], a[0], a[2]);
-          e4m3x4_to_f16x2x2(w1[w], a[1], a[3]);
+      for (int ch = 0; ch < Tr::kKChunks; ++ch) {
+        const uint32_t w0[4] = {kr[g][0][ch].x, kr[g][0][ch].y, kr[g][0][ch].z, kr[g][0][ch].w};
+        const uint32_t w1[4] = {kr[g][1][ch].x, kr[g][1][ch].y, kr[g][1][ch].z, kr[g][1][ch].w};
+        if constexpr (kPg == kF8) {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-            mma16816<false>(s[nt], a, qw[nt][ch][2 * w], qw[nt][ch][2 * w + 1]);
-        }
-      } else {
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a[4];
+            e4m3x4_to_f16x2x2(w0[w], a[0], a[2]);
+            e4m3x4_to_f16x2x2(w1[w], a[1], a[3]);
 #pragma unroll
-        for (int w = 0; w < 4; w += 2) {
-          const uint32_t a[4] = {w0[w], w1[w], w0[w + 1], w1[w + 1]};
+            for (int nt = 0; nt < kNT; ++nt)
+              mma16816<false>(s[g][nt], a, qw[nt][ch][2 * w], qw[nt][ch][2 * w + 1]);
+          }
+        } else {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-            mma16816<kBF>(s[nt], a, qw[nt][ch][w], qw[nt][ch][w + 1]);
+          for (int w = 0; w < 4; w += 2) {
+            const uint32_t a[4] = {w0[w], w1[w], w0[w + 1], w1[w + 1]};
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+              mma16816<kBF>(s[g][nt], a, qw[nt][ch][w], qw[nt][ch][w + 1]);
+          }
         }
       }
     }
-    Entry next{0, -1};
-    if (i + 1 < mine) {
-      next = entry(i + 1);
-      load_k(next);
+    int keys[kP];
+#pragma unroll
+    for (int g = 0; g < kP; ++g) keys[g] = page_keys(cur[g]);
+    if (i + 1 < steps) {
+      entries(i + 1, cur);
+      load_k(cur);
     }
-    // softmax over the page
-    uint32_t pb[kNT][2];
+    // softmax over the step's keys
+    uint32_t pb[kP][kNT][2];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        s[nt][j] = r + 8 * (j >> 1) < keys ? s[nt][j] * score_scale : -INFINITY;
-      float mx[2];
+      for (int g = 0; g < kP; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[g][nt][j] = r + 8 * (j >> 1) < keys[g] ? s[g][nt][j] * score_scale : -INFINITY;
+          mx[j & 1] = fmaxf(mx[j & 1], s[g][nt][j]);
+        }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        mx[j] = fmaxf(s[nt][j], s[nt][j + 2]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(~0u, mx[j], d));
         mx[j] = fmaxf(mx[j], m[nt][j]);
@@ -438,48 +549,52 @@ selected_kernel(const SelParams p) {
       }
       const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
       const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-      const float p0 = exp2f(s[nt][0] - m0), p1 = exp2f(s[nt][1] - m1);
-      const float p2 = exp2f(s[nt][2] - m0), p3 = exp2f(s[nt][3] - m1);
-      l[nt][0] += p0 + p2;
-      l[nt][1] += p1 + p3;
-      // keys as rows -> heads as rows: the second product's operand
-      pb[nt][0] = transpose8x8(pack2<kBF>(p0, p1));
-      pb[nt][1] = transpose8x8(pack2<kBF>(p2, p3));
+#pragma unroll
+      for (int g = 0; g < kP; ++g) {
+        const float p0 = exp2f(s[g][nt][0] - m0), p1 = exp2f(s[g][nt][1] - m1);
+        const float p2 = exp2f(s[g][nt][2] - m0), p3 = exp2f(s[g][nt][3] - m1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        // keys as rows -> heads as rows: the second product's operand
+        pb[g][nt][0] = transpose8x8(pack2<kBF>(p0, p1));
+        pb[g][nt][1] = transpose8x8(pack2<kBF>(p2, p3));
+      }
     }
     // O^T += V^T P^T: channels as rows
 #pragma unroll
-    for (int ch = 0; ch < Tr::kVChunks; ++ch)
+    for (int g = 0; g < kP; ++g)
 #pragma unroll
-      for (int w = 0; w < Tr::kVBytes / 4; ++w) {
-        const uint32_t a0 = vr[0][ch][w], a1 = vr[1][ch][w];
-        const uint32_t a2 = vr[2][ch][w], a3 = vr[3][ch][w];
-        if constexpr (kPg == kF8) {
-          // four channels of two keys: bytes of the two rows side by side
-          const uint32_t l01 = __byte_perm(a0, a1, 0x5140), h01 = __byte_perm(a0, a1, 0x7362);
-          const uint32_t l23 = __byte_perm(a2, a3, 0x5140), h23 = __byte_perm(a2, a3, 0x7362);
-          uint32_t x[4], y[4];
-          e4m3x4_to_f16x2x2(l01, x[0], x[1]);
-          e4m3x4_to_f16x2x2(h01, x[2], x[3]);
-          e4m3x4_to_f16x2x2(l23, y[0], y[1]);
-          e4m3x4_to_f16x2x2(h23, y[2], y[3]);
+      for (int ch = 0; ch < Tr::kVChunks; ++ch)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {x[2 * k], x[2 * k + 1], y[2 * k], y[2 * k + 1]};
+        for (int w = 0; w < Tr::kVBytes / 4; ++w) {
+          const uint32_t a0 = vr[g][0][ch][w], a1 = vr[g][1][ch][w];
+          const uint32_t a2 = vr[g][2][ch][w], a3 = vr[g][3][ch][w];
+          if constexpr (kPg == kF8) {
+            // four channels of two keys: bytes of the two rows side by side
+            const uint32_t l01 = __byte_perm(a0, a1, 0x5140), h01 = __byte_perm(a0, a1, 0x7362);
+            const uint32_t l23 = __byte_perm(a2, a3, 0x5140), h23 = __byte_perm(a2, a3, 0x7362);
+            uint32_t x[4], y[4];
+            e4m3x4_to_f16x2x2(l01, x[0], x[1]);
+            e4m3x4_to_f16x2x2(h01, x[2], x[3]);
+            e4m3x4_to_f16x2x2(l23, y[0], y[1]);
+            e4m3x4_to_f16x2x2(h23, y[2], y[3]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {x[2 * k], x[2 * k + 1], y[2 * k], y[2 * k + 1]};
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt)
+                mma16816<false>(acc[nt][(ch * (Tr::kVBytes / 4) + w) * 2 + k], a,
+                                pb[g][nt][0], pb[g][nt][1]);
+            }
+          } else {
+            const uint32_t a[4] = {__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632),
+                                   __byte_perm(a2, a3, 0x5410), __byte_perm(a2, a3, 0x7632)};
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma16816<false>(acc[nt][(ch * (Tr::kVBytes / 4) + w) * 2 + k], a, pb[nt][0],
-                              pb[nt][1]);
+              mma16816<kBF>(acc[nt][ch * (Tr::kVBytes / 4) + w], a, pb[g][nt][0], pb[g][nt][1]);
           }
-        } else {
-          const uint32_t a[4] = {__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632),
-                                 __byte_perm(a2, a3, 0x5410), __byte_perm(a2, a3, 0x7632)};
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-            mma16816<kBF>(acc[nt][ch * (Tr::kVBytes / 4) + w], a, pb[nt][0], pb[nt][1]);
         }
-      }
-    if (i + 1 < mine) load_v(next);
-    cur = next;
+    if (i + 1 < steps) load_v(cur);
   }
 
   // the four warps' results, joined in shared memory.  Tile tl of lane (r, c):
@@ -507,94 +622,101 @@ selected_kernel(const SelParams p) {
     }
   }
   __syncthreads();
-  // the CTA's result into the place of warp 0's (each thread reads and writes
-  // its own elements), then the cluster's from all of its CTAs
   for (int i = threadIdx.x; i < heads * kD; i += kThreads) {
     const int hd = i / kD, d = i - hd * kD;
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][hd]);
-    float a = 0.f;
+    float a = 0.f, ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      a += (s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx)) * s_acc[w][hd][d];
-    s_acc[0][hd][d] = a;
-  }
-  __shared__ float s_ml[kRows][2];
-  if (threadIdx.x < heads) {
-    const int hd = threadIdx.x;
-    float mx = -INFINITY, ls = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][hd]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      ls += (s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx)) * s_l[w][hd];
-    s_ml[hd][0] = mx;
-    s_ml[hd][1] = ls;
-  }
-  cg::cluster_group cl = cg::this_cluster();
-  if (p.cluster > 1) cl.sync(); else __syncthreads();
-  const int rank = p.cluster > 1 ? (int)cl.block_rank() : 0;
-  for (int i = rank * kThreads + threadIdx.x; i < heads * kD; i += p.cluster * kThreads) {
-    const int hd = i / kD, d = i - hd * kD;
-    float mx = s_ml[hd][0], ls = s_ml[hd][1], a = s_acc[0][hd][d];
-    if (p.cluster > 1) {
-      mx = -INFINITY;
-      for (int c2 = 0; c2 < p.cluster; ++c2)
-        mx = fmaxf(mx, *cl.map_shared_rank(&s_ml[hd][0], c2));
-      ls = a = 0.f;
-      for (int c2 = 0; c2 < p.cluster; ++c2) {
-        const float ms = *cl.map_shared_rank(&s_ml[hd][0], c2);
-        const float f = ms == -INFINITY ? 0.f : exp2f(ms - mx);
-        ls += f * *cl.map_shared_rank(&s_ml[hd][1], c2);
-        a += f * *cl.map_shared_rank(&s_acc[0][hd][d], c2);
-      }
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx);
+      a += f * s_acc[w][hd][d];
+      ls += f * s_l[w][hd];
     }
-    if (p.splits == 1) {
+    if (slot < 0) {
       static_cast<TQ*>(p.out)[(u.t * p.num_q_heads + head0 + hd) * kD + d] =
           from_f32<TQ>(ls == 0.f ? 0.f : a / ls * p.v_scale);
     } else {
-      const int64_t row = (unit * p.splits + range / p.cluster) * p.head_rows + hd;
-      p.part[row * kD + d] = a;
+      const int64_t at =
+          ((int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 2 + slot) * p.head_rows + hd;
+      p.part[at * kD + d] = a;
       if (d == 0) {
-        p.part_ml[2 * row] = mx;
-        p.part_ml[2 * row + 1] = ls;
+        p.part_ml[2 * at] = mx;
+        p.part_ml[2 * at + 1] = ls;
       }
     }
   }
-  if (p.cluster > 1) cl.sync();  // the others may still read this CTA's memory
+  __syncthreads();  // the next part writes the shared memory again
 }
 
-// Join a unit's splits in order: one warp per (unit, query head).
+// Behind the shares: CTA i joins the list that begins in share i and is cut
+// (the part there, then the first part of each share it goes on through), and
+// writes the zeros of the rows i, i + gridDim.x, .. whose list is empty.
 template <typename TQ, int kD>
-__global__ void __launch_bounds__(kThreads) selected_join_kernel(const SelParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t units = p.s.num_tokens * p.num_kv_heads * p.head_parts;
-  const int64_t unit = item / p.head_rows;
-  const int hd = (int)(item - unit * p.head_rows);
-  if (unit >= units) return;
-  const Unit u = find_unit(p, unit, false);
-  pdl_wait();  // the splits' results
-  if (u.count < 0 || hd >= min(p.group - u.part * p.head_rows, p.head_rows)) return;
-  const int64_t row0 = unit * p.splits * p.head_rows + hd;
-  float mx = -INFINITY;
-  for (int s = 0; s < p.splits; ++s)
-    mx = fmaxf(mx, p.part_ml[2 * (row0 + (int64_t)s * p.head_rows)]);
-  float a[kD / 32] = {}, ls = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t row = row0 + (int64_t)s * p.head_rows;
-    const float ms = p.part_ml[2 * row];
-    const float f = ms == -INFINITY ? 0.f : exp2f(ms - mx);
-    ls += f * p.part_ml[2 * row + 1];
-#pragma unroll
-    for (int k = 0; k < kD / 32; ++k) a[k] += f * p.part[row * kD + lane + 32 * k];
+__global__ void __launch_bounds__(kJoinThreads) selected_join_kernel(const SelParams p) {
+  const int part = blockIdx.y;
+  const int64_t rows = p.s.num_tokens * p.num_kv_heads;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    if (list_length(p, row) > 0) continue;
+    const Unit u = find_unit(p, row, part == 0 && threadIdx.x == 0);
+    if (u.count < 0) continue;
+    const int heads = min(p.group - part * p.head_rows, p.head_rows);
+    TQ* out = static_cast<TQ*>(p.out) +
+              (u.t * p.num_q_heads + u.h * p.group + part * p.head_rows) * kD;
+    for (int i = threadIdx.x; i < heads * kD; i += kJoinThreads) out[i] = from_f32<TQ>(0.f);
   }
-  TQ* out = static_cast<TQ*>(p.out) +
-            (u.t * p.num_q_heads + u.h * p.group + u.part * p.head_rows + hd) * kD;
+  pdl_wait();  // the shares' results
+  const int cta = part * gridDim.x + blockIdx.x;
+  const int2 cut = p.cut[cta];
+  if (cut.x < 0) return;
+  const int64_t t = cut.x / p.num_kv_heads;
+  const int h = (int)(cut.x - t * p.num_kv_heads);
+  const int heads = min(p.group - part * p.head_rows, p.head_rows);
+  // the list's parts: place 0 or 1 of this share, place 0 of the next ones
+  const int parts = cut.y / 2;
+  auto place = [&](int k) {
+    return (2 * (int64_t)(cta + k) + (k == 0 ? cut.y % 2 : 0)) * p.head_rows;
+  };
+  // four channels per thread; the parts' loads go out together, four at a time
+  constexpr int kQuads = kD / 4, kBatch = 4;
+  for (int i = threadIdx.x; i < heads * kQuads; i += kJoinThreads) {
+    const int hd = i / kQuads, d = (i - hd * kQuads) * 4;
+    float mx = -INFINITY, ls = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
 #pragma unroll
-  for (int k = 0; k < kD / 32; ++k)
-    out[lane + 32 * k] = from_f32<TQ>(ls == 0.f ? 0.f : a[k] / ls * p.v_scale);
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t at = place(min(k0 + j, parts - 1)) + hd;
+        ml[j] = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+        v[j] = *reinterpret_cast<const float4*>(p.part + at * kD + d);
+      }
+      float top = mx;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, ml[j].x);
+      const float old = mx == -INFINITY ? 0.f : exp2f(mx - top);
+      ls *= old;
+      a = make_float4(a.x * old, a.y * old, a.z * old, a.w * old);
+      mx = top;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float f =
+            k0 + j >= parts || ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - top);
+        ls = fmaf(f, ml[j].y, ls);
+        a.x = fmaf(f, v[j].x, a.x);
+        a.y = fmaf(f, v[j].y, a.y);
+        a.z = fmaf(f, v[j].z, a.z);
+        a.w = fmaf(f, v[j].w, a.w);
+      }
+    }
+    TQ* out = static_cast<TQ*>(p.out) +
+              (t * p.num_q_heads + h * p.group + part * p.head_rows + hd) * kD + d;
+    const float o[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = from_f32<TQ>(ls == 0.f ? 0.f : o[e] / ls * p.v_scale);
+  }
 }
 
 cudaError_t launched() {
@@ -604,8 +726,7 @@ cudaError_t launched() {
 }
 
 template <typename TQ, typename TP>
-cudaError_t launch_generic(SelParams& p, int head_dim, cudaStream_t stream) {
-  p.head_parts = 1;
+cudaError_t launch_generic(const SelParams& p, int head_dim, cudaStream_t stream) {
   const int64_t grid = p.s.num_tokens * p.num_q_heads;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   if (head_dim == 128)
@@ -616,29 +737,22 @@ cudaError_t launch_generic(SelParams& p, int head_dim, cudaStream_t stream) {
 }
 
 template <typename TQ, int kPg, int kD>
-cudaError_t launch_mma_d(const SelParams& p, int64_t units, cudaStream_t stream) {
-  const int64_t grid = units * p.cluster * p.splits;
-  const int64_t join = (units * p.head_rows + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffffll || join > 0x7fffffffll) return cudaErrorInvalidValue;
+cudaError_t launch_mma_d(const SelParams& p, const SelectedPlan& plan, cudaStream_t stream) {
+  const dim3 grid((unsigned)plan.shares, (unsigned)plan.head_parts);
+  if (p.head_rows == 8)
+    selected_kernel<TQ, kPg, kD, 1><<<grid, kThreads, 0, stream>>>(p);
+  else
+    selected_kernel<TQ, kPg, kD, 2><<<grid, kThreads, 0, stream>>>(p);
+  cudaError_t e = launched();
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-  cudaError_t e = p.head_rows == 8
-                      ? cudaLaunchKernelEx(&cfg, selected_kernel<TQ, kPg, kD, 1>, p)
-                      : cudaLaunchKernelEx(&cfg, selected_kernel<TQ, kPg, kD, 2>, p);
-  if (e != cudaSuccess) return e;
-  count_launch();
-  if (p.splits == 1) return cudaSuccess;
-  cfg.gridDim = dim3((unsigned)join);
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, selected_join_kernel<TQ, kD>, p);
   if (e == cudaSuccess) count_launch();
@@ -646,10 +760,10 @@ cudaError_t launch_mma_d(const SelParams& p, int64_t units, cudaStream_t stream)
 }
 
 template <typename TQ, int kPg>
-cudaError_t launch_mma(const SelParams& p, int head_dim, int64_t units,
+cudaError_t launch_mma(const SelParams& p, int head_dim, const SelectedPlan& plan,
                        cudaStream_t stream) {
-  return head_dim == 128 ? launch_mma_d<TQ, kPg, 128>(p, units, stream)
-                         : launch_mma_d<TQ, kPg, 64>(p, units, stream);
+  return head_dim == 128 ? launch_mma_d<TQ, kPg, 128>(p, plan, stream)
+                         : launch_mma_d<TQ, kPg, 64>(p, plan, stream);
 }
 
 }  // namespace
@@ -660,21 +774,15 @@ SelectedPlan make_selected_plan(int64_t num_tokens, int num_q_heads, int num_kv_
   const int group = num_q_heads / num_kv_heads;
   pl.head_rows = group <= 8 ? 8 : 16;
   pl.head_parts = (group + pl.head_rows - 1) / pl.head_rows;
-  pl.units = num_tokens * num_kv_heads * pl.head_parts;
-  // Ranges per list: until the grid is kSelWaves CTAs per SM, of two pages per
-  // warp at least.  Up to 8 (a portable cluster) are joined through the
-  // cluster's shared memory; beyond that, clusters through the workspace.
-  const int64_t want = (int64_t)kSelWaves * num_sms;
-  const int64_t most = std::max(1, max_selected / (2 * kWarps));
-  int64_t ranges = pl.units > 0 ? (want + pl.units - 1) / pl.units : 1;
-  ranges = std::max<int64_t>(1, std::min(ranges, most));
-  pl.cluster = 1;
-  while (pl.cluster < 8 && pl.cluster < ranges) pl.cluster *= 2;
-  if (pl.cluster > most) pl.cluster /= 2;
-  pl.splits = ranges > 8 ? (int)((ranges + 7) / 8) : 1;
-  pl.bytes = pl.splits == 1 ? 0
-                            : pl.units * pl.splits * pl.head_rows * (head_dim + 2) *
-                                  (int64_t)sizeof(float);
+  // a share per resident CTA, fewer where shares would be below kMinShare
+  const int64_t entries = num_tokens * num_kv_heads * (int64_t)max_selected;
+  const int64_t slots = (int64_t)ctas_per_sm(pl.head_rows) * num_sms;
+  pl.shares = std::min(std::max<int64_t>(1, slots / pl.head_parts),
+                       (entries + kMinShare - 1) / kMinShare);
+  const int64_t parts = 2 * pl.shares * pl.head_parts * pl.head_rows;
+  pl.off_ml = parts * head_dim * (int64_t)sizeof(float);
+  pl.off_cut = pl.off_ml + parts * 2 * (int64_t)sizeof(float);
+  pl.bytes = pl.off_cut + pl.shares * pl.head_parts * (int64_t)sizeof(int2);
   return pl;
 }
 
@@ -688,10 +796,7 @@ cudaError_t launch_attention_selected(const StepView& s, const SelectedPlan& pla
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.num_kv_heads;
   p.group = a.num_q_heads / a.num_kv_heads;
-  p.head_parts = plan.head_parts;
   p.head_rows = plan.head_rows;
-  p.cluster = plan.cluster;
-  p.splits = plan.splits;
   p.selected = a.selected;
   p.num_selected = a.num_selected;
   p.max_selected = a.max_selected;
@@ -700,18 +805,19 @@ cudaError_t launch_attention_selected(const StepView& s, const SelectedPlan& pla
   p.k_scale = scaled ? a.k_scale : 1.0f;
   p.v_scale = scaled ? a.v_scale : 1.0f;
   p.out = a.out;
-  p.part = static_cast<float*>(a.workspace);
-  p.part_ml =
-      p.part + plan.units * plan.splits * plan.head_rows * (int64_t)a.head_dim;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + plan.off_ml);
+  p.cut = reinterpret_cast<int2*>(ws + plan.off_cut);
   const bool bf = a.q_dtype == PA_BF16;
   switch (a.cache_dtype) {
     case PA_F32: return launch_generic<float, F32Page>(p, a.head_dim, stream);
-    case PA_F16: return launch_mma<__half, kH16>(p, a.head_dim, plan.units, stream);
+    case PA_F16: return launch_mma<__half, kH16>(p, a.head_dim, plan, stream);
     case PA_BF16:
-      return launch_mma<__nv_bfloat16, kB16>(p, a.head_dim, plan.units, stream);
+      return launch_mma<__nv_bfloat16, kB16>(p, a.head_dim, plan, stream);
     case PA_FP8_E4M3:
-      return bf ? launch_mma<__nv_bfloat16, kF8>(p, a.head_dim, plan.units, stream)
-                : launch_mma<__half, kF8>(p, a.head_dim, plan.units, stream);
+      return bf ? launch_mma<__nv_bfloat16, kF8>(p, a.head_dim, plan, stream)
+                : launch_mma<__half, kF8>(p, a.head_dim, plan, stream);
     case PA_INT4:
       return bf ? launch_generic<__nv_bfloat16, Int4Page>(p, a.head_dim, stream)
                 : launch_generic<__half, Int4Page>(p, a.head_dim, stream);

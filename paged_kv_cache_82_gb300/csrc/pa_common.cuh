@@ -367,6 +367,61 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// fl32(x / s) for many x and one s: from the correctly rounded 1 / s by two of
+// Markstein's corrections (IBM J. Res. Dev. 34, 1990).  x * rcp is within 3/2
+// of a step of x / s; the first correction leaves the quotient within one step,
+// so that the second rounds it correctly.  A third of the instructions of a
+// division.  easy: s and 1 / s are normal with room (the quotient of a 16-bit
+// or narrower x does not vanish, the remainders stay exact where they decide
+// anything); elsewhere, for quotients that overflow and for NaN, the plain
+// operations.
+struct Divisor {
+  float s, rcp;
+  bool easy;
+  __device__ __forceinline__ explicit Divisor(float d) : s(d) {
+    easy = d >= 0x1p-100f && d <= 0x1p+16f;
+    rcp = easy ? __frcp_rn(d) : 0.f;
+  }
+  __device__ __forceinline__ float corrected(float x) const {
+    const float y0 = x * rcp;
+    float y = fmaf(fmaf(-y0, s, x), rcp, y0);
+    y = fmaf(fmaf(-y, s, x), rcp, y);
+    // (a correction turns -0 into 0: the sign is x's)
+    return fabsf(y0) <= 0x1p+100f ? copysignf(y, x) : y0;
+  }
+};
+
+// y[i] = fl32(x[i] / d)
+template <int kN>
+__device__ __forceinline__ void divide(const float (&x)[kN], const Divisor& d,
+                                       float (&y)[kN]) {
+  if (d.easy) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) y[i] = d.corrected(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) y[i] = __fdiv_rn(x[i], d.s);
+  }
+}
+
+// pairs of fp32 operations in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // E2M1 (OCP Microscaling FP4: sign bit 3, exponent bits 2-1 with bias 1,
 // mantissa bit 0; values 0, 0.5, 1, 1.5, 2, 3, 4, 6).
 __device__ __forceinline__ float e2m1_to_f32(uint32_t c) {

@@ -122,12 +122,10 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
 
 // ---- attention over selected blocks (attn_selected.cu) ----------------------
 struct SelectedPlan {
-  int head_rows;   // query heads of one work unit (of one KV head's group)
-  int head_parts;  // units per KV head
-  int cluster;     // ranges of a unit's list that one cluster joins
-  int splits;      // clusters per unit, joined through the workspace
-  int64_t units;
-  int64_t bytes;
+  int head_rows;   // query heads of one KV head that a CTA takes
+  int head_parts;  // CTAs per share, where the group has more
+  int64_t shares;  // equal shares of all the lists' entries
+  int64_t off_ml, off_cut, bytes;  // workspace
 };
 SelectedPlan make_selected_plan(int64_t num_tokens, int num_q_heads, int num_kv_heads,
                                 int head_dim, int max_selected, int num_sms);

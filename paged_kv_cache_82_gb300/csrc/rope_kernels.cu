@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 #ifndef PA_ROPE_CTAS
-#define PA_ROPE_CTAS 3
+#define PA_ROPE_CTAS 4
 #endif
 #ifndef PA_ROPE_H
 #define PA_ROPE_H 4
@@ -125,15 +125,16 @@ struct alignas(16) Row8 {
 // the warp calls it; on: this row is written.
 template <typename T, int kCache, int kD>
 __device__ __forceinline__ void cache_row(void* cache, int64_t page, int o, int sub,
-                                          float (&x)[8], float scale, bool on) {
+                                          float (&x)[8], const Divisor& scale, bool on) {
   if constexpr (kCache == kSame) {
     if (on) store8(static_cast<T*>(cache) + (page * kBS + o) * kD + sub * 8, x);
   } else if constexpr (kCache == kFp8) {
+    float y[8];
+    divide(x, scale, y);
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t c =
-          __nv_cvt_float_to_fp8(__fdiv_rn(x[i], scale), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t c = __nv_cvt_float_to_fp8(y[i], __NV_SATFINITE, __NV_E4M3);
       w[i >> 2] |= c << (8 * (i & 3));
     }
     if (on)
@@ -143,7 +144,7 @@ __device__ __forceinline__ void cache_row(void* cache, int64_t page, int o, int 
     constexpr int kPage = kCache == kNvfp4 ? 9 * kD : 8 * kD + 64;
     // a row's (INT4) or a 16-element block's (NVFP4: two lanes) largest value
     constexpr int kLanes = kCache == kNvfp4 ? 2 : kD / 8;
-    float amax = 0.f;
+    float amax = 0.f, y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
@@ -152,20 +153,21 @@ __device__ __forceinline__ void cache_row(void* cache, int64_t page, int o, int 
     uint32_t codes = 0;
     if constexpr (kCache == kInt4) {
       const float sc = amax > 0.f ? __fdiv_rn(amax, 7.0f) : 0.f;
+      divide(x, Divisor(sc), y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        int c = sc > 0.f ? __float2int_rn(__fdiv_rn(x[i], sc)) : 0;
+        int c = sc > 0.f ? __float2int_rn(y[i]) : 0;
         c = max(-7, min(7, c));
         codes |= ((uint32_t)c & 0xFu) << (4 * i);
       }
       if (on && sub == 0) *reinterpret_cast<float*>(pg + kBS * (kD / 2) + 4 * o) = sc;
     } else {
       const uint8_t bs = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
-          __fdiv_rn(__fdiv_rn(amax, 6.0f), scale), __NV_SATFINITE, __NV_E4M3));
-      const float r = __fmul_rn(e4m3_to_f32(bs), scale);
+          __fdiv_rn(__fdiv_rn(amax, 6.0f), scale.s), __NV_SATFINITE, __NV_E4M3));
+      const float r = __fmul_rn(e4m3_to_f32(bs), scale.s);
+      divide(x, Divisor(r), y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        codes |= (r > 0.f ? e2m1_encode(__fdiv_rn(x[i], r)) : 0u) << (4 * i);
+      for (int i = 0; i < 8; ++i) codes |= (r > 0.f ? e2m1_encode(y[i]) : 0u) << (4 * i);
       if (on && (sub & 1) == 0) pg[kBS * (kD / 2) + o * (kD / 16) + sub / 2] = bs;
     }
     // element 2i in the low nibble of byte i: nibble i of the word
@@ -196,17 +198,18 @@ __global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS) norm_rope_kernel(const
                   : which == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
                                : static_cast<const T*>(p.v) + t * p.v_stride) +
                  sub * 8;
-  if (slot < 0) return;  // a padding token: nothing written
-  if (slot >= p.num_slots || (p.rotary_dim && (pos < 0 || pos >= p.max_position))) {
-    if (item == 0 && lane == 0)
-      flag_error(p.err, slot >= p.num_slots ? PA_DEV_ERR_SLOT : PA_DEV_ERR_METADATA);
-    return;
-  }
+  // the rows do not depend on the slot: their loads go out together
   Row8<T> raw[kH];
 #pragma unroll
   for (int j = 0; j < kH; ++j) {
     const int h = h0 + j * kRows;
     if (h < heads) raw[j].template load<kVec>(src + (int64_t)h * kD);
+  }
+  if (slot < 0) return;  // a padding token: nothing written
+  if (slot >= p.num_slots || (p.rotary_dim && (pos < 0 || pos >= p.max_position))) {
+    if (item == 0 && lane == 0)
+      flag_error(p.err, slot >= p.num_slots ? PA_DEV_ERR_SLOT : PA_DEV_ERR_METADATA);
+    return;
   }
   // The lane's rotation with the weights in it: element i of the result is
   //   r (x_i own_i + x_partner other_i),  r = 1/sqrt(mean + eps),
@@ -262,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS) norm_rope_kernel(const
   const int from = (lane - sub) + partner;
   const int64_t b = slot / kBS;
   const int o = (int)(slot - b * kBS);
+  const Divisor scale(which == 2 ? p.v_scale : p.k_scale);
 #pragma unroll
   for (int j = 0; j < kH; ++j) {
     if (h0 - lane / kLanes + j * kRows >= heads) break;  // the whole warp is past
@@ -271,32 +275,33 @@ __global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS) norm_rope_kernel(const
     raw[j].values(x);
     float r = 1.f;
     if (wp) {
-      float ss = 0.f;
+      float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int i = 0; i < 8; i += 2) {
+        const float2 v = make_float2(x[i], x[i + 1]);
+        s2 = fma2(v, v, s2);
+      }
+      float ss = s2.x + s2.y;
 #pragma unroll
       for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
       r = rsqrtf(ss * (1.0f / kD) + p.eps);
     }
     if (which < 2) {
+      float y[8];
       if (p.interleaved) {
-        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = x[i] * own[i];
-          if (turns) y[i] = fmaf(x[i ^ 1], other[i], y[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = y[i] * r;
-      } else {
-        float y[8];
+        for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+      } else if (p.rotary_dim) {
         raw[j].shuffled(from).values(y);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = x[i] * own[i];
-          if (turns) x[i] = fmaf(y[i], other[i], x[i]);
-          x[i] *= r;
-        }
+      for (int i = 0; i < 8; i += 2) {
+        float2 z = mul2(make_float2(x[i], x[i + 1]), make_float2(own[i], own[i + 1]));
+        if (turns)
+          z = fma2(make_float2(y[i], y[i + 1]), make_float2(other[i], other[i + 1]), z);
+        z = mul2(z, make_float2(r, r));
+        x[i] = z.x;
+        x[i + 1] = z.y;
       }
     }
     if (which == 0) {
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS) norm_rope_kernel(const
       }
       cache_row<T, kCache, kD>(which == 2 ? p.v_cache : p.k_cache,
                                b * p.num_kv_heads + h, o, sub, x,
-                               which == 2 ? p.v_scale : p.k_scale, on);
+                               scale, on);
     }
   }
 }

@@ -142,6 +142,16 @@ struct Range8 {
       lo[i] = min_of(lo[i], __shfl_xor_sync(~0u, lo[i], mask));
     }
   }
+  // the largest magnitude among the lane's channels
+  __device__ __forceinline__ float largest() const {
+    constexpr uint32_t kAbs = kPair ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+    uint32_t m = max_of(hi[0] & kAbs, lo[0] & kAbs);
+#pragma unroll
+    for (int i = 1; i < kN; ++i) m = max_of(m, max_of(hi[i] & kAbs, lo[i] & kAbs));
+    if constexpr (!kPair) return __uint_as_float(m);
+    const uint32_t w[kN] = {m};
+    return fmaxf(value(w, 0), value(w, 1));
+  }
   __device__ __forceinline__ static float value(const uint32_t (&w)[kN], int i) {
     if constexpr (!kPair) {
       return __uint_as_float(w[i]);
@@ -160,15 +170,11 @@ struct Range8 {
 // bytes written, so the kernel is bound by HBM when there are many pages, and
 // by the chain of loads (lengths, block id, page) when there are few.
 template <int kPg, int kD>
-__global__ void __launch_bounds__(kThreads)
-summarise_kernel(StepView s, const void* __restrict__ k_cache, int num_kv_heads,
-                 int ctas_per_seq, uint8_t* __restrict__ bounds) {
+__device__ __forceinline__ void summarise_one(const StepView& s, const void* k_cache,
+                                              int num_kv_heads, int r, int item, int nth,
+                                              int h, uint8_t* bounds) {
   constexpr int kLanes = kD / 8, kRows = 32 / kLanes, kReads = kBS / kRows;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, part = lane / kLanes;
-  const int r = blockIdx.x / ctas_per_seq;
-  const int item =
-      (blockIdx.x - r * ctas_per_seq) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int nth = item / num_kv_heads, h = item - nth * num_kv_heads;
   const ReqMeta m = load_req(s.query_start_loc, s.seq_lens, r, s.num_tokens,
                              s.max_query_len, s.max_seq_len, s.max_blocks_per_seq);
   if (!m.ok) {
@@ -196,17 +202,19 @@ summarise_kernel(StepView s, const void* __restrict__ k_cache, int num_kv_heads,
   for (int i = 0; i < kReads; ++i) range.add(words[i]);
 #pragma unroll
   for (int d = kLanes; d < 32; d <<= 1) range.join(d);
-  float big = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    big = fmaxf(big, fmaxf(fabsf(Range::value(range.hi, i)), fabsf(Range::value(range.lo, i))));
+  float big = range.largest();
   // The first part of the warp has the codes of the largest values, the second
   // those of the smallest, as floor(x) = -ceil(-x).
   const bool low = part & 1;
   float x[8];
+  {
+    uint32_t w[Range::kN];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = low ? -Range::value(range.lo, i) : Range::value(range.hi, i);
+    for (int i = 0; i < Range::kN; ++i)
+      w[i] = low ? range.lo[i] ^ (Range::kPair ? 0x80008000u : 0x80000000u) : range.hi[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = Range::value(w, i);
+  }
   // infinite: an infinite key, or a channel of nothing but NaN (hi -inf, lo inf)
   if (big == INFINITY) {
     big = 0.f;
@@ -221,28 +229,13 @@ summarise_kernel(StepView s, const void* __restrict__ k_cache, int num_kv_heads,
 #pragma unroll
   for (int d = 1; d < kLanes; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
   const float sc = __fdiv_rn(big, 127.0f);
+  Divisor by(sc);
+  if (kPg == kPgF32) by.easy = false;  // fp32 keys may be as small as 2^-149
+  float y[8];
+  divide(x, by, y);
   int c[8];
-  if (kPg != kPgF32 && sc >= 0x1p-100f && sc <= 0x1p+16f) {
-    // fl32(x / s) from the correctly rounded 1 / s in two of Markstein's
-    // corrections (IBM J. Res. Dev. 34, 1990): after the first the quotient is
-    // within one step, so the second rounds correctly.  Half the instructions
-    // of a division each.  The range of s keeps 1 / s normal and the quotient
-    // of any 16-bit (or narrower) key from vanishing; a remainder that
-    // underflows belongs to a quotient far below 1, whose ceiling is its
-    // sign's.
-    const float rcp = __frcp_rn(sc);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float y = x[i] * rcp;
-      y = fmaf(fmaf(-y, sc, x[i]), rcp, y);
-      y = fmaf(fmaf(-y, sc, x[i]), rcp, y);
-      c[i] = __float2int_ru(fminf(y, 127.0f));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      c[i] = sc > 0.f ? __float2int_ru(fminf(__fdiv_rn(x[i], sc), 127.0f)) : 0;
-  }
+  for (int i = 0; i < 8; ++i) c[i] = sc > 0.f ? __float2int_ru(fminf(y[i], 127.0f)) : 0;
   uint32_t code[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -252,6 +245,16 @@ summarise_kernel(StepView s, const void* __restrict__ k_cache, int num_kv_heads,
     *reinterpret_cast<uint2*>(rec + (low ? kD : 0) + sub * 8) = make_uint2(code[0], code[1]);
   if (lane == 0)
     *reinterpret_cast<uint4*>(rec + 2 * kD) = make_uint4(__float_as_uint(sc), 0, 0, 0);
+}
+
+template <int kPg, int kD>
+__global__ void __launch_bounds__(kThreads)
+summarise_kernel(StepView s, const void* __restrict__ k_cache, int num_kv_heads,
+                 uint8_t* __restrict__ bounds) {
+  const int item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int nth = item / num_kv_heads, h = item - nth * num_kv_heads;
+  for (int r = blockIdx.y; r < s.num_seqs; r += gridDim.y)
+    summarise_one<kPg, kD>(s, k_cache, num_kv_heads, r, item, nth, h, bounds);
 }
 
 // ---------------------------------------------------------------------------
@@ -321,7 +324,7 @@ __device__ __forceinline__ void load16(const T* src, float (&x)[16]) {
 }
 
 #ifndef PA_SCORE_FLIGHT
-#define PA_SCORE_FLIGHT 4
+#define PA_SCORE_FLIGHT 2
 #endif
 #ifndef PA_SCORE_CTAS
 #define PA_SCORE_CTAS 3
@@ -396,16 +399,25 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : PA_SCORE_CTAS)
           for (int w = 0; w < 4; ++w)
             code[g][w] = __shfl_sync(~0u, mine[w], (g - g0) * kLanes + sub);
       }
-      for (int b0 = first + (warp / p.num_kv_heads) * kScoreGroup; b0 < last;
-           b0 += sharing * kScoreGroup) {
-        // the group's physical blocks, one per lane; kept blocks are not read
+      // the physical block of a group's block b, one per lane; kept blocks are
+      // not read
+      const uint8_t* head_bounds = p.bounds + (int64_t)h * bounds_bytes(kD);
+      const int64_t block_bytes = (int64_t)p.num_kv_heads * bounds_bytes(kD);
+      auto group_id = [&](int b) {
+        if (b >= last || b < p.keep_first || b >= kept_last) return -1;
+        const int id = __ldg(table + b);
+        if (id >= 0 && (int64_t)id < p.s.num_blocks) return id;
+        flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
+        return -1;
+      };
+      const int stride = sharing * kScoreGroup;
+      const int b_first = first + (warp / p.num_kv_heads) * kScoreGroup;
+      int next_id = group_id(b_first + lane);
+      for (int b0 = b_first; b0 < last; b0 += stride) {
         const int mb = b0 + lane;
         const bool kept = mb < p.keep_first || mb >= kept_last;
-        int id = mb < last && !kept ? __ldg(table + mb) : -1;
-        if (id < -1 || (id == -1 && mb < last && !kept) || (int64_t)id >= p.s.num_blocks) {
-          flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
-          id = -1;
-        }
+        const int id = next_id;
+        next_id = group_id(b0 + stride + lane);
         uint32_t mine = kKeptKey;  // lane l: the key of block b0 + l
 #pragma unroll
         for (int s0 = 0; s0 < kSteps; s0 += kFlight) {
@@ -417,8 +429,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : PA_SCORE_CTAS)
             hi[f] = lo[f] = make_uint4(0, 0, 0, 0);
             sc[f] = 0.f;
             if (blk >= 0) {
-              const uint8_t* r =
-                  p.bounds + ((int64_t)blk * p.num_kv_heads + h) * bounds_bytes(kD);
+              const uint8_t* r = head_bounds + blk * block_bytes;
               hi[f] = __ldg(reinterpret_cast<const uint4*>(r + sub * 16));
               lo[f] = __ldg(reinterpret_cast<const uint4*>(r + kD + sub * 16));
               sc[f] = __ldg(reinterpret_cast<const float*>(r + 2 * kD));
@@ -533,7 +544,7 @@ __global__ void __launch_bounds__(kTopkThreads, 2) topk_kernel(const TopkParams 
   }
   const uint32_t* keys = p.keys + (tp * p.num_kv_heads + h) * p.row_scores;
   // the warp's part: part keys from begin on, 32 at a time
-  const int part = kPer ? 32 * kPer : ((n + kTopkWarps - 1) / kTopkWarps + 31) & ~31;
+  const int part = ((n + kTopkWarps - 1) / kTopkWarps + 31) & ~31;
   const int begin = min(n, warp * part), end = min(n, begin + part);
   uint32_t held[kPer ? kPer : 1];
   if constexpr (kPer > 0) {
@@ -655,10 +666,10 @@ cudaError_t launch_summarise_d(const StepView& s, const void* k_cache, int num_k
   const int64_t wide = std::min<int64_t>((s.max_query_len + kBS - 2) / kBS + 1,
                                          (s.max_seq_len + kBS - 1) / kBS);
   const int64_t per_seq = (wide * num_kv_heads + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t ctas = per_seq * s.num_seqs;
-  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-  summarise_kernel<kPg, kD><<<(unsigned)ctas, kThreads, 0, stream>>>(
-      s, k_cache, num_kv_heads, (int)per_seq, static_cast<uint8_t*>(bounds));
+  if (per_seq * (kThreads / 32) > 0x7fffffffll) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)per_seq, (unsigned)std::min(s.num_seqs, 65535));
+  summarise_kernel<kPg, kD><<<grid, kThreads, 0, stream>>>(
+      s, k_cache, num_kv_heads, static_cast<uint8_t*>(bounds));
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;

@@ -42,7 +42,7 @@ class Loop:
             np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)).cuda()
         self.w = [torch.from_numpy(self.rng.uniform(0.5, 1.5, D).astype(np.float32)
                                    ).bfloat16().cuda() for _ in range(2)]
-        self.ws = workspaces or [torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+        self.ws = workspaces or [torch.zeros(1 << 23, dtype=torch.uint8, device="cuda")
                                  for _ in range(2)]
         self.pad = pad
 
@@ -188,7 +188,7 @@ def test_two_loops_on_two_streams_at_once():
 def test_two_graphs_that_share_a_workspace():
     """Replayed one after the other on one stream, with the previous graph's
     leavings in it."""
-    ws = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ws = [torch.full((1 << 23,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
     loops = [Loop(5, [180, 30], workspaces=ws), Loop(6, [20, 250], "e4m3", workspaces=ws)]
     bufs, graphs = [], []
     for lp in loops:
