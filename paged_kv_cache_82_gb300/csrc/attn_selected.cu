@@ -208,6 +208,13 @@ __global__ void __launch_bounds__(kThreads) selected_generic_kernel(const SelPar
 // ---------------------------------------------------------------------------
 // the MMA form
 // ---------------------------------------------------------------------------
+// 2^x to 2 units in the last place of fp32; below 2^-126: 0
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -358,43 +365,37 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
   auto page_keys = [&](const Entry& e) {
     return e.phys < 0 ? 0 : min(kBS, u.pos - e.block * kBS + 1);
   };
+  // Loads are unconditional: a skipped entry reads block 0, rows past the
+  // position what happens to be there.  The few steps with such keys mask them
+  // where they are used.
   auto load_k = [&](const Entry (&en)[kP]) {
 #pragma unroll
     for (int g = 0; g < kP; ++g) {
       const uint8_t* src = kbase + (int64_t)max(en[g].phys, 0) * block_bytes + koff;
-      const bool on = en[g].phys >= 0;
 #pragma unroll
       for (int i = 0; i < Tr::kKChunks; ++i) {
-        kr[g][0][i] = kr[g][1][i] = make_uint4(0, 0, 0, 0);
-        if (on) {
-          kr[g][0][i] = __ldg(reinterpret_cast<const uint4*>(src + 64 * i));
-          kr[g][1][i] =
-              __ldg(reinterpret_cast<const uint4*>(src + 8 * Tr::kRowBytes + 64 * i));
-        }
+        kr[g][0][i] = __ldg(reinterpret_cast<const uint4*>(src + 64 * i));
+        kr[g][1][i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * Tr::kRowBytes + 64 * i));
       }
     }
   };
-  // a row past the position holds nothing yet (its bits may be anything): 0
   auto load_v = [&](const Entry (&en)[kP]) {
 #pragma unroll
     for (int g = 0; g < kP; ++g) {
-      const uint8_t* src =
-          vbase + (int64_t)max(en[g].phys, 0) * block_bytes + r * Tr::kVBytes;
-      const int keys = page_keys(en[g]);
+      const uint8_t* src = vbase + (int64_t)max(en[g].phys, 0) * block_bytes +
+                           2 * c * Tr::kRowBytes + r * Tr::kVBytes;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = 2 * c + (j & 1) + 8 * (j >> 1);
 #pragma unroll
         for (int i = 0; i < Tr::kVChunks; ++i) {
-          const uint8_t* at = src + key * Tr::kRowBytes + i * 8 * Tr::kVBytes;
+          const uint8_t* at =
+              src + ((j & 1) + 8 * (j >> 1)) * Tr::kRowBytes + i * 8 * Tr::kVBytes;
           if constexpr (Tr::kVBytes == 16) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (key < keys) v = __ldg(reinterpret_cast<const uint4*>(at));
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
             vr[g][j][i][0] = v.x; vr[g][j][i][1] = v.y;
             vr[g][j][i][2] = v.z; vr[g][j][i][3] = v.w;
           } else {
-            uint2 v = make_uint2(0, 0);
-            if (key < keys) v = __ldg(reinterpret_cast<const uint2*>(at));
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
             vr[g][j][i][0] = v.x; vr[g][j][i][1] = v.y;
           }
         }
@@ -454,13 +455,15 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
           big = fmaxf(big, fabsf(x[nt][i][e]));
         }
       }
-    float down = 1.f;
+    // a scale of either sign, or 0: the score's stays positive
+    float down = score_scale > 0.f ? 1.f : score_scale < 0.f ? -1.f : 0.f;
+    score_scale = score_scale == 0.f ? 1.f : fabsf(score_scale);
     if constexpr (kPg == kF8) {
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
       if (big > 16384.f && big < INFINITY) {
         const int ex = ilogbf(big) - 13;
-        down = exp2f((float)-ex);
+        down *= exp2f((float)-ex);
         score_scale *= exp2f((float)ex);
       }
     }
@@ -506,36 +509,52 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
         }
       }
     }
-    int keys[kP];
+    int keys[kP], fewest = kBS;
 #pragma unroll
-    for (int g = 0; g < kP; ++g) keys[g] = page_keys(cur[g]);
+    for (int g = 0; g < kP; ++g) {
+      keys[g] = page_keys(cur[g]);
+      fewest = min(fewest, keys[g]);
+    }
     if (i + 1 < steps) {
       entries(i + 1, cur);
       load_k(cur);
     }
-    // softmax over the step's keys
+    if (fewest < kBS) {  // masked keys: no score, and no value that could be NaN
+#pragma unroll
+      for (int g = 0; g < kP; ++g) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (r + 8 * (j >> 1) >= keys[g]) s[g][nt][j] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (2 * c + (j & 1) + 8 * (j >> 1) >= keys[g])
+#pragma unroll
+            for (int ch = 0; ch < Tr::kVChunks; ++ch)
+#pragma unroll
+              for (int w = 0; w < Tr::kVBytes / 4; ++w) vr[g][j][ch][w] = 0;
+      }
+    }
+    // softmax over the step's keys; m: the largest score times score_scale (> 0)
     uint32_t pb[kP][kNT][2];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int g = 0; g < kP; ++g)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[g][nt][j] = r + 8 * (j >> 1) < keys[g] ? s[g][nt][j] * score_scale : -INFINITY;
-          mx[j & 1] = fmaxf(mx[j & 1], s[g][nt][j]);
-        }
+      float mx[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        mx[j] = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+        for (int g = 1; g < kP; ++g) mx[j] = fmaxf(mx[j], fmaxf(s[g][nt][j], s[g][nt][j + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(~0u, mx[j], d));
-        mx[j] = fmaxf(mx[j], m[nt][j]);
+        mx[j] = fmaxf(mx[j] * score_scale, m[nt][j]);
       }
       if (__any_sync(~0u, mx[0] > m[nt][0] || mx[1] > m[nt][1])) {
         float al[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          al[j] = mx[j] == -INFINITY ? 1.f : exp2f(m[nt][j] - mx[j]);
+          al[j] = mx[j] == -INFINITY ? 1.f : exp2_fast(m[nt][j] - mx[j]);
           m[nt][j] = mx[j];
           l[nt][j] *= al[j];
         }
@@ -547,12 +566,14 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
           acc[nt][tl][3] *= al[1];
         }
       }
-      const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-      const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+      const float m0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0];
+      const float m1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
 #pragma unroll
       for (int g = 0; g < kP; ++g) {
-        const float p0 = exp2f(s[g][nt][0] - m0), p1 = exp2f(s[g][nt][1] - m1);
-        const float p2 = exp2f(s[g][nt][2] - m0), p3 = exp2f(s[g][nt][3] - m1);
+        const float p0 = exp2_fast(fmaf(s[g][nt][0], score_scale, m0));
+        const float p1 = exp2_fast(fmaf(s[g][nt][1], score_scale, m1));
+        const float p2 = exp2_fast(fmaf(s[g][nt][2], score_scale, m0));
+        const float p3 = exp2_fast(fmaf(s[g][nt][3], score_scale, m1));
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
         // keys as rows -> heads as rows: the second product's operand

@@ -944,7 +944,8 @@ pa_status pa_attention_selected(
       !aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 128) ||
       !aligned(v_cache, 128) || !aligned(selected, 4) || !aligned(num_selected, 4))
     return PA_ERR_INVALID_ARG;
-  if (num_tokens * num_kv_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if (num_tokens * num_kv_heads >= (1ll << 31) || max_selected > (1 << 24))
+    return PA_ERR_UNSUPPORTED;
   const DeviceInfo* di = device_info();
   if (!di) return PA_ERR_CUDA;
   const SelectedPlan plan = make_selected_plan(num_tokens, num_q_heads, num_kv_heads,

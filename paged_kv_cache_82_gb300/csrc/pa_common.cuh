@@ -378,8 +378,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 struct Divisor {
   float s, rcp;
   bool easy;
-  __device__ __forceinline__ explicit Divisor(float d) : s(d) {
-    easy = d >= 0x1p-100f && d <= 0x1p+16f;
+  // used: false where no division follows (saves the reciprocal)
+  __device__ __forceinline__ explicit Divisor(float d, bool used = true) : s(d) {
+    easy = used && d >= 0x1p-100f && d <= 0x1p+16f;
     rcp = easy ? __frcp_rn(d) : 0.f;
   }
   __device__ __forceinline__ float corrected(float x) const {
@@ -402,24 +403,6 @@ __device__ __forceinline__ void divide(const float (&x)[kN], const Divisor& d,
 #pragma unroll
     for (int i = 0; i < kN; ++i) y[i] = __fdiv_rn(x[i], d.s);
   }
-}
-
-// pairs of fp32 operations in one instruction
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
 }
 
 // E2M1 (OCP Microscaling FP4: sign bit 3, exponent bits 2-1 with bias 1,

@@ -10,11 +10,13 @@
 // pa_reshape_and_cache's rule for the cache type, so that the result is the
 // two-step result bit for bit.
 //
-// Bound by HBM: each of q, k, v is read once and written once.  A group of
-// head_dim / 8 lanes holds one head's row, 8 elements (16 bytes of a 16-bit
-// type) per lane: the row's sum is a few shuffles, and the rotation's partner
-// of element i lies in the lane rotary_dim / 16 away at the same place (or,
-// interleaved, in the same lane).
+// Bound by HBM: each of q, k, v is read once and written once.  head_dim / 8
+// lanes hold one head's row, two groups of 4 elements each: the groups that
+// the rotation pairs (i, i + R/2), so that it stays within a lane, and two
+// neighbours where nothing turns or neighbours turn.  The row's sum is a few
+// shuffles.
+#include <type_traits>
+
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -22,13 +24,12 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-#ifndef PA_ROPE_CTAS
-#define PA_ROPE_CTAS 4
-#endif
-#ifndef PA_ROPE_H
-#define PA_ROPE_H 4
-#endif
-constexpr int kHeads = PA_ROPE_H;  // rows per lane group of a large step
+// Rows per lane group, and CTAs per SM (64 registers a thread), of a large
+// step.  8192 tokens of 64 + 8 + 8 heads of 128, bf16 over an FP8 cache, in us:
+// 8 rows 70, 4 rows 77, 2 rows 95 with four CTAs; 8 rows 75 with three, 116 with
+// five (spills).
+constexpr int kHeads = 8;
+constexpr int kCtas = 4;
 
 enum : int { kSame = 0, kFp8 = 1, kInt4 = 2, kNvfp4 = 3 };
 
@@ -55,123 +56,179 @@ struct RopeParams {
   unsigned* err;
   int num_sms;
   int items, q_items, kv_items;  // warps of one token: all, per kind
+  uint32_t per_item;             // 2^(32 + shift) / items, rounded up
+  int per_item_shift;
 };
 
-// 8 consecutive elements as fp32
-template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* src, float (&x)[8]) {
-  if constexpr (kVec && sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(src);
-    const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
-  } else if constexpr (kVec) {
-    const float4 a = *reinterpret_cast<const float4*>(src);
-    const float4 b = *reinterpret_cast<const float4*>(src + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(src[i]);
+// A lane's place in a row of kD elements: two groups of four.  pairs = R / 8:
+// the first `pairs` lanes hold the groups g and g + pairs that turn together,
+// the others neighbours.
+struct Place {
+  int g[2];
+  __device__ __forceinline__ Place(int sub, int pairs) {
+    g[0] = sub < pairs ? sub : 2 * sub;
+    g[1] = sub < pairs ? sub + pairs : 2 * sub + 1;
   }
-}
-
-// 8 consecutive elements (16-byte aligned), rounded to T
-template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    uint4 u;
-    T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(x[i]);
-    *reinterpret_cast<uint4*>(dst) = u;
-  } else {
-    *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  // the lane and the half of it that hold group k
+  __device__ __forceinline__ static int lane_of(int k, int pairs) {
+    return k < pairs ? k : k < 2 * pairs ? k - pairs : k >> 1;
   }
-}
+  __device__ __forceinline__ static int half_of(int k, int pairs) {
+    return k < 2 * pairs ? k >= pairs : k & 1;
+  }
+};
 
-// 8 elements of a row as they are read, 16 or 32 bytes
+// The lane's 8 elements, as they are read: kVec by 8 or 16 bytes a group.
+// Pairs of 16-bit types are taken apart and put together as words.
 template <typename T>
-struct alignas(16) Row8 {
-  T e[8];
+struct Row8 {
+  static constexpr int kWords = 2 * sizeof(T), kGroup = kWords / 2;  // of four elements
+  uint32_t w[kWords];
   template <bool kVec>
-  __device__ __forceinline__ void load(const T* src) {
-    if constexpr (kVec) {
-      const uint4* s = reinterpret_cast<const uint4*>(src);
+  __device__ __forceinline__ void load(const T* row, const Place& at) {
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(e)[i] = s[i];
-    } else {
+    for (int k = 0; k < 2; ++k) {
+      const T* src = row + 4 * at.g[k];
+      if constexpr (kVec && sizeof(T) == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(src);
+        w[2 * k] = u.x;
+        w[2 * k + 1] = u.y;
+      } else if constexpr (kVec) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src);
+        w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+      } else if constexpr (sizeof(T) == 2) {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+        w[2 * k] = h[0] | (uint32_t)h[1] << 16;
+        w[2 * k + 1] = h[2] | (uint32_t)h[3] << 16;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = src[i];
+        for (int i = 0; i < 4; ++i) w[4 * k + i] = reinterpret_cast<const uint32_t*>(src)[i];
+      }
     }
-  }
-  __device__ __forceinline__ Row8 shuffled(int from) const {
-    Row8 o;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) * 2; ++i)
-      reinterpret_cast<uint32_t*>(o.e)[i] =
-          __shfl_sync(~0u, reinterpret_cast<const uint32_t*>(e)[i], from);
-    return o;
   }
   __device__ __forceinline__ void values(float (&x)[8]) const {
+    if constexpr (std::is_same<T, float>::value) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void round(const float (&x)[8]) {
+    if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack2<std::is_same<T, __nv_bfloat16>::value>(x[2 * i], x[2 * i + 1]);
+    }
+  }
+  // a row that allows 16-byte stores
+  __device__ __forceinline__ void store(T* row, const Place& at) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(row + 4 * at.g[k]) = make_uint2(w[2 * k], w[2 * k + 1]);
+      else
+        *reinterpret_cast<uint4*>(row + 4 * at.g[k]) =
+            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
   }
 };
 
-// One lane's 8 elements x (lane sub of the kD / 8 of a row) of token offset o
-// into the page of a cache, by pa_reshape_and_cache's rule.  Every lane of
-// the warp calls it; on: this row is written.
+// One lane's 8 elements of token offset o into the page of a cache, by
+// pa_reshape_and_cache's rule.  Every lane of the warp calls it; on: this row
+// is written.  sub: the lane's number in its row, of lane - sub on.
 template <typename T, int kCache, int kD>
-__device__ __forceinline__ void cache_row(void* cache, int64_t page, int o, int sub,
-                                          float (&x)[8], const Divisor& scale, bool on) {
+__device__ __forceinline__ void cache_row(void* cache, int64_t page, int o, int lane, int sub,
+                                          const Place& at, int pairs, const Row8<T>& row,
+                                          const Divisor& scale, bool on) {
   if constexpr (kCache == kSame) {
-    if (on) store8(static_cast<T*>(cache) + (page * kBS + o) * kD + sub * 8, x);
-  } else if constexpr (kCache == kFp8) {
-    float y[8];
+    if (on) row.store(static_cast<T*>(cache) + (page * kBS + o) * kD, at);
+    return;
+  }
+  float x[8], y[8];
+  row.values(x);  // of the input type, whatever the cache's
+  if constexpr (kCache == kFp8) {
     divide(x, scale, y);
-    uint32_t w[2] = {0, 0};
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t c = __nv_cvt_float_to_fp8(y[i], __NV_SATFINITE, __NV_E4M3);
-      w[i >> 2] |= c << (8 * (i & 3));
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k], y[4 * k + 1]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k + 2], y[4 * k + 3]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      w[k] = lo | hi << 16;
     }
-    if (on)
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + (page * kBS + o) * kD +
-                                sub * 8) = make_uint2(w[0], w[1]);
-  } else {
-    constexpr int kPage = kCache == kNvfp4 ? 9 * kD : 8 * kD + 64;
-    // a row's (INT4) or a 16-element block's (NVFP4: two lanes) largest value
-    constexpr int kLanes = kCache == kNvfp4 ? 2 : kD / 8;
-    float amax = 0.f, y[8];
+    uint8_t* dst = static_cast<uint8_t*>(cache) + (page * kBS + o) * kD;
+    if (on) {
+      *reinterpret_cast<uint32_t*>(dst + 4 * at.g[0]) = w[0];
+      *reinterpret_cast<uint32_t*>(dst + 4 * at.g[1]) = w[1];
+    }
+  } else if constexpr (kCache == kInt4) {
+    uint8_t* pg = static_cast<uint8_t*>(cache) + page * (8 * kD + 64);
+    float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
-    uint8_t* pg = static_cast<uint8_t*>(cache) + page * kPage;
-    uint32_t codes = 0;
-    if constexpr (kCache == kInt4) {
-      const float sc = amax > 0.f ? __fdiv_rn(amax, 7.0f) : 0.f;
-      divide(x, Divisor(sc), y);
+    for (int d = 1; d < kD / 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
+    const float sc = amax > 0.f ? __fdiv_rn(amax, 7.0f) : 0.f;
+    divide(x, Divisor(sc), y);
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        int c = sc > 0.f ? __float2int_rn(y[i]) : 0;
-        c = max(-7, min(7, c));
-        codes |= ((uint32_t)c & 0xFu) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+      int c = sc > 0.f ? __float2int_rn(y[i]) : 0;
+      c = max(-7, min(7, c));
+      w[i >> 2] |= ((uint32_t)c & 0xFu) << (4 * (i & 3));
+    }
+    if (on) {
+      if (sub == 0) *reinterpret_cast<float*>(pg + kBS * (kD / 2) + 4 * o) = sc;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<uint16_t*>(pg + o * (kD / 2) + 2 * at.g[k]) = (uint16_t)w[k];
+    }
+  } else {
+    uint8_t* pg = static_cast<uint8_t*>(cache) + page * (9 * kD);
+    float own[2] = {0.f, 0.f};  // the groups' largest values
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own[i >> 2] = fmaxf(own[i >> 2], fabsf(x[i]));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // of the 16-element block: four groups, wherever they are
+      const int first = at.g[k] & ~3;
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int from = lane - sub + Place::lane_of(first + j, pairs);
+        const float a = __shfl_sync(~0u, own[0], from), b = __shfl_sync(~0u, own[1], from);
+        amax = fmaxf(amax, Place::half_of(first + j, pairs) ? b : a);
       }
-      if (on && sub == 0) *reinterpret_cast<float*>(pg + kBS * (kD / 2) + 4 * o) = sc;
-    } else {
       const uint8_t bs = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
           __fdiv_rn(__fdiv_rn(amax, 6.0f), scale.s), __NV_SATFINITE, __NV_E4M3));
       const float r = __fmul_rn(e4m3_to_f32(bs), scale.s);
-      divide(x, Divisor(r), y);
+      const float xk[4] = {x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]};
+      float yk[4];
+      divide(xk, Divisor(r), yk);
+      uint32_t w = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) codes |= (r > 0.f ? e2m1_encode(y[i]) : 0u) << (4 * i);
-      if (on && (sub & 1) == 0) pg[kBS * (kD / 2) + o * (kD / 16) + sub / 2] = bs;
+      for (int i = 0; i < 4; ++i) w |= (r > 0.f ? e2m1_encode(yk[i]) : 0u) << (4 * i);
+      if (on) {
+        if ((at.g[k] & 3) == 0) pg[kBS * (kD / 2) + o * (kD / 16) + at.g[k] / 4] = bs;
+        *reinterpret_cast<uint16_t*>(pg + o * (kD / 2) + 2 * at.g[k]) = (uint16_t)w;
+      }
     }
-    // element 2i in the low nibble of byte i: nibble i of the word
-    if (on) *reinterpret_cast<uint32_t*>(pg + o * (kD / 2) + sub * 4) = codes;
   }
 }
 
@@ -179,32 +236,35 @@ __device__ __forceinline__ void cache_row(void* cache, int64_t page, int o, int 
 // of one token, so the rotation's row and the weights are read once for kH
 // heads; all rows are on their way before the first is used.  kVec: rows and
 // weights allow 16-byte loads.
-template <typename T, int kCache, int kD, bool kVec, int kH>
-__global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS) norm_rope_kernel(const RopeParams p) {
+template <typename T, int kCache, int kD, bool kInter, bool kVec, int kH>
+__global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(const RopeParams p) {
   constexpr int kLanes = kD / 8;      // lanes of one head's row
   constexpr int kRows = 32 / kLanes;  // rows of one warp at a time
   const int lane = threadIdx.x & 31, sub = lane % kLanes;
   const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = warp / (uint32_t)p.items;
+  const uint32_t tok = __umulhi(warp, p.per_item) >> p.per_item_shift;
+  const int64_t t = tok;
   if (t >= p.num_tokens) return;
-  const int item = (int)(warp - (uint32_t)t * (uint32_t)p.items);
+  const int item = (int)(warp - tok * (uint32_t)p.items);
   const int which = item < p.q_items ? 0 : item < p.q_items + p.kv_items ? 1 : 2;
   const int heads = which == 0 ? p.num_q_heads : p.num_kv_heads;
-  const int h0 = (item - (which == 0 ? 0 : p.q_items + (which - 1) * p.kv_items)) *
-                     (kRows * kH) + lane / kLanes;
+  const int first = (item - (which == 0 ? 0 : p.q_items + (which - 1) * p.kv_items)) *
+                    (kRows * kH);
+  const int h0 = first + lane / kLanes;
+  const int half = p.rotary_dim / 2;
+  const int pairs = kInter ? 0 : p.rotary_dim / 8;
+  const Place at(sub, pairs);
+  // the rows do not depend on the slot: their loads go out together
   const int64_t slot = __ldg(p.slot_mapping + t);
   const int64_t pos = p.rotary_dim ? __ldg(p.positions + t) : 0;
   const T* src = (which == 0   ? static_cast<const T*>(p.q) + t * p.q_stride
                   : which == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
                                : static_cast<const T*>(p.v) + t * p.v_stride) +
-                 sub * 8;
-  // the rows do not depend on the slot: their loads go out together
+                 h0 * kD;
   Row8<T> raw[kH];
 #pragma unroll
-  for (int j = 0; j < kH; ++j) {
-    const int h = h0 + j * kRows;
-    if (h < heads) raw[j].template load<kVec>(src + (int64_t)h * kD);
-  }
+  for (int j = 0; j < kH; ++j)
+    if (h0 + j * kRows < heads) raw[j].template load<kVec>(src + j * kRows * kD, at);
   if (slot < 0) return;  // a padding token: nothing written
   if (slot >= p.num_slots || (p.rotary_dim && (pos < 0 || pos >= p.max_position))) {
     if (item == 0 && lane == 0)
@@ -214,107 +274,78 @@ __global__ void __launch_bounds__(kThreads, PA_ROPE_CTAS) norm_rope_kernel(const
   // The lane's rotation with the weights in it: element i of the result is
   //   r (x_i own_i + x_partner other_i),  r = 1/sqrt(mean + eps),
   //   own = w cos, other = -+ w_partner sin
-  // (no norm: w = r = 1; no rotation: cos = 1, sin = 0).  The partner's element
-  // comes as it was read: a shuffle of the packed row.
+  // (no norm: w = r = 1; no rotation: cos = 1, sin = 0).
   const void* wp = which == 0 ? p.q_weight : which == 1 ? p.k_weight : nullptr;
-  const int half = p.rotary_dim / 2;
-  const bool turns = which < 2 && sub * 8 < p.rotary_dim;
-  const bool second = sub * 8 >= half;
-  const int away = p.rotary_dim / 16;  // lanes between the two of a pair
-  const int partner = !turns || p.interleaved ? sub : second ? sub - away : sub + away;
+  const bool turns =
+      which < 2 && (kInter ? sub * 8 < p.rotary_dim : sub < pairs);
   float own[8], other[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) own[i] = 1.f, other[i] = 0.f;
   if (turns) {
-    const float* row = p.cos_sin + pos * p.rotary_dim;
-    if (p.interleaved) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + sub * 4));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + sub * 4));
-      own[0] = own[1] = c.x, own[2] = own[3] = c.y;
-      own[4] = own[5] = c.z, own[6] = own[7] = c.w;
-      other[0] = -s.x, other[1] = s.x, other[2] = -s.y, other[3] = s.y;
-      other[4] = -s.z, other[5] = s.z, other[6] = -s.w, other[7] = s.w;
-    } else {
-      const int f = sub * 8 - (second ? half : 0);
-      const float4* cp = reinterpret_cast<const float4*>(row + f);
-      const float4* sp = reinterpret_cast<const float4*>(row + half + f);
-      *reinterpret_cast<float4*>(own) = __ldg(cp);
-      *reinterpret_cast<float4*>(own + 4) = __ldg(cp + 1);
-      *reinterpret_cast<float4*>(other) = __ldg(sp);
-      *reinterpret_cast<float4*>(other + 4) = __ldg(sp + 1);
-      if (!second)
+    const float* row = p.cos_sin + pos * p.rotary_dim + sub * 4;
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(row));
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half));
+    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) other[i] = -other[i];
+    for (int i = 0; i < 4; ++i) {
+      const int a = kInter ? 2 * i : i, b = kInter ? 2 * i + 1 : i + 4;
+      own[a] = own[b] = c[i];
+      other[a] = -s[i];
+      other[b] = s[i];
     }
   }
   if (wp) {
-    float w[8], v[8];
+    float w[8];
     if (p.weight_f32) {
-      load8<float, kVec>(static_cast<const float*>(wp) + sub * 8, w);
-      load8<float, kVec>(static_cast<const float*>(wp) + partner * 8, v);
+      Row8<float> r8;
+      r8.template load<kVec>(static_cast<const float*>(wp), at);
+      r8.values(w);
     } else {
-      load8<T, kVec>(static_cast<const T*>(wp) + sub * 8, w);
-      load8<T, kVec>(static_cast<const T*>(wp) + partner * 8, v);
+      Row8<T> r8;
+      r8.template load<kVec>(static_cast<const T*>(wp), at);
+      r8.values(w);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       own[i] *= w[i];
-      other[i] *= p.interleaved ? w[i ^ 1] : v[i];
+      other[i] *= kInter ? w[i ^ 1] : w[i ^ 4];
     }
   }
-  const int from = (lane - sub) + partner;
   const int64_t b = slot / kBS;
   const int o = (int)(slot - b * kBS);
-  const Divisor scale(which == 2 ? p.v_scale : p.k_scale);
+  const Divisor scale(which == 2 ? p.v_scale : p.k_scale,
+                      which > 0 && (kCache == kFp8 || kCache == kNvfp4));
+  T* q_out = static_cast<T*>(p.q_out) + (t * p.num_q_heads + h0) * kD;
 #pragma unroll
   for (int j = 0; j < kH; ++j) {
-    if (h0 - lane / kLanes + j * kRows >= heads) break;  // the whole warp is past
-    const int h = h0 + j * kRows;
-    const bool on = h < heads;
-    float x[8];
-    raw[j].values(x);
-    float r = 1.f;
-    if (wp) {
-      float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 v = make_float2(x[i], x[i + 1]);
-        s2 = fma2(v, v, s2);
-      }
-      float ss = s2.x + s2.y;
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
-      r = rsqrtf(ss * (1.0f / kD) + p.eps);
-    }
+    if (first + j * kRows >= heads) break;  // the whole warp is past
+    const bool on = h0 + j * kRows < heads;
     if (which < 2) {
-      float y[8];
-      if (p.interleaved) {
+      float x[8], y[8];
+      raw[j].values(x);
+      float r = 1.f;
+      if (wp) {
+        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-      } else if (p.rotary_dim) {
-        raw[j].shuffled(from).values(y);
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
+        r = rsqrtf(ss * (1.0f / kD) + p.eps);
       }
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        float2 z = mul2(make_float2(x[i], x[i + 1]), make_float2(own[i], own[i + 1]));
-        if (turns)
-          z = fma2(make_float2(y[i], y[i + 1]), make_float2(other[i], other[i + 1]), z);
-        z = mul2(z, make_float2(r, r));
-        x[i] = z.x;
-        x[i + 1] = z.y;
+      for (int i = 0; i < 8; ++i) {
+        y[i] = x[i] * own[i];
+        if (turns) y[i] = fmaf(kInter ? x[i ^ 1] : x[i ^ 4], other[i], y[i]);
+        y[i] *= r;
       }
+      raw[j].round(y);
     }
     if (which == 0) {
-      if (on) store8(static_cast<T*>(p.q_out) + (t * p.num_q_heads + h) * kD + sub * 8, x);
+      if (on) raw[j].store(q_out + j * kRows * kD, at);
     } else {
-      // the stored key is that of the input type, whatever the cache's
-      if constexpr (kCache != kSame) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f32(from_f32<T>(x[i]));
-      }
       cache_row<T, kCache, kD>(which == 2 ? p.v_cache : p.k_cache,
-                               b * p.num_kv_heads + h, o, sub, x,
-                               scale, on);
+                               b * p.num_kv_heads + h0 + j * kRows, o, lane, sub, at, pairs,
+                               raw[j], scale, on);
     }
   }
 }
@@ -327,8 +358,19 @@ cudaError_t launch_h(RopeParams p, cudaStream_t stream) {
   p.items = p.q_items + 2 * p.kv_items;
   const int64_t blocks =
       (p.num_tokens * p.items + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks >= (1ll << 29)) return cudaErrorInvalidValue;  // warps: 32 bits
-  norm_rope_kernel<T, kCache, kD, kVec, kH><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+  if (blocks >= (1ll << 28)) return cudaErrorInvalidValue;  // warps: 31 bits
+  // warp / items by a product (Granlund and Montgomery 1994): with 2^l >= items,
+  // l = shift + 1, the factor m = ceil(2^(31 + l) / items) is exact for 31-bit
+  // numerators, since m items - 2^(31 + l) < items <= 2^l
+  p.per_item_shift = 0;
+  while ((2u << p.per_item_shift) < (uint32_t)p.items) ++p.per_item_shift;
+  p.per_item = (uint32_t)((((uint64_t)1 << (32 + p.per_item_shift)) + p.items - 1) / p.items);
+  if (p.interleaved)
+    norm_rope_kernel<T, kCache, kD, true, kVec, kH>
+        <<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+  else
+    norm_rope_kernel<T, kCache, kD, false, kVec, kH>
+        <<<(unsigned)blocks, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
