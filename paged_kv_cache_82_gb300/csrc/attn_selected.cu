@@ -72,21 +72,14 @@ __device__ __forceinline__ Unit find_unit(const SelParams& p, int64_t row, bool 
   u.t = row / p.num_kv_heads;
   u.h = (int)(row - u.t * p.num_kv_heads);
   u.count = __ldg(p.num_selected + row);
-  // requests of equally many tokens (a decode step's): t's place among the
-  // tokens names its request, one round of loads instead of a search's two or
-  // three before the request's own
-  u.r = (int)(u.t * p.s.num_seqs / p.s.num_tokens);
-  ReqMeta m = load_req(p.s.query_start_loc, p.s.seq_lens, u.r, p.s.num_tokens,
-                       p.s.max_query_len, p.s.max_seq_len, p.s.max_blocks_per_seq);
-  if (u.t < m.q0 || u.t >= (int64_t)m.q0 + m.n) {
-    u.r = warp_find_request(p.s.query_start_loc, p.s.num_seqs, u.t);
-    m = load_req(p.s.query_start_loc, p.s.seq_lens, u.r, p.s.num_tokens,
-                 p.s.max_query_len, p.s.max_seq_len, p.s.max_blocks_per_seq);
-  }
-  u.pos = m.L - m.n + (int)(u.t - m.q0);
-  if (u.t < m.q0 || u.t >= (int64_t)m.q0 + m.n) {
+  const TokenReq q = warp_token_request(
+      p.s.query_start_loc, p.s.seq_lens, p.s.num_seqs, u.t, p.s.num_tokens,
+      p.s.max_query_len, p.s.max_seq_len, p.s.max_blocks_per_seq);
+  u.r = q.r;
+  u.pos = q.m.L - q.m.n + (int)(u.t - q.m.q0);
+  if (!q.in) {
     u.count = -1;
-  } else if (!m.ok) {
+  } else if (!q.m.ok) {
     if (tell) flag_error(p.s.err, PA_DEV_ERR_METADATA);
     u.count = -1;
   } else if (u.count < 0 || u.count > p.max_selected) {

@@ -78,6 +78,33 @@ __device__ __forceinline__ int warp_find_request(const int32_t* __restrict__ qsl
   return lo;
 }
 
+// The same with the request's metadata; in: t is one of its tokens.  Where the
+// requests have equally many tokens (a decode step), t's place among the tokens
+// names the request: one round of loads instead of the search's two or three
+// before the request's own.
+struct TokenReq {
+  int r;
+  ReqMeta m;
+  bool in;
+};
+__device__ __forceinline__ TokenReq warp_token_request(
+    const int32_t* __restrict__ qsl, const int32_t* __restrict__ seq_lens, int num_seqs,
+    int64_t t, int64_t num_tokens, int max_query_len, int max_seq_len,
+    int max_blocks_per_seq) {
+  TokenReq q;
+  q.r = (int)(t * num_seqs / num_tokens);
+  q.m = load_req(qsl, seq_lens, q.r, num_tokens, max_query_len, max_seq_len,
+                 max_blocks_per_seq);
+  q.in = t >= q.m.q0 && t < (int64_t)q.m.q0 + q.m.n;
+  if (!q.in) {
+    q.r = warp_find_request(qsl, num_seqs, t);
+    q.m = load_req(qsl, seq_lens, q.r, num_tokens, max_query_len, max_seq_len,
+                   max_blocks_per_seq);
+    q.in = t >= q.m.q0 && t < (int64_t)q.m.q0 + q.m.n;
+  }
+  return q;
+}
+
 // ----------------------------------------------------------------------------
 // shared-memory address helpers
 // ----------------------------------------------------------------------------

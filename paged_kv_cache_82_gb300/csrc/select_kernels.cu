@@ -290,15 +290,16 @@ struct TokenView {
 };
 __device__ __forceinline__ TokenView token_view(const StepView& s, int64_t t, bool tell) {
   TokenView v{0, 0, -1};
-  v.r = warp_find_request(s.query_start_loc, s.num_seqs, t);
-  const ReqMeta m = load_req(s.query_start_loc, s.seq_lens, v.r, s.num_tokens,
-                             s.max_query_len, s.max_seq_len, s.max_blocks_per_seq);
-  if (t < m.q0 || t >= (int64_t)m.q0 + m.n) return v;
-  if (!m.ok) {
+  const TokenReq q =
+      warp_token_request(s.query_start_loc, s.seq_lens, s.num_seqs, t, s.num_tokens,
+                         s.max_query_len, s.max_seq_len, s.max_blocks_per_seq);
+  if (!q.in) return v;
+  if (!q.m.ok) {
     if (tell) flag_error(s.err, PA_DEV_ERR_METADATA);
     return v;
   }
-  v.pos = m.L - m.n + (int)(t - m.q0);
+  v.r = q.r;
+  v.pos = q.m.L - q.m.n + (int)(t - q.m.q0);
   v.blocks = v.pos / kBS + 1;
   return v;
 }
@@ -308,6 +309,13 @@ __device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %1, 0xba98;" : "=r"(d) : "r"(x));
   return d;
+}
+
+// four channels of a bound: the products of the codes with hi where they are
+// positive, lo where they are negative
+__device__ __forceinline__ int bound_dot(uint32_t hi, uint32_t lo, uint32_t codes, int sum) {
+  const uint32_t neg = sign_bytes(codes);
+  return __dp4a((int)((hi & ~neg) | (lo & neg)), (int)codes, sum);
 }
 
 // 16 consecutive elements as fp32 (16-byte aligned)
@@ -323,36 +331,60 @@ __device__ __forceinline__ void load16(const T* src, float (&x)[16]) {
   }
 }
 
-#ifndef PA_SCORE_FLIGHT
-#define PA_SCORE_FLIGHT 2
-#endif
-#ifndef PA_SCORE_CTAS
-#define PA_SCORE_CTAS 3
-#endif
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 constexpr int kScoreWarps = 8;
-constexpr int kScoreChunkMax = 256;
-constexpr int kScoreGroup = 32;  // blocks a warp scores in a row: one id per lane
+constexpr int kScoreGroup = 16;  // records a warp stages and scores at a time
+// Buffers of a warp, and CTAs per SM: 64 rows of 8 heads x 512 to 4096 blocks,
+// both kernels, 63 us with 2 and 3, 74 with 3 and 2 or with 2 and 2.
+constexpr int kScoreBufs = 2;
+constexpr int kScoreCtas = 3;
+// Blocks of one CTA: 62 us with 128, 63 with 256, 67 with 64 (each warp codes
+// its query anew); one row of 8192 blocks 14.5 us with 32, 15.6 with 64, 17 with
+// 16.
+constexpr int kScoreChunkMax = 128, kScoreChunkMin = 32;
+
+template <int kD, int kG>
+struct ScoreLayout {
+  static constexpr int kRec = PA_BOUNDS_BYTES(kD);
+  static constexpr int kPieces = kRec / 16;               // of 16 bytes, an odd number
+  static constexpr int kBuf = kScoreGroup * kRec;         // bytes
+  static constexpr int kCodes = kG * kD;
+  static constexpr int kWarp = kScoreBufs * kBuf + kCodes;
+  static constexpr int kSmem = kScoreWarps * kWarp;
+};
 
 // One CTA: one token, p.chunk cache blocks, all KV heads.  A warp takes one
 // KV head (the heads' records of a block are one contiguous range, read by the
 // CTA's warps at about the same time); with fewer heads than warps, several
 // warps share a head's blocks.
 //
-// kD / 16 lanes hold a record's 16 channels each, so that a warp reads 512 /
-// kD records with two 16-byte loads per lane, four such steps in flight.  The
-// codes of kG query heads stay in registers, with a byte mask of the negative
-// ones: the product's bound is picked by one logic operation per word, and a
-// word's four products are one dp4a -- 8 instructions per 16 channels and head,
-// 1/4 of the issue slots that the record's bytes leave at 4 heads.
+// Each warp copies 16 records at a time into shared memory of its own, the
+// next ones while it scores these, so that what is on its way does not wait
+// for registers.  Two lanes score a record, half of its channels each; a
+// record's 17 (or 9) pieces of 16 bytes put the 8 lanes of a quarter warp into
+// different banks.  The codes of kG query heads lie in shared memory too: their
+// signs pick the product's bound in two logic operations per word, and a word's
+// four products are one dp4a.
 template <typename TQ, int kD, int kG>
-__global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : PA_SCORE_CTAS) score_kernel(const ScoreParams p) {
-  constexpr int kLanes = kD / 16;
-  constexpr int kRecs = 32 / kLanes;
-  constexpr int kSteps = kScoreGroup / kRecs;
-  constexpr int kFlight = PA_SCORE_FLIGHT;  // steps whose loads are out together
+__global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : kScoreCtas)
+score_kernel(const ScoreParams p) {
+  using Ly = ScoreLayout<kD, kG>;
+  constexpr int kLanes = kD / 16;        // lanes of one query head's codes
+  constexpr int kParts = 32 / kLanes;    // heads coded at a time
+  constexpr int kCopies = (kScoreGroup * Ly::kPieces + 31) / 32;
+  extern __shared__ __align__(16) uint8_t score_smem[];
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane % kLanes, rec = lane / kLanes;
   const int64_t t = p.t0 + blockIdx.y;
   const int first = (int)blockIdx.x * p.chunk;
   const int sharing = max(1, kScoreWarps / p.num_kv_heads);  // warps of one head
@@ -362,14 +394,53 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : PA_SCORE_CTAS)
   const int last = min(first + p.chunk, tv.blocks);
   const int kept_last = tv.blocks - p.keep_last;
   const int32_t* table = p.s.block_tables + (int64_t)tv.r * p.s.max_blocks_per_seq;
+  uint8_t* bufs = score_smem + warp * Ly::kWarp;
+  uint8_t* codes = bufs + kScoreBufs * Ly::kBuf;
+  const uint32_t bufs_at = smem_u32(bufs);
+  // this lane's record and half of the channels
+  const int mine = lane & 15, half = lane >> 4;
   const int passes = (p.group + kG - 1) / kG;
+  const int stride = sharing * kScoreGroup;
+  const int b_first = first + (warp / p.num_kv_heads) * kScoreGroup;
   for (int h = warp % p.num_kv_heads; h < p.num_kv_heads; h += kScoreWarps) {
+    const uint8_t* head_bounds = p.bounds + (int64_t)h * Ly::kRec;
+    const int64_t block_bytes = (int64_t)p.num_kv_heads * Ly::kRec;
+    // the physical block of block b; -1: kept (not read), none, or out of range
+    auto block_id = [&](int b) {
+      if (b >= last || b < p.keep_first || b >= kept_last) return -1;
+      const int id = __ldg(table + b);
+      if (id >= 0 && (int64_t)id < p.s.num_blocks) return id;
+      flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
+      return -1;
+    };
+    // copies of the 16 records from block b on: piece k = lane, lane + 32, ..
+    auto stage = [&](int b, int buf) {
+      const int id = b < last ? block_id(b + mine) : -1;
+      int rec = lane / Ly::kPieces, off = lane - rec * Ly::kPieces;
+      const uint32_t dst = bufs_at + buf * Ly::kBuf + lane * 16;
+#pragma unroll
+      for (int k = 0; k < kCopies; ++k) {
+        const int from = __shfl_sync(~0u, id, rec & 15);
+        if (from >= 0 && rec < kScoreGroup)
+          copy16_async(dst + k * 512, head_bounds + from * block_bytes + off * 16);
+        off += 32 % Ly::kPieces;
+        rec += 32 / Ly::kPieces;
+        if (off >= Ly::kPieces) off -= Ly::kPieces, ++rec;
+      }
+      copy_commit();
+      return id;
+    };
+    int ids[kScoreBufs];
+#pragma unroll
+    for (int k = 0; k < kScoreBufs - 1; ++k) ids[k] = stage(b_first + k * stride, k);
+
     const TQ* qp = static_cast<const TQ*>(p.q) +
-                   (t * p.num_q_heads + (int64_t)h * p.group) * kD + sub * 16;
+                   (t * p.num_q_heads + (int64_t)h * p.group) * kD;
     // one scale for all heads of the group: each part of the warp looks at some
+    const int sub = lane % kLanes, part = lane / kLanes;
     float x[16], big = 0.f;
-    for (int g = rec; g < p.group; g += kRecs) {
-      load16(qp + g * kD, x);
+    for (int g = part; g < p.group; g += kParts) {
+      load16(qp + g * kD + sub * 16, x);
 #pragma unroll
       for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(x[i]));
     }
@@ -378,121 +449,81 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : PA_SCORE_CTAS)
     const float sq = __fdiv_rn(big, 127.0f);
     uint32_t* keys = p.keys + ((int64_t)blockIdx.y * p.num_kv_heads + h) * p.row_scores;
     for (int pass = 0; pass < passes; ++pass) {
-      // codes of the pass's heads (past the group's end: its last head again),
-      // each head's by one part of the warp
-      uint32_t code[kG][4];
+      if (pass > 0) {
 #pragma unroll
-      for (int g0 = 0; g0 < kG; g0 += kRecs) {
-        uint32_t mine[4] = {0, 0, 0, 0};
-        if (g0 + rec < kG) {
-          load16(qp + min(pass * kG + g0 + rec, p.group - 1) * kD, x);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            int c = sq > 0.f ? __float2int_rn(__fdiv_rn(x[i], sq)) : 0;
-            c = min(127, max(-127, c));
-            mine[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
-          }
-        }
-#pragma unroll
-        for (int g = g0; g < g0 + kRecs && g < kG; ++g)
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            code[g][w] = __shfl_sync(~0u, mine[w], (g - g0) * kLanes + sub);
+        for (int k = 0; k < kScoreBufs - 1; ++k) ids[k] = stage(b_first + k * stride, k);
       }
-      // the physical block of a group's block b, one per lane; kept blocks are
-      // not read
-      const uint8_t* head_bounds = p.bounds + (int64_t)h * bounds_bytes(kD);
-      const int64_t block_bytes = (int64_t)p.num_kv_heads * bounds_bytes(kD);
-      auto group_id = [&](int b) {
-        if (b >= last || b < p.keep_first || b >= kept_last) return -1;
-        const int id = __ldg(table + b);
-        if (id >= 0 && (int64_t)id < p.s.num_blocks) return id;
-        flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
-        return -1;
-      };
-      const int stride = sharing * kScoreGroup;
-      const int b_first = first + (warp / p.num_kv_heads) * kScoreGroup;
-      int next_id = group_id(b_first + lane);
+      // codes of the pass's heads (past the group's end: its last head again)
+      __syncwarp();
+      for (int g = part; g < kG; g += kParts) {
+        load16(qp + (int64_t)min(pass * kG + g, p.group - 1) * kD + sub * 16, x);
+        uint32_t c4[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          int c = sq > 0.f ? __float2int_rn(__fdiv_rn(x[i], sq)) : 0;
+          c = min(127, max(-127, c));
+          c4[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+        }
+        *reinterpret_cast<uint4*>(codes + g * kD + sub * 16) =
+            make_uint4(c4[0], c4[1], c4[2], c4[3]);
+      }
+      __syncwarp();
+      int buf = 0;
       for (int b0 = b_first; b0 < last; b0 += stride) {
-        const int mb = b0 + lane;
-        const bool kept = mb < p.keep_first || mb >= kept_last;
-        const int id = next_id;
-        next_id = group_id(b0 + stride + lane);
-        uint32_t mine = kKeptKey;  // lane l: the key of block b0 + l
+        const int id = ids[0];
 #pragma unroll
-        for (int s0 = 0; s0 < kSteps; s0 += kFlight) {
-          uint4 hi[kFlight], lo[kFlight];
-          float sc[kFlight];
+        for (int k = 0; k + 1 < kScoreBufs; ++k) ids[k] = ids[k + 1];
+        {
+          const int to = buf + kScoreBufs - 1;
+          ids[kScoreBufs - 2] = stage(b0 + (kScoreBufs - 1) * stride,
+                                      to >= kScoreBufs ? to - kScoreBufs : to);
+        }
+        copy_wait<kScoreBufs - 1>();
+        __syncwarp();
+        const uint8_t* rec = bufs + buf * Ly::kBuf + mine * Ly::kRec;
+        const uint4* hi = reinterpret_cast<const uint4*>(rec + half * (kD / 2));
+        const uint4* lo = reinterpret_cast<const uint4*>(rec + kD + half * (kD / 2));
+        const uint4* code = reinterpret_cast<const uint4*>(codes + half * (kD / 2));
+        int dot[kG];
 #pragma unroll
-          for (int f = 0; f < kFlight; ++f) {
-            const int blk = __shfl_sync(~0u, id, (s0 + f) * kRecs + rec);
-            hi[f] = lo[f] = make_uint4(0, 0, 0, 0);
-            sc[f] = 0.f;
-            if (blk >= 0) {
-              const uint8_t* r = head_bounds + blk * block_bytes;
-              hi[f] = __ldg(reinterpret_cast<const uint4*>(r + sub * 16));
-              lo[f] = __ldg(reinterpret_cast<const uint4*>(r + kD + sub * 16));
-              sc[f] = __ldg(reinterpret_cast<const float*>(r + 2 * kD));
-            }
-          }
+        for (int g = 0; g < kG; ++g) dot[g] = 0;
 #pragma unroll
-          for (int f = 0; f < kFlight; ++f) {
-            const uint32_t hw[4] = {hi[f].x, hi[f].y, hi[f].z, hi[f].w};
-            const uint32_t lw[4] = {lo[f].x, lo[f].y, lo[f].z, lo[f].w};
-            int dot[kG];
+        for (int w = 0; w < kD / 32; ++w) {
+          const uint4 a = hi[w], c = lo[w];
 #pragma unroll
-            for (int g = 0; g < kG; ++g) {
-              dot[g] = 0;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const uint32_t neg = sign_bytes(code[g][w]);
-                dot[g] = __dp4a((int)((hw[w] & ~neg) | (lw[w] & neg)), (int)code[g][w],
-                                dot[g]);
-              }
-            }
-            // sum over the record's lanes: while a lane holds several heads, it
-            // keeps one half of them and gives the other half away
-            int held = kG, bit = 1;
-#pragma unroll
-            for (; bit < kLanes; bit <<= 1) {
-              if (held > 1) {
-                held >>= 1;
-                const bool up = lane & bit;
-#pragma unroll
-                for (int g = 0; g < kG / 2; ++g)
-                  if (g < held) {
-                    const int give = up ? dot[g] : dot[g + held];
-                    const int keep = up ? dot[g + held] : dot[g];
-                    dot[g] = keep + __shfl_xor_sync(~0u, give, bit);
-                  }
-              } else {
-                dot[0] += __shfl_xor_sync(~0u, dot[0], bit);
-              }
-            }
-            int best = dot[0];
-#pragma unroll
-            for (int g = 1; g < kG; ++g)
-              if (g < held) best = max(best, dot[g]);
-#pragma unroll
-            for (int d = 1; d < kLanes; d <<= 1)
-              best = max(best, __shfl_xor_sync(~0u, best, d));
-            // to the lane of the block, as the score's key; with further passes
-            // over the group's heads, as the sum
-            const int from = (lane % kRecs) * kLanes;
-            const int b_best = __shfl_sync(~0u, best, from);
-            const float b_sc = __shfl_sync(~0u, sc[f], from);
-            if (lane / kRecs == s0 + f && id >= 0) {
-              int all = b_best;
-              if (pass > 0) all = max(all, (int)keys[mb]);
-              // + 0: a zero is a positive zero
-              mine = pass + 1 < passes
-                         ? (uint32_t)all
-                         : score_key(__fmul_rn((float)all, b_sc) + 0.0f);
-            }
+          for (int g = 0; g < kG; ++g) {
+            const uint4 q = code[g * (kD / 16) + w];
+            dot[g] = bound_dot(a.x, c.x, q.x, dot[g]);
+            dot[g] = bound_dot(a.y, c.y, q.y, dot[g]);
+            dot[g] = bound_dot(a.z, c.z, q.z, dot[g]);
+            dot[g] = bound_dot(a.w, c.w, q.w, dot[g]);
           }
         }
-        if (mb < last) keys[mb] = id < 0 && !kept ? score_key(-INFINITY) : mine;
+        const float sc = *reinterpret_cast<const float*>(rec + 2 * kD);
+        __syncwarp();  // the buffer may be copied into again
+        int best = INT_MIN;
+#pragma unroll
+        for (int g = 0; g < kG; ++g)
+          best = max(best, dot[g] + __shfl_xor_sync(~0u, dot[g], 16));
+        const int b = b0 + mine;
+        if (half == 0 && b < last) {
+          uint32_t key;
+          if (b < p.keep_first || b >= kept_last) {
+            key = kKeptKey;
+          } else if (id < 0) {
+            key = score_key(-INFINITY);
+          } else {
+            if (pass > 0) best = max(best, (int)keys[b]);
+            // + 0: a zero is a positive zero
+            key = pass + 1 < passes ? (uint32_t)best
+                                    : score_key(__fmul_rn((float)best, sc) + 0.0f);
+          }
+          keys[b] = key;
+        }
+        buf = buf + 1 == kScoreBufs ? 0 : buf + 1;
       }
+      copy_wait<0>();
+      __syncwarp();
     }
   }
 }
@@ -510,9 +541,7 @@ struct TopkParams {
   int32_t* num_selected;
 };
 
-constexpr int kTopkThreads = 512;
-constexpr int kTopkWarps = kTopkThreads / 32;
-constexpr int kTopkBits = 10;  // of a key per round: two bins per thread
+constexpr int kTopkBits = 10;  // of a key per round
 constexpr int kTopkBins = 1 << kTopkBits;
 
 // One CTA per (token, KV head).  The keys' range is cut into 1024 bins, the
@@ -520,10 +549,13 @@ constexpr int kTopkBins = 1 << kTopkBits;
 // leaves only keys that are all taken (two or three rounds: the first range
 // is that of the row's own keys, so no round is spent on their common bits).
 // Then each warp writes the entries of its contiguous part of the row in
-// order.  kPer keys per lane are held in registers (up to 512 kPer blocks);
+// order.  kPer keys per lane are held in registers (kTopkThreads x kPer blocks);
 // kPer = 0 reads them again each time.
-template <int kPer>
-__global__ void __launch_bounds__(kTopkThreads, 2) topk_kernel(const TopkParams p) {
+template <int kTopkThreads, int kPer>
+__global__ void __launch_bounds__(kTopkThreads, 65536 / kTopkThreads / (kPer > 16 ? 80 : 64))
+topk_kernel(const TopkParams p) {
+  constexpr int kTopkWarps = kTopkThreads / 32;
+  constexpr int kTopkOwn = kTopkBins / kTopkThreads;  // bins of a thread
   __shared__ int hist[kTopkBins];
   __shared__ uint32_t s_lo[kTopkWarps], s_hi[kTopkWarps];
   __shared__ int s_warp[kTopkWarps], s_equal[kTopkWarps];
@@ -597,15 +629,18 @@ __global__ void __launch_bounds__(kTopkThreads, 2) topk_kernel(const TopkParams 
   if (need > 0) {
     while (bits > 0) {
       const int shift = max(0, bits - kTopkBits);
-      hist[tid] = hist[tid + kTopkThreads] = 0;
+#pragma unroll
+      for (int i = 0; i < kTopkOwn; ++i) hist[tid + i * kTopkThreads] = 0;
       __syncthreads();
       each([&](uint32_t k, int, bool on) {
         if (on && k >= lo && k <= top) atomicAdd(&hist[(k - lo) >> shift], 1);
       });
       __syncthreads();
-      // keys in the bins above this thread's two
-      const int c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
-      int above = c0 + c1;
+      // keys in the bins above this thread's
+      int own = 0;
+#pragma unroll
+      for (int i = 0; i < kTopkOwn; ++i) own += hist[kTopkOwn * tid + i];
+      int above = own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_down_sync(~0u, above, d);
@@ -613,13 +648,14 @@ __global__ void __launch_bounds__(kTopkThreads, 2) topk_kernel(const TopkParams 
       }
       if (lane == 0) s_warp[warp] = above;
       __syncthreads();
-      above -= c0 + c1;
+      above -= own;
       for (int w = warp + 1; w < kTopkWarps; ++w) above += s_warp[w];
-      if (above < need && above + c0 + c1 >= need) {
-        const bool second = above + c1 >= need;
-        s_bin = 2 * tid + (second ? 1 : 0);
-        s_need = need - above - (second ? 0 : c1);
-        s_count = second ? c1 : c0;
+      if (above < need && above + own >= need) {
+        int bin = kTopkOwn * tid + kTopkOwn - 1;
+        for (; above + hist[bin] < need; --bin) above += hist[bin];
+        s_bin = bin;
+        s_need = need - above;
+        s_count = hist[bin];
       }
       __syncthreads();
       lo += (uint32_t)s_bin << shift;
@@ -683,20 +719,25 @@ cudaError_t launch_summarise_t(const StepView& s, const void* k_cache, int num_k
              : launch_summarise_d<kPg, 64>(s, k_cache, num_kv_heads, bounds, stream);
 }
 
-template <typename TQ, int kD>
-cudaError_t launch_score_d(const ScoreParams& p, dim3 grid, cudaStream_t stream) {
-  // query heads held at once: the group's, up to 8 (more: in passes)
-  if (p.group == 1)
-    score_kernel<TQ, kD, 1><<<grid, kScoreWarps * 32, 0, stream>>>(p);
-  else if (p.group == 2)
-    score_kernel<TQ, kD, 2><<<grid, kScoreWarps * 32, 0, stream>>>(p);
-  else if (p.group <= 4)
-    score_kernel<TQ, kD, 4><<<grid, kScoreWarps * 32, 0, stream>>>(p);
-  else
-    score_kernel<TQ, kD, 8><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+template <typename TQ, int kD, int kG>
+cudaError_t launch_score_g(const ScoreParams& p, dim3 grid, cudaStream_t stream) {
+  constexpr int kSmem = ScoreLayout<kD, kG>::kSmem;
+  const cudaError_t a = cudaFuncSetAttribute(
+      score_kernel<TQ, kD, kG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (a != cudaSuccess) return a;
+  score_kernel<TQ, kD, kG><<<grid, kScoreWarps * 32, kSmem, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
+}
+
+template <typename TQ, int kD>
+cudaError_t launch_score_d(const ScoreParams& p, dim3 grid, cudaStream_t stream) {
+  // query heads held at once: the group's, up to 8 (more: in passes)
+  if (p.group == 1) return launch_score_g<TQ, kD, 1>(p, grid, stream);
+  if (p.group == 2) return launch_score_g<TQ, kD, 2>(p, grid, stream);
+  if (p.group <= 4) return launch_score_g<TQ, kD, 4>(p, grid, stream);
+  return launch_score_g<TQ, kD, 8>(p, grid, stream);
 }
 
 template <typename TQ>
@@ -767,7 +808,7 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
       // as many blocks per CTA as leave four CTAs per SM: a warp's work on the
       // query (its codes) is then spread over more records
       p.chunk = kScoreChunkMax;
-      while (p.chunk > kScoreGroup &&
+      while (p.chunk > kScoreChunkMin &&
              nt * ((max_blocks + p.chunk - 1) / p.chunk) < 4ll * num_sms)
         p.chunk /= 2;
       const dim3 grid((unsigned)((max_blocks + p.chunk - 1) / p.chunk), (unsigned)nt);
@@ -792,18 +833,24 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
     // starts while the scores are being made, waits for them
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(nt * num_kv_heads));
-    cfg.blockDim = dim3(kTopkThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = max_blocks > max_selected ? 1 : 0;
-    const cudaError_t e = max_blocks <= 4 * kTopkThreads
-                              ? cudaLaunchKernelEx(&cfg, topk_kernel<4>, tp)
-                          : max_blocks <= 16 * kTopkThreads
-                              ? cudaLaunchKernelEx(&cfg, topk_kernel<16>, tp)
-                              : cudaLaunchKernelEx(&cfg, topk_kernel<0>, tp);
+    // rows enough for every SM: 256 threads each (four to an SM: 512 rows of
+    // 512 to 4096 blocks 12.8 us, with 512 threads 15.9); fewer: 1024, for the
+    // one row's sake
+    const bool many = nt * num_kv_heads > num_sms;
+    cfg.blockDim = dim3(many ? 256 : 1024);
+    const cudaError_t e =
+        !many ? (max_blocks <= 8 * 1024 ? cudaLaunchKernelEx(&cfg, topk_kernel<1024, 8>, tp)
+                                        : cudaLaunchKernelEx(&cfg, topk_kernel<1024, 0>, tp))
+        : max_blocks <= 4 * 256  ? cudaLaunchKernelEx(&cfg, topk_kernel<256, 4>, tp)
+        : max_blocks <= 16 * 256 ? cudaLaunchKernelEx(&cfg, topk_kernel<256, 16>, tp)
+        : max_blocks <= 32 * 256 ? cudaLaunchKernelEx(&cfg, topk_kernel<256, 32>, tp)
+                                 : cudaLaunchKernelEx(&cfg, topk_kernel<256, 0>, tp);
     if (e != cudaSuccess) return e;
     count_launch();
   }
