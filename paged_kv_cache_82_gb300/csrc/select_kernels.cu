@@ -142,12 +142,22 @@ struct Range8 {
       lo[i] = min_of(lo[i], __shfl_xor_sync(~0u, lo[i], mask));
     }
   }
+  __device__ __forceinline__ static uint32_t abs_of(uint32_t a) {
+    if constexpr (!kPair) {
+      return a & 0x7FFFFFFFu;
+    } else if constexpr (kBF) {
+      const __nv_bfloat162 m = __habs2(*reinterpret_cast<__nv_bfloat162*>(&a));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+      const __half2 m = __habs2(*reinterpret_cast<__half2*>(&a));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    }
+  }
   // the largest magnitude among the lane's channels
   __device__ __forceinline__ float largest() const {
-    constexpr uint32_t kAbs = kPair ? 0x7FFF7FFFu : 0x7FFFFFFFu;
-    uint32_t m = max_of(hi[0] & kAbs, lo[0] & kAbs);
+    uint32_t m = max_of(abs_of(hi[0]), abs_of(lo[0]));
 #pragma unroll
-    for (int i = 1; i < kN; ++i) m = max_of(m, max_of(hi[i] & kAbs, lo[i] & kAbs));
+    for (int i = 1; i < kN; ++i) m = max_of(m, max_of(abs_of(hi[i]), abs_of(lo[i])));
     if constexpr (!kPair) return __uint_as_float(m);
     const uint32_t w[kN] = {m};
     return fmaxf(value(w, 0), value(w, 1));
@@ -171,14 +181,14 @@ struct Range8 {
 // by the chain of loads (lengths, block id, page) when there are few.
 template <int kPg, int kD>
 __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_cache,
-                                              int num_kv_heads, int r, int item, int nth,
-                                              int h, uint8_t* bounds) {
+                                              int num_kv_heads, int r, int nth, int h,
+                                              uint8_t* bounds) {
   constexpr int kLanes = kD / 8, kRows = 32 / kLanes, kReads = kBS / kRows;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, part = lane / kLanes;
   const ReqMeta m = load_req(s.query_start_loc, s.seq_lens, r, s.num_tokens,
                              s.max_query_len, s.max_seq_len, s.max_blocks_per_seq);
   if (!m.ok) {
-    if (item == 0 && lane == 0) flag_error(s.err, PA_DEV_ERR_METADATA);
+    if (nth == 0 && h == 0 && lane == 0) flag_error(s.err, PA_DEV_ERR_METADATA);
     return;
   }
   const int b = (m.L - m.n) / kBS + nth;  // the nth block this step wrote to
@@ -192,9 +202,15 @@ __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_c
   const int tokens = min(kBS, m.L - b * kBS);
   // a place past the block's tokens reads its last token again
   PageWords<kPg> words[kReads];
+  if (tokens == kBS) {
 #pragma unroll
-  for (int i = 0; i < kReads; ++i)
-    words[i] = page_words<kPg, kD>(k_cache, page, min(i * kRows + part, tokens - 1), sub);
+    for (int i = 0; i < kReads; ++i)
+      words[i] = page_words<kPg, kD>(k_cache, page, i * kRows + part, sub);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kReads; ++i)
+      words[i] = page_words<kPg, kD>(k_cache, page, min(i * kRows + part, tokens - 1), sub);
+  }
   using Range = Range8<kPg>;
   Range range;
   range.clear();
@@ -204,14 +220,13 @@ __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_c
   for (int d = kLanes; d < 32; d <<= 1) range.join(d);
   float big = range.largest();
   // The first part of the warp has the codes of the largest values, the second
-  // those of the smallest, as floor(x) = -ceil(-x).
+  // those of the smallest: ceil(hi / s) and -ceil(lo / -s).
   const bool low = part & 1;
   float x[8];
   {
     uint32_t w[Range::kN];
 #pragma unroll
-    for (int i = 0; i < Range::kN; ++i)
-      w[i] = low ? range.lo[i] ^ (Range::kPair ? 0x80008000u : 0x80000000u) : range.hi[i];
+    for (int i = 0; i < Range::kN; ++i) w[i] = low ? range.lo[i] : range.hi[i];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = Range::value(w, i);
   }
@@ -229,17 +244,33 @@ __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_c
 #pragma unroll
   for (int d = 1; d < kLanes; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
   const float sc = __fdiv_rn(big, 127.0f);
-  Divisor by(sc);
-  if (kPg == kPgF32) by.easy = false;  // fp32 keys may be as small as 2^-149
-  float y[8];
-  divide(x, by, y);
-  int c[8];
+  // fp32 keys may be as small as 2^-149: their quotients are divided out
+  const Divisor by(sc, kPg != kPgF32);
+  const float s1 = low ? -sc : sc, rcp = low ? -by.rcp : by.rcp;
+  // c = 1.5 x 2^23 + ceil(q) by a sum rounded up: the code is its lowest byte.
+  // The smallest values' sign turns about 1.5 x 2^23.
+  constexpr float kUnit = 12582912.0f;
+  const float turn = low ? -1.f : 1.f, about = low ? 2 * kUnit : 0.f;
+  uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = sc > 0.f ? __float2int_ru(fminf(y[i], 127.0f)) : 0;
-  uint32_t code[2] = {0, 0};
+  for (int i = 0; i < 8; ++i) {
+    float q;
+    if (by.easy) {
+      // Divisor's two corrections; |x| <= 127.01 s, so nothing overflows, and a
+      // zero's sign does not matter
+      q = x[i] * rcp;
+      q = fmaf(fmaf(-q, s1, x[i]), rcp, q);
+      q = fmaf(fmaf(-q, s1, x[i]), rcp, q);
+    } else {
+      q = sc > 0.f ? __fdiv_rn(x[i], s1) : 0.f;
+    }
+    c[i] = __float_as_uint(fmaf(__fadd_ru(fminf(q, 127.0f), kUnit), turn, about));
+  }
+  uint32_t code[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    code[i >> 2] |= ((uint32_t)(low ? -c[i] : c[i]) & 0xFFu) << (8 * (i & 3));
+  for (int k = 0; k < 2; ++k)
+    code[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040),
+                          __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040), 0x5410);
   uint8_t* rec = bounds + page * bounds_bytes(kD);
   if (part < 2)
     *reinterpret_cast<uint2*>(rec + (low ? kD : 0) + sub * 8) = make_uint2(code[0], code[1]);
@@ -251,10 +282,10 @@ template <int kPg, int kD>
 __global__ void __launch_bounds__(kThreads)
 summarise_kernel(StepView s, const void* __restrict__ k_cache, int num_kv_heads,
                  uint8_t* __restrict__ bounds) {
-  const int item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int nth = item / num_kv_heads, h = item - nth * num_kv_heads;
+  const int nth = blockIdx.x, h = blockIdx.z * (blockDim.x / 32) + (threadIdx.x >> 5);
+  if (h >= num_kv_heads) return;
   for (int r = blockIdx.y; r < s.num_seqs; r += gridDim.y)
-    summarise_one<kPg, kD>(s, k_cache, num_kv_heads, r, item, nth, h, bounds);
+    summarise_one<kPg, kD>(s, k_cache, num_kv_heads, r, nth, h, bounds);
 }
 
 // ---------------------------------------------------------------------------
@@ -701,10 +732,12 @@ cudaError_t launch_summarise_d(const StepView& s, const void* k_cache, int num_k
   // blocks a request of max_query_len tokens writes to, at most
   const int64_t wide = std::min<int64_t>((s.max_query_len + kBS - 2) / kBS + 1,
                                          (s.max_seq_len + kBS - 1) / kBS);
-  const int64_t per_seq = (wide * num_kv_heads + kThreads / 32 - 1) / (kThreads / 32);
-  if (per_seq * (kThreads / 32) > 0x7fffffffll) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)per_seq, (unsigned)std::min(s.num_seqs, 65535));
-  summarise_kernel<kPg, kD><<<grid, kThreads, 0, stream>>>(
+  // a warp per KV head, eight to a CTA at most
+  const int warps = std::min(num_kv_heads, kThreads / 32);
+  const dim3 grid((unsigned)wide, (unsigned)std::min(s.num_seqs, 65535),
+                  (unsigned)((num_kv_heads + warps - 1) / warps));
+  if (grid.z > 65535) return cudaErrorInvalidValue;
+  summarise_kernel<kPg, kD><<<grid, warps * 32, 0, stream>>>(
       s, k_cache, num_kv_heads, static_cast<uint8_t*>(bounds));
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
