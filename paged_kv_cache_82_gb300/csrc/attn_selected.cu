@@ -22,7 +22,6 @@
 // barrier in the loop: each warp walks its own pages, and the next page's K
 // (then V) loads go out as soon as the MMAs have consumed the registers.
 #include <algorithm>
-#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -39,7 +38,7 @@ constexpr int kJoinThreads = 256;  // 8 heads x 128 channels, four per thread
 constexpr int kMinShare = PA_SEL_SHARE;  // list entries of a CTA, at least
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum : int { kB16 = 0, kH16 = 1, kF8 = 2 };  // bf16, f16, E4M3 pages
+enum : int { kB16 = 0, kH16, kF8, kI4, kN4 };  // bf16, f16, E4M3, INT4, NVFP4 pages
 
 struct SelParams {
   StepView s;
@@ -116,34 +115,11 @@ __device__ __forceinline__ Entry list_entry(const SelParams& p, const Unit& u, i
 }
 
 // ---------------------------------------------------------------------------
-// the types without an MMA form (fp32, 4-bit pages): one warp per (token,
-// query head)'s share of the list, four warps to a list
+// fp32 caches, which have no MMA of their precision: four warps per (token,
+// query head), each with a part of the list
 // ---------------------------------------------------------------------------
-struct F32Page {};
-struct Int4Page {};
-struct Nvfp4Page {};
-
-template <typename TP, int kD>
-__device__ __forceinline__ float page_elem(const void* base, int64_t page, int o, int d) {
-  if constexpr (std::is_same<TP, F32Page>::value) {
-    return __ldg(static_cast<const float*>(base) + (page * kBS + o) * kD + d);
-  } else {
-    constexpr bool nv = std::is_same<TP, Nvfp4Page>::value;
-    const uint8_t* pg =
-        static_cast<const uint8_t*>(base) + page * (nv ? 9 * kD : 8 * kD + 64);
-    const uint32_t byte = __ldg(pg + o * (kD / 2) + d / 2);
-    const uint32_t nib = (d & 1) ? byte >> 4 : byte & 15u;
-    if constexpr (nv)
-      return e4m3_to_f32(__ldg(pg + kBS * (kD / 2) + o * (kD / 16) + d / 16)) *
-             e2m1_to_f32(nib);
-    else
-      return __ldg(reinterpret_cast<const float*>(pg + kBS * (kD / 2) + 4 * o)) *
-             (float)((int)(nib ^ 8u) - 8);
-  }
-}
-
-template <typename TQ, typename TP, int kD>
-__global__ void __launch_bounds__(kThreads) selected_generic_kernel(const SelParams p) {
+template <int kD>
+__global__ void __launch_bounds__(kThreads) selected_f32_kernel(const SelParams p) {
   constexpr int kPer = kD / 32;
   __shared__ float s_acc[kWarps][kD], s_m[kWarps], s_l[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -151,23 +127,25 @@ __global__ void __launch_bounds__(kThreads) selected_generic_kernel(const SelPar
   const int hq = (int)(blockIdx.x % p.num_q_heads);
   const Unit u = find_unit(p, t * p.num_kv_heads + hq / p.group, threadIdx.x == 0);
   if (u.count < 0) return;
-  const TQ* qp = static_cast<const TQ*>(p.q) + (t * p.num_q_heads + hq) * kD;
+  const float* qp = static_cast<const float*>(p.q) + (t * p.num_q_heads + hq) * kD;
   float qv[kPer], acc[kPer], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    qv[k] = to_f32(qp[lane + 32 * k]) * p.scale * p.k_scale;
+    qv[k] = qp[lane + 32 * k] * p.scale;
     acc[k] = 0.f;
   }
   for (int i = warp; i < u.count; i += kWarps) {
     const Entry e = list_entry(p, u, i);
     if (e.phys < 0) continue;
-    const int64_t page = (int64_t)e.phys * p.num_kv_heads + u.h;
+    const int64_t page = ((int64_t)e.phys * p.num_kv_heads + u.h) * (kBS * kD);
+    const float* keys_at = static_cast<const float*>(p.k_cache) + page;
+    const float* values_at = static_cast<const float*>(p.v_cache) + page;
     const int keys = min(kBS, u.pos - e.block * kBS + 1);
     for (int o = 0; o < keys; ++o) {
       float dot = 0.f;
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
-        dot += qv[k] * page_elem<TP, kD>(p.k_cache, page, o, lane + 32 * k);
+        dot += qv[k] * __ldg(keys_at + o * kD + lane + 32 * k);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
       const float mn = fmaxf(m, dot);
@@ -176,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) selected_generic_kernel(const SelPar
       l = l * al + pj;
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
-        acc[k] = acc[k] * al + pj * page_elem<TP, kD>(p.v_cache, page, o, lane + 32 * k);
+        acc[k] = acc[k] * al + pj * __ldg(values_at + o * kD + lane + 32 * k);
       m = mn;
     }
   }
@@ -193,8 +171,7 @@ __global__ void __launch_bounds__(kThreads) selected_generic_kernel(const SelPar
       a += f * s_acc[w][d];
       ls += f * s_l[w];
     }
-    static_cast<TQ*>(p.out)[(t * p.num_q_heads + hq) * kD + d] =
-        from_f32<TQ>(ls > 0.f ? a / ls * p.v_scale : ls);
+    static_cast<float*>(p.out)[(t * p.num_q_heads + hq) * kD + d] = ls > 0.f ? a / ls : ls;
   }
 }
 
@@ -215,24 +192,86 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 
 
-// A lane's words of one row of a page: 16 bytes per chunk
 template <int kPg, int kD>
 struct PageTraits {
-  static constexpr int kEB = kPg == kF8 ? 1 : 2;
-  static constexpr int kRowBytes = kD * kEB;
-  // K: lane (r, c) reads 16 bytes at 16 c + 64 i of rows r and r + 8
-  static constexpr int kKChunks = kRowBytes / 64;
-  // V: lane (r, c) reads kVBytes at kVBytes r (+ 8 kVBytes i) of the rows
-  // 2c, 2c + 1, 2c + 8, 2c + 9
-  static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8;
+  static constexpr bool k4 = kPg == kI4 || kPg == kN4;
+  static constexpr int kRowBytes = k4 ? kD / 2 : kPg == kF8 ? kD : 2 * kD;  // codes
+  static constexpr int kPageBytes = kPg == kI4   ? PA_PAGE_BYTES(PA_INT4, kD)
+                                    : kPg == kN4 ? PA_PAGE_BYTES(PA_NVFP4, kD)
+                                                 : kBS * kRowBytes;
+  // K: lane (r, c) reads kKBytes at kKBytes c + 4 kKBytes i of rows r and r + 8
+  static constexpr int kKBytes = kRowBytes >= 64 ? 16 : kRowBytes / 4;
+  static constexpr int kKChunks = kRowBytes / (4 * kKBytes);
+  // V: lane (r, c) reads kVBytes at kVBytes r + 8 kVBytes i of the rows 2c, 2c +
+  // 1, 2c + 8, 2c + 9
+  static constexpr int kVBytes = kRowBytes >= 128 ? 16 : kRowBytes / 8;
   static constexpr int kVChunks = kRowBytes / (8 * kVBytes);
   static constexpr int kTiles = kD / 16;  // m16 tiles of the output's channels
-  // Pages of one step: 8 KB of K and V in a warp's registers, whatever the
-  // type, are on their way while the step before is computed (one page of
-  // 8-bit types leaves half the bytes in flight: 57 instead of PLACEHOLDER us for 32 tokens'
-  // 256 blocks of 8 KV heads).
-  static constexpr int kPages = 4096 / (kBS * kRowBytes);
+  // channels of a lane's K chunk
+  static constexpr int kKChannels = kD / (4 * kKChunks);
+  // The products' types: Q K in the 16-bit type of the pages, in f16 over the
+  // others; P V as well, over INT4 pages in bf16 (their scales are in P).
+  static constexpr bool kQkBF = kPg == kB16;
+  static constexpr bool kPvBF = kPg == kB16 || kPg == kI4;
+  // NVFP4 values are decoded 2^-7 of their size, so that code and scale stay
+  // within f16 on the way
+  static constexpr float kUnit = kPg == kN4 ? 128.f : 1.f;
+  // Pages of one step: up to 8 KB of K and V in a warp's registers, whatever
+  // the type, are on their way while the step before is computed (4-bit pages,
+  // bound by their decoding: two).
+  static constexpr int kPages = k4 ? 2 : 4096 / (kBS * kRowBytes);
 };
+
+// kBytes (4, 8 or 16) as words
+template <int kBytes>
+__device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* src) {
+  if constexpr (kBytes == 16) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (kBytes == 8) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  }
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Nibble k of each 16-bit half of x, an INT4 code, as a pair: in f16 from 1024 +
+// (code + 8), in bf16 from 128 + (code + 8), both exact.
+template <bool kBF, int k>
+__device__ __forceinline__ uint32_t int4_pair(uint32_t x) {
+  const uint32_t u = ((x >> (4 * k)) & 0x000F000Fu) ^ (kBF ? 0x43084308u : 0x64086408u);
+  uint32_t d;
+  if constexpr (kBF)
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(u), "r"(0x43084308u));
+  else
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(u), "r"(0x64086408u));
+  return d;
+}
+
+// Nibble k of each half, an E2M1 code, as an f16 pair 2^-14 of its size: sign,
+// two exponent bits and the mantissa bit where f16 has its own lowest ones.
+template <int k>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t x) {
+  const uint32_t sign = k == 3 ? x : x << (12 - 4 * k);
+  const uint32_t mag = k == 3 ? x >> 3 : x << (k == 3 ? 0 : 9 - 4 * k);
+  return (sign & 0x80008000u) | (mag & 0x0E000E00u);
+}
+
+// 128 times the values of two E4M3 bytes, as f16; at most 57344
+__device__ __forceinline__ uint32_t e4m3_pair_128(uint32_t bytes) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(d)
+      : "r"(bytes));
+  return mul_f16x2(d, 0x58005800u);
+}
 
 // CTAs per SM that the kernels are built for: what the accumulators of 8 (kNT
 // = 1) or 16 query heads leave of the registers
@@ -326,8 +365,8 @@ template <typename TQ, int kPg, int kD, int kNT>
 __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, int begin,
                                             int end, int slot) {
   using Tr = PageTraits<kPg, kD>;
-  constexpr bool kBF = kPg == kB16;
-  constexpr int kRows = 8 * kNT;  // query heads, at most
+  constexpr bool kScaled = Tr::k4;  // pages with scales of their own
+  constexpr int kRows = 8 * kNT;    // query heads, at most
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int part = blockIdx.y;
@@ -346,13 +385,17 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
   }
 
   constexpr int kP = Tr::kPages;
-  uint4 kr[kP][2][Tr::kKChunks];
-  uint32_t vr[kP][4][Tr::kVChunks][Tr::kVBytes / 4];
-  constexpr int64_t kPageBytes = kBS * (int64_t)Tr::kRowBytes;
+  constexpr int kKW = Tr::kKBytes / 4, kVW = Tr::kVBytes / 4;
+  uint32_t kr[kP][2][Tr::kKChunks][kKW];
+  uint32_t vr[kP][4][Tr::kVChunks][kVW];
+  // 4-bit pages: INT4, the scales of keys r and r + 8 (fp32); NVFP4, E4M3 scales
+  // of K rows r and r + 8 (the lane's blocks) and of the four V rows (its block)
+  uint32_t ks[kP][2], vs[kP][kPg == kN4 ? 4 : 2];
+  constexpr int64_t kPageBytes = Tr::kPageBytes;
   const uint8_t* kbase = static_cast<const uint8_t*>(p.k_cache) + (int64_t)u.h * kPageBytes;
   const uint8_t* vbase = static_cast<const uint8_t*>(p.v_cache) + (int64_t)u.h * kPageBytes;
   const int64_t block_bytes = kPageBytes * p.num_kv_heads;
-  const int koff = r * Tr::kRowBytes + c * 16;
+  constexpr int kScales = kBS * Tr::kRowBytes;  // where they begin
 
   // keys of a page up to the token's position
   auto page_keys = [&](const Entry& e) {
@@ -364,34 +407,41 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
   auto load_k = [&](const Entry (&en)[kP]) {
 #pragma unroll
     for (int g = 0; g < kP; ++g) {
-      const uint8_t* src = kbase + (int64_t)max(en[g].phys, 0) * block_bytes + koff;
+      const uint8_t* page = kbase + (int64_t)max(en[g].phys, 0) * block_bytes;
 #pragma unroll
-      for (int i = 0; i < Tr::kKChunks; ++i) {
-        kr[g][0][i] = __ldg(reinterpret_cast<const uint4*>(src + 64 * i));
-        kr[g][1][i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * Tr::kRowBytes + 64 * i));
+      for (int i = 0; i < Tr::kKChunks; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          load_words<Tr::kKBytes>(kr[g][j][i], page + (r + 8 * j) * Tr::kRowBytes +
+                                                   (c + 4 * i) * Tr::kKBytes);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (kPg == kI4)
+          ks[g][j] = __ldg(reinterpret_cast<const uint32_t*>(page + kScales) + r + 8 * j);
+        else if constexpr (kPg == kN4 && kD == 128)
+          ks[g][j] = __ldg(reinterpret_cast<const uint16_t*>(page + kScales) + (r + 8 * j) * 4 + c);
+        else if constexpr (kPg == kN4)
+          ks[g][j] = __ldg(page + kScales + (r + 8 * j) * 4 + c);
       }
     }
   };
   auto load_v = [&](const Entry (&en)[kP]) {
 #pragma unroll
     for (int g = 0; g < kP; ++g) {
-      const uint8_t* src = vbase + (int64_t)max(en[g].phys, 0) * block_bytes +
-                           2 * c * Tr::kRowBytes + r * Tr::kVBytes;
+      const uint8_t* page = vbase + (int64_t)max(en[g].phys, 0) * block_bytes;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const int key = 2 * c + (j & 1) + 8 * (j >> 1);
 #pragma unroll
-        for (int i = 0; i < Tr::kVChunks; ++i) {
-          const uint8_t* at =
-              src + ((j & 1) + 8 * (j >> 1)) * Tr::kRowBytes + i * 8 * Tr::kVBytes;
-          if constexpr (Tr::kVBytes == 16) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
-            vr[g][j][i][0] = v.x; vr[g][j][i][1] = v.y;
-            vr[g][j][i][2] = v.z; vr[g][j][i][3] = v.w;
-          } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-            vr[g][j][i][0] = v.x; vr[g][j][i][1] = v.y;
-          }
-        }
+        for (int i = 0; i < Tr::kVChunks; ++i)
+          load_words<Tr::kVBytes>(vr[g][j][i],
+                                  page + key * Tr::kRowBytes + (r + 8 * i) * Tr::kVBytes);
+        if constexpr (kPg == kN4)
+          vs[g][j] = __ldg(page + kScales + key * (kD / 16) + (kD == 128 ? r : r / 2));
+      }
+      if constexpr (kPg == kI4) {
+        vs[g][0] = __ldg(reinterpret_cast<const uint32_t*>(page + kScales) + r);
+        vs[g][1] = __ldg(reinterpret_cast<const uint32_t*>(page + kScales) + r + 8);
       }
     }
   };
@@ -421,13 +471,14 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
     load_v(cur);
   }
 
-  // Q operand words, in the channel order of the lane's K words.  Over FP8
-  // pages the products are in f16: a power of two brings the unit's largest
-  // query into f16's range, and leaves through the score's scale.
-  uint32_t qw[kNT][Tr::kKChunks][kPg == kF8 ? 8 : 4];
-  float score_scale = p.scale * p.k_scale * kLog2e;
+  // Q operand words, in the channel order of the lane's K words: neighbours,
+  // over INT4 pages the channels 4 apart that a mask leaves in one word.  Where
+  // the products are in f16 over a narrower page, a power of two brings the
+  // row's largest query into f16's range, and leaves through the score's scale.
+  constexpr int kE = Tr::kKChannels;
+  uint32_t qw[kNT][Tr::kKChunks][kE / 2];
+  float score_scale = p.scale * p.k_scale * (Tr::kUnit * kLog2e);
   {
-    constexpr int kE = 16 / Tr::kEB;  // channels of one chunk
     float x[kNT][Tr::kKChunks][kE];
     float big = 0.f;
 #pragma unroll
@@ -451,7 +502,7 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
     // a scale of either sign, or 0: the score's stays positive
     float down = score_scale > 0.f ? 1.f : score_scale < 0.f ? -1.f : 0.f;
     score_scale = score_scale == 0.f ? 1.f : fabsf(score_scale);
-    if constexpr (kPg == kF8) {
+    if constexpr (kPg == kF8 || kScaled) {
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
       if (big > 16384.f && big < INFINITY) {
@@ -465,8 +516,11 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
 #pragma unroll
       for (int i = 0; i < Tr::kKChunks; ++i)
 #pragma unroll
-        for (int w = 0; w < kE / 2; ++w)
-          qw[nt][i][w] = pack2<kBF>(x[nt][i][2 * w] * down, x[nt][i][2 * w + 1] * down);
+        for (int w = 0; w < kE / 2; ++w) {
+          const int e0 = kPg == kI4 ? 8 * (w / 4) + w % 4 : 2 * w;
+          const int e1 = kPg == kI4 ? e0 + 4 : e0 + 1;
+          qw[nt][i][w] = pack2<Tr::kQkBF>(x[nt][i][e0] * down, x[nt][i][e1] * down);
+        }
   }
 
   for (int i = 0; i < steps; ++i) {
@@ -479,26 +533,69 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
         s[g][nt][0] = s[g][nt][1] = s[g][nt][2] = s[g][nt][3] = 0.f;
 #pragma unroll
       for (int ch = 0; ch < Tr::kKChunks; ++ch) {
-        const uint32_t w0[4] = {kr[g][0][ch].x, kr[g][0][ch].y, kr[g][0][ch].z, kr[g][0][ch].w};
-        const uint32_t w1[4] = {kr[g][1][ch].x, kr[g][1][ch].y, kr[g][1][ch].z, kr[g][1][ch].w};
-        if constexpr (kPg == kF8) {
+        const uint32_t(&w0)[kKW] = kr[g][0][ch];
+        const uint32_t(&w1)[kKW] = kr[g][1][ch];
+        // operand words of a lane's channels, a step's two (per row) at a time
+        auto product = [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int w) {
+          const uint32_t a[4] = {a0, a1, a2, a3};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int nt = 0; nt < kNT; ++nt)
+            mma16816<Tr::kQkBF>(s[g][nt], a, qw[nt][ch][w], qw[nt][ch][w + 1]);
+        };
+        if constexpr (kPg == kB16 || kPg == kH16) {
+#pragma unroll
+          for (int w = 0; w < kKW; w += 2) product(w0[w], w1[w], w0[w + 1], w1[w + 1], w);
+        } else if constexpr (kPg == kF8) {
+#pragma unroll
+          for (int w = 0; w < kKW; ++w) {
             uint32_t a[4];
             e4m3x4_to_f16x2x2(w0[w], a[0], a[2]);
             e4m3x4_to_f16x2x2(w1[w], a[1], a[3]);
+            product(a[0], a[1], a[2], a[3], 2 * w);
+          }
+        } else if constexpr (kPg == kI4) {
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-              mma16816<false>(s[g][nt], a, qw[nt][ch][2 * w], qw[nt][ch][2 * w + 1]);
+          for (int w = 0; w < kKW; ++w) {
+            product(int4_pair<false, 0>(w0[w]), int4_pair<false, 0>(w1[w]),
+                    int4_pair<false, 1>(w0[w]), int4_pair<false, 1>(w1[w]), 4 * w);
+            product(int4_pair<false, 2>(w0[w]), int4_pair<false, 2>(w1[w]),
+                    int4_pair<false, 3>(w0[w]), int4_pair<false, 3>(w1[w]), 4 * w + 2);
           }
         } else {
 #pragma unroll
-          for (int w = 0; w < 4; w += 2) {
-            const uint32_t a[4] = {w0[w], w1[w], w0[w + 1], w1[w + 1]};
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-              mma16816<kBF>(s[g][nt], a, qw[nt][ch][w], qw[nt][ch][w + 1]);
+          for (int w = 0; w < kKW; ++w) {
+            // two words are a block of 16 channels
+            const uint32_t s0 = e4m3_pair_128(((ks[g][0] >> (8 * (w / 2))) & 0xFFu) * 0x0101u);
+            const uint32_t s1 = e4m3_pair_128(((ks[g][1] >> (8 * (w / 2))) & 0xFFu) * 0x0101u);
+            // halves (byte i, byte i + 2) -> neighbours: bytes 0, 1 and 2, 3
+            const uint32_t l0 = __byte_perm(w0[w], 0, 0x4140), h0 = __byte_perm(w0[w], 0, 0x4342);
+            const uint32_t l1 = __byte_perm(w1[w], 0, 0x4140), h1 = __byte_perm(w1[w], 0, 0x4342);
+            // l: byte 0 in the low half, byte 1 in the high one; nibbles 0 and 1
+            // of a half are neighbours
+            auto near = [](uint32_t even, uint32_t odd, bool up) {
+              return __byte_perm(even, odd, up ? 0x7632 : 0x5410);
+            };
+            const uint32_t a0 = e2m1_pair<0>(l0), a1 = e2m1_pair<1>(l0);
+            const uint32_t b0 = e2m1_pair<0>(h0), b1 = e2m1_pair<1>(h0);
+            const uint32_t c0 = e2m1_pair<0>(l1), c1 = e2m1_pair<1>(l1);
+            const uint32_t d0 = e2m1_pair<0>(h1), d1 = e2m1_pair<1>(h1);
+            product(mul_f16x2(near(a0, a1, false), s0), mul_f16x2(near(c0, c1, false), s1),
+                    mul_f16x2(near(a0, a1, true), s0), mul_f16x2(near(c0, c1, true), s1),
+                    4 * w);
+            product(mul_f16x2(near(b0, b1, false), s0), mul_f16x2(near(d0, d1, false), s1),
+                    mul_f16x2(near(b0, b1, true), s0), mul_f16x2(near(d0, d1, true), s1),
+                    4 * w + 2);
           }
+        }
+      }
+      if constexpr (kPg == kI4) {  // the keys' own scales
+        const float s0 = __uint_as_float(ks[g][0]), s1 = __uint_as_float(ks[g][1]);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          s[g][nt][0] *= s0;
+          s[g][nt][1] *= s0;
+          s[g][nt][2] *= s1;
+          s[g][nt][3] *= s1;
         }
       }
     }
@@ -526,11 +623,16 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
 #pragma unroll
             for (int ch = 0; ch < Tr::kVChunks; ++ch)
 #pragma unroll
-              for (int w = 0; w < Tr::kVBytes / 4; ++w) vr[g][j][ch][w] = 0;
+              for (int w = 0; w < kVW; ++w) vr[g][j][ch][w] = 0;
+        if constexpr (kScaled)
+#pragma unroll
+          for (int j = 0; j < (kPg == kN4 ? 4 : 2); ++j)
+            if ((kPg == kN4 ? 2 * c + (j & 1) + 8 * (j >> 1) : r + 8 * j) >= keys[g])
+              vs[g][j] = 0;
       }
     }
     // softmax over the step's keys; m: the largest score times score_scale (> 0)
-    uint32_t pb[kP][kNT][2];
+    uint32_t pb[kP][kNT][2], pl[kP][kNT][2];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
       float mx[2];
@@ -569,9 +671,24 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
         const float p3 = exp2_fast(fmaf(s[g][nt][3], score_scale, m1));
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
-        // keys as rows -> heads as rows: the second product's operand
-        pb[g][nt][0] = transpose8x8(pack2<kBF>(p0, p1));
-        pb[g][nt][1] = transpose8x8(pack2<kBF>(p2, p3));
+        // keys as rows -> heads as rows: the second product's operand.  Over
+        // INT4 pages the values' scales go into P, which is then the sum of two
+        // bf16 numbers: their range, and more than f16's precision.
+        if constexpr (kPg == kI4) {
+          const float s0 = __uint_as_float(vs[g][0]), s1 = __uint_as_float(vs[g][1]);
+          const float x[4] = {p0 * s0, p1 * s0, p2 * s1, p3 * s1};
+          float y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = x[j] - __bfloat162float(__float2bfloat16_rn(x[j]));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            pb[g][nt][j] = transpose8x8(pack2<true>(x[2 * j], x[2 * j + 1]));
+            pl[g][nt][j] = transpose8x8(pack2<true>(y[2 * j], y[2 * j + 1]));
+          }
+        } else {
+          pb[g][nt][0] = transpose8x8(pack2<Tr::kPvBF>(p0, p1));
+          pb[g][nt][1] = transpose8x8(pack2<Tr::kPvBF>(p2, p3));
+        }
       }
     }
     // O^T += V^T P^T: channels as rows
@@ -580,32 +697,60 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
 #pragma unroll
       for (int ch = 0; ch < Tr::kVChunks; ++ch)
 #pragma unroll
-        for (int w = 0; w < Tr::kVBytes / 4; ++w) {
+        for (int w = 0; w < kVW; ++w) {
           const uint32_t a0 = vr[g][0][ch][w], a1 = vr[g][1][ch][w];
           const uint32_t a2 = vr[g][2][ch][w], a3 = vr[g][3][ch][w];
-          if constexpr (kPg == kF8) {
-            // four channels of two keys: bytes of the two rows side by side
-            const uint32_t l01 = __byte_perm(a0, a1, 0x5140), h01 = __byte_perm(a0, a1, 0x7362);
-            const uint32_t l23 = __byte_perm(a2, a3, 0x5140), h23 = __byte_perm(a2, a3, 0x7362);
-            uint32_t x[4], y[4];
-            e4m3x4_to_f16x2x2(l01, x[0], x[1]);
-            e4m3x4_to_f16x2x2(h01, x[2], x[3]);
-            e4m3x4_to_f16x2x2(l23, y[0], y[1]);
-            e4m3x4_to_f16x2x2(h23, y[2], y[3]);
+          // tile tl of the lane's channels 2 tl, 2 tl + 1: keys 2c, 2c + 1 of
+          // each, then keys 2c + 8, 2c + 9
+          auto product = [&](int tl, uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1) {
+            const uint32_t a[4] = {x0, x1, y0, y1};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t a[4] = {x[2 * k], x[2 * k + 1], y[2 * k], y[2 * k + 1]};
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt)
-                mma16816<false>(acc[nt][(ch * (Tr::kVBytes / 4) + w) * 2 + k], a,
-                                pb[g][nt][0], pb[g][nt][1]);
+            for (int nt = 0; nt < kNT; ++nt) {
+              mma16816<Tr::kPvBF>(acc[nt][tl], a, pb[g][nt][0], pb[g][nt][1]);
+              if constexpr (kPg == kI4)
+                mma16816<true>(acc[nt][tl], a, pl[g][nt][0], pl[g][nt][1]);
             }
+          };
+          if constexpr (kPg == kB16 || kPg == kH16) {
+            product(ch * kVW + w, __byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632),
+                    __byte_perm(a2, a3, 0x5410), __byte_perm(a2, a3, 0x7632));
+          } else if constexpr (kPg == kF8) {
+            // four channels of two keys: bytes of the two rows side by side
+            uint32_t x[4], y[4];
+            e4m3x4_to_f16x2x2(__byte_perm(a0, a1, 0x5140), x[0], x[1]);
+            e4m3x4_to_f16x2x2(__byte_perm(a0, a1, 0x7362), x[2], x[3]);
+            e4m3x4_to_f16x2x2(__byte_perm(a2, a3, 0x5140), y[0], y[1]);
+            e4m3x4_to_f16x2x2(__byte_perm(a2, a3, 0x7362), y[2], y[3]);
+            product((ch * kVW + w) * 2, x[0], x[1], y[0], y[1]);
+            product((ch * kVW + w) * 2 + 1, x[2], x[3], y[2], y[3]);
           } else {
-            const uint32_t a[4] = {__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632),
-                                   __byte_perm(a2, a3, 0x5410), __byte_perm(a2, a3, 0x7632)};
+            // eight channels of two keys: the rows' halves side by side, nibble k
+            // of both a pair
+            const uint32_t x[2] = {__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632)};
+            const uint32_t y[2] = {__byte_perm(a2, a3, 0x5410), __byte_perm(a2, a3, 0x7632)};
+            if constexpr (kPg == kI4) {
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-              mma16816<kBF>(acc[nt][ch * (Tr::kVBytes / 4) + w], a, pb[g][nt][0], pb[g][nt][1]);
+              for (int k = 0; k < 2; ++k) {
+                product((ch * kVW + w) * 4 + 2 * k, int4_pair<true, 0>(x[k]),
+                        int4_pair<true, 1>(x[k]), int4_pair<true, 0>(y[k]),
+                        int4_pair<true, 1>(y[k]));
+                product((ch * kVW + w) * 4 + 2 * k + 1, int4_pair<true, 2>(x[k]),
+                        int4_pair<true, 3>(x[k]), int4_pair<true, 2>(y[k]),
+                        int4_pair<true, 3>(y[k]));
+              }
+            } else {
+              const uint32_t s0 = e4m3_pair_128(vs[g][0] | vs[g][1] << 8);
+              const uint32_t s1 = e4m3_pair_128(vs[g][2] | vs[g][3] << 8);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                product((ch * kVW + w) * 4 + 2 * k, mul_f16x2(e2m1_pair<0>(x[k]), s0),
+                        mul_f16x2(e2m1_pair<1>(x[k]), s0), mul_f16x2(e2m1_pair<0>(y[k]), s1),
+                        mul_f16x2(e2m1_pair<1>(y[k]), s1));
+                product((ch * kVW + w) * 4 + 2 * k + 1, mul_f16x2(e2m1_pair<2>(x[k]), s0),
+                        mul_f16x2(e2m1_pair<3>(x[k]), s0), mul_f16x2(e2m1_pair<2>(y[k]), s1),
+                        mul_f16x2(e2m1_pair<3>(y[k]), s1));
+              }
+            }
           }
         }
     if (i + 1 < steps) load_v(cur);
@@ -648,6 +793,7 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
       a += f * s_acc[w][hd][d];
       ls += f * s_l[w][hd];
     }
+    a *= Tr::kUnit;
     if (slot < 0) {
       static_cast<TQ*>(p.out)[(u.t * p.num_q_heads + head0 + hd) * kD + d] =
           from_f32<TQ>(ls == 0.f ? 0.f : a / ls * p.v_scale);
@@ -739,14 +885,13 @@ cudaError_t launched() {
   return e;
 }
 
-template <typename TQ, typename TP>
-cudaError_t launch_generic(const SelParams& p, int head_dim, cudaStream_t stream) {
+cudaError_t launch_f32(const SelParams& p, int head_dim, cudaStream_t stream) {
   const int64_t grid = p.s.num_tokens * p.num_q_heads;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   if (head_dim == 128)
-    selected_generic_kernel<TQ, TP, 128><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+    selected_f32_kernel<128><<<(unsigned)grid, kThreads, 0, stream>>>(p);
   else
-    selected_generic_kernel<TQ, TP, 64><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+    selected_f32_kernel<64><<<(unsigned)grid, kThreads, 0, stream>>>(p);
   return launched();
 }
 
@@ -825,19 +970,18 @@ cudaError_t launch_attention_selected(const StepView& s, const SelectedPlan& pla
   p.cut = reinterpret_cast<int2*>(ws + plan.off_cut);
   const bool bf = a.q_dtype == PA_BF16;
   switch (a.cache_dtype) {
-    case PA_F32: return launch_generic<float, F32Page>(p, a.head_dim, stream);
+    case PA_F32: return launch_f32(p, a.head_dim, stream);
     case PA_F16: return launch_mma<__half, kH16>(p, a.head_dim, plan, stream);
-    case PA_BF16:
-      return launch_mma<__nv_bfloat16, kB16>(p, a.head_dim, plan, stream);
+    case PA_BF16: return launch_mma<__nv_bfloat16, kB16>(p, a.head_dim, plan, stream);
     case PA_FP8_E4M3:
       return bf ? launch_mma<__nv_bfloat16, kF8>(p, a.head_dim, plan, stream)
                 : launch_mma<__half, kF8>(p, a.head_dim, plan, stream);
     case PA_INT4:
-      return bf ? launch_generic<__nv_bfloat16, Int4Page>(p, a.head_dim, stream)
-                : launch_generic<__half, Int4Page>(p, a.head_dim, stream);
+      return bf ? launch_mma<__nv_bfloat16, kI4>(p, a.head_dim, plan, stream)
+                : launch_mma<__half, kI4>(p, a.head_dim, plan, stream);
     case PA_NVFP4:
-      return bf ? launch_generic<__nv_bfloat16, Nvfp4Page>(p, a.head_dim, stream)
-                : launch_generic<__half, Nvfp4Page>(p, a.head_dim, stream);
+      return bf ? launch_mma<__nv_bfloat16, kN4>(p, a.head_dim, plan, stream)
+                : launch_mma<__half, kN4>(p, a.head_dim, plan, stream);
   }
   return cudaErrorInvalidValue;
 }
