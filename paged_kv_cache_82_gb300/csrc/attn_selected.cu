@@ -4,9 +4,10 @@
 //   out = sum_j softmax(scale <q, k_j>)_j v_j  over the keys j of the listed
 //   blocks up to the token's own position; a list of no blocks gives zeros.
 //
-// A row is one (token, KV head) with its list; all rows' list entries in a row,
-// end to end, are cut into equal shares, one CTA each, as many as are resident
-// (every CTA sums the rows' list lengths for itself).  A share holds whole
+// A row is one (token, KV head) with its list; all rows' list entries, end to
+// end and with a few units for each row's start, are cut into equal shares, one
+// CTA each, as many as are resident (every CTA sums the rows' list lengths for
+// itself).  A share holds whole
 // lists and, at its ends, parts of lists; a second kernel joins those, part by
 // part in order.  So a few long lists and many short ones both keep every SM
 // busy to the end.
@@ -32,10 +33,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kJoinThreads = 256;  // 8 heads x 128 channels, four per thread
-#ifndef PA_SEL_SHARE
-#define PA_SEL_SHARE 8
-#endif
-constexpr int kMinShare = PA_SEL_SHARE;  // list entries of a CTA, at least
+// A share's units: a row's list entries, and kRowCost for what a CTA needs to
+// begin a row (its lookups and the first pages' latency, about 4 us: as long as
+// 8 pages of its 4 warps take).  56 rows of 1 to 57 blocks: 9.6 us, without it 28
+// (short rows strung together).  Shares have kMinShare units at least, two pages
+// per warp: one row's 128 blocks 11 to 12 us with 8 or 16, 14 with 4 or 32.
+constexpr int kRowCost = 8;
+constexpr int kMinShare = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum : int { kB16 = 0, kH16, kF8, kI4, kN4 };  // bf16, f16, E4M3, INT4, NVFP4 pages
@@ -52,10 +56,11 @@ struct SelParams {
   int max_selected;
   float scale, k_scale, v_scale;
   void* out;
-  // parts of lists, two per CTA: its first and its last (see write_part)
+  // parts of lists, two per CTA: 0 of a list that began in a CTA before, 1 of
+  // one that begins here and goes on
   float* part;     // [CTA][2][head_rows][D]
   float* part_ml;  // [CTA][2][head_rows][2]: m, l
-  int2* cut;       // [CTA]: the row whose list begins here and is cut (-1: none)
+  int2* cut;       // [CTA]: the row whose list goes on (-1: none), its parts
 };
 
 // A row: its token, request, position and list length (-1: the token belongs
@@ -216,9 +221,10 @@ struct PageTraits {
   // NVFP4 values are decoded 2^-7 of their size, so that code and scale stay
   // within f16 on the way
   static constexpr float kUnit = kPg == kN4 ? 128.f : 1.f;
-  // Pages of one step: up to 8 KB of K and V in a warp's registers, whatever
-  // the type, are on their way while the step before is computed (4-bit pages,
-  // bound by their decoding: two).
+  // Pages of one step: 8 KB of K and V in a warp's registers, whatever the
+  // type, are on their way while the step before is computed (4-bit pages,
+  // bound by their decoding: two).  FP8, 32 tokens x 8 heads x 256 blocks: 57 us
+  // with two pages, 76 with one.
   static constexpr int kPages = k4 ? 2 : 4096 / (kBS * kRowBytes);
 };
 
@@ -283,24 +289,28 @@ __device__ __forceinline__ int list_length(const SelParams& p, int64_t row) {
   return c > 0 && c <= p.max_selected ? c : 0;
 }
 
-// A CTA's share of all the rows' list entries.
+// A CTA's share of all the rows' units (a row's kRowCost come first).
 struct Share {
-  int64_t begin, end;  // entries
+  int64_t begin, end;
   int64_t size;        // of every share
   int64_t row;         // the row that `begin` lies in,
-  int64_t row_begin;   // and where its list begins
+  int64_t row_begin;   // and where its entries begin
 };
 
 __device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // Every thread sums a contiguous part of the rows; the one whose part holds
-// the share's first entry walks it.
+// the share's first unit walks it.
 __device__ __forceinline__ Share find_share(const SelParams& p, int64_t rows) {
   __shared__ int64_t warp_sums[32], total, s_row, s_row_begin;
   const int64_t part = (rows + kThreads - 1) / kThreads;
   const int64_t lo = least(rows, threadIdx.x * part), hi = least(rows, lo + part);
+  auto units = [&](int64_t row) {
+    const int n = list_length(p, row);
+    return n > 0 ? n + kRowCost : 0;
+  };
   int64_t sum = 0;
-  for (int64_t i = lo; i < hi; ++i) sum += list_length(p, i);
+  for (int64_t i = lo; i < hi; ++i) sum += units(i);
   const int64_t before = block_scan_excl(sum, &total, warp_sums);
   Share s;
   s.size = (total + gridDim.x - 1) / gridDim.x;
@@ -309,9 +319,9 @@ __device__ __forceinline__ Share find_share(const SelParams& p, int64_t rows) {
   s.end = least(total, s.begin + s.size);
   if (s.begin < s.end && s.begin >= before && s.begin < before + sum) {
     int64_t at = before, i = lo;
-    for (int c; at + (c = list_length(p, i)) <= s.begin; ++i) at += c;
+    for (int c; at + (c = units(i)) <= s.begin; ++i) at += c;
     s_row = i;
-    s_row_begin = at;
+    s_row_begin = at + kRowCost;
   }
   __syncthreads();
   s.row = s_row;
@@ -334,27 +344,28 @@ selected_kernel(const SelParams p) {
   const Share sh = find_share(p, rows);
   const int cta = blockIdx.y * gridDim.x + blockIdx.x;
   int2 cut = make_int2(-1, 0);
-  int64_t at = sh.begin, row = sh.row, row_begin = sh.row_begin;
-  while (at < sh.end) {
-    const int64_t row_end = row_begin + list_length(p, row);
-    if (row_end > at) {
+  int64_t row = sh.row, row_begin = sh.row_begin;
+  if (sh.begin < sh.end) {
+    while (row_begin < sh.end) {
+      const int64_t row_end = row_begin + list_length(p, row);
+      const int64_t begin = row_begin < sh.begin ? sh.begin : row_begin;
       const int64_t end = least(row_end, sh.end);
       const Unit u = find_unit(p, row, threadIdx.x == 0);
-      // -1: the whole list is here; else the CTA's place for a part: 0 for its
-      // first entry's row, 1 for the row that goes on in the next CTA
-      const int slot = at == row_begin && end == row_end ? -1 : at == sh.begin ? 0 : 1;
       if (u.count > 0) {
-        attend_part<TQ, kPg, kD, kNT>(p, u, (int)(at - row_begin), (int)(end - row_begin),
-                                      slot);
-        if (at == row_begin && end < row_end)
-          // parts x 2 + the place of the first
-          cut = make_int2((int)row,
-                          (int)((row_end - 1) / sh.size - blockIdx.x + 1) * 2 + slot);
+        // -1: the whole list is here; else the CTA's place for a part
+        const int slot = begin == row_begin && end == row_end ? -1 : begin > row_begin ? 0 : 1;
+        attend_part<TQ, kPg, kD, kNT>(p, u, (int)(begin - row_begin),
+                                      (int)(end - row_begin), slot);
+        if (slot == 1)
+          cut = make_int2((int)row, (int)((row_end - 1) / sh.size - blockIdx.x + 1));
       }
-      at = end;
+      // the next row with a list
+      do {
+        if (++row >= rows) break;
+      } while (list_length(p, row) == 0);
+      if (row >= rows) break;
+      row_begin = row_end + kRowCost;
     }
-    row_begin = row_end;
-    ++row;
   }
   if (threadIdx.x == 0) p.cut[cta] = cut;
 }
@@ -833,10 +844,10 @@ __global__ void __launch_bounds__(kJoinThreads) selected_join_kernel(const SelPa
   const int64_t t = cut.x / p.num_kv_heads;
   const int h = (int)(cut.x - t * p.num_kv_heads);
   const int heads = min(p.group - part * p.head_rows, p.head_rows);
-  // the list's parts: place 0 or 1 of this share, place 0 of the next ones
-  const int parts = cut.y / 2;
+  // the list's parts: place 1 of this share, place 0 of the next ones
+  const int parts = cut.y;
   auto place = [&](int k) {
-    return (2 * (int64_t)(cta + k) + (k == 0 ? cut.y % 2 : 0)) * p.head_rows;
+    return (2 * (int64_t)(cta + k) + (k == 0 ? 1 : 0)) * p.head_rows;
   };
   // four channels per thread; the parts' loads go out together, four at a time
   constexpr int kQuads = kD / 4, kBatch = 4;
@@ -933,11 +944,11 @@ SelectedPlan make_selected_plan(int64_t num_tokens, int num_q_heads, int num_kv_
   const int group = num_q_heads / num_kv_heads;
   pl.head_rows = group <= 8 ? 8 : 16;
   pl.head_parts = (group + pl.head_rows - 1) / pl.head_rows;
-  // a share per resident CTA, fewer where shares would be below kMinShare
-  const int64_t entries = num_tokens * num_kv_heads * (int64_t)max_selected;
+  // a share per resident CTA, fewer where the shares would be below kMinShare
+  const int64_t units = num_tokens * num_kv_heads * ((int64_t)max_selected + kRowCost);
   const int64_t slots = (int64_t)ctas_per_sm(pl.head_rows) * num_sms;
   pl.shares = std::min(std::max<int64_t>(1, slots / pl.head_parts),
-                       (entries + kMinShare - 1) / kMinShare);
+                       (units + kMinShare - 1) / kMinShare);
   const int64_t parts = 2 * pl.shares * pl.head_parts * pl.head_rows;
   pl.off_ml = parts * head_dim * (int64_t)sizeof(float);
   pl.off_cut = pl.off_ml + parts * 2 * (int64_t)sizeof(float);
