@@ -24,8 +24,7 @@
 // (then V) loads go out as soon as the MMAs have consumed the registers.
 #include <algorithm>
 
-#include "pa_common.cuh"
-#include "pa_internal.h"
+#include "pa_step.cuh"
 
 namespace pa {
 namespace {

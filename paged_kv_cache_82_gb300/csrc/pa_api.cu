@@ -6,6 +6,7 @@
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "pa_step.h"
 
 namespace pa {
 

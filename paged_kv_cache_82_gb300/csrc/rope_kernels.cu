@@ -17,8 +17,7 @@
 // shuffles.
 #include <type_traits>
 
-#include "pa_common.cuh"
-#include "pa_internal.h"
+#include "pa_step.cuh"
 
 namespace pa {
 namespace {

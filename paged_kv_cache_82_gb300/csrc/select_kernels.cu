@@ -16,8 +16,7 @@
 
 #include <algorithm>
 
-#include "pa_common.cuh"
-#include "pa_internal.h"
+#include "pa_step.cuh"
 
 namespace pa {
 namespace {

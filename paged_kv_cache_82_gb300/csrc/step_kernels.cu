@@ -15,8 +15,7 @@
 // new table entries, so no second kernel waits for the sums.
 #include <cooperative_groups.h>
 
-#include "pa_common.cuh"
-#include "pa_internal.h"
+#include "pa_step.cuh"
 
 namespace cg = cooperative_groups;
 
