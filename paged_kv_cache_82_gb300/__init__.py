@@ -183,18 +183,19 @@ def _load():
     return _lib if _lib is not None else load_library()
 
 
+_TYPE_CODES = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
+               torch.uint8: PA_FP8_E4M3}
+if hasattr(torch, "float8_e4m3fn"):
+    _TYPE_CODES[torch.float8_e4m3fn] = PA_FP8_E4M3
+
+
 def _dtype_code(t: torch.Tensor, override: Optional[str] = None) -> int:
     if override is not None:
         return _DT[override]
-    if t.dtype == torch.float32:
-        return PA_F32
-    if t.dtype == torch.float16:
-        return PA_F16
-    if t.dtype == torch.bfloat16:
-        return PA_BF16
-    if t.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", None)):
-        return PA_FP8_E4M3
-    raise TypeError(f"unsupported tensor dtype {t.dtype}")
+    code = _TYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported tensor dtype {t.dtype}")
+    return code
 
 
 def _dev(t: torch.Tensor, name: str) -> int:
@@ -513,33 +514,33 @@ def pa_attention_noalloc(q: torch.Tensor, k_cache: torch.Tensor,
     return out
 
 
-def _here(names: str, *tensors) -> None:
-    """The tensors (None: absent) are on the current CUDA device, where the
-    library launches; names: theirs, in order."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            break
-    else:
-        if dev == torch.cuda.current_device():
-            return
-    for name, t in zip(names.split(), tensors):
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    for name, t in zip(names.split(), tensors):
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current CUDA device")
-
-
-def _ints(t: torch.Tensor, name: str, n: int, dtype=torch.int32) -> torch.Tensor:
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
-    return t
+def _plain(*specs) -> None:
+    """Check contiguous tensors of a call, (name, tensor, dtype or None: any,
+    elements or None: any) each, None tensors left out: types, sizes, and that
+    all are on the current CUDA device, where the library launches."""
+    dev, off = -2, None
+    for name, t, dtype, n in specs:
+        if t is None:
+            continue
+        if (dtype is not None and t.dtype is not dtype) \
+                or (n is not None and t.numel() != n) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype or ''} tensor"
+                             + (f" of {n} elements" if n is not None else ""))
+        d = t.get_device()
+        if d != dev:
+            if off is None and (d < 0 or dev != -2 or d != torch.cuda.current_device()):
+                off = name, d
+            dev = d
+    if off is not None:
+        raise ValueError(f"{off[0]} must be a CUDA tensor" if off[1] < 0 else
+                         f"{off[0]} must be on the current CUDA device")
 
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+_I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
 
 
 def pa_build_step(query_lens: torch.Tensor, computed_lens: torch.Tensor,
@@ -556,31 +557,30 @@ def pa_build_step(query_lens: torch.Tensor, computed_lens: torch.Tensor,
     int32 [num_tokens], slot_mapping int64 [num_tokens], free_count_out int32
     [1]), allocated where not given; seq_lens may be computed_lens and
     free_count_out may be free_count (updated in place)."""
-    if block_tables.dim() != 2 or block_tables.dtype != torch.int32 \
-            or not block_tables.is_contiguous():
-        raise ValueError("block_tables must be a contiguous int32 [B, M] tensor")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [B, M]")
     B, M = block_tables.shape
     T = int(num_tokens)
-    _ints(query_lens, "query_lens", B)
-    _ints(computed_lens, "computed_lens", B)
-    _ints(free_blocks, "free_blocks", free_blocks.numel())
-    _ints(free_count, "free_count", 1)
     dev = block_tables.device
-
-    def out(t, name, n, dtype=torch.int32):
-        if t is None:
-            return torch.empty(n, dtype=dtype, device=dev)
-        return _ints(t, name, n, dtype)
-    seq_lens = out(seq_lens, "seq_lens", B)
-    query_start_loc = out(query_start_loc, "query_start_loc", B + 1)
-    positions = out(positions, "positions", T)
-    slot_mapping = out(slot_mapping, "slot_mapping", T, torch.int64)
-    free_count_out = out(free_count_out, "free_count_out", 1)
-    _here("query_lens computed_lens block_tables free_blocks free_count "
-          "seq_lens query_start_loc positions slot_mapping "
-          "free_count_out",
-          query_lens, computed_lens, block_tables, free_blocks, free_count,
-          seq_lens, query_start_loc, positions, slot_mapping, free_count_out)
+    if seq_lens is None:
+        seq_lens = torch.empty(B, dtype=_I32, device=dev)
+    if query_start_loc is None:
+        query_start_loc = torch.empty(B + 1, dtype=_I32, device=dev)
+    if positions is None:
+        positions = torch.empty(T, dtype=_I32, device=dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(T, dtype=_I64, device=dev)
+    if free_count_out is None:
+        free_count_out = torch.empty(1, dtype=_I32, device=dev)
+    _plain(("query_lens", query_lens, _I32, B),
+           ("computed_lens", computed_lens, _I32, B),
+           ("block_tables", block_tables, _I32, None),
+           ("free_blocks", free_blocks, _I32, None),
+           ("free_count", free_count, _I32, 1), ("seq_lens", seq_lens, _I32, B),
+           ("query_start_loc", query_start_loc, _I32, B + 1),
+           ("positions", positions, _I32, T),
+           ("slot_mapping", slot_mapping, _I64, T),
+           ("free_count_out", free_count_out, _I32, 1))
     st = _load().pa_build_step(
         query_lens.data_ptr(), computed_lens.data_ptr(), B,
         block_tables.data_ptr(), M, free_blocks.data_ptr(), free_blocks.numel(),
@@ -618,44 +618,36 @@ def pa_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor,
     for t, n in ((q, "q"), (key, "key"), (value, "value")):
         if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
             raise ValueError(f"{n} must have contiguous rows")
-    _ints(slot_mapping, "slot_mapping", T, torch.int64)
     NB, Hc, bs, Dc = _cache_geometry(k_cache, cache_dtype, D)
     if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape \
             or v_cache.dtype != k_cache.dtype:
         raise ValueError("cache shape does not match key/value")
-    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
-        raise ValueError("the caches must be contiguous")
     span = rot = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 \
-                or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous fp32 "
-                             "[max_position, rotary_dim] tensor")
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_position, rotary_dim]")
         span, rot = cos_sin.shape
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _ints(positions, "positions", T)
-    wdt = None
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is None:
-            continue
-        if t.numel() != D or not t.is_contiguous() or (wdt or t.dtype) != t.dtype:
-            raise ValueError(f"{n} must be a contiguous [D] tensor, both of one type")
-        wdt = t.dtype
-    wcode = PA_F32 if wdt is None else _dtype_code(q_weight if q_weight is not None
-                                                   else k_weight)
+    weight = q_weight if q_weight is not None else k_weight
+    wdt = None if weight is None else weight.dtype
     if q_out is None:
         q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
-        raise ValueError("q_out must be a contiguous tensor like q")
-    _here("q key value k_cache v_cache slot_mapping positions cos_sin "
-          "q_weight k_weight q_out",
-          q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
-          q_weight, k_weight, q_out)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must be a tensor like q")
+    _plain(("slot_mapping", slot_mapping, _I64, T),
+           ("positions", positions, _I32, T if rot else None),
+           ("cos_sin", cos_sin, torch.float32, None),
+           ("q_weight", q_weight, wdt, D), ("k_weight", k_weight, wdt, D),
+           ("q_out", q_out, q.dtype, None), ("k_cache", k_cache, None, None),
+           ("v_cache", v_cache, None, None))
+    dev = q_out.get_device()
+    if q.get_device() != dev or key.get_device() != dev or value.get_device() != dev:
+        raise ValueError("q, key and value must be on the current CUDA device")
     st = _load().pa_norm_rope_and_cache(
         q.data_ptr(), key.data_ptr(), value.data_ptr(), _dtype_code(q), T,
         _row_stride(q), _row_stride(key), _row_stride(value), _ptr(q_weight),
-        _ptr(k_weight), wcode, float(eps), _ptr(cos_sin), span, rot,
+        _ptr(k_weight), PA_F32 if weight is None else _dtype_code(weight), float(eps), _ptr(cos_sin), span, rot,
         1 if interleaved else 0, _ptr(positions), q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache, cache_dtype),
         NB, bs, Hq, Hkv, D, slot_mapping.data_ptr(), float(k_scale),
@@ -670,21 +662,18 @@ def _row_stride(t: torch.Tensor) -> int:
 
 
 def _bounds_shape(bounds: torch.Tensor, NB, Hkv: int, D: int) -> int:
-    if bounds.dtype != torch.uint8 or bounds.dim() != 3 or not bounds.is_contiguous() \
-            or tuple(bounds.shape[1:]) != (Hkv, bounds_bytes(D)) \
+    if bounds.dim() != 3 or bounds.shape[1] != Hkv or bounds.shape[2] != 2 * D + 16 \
             or (NB is not None and bounds.shape[0] != NB):
-        raise ValueError("bounds must be a contiguous uint8 [num_blocks, Hkv, "
-                         "bounds_bytes(D)] tensor")
+        raise ValueError("bounds must be a uint8 [num_blocks, Hkv, bounds_bytes(D)] "
+                         "tensor")
     return bounds.shape[0]
 
 
-def _step_ints(block_tables, seq_lens, query_start_loc) -> int:
+def _step_tables(block_tables, seq_lens, query_start_loc) -> int:
     B = seq_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+    if block_tables.dim() != 2 or block_tables.shape[0] != B \
+            or query_start_loc.numel() != B + 1:
         raise ValueError("inconsistent number of sequences")
-    _ints(block_tables, "block_tables", block_tables.numel())
-    _ints(seq_lens, "seq_lens", B)
-    _ints(query_start_loc, "query_start_loc", B + 1)
     return B
 
 
@@ -696,12 +685,12 @@ def pa_summarise_blocks(k_cache: torch.Tensor, bounds: torch.Tensor,
     """Key bounds of the blocks this step's tokens were written to, into bounds
     (uint8 [num_blocks, Hkv, bounds_bytes(D)])."""
     NB, Hkv, bs, D = _cache_geometry(k_cache, cache_dtype)
-    if not k_cache.is_contiguous():
-        raise ValueError("k_cache must be contiguous")
     _bounds_shape(bounds, NB, Hkv, D)
-    B = _step_ints(block_tables, seq_lens, query_start_loc)
-    _here("k_cache bounds block_tables seq_lens query_start_loc",
-          k_cache, bounds, block_tables, seq_lens, query_start_loc)
+    B = _step_tables(block_tables, seq_lens, query_start_loc)
+    _plain(("k_cache", k_cache, None, None), ("bounds", bounds, _U8, None),
+           ("block_tables", block_tables, _I32, None),
+           ("seq_lens", seq_lens, _I32, B),
+           ("query_start_loc", query_start_loc, _I32, None))
     st = _load().pa_summarise_blocks(
         k_cache.data_ptr(), _dtype_code(k_cache, cache_dtype), NB, bs, Hkv, D,
         block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
@@ -729,25 +718,26 @@ def pa_select_blocks(q: torch.Tensor, bounds: torch.Tensor,
                      workspace: Optional[torch.Tensor] = None, stream=None):
     """q [T, Hq, D]; bounds as pa_summarise_blocks leaves them.  Returns
     (selected int32 [T, Hkv, max_selected], num_selected int32 [T, Hkv])."""
-    if q.dim() != 3 or not q.is_contiguous() or bounds.dim() != 3:
-        raise ValueError("q must be a contiguous [T, Hq, D] tensor")
+    if q.dim() != 3 or bounds.dim() != 3:
+        raise ValueError("q must be [T, Hq, D] and bounds [num_blocks, Hkv, bytes]")
     T, Hq, D = q.shape
     Hkv, K = bounds.shape[1], int(max_selected)
     NB = _bounds_shape(bounds, None, Hkv, D)
-    B = _step_ints(block_tables, seq_lens, query_start_loc)
+    B = _step_tables(block_tables, seq_lens, query_start_loc)
     if selected is None:
-        selected = torch.empty(T, Hkv, K, dtype=torch.int32, device=q.device)
+        selected = torch.empty(T, Hkv, K, dtype=_I32, device=q.device)
     if num_selected is None:
-        num_selected = torch.empty(T, Hkv, dtype=torch.int32, device=q.device)
-    _ints(selected, "selected", T * Hkv * K)
-    _ints(num_selected, "num_selected", T * Hkv)
+        num_selected = torch.empty(T, Hkv, dtype=_I32, device=q.device)
     if workspace is None:
         n = pa_select_blocks_workspace_size(T, Hkv, int(max_seq_len))
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-    _here("q bounds block_tables seq_lens query_start_loc selected "
-          "num_selected workspace",
-          q, bounds, block_tables, seq_lens, query_start_loc, selected,
-          num_selected, workspace)
+        workspace = torch.empty(max(n, 1), dtype=_U8, device=q.device)
+    _plain(("q", q, None, None), ("bounds", bounds, _U8, None),
+           ("block_tables", block_tables, _I32, None),
+           ("seq_lens", seq_lens, _I32, B),
+           ("query_start_loc", query_start_loc, _I32, B + 1),
+           ("selected", selected, _I32, T * Hkv * K),
+           ("num_selected", num_selected, _I32, T * Hkv),
+           ("workspace", workspace, None, None))
     st = _load().pa_select_blocks(
         q.data_ptr(), _dtype_code(q), bounds.data_ptr(), NB, BLOCK_SIZE, Hq, Hkv,
         D, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
@@ -782,23 +772,30 @@ def pa_attention_selected(q: torch.Tensor, k_cache: torch.Tensor,
                           stream=None) -> torch.Tensor:
     """pa_attention over the listed blocks only: selected int32 [T, Hkv, K] in
     ascending order per row, num_selected int32 [T, Hkv]."""
-    T, Hq, D, NB, Hkv, bs, B = _step_shapes(q, k_cache, v_cache, block_tables,
-                                            seq_lens, query_start_loc, out,
-                                            cache_dtype)
-    if selected.dim() != 3 or tuple(selected.shape[:2]) != (T, Hkv):
+    if q.dim() != 3 or v_cache.shape != k_cache.shape \
+            or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("q must be [T, Hq, D] and both caches alike")
+    T, Hq, D = q.shape
+    NB, Hkv, bs, Dc = _cache_geometry(k_cache, cache_dtype)
+    if Dc != D:
+        raise ValueError("head_dim of q and of the caches differ")
+    B = _step_tables(block_tables, seq_lens, query_start_loc)
+    if selected.dim() != 3 or selected.shape[0] != T or selected.shape[1] != Hkv:
         raise ValueError("selected must be [T, Hkv, K]")
     K = selected.shape[2]
-    _ints(selected, "selected", T * Hkv * K)
-    _ints(num_selected, "num_selected", T * Hkv)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
         n = pa_attention_selected_workspace_size(T, Hq, Hkv, D, K)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-    _here("q k_cache v_cache block_tables seq_lens query_start_loc "
-          "selected num_selected out workspace",
-          q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
-          selected, num_selected, out, workspace)
+        workspace = torch.empty(max(n, 1), dtype=_U8, device=q.device)
+    _plain(("q", q, None, None), ("k_cache", k_cache, None, None),
+           ("v_cache", v_cache, None, None),
+           ("block_tables", block_tables, _I32, None),
+           ("seq_lens", seq_lens, _I32, B),
+           ("query_start_loc", query_start_loc, _I32, B + 1),
+           ("selected", selected, _I32, None),
+           ("num_selected", num_selected, _I32, T * Hkv),
+           ("out", out, q.dtype, q.numel()), ("workspace", workspace, None, None))
     st = _load().pa_attention_selected(
         q.data_ptr(), _dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(),
         _dtype_code(k_cache, cache_dtype), NB, bs, Hq, Hkv, D,
