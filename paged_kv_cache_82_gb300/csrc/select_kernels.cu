@@ -297,8 +297,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 constexpr uint32_t kKeptKey = 0xFFFFFFFFu;  // above every score's key
 // a score's key; a NaN's (of a record that was never written) is the highest
+// (named: the sign of a NaN's bits may be changed as a number's, which keeps none)
 __device__ __forceinline__ uint32_t score_key(float x) {
-  return min(order_key(x), kKeptKey - 1);
+  return isnan(x) ? kKeptKey - 1 : order_key(x);
 }
 
 struct ScoreParams {
@@ -689,7 +690,8 @@ topk_kernel(const TopkParams p) {
       }
       __syncthreads();
       lo += (uint32_t)s_bin << shift;
-      top = min(top, lo + (uint32_t)((1ull << shift) - 1));
+      // (a difference: with a NaN's key in the range, lo + 2^shift may pass 2^32)
+      top = lo + min(top - lo, (uint32_t)((1ull << shift) - 1));
       need = s_need;
       bits = shift;
       if (s_count == need) break;  // all of the bin

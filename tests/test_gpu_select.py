@@ -214,6 +214,49 @@ def test_odd_queries():
     assert (s.diff(dim=-1) > 0).all() and int(cnt.min()) == 5
 
 
+def _order(x):
+    """fp32 scores as whole numbers of their order, a NaN above all."""
+    u = (x + np.float32(0)).view(np.uint32).astype(np.int64)
+    key = np.where(u >> 31, 0xFFFFFFFF - u, u | 0x80000000)
+    return np.where(np.isnan(x), 0xFFFFFFFE, key)
+
+
+@pytest.mark.parametrize("L", [4800, 40 * 1024, 160 * 1024])
+def test_records_of_any_bytes(L):
+    """Records that were never written: any codes and scales, NaN and infinities
+    among them.  A list is that of the scores all the same, a NaN's above all,
+    and nothing is written past a list's K entries."""
+    n = L // 16
+    rng = np.random.default_rng(n)
+    raw = rng.integers(0, 256, (n, 2, 2 * 64 + 16), dtype=np.uint8)
+    raw[rng.integers(0, n, 3), :, 128:132] = (0, 0, 0xC0, 0x7F)  # NaN
+    raw[rng.integers(0, n, 3), :, 128:132] = (0, 0, 0x80, 0x7F)  # infinite
+    bounds = torch.from_numpy(raw).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = rng.permutation(n).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((1, 4, 64)).astype(np.float32))
+    hi, lo, sc = ref.records(bounds, 64)
+    x = q.numpy()[0].reshape(2, 2, 64)
+    for K in (2, 3, 5, 9, 60, 290):
+        out = torch.full((2 * K + 4096,), -77, **i32)
+        sel, _ = pa.pa_select_blocks(
+            q.cuda(), bounds, torch.from_numpy(table)[None].cuda(), torch.tensor([L], **i32),
+            torch.tensor([0, 1], **i32), 1, L, K, keep_first=1, keep_last=1,
+            selected=out[:2 * K].view(1, 2, K))
+        assert pa.pa_get_device_error() == 0
+        assert (out[2 * K:] == -77).all()
+        for h in range(2):
+            sq = np.float32(np.abs(x[h]).max() / np.float32(127))
+            code = np.rint(x[h] / sq).astype(np.int64)
+            H, Lo = hi[table, h].astype(np.int64), lo[table, h].astype(np.int64)
+            # (a code of -128 may stand in a record as well)
+            dots = (np.maximum(code, 0) @ H.T + np.minimum(code, 0) @ Lo.T).max(0)
+            with np.errstate(all="ignore"):
+                score = _order(dots.astype(np.float32) * sc[table, h])
+            mid = sorted(range(1, n - 1), key=lambda b: (-score[b], b))[:K - 2]
+            assert sel[0, h].tolist() == sorted([0, n - 1] + mid)
+
+
 def test_passes_over_the_step_do_not_change_the_result():
     """A step whose scores exceed the workspace's bound runs in passes."""
     lens = [(16384, 64)] * 4 + [(20000, 1)] * 3
