@@ -41,7 +41,7 @@ constexpr int kRowCost = 8;
 constexpr int kMinShare = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum : int { kB16 = 0, kH16, kF8, kI4, kN4 };  // bf16, f16, E4M3, INT4, NVFP4 pages
+enum : int { kB16 = 0, kH16, kF8, kI4, kN4, kF32 };  // bf16, f16, E4M3, INT4, NVFP4, fp32 pages
 
 struct SelParams {
   StepView s;
@@ -118,70 +118,6 @@ __device__ __forceinline__ Entry list_entry(const SelParams& p, const Unit& u, i
   return e;
 }
 
-// ---------------------------------------------------------------------------
-// fp32 caches, which have no MMA of their precision: four warps per (token,
-// query head), each with a part of the list
-// ---------------------------------------------------------------------------
-template <int kD>
-__global__ void __launch_bounds__(kThreads) selected_f32_kernel(const SelParams p) {
-  constexpr int kPer = kD / 32;
-  __shared__ float s_acc[kWarps][kD], s_m[kWarps], s_l[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x / p.num_q_heads;
-  const int hq = (int)(blockIdx.x % p.num_q_heads);
-  const Unit u = find_unit(p, t * p.num_kv_heads + hq / p.group, threadIdx.x == 0);
-  if (u.count < 0) return;
-  const float* qp = static_cast<const float*>(p.q) + (t * p.num_q_heads + hq) * kD;
-  float qv[kPer], acc[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    qv[k] = qp[lane + 32 * k] * p.scale;
-    acc[k] = 0.f;
-  }
-  for (int i = warp; i < u.count; i += kWarps) {
-    const Entry e = list_entry(p, u, i);
-    if (e.phys < 0) continue;
-    const int64_t page = ((int64_t)e.phys * p.num_kv_heads + u.h) * (kBS * kD);
-    const float* keys_at = static_cast<const float*>(p.k_cache) + page;
-    const float* values_at = static_cast<const float*>(p.v_cache) + page;
-    const int keys = min(kBS, u.pos - e.block * kBS + 1);
-    for (int o = 0; o < keys; ++o) {
-      float dot = 0.f;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        dot += qv[k] * __ldg(keys_at + o * kD + lane + 32 * k);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
-      const float mn = fmaxf(m, dot);
-      if (mn == -INFINITY) continue;  // nothing but -inf so far
-      const float al = expf(m - mn), pj = expf(dot - mn);
-      l = l * al + pj;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        acc[k] = acc[k] * al + pj * __ldg(values_at + o * kD + lane + 32 * k);
-      m = mn;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) s_acc[warp][lane + 32 * k] = acc[k];
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-  __syncthreads();
-  float mx = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w]);
-  for (int d = threadIdx.x; d < kD; d += kThreads) {
-    float a = 0.f, ls = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w] == -INFINITY ? 0.f : expf(s_m[w] - mx);
-      a += f * s_acc[w][d];
-      ls += f * s_l[w];
-    }
-    static_cast<float*>(p.out)[(t * p.num_q_heads + hq) * kD + d] = ls > 0.f ? a / ls : ls;
-  }
-}
-
-// ---------------------------------------------------------------------------
-// the MMA form
-// ---------------------------------------------------------------------------
 // 2^x to 2 units in the last place of fp32; below 2^-126: 0
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -278,9 +214,11 @@ __device__ __forceinline__ uint32_t e4m3_pair_128(uint32_t bytes) {
   return mul_f16x2(d, 0x58005800u);
 }
 
-// CTAs per SM that the kernels are built for: what the accumulators of 8 (kNT
-// = 1) or 16 query heads leave of the registers
-constexpr int ctas_per_sm(int head_rows) { return head_rows == 8 ? 3 : 2; }
+// CTAs per SM that the kernels are built for: what the accumulators of 8 or 16
+// query heads, or a warp's fp32 pages (128 registers), leave of the registers
+constexpr int ctas_per_sm(bool fp32, int head_rows) {
+  return !fp32 && head_rows == 8 ? 3 : 2;
+}
 
 // Entries of a row's list that count: none of a row past the last request.
 __device__ __forceinline__ int list_length(const SelParams& p, int64_t row) {
@@ -328,12 +266,15 @@ __device__ __forceinline__ Share find_share(const SelParams& p, int64_t rows) {
   return s;
 }
 
-template <typename TQ, int kPg, int kD, int kNT>
+template <typename TQ, int kPg, int kD, int kRows>
 __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, int begin,
                                             int end, int slot);
+template <int kD, int kRows>
+__device__ __forceinline__ void attend_part_f32(const SelParams& p, const Unit& u, int begin,
+                                                int end, int slot);
 
-template <typename TQ, int kPg, int kD, int kNT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(8 * kNT))
+template <typename TQ, int kPg, int kD, int kRows>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(kPg == kF32, kRows))
 selected_kernel(const SelParams p) {
   pdl_launch_dependents();
   // rows of tokens up to the last request's
@@ -353,8 +294,11 @@ selected_kernel(const SelParams p) {
       if (u.count > 0) {
         // -1: the whole list is here; else the CTA's place for a part
         const int slot = begin == row_begin && end == row_end ? -1 : begin > row_begin ? 0 : 1;
-        attend_part<TQ, kPg, kD, kNT>(p, u, (int)(begin - row_begin),
-                                      (int)(end - row_begin), slot);
+        const int from = (int)(begin - row_begin), to = (int)(end - row_begin);
+        if constexpr (kPg == kF32)
+          attend_part_f32<kD, kRows>(p, u, from, to, slot);
+        else
+          attend_part<TQ, kPg, kD, kRows>(p, u, from, to, slot);
         if (slot == 1)
           cut = make_int2((int)row, (int)((row_end - 1) / sh.size - blockIdx.x + 1));
       }
@@ -369,14 +313,54 @@ selected_kernel(const SelParams p) {
   if (threadIdx.x == 0) p.cut[cta] = cut;
 }
 
-// Entries begin .. end - 1 of a row's list: to the output if that is all of it
-// (slot < 0), else to the CTA's place for a part.
-template <typename TQ, int kPg, int kD, int kNT>
+// The four warps' results in shared memory -- m, l and the sum of the values
+// for each of the CTA's query heads -- as one: to the output if that is all of
+// the list (slot < 0), else to the CTA's place for a part.
+template <typename TQ, int kRows, int kD>
+__device__ __forceinline__ void finish_part(const SelParams& p, const Unit& u, int slot,
+                                            float unit,
+                                            const float (&s_acc)[kWarps][kRows][kD],
+                                            const float (&s_m)[kWarps][kRows],
+                                            const float (&s_l)[kWarps][kRows]) {
+  const int heads = min(p.group - (int)blockIdx.y * kRows, kRows);
+  const int head0 = u.h * p.group + blockIdx.y * kRows;
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * kD; i += kThreads) {
+    const int hd = i / kD, d = i - hd * kD;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][hd]);
+    float a = 0.f, ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx);
+      a += f * s_acc[w][hd][d];
+      ls += f * s_l[w][hd];
+    }
+    a *= unit;
+    if (slot < 0) {
+      static_cast<TQ*>(p.out)[(u.t * p.num_q_heads + head0 + hd) * kD + d] =
+          from_f32<TQ>(ls == 0.f ? 0.f : a / ls * p.v_scale);
+    } else {
+      const int64_t at =
+          ((int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 2 + slot) * p.head_rows + hd;
+      p.part[at * kD + d] = a;
+      if (d == 0) {
+        p.part_ml[2 * at] = mx;
+        p.part_ml[2 * at + 1] = ls;
+      }
+    }
+  }
+  __syncthreads();  // the next part writes the shared memory again
+}
+
+// Entries begin .. end - 1 of a row's list, by the tensor cores.
+template <typename TQ, int kPg, int kD, int kRows>
 __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, int begin,
                                             int end, int slot) {
   using Tr = PageTraits<kPg, kD>;
   constexpr bool kScaled = Tr::k4;  // pages with scales of their own
-  constexpr int kRows = 8 * kNT;    // query heads, at most
+  constexpr int kNT = kRows / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int part = blockIdx.y;
@@ -790,34 +774,176 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
         }
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < heads * kD; i += kThreads) {
-    const int hd = i / kD, d = i - hd * kD;
-    float mx = -INFINITY;
+  finish_part<TQ, kRows, kD>(p, u, slot, Tr::kUnit, s_acc, s_m, s_l);
+}
+
+// fp32 pages, which no MMA takes in their precision: the same walk over the
+// list, a page's K and V in a warp's registers while the one before is computed,
+// with fp32 FMAs.  kD / 4 lanes hold a key's channels, four each, so the scores
+// of a key are sums over lanes: kL of them (keys x heads) are summed together,
+// each halving of the lanes halving the values too, which takes kL - 1 shuffles
+// and leaves lane l the score of head l % kRows.  About 1400 instructions per
+// page at 8 heads, 350 cycles of an SM; HBM brings an SM one page in 700.
+template <int kD, int kRows>
+__device__ __forceinline__ void attend_part_f32(const SelParams& p, const Unit& u, int begin,
+                                                int end, int slot) {
+  constexpr int kL = kD / 4;           // lanes of a key
+  constexpr int kR = 32 / kL;          // keys of one load
+  constexpr int kN = kBS / kR;         // loads of a page
+  constexpr int kC = kN * kRows / kL;  // scores of a lane
+  constexpr int kCN = kN / kC;         // loads of one sum over lanes
+  __shared__ __align__(16) float s_acc[kWarps][kRows][kD];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ __align__(16) float s_p[kWarps][kBS][kRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % kL, sub = lane / kL;
+  const int part = blockIdx.y;
+  const int heads = min(p.group - part * kRows, kRows);
+  const int head0 = u.h * p.group + part * kRows;
+  const int64_t row = (int64_t)u.h * (kBS * kD);
+  const int64_t block = (int64_t)p.num_kv_heads * (kBS * kD);
+  const float* kbase = static_cast<const float*>(p.k_cache) + row + sub * kD + l * 4;
+  const float* vbase = static_cast<const float*>(p.v_cache) + row + sub * kD + l * 4;
+  float4 kr[kN], vr[kN];
+  // (a skipped entry reads block 0, as over the other types)
+  auto load_k = [&](const Entry& e) {
+    const float* src = kbase + (int64_t)max(e.phys, 0) * block;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][hd]);
-    float a = 0.f, ls = 0.f;
+    for (int n = 0; n < kN; ++n) kr[n] = __ldg(reinterpret_cast<const float4*>(src + n * kR * kD));
+  };
+  auto load_v = [&](const Entry& e) {
+    const float* src = vbase + (int64_t)max(e.phys, 0) * block;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w][hd] == -INFINITY ? 0.f : exp2f(s_m[w][hd] - mx);
-      a += f * s_acc[w][hd][d];
-      ls += f * s_l[w][hd];
+    for (int n = 0; n < kN; ++n) vr[n] = __ldg(reinterpret_cast<const float4*>(src + n * kR * kD));
+  };
+  const int first = begin + warp;
+  const int steps = end > first ? (end - first + kWarps - 1) / kWarps : 0;
+  Entry held{0, -1};
+  auto entry = [&](int i) {
+    if ((i & 31) == 0) {
+      const int at = first + (i + lane) * kWarps;
+      held = Entry{0, -1};
+      if (at < end) held = list_entry(p, u, at);
     }
-    a *= Tr::kUnit;
-    if (slot < 0) {
-      static_cast<TQ*>(p.out)[(u.t * p.num_q_heads + head0 + hd) * kD + d] =
-          from_f32<TQ>(ls == 0.f ? 0.f : a / ls * p.v_scale);
-    } else {
-      const int64_t at =
-          ((int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 2 + slot) * p.head_rows + hd;
-      p.part[at * kD + d] = a;
-      if (d == 0) {
-        p.part_ml[2 * at] = mx;
-        p.part_ml[2 * at + 1] = ls;
-      }
+    return Entry{__shfl_sync(~0u, held.block, i & 31), __shfl_sync(~0u, held.phys, i & 31)};
+  };
+  Entry cur{0, -1};
+  if (steps > 0) {
+    cur = entry(0);
+    load_k(cur);
+    load_v(cur);
+  }
+  float4 q[kRows], acc[kRows];
+  const float scale = p.scale * kLog2e;
+#pragma unroll
+  for (int h = 0; h < kRows; ++h) {
+    acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    q[h] = acc[h];
+    if (h < heads) {
+      q[h] = __ldg(reinterpret_cast<const float4*>(
+          static_cast<const float*>(p.q) + (u.t * p.num_q_heads + head0 + h) * kD + l * 4));
+      q[h] = make_float4(q[h].x * scale, q[h].y * scale, q[h].z * scale, q[h].w * scale);
     }
   }
-  __syncthreads();  // the next part writes the shared memory again
+  // of head lane % kRows; the sum is that of the lane's own scores
+  float m = -INFINITY, sum = 0.f;
+  for (int i = 0; i < steps; ++i) {
+    float s[kC];
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      float d[kL];
+#pragma unroll
+      for (int n = 0; n < kCN; ++n) {
+        const float4 k = kr[j * kCN + n];
+#pragma unroll
+        for (int h = 0; h < kRows; ++h)
+          d[n * kRows + h] =
+              fmaf(k.x, q[h].x, fmaf(k.y, q[h].y, fmaf(k.z, q[h].z, k.w * q[h].w)));
+      }
+#pragma unroll
+      for (int w = kL / 2; w > 0; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int x = 0; x < w; ++x) {
+          const float give = up ? d[x] : d[x + w];
+          const float keep = up ? d[x + w] : d[x];
+          d[x] = keep + __shfl_xor_sync(~0u, give, w);
+        }
+      }
+      s[j] = d[0];
+    }
+    const int keys = cur.phys < 0 ? 0 : min(kBS, u.pos - cur.block * kBS + 1);
+    if (i + 1 < steps) {
+      cur = entry(i + 1);
+      load_k(cur);
+    }
+    // lane's j-th score: key (j kCN + l / kRows) kR + sub
+    if (keys < kBS) {
+#pragma unroll
+      for (int j = 0; j < kC; ++j)
+        if ((j * kCN + l / kRows) * kR + sub >= keys) s[j] = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < kN; ++n)  // no value that could be NaN
+        if (n * kR + sub >= keys) vr[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mx = s[0];
+#pragma unroll
+    for (int j = 1; j < kC; ++j) mx = fmaxf(mx, s[j]);
+#pragma unroll
+    for (int w = kRows; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, w));
+    mx = fmaxf(mx, m);
+    if (__any_sync(~0u, mx > m)) {
+      const float al = mx == -INFINITY ? 1.f : exp2f(m - mx);
+      m = mx;
+      sum *= al;
+#pragma unroll
+      for (int h = 0; h < kRows; ++h) {
+        const float f = __shfl_sync(~0u, al, h);
+        acc[h] = make_float4(acc[h].x * f, acc[h].y * f, acc[h].z * f, acc[h].w * f);
+      }
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      const float e = exp2f(s[j] - base);
+      sum += e;
+      s_p[warp][(j * kCN + l / kRows) * kR + sub][l % kRows] = e;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const float4 v = vr[n];
+#pragma unroll
+      for (int h4 = 0; h4 < kRows; h4 += 4) {
+        const float4 e = *reinterpret_cast<const float4*>(&s_p[warp][n * kR + sub][h4]);
+        const float w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          float4& a = acc[h4 + h];
+          a.x = fmaf(w[h], v.x, a.x);
+          a.y = fmaf(w[h], v.y, a.y);
+          a.z = fmaf(w[h], v.z, a.z);
+          a.w = fmaf(w[h], v.w, a.w);
+        }
+      }
+    }
+    __syncwarp();  // the next page's probabilities
+    if (i + 1 < steps) load_v(cur);
+  }
+#pragma unroll
+  for (int w = kRows; w < 32; w <<= 1) sum += __shfl_xor_sync(~0u, sum, w);
+  if (lane < kRows) s_m[warp][lane] = m, s_l[warp][lane] = sum;
+#pragma unroll
+  for (int h = 0; h < kRows; ++h) {
+    if constexpr (kR == 2) {
+      acc[h].x += __shfl_xor_sync(~0u, acc[h].x, 16);
+      acc[h].y += __shfl_xor_sync(~0u, acc[h].y, 16);
+      acc[h].z += __shfl_xor_sync(~0u, acc[h].z, 16);
+      acc[h].w += __shfl_xor_sync(~0u, acc[h].w, 16);
+    }
+    if (sub == 0) *reinterpret_cast<float4*>(&s_acc[warp][h][l * 4]) = acc[h];
+  }
+  finish_part<float, kRows, kD>(p, u, slot, 1.f, s_acc, s_m, s_l);
 }
 
 // Behind the shares: CTA i joins the list that begins in share i and is cut
@@ -895,23 +1021,14 @@ cudaError_t launched() {
   return e;
 }
 
-cudaError_t launch_f32(const SelParams& p, int head_dim, cudaStream_t stream) {
-  const int64_t grid = p.s.num_tokens * p.num_q_heads;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (head_dim == 128)
-    selected_f32_kernel<128><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-  else
-    selected_f32_kernel<64><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-  return launched();
-}
-
 template <typename TQ, int kPg, int kD>
-cudaError_t launch_mma_d(const SelParams& p, const SelectedPlan& plan, cudaStream_t stream) {
+cudaError_t launch_d(const SelParams& p, const SelectedPlan& plan, cudaStream_t stream) {
   const dim3 grid((unsigned)plan.shares, (unsigned)plan.head_parts);
-  if (p.head_rows == 8)
-    selected_kernel<TQ, kPg, kD, 1><<<grid, kThreads, 0, stream>>>(p);
+  constexpr int kRows = kPg == kF32 ? 4 : 8;  // or twice as many
+  if (p.head_rows == kRows)
+    selected_kernel<TQ, kPg, kD, kRows><<<grid, kThreads, 0, stream>>>(p);
   else
-    selected_kernel<TQ, kPg, kD, 2><<<grid, kThreads, 0, stream>>>(p);
+    selected_kernel<TQ, kPg, kD, 2 * kRows><<<grid, kThreads, 0, stream>>>(p);
   cudaError_t e = launched();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -929,29 +1046,45 @@ cudaError_t launch_mma_d(const SelParams& p, const SelectedPlan& plan, cudaStrea
 }
 
 template <typename TQ, int kPg>
-cudaError_t launch_mma(const SelParams& p, int head_dim, const SelectedPlan& plan,
+cudaError_t launch_t(const SelParams& p, int head_dim, const SelectedPlan& plan,
                        cudaStream_t stream) {
-  return head_dim == 128 ? launch_mma_d<TQ, kPg, 128>(p, plan, stream)
-                         : launch_mma_d<TQ, kPg, 64>(p, plan, stream);
+  return head_dim == 128 ? launch_d<TQ, kPg, 128>(p, plan, stream)
+                         : launch_d<TQ, kPg, 64>(p, plan, stream);
 }
 
 }  // namespace
 
-SelectedPlan make_selected_plan(int64_t num_tokens, int num_q_heads, int num_kv_heads,
-                                int head_dim, int max_selected, int num_sms) {
+namespace {
+
+SelectedPlan plan_for(bool fp32, int64_t num_tokens, int num_q_heads, int num_kv_heads,
+                      int head_dim, int max_selected, int num_sms) {
   SelectedPlan pl{};
   const int group = num_q_heads / num_kv_heads;
-  pl.head_rows = group <= 8 ? 8 : 16;
+  pl.head_rows = fp32 ? (group <= 4 ? 4 : 8) : (group <= 8 ? 8 : 16);
   pl.head_parts = (group + pl.head_rows - 1) / pl.head_rows;
   // a share per resident CTA, fewer where the shares would be below kMinShare
   const int64_t units = num_tokens * num_kv_heads * ((int64_t)max_selected + kRowCost);
-  const int64_t slots = (int64_t)ctas_per_sm(pl.head_rows) * num_sms;
+  const int64_t slots = (int64_t)ctas_per_sm(fp32, pl.head_rows) * num_sms;
   pl.shares = std::min(std::max<int64_t>(1, slots / pl.head_parts),
                        (units + kMinShare - 1) / kMinShare);
   const int64_t parts = 2 * pl.shares * pl.head_parts * pl.head_rows;
   pl.off_ml = parts * head_dim * (int64_t)sizeof(float);
   pl.off_cut = pl.off_ml + parts * 2 * (int64_t)sizeof(float);
   pl.bytes = pl.off_cut + pl.shares * pl.head_parts * (int64_t)sizeof(int2);
+  return pl;
+}
+
+}  // namespace
+
+SelectedPlan make_selected_plan(pa_dtype cache_dtype, int64_t num_tokens, int num_q_heads,
+                                int num_kv_heads, int head_dim, int max_selected,
+                                int num_sms) {
+  const SelectedPlan a = plan_for(false, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                  max_selected, num_sms);
+  const SelectedPlan b =
+      plan_for(true, num_tokens, num_q_heads, num_kv_heads, head_dim, max_selected, num_sms);
+  SelectedPlan pl = cache_dtype == PA_F32 ? b : a;
+  pl.bytes = std::max(a.bytes, b.bytes);  // one size for caches of every type
   return pl;
 }
 
@@ -980,18 +1113,18 @@ cudaError_t launch_attention_selected(const StepView& s, const SelectedPlan& pla
   p.cut = reinterpret_cast<int2*>(ws + plan.off_cut);
   const bool bf = a.q_dtype == PA_BF16;
   switch (a.cache_dtype) {
-    case PA_F32: return launch_f32(p, a.head_dim, stream);
-    case PA_F16: return launch_mma<__half, kH16>(p, a.head_dim, plan, stream);
-    case PA_BF16: return launch_mma<__nv_bfloat16, kB16>(p, a.head_dim, plan, stream);
+    case PA_F32: return launch_t<float, kF32>(p, a.head_dim, plan, stream);
+    case PA_F16: return launch_t<__half, kH16>(p, a.head_dim, plan, stream);
+    case PA_BF16: return launch_t<__nv_bfloat16, kB16>(p, a.head_dim, plan, stream);
     case PA_FP8_E4M3:
-      return bf ? launch_mma<__nv_bfloat16, kF8>(p, a.head_dim, plan, stream)
-                : launch_mma<__half, kF8>(p, a.head_dim, plan, stream);
+      return bf ? launch_t<__nv_bfloat16, kF8>(p, a.head_dim, plan, stream)
+                : launch_t<__half, kF8>(p, a.head_dim, plan, stream);
     case PA_INT4:
-      return bf ? launch_mma<__nv_bfloat16, kI4>(p, a.head_dim, plan, stream)
-                : launch_mma<__half, kI4>(p, a.head_dim, plan, stream);
+      return bf ? launch_t<__nv_bfloat16, kI4>(p, a.head_dim, plan, stream)
+                : launch_t<__half, kI4>(p, a.head_dim, plan, stream);
     case PA_NVFP4:
-      return bf ? launch_mma<__nv_bfloat16, kN4>(p, a.head_dim, plan, stream)
-                : launch_mma<__half, kN4>(p, a.head_dim, plan, stream);
+      return bf ? launch_t<__nv_bfloat16, kN4>(p, a.head_dim, plan, stream)
+                : launch_t<__half, kN4>(p, a.head_dim, plan, stream);
   }
   return cudaErrorInvalidValue;
 }

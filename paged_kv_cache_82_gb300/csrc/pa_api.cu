@@ -908,8 +908,8 @@ pa_status pa_attention_selected_workspace_size(int64_t num_tokens,
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   const DeviceInfo* di = device_info();
   if (!di) return PA_ERR_CUDA;
-  *bytes = (size_t)make_selected_plan(num_tokens, num_q_heads, num_kv_heads, head_dim,
-                                      max_selected, di->num_sms)
+  *bytes = (size_t)make_selected_plan(PA_BF16, num_tokens, num_q_heads, num_kv_heads,
+                                      head_dim, max_selected, di->num_sms)
                .bytes;
   return PA_OK;
 }
@@ -949,8 +949,9 @@ pa_status pa_attention_selected(
     return PA_ERR_UNSUPPORTED;
   const DeviceInfo* di = device_info();
   if (!di) return PA_ERR_CUDA;
-  const SelectedPlan plan = make_selected_plan(num_tokens, num_q_heads, num_kv_heads,
-                                               head_dim, max_selected, di->num_sms);
+  const SelectedPlan plan = make_selected_plan(cache_dtype, num_tokens, num_q_heads,
+                                               num_kv_heads, head_dim, max_selected,
+                                               di->num_sms);
   if (workspace_bytes < (size_t)plan.bytes ||
       (plan.bytes > 0 && (!workspace || !aligned(workspace, 256))))
     return PA_ERR_INVALID_ARG;

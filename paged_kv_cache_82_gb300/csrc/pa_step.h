@@ -87,8 +87,9 @@ struct SelectedPlan {
   int64_t shares;  // equal shares of all the lists' entries
   int64_t off_ml, off_cut, bytes;  // workspace
 };
-SelectedPlan make_selected_plan(int64_t num_tokens, int num_q_heads, int num_kv_heads,
-                                int head_dim, int max_selected, int num_sms);
+SelectedPlan make_selected_plan(pa_dtype cache_dtype, int64_t num_tokens, int num_q_heads,
+                                int num_kv_heads, int head_dim, int max_selected,
+                                int num_sms);
 struct SelectedArgs {
   const void* q;
   pa_dtype q_dtype;

@@ -731,8 +731,8 @@ template <int kPg, int kD>
 cudaError_t launch_summarise_d(const StepView& s, const void* k_cache, int num_kv_heads,
                                void* bounds, cudaStream_t stream) {
   // blocks a request of max_query_len tokens writes to, at most
-  const int64_t wide = std::min<int64_t>((s.max_query_len + kBS - 2) / kBS + 1,
-                                         (s.max_seq_len + kBS - 1) / kBS);
+  const int64_t wide = std::min(((int64_t)s.max_query_len + kBS - 2) / kBS + 1,
+                                ((int64_t)s.max_seq_len + kBS - 1) / kBS);
   // a warp per KV head, eight to a CTA at most
   const int warps = std::min(num_kv_heads, kThreads / 32);
   const dim3 grid((unsigned)wide, (unsigned)std::min(s.num_seqs, 65535),
@@ -822,7 +822,7 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
                                  int max_selected, int keep_first, int keep_last,
                                  int32_t* selected, int32_t* num_selected,
                                  void* workspace, int num_sms, cudaStream_t stream) {
-  const int max_blocks = (s.max_seq_len + kBS - 1) / kBS;
+  const int max_blocks = (int)(((int64_t)s.max_seq_len + kBS - 1) / kBS);
   for (int64_t t0 = 0; t0 < s.num_tokens; t0 += plan.pass_tokens) {
     const int64_t nt = std::min(plan.pass_tokens, s.num_tokens - t0);
     if (max_blocks > max_selected) {

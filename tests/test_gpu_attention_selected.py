@@ -217,3 +217,55 @@ def test_page_offsets_past_32_bits():
                            torch.tensor([0, 64], **i32), 64, 64, 64)
     assert pa.pa_get_device_error() == 0
     assert (bounds[-4:, :, 256:260].view(torch.float32) > 0).all()
+
+
+F32_CASES = [(1, 128, RAGGED, 12), (3, 64, CHUNKS, 9), (4, 64, RAGGED, 30), (5, 128, CHUNKS, 17),
+             (8, 128, RAGGED, 40), (8, 64, CHUNKS, 5), (12, 128, CHUNKS, 8), (20, 64, RAGGED, 6),
+             (4, 128, [(20000, 1)], 1000), (8, 128, [(9000, 2), (31, 1)], 500)]
+
+
+@pytest.mark.parametrize("kind", ["random", "ragged"])
+@pytest.mark.parametrize("group,D,lens,K", F32_CASES)
+def test_fp32_caches(group, D, lens, K, kind):
+    """Heads in fours, eights and several parts; keys of one and of half a row of
+    lanes; lists within a CTA's share and across many."""
+    Hkv = 3 if group < 8 else 2
+    wl, md, dev = step(lens, group * Hkv, Hkv, D, "f32")
+    lists = _lists(np.random.default_rng(group + K), md, Hkv, K, kind)
+    out = _run(wl, md, dev, lists, K)
+    assert pa.pa_get_device_error() == 0
+    _check(wl, md, lists, out)
+    again = _run(wl, md, dev, lists, K)
+    assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype,group", [("bf16", 4), ("f16", 16), ("f32", 3), ("f32", 9)])
+def test_long_lists_among_many_short_ones(dtype, group):
+    """Rows of one to three blocks, empty rows, and two of hundreds: the shares
+    cut the long ones and string the short ones together."""
+    lens = [(1 + 37 * i % 60, 1) for i in range(90)]
+    lens[40], lens[88] = (9000, 1), (7000, 1)
+    wl, md, dev = step(lens, 2 * group, 2, 128, dtype)
+    K = 600
+    lists = _lists(np.random.default_rng(group), md, 2, K)
+    for t in (0, 7, 8, 41, 87):
+        lists[t, 0] = []
+    out = _run(wl, md, dev, lists, K)
+    assert pa.pa_get_device_error() == 0
+    _check(wl, md, lists, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_nan_key_makes_its_heads_nan(dtype):
+    """A NaN key that is visible is no -inf: the rows that read it are NaN, as
+    the sum of the formula is, wherever in the list it stands; and a row that
+    does not list its block is not touched by it."""
+    wl, md, dev = step([(200, 1)] * 3, 4, 2, 128, dtype)
+    lists = {(t, h): [0, 4, 8, 12] for t in range(3) for h in range(2)}
+    for t, block in enumerate((0, 8, 5)):
+        wl.k_cache[md["block_tables"][t, block], 1, 0, 7] = float("nan")
+    out = _run(wl, md, dev, lists, 4)
+    assert pa.pa_get_device_error() == 0
+    nan = out.isnan().all(-1).cpu()
+    assert nan.tolist() == [[False, False, True, True]] * 2 + [[False] * 4]
+    assert out[~nan.cuda()].isfinite().all()
