@@ -93,7 +93,8 @@ typedef enum {
 /* Device-side error flags (bit mask) reported by pa_get_device_error. */
 #define PA_DEV_ERR_SLOT 0x1u      /* slot >= num_blocks * block_size        */
 #define PA_DEV_ERR_BLOCK_ID 0x2u  /* block id outside [0, num_blocks)       */
-#define PA_DEV_ERR_METADATA 0x4u  /* seq_len / query_start_loc inconsistent */
+#define PA_DEV_ERR_METADATA 0x4u  /* seq_len / query_start_loc inconsistent;
+                                     lengths, positions or lists out of range */
 #define PA_DEV_ERR_TIMEOUT 0x8u   /* a bounded pipeline wait ran out
                                      (pa_set_wait_limit_ns)                   */
 #define PA_DEV_ERR_NO_BLOCKS 0x10u /* pa_build_step ran out of free blocks   */
@@ -452,9 +453,10 @@ pa_status pa_build_step(const int32_t* query_lens, const int32_t* computed_lens,
  *              overlaps nothing.
  * slot_mapping, caches, cache_dtype, scales : as pa_reshape_and_cache (16-byte
  *              aligned caches); a token with a negative slot is padding:
- *              nothing of it is read or written, its q_out row included, and
- *              a token whose slot is out of range (PA_DEV_ERR_SLOT) is
- *              skipped as well.
+ *              nothing of it is written, its q_out row included (its rows
+ *              of q, k and v are loaded and not used), and a token whose slot
+ *              is out of range (PA_DEV_ERR_SLOT) is skipped as well.  Two
+ *              tokens of one slot leave it with either's elements.
  */
 pa_status pa_norm_rope_and_cache(
     const void* q, const void* k, const void* v, pa_dtype dtype,
@@ -495,8 +497,8 @@ pa_status pa_norm_rope_and_cache(
  * each over its tokens 0 .. min(16, L_r - 16 b) - 1.  A call whose
  * query_start_loc names all of a request's tokens as new (n_r = L_r) builds
  * all of its records.  Step arguments and their checks as pa_attention.  A
- * block copied by pa_copy_blocks gets its record with the next token written
- * to it; until then the source's record holds for it too.
+ * block copied by pa_copy_blocks has no record of its own until a token is
+ * written to it: copy the source's record with it.
  * bounds : device, 16-byte aligned; other records are left as they were.
  */
 pa_status pa_summarise_blocks(const void* k_cache, pa_dtype cache_dtype,
@@ -522,7 +524,10 @@ pa_status pa_summarise_blocks(const void* k_cache, pa_dtype cache_dtype,
  *   score = fl32(s * max over these heads of
  *                    sum_d qc_d * (qc_d >= 0 ? hi_d : lo_d))
  * with the block's codes hi, lo and scale s.  The sum is one of whole numbers:
- * equal inputs select equal blocks whatever the batch around them.
+ * equal inputs select equal blocks whatever the batch around them.  A query
+ * element that is NaN counts as 0, a NaN score (of a record that was never
+ * written) above all others; a block id out of range sets PA_DEV_ERR_BLOCK_ID
+ * and scores below all others.
  *
  * q            : device [num_tokens][num_q_heads][head_dim] of q_dtype
  *                (PA_F32 / PA_F16 / PA_BF16), 16-byte aligned.
@@ -563,7 +568,8 @@ pa_status pa_select_blocks(const void* q, pa_dtype q_dtype, const void* bounds,
  * Other arguments, types, results and checks as pa_attention (every cache type
  * it takes; an entry whose physical block id is out of range is skipped with
  * PA_DEV_ERR_BLOCK_ID).  The workspace must hold
- * pa_attention_selected_workspace_size bytes for the same sizes.
+ * pa_attention_selected_workspace_size bytes for the same sizes.  max_selected <=
+ * 2^24 and num_tokens * num_kv_heads < 2^31, else PA_ERR_UNSUPPORTED.
  * Results are bitwise deterministic from run to run.
  */
 pa_status pa_attention_selected_workspace_size(int64_t num_tokens,

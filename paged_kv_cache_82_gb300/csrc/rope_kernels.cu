@@ -14,7 +14,10 @@
 // lanes hold one head's row, two groups of 4 elements each: the groups that
 // the rotation pairs (i, i + R/2), so that it stays within a lane, and two
 // neighbours where nothing turns or neighbours turn.  The row's sum is a few
-// shuffles.
+// shuffles.  8192 tokens of 64 + 8 + 8 heads of 128, bf16 over an E4M3 cache: 70 us,
+// 4.6 TB/s (its bytes at the copy rate: 48 us); 65 % of the issue slots are taken
+// by some 20 instructions per element, so what is left lies there.  64 tokens: 2.2
+// us.
 #include <type_traits>
 
 #include "pa_step.cuh"

@@ -177,7 +177,8 @@ struct Range8 {
 // a token, the warp reads 256 / kD tokens at a time and all of the page's 16
 // before it uses the first.  The page is read once and a 1/32 to 1/8 of its
 // bytes written, so the kernel is bound by HBM when there are many pages, and
-// by the chain of loads (lengths, block id, page) when there are few.
+// by the chain of loads (lengths, block id, page) when there are few.  16 x 32K
+// tokens x 8 heads of 128, E4M3: 110 us, 5.6 TB/s; one block of 64 requests: 2.6 us.
 template <int kPg, int kD>
 __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_cache,
                                               int num_kv_heads, int r, int nth, int h,
@@ -405,7 +406,9 @@ struct ScoreLayout {
 // record's 17 (or 9) pieces of 16 bytes put the 8 lanes of a quarter warp into
 // different banks.  The codes of kG query heads lie in shared memory too: their
 // signs pick the product's bound in two logic operations per word, and a word's
-// four products are one dp4a.
+// four products are one dp4a.  64 tokens of 8K to 64K, 32 / 8 heads of 128: 48 us for
+// 232 MB: 6.3 TB/s once a CTA runs, after 4 to 5 us for its query's codes.  (Equal
+// shares of all rows' blocks on resident CTAs instead: 48 us as well.)
 template <typename TQ, int kD, int kG>
 __global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : kScoreCtas)
 score_kernel(const ScoreParams p) {
@@ -581,7 +584,8 @@ constexpr int kTopkBins = 1 << kTopkBits;
 // is that of the row's own keys, so no round is spent on their common bits).
 // Then each warp writes the entries of its contiguous part of the row in
 // order.  kPer keys per lane are held in registers (kTopkThreads x kPer blocks);
-// kPer = 0 reads them again each time.
+// kPer = 0 reads them again each time.  Bound by the rounds' barriers: 512 rows of
+// 512 to 4096 blocks 13 us, 8 rows of 8192 about 8.
 template <int kTopkThreads, int kPer>
 __global__ void __launch_bounds__(kTopkThreads, 65536 / kTopkThreads / (kPer > 16 ? 80 : 64))
 topk_kernel(const TopkParams p) {
