@@ -568,7 +568,7 @@ score_kernel(const ScoreParams p) {
 struct TopkParams {
   StepView s;
   int64_t t0;
-  int num_kv_heads, max_selected;
+  int num_kv_heads, max_selected, kept;  // kept: keep_first + keep_last
   int64_t row_scores;
   const uint32_t* keys;
   int32_t* selected;
@@ -618,45 +618,43 @@ topk_kernel(const TopkParams p) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = begin + 32 * j + lane;
-      held[j] = i < end ? keys[i] : 0u;
+      held[j] = i < end ? keys[i] : kKeptKey;
     }
   }
-  // f(key) for each of the lane's keys in order; every lane of the warp comes
-  // along (on: the key exists)
+  // f(key, block) for each of the lane's keys in order; every lane of the warp
+  // comes along (a lane past the part's end with a kept key)
   auto each = [&](auto&& f) {
     if constexpr (kPer > 0) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         if (begin + 32 * j >= end) break;
         const int i = begin + 32 * j + lane;
-        f(held[j], i, i < end);
+        f(held[j], i);
       }
     } else {
       for (int i0 = begin; i0 < end; i0 += 32) {
         const int i = i0 + lane;
-        f(i < end ? keys[i] : 0u, i, i < end);
+        f(i < end ? keys[i] : kKeptKey, i);
       }
     }
   };
-  // the range of the keys that are scores (the kept ones are above all)
+  // the range of the keys that are scores; a kept key + 1 is 0
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  int kept = 0;
-  each([&](uint32_t k, int, bool on) {
-    const bool score = on && k != kKeptKey;
-    kept += __popc(__ballot_sync(~0u, on && k == kKeptKey));
-    if (score) lo = min(lo, k), hi = max(hi, k);
+  each([&](uint32_t k, int) {
+    lo = min(lo, k);
+    hi = max(hi, k + 1);
   });
   lo = __reduce_min_sync(~0u, lo);
   hi = __reduce_max_sync(~0u, hi);
-  if (lane == 0) s_lo[warp] = lo, s_hi[warp] = hi, s_warp[warp] = kept;
+  if (lane == 0) s_lo[warp] = lo, s_hi[warp] = hi;
   __syncthreads();
-  int need = K;
 #pragma unroll
   for (int w = 0; w < kTopkWarps; ++w) {
     lo = min(lo, s_lo[w]);
     hi = max(hi, s_hi[w]);
-    need -= s_warp[w];
   }
+  --hi;
+  int need = K - p.kept;  // n > K, and the kept blocks are K at most
   // Selected: the kept keys, those above the range [lo, lo + 2^bits), and the
   // first `need` of those inside.  (need = 0, all kept: none inside.)
   int bits = hi > lo ? 32 - __clz(hi - lo) : 0;
@@ -667,8 +665,8 @@ topk_kernel(const TopkParams p) {
 #pragma unroll
       for (int i = 0; i < kTopkOwn; ++i) hist[tid + i * kTopkThreads] = 0;
       __syncthreads();
-      each([&](uint32_t k, int, bool on) {
-        if (on && k >= lo && k <= top) atomicAdd(&hist[(k - lo) >> shift], 1);
+      each([&](uint32_t k, int) {
+        if (k - lo <= top - lo) atomicAdd(&hist[(k - lo) >> shift], 1);
       });
       __syncthreads();
       // keys in the bins above this thread's
@@ -703,14 +701,15 @@ topk_kernel(const TopkParams p) {
     }
   }
   // in order: the keys above, and the first `need` of those inside
-  auto over = [&](uint32_t k) { return k > top; };
-  auto inside = [&](uint32_t k) { return k >= lo && k <= top; };
-  if (need == 0) lo = 0xFFFFFFFFu, top = 0xFFFFFFFEu;  // the kept keys alone
+  if (need == 0) lo = 0xFFFFFFFEu, top = 0xFFFFFFFEu;  // the kept keys alone
   int above = 0, equal = 0;
-  each([&](uint32_t k, int, bool on) {
-    above += __popc(__ballot_sync(~0u, on && over(k)));
-    equal += __popc(__ballot_sync(~0u, on && inside(k)));
+  each([&](uint32_t k, int) {
+    above += k > top;
+    equal += k - lo <= top - lo;
   });
+  // (the lanes past the part's end had kept keys)
+  above = __reduce_add_sync(~0u, above) - (((end - begin + 31) & ~31) - (end - begin));
+  equal = __reduce_add_sync(~0u, equal);
   __syncthreads();  // s_warp was read above
   if (lane == 0) s_warp[warp] = above, s_equal[warp] = equal;
   __syncthreads();
@@ -719,15 +718,18 @@ topk_kernel(const TopkParams p) {
     at += s_warp[w];
     eq += s_equal[w];
   }
-  each([&](uint32_t k, int i, bool on) {
-    const unsigned gt = __ballot_sync(~0u, on && over(k));
-    const unsigned ge = __ballot_sync(~0u, on && inside(k));
-    const unsigned below = (1u << lane) - 1;
-    const int e = eq + __popc(ge & below);  // keys inside before this one
-    if ((gt >> lane & 1) || ((ge >> lane & 1) && e < need))
-      out[at + __popc(gt & below) + min(e, need)] = i;
-    at += __popc(gt);
-    eq += __popc(ge);
+  at += min(eq, need);
+  const unsigned below = (1u << lane) - 1;
+  each([&](uint32_t k, int i) {
+    bool take = k > top && i < end;
+    const unsigned ge = __ballot_sync(~0u, k - lo <= top - lo);
+    if (ge) {  // keys inside: few
+      take |= (ge >> lane & 1) && eq + __popc(ge & below) < need;
+      eq += __popc(ge);
+    }
+    const unsigned taken = __ballot_sync(~0u, take);
+    if (take) out[at + __popc(taken & below)] = i;
+    at += __popc(taken);
   });
 }
 
@@ -863,6 +865,7 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
     tp.t0 = t0;
     tp.num_kv_heads = num_kv_heads;
     tp.max_selected = max_selected;
+    tp.kept = keep_first + keep_last;
     tp.row_scores = plan.row_scores;
     tp.keys = static_cast<const uint32_t*>(workspace);
     tp.selected = selected;
