@@ -20,7 +20,7 @@ cudaError_t launch_build_step(const int32_t* query_lens, const int32_t* computed
                               int64_t* slot_mapping, unsigned* err,
                               cudaStream_t stream);
 
-// ---- norm, rotation and cache write (rope_kernels.cu) -----------------------
+// ---- norm, rotation and cache write (rope_kernels.cuh) ----------------------
 struct RopeArgs {
   const void* q;
   const void* k;

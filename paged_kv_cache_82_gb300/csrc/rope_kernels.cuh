@@ -1,4 +1,4 @@
-// rope_kernels.cu -- what lies between a layer's QKV projection and its
+// rope_kernels.cuh -- what lies between a layer's QKV projection and its
 // attention, in one pass (pa_norm_rope_and_cache): RMS norm of every query and
 // key head, the position rotation, and the write of K and V into the cache.
 //
@@ -14,10 +14,11 @@
 // lanes hold one head's row, two groups of 4 elements each: the groups that
 // the rotation pairs (i, i + R/2), so that it stays within a lane, and two
 // neighbours where nothing turns or neighbours turn.  The row's sum is a few
-// shuffles.  8192 tokens of 64 + 8 + 8 heads of 128, bf16 over an E4M3 cache: 70 us,
-// 4.6 TB/s (its bytes at the copy rate: 48 us); 65 % of the issue slots are taken
-// by some 20 instructions per element, so what is left lies there.  64 tokens: 2.2
-// us.
+// shuffles.  8192 tokens of 64 + 8 + 8 heads of 128, bf16 over an E4M3 cache: 59 us,
+// 5.5 TB/s (its bytes at the copy rate: 48 us); what is left are the instructions,
+// some 15 per element.  64 tokens: 2.2 us.
+#pragma once
+
 #include <type_traits>
 
 #include "pa_step.cuh"
@@ -28,8 +29,8 @@ namespace {
 constexpr int kThreads = 256;
 // Rows per lane group, and CTAs per SM (64 registers a thread), of a large
 // step.  8192 tokens of 64 + 8 + 8 heads of 128, bf16 over an FP8 cache, in us:
-// 8 rows 70, 4 rows 77, 2 rows 95 with four CTAs; 8 rows 75 with three, 116 with
-// five (spills).
+// 8 rows 59, 4 rows 66 with four CTAs; 8 rows 63 with three, 16 rows 78; 4 rows 63
+// with five.
 constexpr int kHeads = 8;
 constexpr int kCtas = 4;
 
@@ -84,7 +85,7 @@ struct Place {
 // Pairs of 16-bit types are taken apart and put together as words.
 template <typename T>
 struct Row8 {
-  static constexpr int kWords = 2 * sizeof(T), kGroup = kWords / 2;  // of four elements
+  static constexpr int kWords = 2 * sizeof(T);
   uint32_t w[kWords];
   template <bool kVec>
   __device__ __forceinline__ void load(const T* row, const Place& at) {
@@ -318,38 +319,54 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(const RopePa
   const Divisor scale(which == 2 ? p.v_scale : p.k_scale,
                       which > 0 && (kCache == kFp8 || kCache == kNvfp4));
   T* q_out = static_cast<T*>(p.q_out) + (t * p.num_q_heads + h0) * kD;
+  // Rows of one kind, each straight through: without a branch between them their
+  // instructions interleave (the chunk above: 59 us, with branches on the kind and
+  // the norm in every row 70).
+  auto rows = [&](auto kind, auto norm) {
 #pragma unroll
-  for (int j = 0; j < kH; ++j) {
-    if (first + j * kRows >= heads) break;  // the whole warp is past
-    const bool on = h0 + j * kRows < heads;
-    if (which < 2) {
-      float x[8], y[8];
-      raw[j].values(x);
-      float r = 1.f;
-      if (wp) {
-        float ss = 0.f;
+    for (int j = 0; j < kH; ++j) {
+      if (first + j * kRows >= heads) break;  // the whole warp is past
+      const bool on = h0 + j * kRows < heads;
+      if constexpr (kind() < 2) {
+        float x[8], y[8];
+        raw[j].values(x);
+        float r = 1.f;
+        if constexpr (norm()) {
+          float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
-        r = rsqrtf(ss * (1.0f / kD) + p.eps);
+          for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
+          r = rsqrtf(ss * (1.0f / kD) + p.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = x[i] * own[i];
+          if (turns) y[i] = fmaf(kInter ? x[i ^ 1] : x[i ^ 4], other[i], y[i]);
+          if constexpr (norm()) y[i] *= r;
+        }
+        raw[j].round(y);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = x[i] * own[i];
-        if (turns) y[i] = fmaf(kInter ? x[i ^ 1] : x[i ^ 4], other[i], y[i]);
-        y[i] *= r;
+      if constexpr (kind() == 0) {
+        if (on) raw[j].store(q_out + j * kRows * kD, at);
+      } else {
+        cache_row<T, kCache, kD>(kind() == 2 ? p.v_cache : p.k_cache,
+                                 b * p.num_kv_heads + h0 + j * kRows, o, lane, sub, at, pairs,
+                                 raw[j], scale, on);
       }
-      raw[j].round(y);
     }
-    if (which == 0) {
-      if (on) raw[j].store(q_out + j * kRows * kD, at);
-    } else {
-      cache_row<T, kCache, kD>(which == 2 ? p.v_cache : p.k_cache,
-                               b * p.num_kv_heads + h0 + j * kRows, o, lane, sub, at, pairs,
-                               raw[j], scale, on);
-    }
-  }
+  };
+  using std::integral_constant;
+  if (which == 2)
+    rows(integral_constant<int, 2>{}, std::false_type{});
+  else if (which == 1 && wp)
+    rows(integral_constant<int, 1>{}, std::true_type{});
+  else if (which == 1)
+    rows(integral_constant<int, 1>{}, std::false_type{});
+  else if (wp)
+    rows(integral_constant<int, 0>{}, std::true_type{});
+  else
+    rows(integral_constant<int, 0>{}, std::false_type{});
 }
 
 template <typename T, int kCache, int kD, bool kVec, int kH>
@@ -407,8 +424,10 @@ cudaError_t launch_c(const RopeParams& p, pa_dtype cache, int head_dim, bool vec
 
 }  // namespace
 
-cudaError_t launch_norm_rope_and_cache(const RopeArgs& a, int num_sms, unsigned* err,
-                                       cudaStream_t stream) {
+// The call for inputs of type T (one translation unit each: their many forms
+// are compiled side by side).
+template <typename T>
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, unsigned* err, cudaStream_t stream) {
   RopeParams p{};
   p.q = a.q;
   p.k = a.k;
@@ -437,13 +456,12 @@ cudaError_t launch_norm_rope_and_cache(const RopeArgs& a, int num_sms, unsigned*
   p.v_scale = a.v_scale;
   p.err = err;
   p.num_sms = num_sms;
-  switch (a.dtype) {
-    case PA_F32: return launch_c<float>(p, a.cache_dtype, a.head_dim, a.vector_ok, stream);
-    case PA_F16: return launch_c<__half>(p, a.cache_dtype, a.head_dim, a.vector_ok, stream);
-    case PA_BF16:
-      return launch_c<__nv_bfloat16>(p, a.cache_dtype, a.head_dim, a.vector_ok, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  return launch_c<T>(p, a.cache_dtype, a.head_dim, a.vector_ok, stream);
 }
+
+extern template cudaError_t launch_rope<float>(const RopeArgs&, int, unsigned*, cudaStream_t);
+extern template cudaError_t launch_rope<__half>(const RopeArgs&, int, unsigned*, cudaStream_t);
+extern template cudaError_t launch_rope<__nv_bfloat16>(const RopeArgs&, int, unsigned*,
+                                                       cudaStream_t);
 
 }  // namespace pa

@@ -585,7 +585,7 @@ constexpr int kTopkBins = 1 << kTopkBits;
 // Then each warp writes the entries of its contiguous part of the row in
 // order.  kPer keys per lane are held in registers (kTopkThreads x kPer blocks);
 // kPer = 0 reads them again each time.  Bound by the rounds' barriers: 512 rows of
-// 512 to 4096 blocks 13 us, 8 rows of 8192 about 8.
+// 512 to 4096 blocks about 10 us, 8 rows of 8192 about 7.
 template <int kTopkThreads, int kPer>
 __global__ void __launch_bounds__(kTopkThreads, 65536 / kTopkThreads / (kPer > 16 ? 80 : 64))
 topk_kernel(const TopkParams p) {
