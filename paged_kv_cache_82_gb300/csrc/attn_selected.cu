@@ -23,9 +23,9 @@
 // barrier in the loop: each warp walks its own pages, and the next page's K
 // (then V) loads go out as soon as the MMAs have consumed the registers.
 //
-// 64 tokens x 8 KV heads x 128 blocks of 128 channels, 4 query heads each: bf16 90
-// us, 6.0 TB/s (89 % of a copy); 32 x 8 x 256 blocks of E4M3, 8 heads: 57 us, 4.7
-// TB/s.  About 13 us of either are the way to the first page (list lengths,
+// 64 tokens x 8 KV heads x 128 blocks of 128 channels, 4 query heads each: bf16 89
+// us, 6.0 TB/s (90 % of a copy); 32 x 8 x 256 blocks of E4M3, 8 heads: 56 us, 4.8
+// TB/s.  About 12 us of either are the way to the first page (list lengths,
 // request, block id, page: four dependent loads) and the join.  One token: 12 us.
 #include <algorithm>
 
@@ -97,20 +97,25 @@ __device__ __forceinline__ Unit find_unit(const SelParams& p, int64_t row, bool 
   return u;
 }
 
-// Entry i of the unit's list: the logical block and its physical block (-1:
-// skipped, with a flag -- not above the entry before it, past the token's
-// position, or a bad physical id).
+// Entry i of a row's list as it is there, and the one before it: read without
+// the row's request, on their way while that is looked up.
+struct Listed {
+  int block, before;
+};
+__device__ __forceinline__ Listed listed(const SelParams& p, int64_t row, int i) {
+  const int32_t* list = p.selected + row * p.max_selected;
+  return Listed{__ldg(list + i), i > 0 ? __ldg(list + i - 1) : -1};
+}
+
+// The logical block and its physical block (-1: skipped, with a flag -- not
+// above the entry before it, past the token's position, or a bad physical id).
 struct Entry {
   int block, phys;
 };
-__device__ __forceinline__ Entry list_entry(const SelParams& p, const Unit& u, int i) {
-  const int32_t* list =
-      p.selected + (u.t * p.num_kv_heads + u.h) * p.max_selected;
-  Entry e;
-  e.block = __ldg(list + i);
-  const int before = i > 0 ? __ldg(list + i - 1) : -1;
-  e.phys = -1;
-  if (e.block <= before || e.block < 0 || e.block > u.pos / kBS) {
+__device__ __forceinline__ Entry list_entry(const SelParams& p, const Unit& u,
+                                            const Listed& at) {
+  Entry e{at.block, -1};
+  if (e.block <= at.before || e.block < 0 || e.block > u.pos / kBS) {
     flag_error(p.s.err, PA_DEV_ERR_METADATA);
     return e;
   }
@@ -241,17 +246,29 @@ struct Share {
 __device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // Every thread sums a contiguous part of the rows; the one whose part holds
-// the share's first unit walks it.
-__device__ __forceinline__ Share find_share(const SelParams& p, int64_t rows) {
+// the share's first unit walks it.  Its first counts go out together with the
+// last request's end, which bounds the rows (*rows).
+__device__ __forceinline__ Share find_share(const SelParams& p, int64_t* rows) {
+  constexpr int kHeld = 4;
   __shared__ int64_t warp_sums[32], total, s_row, s_row_begin;
-  const int64_t part = (rows + kThreads - 1) / kThreads;
-  const int64_t lo = least(rows, threadIdx.x * part), hi = least(rows, lo + part);
-  auto units = [&](int64_t row) {
-    const int n = list_length(p, row);
-    return n > 0 ? n + kRowCost : 0;
+  const int64_t all = p.s.num_tokens * p.num_kv_heads;
+  const int64_t part = (all + kThreads - 1) / kThreads;
+  const int64_t lo = least(all, threadIdx.x * part), hi = least(all, lo + part);
+  int held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    held[k] = lo + k < hi ? __ldg(p.num_selected + lo + k) : 0;
+  const int64_t last = __ldg(p.s.query_start_loc + p.s.num_seqs);
+  *rows = (last < 0 ? 0 : least(last, p.s.num_tokens)) * p.num_kv_heads;
+  const int64_t end = least(hi, *rows);
+  auto units = [&](int count) {
+    return count > 0 && count <= p.max_selected ? count + kRowCost : 0;
   };
   int64_t sum = 0;
-  for (int64_t i = lo; i < hi; ++i) sum += units(i);
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (lo + k < end) sum += units(held[k]);
+  for (int64_t i = lo + kHeld; i < end; ++i) sum += units(__ldg(p.num_selected + i));
   const int64_t before = block_scan_excl(sum, &total, warp_sums);
   Share s;
   s.size = (total + gridDim.x - 1) / gridDim.x;
@@ -260,7 +277,7 @@ __device__ __forceinline__ Share find_share(const SelParams& p, int64_t rows) {
   s.end = least(total, s.begin + s.size);
   if (s.begin < s.end && s.begin >= before && s.begin < before + sum) {
     int64_t at = before, i = lo;
-    for (int c; at + (c = units(i)) <= s.begin; ++i) at += c;
+    for (int c; at + (c = units(__ldg(p.num_selected + i))) <= s.begin; ++i) at += c;
     s_row = i;
     s_row_begin = at + kRowCost;
   }
@@ -271,21 +288,18 @@ __device__ __forceinline__ Share find_share(const SelParams& p, int64_t rows) {
 }
 
 template <typename TQ, int kPg, int kD, int kRows>
-__device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, int begin,
+__device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int begin,
                                             int end, int slot);
 template <int kD, int kRows>
-__device__ __forceinline__ void attend_part_f32(const SelParams& p, const Unit& u, int begin,
+__device__ __forceinline__ bool attend_part_f32(const SelParams& p, int64_t row, int begin,
                                                 int end, int slot);
 
 template <typename TQ, int kPg, int kD, int kRows>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(kPg == kF32, kRows))
 selected_kernel(const SelParams p) {
   pdl_launch_dependents();
-  // rows of tokens up to the last request's
-  const int64_t last = __ldg(p.s.query_start_loc + p.s.num_seqs);
-  const int64_t tokens = last < 0 ? 0 : least(last, p.s.num_tokens);
-  const int64_t rows = tokens * p.num_kv_heads;
-  const Share sh = find_share(p, rows);
+  int64_t rows;  // of tokens up to the last request's
+  const Share sh = find_share(p, &rows);
   const int cta = blockIdx.y * gridDim.x + blockIdx.x;
   int2 cut = make_int2(-1, 0);
   int64_t row = sh.row, row_begin = sh.row_begin;
@@ -294,18 +308,16 @@ selected_kernel(const SelParams p) {
       const int64_t row_end = row_begin + list_length(p, row);
       const int64_t begin = row_begin < sh.begin ? sh.begin : row_begin;
       const int64_t end = least(row_end, sh.end);
-      const Unit u = find_unit(p, row, threadIdx.x == 0);
-      if (u.count > 0) {
-        // -1: the whole list is here; else the CTA's place for a part
-        const int slot = begin == row_begin && end == row_end ? -1 : begin > row_begin ? 0 : 1;
-        const int from = (int)(begin - row_begin), to = (int)(end - row_begin);
-        if constexpr (kPg == kF32)
-          attend_part_f32<kD, kRows>(p, u, from, to, slot);
-        else
-          attend_part<TQ, kPg, kD, kRows>(p, u, from, to, slot);
-        if (slot == 1)
-          cut = make_int2((int)row, (int)((row_end - 1) / sh.size - blockIdx.x + 1));
-      }
+      // -1: the whole list is here; else the CTA's place for a part
+      const int slot = begin == row_begin && end == row_end ? -1 : begin > row_begin ? 0 : 1;
+      const int from = (int)(begin - row_begin), to = (int)(end - row_begin);
+      bool done;
+      if constexpr (kPg == kF32)
+        done = attend_part_f32<kD, kRows>(p, row, from, to, slot);
+      else
+        done = attend_part<TQ, kPg, kD, kRows>(p, row, from, to, slot);
+      if (done && slot == 1)
+        cut = make_int2((int)row, (int)((row_end - 1) / sh.size - blockIdx.x + 1));
       // the next row with a list
       do {
         if (++row >= rows) break;
@@ -358,15 +370,26 @@ __device__ __forceinline__ void finish_part(const SelParams& p, const Unit& u, i
   __syncthreads();  // the next part writes the shared memory again
 }
 
-// Entries begin .. end - 1 of a row's list, by the tensor cores.
+// Entries begin .. end - 1 of a row's list, by the tensor cores.  False: the row
+// is no request's, or its metadata is broken.
 template <typename TQ, int kPg, int kD, int kRows>
-__device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, int begin,
+__device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int begin,
                                             int end, int slot) {
   using Tr = PageTraits<kPg, kD>;
   constexpr bool kScaled = Tr::k4;  // pages with scales of their own
   constexpr int kNT = kRows / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;
+  constexpr int kP = Tr::kPages;
+  // The warp's steps: kP entries in a row from begin + kP warp, then kP kWarps
+  // further on.  The lanes hold the next 32 of the warp's entries.
+  const int first = begin + kP * warp;
+  const int steps = end > first ? (end - first + kP * kWarps - 1) / (kP * kWarps) : 0;
+  auto place = [&](int i) { return first + (i / kP) * (kP * kWarps) + i % kP; };
+  Listed ahead{0, 0};
+  if (place(lane) < end) ahead = listed(p, row, place(lane));
+  const Unit u = find_unit(p, row, threadIdx.x == 0);
+  if (u.count <= 0) return false;
   const int part = blockIdx.y;
   const int heads = min(p.group - part * kRows, kRows);
   const int head0 = u.h * p.group + part * kRows;
@@ -382,7 +405,6 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
     l[nt][0] = l[nt][1] = 0.f;
   }
 
-  constexpr int kP = Tr::kPages;
   constexpr int kKW = Tr::kKBytes / 4, kVW = Tr::kVBytes / 4;
   uint32_t kr[kP][2][Tr::kKChunks][kKW];
   uint32_t vr[kP][4][Tr::kVChunks][kVW];
@@ -444,18 +466,13 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
     }
   };
 
-  // The warp's steps: kP entries in a row from begin + kP warp, then kP kWarps
-  // further on.  The lanes hold the next 32 of the warp's entries.
-  const int first = begin + kP * warp;
-  const int steps = end > first ? (end - first + kP * kWarps - 1) / (kP * kWarps) : 0;
   Entry held{0, -1};
   auto entries = [&](int step, Entry (&en)[kP]) {
     const int i = step * kP;  // of the warp's entries
     if ((i & 31) == 0) {
-      const int mine = i + lane;
-      const int at = first + (mine / kP) * (kP * kWarps) + mine % kP;
+      const int at = place(i + lane);
       held = Entry{0, -1};
-      if (at < end) held = list_entry(p, u, at);
+      if (at < end) held = list_entry(p, u, i == 0 ? ahead : listed(p, row, at));
     }
 #pragma unroll
     for (int g = 0; g < kP; ++g)
@@ -779,6 +796,7 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
     }
   }
   finish_part<TQ, kRows, kD>(p, u, slot, Tr::kUnit, s_acc, s_m, s_l);
+  return true;
 }
 
 // fp32 pages, which no MMA takes in their precision: the same walk over the
@@ -789,7 +807,7 @@ __device__ __forceinline__ void attend_part(const SelParams& p, const Unit& u, i
 // and leaves lane l the score of head l % kRows.  About 1400 instructions per
 // page at 8 heads, 350 cycles of an SM; HBM brings an SM one page in 700.
 template <int kD, int kRows>
-__device__ __forceinline__ void attend_part_f32(const SelParams& p, const Unit& u, int begin,
+__device__ __forceinline__ bool attend_part_f32(const SelParams& p, int64_t row, int begin,
                                                 int end, int slot) {
   constexpr int kL = kD / 4;           // lanes of a key
   constexpr int kR = 32 / kL;          // keys of one load
@@ -801,13 +819,19 @@ __device__ __forceinline__ void attend_part_f32(const SelParams& p, const Unit& 
   __shared__ __align__(16) float s_p[kWarps][kBS][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % kL, sub = lane / kL;
+  const int first = begin + warp;
+  const int steps = end > first ? (end - first + kWarps - 1) / kWarps : 0;
+  Listed ahead{0, 0};
+  if (first + lane * kWarps < end) ahead = listed(p, row, first + lane * kWarps);
+  const Unit u = find_unit(p, row, threadIdx.x == 0);
+  if (u.count <= 0) return false;
   const int part = blockIdx.y;
   const int heads = min(p.group - part * kRows, kRows);
   const int head0 = u.h * p.group + part * kRows;
-  const int64_t row = (int64_t)u.h * (kBS * kD);
+  const int64_t head = (int64_t)u.h * (kBS * kD);
   const int64_t block = (int64_t)p.num_kv_heads * (kBS * kD);
-  const float* kbase = static_cast<const float*>(p.k_cache) + row + sub * kD + l * 4;
-  const float* vbase = static_cast<const float*>(p.v_cache) + row + sub * kD + l * 4;
+  const float* kbase = static_cast<const float*>(p.k_cache) + head + sub * kD + l * 4;
+  const float* vbase = static_cast<const float*>(p.v_cache) + head + sub * kD + l * 4;
   float4 kr[kN], vr[kN];
   // (a skipped entry reads block 0, as over the other types)
   auto load_k = [&](const Entry& e) {
@@ -820,14 +844,12 @@ __device__ __forceinline__ void attend_part_f32(const SelParams& p, const Unit& 
 #pragma unroll
     for (int n = 0; n < kN; ++n) vr[n] = __ldg(reinterpret_cast<const float4*>(src + n * kR * kD));
   };
-  const int first = begin + warp;
-  const int steps = end > first ? (end - first + kWarps - 1) / kWarps : 0;
   Entry held{0, -1};
   auto entry = [&](int i) {
     if ((i & 31) == 0) {
       const int at = first + (i + lane) * kWarps;
       held = Entry{0, -1};
-      if (at < end) held = list_entry(p, u, at);
+      if (at < end) held = list_entry(p, u, i == 0 ? ahead : listed(p, row, at));
     }
     return Entry{__shfl_sync(~0u, held.block, i & 31), __shfl_sync(~0u, held.phys, i & 31)};
   };
@@ -948,6 +970,7 @@ __device__ __forceinline__ void attend_part_f32(const SelParams& p, const Unit& 
     if (sub == 0) *reinterpret_cast<float4*>(&s_acc[warp][h][l * 4]) = acc[h];
   }
   finish_part<float, kRows, kD>(p, u, slot, 1.f, s_acc, s_m, s_l);
+  return true;
 }
 
 // Behind the shares: CTA i joins the list that begins in share i and is cut
