@@ -388,7 +388,6 @@ constexpr int kScoreChunkMax = 128, kScoreChunkMin = 32;
 template <int kD, int kG>
 struct ScoreLayout {
   static constexpr int kRec = PA_BOUNDS_BYTES(kD);
-  static constexpr int kPieces = kRec / 16;               // of 16 bytes, an odd number
   static constexpr int kBuf = kScoreGroup * kRec;         // bytes
   static constexpr int kCodes = kG * kD;
   static constexpr int kWarp = kScoreBufs * kBuf + kCodes;
@@ -403,19 +402,21 @@ struct ScoreLayout {
 // Each warp copies 16 records at a time into shared memory of its own, the
 // next ones while it scores these, so that what is on its way does not wait
 // for registers.  Two lanes score a record, half of its channels each; a
-// record's 17 (or 9) pieces of 16 bytes put the 8 lanes of a quarter warp into
+// record's 17 (or 9) words of 16 bytes put the 8 lanes of a quarter warp into
 // different banks.  The codes of kG query heads lie in shared memory too: their
 // signs pick the product's bound in two logic operations per word, and a word's
 // four products are one dp4a.  64 tokens of 8K to 64K, 32 / 8 heads of 128: 48 us for
-// 232 MB: 6.3 TB/s once a CTA runs, after 4 to 5 us for its query's codes.  (Equal
-// shares of all rows' blocks on resident CTAs instead: 48 us as well.)
+// 232 MB in scattered pieces of 2 KB, 4.8 TB/s.  Neither fewer instructions (a
+// fifth, in the copies and the query's codes), nor a third buffer, nor equal
+// shares of all rows' blocks on resident CTAs changed that.
 template <typename TQ, int kD, int kG>
 __global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : kScoreCtas)
 score_kernel(const ScoreParams p) {
   using Ly = ScoreLayout<kD, kG>;
   constexpr int kLanes = kD / 16;        // lanes of one query head's codes
   constexpr int kParts = 32 / kLanes;    // heads coded at a time
-  constexpr int kCopies = (kScoreGroup * Ly::kPieces + 31) / 32;
+  constexpr int kCodePieces = kD / 8;             // 16-byte pieces of a record's codes
+  constexpr int kCodeRecs = 32 / kCodePieces;
   extern __shared__ __align__(16) uint8_t score_smem[];
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -433,6 +434,8 @@ score_kernel(const ScoreParams p) {
   const uint32_t bufs_at = smem_u32(bufs);
   // this lane's record and half of the channels
   const int mine = lane & 15, half = lane >> 4;
+  const int code_off = lane % kCodePieces * 16;
+  const uint32_t code_at = lane / kCodePieces * Ly::kRec + code_off;
   const int passes = (p.group + kG - 1) / kG;
   const int stride = sharing * kScoreGroup;
   const int b_first = first + (warp / p.num_kv_heads) * kScoreGroup;
@@ -447,20 +450,24 @@ score_kernel(const ScoreParams p) {
       flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
       return -1;
     };
-    // copies of the 16 records from block b on: piece k = lane, lane + 32, ..
+    // Copies of the 16 records from block b on: kCodeRecs records' codes at a
+    // time, then their scales.  A block that is not read has block 0's.
     auto stage = [&](int b, int buf) {
-      const int id = b < last ? block_id(b + mine) : -1;
-      int rec = lane / Ly::kPieces, off = lane - rec * Ly::kPieces;
-      const uint32_t dst = bufs_at + buf * Ly::kBuf + lane * 16;
-#pragma unroll
-      for (int k = 0; k < kCopies; ++k) {
-        const int from = __shfl_sync(~0u, id, rec & 15);
-        if (from >= 0 && rec < kScoreGroup)
-          copy16_async(dst + k * 512, head_bounds + from * block_bytes + off * 16);
-        off += 32 % Ly::kPieces;
-        rec += 32 / Ly::kPieces;
-        if (off >= Ly::kPieces) off -= Ly::kPieces, ++rec;
+      int id = -1;
+      if (b >= last) {
+        copy_commit();
+        return id;
       }
+      id = block_id(b + mine);
+      const int from = max(id, 0);
+      const uint32_t dst = bufs_at + buf * Ly::kBuf;
+#pragma unroll
+      for (int k = 0; k < kScoreGroup; k += kCodeRecs)
+        copy16_async(dst + code_at + k * Ly::kRec,
+                     head_bounds + code_off +
+                         __shfl_sync(~0u, from, k + lane / kCodePieces) * block_bytes);
+      if (lane < kScoreGroup)
+        copy16_async(dst + lane * Ly::kRec + 2 * kD, head_bounds + 2 * kD + from * block_bytes);
       copy_commit();
       return id;
     };
