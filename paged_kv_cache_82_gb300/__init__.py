@@ -608,23 +608,28 @@ def pa_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor,
     then sines; None: no rotation); q_weight / k_weight [D] (None: no norm).
     Writes the caches and returns q_out [T, Hq, D] (q itself if given as such
     and contiguous)."""
-    if q.dim() != 3 or key.dim() != 3 or value.shape != key.shape \
-            or q.shape[0] != key.shape[0] or q.shape[2] != key.shape[2]:
+    qs, ks, dtype = q.shape, key.shape, q.dtype
+    if len(qs) != 3 or len(ks) != 3 or value.shape != ks or qs[0] != ks[0] \
+            or qs[2] != ks[2]:
         raise ValueError("q must be [T, Hq, D] and key/value [T, Hkv, D]")
-    T, Hq, D = q.shape
-    Hkv = key.shape[1]
-    if key.dtype != q.dtype or value.dtype != q.dtype:
+    T, Hq, D = qs
+    Hkv = ks[1]
+    if key.dtype is not dtype or value.dtype is not dtype:
         raise ValueError("q, key and value must be of one type")
-    for t, n in ((q, "q"), (key, "key"), (value, "value")):
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+    rows = []
+    for t, h, n in ((q, Hq, "q"), (key, Hkv, "key"), (value, Hkv, "value")):
+        row, head, one = t.stride()
+        if one != 1 or (h > 1 and head != D):
             raise ValueError(f"{n} must have contiguous rows")
+        # (of a single token: any stride will do)
+        rows.append(row if T > 1 else max(row, h * D))
     NB, Hc, bs, Dc = _cache_geometry(k_cache, cache_dtype, D)
-    if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape \
-            or v_cache.dtype != k_cache.dtype:
+    if Hc != Hkv or Dc != D or v_cache.shape != k_cache.shape \
+            or v_cache.dtype is not k_cache.dtype:
         raise ValueError("cache shape does not match key/value")
     span = rot = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2:
+        if len(cos_sin.shape) != 2:
             raise ValueError("cos_sin must be [max_position, rotary_dim]")
         span, rot = cos_sin.shape
         if positions is None:
@@ -632,23 +637,23 @@ def pa_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor,
     weight = q_weight if q_weight is not None else k_weight
     wdt = None if weight is None else weight.dtype
     if q_out is None:
-        q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
+        q_out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
+    elif q_out.shape != qs:
         raise ValueError("q_out must be a tensor like q")
     _plain(("slot_mapping", slot_mapping, _I64, T),
            ("positions", positions, _I32, T if rot else None),
            ("cos_sin", cos_sin, torch.float32, None),
            ("q_weight", q_weight, wdt, D), ("k_weight", k_weight, wdt, D),
-           ("q_out", q_out, q.dtype, None), ("k_cache", k_cache, None, None),
+           ("q_out", q_out, dtype, None), ("k_cache", k_cache, None, None),
            ("v_cache", v_cache, None, None))
     dev = q_out.get_device()
     if q.get_device() != dev or key.get_device() != dev or value.get_device() != dev:
         raise ValueError("q, key and value must be on the current CUDA device")
     st = _load().pa_norm_rope_and_cache(
         q.data_ptr(), key.data_ptr(), value.data_ptr(), _dtype_code(q), T,
-        _row_stride(q), _row_stride(key), _row_stride(value), _ptr(q_weight),
-        _ptr(k_weight), PA_F32 if weight is None else _dtype_code(weight), float(eps), _ptr(cos_sin), span, rot,
-        1 if interleaved else 0, _ptr(positions), q_out.data_ptr(),
+        *rows, _ptr(q_weight), _ptr(k_weight),
+        PA_F32 if weight is None else _dtype_code(weight), float(eps), _ptr(cos_sin),
+        span, rot, 1 if interleaved else 0, _ptr(positions), q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache, cache_dtype),
         NB, bs, Hq, Hkv, D, slot_mapping.data_ptr(), float(k_scale),
         float(v_scale), _stream(stream))
@@ -656,25 +661,21 @@ def pa_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor,
     return q_out
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements from one token's row to the next (of a single token: any)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
-
-
 def _bounds_shape(bounds: torch.Tensor, NB, Hkv: int, D: int) -> int:
-    if bounds.dim() != 3 or bounds.shape[1] != Hkv or bounds.shape[2] != 2 * D + 16 \
-            or (NB is not None and bounds.shape[0] != NB):
+    shape = bounds.shape
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != 2 * D + 16 \
+            or (NB is not None and shape[0] != NB):
         raise ValueError("bounds must be a uint8 [num_blocks, Hkv, bounds_bytes(D)] "
                          "tensor")
-    return bounds.shape[0]
+    return shape[0]
 
 
-def _step_tables(block_tables, seq_lens, query_start_loc) -> int:
-    B = seq_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != B \
-            or query_start_loc.numel() != B + 1:
+def _step_tables(block_tables, seq_lens, query_start_loc):
+    """(sequences, block-table entries of each)."""
+    B, shape = seq_lens.numel(), block_tables.shape
+    if len(shape) != 2 or shape[0] != B or query_start_loc.numel() != B + 1:
         raise ValueError("inconsistent number of sequences")
-    return B
+    return shape
 
 
 def pa_summarise_blocks(k_cache: torch.Tensor, bounds: torch.Tensor,
@@ -686,14 +687,14 @@ def pa_summarise_blocks(k_cache: torch.Tensor, bounds: torch.Tensor,
     (uint8 [num_blocks, Hkv, bounds_bytes(D)])."""
     NB, Hkv, bs, D = _cache_geometry(k_cache, cache_dtype)
     _bounds_shape(bounds, NB, Hkv, D)
-    B = _step_tables(block_tables, seq_lens, query_start_loc)
+    B, M = _step_tables(block_tables, seq_lens, query_start_loc)
     _plain(("k_cache", k_cache, None, None), ("bounds", bounds, _U8, None),
            ("block_tables", block_tables, _I32, None),
            ("seq_lens", seq_lens, _I32, B),
            ("query_start_loc", query_start_loc, _I32, None))
     st = _load().pa_summarise_blocks(
         k_cache.data_ptr(), _dtype_code(k_cache, cache_dtype), NB, bs, Hkv, D,
-        block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+        block_tables.data_ptr(), M, seq_lens.data_ptr(),
         query_start_loc.data_ptr(), B, int(num_tokens), int(max_query_len),
         int(max_seq_len), bounds.data_ptr(), _stream(stream))
     _check(st, "pa_summarise_blocks")
@@ -718,12 +719,13 @@ def pa_select_blocks(q: torch.Tensor, bounds: torch.Tensor,
                      workspace: Optional[torch.Tensor] = None, stream=None):
     """q [T, Hq, D]; bounds as pa_summarise_blocks leaves them.  Returns
     (selected int32 [T, Hkv, max_selected], num_selected int32 [T, Hkv])."""
-    if q.dim() != 3 or bounds.dim() != 3:
+    shape, records = q.shape, bounds.shape
+    if len(shape) != 3 or len(records) != 3:
         raise ValueError("q must be [T, Hq, D] and bounds [num_blocks, Hkv, bytes]")
-    T, Hq, D = q.shape
-    Hkv, K = bounds.shape[1], int(max_selected)
+    T, Hq, D = shape
+    Hkv, K = records[1], int(max_selected)
     NB = _bounds_shape(bounds, None, Hkv, D)
-    B = _step_tables(block_tables, seq_lens, query_start_loc)
+    B, M = _step_tables(block_tables, seq_lens, query_start_loc)
     if selected is None:
         selected = torch.empty(T, Hkv, K, dtype=_I32, device=q.device)
     if num_selected is None:
@@ -740,11 +742,11 @@ def pa_select_blocks(q: torch.Tensor, bounds: torch.Tensor,
            ("workspace", workspace, None, None))
     st = _load().pa_select_blocks(
         q.data_ptr(), _dtype_code(q), bounds.data_ptr(), NB, BLOCK_SIZE, Hq, Hkv,
-        D, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+        D, block_tables.data_ptr(), M, seq_lens.data_ptr(),
         query_start_loc.data_ptr(), B, T, int(max_query_len), int(max_seq_len), K,
         int(keep_first), int(keep_last), selected.data_ptr(),
         num_selected.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace.nbytes, _stream(stream))
     _check(st, "pa_select_blocks")
     return selected, num_selected
 
@@ -772,17 +774,18 @@ def pa_attention_selected(q: torch.Tensor, k_cache: torch.Tensor,
                           stream=None) -> torch.Tensor:
     """pa_attention over the listed blocks only: selected int32 [T, Hkv, K] in
     ascending order per row, num_selected int32 [T, Hkv]."""
-    if q.dim() != 3 or v_cache.shape != k_cache.shape \
+    shape, lists = q.shape, selected.shape
+    if len(shape) != 3 or v_cache.shape != k_cache.shape \
             or v_cache.dtype is not k_cache.dtype:
         raise ValueError("q must be [T, Hq, D] and both caches alike")
-    T, Hq, D = q.shape
+    T, Hq, D = shape
     NB, Hkv, bs, Dc = _cache_geometry(k_cache, cache_dtype)
     if Dc != D:
         raise ValueError("head_dim of q and of the caches differ")
-    B = _step_tables(block_tables, seq_lens, query_start_loc)
-    if selected.dim() != 3 or selected.shape[0] != T or selected.shape[1] != Hkv:
+    B, M = _step_tables(block_tables, seq_lens, query_start_loc)
+    if len(lists) != 3 or lists[0] != T or lists[1] != Hkv:
         raise ValueError("selected must be [T, Hkv, K]")
-    K = selected.shape[2]
+    K = lists[2]
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
@@ -795,14 +798,14 @@ def pa_attention_selected(q: torch.Tensor, k_cache: torch.Tensor,
            ("query_start_loc", query_start_loc, _I32, B + 1),
            ("selected", selected, _I32, None),
            ("num_selected", num_selected, _I32, T * Hkv),
-           ("out", out, q.dtype, q.numel()), ("workspace", workspace, None, None))
+           ("out", out, q.dtype, T * Hq * D), ("workspace", workspace, None, None))
     st = _load().pa_attention_selected(
         q.data_ptr(), _dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(),
         _dtype_code(k_cache, cache_dtype), NB, bs, Hq, Hkv, D,
-        block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+        block_tables.data_ptr(), M, seq_lens.data_ptr(),
         query_start_loc.data_ptr(), B, T, int(max_query_len), int(max_seq_len),
         selected.data_ptr(), num_selected.data_ptr(), K, float(scale),
         float(k_scale), float(v_scale), out.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace.nbytes, _stream(stream))
     _check(st, "pa_attention_selected")
     return out
