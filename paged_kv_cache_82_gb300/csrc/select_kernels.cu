@@ -406,9 +406,11 @@ struct ScoreLayout {
 // different banks.  The codes of kG query heads lie in shared memory too: their
 // signs pick the product's bound in two logic operations per word, and a word's
 // four products are one dp4a.  64 tokens of 8K to 64K, 32 / 8 heads of 128: 48 us for
-// 232 MB in scattered pieces of 2 KB, 4.8 TB/s.  Neither fewer instructions (a
-// fifth, in the copies and the query's codes), nor a third buffer, nor equal
-// shares of all rows' blocks on resident CTAs changed that.
+// 232 MB: 6.3 TB/s while it streams, after 4 to 5 us for the first records and
+// codes, and before a ragged end.  Neither fewer instructions (a fifth, in the
+// copies and the query's codes), nor a third buffer, nor equal shares of all
+// rows' blocks on resident CTAs (each token's start then costs as much) made it
+// shorter.
 template <typename TQ, int kD, int kG>
 __global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : kScoreCtas)
 score_kernel(const ScoreParams p) {
@@ -888,7 +890,7 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
     cfg.attrs = at;
     cfg.numAttrs = max_blocks > max_selected ? 1 : 0;
     // rows enough for every SM: 256 threads each (four to an SM: 512 rows of
-    // 512 to 4096 blocks 12.8 us, with 512 threads 15.9); fewer: 1024, for the
+    // 512 to 4096 blocks 10 us, with 512 threads a quarter more); fewer: 1024, for the
     // one row's sake
     const bool many = nt * num_kv_heads > num_sms;
     cfg.blockDim = dim3(many ? 256 : 1024);
