@@ -1028,25 +1028,31 @@ __device__ __forceinline__ void join_cut(const SelParams& p, int2 cut) {
 
 // Behind the shares: CTA i joins the list that begins in share i and is cut
 // (the part there, then the first part of each share it goes on through), and
-// writes the zeros of the rows i, i + gridDim.x, .. whose list is empty.
+// writes the zeros of the rows i, i + gridDim.x, .. whose list is empty: a
+// thread looks at a row's count, its warp then writes the empty ones.
 template <typename TQ, int kD>
 __global__ void __launch_bounds__(kJoinThreads) selected_join_kernel(const SelParams p) {
-  const int part = blockIdx.y;
-  const int64_t rows = p.s.num_tokens * p.num_kv_heads;
+  const int part = blockIdx.y, lane = threadIdx.x & 31;
+  const int64_t rows = p.s.num_tokens * p.num_kv_heads, step = gridDim.x;
+  auto empty = [&](int64_t row) { return row < rows && list_length(p, row) == 0; };
   // These CTAs start as the shares' end: what can be read before goes out first,
   // and the zeros come last (before the join: one token's 8 lists 12.0 us, not 10.5).
-  const int count = blockIdx.x < rows ? list_length(p, blockIdx.x) : 1;
+  const bool here = empty(blockIdx.x + threadIdx.x * step);
   pdl_wait();  // the shares' results
   const int2 cut = p.cut[part * gridDim.x + blockIdx.x];
   if (cut.x >= 0) join_cut<TQ, kD>(p, cut);
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    if ((row == blockIdx.x ? count : list_length(p, row)) > 0) continue;
-    const Unit u = find_unit(p, row, part == 0 && threadIdx.x == 0);
-    if (u.count < 0) continue;
-    const int heads = min(p.group - part * p.head_rows, p.head_rows);
-    TQ* out = static_cast<TQ*>(p.out) +
-              (u.t * p.num_q_heads + u.h * p.group + part * p.head_rows) * kD;
-    for (int i = threadIdx.x; i < heads * kD; i += kJoinThreads) out[i] = from_f32<TQ>(0.f);
+  for (int64_t first = 0; blockIdx.x + first * step < rows; first += kJoinThreads) {
+    const int64_t mine = first + threadIdx.x;
+    unsigned todo = __ballot_sync(~0u, first == 0 ? here : empty(blockIdx.x + mine * step));
+    for (; todo != 0; todo &= todo - 1) {
+      const int64_t row = blockIdx.x + (mine - lane + __ffs(todo) - 1) * step;
+      const Unit u = find_unit(p, row, part == 0 && lane == 0);
+      if (u.count < 0) continue;
+      const int heads = min(p.group - part * p.head_rows, p.head_rows);
+      TQ* out = static_cast<TQ*>(p.out) +
+                (u.t * p.num_q_heads + u.h * p.group + part * p.head_rows) * kD;
+      for (int i = lane; i < heads * kD; i += 32) out[i] = from_f32<TQ>(0.f);
+    }
   }
 }
 

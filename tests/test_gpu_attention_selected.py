@@ -269,3 +269,41 @@ def test_a_nan_key_makes_its_heads_nan(dtype):
     nan = out.isnan().all(-1).cpu()
     assert nan.tolist() == [[False, False, True, True]] * 2 + [[False] * 4]
     assert out[~nan.cuda()].isfinite().all()
+
+
+def test_many_rows_with_and_without_lists():
+    """More rows than the joining CTAs have threads' worth of in one look, most of
+    them empty, some of broken counts; rows of no request behind them."""
+    T, Hkv, pad = 20000, 8, 9
+    lens, n = T + 40, T
+    blocks = -(-lens // 16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator("cuda").manual_seed(3)
+    kc = torch.randn(blocks, Hkv, 16, 64, generator=g, device="cuda").bfloat16()
+    vc = torch.randn(blocks, Hkv, 16, 64, generator=g, device="cuda").bfloat16()
+    q = torch.randn(T + pad, Hkv, 64, generator=g, device="cuda").bfloat16()
+    table = torch.randperm(blocks, generator=g, device="cuda").int()[None].contiguous()
+    sel = torch.zeros(T + pad, Hkv, 1, **i32)
+    cnt = (torch.arange((T + pad) * Hkv, **i32).view(T + pad, Hkv) % 7 == 0).int()
+    cnt[T:] = 0
+    out = torch.full_like(q, 7)
+    args = (table, torch.tensor([lens], **i32), torch.tensor([0, n], **i32), n, lens)
+    pa.pa_attention_selected(q, kc, vc, *args, 0.1, sel, cnt, out=out)
+    assert pa.pa_get_device_error() == 0
+    assert (out[T:] == 7).all()
+    assert (out[:T][cnt[:T] == 0] == 0).all()
+    # block 0 alone, whose 16 keys every one of these tokens sees
+    k0, v0 = (c[table[0, 0].long()].double() for c in (kc, vc))
+    x = torch.einsum("thd,hjd->thj", q[:T].double(), k0) * float(np.float32(0.1))
+    p = torch.softmax(x, -1)
+    want = torch.einsum("thj,hjd->thd", p, v0)
+    mag = torch.einsum("thj,hjd->thd", p, v0.abs())
+    qk = torch.einsum("thd,hjd->thj", q[:T].double().abs(), k0.abs()).amax(-1, True) * 0.1
+    tol = torch.from_numpy(ref.attend_tolerance(
+        want.cpu().numpy(), mag.cpu().numpy(), qk.cpu().numpy(), "bf16", "bf16")).cuda()
+    on = cnt[:T] == 1
+    assert ((out[:T].double() - want).abs() <= tol)[on].all()
+    cnt[5, 3], cnt[19000, 1] = 2, -3  # of one entry at most: no list, and a flag
+    pa.pa_attention_selected(q, kc, vc, *args, 0.1, sel, cnt, out=out)
+    assert pa.pa_get_device_error() == pa.PA_DEV_ERR_METADATA
+    assert (out[5, 3] == 0).all() and (out[19000, 1] == 0).all()

@@ -134,6 +134,12 @@ def test_attention_selected_refuses(lib, change, status):
     assert call(lib, "pa_attention_selected", ATTEND, **change) == status
 
 
+def test_attention_selected_limits(lib):
+    """Sizes whose counts the kernels hold in 31 bits are refused beyond them."""
+    assert call(lib, "pa_attention_selected", ATTEND, max_selected=(1 << 24) + 1) == 2
+    assert call(lib, "pa_attention_selected", ATTEND, num_tokens=1 << 30) == 2
+
+
 def test_nothing_to_do_is_no_error(lib):
     """No requests, tokens or keys: PA_OK, and no buffer is looked at."""
     none = dict.fromkeys(("block_tables", "seq_lens", "qsl"))
