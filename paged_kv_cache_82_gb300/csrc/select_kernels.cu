@@ -394,8 +394,8 @@ struct ScoreLayout {
   static constexpr int kSmem = kScoreWarps * kWarp;
 };
 
-// One CTA: one token, p.chunk cache blocks, all KV heads.  A warp takes one
-// KV head (the heads' records of a block are one contiguous range, read by the
+// One CTA: one token, p.chunk cache blocks, up to eight KV heads.  A warp takes
+// one head (the heads' records of a block are one contiguous range, read by the
 // CTA's warps at about the same time); with fewer heads than warps, several
 // warps share a head's blocks.
 //
@@ -424,10 +424,13 @@ score_kernel(const ScoreParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = p.t0 + blockIdx.y;
   const int first = (int)blockIdx.x * p.chunk;
-  const int sharing = max(1, kScoreWarps / p.num_kv_heads);  // warps of one head
+  const int head0 = blockIdx.z * kScoreWarps;
+  const int num_heads = min(kScoreWarps, p.num_kv_heads - head0);  // of the CTA
+  const int sharing = kScoreWarps / num_heads;                     // warps of one head
   const TokenView tv = token_view(p.s, t, false);
   if (tv.blocks <= p.max_selected || first >= tv.blocks) return;  // all of them
-  if (warp >= sharing * p.num_kv_heads) return;
+  if (warp >= sharing * num_heads) return;
+  const int h = head0 + warp % num_heads;
   const int last = min(first + p.chunk, tv.blocks);
   const int kept_last = tv.blocks - p.keep_last;
   const int32_t* table = p.s.block_tables + (int64_t)tv.r * p.s.max_blocks_per_seq;
@@ -440,134 +443,132 @@ score_kernel(const ScoreParams p) {
   const uint32_t code_at = lane / kCodePieces * Ly::kRec + code_off;
   const int passes = (p.group + kG - 1) / kG;
   const int stride = sharing * kScoreGroup;
-  const int b_first = first + (warp / p.num_kv_heads) * kScoreGroup;
-  for (int h = warp % p.num_kv_heads; h < p.num_kv_heads; h += kScoreWarps) {
-    const uint8_t* head_bounds = p.bounds + (int64_t)h * Ly::kRec;
-    const int64_t block_bytes = (int64_t)p.num_kv_heads * Ly::kRec;
-    // the physical block of block b; -1: kept (not read), none, or out of range
-    auto block_id = [&](int b) {
-      if (b >= last || b < p.keep_first || b >= kept_last) return -1;
-      const int id = __ldg(table + b);
-      if (id >= 0 && (int64_t)id < p.s.num_blocks) return id;
-      flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
-      return -1;
-    };
-    // Copies of the 16 records from block b on: kCodeRecs records' codes at a
-    // time, then their scales.  A block that is not read has block 0's.
-    auto stage = [&](int b, int buf) {
-      int id = -1;
-      if (b >= last) {
-        copy_commit();
-        return id;
-      }
-      id = block_id(b + mine);
-      const int from = max(id, 0);
-      const uint32_t dst = bufs_at + buf * Ly::kBuf;
-#pragma unroll
-      for (int k = 0; k < kScoreGroup; k += kCodeRecs)
-        copy16_async(dst + code_at + k * Ly::kRec,
-                     head_bounds + code_off +
-                         __shfl_sync(~0u, from, k + lane / kCodePieces) * block_bytes);
-      if (lane < kScoreGroup)
-        copy16_async(dst + lane * Ly::kRec + 2 * kD, head_bounds + 2 * kD + from * block_bytes);
+  const int b_first = first + (warp / num_heads) * kScoreGroup;
+  const uint8_t* head_bounds = p.bounds + (int64_t)h * Ly::kRec;
+  const int64_t block_bytes = (int64_t)p.num_kv_heads * Ly::kRec;
+  // the physical block of block b; -1: kept (not read), none, or out of range
+  auto block_id = [&](int b) {
+    if (b >= last || b < p.keep_first || b >= kept_last) return -1;
+    const int id = __ldg(table + b);
+    if (id >= 0 && (int64_t)id < p.s.num_blocks) return id;
+    flag_error(p.s.err, PA_DEV_ERR_BLOCK_ID);
+    return -1;
+  };
+  // Copies of the 16 records from block b on: kCodeRecs records' codes at a
+  // time, then their scales.  A block that is not read has block 0's.
+  auto stage = [&](int b, int buf) {
+    int id = -1;
+    if (b >= last) {
       copy_commit();
       return id;
-    };
-    int ids[kScoreBufs];
+    }
+    id = block_id(b + mine);
+    const int from = max(id, 0);
+    const uint32_t dst = bufs_at + buf * Ly::kBuf;
 #pragma unroll
-    for (int k = 0; k < kScoreBufs - 1; ++k) ids[k] = stage(b_first + k * stride, k);
+    for (int k = 0; k < kScoreGroup; k += kCodeRecs)
+      copy16_async(dst + code_at + k * Ly::kRec,
+                   head_bounds + code_off +
+                       __shfl_sync(~0u, from, k + lane / kCodePieces) * block_bytes);
+    if (lane < kScoreGroup)
+      copy16_async(dst + lane * Ly::kRec + 2 * kD, head_bounds + 2 * kD + from * block_bytes);
+    copy_commit();
+    return id;
+  };
+  int ids[kScoreBufs];
+#pragma unroll
+  for (int k = 0; k < kScoreBufs - 1; ++k) ids[k] = stage(b_first + k * stride, k);
 
-    const TQ* qp = static_cast<const TQ*>(p.q) +
-                   (t * p.num_q_heads + (int64_t)h * p.group) * kD;
-    // one scale for all heads of the group: each part of the warp looks at some
-    const int sub = lane % kLanes, part = lane / kLanes;
-    float x[16], big = 0.f;
-    for (int g = part; g < p.group; g += kParts) {
-      load16(qp + g * kD + sub * 16, x);
+  const TQ* qp = static_cast<const TQ*>(p.q) +
+                 (t * p.num_q_heads + (int64_t)h * p.group) * kD;
+  // one scale for all heads of the group: each part of the warp looks at some
+  const int sub = lane % kLanes, part = lane / kLanes;
+  float x[16], big = 0.f;
+  for (int g = part; g < p.group; g += kParts) {
+    load16(qp + g * kD + sub * 16, x);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(x[i]));
+    for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(x[i]));
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
+  const float sq = __fdiv_rn(big, 127.0f);
+  uint32_t* keys = p.keys + ((int64_t)blockIdx.y * p.num_kv_heads + h) * p.row_scores;
+  for (int pass = 0; pass < passes; ++pass) {
+    if (pass > 0) {
+#pragma unroll
+      for (int k = 0; k < kScoreBufs - 1; ++k) ids[k] = stage(b_first + k * stride, k);
     }
+    // codes of the pass's heads (past the group's end: its last head again)
+    __syncwarp();
+    for (int g = part; g < kG; g += kParts) {
+      load16(qp + (int64_t)min(pass * kG + g, p.group - 1) * kD + sub * 16, x);
+      uint32_t c4[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
-    const float sq = __fdiv_rn(big, 127.0f);
-    uint32_t* keys = p.keys + ((int64_t)blockIdx.y * p.num_kv_heads + h) * p.row_scores;
-    for (int pass = 0; pass < passes; ++pass) {
-      if (pass > 0) {
-#pragma unroll
-        for (int k = 0; k < kScoreBufs - 1; ++k) ids[k] = stage(b_first + k * stride, k);
+      for (int i = 0; i < 16; ++i) {
+        int c = sq > 0.f ? __float2int_rn(__fdiv_rn(x[i], sq)) : 0;
+        c = min(127, max(-127, c));
+        c4[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
       }
-      // codes of the pass's heads (past the group's end: its last head again)
-      __syncwarp();
-      for (int g = part; g < kG; g += kParts) {
-        load16(qp + (int64_t)min(pass * kG + g, p.group - 1) * kD + sub * 16, x);
-        uint32_t c4[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          int c = sq > 0.f ? __float2int_rn(__fdiv_rn(x[i], sq)) : 0;
-          c = min(127, max(-127, c));
-          c4[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
-        }
-        *reinterpret_cast<uint4*>(codes + g * kD + sub * 16) =
-            make_uint4(c4[0], c4[1], c4[2], c4[3]);
-      }
-      __syncwarp();
-      int buf = 0;
-      for (int b0 = b_first; b0 < last; b0 += stride) {
-        const int id = ids[0];
-#pragma unroll
-        for (int k = 0; k + 1 < kScoreBufs; ++k) ids[k] = ids[k + 1];
-        {
-          const int to = buf + kScoreBufs - 1;
-          ids[kScoreBufs - 2] = stage(b0 + (kScoreBufs - 1) * stride,
-                                      to >= kScoreBufs ? to - kScoreBufs : to);
-        }
-        copy_wait<kScoreBufs - 1>();
-        __syncwarp();
-        const uint8_t* rec = bufs + buf * Ly::kBuf + mine * Ly::kRec;
-        const uint4* hi = reinterpret_cast<const uint4*>(rec + half * (kD / 2));
-        const uint4* lo = reinterpret_cast<const uint4*>(rec + kD + half * (kD / 2));
-        const uint4* code = reinterpret_cast<const uint4*>(codes + half * (kD / 2));
-        int dot[kG];
-#pragma unroll
-        for (int g = 0; g < kG; ++g) dot[g] = 0;
-#pragma unroll
-        for (int w = 0; w < kD / 32; ++w) {
-          const uint4 a = hi[w], c = lo[w];
-#pragma unroll
-          for (int g = 0; g < kG; ++g) {
-            const uint4 q = code[g * (kD / 16) + w];
-            dot[g] = bound_dot(a.x, c.x, q.x, dot[g]);
-            dot[g] = bound_dot(a.y, c.y, q.y, dot[g]);
-            dot[g] = bound_dot(a.z, c.z, q.z, dot[g]);
-            dot[g] = bound_dot(a.w, c.w, q.w, dot[g]);
-          }
-        }
-        const float sc = *reinterpret_cast<const float*>(rec + 2 * kD);
-        __syncwarp();  // the buffer may be copied into again
-        int best = INT_MIN;
-#pragma unroll
-        for (int g = 0; g < kG; ++g)
-          best = max(best, dot[g] + __shfl_xor_sync(~0u, dot[g], 16));
-        const int b = b0 + mine;
-        if (half == 0 && b < last) {
-          uint32_t key;
-          if (b < p.keep_first || b >= kept_last) {
-            key = kKeptKey;
-          } else if (id < 0) {
-            key = score_key(-INFINITY);
-          } else {
-            if (pass > 0) best = max(best, (int)keys[b]);
-            // + 0: a zero is a positive zero
-            key = pass + 1 < passes ? (uint32_t)best
-                                    : score_key(__fmul_rn((float)best, sc) + 0.0f);
-          }
-          keys[b] = key;
-        }
-        buf = buf + 1 == kScoreBufs ? 0 : buf + 1;
-      }
-      copy_wait<0>();
-      __syncwarp();
+      *reinterpret_cast<uint4*>(codes + g * kD + sub * 16) =
+          make_uint4(c4[0], c4[1], c4[2], c4[3]);
     }
+    __syncwarp();
+    int buf = 0;
+    for (int b0 = b_first; b0 < last; b0 += stride) {
+      const int id = ids[0];
+#pragma unroll
+      for (int k = 0; k + 1 < kScoreBufs; ++k) ids[k] = ids[k + 1];
+      {
+        const int to = buf + kScoreBufs - 1;
+        ids[kScoreBufs - 2] = stage(b0 + (kScoreBufs - 1) * stride,
+                                    to >= kScoreBufs ? to - kScoreBufs : to);
+      }
+      copy_wait<kScoreBufs - 1>();
+      __syncwarp();
+      const uint8_t* rec = bufs + buf * Ly::kBuf + mine * Ly::kRec;
+      const uint4* hi = reinterpret_cast<const uint4*>(rec + half * (kD / 2));
+      const uint4* lo = reinterpret_cast<const uint4*>(rec + kD + half * (kD / 2));
+      const uint4* code = reinterpret_cast<const uint4*>(codes + half * (kD / 2));
+      int dot[kG];
+#pragma unroll
+      for (int g = 0; g < kG; ++g) dot[g] = 0;
+#pragma unroll
+      for (int w = 0; w < kD / 32; ++w) {
+        const uint4 a = hi[w], c = lo[w];
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          const uint4 q = code[g * (kD / 16) + w];
+          dot[g] = bound_dot(a.x, c.x, q.x, dot[g]);
+          dot[g] = bound_dot(a.y, c.y, q.y, dot[g]);
+          dot[g] = bound_dot(a.z, c.z, q.z, dot[g]);
+          dot[g] = bound_dot(a.w, c.w, q.w, dot[g]);
+        }
+      }
+      const float sc = *reinterpret_cast<const float*>(rec + 2 * kD);
+      __syncwarp();  // the buffer may be copied into again
+      int best = INT_MIN;
+#pragma unroll
+      for (int g = 0; g < kG; ++g)
+        best = max(best, dot[g] + __shfl_xor_sync(~0u, dot[g], 16));
+      const int b = b0 + mine;
+      if (half == 0 && b < last) {
+        uint32_t key;
+        if (b < p.keep_first || b >= kept_last) {
+          key = kKeptKey;
+        } else if (id < 0) {
+          key = score_key(-INFINITY);
+        } else {
+          if (pass > 0) best = max(best, (int)keys[b]);
+          // + 0: a zero is a positive zero
+          key = pass + 1 < passes ? (uint32_t)best
+                                  : score_key(__fmul_rn((float)best, sc) + 0.0f);
+        }
+        keys[b] = key;
+      }
+      buf = buf + 1 == kScoreBufs ? 0 : buf + 1;
+    }
+    copy_wait<0>();
+    __syncwarp();
   }
 }
 
@@ -856,11 +857,14 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
       p.keys = static_cast<uint32_t*>(workspace);
       // as many blocks per CTA as leave four CTAs per SM: a warp's work on the
       // query (its codes) is then spread over more records
+      const int64_t heads = (num_kv_heads + kScoreWarps - 1) / kScoreWarps;
+      if (heads > 65535) return cudaErrorInvalidValue;
       p.chunk = kScoreChunkMax;
       while (p.chunk > kScoreChunkMin &&
-             nt * ((max_blocks + p.chunk - 1) / p.chunk) < 4ll * num_sms)
+             nt * heads * ((max_blocks + p.chunk - 1) / p.chunk) < 4ll * num_sms)
         p.chunk /= 2;
-      const dim3 grid((unsigned)((max_blocks + p.chunk - 1) / p.chunk), (unsigned)nt);
+      const dim3 grid((unsigned)((max_blocks + p.chunk - 1) / p.chunk), (unsigned)nt,
+                      (unsigned)heads);
       cudaError_t e;
       switch (q_dtype) {
         case PA_F32: e = launch_score<float>(p, head_dim, grid, stream); break;
