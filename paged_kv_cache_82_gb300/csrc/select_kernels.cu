@@ -893,14 +893,18 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = max_blocks > max_selected ? 1 : 0;
-    // rows enough for every SM: 256 threads each (four to an SM: 512 rows of
-    // 512 to 4096 blocks 10 us, with 512 threads a quarter more); fewer: 1024, for the
-    // one row's sake
-    const bool many = nt * num_kv_heads > num_sms;
-    cfg.blockDim = dim3(many ? 256 : 1024);
+    // 256 threads to a row where there are rows enough for every SM (four to an
+    // SM: 512 rows of 512 to 4096 blocks 10 us, with 512 threads a quarter more) or
+    // few blocks (both kernels, 8 rows of 512 blocks: 8.4 us, with 1024 threads
+    // 10.0; 32 rows of 2048: 10.5 and 11.5); else 1024 (8 rows of 8192: 13.7 us,
+    // with 256 14.6).  A row's keys stay in registers up to 8192 blocks, or 16384
+    // by 1024 threads (8 rows of those: 23.2 us, read again each time 27.2).
+    const bool narrow = nt * num_kv_heads > num_sms || max_blocks <= 16 * 256;
+    cfg.blockDim = dim3(narrow ? 256 : 1024);
     const cudaError_t e =
-        !many ? (max_blocks <= 8 * 1024 ? cudaLaunchKernelEx(&cfg, topk_kernel<1024, 8>, tp)
-                                        : cudaLaunchKernelEx(&cfg, topk_kernel<1024, 0>, tp))
+        !narrow ? (max_blocks <= 8 * 1024    ? cudaLaunchKernelEx(&cfg, topk_kernel<1024, 8>, tp)
+                   : max_blocks <= 16 * 1024 ? cudaLaunchKernelEx(&cfg, topk_kernel<1024, 16>, tp)
+                                             : cudaLaunchKernelEx(&cfg, topk_kernel<1024, 0>, tp))
         : max_blocks <= 4 * 256  ? cudaLaunchKernelEx(&cfg, topk_kernel<256, 4>, tp)
         : max_blocks <= 16 * 256 ? cudaLaunchKernelEx(&cfg, topk_kernel<256, 16>, tp)
         : max_blocks <= 32 * 256 ? cudaLaunchKernelEx(&cfg, topk_kernel<256, 32>, tp)

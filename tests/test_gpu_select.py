@@ -257,6 +257,26 @@ def test_records_of_any_bytes(L):
             assert sel[0, h].tolist() == sorted([0, n - 1] + mid)
 
 
+@pytest.mark.parametrize("T", [3, 20])
+def test_lists_do_not_depend_on_the_longest_length_named(T):
+    """max_seq_len chooses how a row's keys are held (registers of 256 or 1024
+    threads, or read again); 24 rows and 160 of them, the same lists."""
+    lens = [(15000 - 100 * i, 1) for i in range(T)]
+    wl, md, dev = step(lens, 16, 8, 64)
+    bounds = _random_bounds(wl.k_cache.shape[0], 8, 64, T, ties=True)
+    hi, lo, sc = ref.records(bounds, 64)
+    want = ref.select(wl.q.float().numpy(), hi, lo, sc, md, 2, 40, 1, 2)
+    for blocks in (938, 1024, 1025, 4096, 4097, 8192, 8193, 16384, 16385, 20001):
+        table = torch.zeros(T, blocks, dtype=torch.int32, device="cuda")
+        table[:, :938] = dev["block_tables"][:, :938]
+        sel, cnt = pa.pa_select_blocks(wl.q.cuda(), bounds, table, dev["seq_lens"],
+                                       dev["query_start_loc"], 1, 16 * blocks, 40, 1, 2)
+        assert pa.pa_get_device_error() == 0
+        sel = sel.cpu()
+        for (t, h), b in want.items():
+            assert sel[t, h].tolist() == b, (blocks, t, h)
+
+
 def test_passes_over_the_step_do_not_change_the_result():
     """A step whose scores exceed the workspace's bound runs in passes."""
     lens = [(16384, 64)] * 4 + [(20000, 1)] * 3
