@@ -412,7 +412,7 @@ struct ScoreLayout {
 // rows' blocks on resident CTAs (each token's start then costs as much) made it
 // shorter.
 template <typename TQ, int kD, int kG>
-__global__ void __launch_bounds__(kScoreWarps * 32, kG == 8 ? 2 : kScoreCtas)
+__global__ void __launch_bounds__(kScoreWarps * 32, kG > 4 ? 2 : kScoreCtas)
 score_kernel(const ScoreParams p) {
   using Ly = ScoreLayout<kD, kG>;
   constexpr int kLanes = kD / 16;        // lanes of one query head's codes
@@ -783,10 +783,14 @@ cudaError_t launch_score_g(const ScoreParams& p, dim3 grid, cudaStream_t stream)
 
 template <typename TQ, int kD>
 cudaError_t launch_score_d(const ScoreParams& p, dim3 grid, cudaStream_t stream) {
-  // query heads held at once: the group's, up to 8 (more: in passes)
-  if (p.group == 1) return launch_score_g<TQ, kD, 1>(p, grid, stream);
-  if (p.group == 2) return launch_score_g<TQ, kD, 2>(p, grid, stream);
-  if (p.group <= 4) return launch_score_g<TQ, kD, 4>(p, grid, stream);
+  // query heads held at once: the group's, up to 8; more in equal passes
+  const int passes = (p.group + 7) / 8, heads = (p.group + passes - 1) / passes;
+  if (heads == 1) return launch_score_g<TQ, kD, 1>(p, grid, stream);
+  if (heads == 2) return launch_score_g<TQ, kD, 2>(p, grid, stream);
+  if (heads <= 4) return launch_score_g<TQ, kD, 4>(p, grid, stream);
+#ifndef NO6
+  if (heads <= 6) return launch_score_g<TQ, kD, 6>(p, grid, stream);
+#endif
   return launch_score_g<TQ, kD, 8>(p, grid, stream);
 }
 
