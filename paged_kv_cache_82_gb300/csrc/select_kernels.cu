@@ -343,23 +343,34 @@ __device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
   return d;
 }
 
-// four channels of a bound: the products of the codes with hi where they are
-// positive, lo where they are negative
-__device__ __forceinline__ int bound_dot(uint32_t hi, uint32_t lo, uint32_t codes, int sum) {
-  const uint32_t neg = sign_bytes(codes);
-  return __dp4a((int)((hi & ~neg) | (lo & neg)), (int)codes, sum);
+// d += a b: 16 rows (records) x 32 codes, times 32 codes x 8 columns (heads), in
+// whole numbers
+__device__ __forceinline__ void mma_codes(int (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four 8 x 8 matrices of 16-bit pairs: their rows' addresses in lanes 0-7, 8-15, ..
+__device__ __forceinline__ void load_matrices(uint32_t (&a)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(at)
+               : "memory");
 }
 
-// 16 consecutive elements as fp32 (16-byte aligned)
+// 4 consecutive elements as fp32 (aligned to as much)
 template <typename T>
-__device__ __forceinline__ void load16(const T* src, float (&x)[16]) {
-  constexpr int kV = 16 / sizeof(T);
-#pragma unroll
-  for (int i = 0; i < 16 / kV; ++i) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+__device__ __forceinline__ void load4(const T* src, float* x) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(src));
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  } else {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
     const T* e = reinterpret_cast<const T*>(&u);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) x[i * kV + j] = to_f32(e[j]);
+    for (int j = 0; j < 4; ++j) x[j] = to_f32(e[j]);
   }
 }
 
@@ -385,12 +396,13 @@ constexpr int kScoreCtas = 3;
 // 16.
 constexpr int kScoreChunkMax = 128, kScoreChunkMin = 32;
 
-template <int kD, int kG>
+constexpr int kScoreHeads = 8;   // query heads scored at a time
+
+template <int kD>
 struct ScoreLayout {
   static constexpr int kRec = PA_BOUNDS_BYTES(kD);
-  static constexpr int kBuf = kScoreGroup * kRec;         // bytes
-  static constexpr int kCodes = kG * kD;
-  static constexpr int kWarp = kScoreBufs * kBuf + kCodes;
+  static constexpr int kBuf = kScoreGroup * kRec;  // bytes
+  static constexpr int kWarp = kScoreBufs * kBuf;
   static constexpr int kSmem = kScoreWarps * kWarp;
 };
 
@@ -401,22 +413,30 @@ struct ScoreLayout {
 //
 // Each warp copies 16 records at a time into shared memory of its own, the
 // next ones while it scores these, so that what is on its way does not wait
-// for registers.  Two lanes score a record, half of its channels each; a
-// record's 17 (or 9) words of 16 bytes put the 8 lanes of a quarter warp into
-// different banks.  The codes of kG query heads lie in shared memory too: their
-// signs pick the product's bound in two logic operations per word, and a word's
-// four products are one dp4a.  64 tokens of 8K to 64K, 32 / 8 heads of 128: 48 us for
-// 232 MB: 6.3 TB/s while it streams, after 4 to 5 us for the first records and
-// codes, and before a ragged end.  Neither fewer instructions (a fifth, in the
-// copies and the query's codes), nor a third buffer, nor equal shares of all
-// rows' blocks on resident CTAs (each token's start then costs as much) made it
-// shorter.
-template <typename TQ, int kD, int kG>
-__global__ void __launch_bounds__(kScoreWarps * 32, kG > 4 ? 2 : kScoreCtas)
+// for registers.  The sum over the channels of a code times the bound of its
+// side is a product of 2 kD columns: the records' hi codes times the positive
+// codes of the query, and their lo codes times the negative ones (0 elsewhere).
+// 16 records by 8 query heads by 32 codes are one integer MMA, whose operands a
+// record's row and the codes in a lane's registers are; a record's 17 (or 9)
+// words of 16 bytes put eight rows into different banks.  GB300's integer MMAs are
+// slow beside its others, and still quicker than the same sums by dp4a with the
+// bound picked by the code's sign: 64 tokens of 8K to 64K, both kernels, 8 query
+// heads per KV head 63 us (dp4a 83), 5 heads 41 (51), 12 heads 34 (41), 4 heads 59
+// (60).
+//
+// The last one's 232 MB take 48 us of it: 6.3 TB/s while it streams, after 4 to 5
+// us for the first records and codes, and before a ragged end.  Neither a third
+// buffer nor equal shares of all rows' blocks on resident CTAs (each token's start
+// then costs as much) made it shorter.
+//
+// kFew: up to four query heads, which are columns 0-3 and once more 4-7; the two
+// lanes of a head's channels then code half of them each.
+template <typename TQ, int kD, bool kFew>
+__global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas)
 score_kernel(const ScoreParams p) {
-  using Ly = ScoreLayout<kD, kG>;
-  constexpr int kLanes = kD / 16;        // lanes of one query head's codes
-  constexpr int kParts = 32 / kLanes;    // heads coded at a time
+  using Ly = ScoreLayout<kD>;
+  constexpr int kSteps = kD / 32;                     // MMAs of a side
+  constexpr int kCoded = kFew ? kSteps : 2 * kSteps;  // words of codes a lane makes
   constexpr int kCodePieces = kD / 8;             // 16-byte pieces of a record's codes
   constexpr int kCodeRecs = 32 / kCodePieces;
   extern __shared__ __align__(16) uint8_t score_smem[];
@@ -435,13 +455,13 @@ score_kernel(const ScoreParams p) {
   const int kept_last = tv.blocks - p.keep_last;
   const int32_t* table = p.s.block_tables + (int64_t)tv.r * p.s.max_blocks_per_seq;
   uint8_t* bufs = score_smem + warp * Ly::kWarp;
-  uint8_t* codes = bufs + kScoreBufs * Ly::kBuf;
   const uint32_t bufs_at = smem_u32(bufs);
-  // this lane's record and half of the channels
-  const int mine = lane & 15, half = lane >> 4;
+  // this lane's record, and its row of the four matrices of an operand
+  const int mine = lane & 15;
+  const uint32_t row_at = mine * Ly::kRec + (lane >> 4) * 16;
   const int code_off = lane % kCodePieces * 16;
   const uint32_t code_at = lane / kCodePieces * Ly::kRec + code_off;
-  const int passes = (p.group + kG - 1) / kG;
+  const int passes = (p.group + kScoreHeads - 1) / kScoreHeads;
   const int stride = sharing * kScoreGroup;
   const int b_first = first + (warp / num_heads) * kScoreGroup;
   const uint8_t* head_bounds = p.bounds + (int64_t)h * Ly::kRec;
@@ -481,38 +501,64 @@ score_kernel(const ScoreParams p) {
 
   const TQ* qp = static_cast<const TQ*>(p.q) +
                  (t * p.num_q_heads + (int64_t)h * p.group) * kD;
-  // one scale for all heads of the group: each part of the warp looks at some
-  const int sub = lane % kLanes, part = lane / kLanes;
-  float x[16], big = 0.f;
-  for (int g = part; g < p.group; g += kParts) {
-    load16(qp + g * kD + sub * 16, x);
+  // this lane's head of a pass (past the group's end: its last head again), and
+  // its channels: 4 from 32 j + 4 column and from 16 further on
+  const int column = lane & 3, head = kFew ? lane >> 2 & 3 : lane >> 2;
+  const int coded = kFew ? lane / 16 * kCoded : 0;  // the first of the words
+  auto load_query = [&](int pass, float (&x)[4 * kCoded]) {
+    const TQ* src = qp + (int64_t)min(pass * kScoreHeads + head, p.group - 1) * kD +
+                    4 * column + 16 * coded;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(x[i]));
+    for (int i = 0; i < kCoded; ++i) load4(src + 16 * i, x + 4 * i);
+  };
+  // one scale for all heads of the group
+  float x[4 * kCoded], big = 0.f;
+  for (int pass = passes - 1; pass >= 0; --pass) {
+    load_query(pass, x);
+#pragma unroll
+    for (int i = 0; i < 4 * kCoded; ++i) big = fmaxf(big, fabsf(x[i]));
   }
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
   const float sq = __fdiv_rn(big, 127.0f);
+  const Divisor by(sq);
   uint32_t* keys = p.keys + ((int64_t)blockIdx.y * p.num_kv_heads + h) * p.row_scores;
   for (int pass = 0; pass < passes; ++pass) {
     if (pass > 0) {
 #pragma unroll
       for (int k = 0; k < kScoreBufs - 1; ++k) ids[k] = stage(b_first + k * stride, k);
     }
-    // codes of the pass's heads (past the group's end: its last head again)
-    __syncwarp();
-    for (int g = part; g < kG; g += kParts) {
-      load16(qp + (int64_t)min(pass * kG + g, p.group - 1) * kD + sub * 16, x);
-      uint32_t c4[4] = {0, 0, 0, 0};
+    // the codes of the lane's head: positive ones, negative ones
+    uint32_t up[2 * kSteps], down[2 * kSteps];
+    if (pass > 0) load_query(pass, x);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        int c = sq > 0.f ? __float2int_rn(__fdiv_rn(x[i], sq)) : 0;
+    for (int w = 0; w < kCoded; ++w) {
+      const float x4[4] = {x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3]};
+      float y[4];
+      divide(x4, by, y);
+      uint32_t c4 = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int c = sq > 0.f ? __float2int_rn(y[i]) : 0;
         c = min(127, max(-127, c));
-        c4[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+        c4 |= ((uint32_t)c & 0xFFu) << (8 * i);
       }
-      *reinterpret_cast<uint4*>(codes + g * kD + sub * 16) =
-          make_uint4(c4[0], c4[1], c4[2], c4[3]);
+      up[w] = c4;
     }
-    __syncwarp();
+    if constexpr (kFew) {
+#pragma unroll
+      for (int w = 0; w < kCoded; ++w) {
+        const uint32_t other = __shfl_xor_sync(~0u, up[w], 16);
+        up[w + kCoded] = coded ? up[w] : other;
+        up[w] = coded ? other : up[w];
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 2 * kSteps; ++w) {
+      const uint32_t neg = sign_bytes(up[w]);
+      down[w] = up[w] & neg;
+      up[w] &= ~neg;
+    }
     int buf = 0;
     for (int b0 = b_first; b0 < last; b0 += stride) {
       const int id = ids[0];
@@ -525,33 +571,31 @@ score_kernel(const ScoreParams p) {
       }
       copy_wait<kScoreBufs - 1>();
       __syncwarp();
-      const uint8_t* rec = bufs + buf * Ly::kBuf + mine * Ly::kRec;
-      const uint4* hi = reinterpret_cast<const uint4*>(rec + half * (kD / 2));
-      const uint4* lo = reinterpret_cast<const uint4*>(rec + kD + half * (kD / 2));
-      const uint4* code = reinterpret_cast<const uint4*>(codes + half * (kD / 2));
-      int dot[kG];
+      const uint32_t rows = bufs_at + buf * Ly::kBuf + row_at;
+      int hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int g = 0; g < kG; ++g) dot[g] = 0;
-#pragma unroll
-      for (int w = 0; w < kD / 32; ++w) {
-        const uint4 a = hi[w], c = lo[w];
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          const uint4 q = code[g * (kD / 16) + w];
-          dot[g] = bound_dot(a.x, c.x, q.x, dot[g]);
-          dot[g] = bound_dot(a.y, c.y, q.y, dot[g]);
-          dot[g] = bound_dot(a.z, c.z, q.z, dot[g]);
-          dot[g] = bound_dot(a.w, c.w, q.w, dot[g]);
-        }
+      for (int j = 0; j < kSteps; ++j) {
+        uint32_t a[4];
+        load_matrices(a, rows + 32 * j);
+        mma_codes(hi, a, up[2 * j], up[2 * j + 1]);
+        load_matrices(a, rows + kD + 32 * j);
+        mma_codes(lo, a, down[2 * j], down[2 * j + 1]);
       }
-      const float sc = *reinterpret_cast<const float*>(rec + 2 * kD);
+      const float sc =
+          *reinterpret_cast<const float*>(bufs + buf * Ly::kBuf + mine * Ly::kRec + 2 * kD);
       __syncwarp();  // the buffer may be copied into again
-      int best = INT_MIN;
+      // rows lane / 4 and that + 8, heads 2 column and that + 1
+      int top = max(hi[0] + lo[0], hi[1] + lo[1]), low = max(hi[2] + lo[2], hi[3] + lo[3]);
 #pragma unroll
-      for (int g = 0; g < kG; ++g)
-        best = max(best, dot[g] + __shfl_xor_sync(~0u, dot[g], 16));
+      for (int d = 1; d < 4; d <<= 1) {
+        top = max(top, __shfl_xor_sync(~0u, top, d));
+        low = max(low, __shfl_xor_sync(~0u, low, d));
+      }
+      top = __shfl_sync(~0u, top, (lane & 7) * 4);
+      low = __shfl_sync(~0u, low, (lane & 7) * 4);
+      int best = lane & 8 ? low : top;
       const int b = b0 + mine;
-      if (half == 0 && b < last) {
+      if (lane < kScoreGroup && b < last) {
         uint32_t key;
         if (b < p.keep_first || b >= kept_last) {
           key = kKeptKey;
@@ -769,13 +813,13 @@ cudaError_t launch_summarise_t(const StepView& s, const void* k_cache, int num_k
              : launch_summarise_d<kPg, 64>(s, k_cache, num_kv_heads, bounds, stream);
 }
 
-template <typename TQ, int kD, int kG>
+template <typename TQ, int kD, bool kFew>
 cudaError_t launch_score_g(const ScoreParams& p, dim3 grid, cudaStream_t stream) {
-  constexpr int kSmem = ScoreLayout<kD, kG>::kSmem;
+  constexpr int kSmem = ScoreLayout<kD>::kSmem;
   const cudaError_t a = cudaFuncSetAttribute(
-      score_kernel<TQ, kD, kG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      score_kernel<TQ, kD, kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (a != cudaSuccess) return a;
-  score_kernel<TQ, kD, kG><<<grid, kScoreWarps * 32, kSmem, stream>>>(p);
+  score_kernel<TQ, kD, kFew><<<grid, kScoreWarps * 32, kSmem, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
@@ -783,15 +827,8 @@ cudaError_t launch_score_g(const ScoreParams& p, dim3 grid, cudaStream_t stream)
 
 template <typename TQ, int kD>
 cudaError_t launch_score_d(const ScoreParams& p, dim3 grid, cudaStream_t stream) {
-  // query heads held at once: the group's, up to 8; more in equal passes
-  const int passes = (p.group + 7) / 8, heads = (p.group + passes - 1) / passes;
-  if (heads == 1) return launch_score_g<TQ, kD, 1>(p, grid, stream);
-  if (heads == 2) return launch_score_g<TQ, kD, 2>(p, grid, stream);
-  if (heads <= 4) return launch_score_g<TQ, kD, 4>(p, grid, stream);
-#ifndef NO6
-  if (heads <= 6) return launch_score_g<TQ, kD, 6>(p, grid, stream);
-#endif
-  return launch_score_g<TQ, kD, 8>(p, grid, stream);
+  return p.group <= kScoreHeads / 2 ? launch_score_g<TQ, kD, true>(p, grid, stream)
+                                    : launch_score_g<TQ, kD, false>(p, grid, stream);
 }
 
 template <typename TQ>
