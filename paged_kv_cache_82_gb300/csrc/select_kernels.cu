@@ -388,14 +388,15 @@ __device__ __forceinline__ void copy_wait() {
 constexpr int kScoreWarps = 8;
 constexpr int kScoreGroup = 16;  // records a warp stages and scores at a time
 // Buffers of a warp, and CTAs per SM: 64 rows of 8 heads x 512 to 4096 blocks,
-// both kernels, 63 us with 2 and 3, 74 with 3 and 2 or with 2 and 2.
+// both kernels, 59 us with 2 and 3, 68 with 3 and 2 or with 2 and 2.
 constexpr int kScoreBufs = 2;
 constexpr int kScoreCtas = 3;
-// Blocks of one CTA: 62 us with 128, 63 with 256, 67 with 64 (each warp codes
-// its query anew); one row of 8192 blocks 14.5 us with 32, 15.6 with 64, 17 with
-// 16.
+// Blocks of one CTA with a warp to each head; as many times more where several
+// warps share one: 59 us with 128, 60 with 256, 62 with 64 (each warp codes its
+// query anew); one KV head, 29 us with 256, 34 with 128.  Where that leaves fewer
+// than four CTAs per SM, down to kScoreChunkMin: one row of 8192 blocks 13.9 us
+// with 32, 15.1 with 16 or 64.
 constexpr int kScoreChunkMax = 128, kScoreChunkMin = 32;
-
 constexpr int kScoreHeads = 8;   // query heads scored at a time
 
 template <int kD>
@@ -900,7 +901,7 @@ cudaError_t launch_select_blocks(const StepView& s, const SelectPlan& plan,
       // query (its codes) is then spread over more records
       const int64_t heads = (num_kv_heads + kScoreWarps - 1) / kScoreWarps;
       if (heads > 65535) return cudaErrorInvalidValue;
-      p.chunk = kScoreChunkMax;
+      p.chunk = kScoreChunkMax * std::max(1, kScoreWarps / num_kv_heads);
       while (p.chunk > kScoreChunkMin &&
              nt * heads * ((max_blocks + p.chunk - 1) / p.chunk) < 4ll * num_sms)
         p.chunk /= 2;
