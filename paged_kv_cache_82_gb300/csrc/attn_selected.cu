@@ -1011,8 +1011,9 @@ __device__ __forceinline__ void join_cut(const SelParams& p, int2 cut) {
       mx = top;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const float f =
-            k0 + j >= parts || ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - top);
+        // (a place past the last part: not even 0 times its sum, which may be infinite)
+        if (k0 + j >= parts) break;
+        const float f = ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - top);
         ls = fmaf(f, ml[j].y, ls);
         a.x = fmaf(f, v[j].x, a.x);
         a.y = fmaf(f, v[j].y, a.y);

@@ -6,6 +6,8 @@ import torch
 
 import paged_kv_cache_82_gb300 as pa
 from tests import _sparse_ref as ref
+from tests.test_gpu_attention_selected import PROB, _run
+from tests.test_gpu_select import step
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +54,43 @@ def test_codes_of_subnormal_keys(cache, D):
         np.testing.assert_array_equal(hi[b, 0], w[0])
         np.testing.assert_array_equal(lo[b, 0], w[1])
         assert s[b, 0] == w[2]
+
+
+def _attend(wl, md, lists, scale=None):
+    D, c = wl.head_dim, wl.cache_dtype
+    scaled = c in ("e4m3", "nvfp4")
+    return ref.attend(
+        wl.q.double().numpy(), ref.decode_pages(wl.k_cache, c, D),
+        ref.decode_pages(wl.v_cache, c, D), md, lists, wl.group,
+        wl.scale if scale is None else scale, wl.k_scale if scaled else 1.0,
+        wl.v_scale if scaled else 1.0)
+
+
+@pytest.mark.parametrize("blocks", [1, 3, 29, 2000])
+@pytest.mark.parametrize("dtype,group", [("bf16", 4), ("bf16", 16), ("f16", 4), ("f32", 4),
+                                         ("f32", 8)])
+def test_an_infinite_value_makes_its_channel_infinite(dtype, group, blocks):
+    """Wherever in the list it stands, and whether or not the shares cut the list
+    (2000 blocks: some 250 parts, no multiple of those that the join loads at a
+    time); two infinities of both signs make NaN."""
+    wl, md, dev = step([(16 * blocks, 1)], group, 1, 128, dtype)
+    lists = {(0, 0): list(range(blocks))}
+    at = md["block_tables"][0]
+    inf = float("inf")
+    wl.v_cache[at[0], 0, 3, 8] = inf
+    wl.v_cache[at[blocks - 1], 0, 15, 5] = inf
+    wl.v_cache[at[blocks - 1], 0, 7, 77] = -inf
+    wl.v_cache[at[blocks // 2], 0, 9, 101] = inf
+    wl.v_cache[at[blocks - 1], 0, 0, 101] = -inf
+    # scores so near that no probability vanishes in the product's type
+    out = _run(wl, md, dev, lists, blocks, scale=0.01).cpu()
+    assert pa.pa_get_device_error() == 0
+    assert (out[..., 5] == inf).all() and (out[..., 8] == inf).all()
+    assert (out[..., 77] == -inf).all() and out[..., 101].isnan().all()
+    rest = torch.ones(128, dtype=torch.bool)
+    rest[[5, 8, 77, 101]] = False
+    wl.v_cache[..., ~rest] = 0
+    want, mag, qk = _attend(wl, md, lists, 0.01)
+    tol = ref.attend_tolerance(want, mag, qk, dtype, PROB[dtype])
+    err = np.abs(out.double().numpy() - want)
+    assert (err <= tol)[..., rest.numpy()].all()
