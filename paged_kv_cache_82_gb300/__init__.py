@@ -219,6 +219,25 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _new(shape, dtype, device, stream, returned: bool = True) -> torch.Tensor:
+    """A tensor that a call on `stream` allocates, from that stream's memory, so
+    that neither what the memory held before nor what is put there after the
+    tensor's release meets the call's kernels.  One that is returned is known to
+    the current stream too, where the caller will use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    current = torch.cuda.current_stream()
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
 def _check(status: int, what: str) -> None:
     if status != PA_OK:
         raise PaError(status, what)
@@ -322,12 +341,11 @@ def pa_attention(q: torch.Tensor, k_cache: torch.Tensor,
                                             seq_lens, query_start_loc, out,
                                             cache_dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if workspace is None:
         nbytes = pa_attention_workspace_size(T, Hq, Hkv, D, B, max_query_len,
                                              max_seq_len)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _new(max(nbytes, 1), torch.uint8, q.device, stream, False)
     lib = _load()
     st = lib.pa_attention(
         _dev(q, "q"), _dtype_code(q), _dev(k_cache, "k_cache"),
@@ -371,12 +389,11 @@ def pa_attention_window(q: torch.Tensor, k_cache: torch.Tensor,
                                             seq_lens, query_start_loc, out,
                                             cache_dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if workspace is None:
         nbytes = pa_attention_window_workspace_size(
             T, Hq, Hkv, D, B, max_query_len, max_seq_len, sliding_window)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _new(max(nbytes, 1), torch.uint8, q.device, stream, False)
     st = _load().pa_attention_window(
         _dev(q, "q"), _dtype_code(q), _dev(k_cache, "k_cache"),
         _dev(v_cache, "v_cache"), _dtype_code(k_cache, cache_dtype), NB, bs, Hq,
@@ -419,12 +436,11 @@ def pa_attention_cascade(q: torch.Tensor, k_cache: torch.Tensor,
                                             seq_lens, query_start_loc, out,
                                             cache_dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if workspace is None:
         nbytes = pa_attention_cascade_workspace_size(
             T, Hq, Hkv, D, B, max_query_len, max_seq_len)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _new(max(nbytes, 1), torch.uint8, q.device, stream, False)
     st = _load().pa_attention_cascade(
         _dev(q, "q"), _dtype_code(q), _dev(k_cache, "k_cache"),
         _dev(v_cache, "v_cache"), _dtype_code(k_cache, cache_dtype), NB, bs, Hq,
@@ -563,15 +579,15 @@ def pa_build_step(query_lens: torch.Tensor, computed_lens: torch.Tensor,
     T = int(num_tokens)
     dev = block_tables.device
     if seq_lens is None:
-        seq_lens = torch.empty(B, dtype=_I32, device=dev)
+        seq_lens = _new(B, _I32, dev, stream)
     if query_start_loc is None:
-        query_start_loc = torch.empty(B + 1, dtype=_I32, device=dev)
+        query_start_loc = _new(B + 1, _I32, dev, stream)
     if positions is None:
-        positions = torch.empty(T, dtype=_I32, device=dev)
+        positions = _new(T, _I32, dev, stream)
     if slot_mapping is None:
-        slot_mapping = torch.empty(T, dtype=_I64, device=dev)
+        slot_mapping = _new(T, _I64, dev, stream)
     if free_count_out is None:
-        free_count_out = torch.empty(1, dtype=_I32, device=dev)
+        free_count_out = _new(1, _I32, dev, stream)
     _plain(("query_lens", query_lens, _I32, B),
            ("computed_lens", computed_lens, _I32, B),
            ("block_tables", block_tables, _I32, None),
@@ -637,7 +653,7 @@ def pa_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor,
     weight = q_weight if q_weight is not None else k_weight
     wdt = None if weight is None else weight.dtype
     if q_out is None:
-        q_out = torch.empty(T, Hq, D, dtype=dtype, device=q.device)
+        q_out = _new((T, Hq, D), dtype, q.device, stream)
     elif q_out.shape != qs:
         raise ValueError("q_out must be a tensor like q")
     _plain(("slot_mapping", slot_mapping, _I64, T),
@@ -727,12 +743,12 @@ def pa_select_blocks(q: torch.Tensor, bounds: torch.Tensor,
     NB = _bounds_shape(bounds, None, Hkv, D)
     B, M = _step_tables(block_tables, seq_lens, query_start_loc)
     if selected is None:
-        selected = torch.empty(T, Hkv, K, dtype=_I32, device=q.device)
+        selected = _new((T, Hkv, K), _I32, q.device, stream)
     if num_selected is None:
-        num_selected = torch.empty(T, Hkv, dtype=_I32, device=q.device)
+        num_selected = _new((T, Hkv), _I32, q.device, stream)
     if workspace is None:
         n = pa_select_blocks_workspace_size(T, Hkv, int(max_seq_len))
-        workspace = torch.empty(max(n, 1), dtype=_U8, device=q.device)
+        workspace = _new(max(n, 1), _U8, q.device, stream, False)
     _plain(("q", q, None, None), ("bounds", bounds, _U8, None),
            ("block_tables", block_tables, _I32, None),
            ("seq_lens", seq_lens, _I32, B),
@@ -787,10 +803,10 @@ def pa_attention_selected(q: torch.Tensor, k_cache: torch.Tensor,
         raise ValueError("selected must be [T, Hkv, K]")
     K = lists[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if workspace is None:
         n = pa_attention_selected_workspace_size(T, Hq, Hkv, D, K)
-        workspace = torch.empty(max(n, 1), dtype=_U8, device=q.device)
+        workspace = _new(max(n, 1), _U8, q.device, stream, False)
     _plain(("q", q, None, None), ("k_cache", k_cache, None, None),
            ("v_cache", v_cache, None, None),
            ("block_tables", block_tables, _I32, None),

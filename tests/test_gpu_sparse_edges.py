@@ -6,7 +6,7 @@ import torch
 
 import paged_kv_cache_82_gb300 as pa
 from tests import _sparse_ref as ref
-from tests.test_gpu_attention_selected import PROB, _run
+from tests.test_gpu_attention_selected import PROB, _run, _tensors
 from tests.test_gpu_select import step
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,56 @@ def test_an_infinite_value_makes_its_channel_infinite(dtype, group, blocks):
     tol = ref.attend_tolerance(want, mag, qk, dtype, PROB[dtype])
     err = np.abs(out.double().numpy() - want)
     assert (err <= tol)[..., rest.numpy()].all()
+
+
+class Spy:
+    """The library, with the arguments of the last call."""
+
+    def __init__(self, lib):
+        self.lib, self.args = lib, None
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+
+        def call(*args):
+            if not name.endswith("_size"):
+                self.args = args
+            return f(*args)
+        return call
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+@pytest.mark.parametrize("name", ["select", "selected", "attention", "window", "cascade"])
+def test_a_workspace_belongs_to_the_stream_it_is_used_on(name, as_handle, monkeypatch):
+    """A call on another stream than the current one: what it allocates is not
+    handed out again on the current stream while the kernels may still use it."""
+    wl, md, dev = step([(900, 1), (64, 1)], 8, 2, 128)
+    q, kc, vc = wl.q.cuda(), wl.k_cache.cuda(), wl.v_cache.cuda()
+    lists = {(t, h): [0, 2, 3] for t in range(2) for h in range(2)}
+    sel, cnt = _tensors(lists, 2, 2, 3)
+    bounds = torch.ones(kc.shape[0], 2, pa.bounds_bytes(128), dtype=torch.uint8, device="cuda")
+    table = dev["block_tables"].clone()
+    table[:, 0] = table[0, 0]
+    m = (dev["seq_lens"], dev["query_start_loc"])
+    run = {
+        "select": lambda s: pa.pa_select_blocks(q, bounds, table, *m, 1, 900, 3, stream=s)[0],
+        "selected": lambda s: pa.pa_attention_selected(q, kc, vc, table, *m, 1, 900, wl.scale,
+                                                       sel, cnt, stream=s),
+        "attention": lambda s: pa.pa_attention(q, kc, vc, table, *m, 1, 900, wl.scale,
+                                               stream=s),
+        "window": lambda s: pa.pa_attention_window(q, kc, vc, table, *m, 1, 900, wl.scale, 100,
+                                                   stream=s),
+        "cascade": lambda s: pa.pa_attention_cascade(q, kc, vc, table, *m, 1, 900, wl.scale, 1,
+                                                     stream=s)}[name]
+    want = run(None)
+    spy = Spy(pa.load_library())
+    monkeypatch.setattr(pa, "_lib", spy)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = run(side.cuda_stream if as_handle else side)
+    ws, nbytes, handle = spy.args[-3:]
+    assert handle == side.cuda_stream and nbytes > 0
+    again = torch.empty(nbytes, dtype=torch.uint8, device="cuda")  # (not written)
+    assert again.data_ptr() + nbytes <= ws or ws + nbytes <= again.data_ptr()
+    side.synchronize()
+    assert torch.equal(got, want) and pa.pa_get_device_error() == 0
