@@ -176,9 +176,13 @@ cudaError_t launch_build_step(const int32_t* query_lens, const int32_t* computed
   int cluster = 1;
   while (cluster < kStepMaxCluster && (int64_t)cluster * kStepPerCta < work) cluster *= 2;
   const size_t smem = (size_t)3 * num_seqs * sizeof(int);
-  if (smem > 48 * 1024) {
+  // Steps that may not fit the default 48 KB, of which the kernel's static shared
+  // memory takes some 300 bytes.  Always the same limit, the largest step's: one of
+  // each call's own size could be lowered by another thread before this launch.
+  if (smem > 40 * 1024) {
+    constexpr int kMaxSmem = 3 * kMaxBuildSeqs * (int)sizeof(int);
     const cudaError_t e = cudaFuncSetAttribute(
-        build_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        build_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};

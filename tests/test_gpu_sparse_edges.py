@@ -1,5 +1,10 @@
 """The sparse decode step's operators at their edges: the sizes, values and
 streams where a result could be wrong although the ordinary cases are right."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +15,8 @@ from tests.test_gpu_attention_selected import PROB, _run, _tensors
 from tests.test_gpu_select import step
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _summarise_whole(kc, blocks, H, D, cache):
@@ -147,3 +154,55 @@ def test_a_workspace_belongs_to_the_stream_it_is_used_on(name, as_handle, monkey
     assert again.data_ptr() + nbytes <= ws or ws + nbytes <= again.data_ptr()
     side.synchronize()
     assert torch.equal(got, want) and pa.pa_get_device_error() == 0
+
+
+BUILD_SIZES = """
+import sys
+import numpy as np
+import torch
+from tests.test_gpu_build_step import _case, _run
+# ascending: no earlier call has raised the kernel's shared memory
+for B in (4071, 4072, 4073, 4096, 4097, 16384, 4096, 64):
+    rng = np.random.default_rng(B)
+    lens = [(int(c), int(n)) for c, n in zip(rng.integers(0, 40, B), rng.integers(0, 3, B))]
+    _run(_case(rng, lens, pad=3))
+print("sizes ok")
+"""
+
+
+def test_step_sizes_around_48_kb_of_shared_memory():
+    """The kernel's static shared memory counts too: a fresh process, since the
+    opt-in to more lasts for the process."""
+    r = subprocess.run([sys.executable, "-c", BUILD_SIZES], cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "sizes ok" in r.stdout, r.stderr[-2000:]
+
+
+def test_steps_of_different_sizes_from_two_threads():
+    """Each thread's launches find the shared memory that they need, whatever the
+    other asks for between."""
+    failed = []
+
+    def loop(B):
+        try:
+            i32 = dict(dtype=torch.int32, device="cuda")
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                new, done = torch.ones(B, **i32), torch.zeros(B, **i32)
+                table = torch.full((B, 1), -1, **i32)
+                free, count = torch.arange(B, **i32), torch.tensor([B], **i32)
+                for _ in range(300):
+                    out = pa.pa_build_step(new, done, table, free, count, B, B)
+                stream.synchronize()
+                assert int(out[4]) == 0 and out[1][-1] == B
+                assert torch.equal(out[3], 16 * torch.arange(B - 1, -1, -1, device="cuda"))
+        except Exception as e:  # noqa: BLE001 (a thread's failure is the test's)
+            failed.append((B, e))
+
+    threads = [threading.Thread(target=loop, args=(B,)) for B in (16384, 4200, 5000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    assert pa.pa_get_device_error() == 0
