@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kStepThreads) build_step_kernel(StepArgs p) {
   const int rank = (int)cl.block_rank(), nranks = (int)cl.num_blocks();
   const int tid = threadIdx.x;
   const bool lead = rank == 0;
-  int64_t free_n = __ldg(p.free_count);
+  int64_t free_n = *p.free_count;  // (free_count_out may be the same word)
   unsigned bad = 0;
   if (free_n < 0 || free_n > p.free_capacity) {
     bad = PA_DEV_ERR_METADATA;
