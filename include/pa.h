@@ -539,7 +539,8 @@ pa_status pa_summarise_blocks(const void* k_cache, pa_dtype cache_dtype,
  * Rows of tokens that belong to no request are left as they were.
  * The step's arguments and their checks as pa_attention; workspace as there,
  * of pa_select_blocks_workspace_size bytes (at most 48 MiB, or one token's
- * scores if they are more).
+ * scores if they are more), which never shrink as a size grows: a buffer for
+ * a loop's longest step holds its shorter ones.
  */
 pa_status pa_select_blocks_workspace_size(int64_t num_tokens, int num_kv_heads,
                                           int max_seq_len, size_t* bytes);

@@ -67,6 +67,7 @@ cudaError_t launch_summarise_blocks(const StepView& s, const void* k_cache,
 // scores of the tokens of one pass over the step: room for as many tokens as
 // kSelectScoreBytes hold, one token at least
 constexpr int64_t kSelectScoreBytes = 48ll << 20;
+constexpr int64_t kSelectPassTokens = 32768;  // of a pass at most (grid.y)
 struct SelectPlan {
   int64_t row_scores;   // scores of one (token, KV head): blocks, a multiple of 4
   int64_t pass_tokens;  // tokens of one pass

@@ -870,9 +870,13 @@ SelectPlan make_select_plan(int64_t num_tokens, int num_kv_heads, int max_seq_le
   pl.row_scores = (blocks + 3) / 4 * 4;
   const int64_t token_bytes = pl.row_scores * num_kv_heads * 4;
   pl.pass_tokens = token_bytes > 0 ? kSelectScoreBytes / token_bytes : num_tokens;
-  pl.pass_tokens = std::max<int64_t>(1, std::min<int64_t>(pl.pass_tokens, 32768));
+  pl.pass_tokens = std::max<int64_t>(1, std::min(pl.pass_tokens, kSelectPassTokens));
   pl.pass_tokens = std::min(pl.pass_tokens, num_tokens);
-  pl.bytes = pl.pass_tokens * token_bytes;
+  // What is asked for grows with every size, so that a buffer for a loop's longest
+  // step holds every shorter one: of a step in passes, the whole bound, not the
+  // tokens of a pass times their bytes.
+  pl.bytes = std::min(std::min<int64_t>(num_tokens, kSelectPassTokens) * token_bytes,
+                      std::max(kSelectScoreBytes, token_bytes));
   return pl;
 }
 

@@ -3,6 +3,8 @@ without a GPU."""
 import os
 import re
 
+import pytest
+
 import paged_kv_cache_82_gb300 as pa
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(pa.__file__)), "csrc")
@@ -29,3 +31,21 @@ def test_words_that_a_step_replaces_are_not_read_as_constants():
     assert "free_blocks" in constant  # never written
     in_place = {"computed_lens", "free_count", "block_tables"}
     assert all(f"p.{w}" in body for w in in_place) and not in_place & constant
+
+
+@pytest.mark.parametrize("heads", [1, 8, 128])
+def test_a_selection_workspace_holds_every_shorter_step(heads):
+    """Sizes up to the 48 MiB of scores and past them, in tokens, in length and
+    in heads; never more than all the step's scores, nor than the bound."""
+    size = pa.pa_select_blocks_workspace_size
+    tokens = [1, 2, 5, 64, 127, 128, 512, 513, 2047, 32767, 32768, 32769, 100000]
+    lengths = [1, 16, 17, 100, 4096, 65536, 99999, 100000, 128000, 131072, 1 << 20, 1 << 27]
+    table = [[size(T, heads, L) for L in lengths] for T in tokens]
+    for i, row in enumerate(table):
+        assert row == sorted(row), (tokens[i], row)
+        for L, n in zip(lengths, row):
+            one = size(1, heads, L)
+            assert one <= n <= min(tokens[i] * one, max(48 << 20, one))
+            assert n <= size(tokens[i], heads + 1, L)
+    for column in zip(*table):
+        assert list(column) == sorted(column)
