@@ -1002,6 +1002,15 @@ __device__ __forceinline__ void join_cut(const SelParams& p, int2 cut) {
         ml[j] = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
         v[j] = *reinterpret_cast<const float4*>(p.part + at * kD + d);
       }
+      // a place past the last part holds that one again: nothing of it, not even 0
+      // times its sum, which may be infinite.  (Selected here: with a branch below
+      // the loads go out one by one, and one token takes 12.2 us.)
+#pragma unroll
+      for (int j = 1; j < kBatch; ++j)
+        if (k0 + j >= parts) {
+          ml[j] = make_float2(-INFINITY, 0.f);
+          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       float top = mx;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) top = fmaxf(top, ml[j].x);
@@ -1011,8 +1020,6 @@ __device__ __forceinline__ void join_cut(const SelParams& p, int2 cut) {
       mx = top;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        // (a place past the last part: not even 0 times its sum, which may be infinite)
-        if (k0 + j >= parts) break;
         const float f = ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - top);
         ls = fmaf(f, ml[j].y, ls);
         a.x = fmaf(f, v[j].x, a.x);
