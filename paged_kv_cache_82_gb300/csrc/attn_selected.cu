@@ -141,6 +141,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+// x >= 0 as the sum of two bf16 numbers: its upper half, and what that leaves,
+// rounded; together off by 2^-16 of x.  Cut off and not rounded, the head leaves
+// a tail that is not negative, and a tail of 2^-126 at least is none that is 0:
+// both times an infinite value are the same infinity.
+__device__ __forceinline__ uint32_t bf16_heads(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float bf16_tail(float x) {
+  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), 0x1p-126f);
+}
+
 template <int kPg, int kD>
 struct PageTraits {
   static constexpr bool k4 = kPg == kI4 || kPg == kN4;
@@ -159,7 +170,10 @@ struct PageTraits {
   // channels of a lane's K chunk
   static constexpr int kKChannels = kD / (4 * kKChunks);
   // The products' types: Q K in the 16-bit type of the pages, in f16 over the
-  // others; P V as well, over INT4 pages in bf16 (their scales are in P).
+  // others; P V as well, over INT4 pages in bf16 (their scales are in P, which
+  // then needs that range).  P is one f16 number (11 bits: off by 2^-11 of it), or
+  // two bf16 numbers: one has 8 bits, and two keys' average was off by 5e-3, where
+  // pa_attention is within 2e-3.
   static constexpr bool kQkBF = kPg == kB16;
   static constexpr bool kPvBF = kPg == kB16 || kPg == kI4;
   // NVFP4 values are decoded 2^-7 of their size, so that code and scale stay
@@ -686,23 +700,24 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
         const float p3 = exp2_fast(fmaf(s[g][nt][3], score_scale, m1));
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
-        // keys as rows -> heads as rows: the second product's operand.  Over
-        // INT4 pages the values' scales go into P, which is then the sum of two
-        // bf16 numbers: their range, and more than f16's precision.
-        if constexpr (kPg == kI4) {
-          const float s0 = __uint_as_float(vs[g][0]), s1 = __uint_as_float(vs[g][1]);
-          const float x[4] = {p0 * s0, p1 * s0, p2 * s1, p3 * s1};
-          float y[4];
+        // keys as rows -> heads as rows: the second product's operand, by bf16
+        // products in two parts.  Over INT4 pages the values' scales go into P.
+        if constexpr (Tr::kPvBF) {
+          float x[4] = {p0, p1, p2, p3}, y[4];
+          if constexpr (kPg == kI4) {
+            const float s0 = __uint_as_float(vs[g][0]), s1 = __uint_as_float(vs[g][1]);
+            x[0] *= s0, x[1] *= s0, x[2] *= s1, x[3] *= s1;
+          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = x[j] - __bfloat162float(__float2bfloat16_rn(x[j]));
+          for (int j = 0; j < 4; ++j) y[j] = bf16_tail(x[j]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            pb[g][nt][j] = transpose8x8(pack2<true>(x[2 * j], x[2 * j + 1]));
+            pb[g][nt][j] = transpose8x8(bf16_heads(x[2 * j], x[2 * j + 1]));
             pl[g][nt][j] = transpose8x8(pack2<true>(y[2 * j], y[2 * j + 1]));
           }
         } else {
-          pb[g][nt][0] = transpose8x8(pack2<Tr::kPvBF>(p0, p1));
-          pb[g][nt][1] = transpose8x8(pack2<Tr::kPvBF>(p2, p3));
+          pb[g][nt][0] = transpose8x8(pack2<false>(p0, p1));
+          pb[g][nt][1] = transpose8x8(pack2<false>(p2, p3));
         }
       }
     }
@@ -722,7 +737,7 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
               mma16816<Tr::kPvBF>(acc[nt][tl], a, pb[g][nt][0], pb[g][nt][1]);
-              if constexpr (kPg == kI4)
+              if constexpr (Tr::kPvBF)
                 mma16816<true>(acc[nt][tl], a, pl[g][nt][0], pl[g][nt][1]);
             }
           };

@@ -11,8 +11,8 @@ import torch
 
 import paged_kv_cache_82_gb300 as pa
 from tests import _sparse_ref as ref
-from tests.test_gpu_attention_selected import PROB, _run, _tensors
-from tests.test_gpu_select import step
+from tests.test_gpu_attention_selected import PROB, _lists, _run, _tensors
+from tests.test_gpu_select import meta, step
 
 pytestmark = pytest.mark.gpu
 
@@ -206,3 +206,40 @@ def test_steps_of_different_sizes_from_two_threads():
         t.join()
     assert not failed, failed
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("group,D", [(4, 128), (8, 64), (16, 128), (20, 64)])
+def test_probabilities_over_bf16_pages_keep_16_bits(group, D):
+    """Lists of few keys, whose values nearly cancel: what is left shows the
+    probabilities' own rounding.  Each is a head of 8 significant bits, cut off
+    (the tail is less than 2^-7 of it), and the tail rounded to 8 bits: off by at
+    most 2^-16 of the probability, and so 2^-16 of sum p |v|.  The fp32
+    arithmetic is as in attend_tolerance."""
+    lens = [(L, 1) for L in (1, 2, 3, 5, 16, 17, 31, 48)] + [(7, 7)]
+    wl, md, dev = step(lens, 2 * group, 2, D)
+    sign = torch.tensor([1.0, -1.0] * 8)[None, None, :, None]
+    wl.v_cache = (wl.v_cache.float() * 0.125 + 8 * sign).bfloat16()
+    lists = _lists(None, md, 2, 3, "all")
+    out = _run(wl, md, dev, lists, 3)
+    assert pa.pa_get_device_error() == 0
+    want, mag, qk = _attend(wl, md, lists)
+    tol = (ref.half("bf16") * np.abs(want) + (1 + ref.half("bf16")) * (
+        2.0 ** -16 * mag + 2.0 ** -16 * (1 + qk) * mag + 2.0 ** -24))
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_short_lists_are_within_the_bar_of_pa_attention():
+    """N(0, 1) keys and values, lists of 1 to 48 keys: 2e-3 and half a step of
+    the output, and pa_attention, which is within the same, no further off."""
+    lens = [(1 + i % 48, 1) for i in range(144)]
+    wl, md, dev = step(lens, 32, 8, 128)
+    lists = _lists(None, md, 8, 3, "all")
+    out = _run(wl, md, dev, lists, 3).double().cpu().numpy()
+    full = pa.pa_attention(wl.q.cuda(), wl.k_cache.cuda(), wl.v_cache.cuda(), *meta(dev),
+                           md["max_query_len"], md["max_seq_len"], wl.scale)
+    assert pa.pa_get_device_error() == 0
+    want, _, _ = _attend(wl, md, lists)
+    bar = 2e-3 + ref.half("bf16") * np.abs(want)
+    assert (np.abs(out - want) <= bar).all()
+    assert (np.abs(full.double().cpu().numpy() - want) <= bar).all()
