@@ -660,10 +660,16 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
               vs[g][j] = 0;
       }
     }
-    // softmax over the step's keys; m: the largest score times score_scale (> 0)
+    // softmax over the step's keys, by scores that are rounded once: in one fma with
+    // the maximum the largest one's own exponent would be that rounding and not 0,
+    // 2^5 where scores reach 2^30
     uint32_t pb[kP][kNT][2], pl[kP][kNT][2];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+      for (int g = 0; g < kP; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[g][nt][j] *= score_scale;
       float mx[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -672,7 +678,7 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
         for (int g = 1; g < kP; ++g) mx[j] = fmaxf(mx[j], fmaxf(s[g][nt][j], s[g][nt][j + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(~0u, mx[j], d));
-        mx[j] = fmaxf(mx[j] * score_scale, m[nt][j]);
+        mx[j] = fmaxf(mx[j], m[nt][j]);
       }
       if (__any_sync(~0u, mx[0] > m[nt][0] || mx[1] > m[nt][1])) {
         float al[2];
@@ -694,10 +700,10 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
       const float m1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
 #pragma unroll
       for (int g = 0; g < kP; ++g) {
-        const float p0 = exp2_fast(fmaf(s[g][nt][0], score_scale, m0));
-        const float p1 = exp2_fast(fmaf(s[g][nt][1], score_scale, m1));
-        const float p2 = exp2_fast(fmaf(s[g][nt][2], score_scale, m0));
-        const float p3 = exp2_fast(fmaf(s[g][nt][3], score_scale, m1));
+        const float p0 = exp2_fast(s[g][nt][0] + m0);
+        const float p1 = exp2_fast(s[g][nt][1] + m1);
+        const float p2 = exp2_fast(s[g][nt][2] + m0);
+        const float p3 = exp2_fast(s[g][nt][3] + m1);
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
         // keys as rows -> heads as rows: the second product's operand, by bf16

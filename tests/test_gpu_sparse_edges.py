@@ -243,3 +243,37 @@ def test_short_lists_are_within_the_bar_of_pa_attention():
     bar = 2e-3 + ref.half("bf16") * np.abs(want)
     assert (np.abs(out - want) <= bar).all()
     assert (np.abs(full.double().cpu().numpy() - want) <= bar).all()
+
+
+@pytest.mark.parametrize("size", [1e5, 1e9, 1e13, 1e30])
+@pytest.mark.parametrize("cache", ["bf16", "f16", "f32", "e4m3", "int4", "nvfp4"])
+def test_scores_far_past_the_exponentials_range(cache, size):
+    """Finite scores of any size: a row whose largest score leads by more than
+    the scores' rounding is that key's value, and none is NaN."""
+    dtype = cache if cache in ("f16", "f32") else "bf16"
+    wl, md, dev = step([(200, 1), (77, 2), (1, 1), (16, 1)], 16, 2, 128, dtype, cache)
+    lists = _lists(np.random.default_rng(6), md, 2, 8)
+    out = _run(wl, md, dev, lists, 8, scale=size).double().cpu().numpy()
+    assert pa.pa_get_device_error() == 0
+    assert np.isfinite(out).all()
+    k, v = (ref.decode_pages(c, cache, 128) for c in (wl.k_cache, wl.v_cache))
+    v = v * (wl.v_scale if cache in ("e4m3", "nvfp4") else 1.0)
+    sure = 0
+    for t, r, p in ref.tokens_of(md):
+        for h in range(2):
+            keys = [j for b in lists[t, h] for j in range(16 * b, min(16 * b + 16, p + 1))]
+            at = md["block_tables"][r, np.array(keys) // 16], h, np.array(keys) % 16
+            for g in range(8 * h, 8 * h + 8):
+                x = wl.q[t, g].double().numpy()
+                score = k[at] @ x
+                best = int(score.argmax())
+                # (fp32 sums of 128 products: 2^-17 of the terms' sum covers them)
+                lead = score[best] - np.partition(score, -2)[-2] if len(score) > 1 else np.inf
+                slack = 2.0 ** -16 * (np.abs(k[at]) @ np.abs(x)).max()
+                # and 2^-40 of the others' weight, at the smallest of the scales
+                if lead > slack + 40 / size:
+                    sure += 1
+                    want = v[at][best]
+                    assert (np.abs(out[t, g] - want) <= ref.half(dtype) * np.abs(want) +
+                            2.0 ** -20).all()
+    assert sure >= 60
