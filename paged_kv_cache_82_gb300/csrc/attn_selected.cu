@@ -502,19 +502,25 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
 
   // Q operand words, in the channel order of the lane's K words: neighbours,
   // over INT4 pages the channels 4 apart that a mask leaves in one word.  Where
-  // the products are in f16 over a narrower page, a power of two brings the
-  // row's largest query into f16's range, and leaves through the score's scale.
+  // the products are in f16 over a narrower page, a power of two of each head's own
+  // brings its largest query to 2^13, well inside f16's range either way, and leaves
+  // through the score's scale (that of the heads 2c, 2c + 1 of the scores here).
   constexpr int kE = Tr::kKChannels;
+  constexpr bool kHeadScale = kPg == kF8 || kScaled;
   uint32_t qw[kNT][Tr::kKChunks][kE / 2];
-  float score_scale = p.scale * p.k_scale * (Tr::kUnit * kLog2e);
+  float score_scale[kHeadScale ? kNT : 1][kHeadScale ? 2 : 1];
   {
-    float x[kNT][Tr::kKChunks][kE];
-    float big = 0.f;
+    // a scale of either sign, or 0: the score's stays positive
+    const float scale = p.scale * p.k_scale * (Tr::kUnit * kLog2e);
+    const float sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+    score_scale[0][0] = scale == 0.f ? 1.f : fabsf(scale);
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+    for (int nt = 0; nt < kNT; ++nt) {
+      const int hd = nt * 8 + r;
+      float x[Tr::kKChunks][kE], down = sign;
+      float big = 0.f;  // the largest finite one
 #pragma unroll
       for (int i = 0; i < Tr::kKChunks; ++i) {
-        const int hd = nt * 8 + r;
         const TQ* src = static_cast<const TQ*>(p.q) +
                         (u.t * p.num_q_heads + head0 + hd) * kD + (c + 4 * i) * kE;
         uint4 w[kE / 8];
@@ -524,32 +530,31 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
                             : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
-          x[nt][i][e] = to_f32(reinterpret_cast<const TQ*>(w)[e]);
-          big = fmaxf(big, fabsf(x[nt][i][e]));
+          x[i][e] = to_f32(reinterpret_cast<const TQ*>(w)[e]);
+          if constexpr (kHeadScale)
+            if (fabsf(x[i][e]) < INFINITY) big = fmaxf(big, fabsf(x[i][e]));
         }
       }
-    // a scale of either sign, or 0: the score's stays positive
-    float down = score_scale > 0.f ? 1.f : score_scale < 0.f ? -1.f : 0.f;
-    score_scale = score_scale == 0.f ? 1.f : fabsf(score_scale);
-    if constexpr (kPg == kF8 || kScaled) {
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
-      if (big > 16384.f && big < INFINITY) {
-        const int ex = ilogbf(big) - 13;
+      if constexpr (kHeadScale) {
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+        // (2^120 and a bf16 query of 2^-133 are a normal f16 number as well)
+        const int ex = big > 0.f ? max(ilogbf(big) - 13, -120) : 0;
         down *= exp2f((float)-ex);
-        score_scale *= exp2f((float)ex);
-      }
-    }
+        const float up = fabsf(scale == 0.f ? 1.f : scale) * exp2f((float)ex);
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+        for (int j = 0; j < 2; ++j)
+          score_scale[nt][j] = __shfl_sync(~0u, up, (2 * c + j) * 4);
+      }
 #pragma unroll
       for (int i = 0; i < Tr::kKChunks; ++i)
 #pragma unroll
         for (int w = 0; w < kE / 2; ++w) {
           const int e0 = kPg == kI4 ? 8 * (w / 4) + w % 4 : 2 * w;
           const int e1 = kPg == kI4 ? e0 + 4 : e0 + 1;
-          qw[nt][i][w] = pack2<Tr::kQkBF>(x[nt][i][e0] * down, x[nt][i][e1] * down);
+          qw[nt][i][w] = pack2<Tr::kQkBF>(x[i][e0] * down, x[i][e1] * down);
         }
+    }
   }
 
   for (int i = 0; i < steps; ++i) {
@@ -669,7 +674,8 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
 #pragma unroll
       for (int g = 0; g < kP; ++g)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[g][nt][j] *= score_scale;
+        for (int j = 0; j < 4; ++j)
+          s[g][nt][j] *= score_scale[kHeadScale ? nt : 0][kHeadScale ? j & 1 : 0];
       float mx[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {

@@ -277,3 +277,36 @@ def test_scores_far_past_the_exponentials_range(cache, size):
                     assert (np.abs(out[t, g] - want) <= ref.half(dtype) * np.abs(want) +
                             2.0 ** -20).all()
     assert sure >= 60
+
+
+@pytest.mark.parametrize("cache,D", [("e4m3", 128), ("e4m3", 64), ("int4", 128), ("int4", 64),
+                                     ("nvfp4", 128), ("nvfp4", 64)])
+@pytest.mark.parametrize("power", [-100, -40, -12, 0])
+def test_small_queries_over_narrow_pages(cache, D, power):
+    """The products are in f16, the bf16 queries reach far below its range: a
+    query times 2^power and a scale divided by it give the same scores."""
+    wl, md, dev = step([(200, 1), (77, 2), (16, 1)], 16, 2, D, "bf16", cache)
+    scale = wl.scale * 2.0 ** -power
+    wl.q *= 2.0 ** power
+    lists = _lists(np.random.default_rng(3), md, 2, 8)
+    out = _run(wl, md, dev, lists, 8, scale=scale)
+    assert pa.pa_get_device_error() == 0
+    want, mag, qk = _attend(wl, md, lists, scale)
+    tol = ref.attend_tolerance(want, mag, qk, "bf16", "f16")
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("group", [4, 8, 12])
+@pytest.mark.parametrize("cache", ["e4m3", "int4", "nvfp4"])
+def test_heads_of_very_different_sizes_over_narrow_pages(cache, group):
+    """Each head is brought into f16's range by a power of two of its own: a
+    head beside one 2^40 times as large keeps its bits."""
+    wl, md, dev = step([(200, 1), (77, 2), (16, 1)], 2 * group, 2, 128, "bf16", cache)
+    wl.q[:, 1::3] *= 2.0 ** 40
+    wl.q[:, 2::5] *= 2.0 ** -30
+    lists = _lists(np.random.default_rng(4), md, 2, 8)
+    out = _run(wl, md, dev, lists, 8)
+    assert pa.pa_get_device_error() == 0
+    want, mag, qk = _attend(wl, md, lists)
+    tol = ref.attend_tolerance(want, mag, qk, "bf16", "f16")
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
