@@ -637,8 +637,8 @@ def pa_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor,
         row, head, one = t.stride()
         if one != 1 or (h > 1 and head != D):
             raise ValueError(f"{n} must have contiguous rows")
-        # (of a single token: any stride will do)
-        rows.append(row if T > 1 else max(row, h * D))
+        # (a single token's row is contiguous whatever its stride)
+        rows.append(row if T > 1 else h * D)
     NB, Hc, bs, Dc = _cache_geometry(k_cache, cache_dtype, D)
     if Hc != Hkv or Dc != D or v_cache.shape != k_cache.shape \
             or v_cache.dtype is not k_cache.dtype:

@@ -310,3 +310,26 @@ def test_heads_of_very_different_sizes_over_narrow_pages(cache, group):
     want, mag, qk = _attend(wl, md, lists)
     tol = ref.attend_tolerance(want, mag, qk, "bf16", "f16")
     assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+
+
+def test_one_token_of_a_qkv_row_in_place():
+    """A single token's slice of a QKV row is contiguous whatever its row
+    stride: its rotation in place is the one into a buffer."""
+    Hq, Hkv, D = 8, 2, 128
+    g = torch.Generator("cuda").manual_seed(5)
+    qkv = torch.randn(1, (Hq + 2 * Hkv) * D, generator=g, device="cuda").bfloat16()
+    q, k, v = qkv.view(1, Hq + 2 * Hkv, D).split((Hq, Hkv, Hkv), dim=1)
+    assert q.is_contiguous() and q.stride(0) != Hq * D
+    cs = torch.randn(9, D, generator=g, device="cuda")
+    pos = torch.tensor([7], dtype=torch.int32, device="cuda")
+    slot = torch.tensor([21], device="cuda")
+    w = torch.rand(D, generator=g, device="cuda").bfloat16()
+    kc, vc = (torch.zeros(2, Hkv, 16, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    want = pa.pa_norm_rope_and_cache(q, k, v, kc, vc, slot, pos, cs, w, w)
+    keys = kc.clone(), vc.clone()
+    kc.zero_(), vc.zero_()
+    rest = qkv[:, Hq * D:].clone()
+    got = pa.pa_norm_rope_and_cache(q, k, v, kc, vc, slot, pos, cs, w, w, q_out=q)
+    assert pa.pa_get_device_error() == 0
+    assert got is q and torch.equal(q, want) and torch.equal(qkv[:, Hq * D:], rest)
+    assert torch.equal(kc, keys[0]) and torch.equal(vc, keys[1])
