@@ -68,7 +68,7 @@ struct SelParams {
 };
 
 // A row: its token, request, position and list length (-1: the token belongs
-// to no request, or its metadata is broken).
+// to no request, or its metadata is broken, which check_requests flags).
 struct Unit {
   int64_t t;
   int h;
@@ -85,10 +85,7 @@ __device__ __forceinline__ Unit find_unit(const SelParams& p, int64_t row, bool 
       p.s.max_query_len, p.s.max_seq_len, p.s.max_blocks_per_seq);
   u.r = q.r;
   u.pos = q.m.L - q.m.n + (int)(u.t - q.m.q0);
-  if (!q.in) {
-    u.count = -1;
-  } else if (!q.m.ok) {
-    if (tell) flag_error(p.s.err, PA_DEV_ERR_METADATA);
+  if (!q.in || !q.m.ok) {
     u.count = -1;
   } else if (u.count < 0 || u.count > p.max_selected) {
     if (tell) flag_error(p.s.err, PA_DEV_ERR_METADATA);
@@ -273,7 +270,8 @@ __device__ __forceinline__ Share find_share(const SelParams& p, int64_t* rows) {
   for (int k = 0; k < kHeld; ++k)
     held[k] = lo + k < hi ? __ldg(p.num_selected + lo + k) : 0;
   const int64_t last = __ldg(p.s.query_start_loc + p.s.num_seqs);
-  *rows = (last < 0 ? 0 : least(last, p.s.num_tokens)) * p.num_kv_heads;
+  // (an end before the first token is broken metadata: each row looks for itself)
+  *rows = (last < 0 ? p.s.num_tokens : least(last, p.s.num_tokens)) * p.num_kv_heads;
   const int64_t end = least(hi, *rows);
   auto units = [&](int count) {
     return count > 0 && count <= p.max_selected ? count + kRowCost : 0;
@@ -1075,6 +1073,9 @@ __global__ void __launch_bounds__(kJoinThreads) selected_join_kernel(const SelPa
   // These CTAs start as the shares' end: what can be read before goes out first,
   // and the zeros come last (before the join: one token's 8 lists 12.0 us, not 10.5).
   const bool here = empty(blockIdx.x + threadIdx.x * step);
+  if (part == 0)
+    check_requests(p.s, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x,
+                   step * kJoinThreads);
   pdl_wait();  // the shares' results
   const int2 cut = p.cut[part * gridDim.x + blockIdx.x];
   if (cut.x >= 0) join_cut<TQ, kD>(p, cut);

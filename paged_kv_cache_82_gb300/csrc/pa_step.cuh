@@ -53,6 +53,18 @@ __device__ __forceinline__ TokenReq warp_token_request(
   return q;
 }
 
+// Flags broken metadata of any request, of those no token points to as well (a
+// negative length or count of tokens).  Every thread of the grid calls it, with its
+// number and how many they are.
+__device__ __forceinline__ void check_requests(const StepView& s, int64_t thread,
+                                               int64_t threads) {
+  for (int64_t r = thread; r < s.num_seqs; r += threads)
+    if (!load_req(s.query_start_loc, s.seq_lens, (int)r, s.num_tokens, s.max_query_len,
+                  s.max_seq_len, s.max_blocks_per_seq)
+             .ok)
+      flag_error(s.err, PA_DEV_ERR_METADATA);
+}
+
 // fl32(x / s) for many x and one s: from the correctly rounded 1 / s by two of
 // Markstein's corrections (IBM J. Res. Dev. 34, 1990).  x * rcp is within 3/2
 // of a step of x / s; the first correction leaves the quotient within one step,

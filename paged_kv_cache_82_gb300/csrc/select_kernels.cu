@@ -318,20 +318,16 @@ struct ScoreParams {
 };
 
 // Token t's request, position and visible blocks; -1 blocks: none (a token of
-// no request, or broken metadata, which is flagged if tell).
+// no request, or broken metadata, which check_requests flags).
 struct TokenView {
   int r, pos, blocks;
 };
-__device__ __forceinline__ TokenView token_view(const StepView& s, int64_t t, bool tell) {
+__device__ __forceinline__ TokenView token_view(const StepView& s, int64_t t) {
   TokenView v{0, 0, -1};
   const TokenReq q =
       warp_token_request(s.query_start_loc, s.seq_lens, s.num_seqs, t, s.num_tokens,
                          s.max_query_len, s.max_seq_len, s.max_blocks_per_seq);
-  if (!q.in) return v;
-  if (!q.m.ok) {
-    if (tell) flag_error(s.err, PA_DEV_ERR_METADATA);
-    return v;
-  }
+  if (!q.in || !q.m.ok) return v;
   v.r = q.r;
   v.pos = q.m.L - q.m.n + (int)(t - q.m.q0);
   v.blocks = v.pos / kBS + 1;
@@ -450,7 +446,7 @@ score_kernel(const ScoreParams p) {
   const int head0 = blockIdx.z * kScoreWarps;
   const int num_heads = min(kScoreWarps, p.num_kv_heads - head0);  // of the CTA
   const int sharing = kScoreWarps / num_heads;                     // warps of one head
-  const TokenView tv = token_view(p.s, t, false);
+  const TokenView tv = token_view(p.s, t);
   if (tv.blocks <= p.max_selected || first >= tv.blocks) return;  // all of them
   if (warp >= sharing * num_heads) return;
   const int h = head0 + warp % num_heads;
@@ -655,7 +651,10 @@ topk_kernel(const TopkParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = (int)(blockIdx.x % p.num_kv_heads);
   const int64_t tp = blockIdx.x / p.num_kv_heads, t = p.t0 + tp;
-  const TokenView tv = token_view(p.s, t, h == 0 && tid == 0);
+  const TokenView tv = token_view(p.s, t);
+  if (p.t0 == 0)
+    check_requests(p.s, (int64_t)blockIdx.x * kTopkThreads + tid,
+                   (int64_t)gridDim.x * kTopkThreads);
   pdl_wait();  // the scores
   if (tv.blocks < 0) return;
   const int64_t row = t * p.num_kv_heads + h;

@@ -333,3 +333,58 @@ def test_one_token_of_a_qkv_row_in_place():
     assert pa.pa_get_device_error() == 0
     assert got is q and torch.equal(q, want) and torch.equal(qkv[:, Hq * D:], rest)
     assert torch.equal(kc, keys[0]) and torch.equal(vc, keys[1])
+
+
+@pytest.mark.parametrize("op", ["summarise", "select", "selected", "attention"])
+@pytest.mark.parametrize("broken", ["length", "offset", "last", "table"])
+def test_a_broken_request_without_tokens_is_flagged(op, broken):
+    """As in pa_attention: every request's metadata is checked, whether or not
+    a token points to it, and the other requests' results stand."""
+    wl, md, dev = step([(300, 1), (64, 0), (90, 1)], 8, 2, 128)
+    q, kc, vc = wl.q.cuda(), wl.k_cache.cuda(), wl.v_cache.cuda()
+    L, qsl = dev["seq_lens"].clone(), dev["query_start_loc"].clone()
+    rows = [0, 1]
+    if broken == "length":
+        L[1] = -5
+    elif broken == "table":
+        L[1] = 16 * dev["block_tables"].shape[1] + 1
+    elif broken == "offset":
+        qsl[2] = 0  # requests 1 and 2: of -1 tokens, and of two
+        rows = [0]
+    else:
+        qsl[3] = -1
+        rows = [0]
+    lists = {(t, h): [0, 2, 3] for t in range(2) for h in range(2)}
+    sel, cnt = _tensors(lists, 2, 2, 3)
+    bounds = _bounds(kc, 2)
+
+    def run(L, qsl):
+        m = (dev["block_tables"], L, qsl)
+        if op == "summarise":
+            out = bounds.clone()
+            pa.pa_summarise_blocks(kc, out, *m, 2, 1, 300)
+            # of each token's own block
+            return torch.stack([out[int(md["block_tables"][r, p // 16])]
+                                for r, p in ((0, 299), (2, 89))])
+        if op == "select":
+            return pa.pa_select_blocks(q, bounds, *m, 1, 300, 3)[0]
+        if op == "selected":
+            return pa.pa_attention_selected(q, kc, vc, *m, 1, 300, wl.scale, sel, cnt)
+        return pa.pa_attention(q, kc, vc, *m, 1, 300, wl.scale)
+
+    want = run(dev["seq_lens"], dev["query_start_loc"])
+    assert pa.pa_get_device_error() == 0
+    got = run(L, qsl)
+    assert pa.pa_get_device_error() == pa.PA_DEV_ERR_METADATA
+    got, want = got[rows], want[rows]
+    if op == "attention":  # split-K ranges follow the work there is
+        assert ((got.float() - want.float()).abs() <= 2.0 ** -7 * (1 + want.abs())).all()
+    else:
+        assert torch.equal(got, want)
+
+
+def _bounds(kc, Hkv):
+    rng = np.random.default_rng(9)
+    b = rng.integers(0, 100, (kc.shape[0], Hkv, pa.bounds_bytes(128)), dtype=np.uint8)
+    b[..., 256:260] = np.array([0.01], np.float32).view(np.uint8)
+    return torch.from_numpy(b).cuda()
