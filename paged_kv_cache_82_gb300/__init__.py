@@ -51,6 +51,7 @@ EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_copy_blocks",
 
 _DT = {"f32": PA_F32, "f16": PA_F16, "bf16": PA_BF16, "e4m3": PA_FP8_E4M3,
        "int4": PA_INT4, "nvfp4": PA_NVFP4}
+_ELEM_BYTES = {"f32": 4, "f16": 2, "bf16": 2, "e4m3": 1}
 
 
 def page_bytes_4bit(cache_dtype: str, head_dim: int) -> int:
@@ -83,7 +84,11 @@ def _cache_geometry(cache: torch.Tensor, cache_dtype: Optional[str],
         return NB, H, BLOCK_SIZE, D
     if cache.dim() != 4:
         raise ValueError("the caches must be [NB, Hkv, 16, D]")
+    if cache_dtype is not None and cache.element_size() != _ELEM_BYTES[cache_dtype]:
+        raise ValueError(f"a cache of {cache.dtype} holds no {cache_dtype} elements")
     return tuple(cache.shape)
+
+
 _lib = None
 
 

@@ -4,6 +4,7 @@ import os
 import re
 
 import pytest
+import torch
 
 import paged_kv_cache_82_gb300 as pa
 
@@ -49,3 +50,31 @@ def test_a_selection_workspace_holds_every_shorter_step(heads):
             assert n <= size(tokens[i], heads + 1, L)
     for column in zip(*table):
         assert list(column) == sorted(column)
+
+
+@pytest.mark.parametrize("dtype,name", [("bfloat16", "f32"), ("uint8", "bf16"),
+                                        ("uint8", "f16"), ("float16", "e4m3"),
+                                        ("float32", "bf16")])
+def test_a_cache_is_not_read_as_elements_of_another_size(dtype, name):
+    """A type named for the cache that its elements do not have the size of: the
+    kernels would read past its end, or half of it."""
+    cache = torch.zeros(4, 2, 16, 128, dtype=getattr(torch, dtype))
+    q = torch.zeros(1, 8, 128, dtype=torch.float32 if name == "f32" else torch.float16)
+    kv = torch.zeros(1, 2, 128, dtype=q.dtype)
+    i32 = dict(dtype=torch.int32)
+    m = (torch.zeros(1, 4, **i32), torch.ones(1, **i32), torch.tensor([0, 1], **i32))
+    slot = torch.zeros(1, dtype=torch.int64)
+    sel, cnt = torch.zeros(1, 2, 1, **i32), torch.ones(1, 2, **i32)
+    bounds = torch.zeros(4, 2, pa.bounds_bytes(128), dtype=torch.uint8)
+    calls = [
+        lambda **k: pa.pa_attention_selected(q, cache, cache.clone(), *m, 1, 1, 0.1, sel, cnt,
+                                             **k),
+        lambda **k: pa.pa_summarise_blocks(cache, bounds, *m, 1, 1, 1, **k),
+        lambda **k: pa.pa_norm_rope_and_cache(q, kv, kv, cache, cache.clone(), slot, **k),
+        lambda **k: pa.pa_attention(q, cache, cache.clone(), *m, 1, 1, 0.1, **k),
+        lambda **k: pa.pa_reshape_and_cache(kv, kv, cache, cache.clone(), slot, **k),
+        lambda **k: pa.pa_copy_blocks(cache, cache.clone(), torch.zeros(1, 2, dtype=torch.int64),
+                                      **k)]
+    for call in calls:
+        with pytest.raises(ValueError, match=f"no {name} elements"):
+            call(cache_dtype=name)
