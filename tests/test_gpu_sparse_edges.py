@@ -13,6 +13,7 @@ import paged_kv_cache_82_gb300 as pa
 from tests import _sparse_ref as ref
 from tests.test_gpu_attention_selected import PROB, _lists, _run, _tensors
 from tests.test_gpu_select import meta, step
+from tests.test_gpu_sparse_step import Loop
 
 pytestmark = pytest.mark.gpu
 
@@ -103,109 +104,33 @@ def test_an_infinite_value_makes_its_channel_infinite(dtype, group, blocks):
     assert (err <= tol)[..., rest.numpy()].all()
 
 
-class Spy:
-    """The library, with the arguments of the last call."""
-
-    def __init__(self, lib):
-        self.lib, self.args = lib, None
-
-    def __getattr__(self, name):
-        f = getattr(self.lib, name)
-
-        def call(*args):
-            if not name.endswith("_size"):
-                self.args = args
-            return f(*args)
-        return call
-
-
-@pytest.mark.parametrize("as_handle", [False, True])
-@pytest.mark.parametrize("name", ["select", "selected", "attention", "window", "cascade"])
-def test_a_workspace_belongs_to_the_stream_it_is_used_on(name, as_handle, monkeypatch):
-    """A call on another stream than the current one: what it allocates is not
-    handed out again on the current stream while the kernels may still use it."""
-    wl, md, dev = step([(900, 1), (64, 1)], 8, 2, 128)
-    q, kc, vc = wl.q.cuda(), wl.k_cache.cuda(), wl.v_cache.cuda()
-    lists = {(t, h): [0, 2, 3] for t in range(2) for h in range(2)}
-    sel, cnt = _tensors(lists, 2, 2, 3)
-    bounds = torch.ones(kc.shape[0], 2, pa.bounds_bytes(128), dtype=torch.uint8, device="cuda")
-    table = dev["block_tables"].clone()
-    table[:, 0] = table[0, 0]
-    m = (dev["seq_lens"], dev["query_start_loc"])
-    run = {
-        "select": lambda s: pa.pa_select_blocks(q, bounds, table, *m, 1, 900, 3, stream=s)[0],
-        "selected": lambda s: pa.pa_attention_selected(q, kc, vc, table, *m, 1, 900, wl.scale,
-                                                       sel, cnt, stream=s),
-        "attention": lambda s: pa.pa_attention(q, kc, vc, table, *m, 1, 900, wl.scale,
-                                               stream=s),
-        "window": lambda s: pa.pa_attention_window(q, kc, vc, table, *m, 1, 900, wl.scale, 100,
-                                                   stream=s),
-        "cascade": lambda s: pa.pa_attention_cascade(q, kc, vc, table, *m, 1, 900, wl.scale, 1,
-                                                     stream=s)}[name]
-    want = run(None)
-    spy = Spy(pa.load_library())
-    monkeypatch.setattr(pa, "_lib", spy)
-    side = torch.cuda.Stream()
-    torch.cuda.synchronize()
-    got = run(side.cuda_stream if as_handle else side)
-    ws, nbytes, handle = spy.args[-3:]
-    assert handle == side.cuda_stream and nbytes > 0
-    again = torch.empty(nbytes, dtype=torch.uint8, device="cuda")  # (not written)
-    assert again.data_ptr() + nbytes <= ws or ws + nbytes <= again.data_ptr()
-    side.synchronize()
-    assert torch.equal(got, want) and pa.pa_get_device_error() == 0
-
-
-BUILD_SIZES = """
-import sys
-import numpy as np
-import torch
-from tests.test_gpu_build_step import _case, _run
-# ascending: no earlier call has raised the kernel's shared memory
-for B in (4071, 4072, 4073, 4096, 4097, 16384, 4096, 64):
-    rng = np.random.default_rng(B)
-    lens = [(int(c), int(n)) for c, n in zip(rng.integers(0, 40, B), rng.integers(0, 3, B))]
-    _run(_case(rng, lens, pad=3))
-print("sizes ok")
-"""
-
-
-def test_step_sizes_around_48_kb_of_shared_memory():
-    """The kernel's static shared memory counts too: a fresh process, since the
-    opt-in to more lasts for the process."""
-    r = subprocess.run([sys.executable, "-c", BUILD_SIZES], cwd=ROOT, capture_output=True,
-                       text=True, timeout=300)
-    assert r.returncode == 0 and "sizes ok" in r.stdout, r.stderr[-2000:]
-
-
-def test_steps_of_different_sizes_from_two_threads():
-    """Each thread's launches find the shared memory that they need, whatever the
-    other asks for between."""
-    failed = []
-
-    def loop(B):
-        try:
-            i32 = dict(dtype=torch.int32, device="cuda")
-            stream = torch.cuda.Stream()
-            with torch.cuda.stream(stream):
-                new, done = torch.ones(B, **i32), torch.zeros(B, **i32)
-                table = torch.full((B, 1), -1, **i32)
-                free, count = torch.arange(B, **i32), torch.tensor([B], **i32)
-                for _ in range(300):
-                    out = pa.pa_build_step(new, done, table, free, count, B, B)
-                stream.synchronize()
-                assert int(out[4]) == 0 and out[1][-1] == B
-                assert torch.equal(out[3], 16 * torch.arange(B - 1, -1, -1, device="cuda"))
-        except Exception as e:  # noqa: BLE001 (a thread's failure is the test's)
-            failed.append((B, e))
-
-    threads = [threading.Thread(target=loop, args=(B,)) for B in (16384, 4200, 5000)]
-    for t in threads:
-        t.start()
-    for t in threads:
-        t.join()
-    assert not failed, failed
+@pytest.mark.parametrize("blocks", [2, 2000])
+@pytest.mark.parametrize("cache", ["bf16", "f16", "f32", "e4m3", "int4", "nvfp4"])
+def test_a_nan_query_makes_its_head_nan(cache, blocks):
+    """All of a head's scores are NaN, in every warp and every part."""
+    dtype = cache if cache in ("f16", "f32") else "bf16"
+    wl, md, dev = step([(16 * blocks - 3, 1)], 4, 1, 128, dtype, cache)
+    wl.q[0, 2, 17] = float("nan")
+    lists = {(0, 0): list(range(blocks))}
+    out = _run(wl, md, dev, lists, blocks).cpu()
     assert pa.pa_get_device_error() == 0
+    assert out[0, 2].isnan().all() and out[0, [0, 1, 3]].isfinite().all()
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 5, 2000])
+@pytest.mark.parametrize("cache", ["bf16", "f16", "f32", "e4m3"])
+def test_a_nan_key_alone_in_its_block(cache, blocks):
+    """The token's own key is the only visible one of the last block: its NaN is
+    the only score of the warp that takes the block."""
+    dtype = cache if cache in ("f16", "f32") else "bf16"
+    wl, md, dev = step([(16 * blocks - 15, 1)] * 2, 8, 2, 128, dtype, cache)
+    last = int(md["block_tables"][0, blocks - 1])
+    wl.k_cache[last, 1, 0, 3] = 0x7F if cache == "e4m3" else float("nan")
+    lists = {(t, h): list(range(blocks)) for t in range(2) for h in range(2)}
+    out = _run(wl, md, dev, lists, blocks).cpu()
+    assert pa.pa_get_device_error() == 0
+    assert out[0, 4:].isnan().all() and out[0, :4].isfinite().all()
+    assert out[1].isfinite().all()
 
 
 @pytest.mark.parametrize("group,D", [(4, 128), (8, 64), (16, 128), (20, 64)])
@@ -335,6 +260,111 @@ def test_one_token_of_a_qkv_row_in_place():
     assert torch.equal(kc, keys[0]) and torch.equal(vc, keys[1])
 
 
+class Spy:
+    """The library, with the arguments of the last call."""
+
+    def __init__(self, lib):
+        self.lib, self.args = lib, None
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+
+        def call(*args):
+            if not name.endswith("_size"):
+                self.args = args
+            return f(*args)
+        return call
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+@pytest.mark.parametrize("name", ["select", "selected", "attention", "window", "cascade"])
+def test_a_workspace_belongs_to_the_stream_it_is_used_on(name, as_handle, monkeypatch):
+    """A call on another stream than the current one: what it allocates is not
+    handed out again on the current stream while the kernels may still use it."""
+    wl, md, dev = step([(900, 1), (64, 1)], 8, 2, 128)
+    q, kc, vc = wl.q.cuda(), wl.k_cache.cuda(), wl.v_cache.cuda()
+    lists = {(t, h): [0, 2, 3] for t in range(2) for h in range(2)}
+    sel, cnt = _tensors(lists, 2, 2, 3)
+    bounds = torch.ones(kc.shape[0], 2, pa.bounds_bytes(128), dtype=torch.uint8, device="cuda")
+    table = dev["block_tables"].clone()
+    table[:, 0] = table[0, 0]
+    m = (dev["seq_lens"], dev["query_start_loc"])
+    run = {
+        "select": lambda s: pa.pa_select_blocks(q, bounds, table, *m, 1, 900, 3, stream=s)[0],
+        "selected": lambda s: pa.pa_attention_selected(q, kc, vc, table, *m, 1, 900, wl.scale,
+                                                       sel, cnt, stream=s),
+        "attention": lambda s: pa.pa_attention(q, kc, vc, table, *m, 1, 900, wl.scale,
+                                               stream=s),
+        "window": lambda s: pa.pa_attention_window(q, kc, vc, table, *m, 1, 900, wl.scale, 100,
+                                                   stream=s),
+        "cascade": lambda s: pa.pa_attention_cascade(q, kc, vc, table, *m, 1, 900, wl.scale, 1,
+                                                     stream=s)}[name]
+    want = run(None)
+    spy = Spy(pa.load_library())
+    monkeypatch.setattr(pa, "_lib", spy)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = run(side.cuda_stream if as_handle else side)
+    ws, nbytes, handle = spy.args[-3:]
+    assert handle == side.cuda_stream and nbytes > 0
+    again = torch.empty(nbytes, dtype=torch.uint8, device="cuda")  # (not written)
+    assert again.data_ptr() + nbytes <= ws or ws + nbytes <= again.data_ptr()
+    side.synchronize()
+    assert torch.equal(got, want) and pa.pa_get_device_error() == 0
+
+
+BUILD_SIZES = """
+import sys
+import numpy as np
+import torch
+from tests.test_gpu_build_step import _case, _run
+# ascending: no earlier call has raised the kernel's shared memory
+for B in (4071, 4072, 4073, 4096, 4097, 16384, 4096, 64):
+    rng = np.random.default_rng(B)
+    lens = [(int(c), int(n)) for c, n in zip(rng.integers(0, 40, B), rng.integers(0, 3, B))]
+    _run(_case(rng, lens, pad=3))
+print("sizes ok")
+"""
+
+
+def test_step_sizes_around_48_kb_of_shared_memory():
+    """The kernel's static shared memory counts too: a fresh process, since the
+    opt-in to more lasts for the process."""
+    r = subprocess.run([sys.executable, "-c", BUILD_SIZES], cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "sizes ok" in r.stdout, r.stderr[-2000:]
+
+
+def test_steps_of_different_sizes_from_two_threads():
+    """Each thread's launches find the shared memory that they need, whatever the
+    other asks for between."""
+    failed = []
+
+    def loop(B):
+        try:
+            i32 = dict(dtype=torch.int32, device="cuda")
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                new, done = torch.ones(B, **i32), torch.zeros(B, **i32)
+                table = torch.full((B, 1), -1, **i32)
+                free, count = torch.arange(B, **i32), torch.tensor([B], **i32)
+                for _ in range(300):
+                    out = pa.pa_build_step(new, done, table, free, count, B, B)
+                stream.synchronize()
+                assert int(out[4]) == 0 and out[1][-1] == B
+                assert torch.equal(out[3], 16 * torch.arange(B - 1, -1, -1, device="cuda"))
+        except Exception as e:  # noqa: BLE001 (a thread's failure is the test's)
+            failed.append((B, e))
+
+    threads = [threading.Thread(target=loop, args=(B,)) for B in (16384, 4200, 5000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    assert pa.pa_get_device_error() == 0
+
+
 @pytest.mark.parametrize("op", ["summarise", "select", "selected", "attention"])
 @pytest.mark.parametrize("broken", ["length", "offset", "last", "table"])
 def test_a_broken_request_without_tokens_is_flagged(op, broken):
@@ -388,3 +418,67 @@ def _bounds(kc, Hkv):
     b = rng.integers(0, 100, (kc.shape[0], Hkv, pa.bounds_bytes(128)), dtype=np.uint8)
     b[..., 256:260] = np.array([0.01], np.float32).view(np.uint8)
     return torch.from_numpy(b).cuda()
+
+
+def test_the_step_ends_at_the_first_request_without_a_block():
+    """The requests before it run, it and those behind it wait, one that needs
+    no block among them; a released block lets them go on."""
+    loop = Loop(11, [16, 40, 32, 30])
+    loop.prefill()
+    loop.count.fill_(1)
+    b = loop.buffers(4)
+    loop.fill(b, [1, 1, 1, 1])
+    loop.step(b, 1)
+    assert pa.pa_get_device_error() == pa.PA_DEV_ERR_NO_BLOCKS
+    assert loop.lens.tolist() == [17, 41, 32, 30] and b["qsl"].tolist() == [0, 1, 2, 2, 2]
+    loop.check(b)
+    loop.count.fill_(1)
+    loop.fill(b, [0, 0, 1, 1])
+    loop.step(b, 1)
+    assert pa.pa_get_device_error() == 0
+    assert loop.lens.tolist() == [17, 41, 33, 31]
+    loop.check(b)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_copied_block_gets_its_record_in_the_step_that_writes_to_it(cache):
+    """A request forked in the middle of a block: the block is copied, the next
+    token goes into the copy, and that step's summary makes the copy's record
+    before the selection reads it, whatever stood there."""
+    loop = Loop(12, [40, 1, 75], cache)
+    loop.check(loop.prefill())
+    new = int(loop.free[int(loop.count) - 1])
+    loop.count -= 1
+    old = int(loop.table[0, 2])
+    loop.table[1, :2] = loop.table[0, :2]
+    loop.table[1, 2] = new
+    loop.lens[1] = 40
+    loop.bounds[new] = 255  # codes of -1 and a NaN scale
+    pa.pa_copy_blocks(loop.kc, loop.vc, torch.tensor([[old, new]], device="cuda"))
+    b = loop.buffers(3)
+    for _ in range(10):  # into the next block
+        loop.fill(b, [1, 1, 1])
+        loop.step(b, 1)
+        loop.check(b)
+    assert pa.pa_get_device_error() == 0
+    assert not torch.equal(loop.bounds[old], loop.bounds[new])
+
+
+def test_a_copied_full_block_takes_its_record_along():
+    """A copy that no token is written to has no record of its own: the caller
+    copies the source's, as the caches' pages."""
+    loop = Loop(13, [64, 20])
+    loop.check(loop.prefill())
+    new = int(loop.free[int(loop.count) - 1])
+    loop.count -= 1
+    old = int(loop.table[0, 1])
+    loop.bounds[new] = 255
+    pa.pa_copy_blocks(loop.kc, loop.vc, torch.tensor([[old, new]], device="cuda"))
+    loop.bounds[new] = loop.bounds[old]
+    loop.table[0, 1] = new
+    loop.kc[old], loop.vc[old], loop.bounds[old] = 99, 99, 255
+    b = loop.buffers(2)
+    loop.fill(b, [1, 1])
+    loop.step(b, 1)
+    loop.check(b)
+    assert pa.pa_get_device_error() == 0
