@@ -248,8 +248,7 @@ __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_c
   const Divisor by(sc, kPg != kPgF32);
   const float s1 = low ? -sc : sc, rcp = low ? -by.rcp : by.rcp;
   // c = 1.5 x 2^23 + ceil(q) by a sum rounded up: the code is its lowest byte.
-  // The smallest values' sign turns about 1.5 x 2^23.  A scale that is a subnormal
-  // of few bits may leave a quotient well past 127, of either sign.
+  // The smallest values' sign turns about 1.5 x 2^23.
   constexpr float kUnit = 12582912.0f;
   const float turn = low ? -1.f : 1.f, about = low ? 2 * kUnit : 0.f;
   uint32_t c[8];
@@ -263,10 +262,11 @@ __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_c
       q = fmaf(fmaf(-q, s1, x[i]), rcp, q);
       q = fmaf(fmaf(-q, s1, x[i]), rcp, q);
     } else {
-      q = sc > 0.f ? __fdiv_rn(x[i], s1) : 0.f;
+      // (a scale that is a subnormal of few bits may leave a quotient well past 127,
+      // of either sign)
+      q = sc > 0.f ? fmaxf(__fdiv_rn(x[i], s1), -127.0f) : 0.f;
     }
-    c[i] = __float_as_uint(fmaf(__fadd_ru(fmaxf(fminf(q, 127.0f), -127.0f), kUnit), turn,
-                                about));
+    c[i] = __float_as_uint(fmaf(__fadd_ru(fminf(q, 127.0f), kUnit), turn, about));
   }
   uint32_t code[2];
 #pragma unroll
