@@ -472,6 +472,13 @@ pa_status pa_norm_rope_and_cache(
  * Sparse attention over selected blocks: for long contexts, each query reads
  * the blocks whose keys can matter most instead of all of them (no counterpart
  * on the pages; the same paged cache, tables and lengths as pa_attention).
+ * A token then reads the bounds of its context, 1/30 of a bf16 cache's bytes,
+ * and max_selected blocks.  When that pays, on a GB300 over a bf16 cache (32
+ * query / 8 KV heads of 128, 128 blocks): the three calls of a decode step took
+ * the time of pa_attention or less from 4K keys on, a third of it at 32K and one
+ * request, a tenth at 64K and 64 requests.  Every token reads its own bounds and
+ * blocks, so several tokens of one request gain less (64 tokens: 2x at 32K), and
+ * a prompt chunk of 512 tokens is faster by pa_attention.
  *
  *   pa_summarise_blocks    after a step's cache write: bounds of the keys of
  *                          the blocks it wrote to
@@ -498,7 +505,9 @@ pa_status pa_norm_rope_and_cache(
  * query_start_loc names all of a request's tokens as new (n_r = L_r) builds
  * all of its records.  Step arguments and their checks as pa_attention.  A
  * block copied by pa_copy_blocks has no record of its own until a token is
- * written to it: copy the source's record with it.
+ * written to it.  A block copied to be written to gets it from the call of that
+ * step; for one that is read first, copy the source's record as well
+ * (bounds[dst] = bounds[src]).
  * bounds : device, 16-byte aligned; other records are left as they were.
  */
 pa_status pa_summarise_blocks(const void* k_cache, pa_dtype cache_dtype,
@@ -523,7 +532,9 @@ pa_status pa_summarise_blocks(const void* k_cache, pa_dtype cache_dtype,
  *           sq = fl32(max |q| over the query heads of the KV head / 127)
  *   score = fl32(s * max over these heads of
  *                    sum_d qc_d * (qc_d >= 0 ? hi_d : lo_d))
- * with the block's codes hi, lo and scale s.  The sum is one of whole numbers:
+ * with the block's codes hi, lo and scale s.  The query's scale sq is that of all
+ * heads of the KV head: one much smaller than the largest has few codes and does
+ * not decide.  The sum is one of whole numbers:
  * equal inputs select equal blocks whatever the batch around them.  A query
  * element that is NaN counts as 0, a NaN score (of a record that was never
  * written) above all others; a block id out of range sets PA_DEV_ERR_BLOCK_ID

@@ -26,7 +26,7 @@
 // 64 tokens x 8 KV heads x 128 blocks of 128 channels, 4 query heads each: bf16 89
 // us, 6.0 TB/s (90 % of a copy); 32 x 8 x 256 blocks of E4M3, 8 heads: 56 us, 4.8
 // TB/s.  About 12 us of either are the way to the first page (list lengths,
-// request, block id, page: four dependent loads) and the join.  One token: 9.9 us.
+// request, block id, page: four dependent loads) and the join.  One token: 9.3 us.
 #include <algorithm>
 
 #include "pa_step.cuh"
@@ -170,7 +170,8 @@ struct PageTraits {
   // others; P V as well, over INT4 pages in bf16 (their scales are in P, which
   // then needs that range).  P is one f16 number (11 bits: off by 2^-11 of it), or
   // two bf16 numbers: one has 8 bits, and two keys' average was off by 5e-3, where
-  // pa_attention is within 2e-3.
+  // pa_attention is within 2e-3.  The second MMA per tile costs little beside the
+  // pages: 64 tokens x 8 heads x 128 blocks 89.2 us, with one part 88.7.
   static constexpr bool kQkBF = kPg == kB16;
   static constexpr bool kPvBF = kPg == kB16 || kPg == kI4;
   // NVFP4 values are decoded 2^-7 of their size, so that code and scale stay
@@ -1011,8 +1012,8 @@ __device__ __forceinline__ void join_cut(const SelParams& p, int2 cut) {
     return (2 * (int64_t)(cta + k) + (k == 0 ? 1 : 0)) * p.head_rows;
   };
   // Four channels per thread; the parts' loads go out together, eight at a time:
-  // one token's lists of 17 parts 9.9 us, with four at a time 10.7, with sixteen
-  // 9.2, but the batch of 64 tokens 91.5 instead of 89.
+  // one token's lists of 17 parts 9.3 us, with four at a time 10.1, with sixteen
+  // 9.1, but the batch of 64 tokens 92 instead of 89.
   constexpr int kQuads = kD / 4, kBatch = 8;
   for (int i = threadIdx.x; i < heads * kQuads; i += kJoinThreads) {
     const int hd = i / kQuads, d = (i - hd * kQuads) * 4;

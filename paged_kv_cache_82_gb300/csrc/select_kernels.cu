@@ -4,7 +4,7 @@
 // A block's record holds, per KV head and channel d, the largest and smallest
 // key value hi_d, lo_d of its written tokens as 8-bit codes of one scale s
 // (rounded outwards).  For a query q, sum_d max(q_d hi_d, q_d lo_d) is then at
-// least the score of the block's best key: the block's own bound, for 1/32 of
+// least the score of the block's best key: the block's own bound, for 1/30 of
 // the bytes of its bf16 K and V pages.
 //
 // The query is quantised to 8 bits too (one scale for the query heads of a KV
@@ -178,7 +178,7 @@ struct Range8 {
 // before it uses the first.  The page is read once and a 1/32 to 1/8 of its
 // bytes written, so the kernel is bound by HBM when there are many pages, and
 // by the chain of loads (lengths, block id, page) when there are few.  16 x 32K
-// tokens x 8 heads of 128, E4M3: 110 us, 5.6 TB/s; one block of 64 requests: 2.6 us.
+// tokens x 8 heads of 128, E4M3: 109 us, 5.6 TB/s; one block of 64 requests: 2.6 us.
 template <int kPg, int kD>
 __device__ __forceinline__ void summarise_one(const StepView& s, const void* k_cache,
                                               int num_kv_heads, int r, int nth, int h,
