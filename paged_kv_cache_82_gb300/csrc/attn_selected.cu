@@ -138,15 +138,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// x >= 0 as the sum of two bf16 numbers: its upper half, and what that leaves,
-// rounded; together off by 2^-16 of x.  Cut off and not rounded, the head leaves
-// a tail that is not negative, and a tail of 2^-126 at least is none that is 0:
-// both times an infinite value are the same infinity.
+// x as the sum of two bf16 numbers: its upper half, and what that leaves, rounded;
+// together off by 2^-16 of x.  Cut off and not rounded, the head leaves a tail of
+// x's sign.  kPositive, x >= 0: the tail is 2^-126 at least and not 0, so that both
+// times an infinite value are the same infinity.
 __device__ __forceinline__ uint32_t bf16_heads(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
+template <bool kPositive>
 __device__ __forceinline__ float bf16_tail(float x) {
-  return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u), 0x1p-126f);
+  const float tail = x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+  return kPositive ? fmaxf(tail, 0x1p-126f) : tail;
 }
 
 template <int kPg, int kD>
@@ -720,7 +722,7 @@ __device__ __forceinline__ bool attend_part(const SelParams& p, int64_t row, int
             x[0] *= s0, x[1] *= s0, x[2] *= s1, x[3] *= s1;
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = bf16_tail(x[j]);
+          for (int j = 0; j < 4; ++j) y[j] = bf16_tail<kPg == kB16>(x[j]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             pb[g][nt][j] = transpose8x8(bf16_heads(x[2 * j], x[2 * j + 1]));

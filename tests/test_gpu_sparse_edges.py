@@ -170,6 +170,24 @@ def test_short_lists_are_within_the_bar_of_pa_attention():
     assert (np.abs(full.double().cpu().numpy() - want) <= bar).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_int4_values_with_scales_of_either_sign(D):
+    """The values' scales go into the probabilities, whose two parts have their
+    sign: pages that another writer left with negative scales are read as such."""
+    wl, md, dev = step([(200, 1), (77, 2), (1, 1)], 16, 2, D, "bf16", "int4")
+    scales = wl.v_cache[..., 8 * D:].contiguous().view(torch.float32)
+    scales[..., 1::2] *= -1
+    wl.v_cache[..., 8 * D:] = scales.view(torch.uint8)
+    lists = _lists(np.random.default_rng(8), md, 2, 8)
+    out = _run(wl, md, dev, lists, 8)
+    assert pa.pa_get_device_error() == 0
+    want, mag, qk = _attend(wl, md, lists)
+    # two parts of a probability times its scale: off by 2^-16, as over bf16 pages
+    tol = (ref.half("bf16") * np.abs(want) + (1 + ref.half("bf16")) * (
+        2.0 ** -16 * mag + 2.0 ** -16 * (1 + qk) * mag + 2.0 ** -24))
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+
+
 @pytest.mark.parametrize("size", [1e5, 1e9, 1e13, 1e30])
 @pytest.mark.parametrize("cache", ["bf16", "f16", "f32", "e4m3", "int4", "nvfp4"])
 def test_scores_far_past_the_exponentials_range(cache, size):
