@@ -229,7 +229,7 @@ def _new(shape, dtype, device, stream, returned: bool = True) -> torch.Tensor:
     that neither what the memory held before nor what is put there after the
     tensor's release meets the call's kernels.  One that is returned is known to
     the current stream too, where the caller will use it."""
-    if stream is None:
+    if stream is None or device.type != "cuda":
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))

@@ -78,3 +78,18 @@ def test_a_cache_is_not_read_as_elements_of_another_size(dtype, name):
     for call in calls:
         with pytest.raises(ValueError, match=f"no {name} elements"):
             call(cache_dtype=name)
+
+
+def test_a_stream_does_not_make_host_tensors_pass():
+    """Tensors in the wrong place are named as such on a given stream too."""
+    i32 = dict(dtype=torch.int32)
+    q, cache = torch.zeros(1, 8, 128), torch.zeros(4, 2, 16, 128)
+    m = (torch.zeros(1, 4, **i32), torch.ones(1, **i32), torch.tensor([0, 1], **i32))
+    ws = torch.zeros(64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_attention_selected(q, cache, cache.clone(), *m, 1, 1, 0.1,
+                                 torch.zeros(1, 2, 1, **i32), torch.ones(1, 2, **i32),
+                                 workspace=ws, stream=7)
+    with pytest.raises(ValueError, match="CUDA"):
+        pa.pa_build_step(torch.ones(1, **i32), torch.zeros(1, **i32), torch.zeros(1, 4, **i32),
+                         torch.zeros(3, **i32), torch.ones(1, **i32), 8, 1, stream=7)
