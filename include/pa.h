@@ -645,6 +645,209 @@ pa_status pa_set_debug_bounds(int enable);
 pa_status pa_get_device_error(pa_stream_t stream, uint32_t* flags);
 
 /*
+ * Decoding with several hypotheses (beams, parallel samples) and with tokens that
+ * are taken back (drafts that were not accepted, contexts cut to the tokens that
+ * matter), without the host between steps.  Blocks are shared by reference counts
+ * ([Anatomy], "PagedAttention", the sharing and copy-on-write items):
+ *
+ *   pa_beam_select         the best continuations of each group of beams
+ *   pa_fork_blocks         rows take over other rows' blocks; what nobody holds any
+ *                          more goes back on the stack of free ids
+ *   pa_copy_blocks_layers  the copies of shared last blocks, in all layers
+ *   pa_compact_blocks      tokens dropped from rows
+ *   pa_move_tokens         the moves that close the gaps, in all layers
+ *
+ * extra_refs : int32 [num_blocks], a block's holders beyond the first: 0 for a block
+ * in one row's table (as pa_build_step hands them out) and for a free one.  Holders
+ * are the entries of block tables and whatever else keeps a block (a prefix cache).
+ *
+ * A beam step: pa_beam_select with num_selected = beam_width, whose `parents` are
+ * the `sources` of pa_fork_blocks, pa_copy_blocks_layers with the pairs that leaves,
+ * then pa_build_step for the new tokens.
+ */
+
+/*
+ * pa_beam_select -- the num_selected = K best continuations of each group of
+ * beam_width = W beams (beam search; no counterpart on the pages).
+ *
+ * For group g and its beam w (row g * W + w):
+ *   score(w, t) = beam_scores[g][w] + x_t - log(sum over u of exp(x_u)),
+ *   x = logits[g * W + w]
+ * over tokens t < vocab_size.  The K largest scores of a group, largest first;
+ * equal scores (to 64 bits): the lower beam first, within a beam the larger logit,
+ * then the lower token.  Scores are compared in 64 bits, closer ones than fp32 sums
+ * resolve by sums in two fp32 parts, and rounded to fp32 once.
+ *
+ * What is no candidate: a logit of -inf (a NaN logit counts as -inf, +inf as the
+ * largest fp32 number); any token of a beam whose beam_score is not finite (at the
+ * first step, give all beams but one -inf); a score below fp32's range.  Where a
+ * group has fewer than K candidates, the places left hold score -inf, parent -1 and
+ * token -1.
+ *
+ * logits       : device, PA_F32 / PA_F16 / PA_BF16; row r starts at element r *
+ *                row_stride >= vocab_size (any alignment of its elements).
+ * beam_scores  : device fp32 [num_groups][W].
+ * finished     : device uint8 [num_groups][W], or NULL: a beam with a non-zero entry
+ *                has ended and offers one candidate, itself: its unchanged score with
+ *                token end_token.  Its logits are not looked at.
+ * end_token    : a token, or -1 for none (then finished must be NULL).
+ * scores       : device fp32 [num_groups][K];  may be beam_scores if K = W.
+ * parents      : device int32 [num_groups][K]: row g * W + w of each pick.
+ * tokens       : device int32 [num_groups][K].
+ * finished_out : device uint8 [num_groups][K], or NULL: 1 where the token is
+ *                end_token, else 0; may be finished if K = W.
+ * workspace    : device, pa_beam_select_workspace_size bytes, 256-byte aligned.
+ * W <= 64, K <= 128, vocab_size <= 2^24 (else PA_ERR_UNSUPPORTED).
+ */
+pa_status pa_beam_select(const void* logits, pa_dtype logits_dtype, int num_groups,
+                         int beam_width, int vocab_size, int64_t row_stride,
+                         const float* beam_scores, const uint8_t* finished,
+                         int end_token, int num_selected, float* scores,
+                         int32_t* parents, int32_t* tokens, uint8_t* finished_out,
+                         void* workspace, size_t workspace_bytes, pa_stream_t stream);
+pa_status pa_beam_select_workspace_size(int num_groups, int beam_width, int vocab_size,
+                                        int num_selected, size_t* bytes);
+
+/*
+ * pa_fork_blocks -- rows of a step take over other rows' blocks: beams after a
+ * selection, samples that part from one prompt, rows that end ([Anatomy],
+ * "PagedAttention", the sharing and copy-on-write items; [V0vsV1], blocks_to_copy).
+ *
+ * Row r becomes what row s = sources[r] was (all rows at once): its length, and the
+ * ceil(length / 16) entries of its table.  s = -1: the row becomes empty; s = r: it
+ * stays.  A row nobody takes over is released.
+ *   extra_refs  changes by (rows that took over s) - 1 for each entry of each old
+ *               row s; a block without a holder left goes onto the stack of free
+ *               ids, in the order of the released rows' entries.
+ *   last block  a row whose length is not a multiple of 16 writes its next token
+ *               into its last block.  Where that block has other holders, the row
+ *               gets a block of its own, popped from the stack (after the pushes: a
+ *               step that replaces beams by beams needs no spare block), and
+ *               (shared, popped) becomes a pair of block_mapping, in row order.  Of
+ *               the rows that hold a block which nothing else holds, the first keeps
+ *               it.  Copy the pairs' blocks (pa_copy_blocks_layers) before the next
+ *               write or fork.  If the stack runs out, the remaining rows keep
+ *               sharing (PA_DEV_ERR_NO_BLOCKS): do not write; a later call with
+ *               s = r finds them again.
+ *
+ * sources          : device int32 [num_rows]; a value outside [-1, num_rows) sets
+ *                    PA_DEV_ERR_METADATA and counts as r.
+ * block_tables     : device int32 [num_rows][max_blocks_per_seq]; _out: the same
+ *                    shape, may be block_tables.  Entries past a row's blocks are
+ *                    left as they were.  An id outside [0, num_blocks) sets
+ *                    PA_DEV_ERR_BLOCK_ID and counts for nothing.
+ * seq_lens, _out   : device int32 [num_rows]; tokens in the cache (one out of range:
+ *                    PA_DEV_ERR_METADATA, counts as 0).
+ * extra_refs, _out : above; a count that falls below -1 sets PA_DEV_ERR_METADATA.
+ * free_blocks      : device int32 [free_capacity], as pa_build_step, pushed to here
+ *                    (past its capacity: PA_DEV_ERR_METADATA, the id is lost).
+ * free_count, _out : device int32.
+ * block_mapping    : device int64 [num_rows][2]; past the pairs: (-1, -1).
+ * num_pairs        : device int32.
+ * Every _out may be its input (updated in place); nothing else may overlap.
+ * workspace        : device, pa_fork_blocks_workspace_size bytes, 256-byte aligned.
+ * num_rows <= 4096, num_rows * max_blocks_per_seq < 2^30 (else PA_ERR_UNSUPPORTED).
+ */
+pa_status pa_fork_blocks(const int32_t* sources, int num_rows,
+                         const int32_t* block_tables, int32_t* block_tables_out,
+                         int max_blocks_per_seq, const int32_t* seq_lens,
+                         int32_t* seq_lens_out, const int32_t* extra_refs,
+                         int32_t* extra_refs_out, int64_t num_blocks, int block_size,
+                         int32_t* free_blocks, int64_t free_capacity,
+                         const int32_t* free_count, int32_t* free_count_out,
+                         int64_t* block_mapping, int32_t* num_pairs, void* workspace,
+                         size_t workspace_bytes, pa_stream_t stream);
+pa_status pa_fork_blocks_workspace_size(int num_rows, int max_blocks_per_seq,
+                                        size_t* bytes);
+
+/*
+ * pa_copy_blocks_layers -- pa_copy_blocks in the caches of num_layers layers, of as
+ * many pairs as the device says.
+ *
+ * k_cache, v_cache : the first layer's; the next layers' follow k_layer_stride (resp.
+ *                    v_layer_stride) BYTES apart, a multiple of 16 and no less than a
+ *                    layer's bytes.  K and V may lie layer by layer in one buffer.
+ * block_mapping    : device int64 [max_pairs][2], as pa_copy_blocks.
+ * num_pairs        : device int32, pairs that there are (outside [0, max_pairs]:
+ *                    PA_DEV_ERR_METADATA, clamped); NULL: max_pairs.
+ * Of a block's bounds (pa_summarise_blocks), see there.
+ */
+pa_status pa_copy_blocks_layers(void* k_cache, void* v_cache, pa_dtype cache_dtype,
+                                int num_layers, int64_t k_layer_stride,
+                                int64_t v_layer_stride, int64_t num_blocks,
+                                int block_size, int num_kv_heads, int head_dim,
+                                const int64_t* block_mapping, int64_t max_pairs,
+                                const int32_t* num_pairs, pa_stream_t stream);
+
+/*
+ * pa_compact_blocks -- tokens dropped from rows: the branches of a draft tree that
+ * were not accepted, or all but the tokens that matter of a long context (no
+ * counterpart on the pages).
+ *
+ * Row r keeps its first keep_start[r] tokens and the tokens at the keep_lens[r]
+ * positions keep[r][..], ascending, in [keep_start[r], seq_lens[r]); they become its
+ * tokens 0 .. n - 1.  (Keys stay rotated as they are.)  keep_lens[r] < 0: the row is
+ * left as it is.  From the first block that changes on, or that holds the row's end,
+ *   a block among the first ceil(n / 16) is kept if the row is its only holder, else
+ *   replaced by one popped from the stack (in the order of the rows' entries; the
+ *   rows whose running need fits the stack are served, the others left as they are,
+ *   PA_DEV_ERR_NO_BLOCKS);
+ *   replaced blocks and those past ceil(n / 16) lose a reference, and without one go
+ *   onto the stack (after the pops) as in pa_fork_blocks.
+ * The tokens to move are listed: the i-th of row r from src_slots[r][i] to
+ * dst_slots[r][i], i < num_moves[r] <= max_keep + 15.  Run pa_move_tokens on the list
+ * before anything is written to the cache or popped from the stack.  Rebuild the
+ * records of changed blocks (pa_summarise_blocks) where they are used.
+ *
+ * keep       : device int32 [num_rows][max_keep].
+ * keep_lens  : device int32 [num_rows].
+ * keep_start : device int32 [num_rows], or NULL: 0.
+ *              A list that is not ascending or leaves its range, or a length out of
+ *              range, sets PA_DEV_ERR_METADATA; that row is left as it is.
+ * block_tables .. free_count_out : as pa_fork_blocks.
+ * src_slots, dst_slots : device int64 [num_rows][max_keep + 16]; entries past
+ *              num_moves are left as they were; -1 where a table entry is no block.
+ * num_moves  : device int32 [num_rows].
+ * workspace  : device, pa_compact_blocks_workspace_size bytes, 256-byte aligned.
+ * Every _out may be its input; limits as pa_fork_blocks, and num_rows * max_keep <
+ * 2^31.
+ */
+pa_status pa_compact_blocks(const int32_t* keep, int max_keep, const int32_t* keep_lens,
+                            const int32_t* keep_start, int num_rows,
+                            const int32_t* block_tables, int32_t* block_tables_out,
+                            int max_blocks_per_seq, const int32_t* seq_lens,
+                            int32_t* seq_lens_out, const int32_t* extra_refs,
+                            int32_t* extra_refs_out, int64_t num_blocks, int block_size,
+                            int32_t* free_blocks, int64_t free_capacity,
+                            const int32_t* free_count, int32_t* free_count_out,
+                            int64_t* src_slots, int64_t* dst_slots, int32_t* num_moves,
+                            void* workspace, size_t workspace_bytes, pa_stream_t stream);
+pa_status pa_compact_blocks_workspace_size(int num_rows, int max_blocks_per_seq,
+                                           size_t* bytes);
+
+/*
+ * pa_move_tokens -- tokens' keys and values moved from slot to slot, in place, in the
+ * caches of all layers.
+ *
+ * For each row r and i < num_moves[r], in this order, the K and V of all heads at
+ * src_slots[r][i] go to dst_slots[r][i] (with their scales, 4-bit pages); a negative
+ * slot: no move.  A slot beyond the cache sets PA_DEV_ERR_SLOT, no move.
+ * A move's destination must be neither a later source of its row, nor any slot that
+ * another row reads or writes, nor another destination: what pa_compact_blocks lists
+ * is so.
+ * Caches and layers as pa_copy_blocks_layers.
+ * src_slots, dst_slots : device int64 [num_rows][max_moves].
+ * num_moves            : device int32 [num_rows] (outside [0, max_moves]:
+ *                        PA_DEV_ERR_METADATA, the row is not moved).
+ */
+pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype cache_dtype,
+                         int num_layers, int64_t k_layer_stride, int64_t v_layer_stride,
+                         int64_t num_blocks, int block_size, int num_kv_heads,
+                         int head_dim, const int64_t* src_slots,
+                         const int64_t* dst_slots, const int32_t* num_moves,
+                         int num_rows, int64_t max_moves, pa_stream_t stream);
+
+/*
  * pa_attention_noalloc -- pa_attention without a caller-provided workspace.
  * No counterpart on the pages: it exists for callers that cannot allocate
  * device memory per step -- for instance an engine that gives all free HBM

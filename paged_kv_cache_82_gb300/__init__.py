@@ -16,6 +16,11 @@ calls raise; nothing falls back.
     pa_norm_rope_and_cache -- q/k norm per head, position rotation, K/V write
     pa_summarise_blocks, pa_select_blocks, pa_attention_selected -- attention
                              over the blocks that a cheap score selects
+    pa_beam_select        -- the best continuations of each group of beams
+    pa_fork_blocks        -- rows take over other rows' blocks, by references
+    pa_compact_blocks     -- tokens dropped from rows
+    pa_copy_blocks_layers, pa_move_tokens -- the copies and moves that these
+                             two leave, in the caches of all layers
 """
 from __future__ import annotations
 
@@ -47,7 +52,11 @@ EXPORTED = ("pa_status_string", "pa_reshape_and_cache", "pa_copy_blocks",
             "pa_attention_cascade_workspace_size", "pa_build_step",
             "pa_norm_rope_and_cache", "pa_summarise_blocks",
             "pa_select_blocks_workspace_size", "pa_select_blocks",
-            "pa_attention_selected_workspace_size", "pa_attention_selected")
+            "pa_attention_selected_workspace_size", "pa_attention_selected",
+            "pa_beam_select_workspace_size", "pa_beam_select",
+            "pa_fork_blocks_workspace_size", "pa_fork_blocks",
+            "pa_copy_blocks_layers", "pa_compact_blocks_workspace_size",
+            "pa_compact_blocks", "pa_move_tokens")
 
 _DT = {"f32": PA_F32, "f16": PA_F16, "bf16": PA_BF16, "e4m3": PA_FP8_E4M3,
        "int4": PA_INT4, "nvfp4": PA_NVFP4}
@@ -180,6 +189,28 @@ def load_library(path: str = LIB_PATH):
         P, i32, P, P, i32, i64, i32, i32, i32, i32, P, i32, P, P, i32, i64, i32,
         i32, P, P, i32, f32, f32, f32, P, P, sz, P]
     lib.pa_attention_selected.restype = i32
+    size_out = ctypes.POINTER(sz)
+    lib.pa_beam_select_workspace_size.argtypes = [i32, i32, i32, i32, size_out]
+    lib.pa_beam_select_workspace_size.restype = i32
+    lib.pa_beam_select.argtypes = [P, i32, i32, i32, i32, i64, P, P, i32, i32, P, P,
+                                   P, P, P, sz, P]
+    lib.pa_beam_select.restype = i32
+    lib.pa_fork_blocks_workspace_size.argtypes = [i32, i32, size_out]
+    lib.pa_fork_blocks_workspace_size.restype = i32
+    lib.pa_fork_blocks.argtypes = [P, i32, P, P, i32, P, P, P, P, i64, i32, P, i64, P,
+                                   P, P, P, P, sz, P]
+    lib.pa_fork_blocks.restype = i32
+    lib.pa_copy_blocks_layers.argtypes = [P, P, i32, i32, i64, i64, i64, i32, i32, i32,
+                                          P, i64, P, P]
+    lib.pa_copy_blocks_layers.restype = i32
+    lib.pa_compact_blocks_workspace_size.argtypes = [i32, i32, size_out]
+    lib.pa_compact_blocks_workspace_size.restype = i32
+    lib.pa_compact_blocks.argtypes = [P, i32, P, P, i32, P, P, i32, P, P, P, P, i64, i32,
+                                      P, i64, P, P, P, P, P, P, sz, P]
+    lib.pa_compact_blocks.restype = i32
+    lib.pa_move_tokens.argtypes = [P, P, i32, i32, i64, i64, i64, i32, i32, i32, P, P, P,
+                                   i32, i64, P]
+    lib.pa_move_tokens.restype = i32
     _lib = lib
     return lib
 
@@ -830,3 +861,244 @@ def pa_attention_selected(q: torch.Tensor, k_cache: torch.Tensor,
         workspace.nbytes, _stream(stream))
     _check(st, "pa_attention_selected")
     return out
+
+
+def _size(name: str, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(getattr(_load(), name)(*args, ctypes.byref(out)), name)
+    return int(out.value)
+
+
+def pa_beam_select_workspace_size(num_groups: int, beam_width: int, vocab_size: int,
+                                  num_selected: int) -> int:
+    return _size("pa_beam_select_workspace_size", num_groups, beam_width, vocab_size,
+                 num_selected)
+
+
+def pa_beam_select(logits: torch.Tensor, beam_scores: torch.Tensor, num_selected: int,
+                   finished: Optional[torch.Tensor] = None, end_token: int = -1,
+                   scores: Optional[torch.Tensor] = None,
+                   parents: Optional[torch.Tensor] = None,
+                   tokens: Optional[torch.Tensor] = None,
+                   finished_out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """logits [B * W, V] (rows may be slices of longer ones); beam_scores fp32 [B, W];
+    finished uint8 (or bool) [B, W].  Returns (scores fp32 [B, K], parents int32
+    [B, K], rows of logits, tokens int32 [B, K]), allocated where not given; 1 where a
+    token is end_token goes to finished_out [B, K] if given.  scores may be beam_scores
+    and finished_out may be finished if K = W (updated in place)."""
+    shape, rows = beam_scores.shape, logits.shape
+    if len(shape) != 2 or len(rows) != 2 or rows[0] != shape[0] * shape[1]:
+        raise ValueError("logits must be [B * W, V] and beam_scores [B, W]")
+    B, W = shape
+    V, K = rows[1], int(num_selected)
+    stride, one = logits.stride()
+    if one != 1 and V > 1:
+        raise ValueError("logits must have contiguous rows")
+    # (a single row is contiguous whatever its stride)
+    stride = stride if rows[0] > 1 else V
+    if stride < V:
+        raise ValueError("rows of logits overlap")
+    if scores is None:
+        scores = _new((B, K), torch.float32, logits.device, stream)
+    if parents is None:
+        parents = _new((B, K), _I32, logits.device, stream)
+    if tokens is None:
+        tokens = _new((B, K), _I32, logits.device, stream)
+    if workspace is None:
+        n = pa_beam_select_workspace_size(B, W, V, K)
+        workspace = _new(max(n, 1), _U8, logits.device, stream, False)
+    for name, t in (("finished", finished), ("finished_out", finished_out)):
+        if t is not None and t.dtype not in (_U8, torch.bool):
+            raise ValueError(f"{name} must be a uint8 or bool tensor")
+    _plain(("beam_scores", beam_scores, torch.float32, B * W),
+           ("finished", finished, None, B * W), ("scores", scores, torch.float32, B * K),
+           ("parents", parents, _I32, B * K), ("tokens", tokens, _I32, B * K),
+           ("finished_out", finished_out, None, B * K),
+           ("workspace", workspace, None, None))
+    if logits.get_device() != scores.get_device():
+        raise ValueError("logits must be on the current CUDA device")
+    st = _load().pa_beam_select(
+        logits.data_ptr(), _dtype_code(logits), B, W, V, stride, beam_scores.data_ptr(),
+        _ptr(finished), int(end_token), K, scores.data_ptr(), parents.data_ptr(),
+        tokens.data_ptr(), _ptr(finished_out), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    _check(st, "pa_beam_select")
+    return scores, parents, tokens
+
+
+def _rows_state(block_tables, seq_lens, extra_refs, free_blocks, free_count,
+                block_tables_out, seq_lens_out, extra_refs_out, free_count_out):
+    """Check the state that pa_fork_blocks and pa_compact_blocks change: (rows, table
+    entries of each, specs for _plain, pointers in the ABI's order: tables .. refs,
+    then the stack's)."""
+    if len(block_tables.shape) != 2:
+        raise ValueError("block_tables must be [R, M]")
+    R, M = block_tables.shape
+    bto = block_tables if block_tables_out is None else block_tables_out
+    slo = seq_lens if seq_lens_out is None else seq_lens_out
+    ero = extra_refs if extra_refs_out is None else extra_refs_out
+    fco = free_count if free_count_out is None else free_count_out
+    if bto.shape != block_tables.shape:
+        raise ValueError("block_tables_out must be a tensor like block_tables")
+    NB = extra_refs.numel()
+    specs = (("block_tables", block_tables, _I32, None), ("block_tables_out", bto, _I32, None),
+             ("seq_lens", seq_lens, _I32, R), ("seq_lens_out", slo, _I32, R),
+             ("extra_refs", extra_refs, _I32, None), ("extra_refs_out", ero, _I32, NB),
+             ("free_blocks", free_blocks, _I32, None), ("free_count", free_count, _I32, 1),
+             ("free_count_out", fco, _I32, 1))
+    tables = (block_tables.data_ptr(), bto.data_ptr(), M, seq_lens.data_ptr(),
+              slo.data_ptr(), extra_refs.data_ptr(), ero.data_ptr(), NB, BLOCK_SIZE,
+              free_blocks.data_ptr(), free_blocks.numel(), free_count.data_ptr(),
+              fco.data_ptr())
+    return R, M, specs, tables
+
+
+def pa_fork_blocks_workspace_size(num_rows: int, max_blocks_per_seq: int) -> int:
+    return _size("pa_fork_blocks_workspace_size", num_rows, max_blocks_per_seq)
+
+
+def pa_fork_blocks(sources: torch.Tensor, block_tables: torch.Tensor,
+                   seq_lens: torch.Tensor, extra_refs: torch.Tensor,
+                   free_blocks: torch.Tensor, free_count: torch.Tensor,
+                   block_tables_out: Optional[torch.Tensor] = None,
+                   seq_lens_out: Optional[torch.Tensor] = None,
+                   extra_refs_out: Optional[torch.Tensor] = None,
+                   free_count_out: Optional[torch.Tensor] = None,
+                   block_mapping: Optional[torch.Tensor] = None,
+                   num_pairs: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """sources int32 [R] (a row, or -1: becomes empty); block_tables int32 [R, M];
+    seq_lens int32 [R], tokens in the cache; extra_refs int32 [num_blocks]; free_blocks
+    int32 [F], a stack of free ids; free_count int32 [1].  All but sources are updated
+    in place where no *_out is given.  Returns (block_mapping int64 [R, 2], num_pairs
+    int32 [1]), the copies to make (pa_copy_blocks_layers), allocated where not given."""
+    R, M, specs, rows = _rows_state(block_tables, seq_lens, extra_refs, free_blocks,
+                                    free_count, block_tables_out, seq_lens_out,
+                                    extra_refs_out, free_count_out)
+    dev = block_tables.device
+    if block_mapping is None:
+        block_mapping = _new((R, 2), _I64, dev, stream)
+    if num_pairs is None:
+        num_pairs = _new(1, _I32, dev, stream)
+    if workspace is None:
+        n = pa_fork_blocks_workspace_size(R, M)
+        workspace = _new(max(n, 1), _U8, dev, stream, False)
+    _plain(("sources", sources, _I32, R), *specs, ("block_mapping", block_mapping, _I64, 2 * R),
+           ("num_pairs", num_pairs, _I32, 1), ("workspace", workspace, None, None))
+    st = _load().pa_fork_blocks(
+        sources.data_ptr(), R, *rows, block_mapping.data_ptr(), num_pairs.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check(st, "pa_fork_blocks")
+    return block_mapping, num_pairs
+
+
+def _layers(k_cache: torch.Tensor, v_cache: torch.Tensor, cache_dtype: Optional[str]):
+    """(num_layers, byte strides between the layers of K and V, num_blocks, block size,
+    KV heads, head_dim) of caches [L, NB, Hkv, 16, D] (4-bit: [L, NB, Hkv, bytes]), or of
+    one layer's without the first dimension.  Within a layer they are contiguous."""
+    if v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("both caches must be alike")
+    four_bit = cache_dtype in ("int4", "nvfp4")
+    if k_cache.dim() == (3 if four_bit else 4):
+        k_cache, v_cache = k_cache.unsqueeze(0), v_cache.unsqueeze(0)
+    elif k_cache.dim() != (4 if four_bit else 5):
+        raise ValueError("the caches must be [L, NB, Hkv, 16, D] or [NB, Hkv, 16, D]"
+                         + (" with pages of bytes" if four_bit else ""))
+    L = k_cache.shape[0]
+    if L < 1:
+        raise ValueError("the caches hold no layer")
+    NB, Hkv, bs, D = _cache_geometry(k_cache[0], cache_dtype)
+    strides, dev = [], torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t[0].is_contiguous():
+            raise ValueError(f"{n} must be contiguous within a layer")
+        if t.get_device() < 0 or t.get_device() != dev:
+            raise ValueError(f"{n} must be on the current CUDA device")
+        strides.append(t.stride(0) * t.element_size())
+    return (L, *strides, NB, bs, Hkv, D)
+
+
+def pa_copy_blocks_layers(k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_mapping: torch.Tensor,
+                          num_pairs: Optional[torch.Tensor] = None,
+                          cache_dtype: Optional[str] = None, stream=None) -> None:
+    """pa_copy_blocks in the caches of all layers, [L, NB, Hkv, 16, D] each (a layer's
+    place in them may be a slice, as of one buffer for K and V): block_mapping int64
+    [P, 2] of (src, dst) pairs, the first num_pairs int32 [1] of them (None: all)."""
+    if len(block_mapping.shape) != 2 or block_mapping.shape[1] != 2:
+        raise ValueError("block_mapping must be [P, 2]")
+    geometry = _layers(k_cache, v_cache, cache_dtype)
+    _plain(("block_mapping", block_mapping, _I64, None), ("num_pairs", num_pairs, _I32, 1))
+    st = _load().pa_copy_blocks_layers(
+        k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache, cache_dtype), *geometry,
+        block_mapping.data_ptr(), block_mapping.shape[0], _ptr(num_pairs), _stream(stream))
+    _check(st, "pa_copy_blocks_layers")
+
+
+def pa_compact_blocks_workspace_size(num_rows: int, max_blocks_per_seq: int) -> int:
+    return _size("pa_compact_blocks_workspace_size", num_rows, max_blocks_per_seq)
+
+
+def pa_compact_blocks(keep: torch.Tensor, keep_lens: torch.Tensor,
+                      block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                      extra_refs: torch.Tensor, free_blocks: torch.Tensor,
+                      free_count: torch.Tensor, keep_start: Optional[torch.Tensor] = None,
+                      block_tables_out: Optional[torch.Tensor] = None,
+                      seq_lens_out: Optional[torch.Tensor] = None,
+                      extra_refs_out: Optional[torch.Tensor] = None,
+                      free_count_out: Optional[torch.Tensor] = None,
+                      src_slots: Optional[torch.Tensor] = None,
+                      dst_slots: Optional[torch.Tensor] = None,
+                      num_moves: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """keep int32 [R, K], ascending positions of the tokens kept behind the first
+    keep_start int32 [R] (None: 0) of each row, keep_lens int32 [R] of them (negative:
+    the row stays as it is); the rows' state as pa_fork_blocks, updated in place where
+    no *_out is given.  Returns (src_slots int64 [R, K + 16], dst_slots, num_moves int32
+    [R]), the moves to make (pa_move_tokens), allocated where not given."""
+    if len(keep.shape) != 2:
+        raise ValueError("keep must be [R, K]")
+    R, M, specs, rows = _rows_state(block_tables, seq_lens, extra_refs, free_blocks,
+                                    free_count, block_tables_out, seq_lens_out,
+                                    extra_refs_out, free_count_out)
+    K, dev = keep.shape[1], block_tables.device
+    if src_slots is None:
+        src_slots = _new((R, K + BLOCK_SIZE), _I64, dev, stream)
+    if dst_slots is None:
+        dst_slots = _new((R, K + BLOCK_SIZE), _I64, dev, stream)
+    if num_moves is None:
+        num_moves = _new(R, _I32, dev, stream)
+    if workspace is None:
+        n = pa_compact_blocks_workspace_size(R, M)
+        workspace = _new(max(n, 1), _U8, dev, stream, False)
+    _plain(("keep", keep, _I32, R * K), ("keep_lens", keep_lens, _I32, R),
+           ("keep_start", keep_start, _I32, R), *specs,
+           ("src_slots", src_slots, _I64, R * (K + BLOCK_SIZE)),
+           ("dst_slots", dst_slots, _I64, R * (K + BLOCK_SIZE)),
+           ("num_moves", num_moves, _I32, R), ("workspace", workspace, None, None))
+    st = _load().pa_compact_blocks(
+        keep.data_ptr(), K, keep_lens.data_ptr(), _ptr(keep_start), R, *rows,
+        src_slots.data_ptr(), dst_slots.data_ptr(), num_moves.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check(st, "pa_compact_blocks")
+    return src_slots, dst_slots, num_moves
+
+
+def pa_move_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, src_slots: torch.Tensor,
+                   dst_slots: torch.Tensor, num_moves: torch.Tensor,
+                   cache_dtype: Optional[str] = None, stream=None) -> None:
+    """Moves K and V of tokens from slot to slot in the caches of all layers, in place:
+    src_slots, dst_slots int64 [R, N], the first num_moves int32 [R] of each row, in
+    order; caches as pa_copy_blocks_layers."""
+    if len(src_slots.shape) != 2 or dst_slots.shape != src_slots.shape:
+        raise ValueError("src_slots and dst_slots must be [R, N]")
+    R, N = src_slots.shape
+    geometry = _layers(k_cache, v_cache, cache_dtype)
+    _plain(("src_slots", src_slots, _I64, None), ("dst_slots", dst_slots, _I64, None),
+           ("num_moves", num_moves, _I32, R))
+    st = _load().pa_move_tokens(
+        k_cache.data_ptr(), v_cache.data_ptr(), _dtype_code(k_cache, cache_dtype), *geometry,
+        src_slots.data_ptr(), dst_slots.data_ptr(), num_moves.data_ptr(), R, N,
+        _stream(stream))
+    _check(st, "pa_move_tokens")

@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(HERE, "libpa.so")
 SOURCES = ["pa_api.cu", "cache_kernels.cu", "attn_fast.cu", "attn_prefill_tc.cu",
            "attn_generic.cu",
            "pa_noalloc.cu", "step_kernels.cu", "rope_bf16.cu", "rope_f16.cu",
-           "rope_f32.cu", "select_kernels.cu", "attn_selected.cu"]
+           "rope_f32.cu", "select_kernels.cu", "attn_selected.cu", "beam_kernels.cu",
+           "fork_kernels.cu", "move_kernels.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I" + INCLUDE]

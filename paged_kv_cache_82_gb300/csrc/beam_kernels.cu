@@ -1,0 +1,634 @@
+// beam_kernels.cu -- the best continuations of each group of beams
+// (pa_beam_select).
+//
+//   score(w, t) = beam_scores[w] + x[w][t] - log sum_u exp(x[w][u])
+//   the K largest over the W beams and V tokens of a group
+//
+// Each logit is read once.  A CTA takes a chunk of a row into registers and
+// leaves the chunk's maximum m, its sum of exp(x - m) and its K largest logits;
+// a second kernel, one CTA per group, joins the sums of each row (the running
+// maximum of an online softmax, over chunks) and picks K of the W x chunks x K
+// candidates.
+//
+// The K largest of a chunk without sorting it: eight warps, each with its q-th
+// largest lane maximum, q = ceil(K / 8); the smallest of these eight numbers is
+// a threshold that at least 8 q >= K logits reach, and about 20 of 8192 do for K
+// = 8.  Those go to a list in shared memory, where each counts the larger ones.
+//
+// Which tokens come back must not depend on the rounding of fp32 sums: scores are
+// compared in 64 bits, and where two beams' scores lie closer than the fp32 sums
+// resolve (kNear), the sums of those rows are taken again with exponentials in
+// two fp32 parts and the group is picked again (about one group in 2000 of
+// unlike beams, always for beams that are copies of each other).
+#include <float.h>
+#include <math.h>
+
+#include "pa_beam.h"
+#include "pa_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kWarps = kBeamThreads / 32;
+constexpr int kListCap = 1024;
+// log2(e) in two parts, the first rounded towards zero so that the second is
+// positive (a product with -inf then keeps its sign)
+constexpr float kLog2eHi = 1.44269502162933349609375f;
+constexpr float kLog2eLo = 1.925963033500789e-8f;
+// Two scores' difference from which on the fp32 sums decide.  A row's log-sum is
+// off by at most: 2^-22 (the exponential) + ln 2 x 2^-23 x the mean of |log2 p|
+// over the row, below log2 V <= 24 (the exponent's two roundings) + 18 x 2^-24 (8
+// additions in a thread, 10 above) + 2^-22 (chunks joined) = 3.5e-6.
+constexpr double kNear = 1e-5;
+
+// ---- order of logits ---------------------------------------------------------
+// whole numbers in the order of the floats (-0 = 0)
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t ordered(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
+  return b >> 63 ? ~b : b | (1ull << 63);
+}
+// a logit and its token: larger keys are better (equal logits: the lower token);
+// 0: none
+__device__ __forceinline__ uint64_t make_key(float x, int token) {
+  return (uint64_t)ordered(x) << 32 | (uint32_t)~token;
+}
+// NaN counts as -inf, +inf as the largest number
+__device__ __forceinline__ float clean(float x) {
+  return fminf(fmaxf(x, -INFINITY), FLT_MAX);
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t warp_max_u64(uint64_t v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    const uint64_t o = __shfl_xor_sync(~0u, v, d);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// This warp's q-th largest of its lanes' numbers (0 where there are fewer than
+// q above 0).
+__device__ __forceinline__ uint32_t warp_qth_largest(uint32_t v, int q) {
+  uint32_t top = __reduce_max_sync(~0u, v);
+  for (int i = 1; i < q && i < 32; ++i) {
+    const unsigned who = __ballot_sync(~0u, v == top);
+    if ((threadIdx.x & 31) == __ffs(who) - 1) v = 0;
+    top = __reduce_max_sync(~0u, v);
+  }
+  return q > 32 ? 0 : top;
+}
+
+// ---- elements of a 16-byte load ------------------------------------------------
+template <typename T>
+struct Pack;
+template <>
+struct Pack<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return __uint_as_float(w);
+  }
+  static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
+  static constexpr uint32_t kNegInf = 0xff800000u;
+};
+template <>
+struct Pack<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) {
+    return __bfloat16_as_ushort(*p);
+  }
+  static constexpr uint32_t kNegInf = 0xff80u;
+};
+template <>
+struct Pack<__half> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
+    return __half2float(__ushort_as_half((unsigned short)(i & 1 ? w >> 16 : w & 0xffffu)));
+  }
+  static __device__ __forceinline__ uint32_t bits(const __half* p) { return __half_as_ushort(*p); }
+  static constexpr uint32_t kNegInf = 0xfc00u;
+};
+
+// the elements [i0, i0 + kN) of a row of n, 16-byte aligned where whole; what lies
+// outside the row is -inf and not read
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T* row, int64_t i0, int n) {
+  constexpr int kN = Pack<T>::kN;
+  if (i0 >= 0 && i0 + kN <= n)
+    return __ldcs(reinterpret_cast<const uint4*>(row + i0));
+  uint32_t w[4];
+  constexpr int kPer = kN / 4;  // elements of a 32-bit word
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[k] = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int64_t i = i0 + k * kPer + e;
+      const uint32_t b = i >= 0 && i < n ? Pack<T>::bits(row + i) : Pack<T>::kNegInf;
+      w[k] |= b << (e * 16);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct BeamK {
+  BeamArgs a;
+  int chunks;
+  uint64_t* keys;  // [rows][chunks][K], best first
+  float2* stats;   // [rows][chunks]: maximum, sum of exp(x - maximum)
+};
+
+// One chunk of one row.
+template <typename T, int kVecs>
+__global__ void __launch_bounds__(kBeamThreads) beam_chunk_kernel(BeamK p) {
+  using P = Pack<T>;
+  constexpr int kN = P::kN, kE = kVecs * kN;
+  __shared__ uint64_t list[kListCap];
+  __shared__ uint32_t s_max[kWarps], s_bar[kWarps];
+  __shared__ float s_sum[kWarps];
+  __shared__ uint64_t s_best[kWarps];
+  __shared__ int s_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / (unsigned)p.chunks;
+  const int chunk = (int)(blockIdx.x - row * p.chunks);
+  const int K = p.a.num_selected, V = p.a.vocab_size;
+  pdl_launch_dependents();
+  if (p.a.finished && p.a.finished[row]) return;  // (its logits are not looked at)
+  const T* x = static_cast<const T*>(p.a.logits) + row * p.a.row_stride;
+  // the row seen from the 16-byte boundary at or before its start
+  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  const int64_t base = (int64_t)chunk * (kBeamThreads * kE) + tid * kN - off;
+  uint4 v[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+    v[i] = load_vec<T>(x, base + (int64_t)i * kBeamThreads * kN, V);
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int j = 0; j < kN; ++j) m = fmaxf(m, P::get(v[i], j));
+  m = fminf(m, FLT_MAX);
+  const uint32_t om = ordered(m);
+  // (at least q lanes of each warp reach the q-th largest: 8 q logits of the CTA)
+  const int q = (K + kWarps - 1) / kWarps;
+  const uint32_t wmax = __reduce_max_sync(~0u, om);
+  const uint32_t bar = q == 1 ? wmax : warp_qth_largest(om, q);
+  if (lane == 0) {
+    s_max[warp] = wmax;
+    s_bar[warp] = bar;
+  }
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+  uint32_t omax = 0, least = ~0u;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    omax = max(omax, s_max[w]);
+    least = min(least, s_bar[w]);
+  }
+  const float mx = unordered(omax);
+  const int64_t out = row * p.chunks + chunk;
+  if (mx == -INFINITY) {  // nothing here (uniform over the CTA)
+    if (tid == 0) p.stats[out] = make_float2(-INFINITY, 0.f);
+    for (int i = tid; i < K; i += kBeamThreads) p.keys[out * K + i] = 0;
+    return;
+  }
+  // ---- sum of 2^(x log2 e - c), c = fl32(mx log2 e): c's rounding is put right
+  // at the end, so every exponent is good to 2^-23 of itself
+  const float c = mx * kLog2eHi;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const float e = P::get(v[i], j);
+      acc[j & 3] += exp2_approx(fmaf(e, kLog2eLo, fmaf(e, kLog2eHi, -c)));
+    }
+  float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  // ---- the chunk's logits at or above the threshold
+  const float floor_x = fmaxf(unordered(least), -FLT_MAX);
+  if (m >= floor_x) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const float e = P::get(v[i], j);
+        if (e >= floor_x) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kListCap)
+            list[at] = make_key(fminf(e, FLT_MAX),
+                                (int)(base + (int64_t)i * kBeamThreads * kN + j));
+        }
+      }
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += s_sum[w];
+  const int n = s_count;
+  // NaN, infinite or huge logits: the exponents above overflowed.  (Uniform.)
+  const bool odd = !(sum >= 0.25f && sum < INFINITY) || fabsf(mx) > 1e30f;
+  if (odd) {
+    float a4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        a4[j & 3] += exp2_approx((clean(P::get(v[i], j)) - mx) * kLog2eHi);
+    float t = (a4[0] + a4[1]) + (a4[2] + a4[3]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) t += __shfl_xor_sync(~0u, t, d);
+    __syncthreads();
+    if (lane == 0) s_sum[warp] = t;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_sum[w];
+  }
+  if (tid == 0) {
+    // 2^c against exp(mx): d = mx log2 e - c
+    const float d = odd ? 0.f : fmaf(mx, kLog2eLo, fmaf(mx, kLog2eHi, -c));
+    p.stats[out] = make_float2(mx, sum * exp2f(-d));
+  }
+  uint64_t* keys = p.keys + out * K;
+  if (n <= kListCap) {
+    for (int i = tid; i < n; i += kBeamThreads) {
+      const uint64_t mine = list[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += list[j] > mine;
+      if (rank < K) keys[rank] = mine;
+    }
+    for (int i = n + tid; i < K; i += kBeamThreads) keys[i] = 0;
+    return;
+  }
+  // More logits than the list holds reach the threshold (long runs of equal ones):
+  // the best key below the last one taken, K times.
+  uint64_t last = ~0ull;
+  for (int k = 0; k < K; ++k) {
+    uint64_t best = 0;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const float e = P::get(v[i], j);
+        const uint64_t key = make_key(fminf(e, FLT_MAX),
+                                      (int)(base + (int64_t)i * kBeamThreads * kN + j));
+        if (e > -INFINITY && key < last && key > best) best = key;
+      }
+    best = warp_max_u64(best);
+    if (lane == 0) s_best[warp] = best;
+    __syncthreads();
+    best = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
+    __syncthreads();
+    if (tid == 0) keys[k] = best;
+    last = best;
+  }
+}
+
+// ---- sums again, in two fp32 parts ---------------------------------------------
+// exp(t) for t in [-60, 0]: t = (64 n + j) ln 2 / 64 + r, exp = 2^n 2^(j/64) e^r
+// (P. T. P. Tang, "Table-Driven Implementation of the Exponential Function", ACM
+// TOMS 15, 1989).  ln 2 / 64 in three parts, the first two of 11 bits, so that
+// their products with 64 n + j (13 bits) and the differences from t are exact.
+constexpr double kLn2By64 = 0.010830424696249145;  // ln 2 / 64
+constexpr float kC1 = (float)((long long)(kLn2By64 * 131072.0) / 131072.0);  // to 2^-17
+constexpr float kC2 =
+    (float)((long long)((kLn2By64 - (double)kC1) * 268435456.0) / 268435456.0);  // to 2^-28
+constexpr float kC3 = (float)(kLn2By64 - (double)kC1 - (double)kC2);
+
+struct Sum2 {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float a, float b) {  // a + b, |b| small
+    const float s = hi + a, z = s - hi;
+    lo += ((hi - (s - z)) + (a - z)) + b;
+    hi = s;
+  }
+};
+
+__device__ __forceinline__ void add_exp(Sum2& acc, float x, float mx, const float2* table) {
+  // t + t_lo = x - mx exactly
+  const float t = x - mx, z = t - x;
+  if (!(t >= -60.f)) return;  // (below 2^-86 of the largest term; NaN and -inf too)
+  const float t_lo = (x - (t - z)) - (mx + z);
+  const float kf = rintf(t * (float)(1.0 / kLn2By64));
+  const int k = (int)kf;
+  const float r2 = fmaf(-kf, kC2, fmaf(-kf, kC1, t));
+  const float p3 = kf * kC3;
+  const float r = r2 - p3;
+  const float r_lo = ((r2 - r) - p3) + t_lo;
+  // e^r - 1 = r + q, |r| < 2^-7.5
+  const float q = fmaf(r * r, fmaf(r, fmaf(r, 1.f / 24, 1.f / 6), 0.5f), r_lo);
+  const float2 w = table[k & 63];
+  const float a = w.x * r, a_lo = fmaf(w.x, r, -a);
+  const float s = w.x + a;
+  const float s_lo = ((w.x - s) + a) + (a_lo + fmaf(w.x, q, fmaf(w.y, r, w.y)));
+  const float scale = __int_as_float((127 + (k >> 6)) << 23);
+  acc.add(s * scale, s_lo * scale);
+}
+
+template <typename T>
+__device__ __forceinline__ void precise_sum(Sum2& acc, const T* x, int V, float mx,
+                                            const float2* table) {
+  using P = Pack<T>;
+  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  for (int64_t i = (int64_t)threadIdx.x * P::kN - off; i < V; i += kBeamThreads * P::kN) {
+    const uint4 v = load_vec<T>(x, i, V);
+#pragma unroll
+    for (int j = 0; j < P::kN; ++j) add_exp(acc, clean(P::get(v, j)), mx, table);
+  }
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+  return v;
+}
+
+struct Cand {
+  uint64_t score;  // ordered(double)
+  uint64_t key;
+  int beam;
+};
+__device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
+  if (a.score != b.score) return a.score > b.score;
+  if (a.beam != b.beam) return a.beam < b.beam;
+  return a.key > b.key;
+}
+
+// One group: the sums of its rows, then the K best of their candidates.
+__global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
+  __shared__ double s_off[kMaxBeams];    // -log sum + beam score
+  __shared__ float s_top[kMaxBeams];     // row maximum
+  __shared__ float s_cum[kMaxBeams];     // beam score; NaN: the beam offers nothing
+  __shared__ uint8_t s_done[kMaxBeams];  // finished: one candidate, the end token
+  __shared__ uint8_t s_again[kMaxBeams];
+  __shared__ Cand list[kListCap];
+  __shared__ double s_part[kWarps];
+  __shared__ uint32_t s_bar[kWarps];
+  __shared__ Cand s_best[kWarps];
+  __shared__ Cand picked[kMaxBeamSelected];
+  __shared__ float2 table[64];
+  __shared__ int s_count, s_near;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int W = p.a.beam_width, K = p.a.num_selected, S = p.chunks;
+  const int64_t row0 = (int64_t)blockIdx.x * W;
+  for (int w = tid; w < W; w += kBeamThreads) {
+    const float cum = p.a.beam_scores[row0 + w];
+    s_cum[w] = isfinite(cum) ? cum : NAN;
+    s_done[w] = p.a.finished && p.a.finished[row0 + w];
+    s_again[w] = 0;
+  }
+  pdl_wait();
+  __syncthreads();
+  for (int w = warp; w < W; w += kWarps) {
+    float m = -INFINITY;
+    double sum = 0.0;
+    if (!s_done[w]) {
+      const float2* st = p.stats + (row0 + w) * S;
+      for (int i = lane; i < S; i += 32) {
+        const float2 v = __ldcg(st + i);
+        if (v.x > m) {
+          sum = sum * (double)expf(m - v.x) + (double)v.y;
+          m = v.x;
+        } else if (v.x > -INFINITY) {
+          sum += (double)v.y * (double)expf(v.x - m);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      if (m > -INFINITY) sum *= (double)expf(m - top);
+      m = top;
+      sum = warp_sum(sum);
+    }
+    if (lane == 0) {
+      s_top[w] = m;
+      s_off[w] = -log(sum);
+      if (m == -INFINITY && !s_done[w]) s_cum[w] = NAN;
+    }
+  }
+  __syncthreads();
+  const int per_row = S * K, n_all = W * per_row;
+  const uint64_t* keys = p.keys + row0 * per_row;
+  // the c-th candidate; false: there is none
+  auto candidate = [&](int c, Cand* o) {
+    const int w = c / per_row;
+    const float cum = s_cum[w];
+    if (isnan(cum)) return false;
+    o->beam = w;
+    double s;
+    if (s_done[w]) {
+      if (c != w * per_row) return false;
+      o->key = (uint32_t)~p.a.end_token;
+      s = (double)cum;
+    } else {
+      o->key = __ldcg(keys + c);
+      if (o->key == 0) return false;
+      const float x = unordered((uint32_t)(o->key >> 32));
+      s = (double)cum + (((double)x - (double)s_top[w]) + s_off[w]);
+      if ((float)s == -INFINITY) return false;
+    }
+    o->score = ordered(s);
+    return true;
+  };
+  auto value = [](uint64_t o) {
+    return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
+  };
+  for (int pass = 0;; ++pass) {
+    // threshold as in the chunks, on the upper halves of the ordered scores
+    uint32_t mine = 0;
+    for (int c = tid; c < n_all; c += kBeamThreads) {
+      Cand o;
+      if (candidate(c, &o)) mine = max(mine, (uint32_t)(o.score >> 32));
+    }
+    const uint32_t bar = warp_qth_largest(mine, (K + kWarps - 1) / kWarps);
+    if (lane == 0) s_bar[warp] = bar;
+    if (tid == 0) s_count = s_near = 0;
+    __syncthreads();
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) least = min(least, s_bar[w]);
+    for (int c = tid; c < n_all; c += kBeamThreads) {
+      Cand o;
+      if (candidate(c, &o) && (uint32_t)(o.score >> 32) >= least) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kListCap) list[at] = o;
+      }
+    }
+    __syncthreads();
+    const int n = s_count;
+    int got = min(n, K);
+    if (n <= kListCap) {
+      for (int i = tid; i < n; i += kBeamThreads) {
+        int rank = 0;
+        const Cand o = list[i];
+        for (int j = 0; j < n; ++j) rank += better(list[j], o);
+        if (rank < K) picked[rank] = o;
+      }
+      __syncthreads();
+    } else {
+      // more candidates than the list holds: the best after the last one, K times
+      Cand last{~0ull, ~0ull, -1};
+      for (int k = 0; k < K; ++k) {
+        Cand best{0, 0, kMaxBeams};
+        for (int c = tid; c < n_all; c += kBeamThreads) {
+          Cand o;
+          if (candidate(c, &o) && better(last, o) && better(o, best)) best = o;
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+          Cand o;
+          o.score = __shfl_xor_sync(~0u, best.score, d);
+          o.key = __shfl_xor_sync(~0u, best.key, d);
+          o.beam = __shfl_xor_sync(~0u, best.beam, d);
+          if (better(o, best)) best = o;
+        }
+        if (lane == 0) s_best[warp] = best;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w)
+          if (better(s_best[w], best)) best = s_best[w];
+        last = best;
+        if (tid == 0) picked[k] = best;
+        __syncthreads();
+      }
+    }
+    if (pass == 1 || got == 0) break;
+    // ---- scores of two beams too close for the fp32 sums: next to each other, or
+    // one left out next to the last one picked
+    for (int i = tid; i + 1 < got; i += kBeamThreads)
+      if (picked[i].beam != picked[i + 1].beam &&
+          value(picked[i].score) - value(picked[i + 1].score) <=
+              kNear + 1e-15 * fabs(value(picked[i].score))) {
+        s_again[picked[i].beam] = s_again[picked[i + 1].beam] = 1;
+        s_near = 1;
+      }
+    const Cand end = picked[got - 1];
+    if (got == K)
+      for (int c = tid; c < n_all; c += kBeamThreads) {
+        Cand o;
+        if (candidate(c, &o) && o.beam != end.beam && better(end, o) &&
+            value(end.score) - value(o.score) <= kNear + 1e-15 * fabs(value(end.score))) {
+          s_again[o.beam] = s_again[end.beam] = 1;
+          s_near = 1;
+        }
+      }
+    if (tid < 64) {
+      const double t = exp2((double)tid / 64);
+      table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
+    }
+    __syncthreads();
+    const bool near = s_near != 0;
+    __syncthreads();  // (s_near is cleared by the next pass)
+    if (!near) break;
+    for (int w = 0; w < W; ++w) {
+      if (!s_again[w] || s_done[w]) continue;
+      Sum2 acc;
+      const int64_t at = (row0 + w) * p.a.row_stride;
+      if (p.a.dtype == PA_F32)
+        precise_sum(acc, static_cast<const float*>(p.a.logits) + at, p.a.vocab_size, s_top[w],
+                    table);
+      else if (p.a.dtype == PA_F16)
+        precise_sum(acc, static_cast<const __half*>(p.a.logits) + at, p.a.vocab_size, s_top[w],
+                    table);
+      else
+        precise_sum(acc, static_cast<const __nv_bfloat16*>(p.a.logits) + at, p.a.vocab_size,
+                    s_top[w], table);
+      const double part = warp_sum((double)acc.hi + (double)acc.lo);
+      if (lane == 0) s_part[warp] = part;
+      __syncthreads();
+      if (tid == 0) {
+        double sum = 0.0;
+        for (int i = 0; i < kWarps; ++i) sum += s_part[i];
+        s_off[w] = -log(sum);
+      }
+      __syncthreads();
+    }
+  }
+  const int got = min(s_count, K);
+  for (int i = tid; i < K; i += kBeamThreads) {
+    const int64_t at = (int64_t)blockIdx.x * K + i;
+    float score = -INFINITY;
+    int parent = -1, token = -1;
+    if (i < got) {
+      score = (float)value(picked[i].score);
+      parent = (int)row0 + picked[i].beam;
+      token = (int)~(uint32_t)picked[i].key;
+    }
+    p.a.scores[at] = score;
+    p.a.parents[at] = parent;
+    p.a.tokens[at] = token;
+    if (p.a.finished_out) p.a.finished_out[at] = token >= 0 && token == p.a.end_token;
+  }
+}
+
+template <typename T>
+cudaError_t launch_chunks(const BeamK& p, int per_thread, unsigned grid, cudaStream_t stream) {
+  constexpr int kN = Pack<T>::kN;
+  if (per_thread == 32)
+    beam_chunk_kernel<T, 32 / kN><<<grid, kBeamThreads, 0, stream>>>(p);
+  else
+    beam_chunk_kernel<T, 8 / kN><<<grid, kBeamThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+BeamPlan make_beam_plan(int num_groups, int beam_width, int vocab_size, int num_selected) {
+  BeamPlan b{};
+  const int64_t rows = (int64_t)num_groups * beam_width;
+  const int64_t span = (int64_t)vocab_size + kBeamAlign - 1;
+  auto chunks = [&](int e) { return (span + kBeamThreads * e - 1) / (kBeamThreads * e); };
+  // chunks of 8192 logits where they give each of the 152 SMs two CTAs, else of 2048
+  b.per_thread = rows * chunks(32) >= 2 * 152 ? 32 : 8;
+  b.chunks = (int)chunks(b.per_thread);
+  b.off_stats = (rows * b.chunks * num_selected * 8 + 255) / 256 * 256;
+  b.bytes = b.off_stats + rows * b.chunks * 8;
+  return b;
+}
+
+cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStream_t stream) {
+  BeamK p{a, plan.chunks, static_cast<uint64_t*>(a.workspace),
+          reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + plan.off_stats)};
+  const unsigned grid = (unsigned)((int64_t)a.num_groups * a.beam_width * plan.chunks);
+  cudaError_t e = a.dtype == PA_F32   ? launch_chunks<float>(p, plan.per_thread, grid, stream)
+                  : a.dtype == PA_F16 ? launch_chunks<__half>(p, plan.per_thread, grid, stream)
+                                      : launch_chunks<__nv_bfloat16>(p, plan.per_thread, grid,
+                                                                     stream);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.num_groups);
+  cfg.blockDim = dim3(kBeamThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, beam_join_kernel, p);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace pa

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <mutex>
 
+#include "pa_beam.h"
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_step.h"
@@ -989,6 +990,299 @@ pa_status pa_attention_selected(
   a.workspace = workspace;
   const cudaError_t e =
       launch_attention_selected(s, plan, a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---- several hypotheses: beam selection, forked and compacted rows, copies ----
+
+namespace {
+
+// a workspace of `bytes` is there
+bool has_workspace(const void* workspace, size_t given, int64_t bytes) {
+  return given >= (size_t)bytes && (bytes == 0 || (workspace && aligned(workspace, 256)));
+}
+
+// the checks of tables, counts and stack that pa_fork_blocks and pa_compact_blocks
+// share
+pa_status rows_status(const RowState& a, int block_size) {
+  if (a.num_rows < 0 || a.max_blocks_per_seq < 0 || a.free_capacity < 0 ||
+      a.num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (block_size != PA_BLOCK_SIZE || a.num_rows > kMaxForkRows ||
+      (int64_t)a.num_rows * a.max_blocks_per_seq >= kMaxForkEntries ||
+      (int64_t)a.max_blocks_per_seq * PA_BLOCK_SIZE >= (1ll << 31) ||
+      a.num_blocks >= (1ll << 31) || a.free_capacity >= (1ll << 31))
+    return PA_ERR_UNSUPPORTED;
+  const void* i32[] = {a.block_tables, a.block_tables_out, a.seq_lens,    a.seq_lens_out,
+                       a.extra_refs,   a.extra_refs_out,   a.free_blocks, a.free_count,
+                       a.free_count_out};
+  for (const void* p : i32)
+    if (!aligned(p, 4)) return PA_ERR_INVALID_ARG;
+  if (!a.extra_refs || !a.extra_refs_out || !a.free_count || !a.free_count_out ||
+      (a.free_capacity > 0 && !a.free_blocks) ||
+      (a.num_rows > 0 &&
+       (!a.seq_lens || !a.seq_lens_out ||
+        (a.max_blocks_per_seq > 0 && (!a.block_tables || !a.block_tables_out)))))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+// true if any buffer of the call, `more` included, overlaps another one that it must
+// not; an output that is its input counts once
+bool rows_overlap(const RowState& a, const Span* more_outs, int n_outs,
+                  const Span* more_ins, int n_ins) {
+  const size_t R = (size_t)a.num_rows, table = R * a.max_blocks_per_seq * 4;
+  const size_t refs = (size_t)a.num_blocks * 4;
+  Span outs[10] = {{a.block_tables_out, table},
+                   {a.seq_lens_out, R * 4},
+                   {a.extra_refs_out, refs},
+                   {a.free_blocks, (size_t)a.free_capacity * 4},
+                   {a.free_count_out, 4}};
+  Span ins[8] = {{a.block_tables == a.block_tables_out ? nullptr : a.block_tables, table},
+                 {a.seq_lens == a.seq_lens_out ? nullptr : a.seq_lens, R * 4},
+                 {a.extra_refs == a.extra_refs_out ? nullptr : a.extra_refs, refs},
+                 {a.free_count == a.free_count_out ? nullptr : a.free_count, 4}};
+  for (int i = 0; i < n_outs; ++i) outs[5 + i] = more_outs[i];
+  for (int i = 0; i < n_ins; ++i) ins[4 + i] = more_ins[i];
+  return any_overlap(outs, 5 + n_outs, ins, 4 + n_ins);
+}
+
+// the checks of caches of several layers; *span_k, *span_v: from the first layer's
+// start to the last one's end
+pa_status layers_status(const LayerCaches& c, int block_size, Span* span_k, Span* span_v) {
+  if (!valid_dtype(c.dtype) || c.num_layers <= 0) return PA_ERR_INVALID_ARG;
+  if (pa_status st = cache_shape_status(c.num_blocks, block_size, c.num_kv_heads, c.head_dim))
+    return st;
+  if (c.num_layers > (1 << 16)) return PA_ERR_UNSUPPORTED;
+  if (!c.k || !c.v || !aligned(c.k, 16) || !aligned(c.v, 16)) return PA_ERR_INVALID_ARG;
+  const int64_t bytes = c.num_blocks * c.num_kv_heads * page_bytes(c.dtype, c.head_dim);
+  const int64_t far = c.num_layers - 1;
+  if (far > 0)
+    for (int64_t s : {c.k_layer_bytes, c.v_layer_bytes})
+      if (s < bytes || s % 16 != 0 || s > (1ll << 46)) return PA_ERR_INVALID_ARG;
+  *span_k = Span{c.k, (size_t)(far ? far * c.k_layer_bytes + bytes : bytes)};
+  *span_v = Span{c.v, (size_t)(far ? far * c.v_layer_bytes + bytes : bytes)};
+  if (!overlaps(span_k->p, span_k->n, span_v->p, span_v->n)) return PA_OK;
+  // layer by layer in one buffer: each V between two K
+  if (far == 0 || c.k_layer_bytes != c.v_layer_bytes) return PA_ERR_INVALID_ARG;
+  const int64_t s = c.k_layer_bytes;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(c.v) -
+                              reinterpret_cast<uintptr_t>(c.k));
+  const int64_t at = ((d % s) + s) % s;
+  return at >= bytes && s - at >= bytes ? PA_OK : PA_ERR_INVALID_ARG;
+}
+
+bool clear_of(const Span* lists, int n, const Span& k, const Span& v) {
+  for (int i = 0; i < n; ++i)
+    if (overlaps(lists[i].p, lists[i].n, k.p, k.n) || overlaps(lists[i].p, lists[i].n, v.p, v.n))
+      return false;
+  return true;
+}
+
+pa_status beam_size_status(int num_groups, int beam_width, int vocab_size,
+                           int num_selected) {
+  if (num_groups < 0 || beam_width < 1 || vocab_size < 1 || num_selected < 1)
+    return PA_ERR_INVALID_ARG;
+  if (beam_width > kMaxBeams || num_selected > kMaxBeamSelected ||
+      vocab_size > (1 << 24) || (int64_t)num_groups * beam_width >= (1 << 24))
+    return PA_ERR_UNSUPPORTED;
+  const BeamPlan plan = make_beam_plan(num_groups, beam_width, vocab_size, num_selected);
+  if ((int64_t)num_groups * beam_width * plan.chunks >= (1ll << 31))
+    return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_beam_select_workspace_size(int num_groups, int beam_width, int vocab_size,
+                                        int num_selected, size_t* bytes) {
+  if (!bytes) return PA_ERR_INVALID_ARG;
+  if (pa_status st = beam_size_status(num_groups, beam_width, vocab_size, num_selected))
+    return st;
+  *bytes = (size_t)make_beam_plan(num_groups, beam_width, vocab_size, num_selected).bytes;
+  return PA_OK;
+}
+
+pa_status pa_beam_select(const void* logits, pa_dtype logits_dtype, int num_groups,
+                         int beam_width, int vocab_size, int64_t row_stride,
+                         const float* beam_scores, const uint8_t* finished,
+                         int end_token, int num_selected, float* scores,
+                         int32_t* parents, int32_t* tokens, uint8_t* finished_out,
+                         void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  if (!valid_dtype(logits_dtype)) return PA_ERR_INVALID_ARG;
+  if (!plain_type(logits_dtype)) return PA_ERR_UNSUPPORTED;
+  if (pa_status st = beam_size_status(num_groups, beam_width, vocab_size, num_selected))
+    return st;
+  if (row_stride < vocab_size || row_stride > (1ll << 36) || end_token < -1 ||
+      end_token >= vocab_size || (finished && end_token < 0))
+    return PA_ERR_INVALID_ARG;
+  if (num_groups == 0) return PA_OK;
+  const size_t eb = (size_t)elem_bytes(logits_dtype);
+  if (!logits || !beam_scores || !scores || !parents || !tokens || !aligned(logits, eb) ||
+      !aligned(beam_scores, 4) || !aligned(scores, 4) || !aligned(parents, 4) ||
+      !aligned(tokens, 4))
+    return PA_ERR_INVALID_ARG;
+  const BeamPlan plan = make_beam_plan(num_groups, beam_width, vocab_size, num_selected);
+  if (!has_workspace(workspace, workspace_bytes, plan.bytes)) return PA_ERR_INVALID_ARG;
+  const size_t rows = (size_t)num_groups * beam_width;
+  const size_t picks = (size_t)num_groups * num_selected;
+  // a group's scores and flags are read before its picks are written: in place where
+  // the two have one shape
+  const bool same = num_selected == beam_width;
+  const Span outs[] = {{scores, picks * 4},
+                       {parents, picks * 4},
+                       {tokens, picks * 4},
+                       {finished_out, picks},
+                       {workspace, (size_t)plan.bytes}};
+  const Span ins[] = {{logits, ((rows - 1) * row_stride + vocab_size) * eb},
+                      {same && beam_scores == scores ? nullptr : beam_scores, rows * 4},
+                      {same && finished == finished_out ? nullptr : finished, rows}};
+  if (any_overlap(outs, 5, ins, 3)) return PA_ERR_INVALID_ARG;
+  const BeamArgs a{logits,     logits_dtype, num_groups, beam_width,   vocab_size,
+                   row_stride, beam_scores,  finished,   end_token,    num_selected,
+                   scores,     parents,      tokens,     finished_out, workspace};
+  const cudaError_t e =
+      launch_beam_select(a, plan, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_fork_blocks_workspace_size(int num_rows, int max_blocks_per_seq,
+                                        size_t* bytes) {
+  if (!bytes || num_rows < 0 || max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+  *bytes = (size_t)fork_workspace_bytes(num_rows, max_blocks_per_seq);
+  return PA_OK;
+}
+
+pa_status pa_fork_blocks(const int32_t* sources, int num_rows,
+                         const int32_t* block_tables, int32_t* block_tables_out,
+                         int max_blocks_per_seq, const int32_t* seq_lens,
+                         int32_t* seq_lens_out, const int32_t* extra_refs,
+                         int32_t* extra_refs_out, int64_t num_blocks, int block_size,
+                         int32_t* free_blocks, int64_t free_capacity,
+                         const int32_t* free_count, int32_t* free_count_out,
+                         int64_t* block_mapping, int32_t* num_pairs, void* workspace,
+                         size_t workspace_bytes, pa_stream_t stream) {
+  const RowState rows{num_rows,   block_tables,   block_tables_out, max_blocks_per_seq,
+                      seq_lens,   seq_lens_out,   extra_refs,       extra_refs_out,
+                      num_blocks, free_blocks,    free_capacity,    free_count,
+                      free_count_out};
+  if (pa_status st = rows_status(rows, block_size)) return st;
+  if (!num_pairs || !aligned(num_pairs, 4) || !aligned(sources, 4) ||
+      !aligned(block_mapping, 8) || (num_rows > 0 && (!sources || !block_mapping)))
+    return PA_ERR_INVALID_ARG;
+  const int64_t need = fork_workspace_bytes(num_rows, max_blocks_per_seq);
+  if (!has_workspace(workspace, workspace_bytes, need)) return PA_ERR_INVALID_ARG;
+  const size_t R = (size_t)num_rows;
+  const Span outs[] = {{block_mapping, R * 16}, {num_pairs, 4}, {workspace, (size_t)need}};
+  const Span ins[] = {{sources, R * 4}};
+  if (rows_overlap(rows, outs, 3, ins, 1)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  const ForkArgs a{rows, sources, block_mapping, num_pairs, workspace, di->err};
+  const cudaError_t e = launch_fork_blocks(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_copy_blocks_layers(void* k_cache, void* v_cache, pa_dtype cache_dtype,
+                                int num_layers, int64_t k_layer_stride,
+                                int64_t v_layer_stride, int64_t num_blocks,
+                                int block_size, int num_kv_heads, int head_dim,
+                                const int64_t* block_mapping, int64_t max_pairs,
+                                const int32_t* num_pairs, pa_stream_t stream) {
+  const LayerCaches c{k_cache,    v_cache,      k_layer_stride, v_layer_stride, num_layers,
+                      num_blocks, num_kv_heads, cache_dtype,    head_dim};
+  Span k, v;
+  if (pa_status st = layers_status(c, block_size, &k, &v)) return st;
+  if (max_pairs < 0 || !aligned(num_pairs, 4)) return PA_ERR_INVALID_ARG;
+  if (max_pairs == 0) return PA_OK;
+  if (max_pairs >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if (!block_mapping || !aligned(block_mapping, 8)) return PA_ERR_INVALID_ARG;
+  const Span lists[] = {{block_mapping, (size_t)max_pairs * 16}, {num_pairs, 4}};
+  if (!clear_of(lists, 2, k, v)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  const cudaError_t e = launch_copy_blocks_layers(
+      c, num_kv_heads * page_bytes(cache_dtype, head_dim), block_mapping, max_pairs,
+      num_pairs, di->num_sms, di->err, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_compact_blocks_workspace_size(int num_rows, int max_blocks_per_seq,
+                                           size_t* bytes) {
+  if (!bytes || num_rows < 0 || max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+  *bytes = (size_t)compact_workspace_bytes(num_rows, max_blocks_per_seq);
+  return PA_OK;
+}
+
+pa_status pa_compact_blocks(const int32_t* keep, int max_keep, const int32_t* keep_lens,
+                            const int32_t* keep_start, int num_rows,
+                            const int32_t* block_tables, int32_t* block_tables_out,
+                            int max_blocks_per_seq, const int32_t* seq_lens,
+                            int32_t* seq_lens_out, const int32_t* extra_refs,
+                            int32_t* extra_refs_out, int64_t num_blocks, int block_size,
+                            int32_t* free_blocks, int64_t free_capacity,
+                            const int32_t* free_count, int32_t* free_count_out,
+                            int64_t* src_slots, int64_t* dst_slots, int32_t* num_moves,
+                            void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  const RowState rows{num_rows,   block_tables,   block_tables_out, max_blocks_per_seq,
+                      seq_lens,   seq_lens_out,   extra_refs,       extra_refs_out,
+                      num_blocks, free_blocks,    free_capacity,    free_count,
+                      free_count_out};
+  if (max_keep < 0) return PA_ERR_INVALID_ARG;
+  if (pa_status st = rows_status(rows, block_size)) return st;
+  if ((int64_t)num_rows * max_keep >= (1ll << 31) || max_keep > INT32_MAX - PA_BLOCK_SIZE)
+    return PA_ERR_UNSUPPORTED;
+  if (!aligned(keep, 4) || !aligned(keep_lens, 4) || !aligned(keep_start, 4) ||
+      !aligned(src_slots, 8) || !aligned(dst_slots, 8) || !aligned(num_moves, 4) ||
+      (num_rows > 0 && (!keep_lens || !src_slots || !dst_slots || !num_moves ||
+                        (max_keep > 0 && !keep))))
+    return PA_ERR_INVALID_ARG;
+  const int64_t need = compact_workspace_bytes(num_rows, max_blocks_per_seq);
+  if (!has_workspace(workspace, workspace_bytes, need)) return PA_ERR_INVALID_ARG;
+  const size_t R = (size_t)num_rows, slots = R * ((size_t)max_keep + PA_BLOCK_SIZE) * 8;
+  const Span outs[] = {
+      {src_slots, slots}, {dst_slots, slots}, {num_moves, R * 4}, {workspace, (size_t)need}};
+  const Span ins[] = {{keep, R * max_keep * 4}, {keep_lens, R * 4}, {keep_start, R * 4}};
+  if (rows_overlap(rows, outs, 4, ins, 3)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  const CompactArgs a{rows,      keep,      max_keep,  keep_lens, keep_start,
+                      src_slots, dst_slots, num_moves, workspace, di->err};
+  const cudaError_t e = launch_compact_blocks(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype cache_dtype,
+                         int num_layers, int64_t k_layer_stride, int64_t v_layer_stride,
+                         int64_t num_blocks, int block_size, int num_kv_heads,
+                         int head_dim, const int64_t* src_slots,
+                         const int64_t* dst_slots, const int32_t* num_moves,
+                         int num_rows, int64_t max_moves, pa_stream_t stream) {
+  const LayerCaches c{k_cache,    v_cache,      k_layer_stride, v_layer_stride, num_layers,
+                      num_blocks, num_kv_heads, cache_dtype,    head_dim};
+  Span k, v;
+  if (pa_status st = layers_status(c, block_size, &k, &v)) return st;
+  if (num_rows < 0 || max_moves < 0) return PA_ERR_INVALID_ARG;
+  if (num_rows == 0 || max_moves == 0) return PA_OK;
+  // (a warp to each slice of a head's tokens, 17 slices at most)
+  if (max_moves >= (1ll << 30) || (int64_t)num_layers * num_kv_heads > (1 << 24) ||
+      (int64_t)num_rows * num_layers * num_kv_heads > (1ll << 28))
+    return PA_ERR_UNSUPPORTED;
+  if (!src_slots || !dst_slots || !num_moves || !aligned(src_slots, 8) ||
+      !aligned(dst_slots, 8) || !aligned(num_moves, 4))
+    return PA_ERR_INVALID_ARG;
+  const size_t slots = (size_t)num_rows * max_moves * 8;
+  const Span lists[] = {
+      {src_slots, slots}, {dst_slots, slots}, {num_moves, (size_t)num_rows * 4}};
+  if (!clear_of(lists, 3, k, v)) return PA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
+  const cudaError_t e =
+      launch_move_tokens(c, src_slots, dst_slots, num_moves, num_rows, max_moves,
+                         di->num_sms, di->err, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
