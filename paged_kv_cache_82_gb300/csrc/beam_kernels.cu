@@ -91,61 +91,120 @@ __device__ __forceinline__ uint32_t warp_qth_largest(uint32_t v, int q) {
 }
 
 // ---- elements of a 16-byte load ------------------------------------------------
+// get: one element; pair: elements 2 i and 2 i + 1; Max: the largest of what it has
+// been given, NaN passed over
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
 template <typename T>
 struct Pack;
 template <>
 struct Pack<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-    return __uint_as_float(w);
-  }
-  static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
   static constexpr uint32_t kNegInf = 0xff800000u;
+  static constexpr float kLowest = -FLT_MAX;
+  static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    return __uint_as_float(word(v, i));
+  }
+  static __device__ __forceinline__ float2 pair(const uint4& v, int i) {
+    return make_float2(get(v, 2 * i), get(v, 2 * i + 1));
+  }
+  struct Max {
+    float m;
+    __device__ __forceinline__ explicit Max(const uint4& v)
+        : m(fmaxf(fmaxf(get(v, 0), get(v, 1)), fmaxf(get(v, 2), get(v, 3)))) {}
+    __device__ __forceinline__ void add(const Max& o) { m = fmaxf(m, o.m); }
+    __device__ __forceinline__ float value() const { return fmaxf(m, -INFINITY); }
+    __device__ __forceinline__ bool reaches(float x) const { return m >= x; }
+  };
 };
 template <>
 struct Pack<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
-    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-  }
+  static constexpr uint32_t kNegInf = 0xff80u;
+  static constexpr float kLowest = -0x1.fep127f;
   static __device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) {
     return __bfloat16_as_ushort(*p);
   }
-  static constexpr uint32_t kNegInf = 0xff80u;
+  static __device__ __forceinline__ float2 pair(const uint4& v, int i) {
+    const uint32_t w = word(v, i);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const float2 p = pair(v, i >> 1);
+    return i & 1 ? p.y : p.x;
+  }
+  struct Max {
+    __nv_bfloat162 m;
+    __device__ __forceinline__ explicit Max(const uint4& v) {
+      const auto* w = reinterpret_cast<const __nv_bfloat162*>(&v);
+      m = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+    }
+    __device__ __forceinline__ void add(const Max& o) { m = __hmax2(m, o.m); }
+    __device__ __forceinline__ float value() const {
+      const float2 p = __bfloat1622float2(m);
+      return fmaxf(fmaxf(p.x, p.y), -INFINITY);
+    }
+    __device__ __forceinline__ bool reaches(float x) const {
+      return __hge2_mask(m, __float2bfloat162_rn(x)) != 0;
+    }
+  };
 };
 template <>
 struct Pack<__half> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
-    return __half2float(__ushort_as_half((unsigned short)(i & 1 ? w >> 16 : w & 0xffffu)));
-  }
-  static __device__ __forceinline__ uint32_t bits(const __half* p) { return __half_as_ushort(*p); }
   static constexpr uint32_t kNegInf = 0xfc00u;
+  static constexpr float kLowest = -65504.f;
+  static __device__ __forceinline__ uint32_t bits(const __half* p) { return __half_as_ushort(*p); }
+  static __device__ __forceinline__ float2 pair(const uint4& v, int i) {
+    const uint32_t w = word(v, i);
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const float2 p = pair(v, i >> 1);
+    return i & 1 ? p.y : p.x;
+  }
+  struct Max {
+    __half2 m;
+    __device__ __forceinline__ explicit Max(const uint4& v) {
+      const auto* w = reinterpret_cast<const __half2*>(&v);
+      m = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+    }
+    __device__ __forceinline__ void add(const Max& o) { m = __hmax2(m, o.m); }
+    __device__ __forceinline__ float value() const {
+      const float2 p = __half22float2(m);
+      return fmaxf(fmaxf(p.x, p.y), -INFINITY);
+    }
+    __device__ __forceinline__ bool reaches(float x) const {
+      return __hge2_mask(m, __float2half2_rn(x)) != 0;
+    }
+  };
 };
 
-// the elements [i0, i0 + kN) of a row of n, 16-byte aligned where whole; what lies
-// outside the row is -inf and not read
+// the elements [i0, i0 + kN) of a row of n where they are not all inside it: what lies
+// outside is -inf and not read
 template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T* row, int64_t i0, int n) {
-  constexpr int kN = Pack<T>::kN;
-  if (i0 >= 0 && i0 + kN <= n)
-    return __ldcs(reinterpret_cast<const uint4*>(row + i0));
+__device__ __noinline__ uint4 load_edge(const T* row, int i0, int n) {
+  constexpr int kN = Pack<T>::kN, kPer = kN / 4;  // kPer: elements of a 32-bit word
   uint32_t w[4];
-  constexpr int kPer = kN / 4;  // elements of a 32-bit word
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     w[k] = 0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      const int64_t i = i0 + k * kPer + e;
+      const int i = i0 + k * kPer + e;
       const uint32_t b = i >= 0 && i < n ? Pack<T>::bits(row + i) : Pack<T>::kNegInf;
       w[k] |= b << (e * 16);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 16-byte aligned where whole
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T* row, int i0, int n) {
+  if (i0 >= 0 && i0 + Pack<T>::kN <= n) return __ldcs(reinterpret_cast<const uint4*>(row + i0));
+  return load_edge<T>(row, i0, n);
 }
 
 struct BeamK {
@@ -155,11 +214,65 @@ struct BeamK {
   float2* stats;   // [rows][chunks]: maximum, sum of exp(x - maximum)
 };
 
+// The chunk's sum where the fast one's exponents overflowed (the logits read again).
+template <typename T, int kVecs>
+__device__ __noinline__ float odd_sum(const T* x, int base, int V, float mx) {
+  using P = Pack<T>;
+  float2 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int i = 0; i < kVecs; ++i) {
+    const uint4 v = load_vec<T>(x, base + i * kBeamThreads * P::kN, V);
+#pragma unroll
+    for (int j = 0; j < P::kN / 2; ++j) {
+      const float2 e = P::pair(v, j);
+      acc[j & 3].x += exp2_approx((clean(e.x) - mx) * kLog2eHi);
+      acc[j & 3].y += exp2_approx((clean(e.y) - mx) * kLog2eHi);
+    }
+  }
+  return ((acc[0].x + acc[1].x) + (acc[2].x + acc[3].x)) +
+         ((acc[0].y + acc[1].y) + (acc[2].y + acc[3].y));
+}
+
+// More logits than the list holds reach the threshold (long runs of equal ones): the
+// best key below the last one taken, K times.
+template <typename T, int kVecs>
+__device__ __noinline__ void pick_one_by_one(const T* x, int base, int V, int K,
+                                             uint64_t* s_best, uint64_t* keys) {
+  using P = Pack<T>;
+  uint64_t last = ~0ull;
+  for (int k = 0; k < K; ++k) {
+    uint64_t best = 0;
+#pragma unroll 1
+    for (int i = 0; i < kVecs; ++i) {
+      const int at = base + i * kBeamThreads * P::kN;
+      const uint4 v = load_vec<T>(x, at, V);
+#pragma unroll
+      for (int j = 0; j < P::kN; ++j) {
+        const float e = P::get(v, j);
+        const uint64_t key = make_key(fminf(e, FLT_MAX), at + j);
+        if (e > -INFINITY && key < last && key > best) best = key;
+      }
+    }
+    best = warp_max_u64(best);
+    if ((threadIdx.x & 31) == 0) s_best[threadIdx.x >> 5] = best;
+    __syncthreads();
+    best = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
+    __syncthreads();
+    if (threadIdx.x == 0) keys[k] = best;
+    last = best;
+  }
+}
+
 // One chunk of one row.
 template <typename T, int kVecs>
-__global__ void __launch_bounds__(kBeamThreads) beam_chunk_kernel(BeamK p) {
+__global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
+    beam_chunk_kernel(BeamK p) {
   using P = Pack<T>;
-  constexpr int kN = P::kN, kE = kVecs * kN;
+  constexpr int kN = P::kN, kStep = kBeamThreads * kN;
   __shared__ uint64_t list[kListCap];
   __shared__ uint32_t s_max[kWarps], s_bar[kWarps];
   __shared__ float s_sum[kWarps];
@@ -173,18 +286,22 @@ __global__ void __launch_bounds__(kBeamThreads) beam_chunk_kernel(BeamK p) {
   if (p.a.finished && p.a.finished[row]) return;  // (its logits are not looked at)
   const T* x = static_cast<const T*>(p.a.logits) + row * p.a.row_stride;
   // the row seen from the 16-byte boundary at or before its start
-  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const int64_t base = (int64_t)chunk * (kBeamThreads * kE) + tid * kN - off;
+  const int first = chunk * (kVecs * kStep) -
+                    (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  const int base = first + tid * kN;
   uint4 v[kVecs];
+  if (first >= 0 && first + kVecs * kStep <= V) {
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    v[i] = load_vec<T>(x, base + (int64_t)i * kBeamThreads * kN, V);
-  float m = -INFINITY;
+    for (int i = 0; i < kVecs; ++i)
+      v[i] = __ldcs(reinterpret_cast<const uint4*>(x + base + i * kStep));
+  } else {
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
+    for (int i = 0; i < kVecs; ++i) v[i] = load_vec<T>(x, base + i * kStep, V);
+  }
+  typename P::Max tops(v[0]);
 #pragma unroll
-    for (int j = 0; j < kN; ++j) m = fmaxf(m, P::get(v[i], j));
-  m = fminf(m, FLT_MAX);
+  for (int i = 1; i < kVecs; ++i) tops.add(typename P::Max(v[i]));
+  const float m = fminf(tops.value(), FLT_MAX);
   const uint32_t om = ordered(m);
   // (at least q lanes of each warp reach the q-th largest: 8 q logits of the CTA)
   const int q = (K + kWarps - 1) / kWarps;
@@ -209,34 +326,48 @@ __global__ void __launch_bounds__(kBeamThreads) beam_chunk_kernel(BeamK p) {
     for (int i = tid; i < K; i += kBeamThreads) p.keys[out * K + i] = 0;
     return;
   }
+  // ---- the chunk's logits at or above the threshold: the vectors that hold one, one
+  // at a time
+  const float floor_x = fmaxf(unordered(least), P::kLowest);
+  unsigned hits = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+    hits |= (typename P::Max(v[i])).reaches(floor_x) ? 1u << i : 0u;
+  while (hits) {
+    const int i = __ffs(hits) - 1;
+    hits &= hits - 1;
+    uint4 one = v[0];
+#pragma unroll
+    for (int k = 1; k < kVecs; ++k)
+      if (k == i) one = v[k];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const float e = P::get(one, j);
+      if (e >= floor_x) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kListCap) list[at] = make_key(fminf(e, FLT_MAX), base + i * kStep + j);
+      }
+    }
+  }
   // ---- sum of 2^(x log2 e - c), c = fl32(mx log2 e): c's rounding is put right
   // at the end, so every exponent is good to 2^-23 of itself
   const float c = mx * kLog2eHi;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float2 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+  const float2 hi2 = make_float2(kLog2eHi, kLog2eHi), lo2 = make_float2(kLog2eLo, kLog2eLo),
+               c2 = make_float2(-c, -c);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const float e = P::get(v[i], j);
-      acc[j & 3] += exp2_approx(fmaf(e, kLog2eLo, fmaf(e, kLog2eHi, -c)));
+    for (int j = 0; j < kN / 2; ++j) {
+      const float2 e = P::pair(v[i], j);
+      const float2 y = __ffma2_rn(e, lo2, __ffma2_rn(e, hi2, c2));
+      acc[j & 3] = __fadd2_rn(acc[j & 3], make_float2(exp2_approx(y.x), exp2_approx(y.y)));
     }
-  float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-  // ---- the chunk's logits at or above the threshold
-  const float floor_x = fmaxf(unordered(least), -FLT_MAX);
-  if (m >= floor_x) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const float e = P::get(v[i], j);
-        if (e >= floor_x) {
-          const int at = atomicAdd(&s_count, 1);
-          if (at < kListCap)
-            list[at] = make_key(fminf(e, FLT_MAX),
-                                (int)(base + (int64_t)i * kBeamThreads * kN + j));
-        }
-      }
-  }
+  const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+  const float2 a03 = __fadd2_rn(a01, a23);
+  float sum = a03.x + a03.y;
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   if (lane == 0) s_sum[warp] = sum;
@@ -248,13 +379,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_chunk_kernel(BeamK p) {
   // NaN, infinite or huge logits: the exponents above overflowed.  (Uniform.)
   const bool odd = !(sum >= 0.25f && sum < INFINITY) || fabsf(mx) > 1e30f;
   if (odd) {
-    float a4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < kN; ++j)
-        a4[j & 3] += exp2_approx((clean(P::get(v[i], j)) - mx) * kLog2eHi);
-    float t = (a4[0] + a4[1]) + (a4[2] + a4[3]);
+    float t = odd_sum<T, kVecs>(x, base, V, mx);
 #pragma unroll
     for (int d = 16; d; d >>= 1) t += __shfl_xor_sync(~0u, t, d);
     __syncthreads();
@@ -280,30 +405,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_chunk_kernel(BeamK p) {
     for (int i = n + tid; i < K; i += kBeamThreads) keys[i] = 0;
     return;
   }
-  // More logits than the list holds reach the threshold (long runs of equal ones):
-  // the best key below the last one taken, K times.
-  uint64_t last = ~0ull;
-  for (int k = 0; k < K; ++k) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const float e = P::get(v[i], j);
-        const uint64_t key = make_key(fminf(e, FLT_MAX),
-                                      (int)(base + (int64_t)i * kBeamThreads * kN + j));
-        if (e > -INFINITY && key < last && key > best) best = key;
-      }
-    best = warp_max_u64(best);
-    if (lane == 0) s_best[warp] = best;
-    __syncthreads();
-    best = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
-    __syncthreads();
-    if (tid == 0) keys[k] = best;
-    last = best;
-  }
+  pick_one_by_one<T, kVecs>(x, base, V, K, s_best, keys);
 }
 
 // ---- sums again, in two fp32 parts ---------------------------------------------
@@ -352,7 +454,7 @@ __device__ __forceinline__ void precise_sum(Sum2& acc, const T* x, int V, float 
                                             const float2* table) {
   using P = Pack<T>;
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  for (int64_t i = (int64_t)threadIdx.x * P::kN - off; i < V; i += kBeamThreads * P::kN) {
+  for (int i = threadIdx.x * P::kN - off; i < V; i += kBeamThreads * P::kN) {
     const uint4 v = load_vec<T>(x, i, V);
 #pragma unroll
     for (int j = 0; j < P::kN; ++j) add_exp(acc, clean(P::get(v, j)), mx, table);
@@ -376,9 +478,11 @@ __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
   return a.key > b.key;
 }
 
-// One group: the sums of its rows, then the K best of their candidates.
+// One group: the sums of its rows, then the K best of their candidates.  What a
+// thread's first kHeld candidates are is loaded while the sums are, and kept.
+constexpr int kHeld = 4;
 __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
-  __shared__ double s_off[kMaxBeams];    // -log sum + beam score
+  __shared__ double s_off[kMaxBeams];    // -log sum
   __shared__ float s_top[kMaxBeams];     // row maximum
   __shared__ float s_cum[kMaxBeams];     // beam score; NaN: the beam offers nothing
   __shared__ uint8_t s_done[kMaxBeams];  // finished: one candidate, the end token
@@ -399,8 +503,18 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
     s_done[w] = p.a.finished && p.a.finished[row0 + w];
     s_again[w] = 0;
   }
-  pdl_wait();
+  if (tid == 0) s_count = s_near = 0;
+  const int per_row = S * K, n_all = W * per_row;
+  const uint64_t* keys = p.keys + row0 * per_row;
   __syncthreads();
+  pdl_wait();
+  // (a finished row's keys are not written, and not used)
+  uint64_t held_key[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = tid + i * kBeamThreads;
+    held_key[i] = c < n_all ? __ldcg(keys + c) : 0;
+  }
   for (int w = warp; w < W; w += kWarps) {
     float m = -INFINITY;
     double sum = 0.0;
@@ -409,16 +523,16 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
       for (int i = lane; i < S; i += 32) {
         const float2 v = __ldcg(st + i);
         if (v.x > m) {
-          sum = sum * (double)expf(m - v.x) + (double)v.y;
+          sum = (m > -INFINITY ? sum * (double)expf(m - v.x) : 0.0) + (double)v.y;
           m = v.x;
         } else if (v.x > -INFINITY) {
-          sum += (double)v.y * (double)expf(v.x - m);
+          sum += (double)(v.y * expf(v.x - m));
         }
       }
       float top = m;
 #pragma unroll
       for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      if (m > -INFINITY) sum *= (double)expf(m - top);
+      if (m > -INFINITY && m < top) sum *= (double)expf(m - top);
       m = top;
       sum = warp_sum(sum);
     }
@@ -429,10 +543,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
     }
   }
   __syncthreads();
-  const int per_row = S * K, n_all = W * per_row;
-  const uint64_t* keys = p.keys + row0 * per_row;
-  // the c-th candidate; false: there is none
-  auto candidate = [&](int c, Cand* o) {
+  // the c-th candidate, whose key (unless its beam is finished) is `key`; false: none
+  auto candidate = [&](int c, uint64_t key, Cand* o) {
     const int w = c / per_row;
     const float cum = s_cum[w];
     if (isnan(cum)) return false;
@@ -443,9 +555,9 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
       o->key = (uint32_t)~p.a.end_token;
       s = (double)cum;
     } else {
-      o->key = __ldcg(keys + c);
-      if (o->key == 0) return false;
-      const float x = unordered((uint32_t)(o->key >> 32));
+      o->key = key;
+      if (key == 0) return false;
+      const float x = unordered((uint32_t)(key >> 32));
       s = (double)cum + (((double)x - (double)s_top[w]) + s_off[w]);
       if ((float)s == -INFINITY) return false;
     }
@@ -456,29 +568,38 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
     return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
   };
   for (int pass = 0;; ++pass) {
+    Cand held[kHeld];
+    bool has[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = tid + i * kBeamThreads;
+      has[i] = c < n_all && candidate(c, held_key[i], &held[i]);
+    }
+    auto for_each = [&](auto&& f) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (has[i]) f(held[i]);
+      for (int c = tid + kHeld * kBeamThreads; c < n_all; c += kBeamThreads) {
+        Cand o;
+        if (candidate(c, __ldcg(keys + c), &o)) f(o);
+      }
+    };
     // threshold as in the chunks, on the upper halves of the ordered scores
     uint32_t mine = 0;
-    for (int c = tid; c < n_all; c += kBeamThreads) {
-      Cand o;
-      if (candidate(c, &o)) mine = max(mine, (uint32_t)(o.score >> 32));
-    }
+    for_each([&](const Cand& o) { mine = max(mine, (uint32_t)(o.score >> 32)); });
     const uint32_t bar = warp_qth_largest(mine, (K + kWarps - 1) / kWarps);
     if (lane == 0) s_bar[warp] = bar;
-    if (tid == 0) s_count = s_near = 0;
     __syncthreads();
     uint32_t least = ~0u;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) least = min(least, s_bar[w]);
-    for (int c = tid; c < n_all; c += kBeamThreads) {
-      Cand o;
-      if (candidate(c, &o) && (uint32_t)(o.score >> 32) >= least) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kListCap) list[at] = o;
-      }
-    }
+    for_each([&](const Cand& o) {
+      if ((uint32_t)(o.score >> 32) < least) return;
+      const int at = atomicAdd(&s_count, 1);
+      if (at < kListCap) list[at] = o;
+    });
     __syncthreads();
-    const int n = s_count;
-    int got = min(n, K);
+    const int n = s_count, got = min(n, K);
     if (n <= kListCap) {
       for (int i = tid; i < n; i += kBeamThreads) {
         int rank = 0;
@@ -492,10 +613,9 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
       Cand last{~0ull, ~0ull, -1};
       for (int k = 0; k < K; ++k) {
         Cand best{0, 0, kMaxBeams};
-        for (int c = tid; c < n_all; c += kBeamThreads) {
-          Cand o;
-          if (candidate(c, &o) && better(last, o) && better(o, best)) best = o;
-        }
+        for_each([&](const Cand& o) {
+          if (better(last, o) && better(o, best)) best = o;
+        });
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
           Cand o;
@@ -523,24 +643,25 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
         s_again[picked[i].beam] = s_again[picked[i + 1].beam] = 1;
         s_near = 1;
       }
-    const Cand end = picked[got - 1];
-    if (got == K)
-      for (int c = tid; c < n_all; c += kBeamThreads) {
-        Cand o;
-        if (candidate(c, &o) && o.beam != end.beam && better(end, o) &&
-            value(end.score) - value(o.score) <= kNear + 1e-15 * fabs(value(end.score))) {
+    if (got == K) {
+      const Cand end = picked[got - 1];
+      const double near = value(end.score) - (kNear + 1e-15 * fabs(value(end.score)));
+      const uint64_t bound = ordered(near);
+      for_each([&](const Cand& o) {
+        if (o.score >= bound && o.beam != end.beam && better(end, o)) {
           s_again[o.beam] = s_again[end.beam] = 1;
           s_near = 1;
         }
-      }
+      });
+    }
+    __syncthreads();
+    if (!s_near) break;
     if (tid < 64) {
       const double t = exp2((double)tid / 64);
       table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
     }
+    if (tid == 0) s_count = 0;
     __syncthreads();
-    const bool near = s_near != 0;
-    __syncthreads();  // (s_near is cleared by the next pass)
-    if (!near) break;
     for (int w = 0; w < W; ++w) {
       if (!s_again[w] || s_done[w]) continue;
       Sum2 acc;
@@ -585,7 +706,10 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
 template <typename T>
 cudaError_t launch_chunks(const BeamK& p, int per_thread, unsigned grid, cudaStream_t stream) {
   constexpr int kN = Pack<T>::kN;
-  if (per_thread == 32)
+  constexpr int kLongest = sizeof(T) == 4 ? 32 : 64;
+  if (per_thread == kLongest)
+    beam_chunk_kernel<T, kLongest / kN><<<grid, kBeamThreads, 0, stream>>>(p);
+  else if (per_thread == 32)
     beam_chunk_kernel<T, 32 / kN><<<grid, kBeamThreads, 0, stream>>>(p);
   else
     beam_chunk_kernel<T, 8 / kN><<<grid, kBeamThreads, 0, stream>>>(p);
@@ -594,13 +718,18 @@ cudaError_t launch_chunks(const BeamK& p, int per_thread, unsigned grid, cudaStr
 
 }  // namespace
 
-BeamPlan make_beam_plan(int num_groups, int beam_width, int vocab_size, int num_selected) {
+BeamPlan make_beam_plan(pa_dtype dtype, int num_groups, int beam_width, int vocab_size,
+                        int num_selected) {
   BeamPlan b{};
   const int64_t rows = (int64_t)num_groups * beam_width;
   const int64_t span = (int64_t)vocab_size + kBeamAlign - 1;
   auto chunks = [&](int e) { return (span + kBeamThreads * e - 1) / (kBeamThreads * e); };
-  // chunks of 8192 logits where they give each of the 152 SMs two CTAs, else of 2048
-  b.per_thread = rows * chunks(32) >= 2 * 152 ? 32 : 8;
+  // the longest chunks (32 registers of logits a thread) that give each of the 152 SMs
+  // two CTAs
+  const int longest = dtype == PA_F32 ? 32 : 64;
+  b.per_thread = 8;
+  for (int e = longest; e > 8 && b.per_thread == 8; e /= 2)
+    if (e != 16 && rows * chunks(e) >= 2 * 152) b.per_thread = e;
   b.chunks = (int)chunks(b.per_thread);
   b.off_stats = (rows * b.chunks * num_selected * 8 + 255) / 256 * 256;
   b.bytes = b.off_stats + rows * b.chunks * 8;

@@ -14,10 +14,12 @@
 // released entry of a block whose count fell below 0 proposes INT_MIN + its place
 // to the count itself by atomicMin; the lowest wins, and afterwards owns the push.
 //
-// A few MB at most are read (tables, counts), in four dependent passes over the
-// released entries: latency bounds it, so the passes run in one cluster of CTAs
-// with cluster barriers between them (a grid's barrier or a launch costs several
-// of those), and a wide second kernel writes the tables and lists.
+// Shape.  A few MB at most are read and written (tables, counts, lists), but by
+// passes that each need all of the one before: references, claims, owners counted,
+// owners pushed, tables.  So a call is one kernel whose CTAs meet at a barrier
+// between the passes: up to eight CTAs as one cluster, more (one per SM at most) as
+// a cooperative grid.  Every CTA keeps the rows' sources and lengths in shared memory
+// and does the small scans over rows or pieces for itself.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -31,8 +33,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarpsPerCta = kThreads / 32;
-constexpr int kCluster = 8;  // the portable size
-constexpr int kSeg = 256;    // table entries of one piece: 8 per lane
+constexpr int kMaxCluster = 8;  // the portable size
+constexpr int kSeg = 256;       // table entries (or listed tokens) of one piece: 8 per lane
+constexpr int kPer = kSeg / 32;
 // counts below this are claims: INT_MIN + the place of a released entry
 constexpr int kClaim = -(1 << 30);
 
@@ -48,30 +51,32 @@ struct Pool {
   unsigned* err;
 };
 
-struct Cta {
-  int rank, ranks, tid, lane, warp;  // this CTA in the cluster, this thread in it
-  int64_t gwarp, gwarps;             // this warp among the cluster's
+// The CTAs of a call, and this thread's place among them.
+struct Team {
+  int rank, ranks, tid, lane, warp;
+  int gwarp, gwarps;  // this warp among all
+  bool cluster;
+  __device__ __forceinline__ explicit Team(bool one_cluster) : cluster(one_cluster) {
+    rank = (int)blockIdx.x;
+    ranks = (int)gridDim.x;
+    tid = threadIdx.x;
+    lane = tid & 31;
+    warp = tid >> 5;
+    gwarp = warp * ranks + rank;
+    gwarps = kWarpsPerCta * ranks;
+  }
+  // global writes before it are seen after it, by all
+  __device__ __forceinline__ void sync() const {
+    if (cluster) {
+      __threadfence();
+      cg::this_cluster().sync();
+    } else {
+      cg::this_grid().sync();
+    }
+  }
 };
-__device__ __forceinline__ Cta this_cta() {
-  cg::cluster_group cl = cg::this_cluster();
-  Cta t;
-  t.rank = (int)cl.block_rank();
-  t.ranks = (int)cl.num_blocks();
-  t.tid = threadIdx.x;
-  t.lane = t.tid & 31;
-  t.warp = t.tid >> 5;
-  t.gwarp = (int64_t)t.warp * t.ranks + t.rank;
-  t.gwarps = (int64_t)kWarpsPerCta * t.ranks;
-  return t;
-}
-// cluster barrier; global writes before it are seen after it
-__device__ __forceinline__ void cluster_sync() {
-  __threadfence();
-  cg::this_cluster().sync();
-}
 
-__device__ __forceinline__ void copy_refs(const Pool& p, const Cta& t) {
-  if (p.extra_refs == p.extra_refs_out) return;
+__device__ __forceinline__ void copy_refs(const Pool& p, const Team& t) {
   const int64_t step = (int64_t)kThreads * t.ranks;
   const int64_t first = (int64_t)t.rank * kThreads + t.tid;
   if (((reinterpret_cast<uintptr_t>(p.extra_refs) |
@@ -101,104 +106,114 @@ __device__ __forceinline__ bool in_pool(const Pool& p, int id) {
   return id >= 0 && (int64_t)id < p.num_blocks;
 }
 
-// The released pieces: piece i is entries [col0, col0 + kSeg) of a row; entry(row,
-// col) says whether the call releases it and which block it names.  counts: one
-// int per piece, global (pieces <= max_pieces of the plan).
+// Released entries come in pieces: piece i is entries [col0, col0 + kSeg) of the
+// (i / pieces_per_row)-th row that releases any.  load(k, col, &row, &id): whether the
+// call releases that entry, its row, and the block that it names.
 //
-// claim(): every released entry of a block out of references proposes itself.
-template <class Entry>
-__device__ __forceinline__ void claim_released(const Pool& p, const Cta& t, int pieces,
+// claim_released: every released entry of a block out of references proposes itself.
+template <class Load>
+__device__ __forceinline__ void claim_released(const Pool& p, const Team& t, int pieces,
                                                int pieces_per_row, int width,
-                                               const Entry& entry) {
-  for (int64_t i = t.gwarp; i < pieces; i += t.gwarps) {
-    const int k = (int)(i / pieces_per_row), col0 = (int)(i % pieces_per_row) * kSeg;
+                                               const Load& load) {
+  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+    const int k = i / pieces_per_row, col0 = i % pieces_per_row * kSeg;
+    int ids[kPer], count[kPer], row = 0;
 #pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) {
-      int row, id;
-      const int col = col0 + e * 32 + t.lane;
-      if (!entry(k, col, &row, &id)) continue;
-      const int v = __ldcg(p.extra_refs_out + id);
-      if (v >= 0) continue;
-      if (v < -1 && v > kClaim) flag_error(p.err, PA_DEV_ERR_METADATA);
-      atomicMin(p.extra_refs_out + id, INT_MIN + row * width + col);
+    for (int e = 0; e < kPer; ++e)
+      if (!load(k, col0 + e * 32 + t.lane, &row, &ids[e])) ids[e] = -1;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) count[e] = ids[e] >= 0 ? __ldcg(p.extra_refs_out + ids[e]) : 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (count[e] >= 0) continue;
+      if (count[e] < -1 && count[e] > kClaim) flag_error(p.err, PA_DEV_ERR_METADATA);
+      atomicMin(p.extra_refs_out + ids[e], INT_MIN + row * width + col0 + e * 32 + t.lane);
     }
   }
 }
 // owners among a piece's entries: a mask per 32 entries
-template <class Entry>
-__device__ __forceinline__ void owners_of(const Pool& p, const Cta& t, int k, int col0,
-                                          int width, const Entry& entry,
-                                          unsigned (&mask)[kSeg / 32], int (&ids)[kSeg / 32]) {
-  bool mine[kSeg / 32];
+template <class Load>
+__device__ __forceinline__ void owners_of(const Pool& p, const Team& t, int k, int col0,
+                                          int width, const Load& load, unsigned (&mask)[kPer],
+                                          int (&ids)[kPer]) {
+  int count[kPer], row = 0;
 #pragma unroll
-  for (int e = 0; e < kSeg / 32; ++e) {
-    int row;
-    const int col = col0 + e * 32 + t.lane;
-    mine[e] = entry(k, col, &row, &ids[e]) &&
-              __ldcg(p.extra_refs_out + ids[e]) == INT_MIN + row * width + col;
-  }
+  for (int e = 0; e < kPer; ++e)
+    if (!load(k, col0 + e * 32 + t.lane, &row, &ids[e])) ids[e] = -1;
 #pragma unroll
-  for (int e = 0; e < kSeg / 32; ++e) mask[e] = __ballot_sync(~0u, mine[e]);
+  for (int e = 0; e < kPer; ++e) count[e] = ids[e] >= 0 ? __ldcg(p.extra_refs_out + ids[e]) : 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    mask[e] = __ballot_sync(~0u, count[e] == INT_MIN + row * width + col0 + e * 32 + t.lane);
 }
-template <class Entry>
-__device__ __forceinline__ void count_owners(const Pool& p, const Cta& t, int pieces,
-                                             int pieces_per_row, int width,
-                                             const Entry& entry, int* counts) {
-  for (int64_t i = t.gwarp; i < pieces; i += t.gwarps) {
-    unsigned mask[kSeg / 32];
-    int ids[kSeg / 32];
-    owners_of(p, t, (int)(i / pieces_per_row), (int)(i % pieces_per_row) * kSeg, width, entry,
-              mask, ids);
+template <class Load>
+__device__ __forceinline__ void count_owners(const Pool& p, const Team& t, int pieces,
+                                             int pieces_per_row, int width, const Load& load,
+                                             int* counts) {
+  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+    unsigned mask[kPer];
+    int ids[kPer];
+    owners_of(p, t, i / pieces_per_row, i % pieces_per_row * kSeg, width, load, mask, ids);
     int n = 0;
 #pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) n += __popc(mask[e]);
+    for (int e = 0; e < kPer; ++e) n += __popc(mask[e]);
     if (t.lane == 0) counts[i] = n;
   }
 }
-// Pushes the freed blocks from stack position `base` on; returns how many there
-// are (in every thread).  scratch: a long long of shared memory and a warp's 32.
-template <class Entry>
-__device__ __forceinline__ int64_t push_owners(const Pool& p, const Cta& t, int pieces,
-                                               int pieces_per_row, int width,
-                                               const Entry& entry, const int* counts,
-                                               int64_t base, long long* total,
-                                               long long* warp_sums, int* starts) {
-  // every CTA scans all counts, a round of kThreads at a time, and pushes what its
-  // warps have of the round
+
+struct Scan {  // shared memory of the scans
+  long long warp_sums[32];
+  long long total;
+  int starts[kThreads];
+};
+
+// f(piece, sum of the counts before it) for each piece whose count is not 0, by the
+// warp of the team that takes it; the sum of all counts, in every thread.  (Every CTA
+// scans all counts, a round of kThreads at a time.)
+template <class F>
+__device__ __forceinline__ int64_t in_order(const Team& t, int pieces, const int* counts,
+                                            Scan& sh, const F& f) {
   int64_t sum = 0;
   for (int first = 0; first < pieces; first += kThreads) {
     const int i = first + t.tid;
-    const long long n = i < pieces ? __ldcg(counts + i) : 0;
-    const long long before = block_scan_excl(n, total, warp_sums);
-    starts[t.tid] = n ? (int)before : -1;
-    const int64_t round = *total;
+    const int n = i < pieces ? __ldcg(counts + i) : 0;
+    const int before = (int)block_scan_excl((long long)n, &sh.total, sh.warp_sums);
+    sh.starts[t.tid] = n ? before : -1;
+    const int64_t round = sh.total;
     __syncthreads();
-    for (int j = t.warp * t.ranks + t.rank; j < kThreads; j += kWarpsPerCta * t.ranks) {
-      const int start = starts[j];
-      if (start < 0) continue;  // (same for the whole warp)
-      const int piece = first + j;
-      unsigned mask[kSeg / 32];
-      int ids[kSeg / 32];
-      owners_of(p, t, piece / pieces_per_row, piece % pieces_per_row * kSeg, width, entry,
-                mask, ids);
-      int64_t at = base + sum + start;
-#pragma unroll
-      for (int e = 0; e < kSeg / 32; ++e) {
-        if (mask[e] >> t.lane & 1) {
-          const int64_t pos = at + __popc(mask[e] & ((1u << t.lane) - 1));
-          if (pos < p.free_capacity)
-            p.free_blocks[pos] = ids[e];
-          else
-            flag_error(p.err, PA_DEV_ERR_METADATA);
-          p.extra_refs_out[ids[e]] = 0;
-        }
-        at += __popc(mask[e]);
-      }
-    }
+    for (int j = t.gwarp; j < kThreads; j += t.gwarps)
+      if (sh.starts[j] >= 0) f(first + j, sum + sh.starts[j]);  // (one j to a warp)
     sum += round;
     __syncthreads();  // starts and total are written again
   }
   return sum;
+}
+
+// Pushes the freed blocks from stack position `base` on; how many there are.
+template <class Load>
+__device__ __forceinline__ int64_t push_owners(const Pool& p, const Team& t, int pieces,
+                                               int pieces_per_row, int width,
+                                               const Load& load, const int* counts,
+                                               int64_t base, Scan& sh) {
+  return in_order(t, pieces, counts, sh, [&](int piece, int64_t before) {
+    unsigned mask[kPer];
+    int ids[kPer];
+    owners_of(p, t, piece / pieces_per_row, piece % pieces_per_row * kSeg, width, load, mask,
+              ids);
+    int64_t at = base + before;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (mask[e] >> t.lane & 1) {
+        const int64_t pos = at + __popc(mask[e] & ((1u << t.lane) - 1));
+        if (pos < p.free_capacity)
+          p.free_blocks[pos] = ids[e];
+        else
+          flag_error(p.err, PA_DEV_ERR_METADATA);
+        p.extra_refs_out[ids[e]] = 0;
+      }
+      at += __popc(mask[e]);
+    }
+  });
 }
 
 // ---- fork --------------------------------------------------------------------------
@@ -213,33 +228,31 @@ struct ForkK {
   Pool pool;
   int64_t* block_mapping;
   int32_t* num_pairs;
+  int cols;      // table columns of one tile
+  bool cluster;
   // workspace
-  int32_t* row_info;  // [rows] source row, -1: none, or its own in place: nothing to do
-  int32_t* row_len;   // [rows] length of the new row
-  int32_t* row_last;  // [rows] fresh last block, -1: the source's
   int32_t* row_need;  // [rows] partly filled shared last block (its id), -1: none
   int32_t* counts;    // [pieces]
 };
 
-__global__ void __launch_bounds__(kThreads) fork_plan_kernel(ForkK p) {
+__global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   extern __shared__ int sh[];
   const int R = p.num_rows;
   int* s_src = sh;            // source of each new row (-1: none)
   int* s_uses = sh + R;       // new rows of each old row
   int* s_len = sh + 2 * R;    // old rows' lengths
-  int* s_part = sh + 3 * R;   // new rows' partly filled last block, -1: none
+  int* s_part = sh + 3 * R;   // new rows' partly filled last block, -1: none; then the
+                              // fresh block in its place, -1: none
   int* s_gone = sh + 4 * R;   // old rows nobody takes over, in order
-  __shared__ int starts[kThreads];
-  __shared__ long long warp_sums[32];
-  __shared__ long long total;
-  const Cta t = this_cta();
+  int* s_tile = sh + 5 * R;   // [rows][cols] of the new tables
+  __shared__ Scan scan;
+  const Team t(p.cluster);
   const bool lead = t.rank == 0;
   const Pool& q = p.pool;
-  copy_refs(q, t);
   const int64_t height = stack_height(q, lead && t.tid == 0);
   unsigned bad = 0;
   for (int r = t.tid; r < R; r += kThreads) {
-    const int s = p.sources[r];
+    const int s = __ldg(p.sources + r);
     const int64_t L = p.seq_lens[r];
     const bool fits = L >= 0 && L <= (int64_t)p.width * kBS;
     if (s < -1 || s >= R || !fits) bad = PA_DEV_ERR_METADATA;
@@ -251,52 +264,59 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(ForkK p) {
   __syncthreads();
   for (int r = t.tid; r < R; r += kThreads)
     if (s_src[r] >= 0) atomicAdd(&s_uses[s_src[r]], 1);
-  // sources, lengths and counts are read: the outputs may replace them
-  cluster_sync();
-  // rows nobody takes over, in order
-  int gone = 0;
-  for (int base = 0; base < R; base += kThreads) {
-    const int r = base + t.tid;
-    const bool g = r < R && s_uses[r] == 0;
-    const int at = (int)block_scan_excl((long long)g, &total, warp_sums);
-    if (g) s_gone[gone + at] = r;
-    gone += (int)total;
+  if (q.extra_refs != q.extra_refs_out) {
+    copy_refs(q, t);
+    t.sync();
+  } else {
     __syncthreads();
   }
   // ---- references: u - 1 for each block of an old row that u new rows take over
   const int segs = (p.width + kSeg - 1) / kSeg;
-  for (int64_t i = t.gwarp; i < (int64_t)R * segs; i += t.gwarps) {
-    const int s = (int)(i / segs), col0 = (int)(i % segs) * kSeg;
+  for (int i = t.gwarp; i < R * segs; i += t.gwarps) {
+    const int s = i / segs, col0 = i % segs * kSeg;
     const int change = s_uses[s] - 1;
     const int nb = (s_len[s] + kBS - 1) / kBS;
     if (change == 0 || col0 >= nb) continue;
     const int32_t* row = p.tables + (int64_t)s * p.width;
+    int ids[kPer];
 #pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) {
+    for (int e = 0; e < kPer; ++e) {
       const int col = col0 + e * 32 + t.lane;
-      if (col >= nb) break;
-      const int id = __ldg(row + col);
-      if (in_pool(q, id))
-        atomicAdd(q.extra_refs_out + id, change);
-      else
+      ids[e] = col < nb ? __ldg(row + col) : INT_MIN;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (in_pool(q, ids[e]))
+        atomicAdd(q.extra_refs_out + ids[e], change);
+      else if (ids[e] != INT_MIN || col0 + e * 32 + t.lane < nb)
         flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
     }
   }
-  // ---- the new rows' partly filled last blocks (by every CTA for itself)
+  // ---- the new rows' partly filled last blocks, and the rows nobody takes over (by
+  // every CTA for itself)
   for (int r = t.tid; r < R; r += kThreads) {
     const int s = s_src[r];
     int id = -1;
     if (s >= 0 && s_len[s] % kBS != 0) {
       id = __ldg(p.tables + (int64_t)s * p.width + s_len[s] / kBS);
       if (!in_pool(q, id)) {
-        flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
+        if (lead) flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
         id = -1;
       }
     }
     s_part[r] = id;
   }
-  cluster_sync();
-  auto entry = [&](int k, int col, int* row, int* id) {
+  int gone = 0;
+  for (int base = 0; base < R; base += kThreads) {
+    const int r = base + t.tid;
+    const bool g = r < R && s_uses[r] == 0 && s_len[r] > 0;
+    const int at = (int)block_scan_excl((long long)g, &scan.total, scan.warp_sums);
+    if (g) s_gone[gone + at] = r;
+    gone += (int)scan.total;
+    __syncthreads();
+  }
+  t.sync();
+  auto load = [&](int k, int col, int* row, int* id) {
     const int s = s_gone[k];
     *row = s;
     if (col >= (s_len[s] + kBS - 1) / kBS) return false;
@@ -304,13 +324,14 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(ForkK p) {
     return in_pool(q, *id);
   };
   const int pieces = gone * segs;
-  claim_released(q, t, pieces, segs, p.width, entry);
+  claim_released(q, t, pieces, segs, p.width, load);
   // ---- which rows need a copy of their last block: all that hold it but the first,
   // and that one too where others outside hold it (a warp per row)
-  for (int64_t r = t.gwarp; r < R; r += t.gwarps) {
+  for (int r = t.gwarp; r < R; r += t.gwarps) {
     const int id = s_part[r];
     int need = -1;
     if (id >= 0) {
+      const int extra = __ldcg(q.extra_refs_out + id);
       int holders = 0, before = 0;
       for (int o = t.lane; o < R; o += 32)
         if (s_part[o] == id) {
@@ -319,29 +340,31 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(ForkK p) {
         }
       holders = __reduce_add_sync(~0u, holders);
       before = __reduce_add_sync(~0u, before);
-      const int others = max(__ldcg(q.extra_refs_out + id), 0) + 1 - holders;
-      if (before > 0 || others > 0) need = id;
+      if (before > 0 || max(extra, 0) + 1 - holders > 0) need = id;
     }
     if (t.lane == 0) p.row_need[r] = need;
   }
-  cluster_sync();
-  count_owners(q, t, pieces, segs, p.width, entry, p.counts);
-  cluster_sync();
-  const int64_t freed = push_owners(q, t, pieces, segs, p.width, entry, p.counts, height,
-                                    &total, warp_sums, starts);
-  cluster_sync();
-  // ---- copies, in row order, onto blocks popped from the stack (the first CTA)
-  if (!lead) return;
+  int64_t freed = 0;
+  t.sync();
+  if (pieces > 0) {  // (the same in every CTA)
+    count_owners(q, t, pieces, segs, p.width, load, p.counts);
+    t.sync();
+    freed = push_owners(q, t, pieces, segs, p.width, load, p.counts, height, scan);
+    t.sync();
+  }
+  // ---- copies, in row order, onto blocks popped from the stack
   const int64_t top = min(height + freed, q.free_capacity);
   int64_t pairs = 0;
   for (int base = 0; base < R; base += kThreads) {
     const int r = base + t.tid;
     const int id = r < R ? __ldcg(p.row_need + r) : -1;
-    const int64_t k = pairs + block_scan_excl((long long)(id >= 0), &total, warp_sums);
+    const int64_t k = pairs + block_scan_excl((long long)(id >= 0), &scan.total,
+                                              scan.warp_sums);
     int fresh = -1;
-    if (id >= 0) {
+    if (id >= 0 && k < top) fresh = __ldcg(q.free_blocks + (top - 1 - k));
+    if (r < R) s_part[r] = fresh;
+    if (lead && id >= 0) {
       if (k < top) {
-        fresh = __ldcg(q.free_blocks + (top - 1 - k));
         p.block_mapping[2 * k] = id;
         p.block_mapping[2 * k + 1] = fresh;
         atomicAdd(q.extra_refs_out + id, -1);
@@ -350,48 +373,42 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(ForkK p) {
         flag_error(q.err, PA_DEV_ERR_NO_BLOCKS);
       }
     }
-    if (r < R) {
-      const int s = s_src[r];
-      const int L = s >= 0 ? s_len[s] : 0;
-      p.row_info[r] = s;
-      p.row_len[r] = L;
-      p.row_last[r] = fresh;
-      p.seq_lens_out[r] = L;
-    }
-    pairs += total;
+    pairs += scan.total;
     __syncthreads();
   }
   pairs = min(pairs, top);
-  if (t.tid == 0) {
-    *p.num_pairs = (int)pairs;
-    *q.free_count_out = (int)(top - pairs);
+  if (lead) {
+    if (t.tid == 0) {
+      *p.num_pairs = (int)pairs;
+      *q.free_count_out = (int)(top - pairs);
+    }
+    for (int64_t k = pairs + t.tid; k < R; k += kThreads)
+      p.block_mapping[2 * k] = p.block_mapping[2 * k + 1] = -1;
+    for (int r = t.tid; r < R; r += kThreads)
+      p.seq_lens_out[r] = s_src[r] >= 0 ? s_len[s_src[r]] : 0;
   }
-  for (int64_t k = pairs + t.tid; k < R; k += kThreads)
-    p.block_mapping[2 * k] = p.block_mapping[2 * k + 1] = -1;
-}
-
-// The new tables.  A CTA takes some columns of all rows: what it will write is read
-// first, so that the tables may be changed in place whatever rows trade places.
-__global__ void __launch_bounds__(256) fork_tables_kernel(ForkK p, int cols) {
-  extern __shared__ int sh[];  // [rows][cols]
-  const int col0 = blockIdx.x * cols;
+  // ---- the new tables.  A CTA takes some columns of all rows: what it will write is
+  // read first, so that the tables may be changed in place whatever rows trade places.
   const bool in_place = p.tables == p.tables_out;
-  const int n = p.num_rows * cols;
-  pdl_wait();
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int r = i / cols, col = col0 + i % cols;
-    const int L = __ldcg(p.row_len + r);
-    if (col >= (L + kBS - 1) / kBS) continue;
-    const int s = __ldcg(p.row_info + r), last = __ldcg(p.row_last + r);
-    sh[i] = last != -1 && col == L / kBS ? last : p.tables[(int64_t)s * p.width + col];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int r = i / cols, col = col0 + i % cols;
-    const int L = __ldcg(p.row_len + r);
-    if (col >= (L + kBS - 1) / kBS) continue;
-    if (in_place && __ldcg(p.row_info + r) == r && __ldcg(p.row_last + r) == -1) continue;
-    p.tables_out[(int64_t)r * p.width + col] = sh[i];
+  const int cols = p.cols, items = R * cols;
+  for (int col0 = t.rank * cols; col0 < p.width; col0 += t.ranks * cols) {
+#pragma unroll 4
+    for (int i = t.tid; i < items; i += kThreads) {
+      const int r = i / cols, col = col0 + i % cols, s = s_src[r];
+      if (s < 0) continue;
+      const int L = s_len[s], fresh = s_part[r];
+      if (col < (L + kBS - 1) / kBS)
+        s_tile[i] = fresh != -1 && col == L / kBS ? fresh
+                                                  : p.tables[(int64_t)s * p.width + col];
+    }
+    __syncthreads();
+    for (int i = t.tid; i < items; i += kThreads) {
+      const int r = i / cols, col = col0 + i % cols, s = s_src[r];
+      if (s < 0 || col >= (s_len[s] + kBS - 1) / kBS) continue;
+      if (in_place && s == r && s_part[r] == -1) continue;
+      p.tables_out[(int64_t)r * p.width + col] = s_tile[i];
+    }
+    __syncthreads();
   }
 }
 
@@ -411,82 +428,91 @@ struct CompactK {
   int64_t* src_slots;
   int64_t* dst_slots;
   int32_t* num_moves;
+  bool cluster;
   // workspace
-  int32_t* same;    // [rows] listed tokens that stay where they are
-  int32_t* broken;  // [rows] the list is not one
-  int32_t* info;    // [rows][4]: tokens kept (-1: as it is), first changed block, old
-                    // length, moves
+  int32_t* same;    // [rows][list pieces] listed tokens that stay where they are, -1: the
+                    // list is not one
+  int32_t* counts;  // [pieces]
+  uint32_t* masks;  // [pieces][kPer] entries that get a fresh block
   int32_t* fresh;   // [rows][width], of the changed blocks: the id that replaces it,
                     // INT_MIN: none does
-  int32_t* counts;  // [pieces]
-  int32_t* bases;   // [pieces] blocks popped before a piece's
 };
 
-__global__ void __launch_bounds__(kThreads) compact_plan_kernel(CompactK p) {
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
   extern __shared__ int sh[];
   const int R = p.num_rows;
   int* s_len = sh;            // old lengths
-  int* s_n = sh + R;          // tokens kept (-1: the row stays as it is)
-  int* s_first = sh + 2 * R;  // first block that changes
-  int* s_end = sh + 3 * R;    // blocks popped up to and including the row
-  __shared__ int starts[kThreads];
-  __shared__ long long warp_sums[32];
-  __shared__ long long total;
+  int* s_start = sh + R;      // tokens kept as they are
+  int* s_n = sh + 2 * R;      // tokens kept (-1: the row stays as it is)
+  int* s_first = sh + 3 * R;  // first block that changes
+  int* s_end = sh + 4 * R;    // 1: the list is not one; then the blocks popped up to and
+                              // including the row
+  __shared__ Scan scan;
   __shared__ int s_popped;
-  const Cta t = this_cta();
+  const Team t(p.cluster);
   const bool lead = t.rank == 0;
   const Pool& q = p.pool;
-  copy_refs(q, t);
   const int64_t height = stack_height(q, lead && t.tid == 0);
   unsigned bad = 0;
   for (int r = t.tid; r < R; r += kThreads) {
     const int64_t L = p.seq_lens[r];
-    const int k = p.keep_lens[r], start = p.keep_start ? p.keep_start[r] : 0;
+    const int k = __ldg(p.keep_lens + r), start = p.keep_start ? __ldg(p.keep_start + r) : 0;
     const bool fits = L >= 0 && L <= (int64_t)p.width * kBS;
-    const bool ok = fits && k <= p.max_keep && (k < 0 || (start >= 0 && start <= L));
+    const bool ok = fits && k <= p.max_keep && (k < 0 || (start >= 0 && start <= L - k));
     if (!ok) bad = PA_DEV_ERR_METADATA;
     s_len[r] = fits ? (int)L : 0;
     s_n[r] = ok && k >= 0 ? start + k : -1;
-    s_first[r] = start;
-    if (lead) p.same[r] = p.broken[r] = 0;
+    s_start[r] = start;
+    s_first[r] = s_end[r] = 0;
   }
-  if (lead && bad) flag_error(q.err, bad);
   if (t.tid == 0) s_popped = 0;
-  cluster_sync();
+  if (q.extra_refs != q.extra_refs_out) copy_refs(q, t);
+  __syncthreads();
   // ---- the lists: ascending positions in [start, L); how many stay in place
-  const int lsegs = (p.max_keep + kSeg - 1) / kSeg;
-  for (int64_t i = t.gwarp; i < (int64_t)R * lsegs; i += t.gwarps) {
-    const int r = (int)(i / lsegs), j0 = (int)(i % lsegs) * kSeg;
-    const int start = s_first[r], k = s_n[r] - start;
+  const int lsegs = (min(p.max_keep, p.width * kBS) + kSeg - 1) / kSeg;
+  for (int i = t.gwarp; i < R * lsegs; i += t.gwarps) {
+    const int r = i / lsegs, j0 = i % lsegs * kSeg;
+    const int start = s_start[r], k = s_n[r] - start;
     if (s_n[r] < 0 || j0 >= k) continue;
     const int32_t* list = p.keep + (int64_t)r * p.max_keep;
+    int v[kPer], before[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int j = j0 + e * 32 + t.lane;
+      v[e] = j < k ? __ldg(list + j) : 0;
+      before[e] = j < k && j > 0 ? __ldg(list + j - 1) : start - 1;
+    }
     int same = 0;
     bool ok = true;
 #pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) {
+    for (int e = 0; e < kPer; ++e) {
       const int j = j0 + e * 32 + t.lane;
       if (j >= k) break;
-      const int v = __ldg(list + j);
-      const int before = j ? __ldg(list + j - 1) : start - 1;
-      ok = ok && v > before && v < s_len[r];
-      same += v == start + j;
+      ok = ok && v[e] > before[e] && v[e] < s_len[r];
+      same += v[e] == start + j;
     }
     same = __reduce_add_sync(~0u, same);
     const bool all = __all_sync(~0u, ok);
-    if (t.lane == 0) {
-      if (same) atomicAdd(p.same + r, same);
-      if (!all) p.broken[r] = 1;
-    }
+    if (t.lane == 0) p.same[i] = all ? same : -1;
   }
-  cluster_sync();
-  bad = 0;
+  t.sync();
+  for (int i = t.tid; i < R * lsegs; i += kThreads) {
+    const int r = i / lsegs;
+    if (s_n[r] < 0 || i % lsegs * kSeg >= s_n[r] - s_start[r]) continue;
+    const int same = __ldcg(p.same + i);
+    if (same < 0)
+      s_end[r] = 1;
+    else
+      atomicAdd(&s_first[r], same);
+  }
+  __syncthreads();
   for (int r = t.tid; r < R; r += kThreads) {
     if (s_n[r] < 0) continue;
-    if (__ldcg(p.broken + r)) {
+    if (s_end[r]) {
       bad = PA_DEV_ERR_METADATA;
       s_n[r] = -1;
     } else {
-      s_first[r] = (s_first[r] + __ldcg(p.same + r)) / kBS;
+      s_first[r] = (s_start[r] + s_first[r]) / kBS;
     }
   }
   if (lead && bad) flag_error(q.err, bad);
@@ -494,217 +520,231 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(CompactK p) {
   // ---- blocks that change and have other holders: replaced by fresh ones
   const int segs = (p.width + kSeg - 1) / kSeg;
   const int pieces = R * segs;
-  auto shared_of = [&](int r, int col0, unsigned (&mask)[kSeg / 32]) {
-    const int left = (s_n[r] + kBS - 1) / kBS;
-    const int32_t* row = p.tables + (int64_t)r * p.width;
-    bool shared[kSeg / 32];
-#pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) {
-      const int col = col0 + e * 32 + t.lane;
-      shared[e] = false;
-      if (col >= s_first[r] && col < left) {
-        const int id = __ldg(row + col);
-        shared[e] = in_pool(q, id) && __ldcg(q.extra_refs + id) > 0;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) mask[e] = __ballot_sync(~0u, shared[e]);
-  };
-  auto changes = [&](int r, int col0) {  // any block of a piece that may change
-    return s_n[r] > col0 * kBS && col0 + kSeg > s_first[r];
-  };
-  for (int64_t i = t.gwarp; i < pieces; i += t.gwarps) {
-    const int r = (int)(i / segs), col0 = (int)(i % segs) * kSeg;
+  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+    const int r = i / segs, col0 = i % segs * kSeg;
+    const int left = (s_n[r] + kBS - 1) / kBS, first = s_first[r];
     int n = 0;
-    if (changes(r, col0)) {
-      unsigned mask[kSeg / 32];
-      shared_of(r, col0, mask);
+    if (s_n[r] >= 0 && left > col0 && first < col0 + kSeg) {
+      const int32_t* row = p.tables + (int64_t)r * p.width;
+      int ids[kPer], extra[kPer];
 #pragma unroll
-      for (int e = 0; e < kSeg / 32; ++e) n += __popc(mask[e]);
+      for (int e = 0; e < kPer; ++e) {
+        const int col = col0 + e * 32 + t.lane;
+        ids[e] = col >= first && col < left ? __ldg(row + col) : -1;
+      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        extra[e] = in_pool(q, ids[e]) ? __ldcg(q.extra_refs + ids[e]) : 0;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int col = col0 + e * 32 + t.lane;
+        if (col >= first && col < left && !in_pool(q, ids[e]))
+          flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
+        const unsigned mask = __ballot_sync(~0u, extra[e] > 0);
+        n += __popc(mask);
+        if (t.lane == 0) p.masks[i * kPer + e] = mask;
+      }
     }
     if (t.lane == 0) p.counts[i] = n;
   }
-  cluster_sync();
+  t.sync();
   // ---- pops in row order; the rows whose running need fits the stack run
-  int64_t sum = 0;
-  for (int base = 0; base < pieces; base += kThreads) {
-    const int i = base + t.tid;
+  for (int64_t sum = 0, base = 0; base < pieces; base += kThreads) {
+    const int i = (int)base + t.tid;
     const long long n = i < pieces ? __ldcg(p.counts + i) : 0;
-    const int64_t before = sum + block_scan_excl(n, &total, warp_sums);
-    if (i < pieces) {
-      if (lead) p.bases[i] = (int)before;
-      if (i % segs == segs - 1) s_end[i / segs] = (int)(before + n);
-    }
-    sum += total;
+    const int64_t before = sum + block_scan_excl(n, &scan.total, scan.warp_sums);
+    if (i < pieces && i % segs == segs - 1) s_end[i / segs] = (int)(before + n);
+    sum += scan.total;
     __syncthreads();
   }
-  cluster_sync();
   bad = 0;
-  for (int r = t.tid; r < R; r += kThreads) {
-    if (pieces > 0 && s_end[r] > height) {
+  for (int r = t.tid; r < R && pieces > 0; r += kThreads) {
+    if (s_end[r] > height) {
       bad = PA_DEV_ERR_NO_BLOCKS;
       s_n[r] = -1;
-    } else if (pieces > 0) {
+    } else {
       atomicMax(&s_popped, s_end[r]);
     }
   }
   if (lead && bad) flag_error(q.err, bad);
   __syncthreads();
   const int64_t popped = s_popped;
-  // ---- fresh ids.  What is shared is told by the counts before any of them changes,
-  // and is marked in p.fresh for what follows.
-  for (int64_t i = t.gwarp; i < pieces; i += t.gwarps) {
-    const int r = (int)(i / segs), col0 = (int)(i % segs) * kSeg;
-    if (!changes(r, col0)) continue;
+  // ---- fresh ids
+  for (int i = t.gwarp; i < pieces && popped > 0; i += t.gwarps) {  // (pieces without a pop)
+    const int r = i / segs, col0 = i % segs * kSeg;
+    if (s_n[r] < 0 || __ldcg(p.counts + i) != 0) continue;
     const int left = (s_n[r] + kBS - 1) / kBS;
-    unsigned mask[kSeg / 32];
-    shared_of(r, col0, mask);
-    int64_t nth = __ldcg(p.bases + i);
 #pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) {
+    for (int e = 0; e < kPer; ++e) {
       const int col = col0 + e * 32 + t.lane;
-      if (col >= s_first[r] && col < left) {
-        int fresh = INT_MIN;
-        if (mask[e] >> t.lane & 1) {
-          fresh = __ldcg(q.free_blocks +
-                         (height - 1 - nth - __popc(mask[e] & ((1u << t.lane) - 1))));
-          if (!in_pool(q, fresh)) {
-            flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
-            fresh = -1;
-          }
-        }
-        p.fresh[(int64_t)r * p.width + col] = fresh;
-      }
-      nth += __popc(mask[e]);
+      if (col >= s_first[r] && col < left) p.fresh[(int64_t)r * p.width + col] = INT_MIN;
     }
   }
-  cluster_sync();
-  auto entry = [&](int r, int col, int* row, int* id) {
+  if (popped > 0)
+    in_order(t, pieces, p.counts, scan, [&](int i, int64_t before) {
+      const int r = i / segs, col0 = i % segs * kSeg;
+      if (s_n[r] < 0) return;
+      const int left = (s_n[r] + kBS - 1) / kBS;
+      const int32_t* row = p.tables + (int64_t)r * p.width;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int col = col0 + e * 32 + t.lane;
+        const unsigned mask = __ldcg(p.masks + i * kPer + e);
+        if (col >= s_first[r] && col < left) {
+          int fresh = INT_MIN;
+          if (mask >> t.lane & 1) {
+            fresh = __ldcg(q.free_blocks +
+                           (height - 1 - before - __popc(mask & ((1u << t.lane) - 1))));
+            if (!in_pool(q, fresh)) {
+              flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
+              fresh = -1;
+            }
+            atomicAdd(q.extra_refs_out + __ldg(row + col), -1);
+          }
+          p.fresh[(int64_t)r * p.width + col] = fresh;
+        }
+        before += __popc(mask);
+      }
+    });
+  // ---- a reference less for the blocks past the kept ones
+  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+    const int r = i / segs, col0 = i % segs * kSeg;
+    const int had = (s_len[r] + kBS - 1) / kBS;
+    const int left = max((s_n[r] + kBS - 1) / kBS, s_first[r]);
+    if (s_n[r] < 0 || had <= col0 || left >= col0 + kSeg) continue;
+    const int32_t* row = p.tables + (int64_t)r * p.width;
+    int ids[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int col = col0 + e * 32 + t.lane;
+      ids[e] = col >= left && col < had ? __ldg(row + col) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (in_pool(q, ids[e])) atomicAdd(q.extra_refs_out + ids[e], -1);
+  }
+  t.sync();
+  auto load = [&](int r, int col, int* row, int* id) {
     *row = r;
     const int n = s_n[r];
     if (n < 0 || col < s_first[r] || col >= (s_len[r] + kBS - 1) / kBS) return false;
-    if (col < (n + kBS - 1) / kBS && __ldcg(p.fresh + (int64_t)r * p.width + col) == INT_MIN)
+    if (col < (n + kBS - 1) / kBS &&
+        (popped == 0 || __ldcg(p.fresh + (int64_t)r * p.width + col) == INT_MIN))
       return false;
     *id = __ldg(p.tables + (int64_t)r * p.width + col);
     return in_pool(q, *id);
   };
-  for (int64_t i = t.gwarp; i < pieces; i += t.gwarps) {
-    const int r = (int)(i / segs), col0 = (int)(i % segs) * kSeg;
-#pragma unroll
-    for (int e = 0; e < kSeg / 32; ++e) {
-      int row, id;
-      if (entry(r, col0 + e * 32 + t.lane, &row, &id)) atomicAdd(q.extra_refs_out + id, -1);
-    }
-  }
-  cluster_sync();
-  claim_released(q, t, pieces, segs, p.width, entry);
-  cluster_sync();
-  count_owners(q, t, pieces, segs, p.width, entry, p.counts);
-  cluster_sync();
-  // the popped ids are read: pushes may take their places
-  const int64_t freed = push_owners(q, t, pieces, segs, p.width, entry, p.counts,
-                                    height - popped, &total, warp_sums, starts);
-  if (!lead) return;
-  if (t.tid == 0)
+  claim_released(q, t, pieces, segs, p.width, load);
+  t.sync();
+  count_owners(q, t, pieces, segs, p.width, load, p.counts);
+  t.sync();
+  const int64_t freed =
+      push_owners(q, t, pieces, segs, p.width, load, p.counts, height - popped, scan);
+  if (lead && t.tid == 0)
     *q.free_count_out = (int)min(height - popped + freed, q.free_capacity);
-  for (int r = t.tid; r < R; r += kThreads) {
-    const int n = s_n[r], first = s_first[r];
+  // ---- the moves: of a row that only loses its end none, unless its last block is
+  // replaced
+  const int64_t wide = (int64_t)p.max_keep + kBS;
+  const int msegs = (int)((wide + kSeg - 1) / kSeg);
+  for (int64_t i = t.gwarp; i < (int64_t)R * msegs; i += t.gwarps) {
+    const int r = (int)(i / msegs), j0 = (int)(i % msegs) * kSeg;
+    const int n = s_n[r], at0 = s_first[r] * kBS, start = s_start[r];
+    const int32_t* list = p.keep + (int64_t)r * p.max_keep;
     int moves = 0;
-    if (n >= 0) {
-      // a row that only loses its end moves nothing, unless its last block is replaced
-      const int start = p.keep_start ? p.keep_start[r] : 0;
-      const bool whole = start + __ldcg(p.same + r) == n;
-      const bool swapped = first * kBS < n &&
-                           __ldcg(p.fresh + (int64_t)r * p.width + first) != INT_MIN;
-      if (!whole || swapped) moves = n - first * kBS;
+    if (n > at0) {
+      // the last token stays where it is if and only if all do
+      const bool whole = n == start || __ldg(list + (n - 1 - start)) == n - 1;
+      const bool swapped =
+          popped > 0 && __ldcg(p.fresh + (int64_t)r * p.width + s_first[r]) != INT_MIN;
+      if (!whole || swapped) moves = n - at0;
     }
-    p.num_moves[r] = moves;
-    int4 info = make_int4(n, first, s_len[r], moves);
-    reinterpret_cast<int4*>(p.info)[r] = info;
-    p.seq_lens_out[r] = n >= 0 ? n : s_len[r];
+    if (j0 == 0 && t.lane == 0) {
+      p.num_moves[r] = moves;
+      p.seq_lens_out[r] = n >= 0 ? n : s_len[r];
+    }
+    const int32_t* row = p.tables + (int64_t)r * p.width;
+    const int32_t* fresh = p.fresh + (int64_t)r * p.width;
+    int pos[kPer], from[kPer], to[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int j = j0 + e * 32 + t.lane, at = at0 + j;
+      pos[e] = j >= moves ? -1 : at < start ? at : __ldg(list + (at - start));
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int at = (at0 + j0 + e * 32 + t.lane) / kBS;
+      from[e] = to[e] = 0;
+      if (pos[e] >= 0) {
+        from[e] = __ldg(row + pos[e] / kBS);
+        const int now = popped > 0 ? __ldcg(fresh + at) : INT_MIN;
+        to[e] = now == INT_MIN ? __ldg(row + at) : now;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (pos[e] < 0) continue;
+      const int j = j0 + e * 32 + t.lane;
+      const bool ok = in_pool(q, from[e]) && in_pool(q, to[e]);
+      if (!ok) flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
+      p.src_slots[r * wide + j] = ok ? (int64_t)from[e] * kBS + pos[e] % kBS : -1;
+      p.dst_slots[r * wide + j] = ok ? (int64_t)to[e] * kBS + (at0 + j) % kBS : -1;
+    }
   }
-}
-
-// The moves: a thread per listed place.
-__global__ void __launch_bounds__(256) compact_moves_kernel(CompactK p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t wide = p.max_keep + kBS;
-  const int r = blockIdx.y;
-  const int4 info = __ldcg(reinterpret_cast<const int4*>(p.info) + r);
-  const int32_t* row = p.tables + (int64_t)r * p.width;
-  const int32_t* fresh = p.fresh + (int64_t)r * p.width;
-  const int start = info.w ? (p.keep_start ? p.keep_start[r] : 0) : 0;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < info.w; i += gridDim.x * 256) {
-    const int at = info.y * kBS + i;
-    const int pos = at < start ? at : p.keep[(int64_t)r * p.max_keep + at - start];
-    const int from = row[pos / kBS];
-    const int was = row[at / kBS], now = fresh[at / kBS];
-    const int to = now == INT_MIN ? was : now;
-    const bool ok = from >= 0 && from < p.pool.num_blocks && to >= 0 &&
-                    to < p.pool.num_blocks;
-    if (!ok) flag_error(p.pool.err, PA_DEV_ERR_BLOCK_ID);
-    p.src_slots[r * wide + i] = ok ? (int64_t)from * kBS + pos % kBS : -1;
-    p.dst_slots[r * wide + i] = ok ? (int64_t)to * kBS + at % kBS : -1;
-  }
-}
-
-// The tables: in place, only what is replaced.
-__global__ void __launch_bounds__(256) compact_tables_kernel(CompactK p) {
-  pdl_wait();
-  const int r = blockIdx.y;
-  const int4 info = __ldcg(reinterpret_cast<const int4*>(p.info) + r);
+  // ---- the tables: in place, only what is replaced, once nobody reads the old ones
   const bool in_place = p.tables == p.tables_out;
-  const int blocks = ((info.x >= 0 ? info.x : info.z) + kBS - 1) / kBS;
-  const int64_t at = (int64_t)r * p.width;
-  for (int col = blockIdx.x * 256 + threadIdx.x; col < blocks; col += gridDim.x * 256) {
-    const int now = info.x >= 0 && col >= info.y ? p.fresh[at + col] : INT_MIN;
-    if (now != INT_MIN)
-      p.tables_out[at + col] = now;
-    else if (!in_place)
-      p.tables_out[at + col] = p.tables[at + col];
+  if (in_place) {
+    if (popped == 0) return;  // (the same in every CTA)
+    t.sync();
+  }
+  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+    const int r = i / segs, col0 = i % segs * kSeg;
+    const int n = s_n[r], blocks = ((n >= 0 ? n : s_len[r]) + kBS - 1) / kBS;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int col = col0 + e * 32 + t.lane;
+      if (col >= blocks) break;
+      const int64_t at = (int64_t)r * p.width + col;
+      const int now = popped > 0 && n >= 0 && col >= s_first[r] ? __ldcg(p.fresh + at) : INT_MIN;
+      if (now != INT_MIN)
+        p.tables_out[at] = now;
+      else if (!in_place)
+        p.tables_out[at] = __ldg(p.tables + at);
+    }
   }
 }
 
+// One kernel over `want` CTAs: a cluster, or a cooperative grid of at most one CTA per
+// SM.  p.cluster tells the kernel which.
 template <class P>
-cudaError_t launch_plan(void (*kernel)(P), const P& p, size_t smem, size_t max_smem,
-                        cudaStream_t stream) {
+cudaError_t launch_team(void (*kernel)(P), P& p, int64_t want, size_t smem, size_t max_smem,
+                        int num_sms, cudaStream_t stream) {
   // (always the largest step's limit: see launch_build_step)
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)max_smem);
     if (e != cudaSuccess) return e;
   }
+  unsigned ctas = 1;
+  while (ctas < kMaxCluster && ctas < want) ctas *= 2;
+  p.cluster = want <= kMaxCluster;
+  if (!p.cluster) ctas = (unsigned)(want < num_sms ? want : num_sms);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  if (p.cluster) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  } else {
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+  }
   cfg.attrs = at;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (e == cudaSuccess) count_launch();
-  return e;
-}
-
-template <class... A>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, size_t smem, cudaStream_t stream,
-                         A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e == cudaSuccess) count_launch();
   return e;
 }
@@ -716,13 +756,23 @@ Pool pool_of(const RowState& r, unsigned* err) {
 
 int64_t pieces_of(int64_t rows, int64_t width) { return rows * ((width + kSeg - 1) / kSeg); }
 
+// CTAs for a call: table entries, listed tokens and counts to copy, a few per thread
+int64_t ctas_for(int64_t entries, int64_t listed, const RowState& r) {
+  const int64_t copied = r.extra_refs == r.extra_refs_out ? 0 : r.num_blocks;
+  const int64_t a = entries / (2 * kThreads), b = listed / (4 * kThreads),
+                c = copied / (8 * kThreads);
+  return 1 + (a > b ? (a > c ? a : c) : (b > c ? b : c));
+}
+
+constexpr size_t kTileBytes = 64 * 1024;  // of a tile of the new tables, at most
+
 }  // namespace
 
 int64_t fork_workspace_bytes(int num_rows, int max_blocks_per_seq) {
-  return 4 * (4ll * num_rows + pieces_of(num_rows, max_blocks_per_seq));
+  return 4 * (num_rows + pieces_of(num_rows, max_blocks_per_seq));
 }
 
-cudaError_t launch_fork_blocks(const ForkArgs& a, cudaStream_t stream) {
+cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, cudaStream_t stream) {
   ForkK p{};
   p.sources = a.sources;
   p.num_rows = a.rows.num_rows;
@@ -735,28 +785,25 @@ cudaError_t launch_fork_blocks(const ForkArgs& a, cudaStream_t stream) {
   p.block_mapping = a.block_mapping;
   p.num_pairs = a.num_pairs;
   const int64_t R = a.rows.num_rows;
-  p.row_info = static_cast<int32_t*>(a.workspace);
-  p.row_len = p.row_info + R;
-  p.row_last = p.row_len + R;
-  p.row_need = p.row_last + R;
+  p.row_need = static_cast<int32_t*>(a.workspace);
   p.counts = p.row_need + R;
-  cudaError_t e = launch_plan(fork_plan_kernel, p, (size_t)(5 * R * 4),
-                              (size_t)5 * kMaxForkRows * 4, stream);
-  if (e != cudaSuccess || R == 0 || p.width == 0) return e;
-  // columns of a CTA: a line of 32 where all rows' fit 40 KB of shared memory, 2 of
-  // them at the largest number of rows
-  int cols = 32;
-  while ((int64_t)cols * R * 4 > 40 * 1024 && cols > 2) cols /= 2;
-  return launch_after(fork_tables_kernel, dim3((unsigned)((p.width + cols - 1) / cols)),
-                      (size_t)cols * R * 4, stream, p, cols);
+  const int64_t want = ctas_for(R * p.width, 0, a.rows);
+  // columns of a tile: a line of 32, fewer (a sector of 8) where that spreads the
+  // columns over more CTAs, and what fits at the largest numbers of rows
+  p.cols = 32;
+  while (p.cols > 8 && (int64_t)p.width <= want * (p.cols / 2)) p.cols /= 2;
+  while (p.cols > 1 && (size_t)(p.cols * R * 4) > kTileBytes) p.cols /= 2;
+  return launch_team(fork_kernel, p, want, (size_t)((5 + p.cols) * R * 4),
+                     (size_t)5 * kMaxForkRows * 4 + kTileBytes, num_sms, stream);
 }
 
 int64_t compact_workspace_bytes(int num_rows, int max_blocks_per_seq) {
-  return 4 * (6ll * num_rows + (int64_t)num_rows * max_blocks_per_seq +
-              2 * pieces_of(num_rows, max_blocks_per_seq));
+  return 4 * (pieces_of(num_rows, (int64_t)max_blocks_per_seq * kBS) +
+              (1 + kPer) * pieces_of(num_rows, max_blocks_per_seq) +
+              (int64_t)num_rows * max_blocks_per_seq);
 }
 
-cudaError_t launch_compact_blocks(const CompactArgs& a, cudaStream_t stream) {
+cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_t stream) {
   CompactK p{};
   p.keep = a.keep;
   p.max_keep = a.max_keep;
@@ -773,21 +820,12 @@ cudaError_t launch_compact_blocks(const CompactArgs& a, cudaStream_t stream) {
   p.dst_slots = a.dst_slots;
   p.num_moves = a.num_moves;
   const int64_t R = a.rows.num_rows;
-  p.info = static_cast<int32_t*>(a.workspace);  // 16-byte aligned
-  p.same = p.info + 4 * R;
-  p.broken = p.same + R;
-  p.counts = p.broken + R;
-  p.bases = p.counts + pieces_of(R, p.width);
-  p.fresh = p.bases + pieces_of(R, p.width);
-  cudaError_t e = launch_plan(compact_plan_kernel, p, (size_t)(4 * R * 4),
-                              (size_t)4 * kMaxForkRows * 4, stream);
-  if (e != cudaSuccess || R == 0 || p.width == 0) return e;
-  const int64_t wide = (int64_t)p.max_keep + kBS;
-  const unsigned gm = (unsigned)((wide + 255) / 256 < 64 ? (wide + 255) / 256 : 64);
-  e = launch_after(compact_moves_kernel, dim3(gm, (unsigned)R), 0, stream, p);
-  if (e != cudaSuccess) return e;
-  const unsigned gt = (unsigned)((p.width + 255) / 256 < 64 ? (p.width + 255) / 256 : 64);
-  return launch_after(compact_tables_kernel, dim3(gt, (unsigned)R), 0, stream, p);
+  p.same = static_cast<int32_t*>(a.workspace);
+  p.counts = p.same + pieces_of(R, (int64_t)p.width * kBS);
+  p.masks = reinterpret_cast<uint32_t*>(p.counts + pieces_of(R, p.width));
+  p.fresh = reinterpret_cast<int32_t*>(p.masks) + kPer * pieces_of(R, p.width);
+  return launch_team(compact_kernel, p, ctas_for(R * p.width, R * (int64_t)p.max_keep, a.rows),
+                     (size_t)(5 * R * 4), (size_t)5 * kMaxForkRows * 4, num_sms, stream);
 }
 
 }  // namespace pa

@@ -1087,7 +1087,8 @@ pa_status beam_size_status(int num_groups, int beam_width, int vocab_size,
   if (beam_width > kMaxBeams || num_selected > kMaxBeamSelected ||
       vocab_size > (1 << 24) || (int64_t)num_groups * beam_width >= (1 << 24))
     return PA_ERR_UNSUPPORTED;
-  const BeamPlan plan = make_beam_plan(num_groups, beam_width, vocab_size, num_selected);
+  const BeamPlan plan =
+      make_beam_plan(PA_F32, num_groups, beam_width, vocab_size, num_selected);
   if ((int64_t)num_groups * beam_width * plan.chunks >= (1ll << 31))
     return PA_ERR_UNSUPPORTED;
   return PA_OK;
@@ -1102,7 +1103,9 @@ pa_status pa_beam_select_workspace_size(int num_groups, int beam_width, int voca
   if (!bytes) return PA_ERR_INVALID_ARG;
   if (pa_status st = beam_size_status(num_groups, beam_width, vocab_size, num_selected))
     return st;
-  *bytes = (size_t)make_beam_plan(num_groups, beam_width, vocab_size, num_selected).bytes;
+  // (fp32 logits are cut into the most chunks)
+  *bytes =
+      (size_t)make_beam_plan(PA_F32, num_groups, beam_width, vocab_size, num_selected).bytes;
   return PA_OK;
 }
 
@@ -1125,8 +1128,11 @@ pa_status pa_beam_select(const void* logits, pa_dtype logits_dtype, int num_grou
       !aligned(beam_scores, 4) || !aligned(scores, 4) || !aligned(parents, 4) ||
       !aligned(tokens, 4))
     return PA_ERR_INVALID_ARG;
-  const BeamPlan plan = make_beam_plan(num_groups, beam_width, vocab_size, num_selected);
-  if (!has_workspace(workspace, workspace_bytes, plan.bytes)) return PA_ERR_INVALID_ARG;
+  const BeamPlan plan =
+      make_beam_plan(logits_dtype, num_groups, beam_width, vocab_size, num_selected);
+  size_t bytes;
+  pa_beam_select_workspace_size(num_groups, beam_width, vocab_size, num_selected, &bytes);
+  if (!has_workspace(workspace, workspace_bytes, (int64_t)bytes)) return PA_ERR_INVALID_ARG;
   const size_t rows = (size_t)num_groups * beam_width;
   const size_t picks = (size_t)num_groups * num_selected;
   // a group's scores and flags are read before its picks are written: in place where
@@ -1182,7 +1188,7 @@ pa_status pa_fork_blocks(const int32_t* sources, int num_rows,
   const DeviceInfo* di = device_info();
   if (!di) return PA_ERR_CUDA;
   const ForkArgs a{rows, sources, block_mapping, num_pairs, workspace, di->err};
-  const cudaError_t e = launch_fork_blocks(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_fork_blocks(a, di->num_sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -1251,7 +1257,7 @@ pa_status pa_compact_blocks(const int32_t* keep, int max_keep, const int32_t* ke
   if (!di) return PA_ERR_CUDA;
   const CompactArgs a{rows,      keep,      max_keep,  keep_lens, keep_start,
                       src_slots, dst_slots, num_moves, workspace, di->err};
-  const cudaError_t e = launch_compact_blocks(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_compact_blocks(a, di->num_sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -17,7 +17,8 @@ struct BeamPlan {
   int chunks;                 // of a row
   int64_t off_stats, bytes;   // workspace: keys, then each chunk's (max, sum)
 };
-BeamPlan make_beam_plan(int num_groups, int beam_width, int vocab_size, int num_selected);
+BeamPlan make_beam_plan(pa_dtype dtype, int num_groups, int beam_width, int vocab_size,
+                        int num_selected);
 struct BeamArgs {
   const void* logits;
   pa_dtype dtype;
@@ -65,7 +66,7 @@ struct ForkArgs {
   unsigned* err;
 };
 int64_t fork_workspace_bytes(int num_rows, int max_blocks_per_seq);
-cudaError_t launch_fork_blocks(const ForkArgs& a, cudaStream_t stream);
+cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, cudaStream_t stream);
 
 struct CompactArgs {
   RowState rows;
@@ -80,7 +81,7 @@ struct CompactArgs {
   unsigned* err;
 };
 int64_t compact_workspace_bytes(int num_rows, int max_blocks_per_seq);
-cudaError_t launch_compact_blocks(const CompactArgs& a, cudaStream_t stream);
+cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_t stream);
 
 // ---- copies and moves of all layers (move_kernels.cu) --------------------------
 struct LayerCaches {
