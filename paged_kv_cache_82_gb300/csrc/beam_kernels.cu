@@ -30,7 +30,8 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = kBeamThreads / 32;
-constexpr int kListCap = 1024;
+constexpr int kVecCap = 256;    // 16-byte vectors of a chunk that hold a candidate
+constexpr int kListCap = 1024;  // candidates of a group
 // log2(e) in two parts, the first rounded towards zero so that the second is
 // positive (a product with -inf then keeps its sign)
 constexpr float kLog2eHi = 1.44269502162933349609375f;
@@ -104,6 +105,7 @@ struct Pack<float> {
   static constexpr uint32_t kNegInf = 0xff800000u;
   static constexpr float kLowest = -FLT_MAX;
   static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
   static __device__ __forceinline__ float get(const uint4& v, int i) {
     return __uint_as_float(word(v, i));
   }
@@ -126,6 +128,9 @@ struct Pack<__nv_bfloat16> {
   static constexpr float kLowest = -0x1.fep127f;
   static __device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) {
     return __bfloat16_as_ushort(*p);
+  }
+  static __device__ __forceinline__ float get(const __nv_bfloat16* p) {
+    return __bfloat162float(*p);
   }
   static __device__ __forceinline__ float2 pair(const uint4& v, int i) {
     const uint32_t w = word(v, i);
@@ -157,6 +162,7 @@ struct Pack<__half> {
   static constexpr uint32_t kNegInf = 0xfc00u;
   static constexpr float kLowest = -65504.f;
   static __device__ __forceinline__ uint32_t bits(const __half* p) { return __half_as_ushort(*p); }
+  static __device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
   static __device__ __forceinline__ float2 pair(const uint4& v, int i) {
     const uint32_t w = word(v, i);
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -235,7 +241,7 @@ __device__ __noinline__ float odd_sum(const T* x, int base, int V, float mx) {
          ((acc[0].y + acc[1].y) + (acc[2].y + acc[3].y));
 }
 
-// More logits than the list holds reach the threshold (long runs of equal ones): the
+// More vectors than there is room for hold a candidate (long runs of equal logits): the
 // best key below the last one taken, K times.
 template <typename T, int kVecs>
 __device__ __noinline__ void pick_one_by_one(const T* x, int base, int V, int K,
@@ -273,11 +279,13 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     beam_chunk_kernel(BeamK p) {
   using P = Pack<T>;
   constexpr int kN = P::kN, kStep = kBeamThreads * kN;
-  __shared__ uint64_t list[kListCap];
+  __shared__ uint4 vecs[kVecCap];
+  __shared__ int vec_at[kVecCap];
+  __shared__ uint64_t list[kVecCap * kN];
   __shared__ uint32_t s_max[kWarps], s_bar[kWarps];
   __shared__ float s_sum[kWarps];
   __shared__ uint64_t s_best[kWarps];
-  __shared__ int s_count;
+  __shared__ int s_count, s_vecs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / (unsigned)p.chunks;
   const int chunk = (int)(blockIdx.x - row * p.chunks);
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     s_max[warp] = wmax;
     s_bar[warp] = bar;
   }
-  if (tid == 0) s_count = 0;
+  if (tid == 0) s_count = s_vecs = 0;
   __syncthreads();
   uint32_t omax = 0, least = ~0u;
 #pragma unroll
@@ -326,28 +334,22 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     for (int i = tid; i < K; i += kBeamThreads) p.keys[out * K + i] = 0;
     return;
   }
-  // ---- the chunk's logits at or above the threshold: the vectors that hold one, one
-  // at a time
+  // ---- the vectors that hold a logit at or above the threshold, to shared memory
   const float floor_x = fmaxf(unordered(least), P::kLowest);
   unsigned hits = 0;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    hits |= (typename P::Max(v[i])).reaches(floor_x) ? 1u << i : 0u;
-  while (hits) {
-    const int i = __ffs(hits) - 1;
-    hits &= hits - 1;
-    uint4 one = v[0];
+  for (int i = 0; i < kVecs; ++i) hits |= (typename P::Max(v[i])).reaches(floor_x) ? 1u << i : 0u;
+  if (hits) {
+    int at = atomicAdd(&s_vecs, __popc(hits));
 #pragma unroll
-    for (int k = 1; k < kVecs; ++k)
-      if (k == i) one = v[k];
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const float e = P::get(one, j);
-      if (e >= floor_x) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kListCap) list[at] = make_key(fminf(e, FLT_MAX), base + i * kStep + j);
+    for (int i = 0; i < kVecs; ++i)
+      if (hits >> i & 1) {
+        if (at < kVecCap) {
+          vecs[at] = v[i];
+          vec_at[at] = base + i * kStep;
+        }
+        ++at;
       }
-    }
   }
   // ---- sum of 2^(x log2 e - c), c = fl32(mx log2 e): c's rounding is put right
   // at the end, so every exponent is good to 2^-23 of itself
@@ -375,7 +377,13 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
   sum = 0.f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) sum += s_sum[w];
-  const int n = s_count;
+  const int n_vecs = s_vecs;
+  if (n_vecs <= kVecCap)  // the logits among theirs
+    for (int e = tid; e < n_vecs * kN; e += kBeamThreads) {
+      const float f = P::get(reinterpret_cast<const T*>(vecs) + e);
+      if (f >= floor_x)
+        list[atomicAdd(&s_count, 1)] = make_key(fminf(f, FLT_MAX), vec_at[e / kN] + e % kN);
+    }
   // NaN, infinite or huge logits: the exponents above overflowed.  (Uniform.)
   const bool odd = !(sum >= 0.25f && sum < INFINITY) || fabsf(mx) > 1e30f;
   if (odd) {
@@ -395,7 +403,9 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     p.stats[out] = make_float2(mx, sum * exp2f(-d));
   }
   uint64_t* keys = p.keys + out * K;
-  if (n <= kListCap) {
+  if (n_vecs <= kVecCap) {
+    __syncthreads();
+    const int n = s_count;
     for (int i = tid; i < n; i += kBeamThreads) {
       const uint64_t mine = list[i];
       int rank = 0;
@@ -478,10 +488,15 @@ __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
   return a.key > b.key;
 }
 
-// One group: the sums of its rows, then the K best of their candidates.  What a
+// One group: the sums of its rows, then the K best of their candidates.
+//
+// FP64 units are few, so 64-bit scores are computed only where they can decide: an
+// fp32 score and a bound of its error sort out the candidates that reach the K-th
+// best score less kNear (some 20 to 50), and those are scored in 64 bits.  What a
 // thread's first kHeld candidates are is loaded while the sums are, and kept.
 constexpr int kHeld = 4;
 __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
+  __shared__ double s_sum[kMaxBeams];
   __shared__ double s_off[kMaxBeams];    // -log sum
   __shared__ float s_top[kMaxBeams];     // row maximum
   __shared__ float s_cum[kMaxBeams];     // beam score; NaN: the beam offers nothing
@@ -493,7 +508,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
   __shared__ Cand s_best[kWarps];
   __shared__ Cand picked[kMaxBeamSelected];
   __shared__ float2 table[64];
-  __shared__ int s_count, s_near;
+  __shared__ int s_count, s_near, s_there[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = p.a.beam_width, K = p.a.num_selected, S = p.chunks;
   const int64_t row0 = (int64_t)blockIdx.x * W;
@@ -516,94 +531,101 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
     held_key[i] = c < n_all ? __ldcg(keys + c) : 0;
   }
   for (int w = warp; w < W; w += kWarps) {
+    if (s_done[w]) continue;
+    const float2* st = p.stats + (row0 + w) * S;
     float m = -INFINITY;
-    double sum = 0.0;
-    if (!s_done[w]) {
-      const float2* st = p.stats + (row0 + w) * S;
-      for (int i = lane; i < S; i += 32) {
-        const float2 v = __ldcg(st + i);
-        if (v.x > m) {
-          sum = (m > -INFINITY ? sum * (double)expf(m - v.x) : 0.0) + (double)v.y;
-          m = v.x;
-        } else if (v.x > -INFINITY) {
-          sum += (double)(v.y * expf(v.x - m));
-        }
-      }
-      float top = m;
+    for (int i = lane; i < S; i += 32) m = fmaxf(m, __ldcg(&st[i].x));
 #pragma unroll
-      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      if (m > -INFINITY && m < top) sum *= (double)expf(m - top);
-      m = top;
-      sum = warp_sum(sum);
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    double sum = 0.0;
+    for (int i = lane; i < S; i += 32) {
+      const float2 v = __ldcg(st + i);
+      if (v.x > -INFINITY) sum += (double)(v.y * expf(v.x - m));
     }
+    sum = warp_sum(sum);
     if (lane == 0) {
       s_top[w] = m;
-      s_off[w] = -log(sum);
-      if (m == -INFINITY && !s_done[w]) s_cum[w] = NAN;
+      s_sum[w] = sum;
+      if (m == -INFINITY) s_cum[w] = NAN;
     }
   }
   __syncthreads();
-  // the c-th candidate, whose key (unless its beam is finished) is `key`; false: none
-  auto candidate = [&](int c, uint64_t key, Cand* o) {
+  for (int w = tid; w < W; w += kBeamThreads) s_off[w] = s_done[w] ? 0.0 : -log(s_sum[w]);
+  __syncthreads();
+  // The c-th candidate, whose key (unless its beam is finished) is `key`: f(beam, key,
+  // fp32 score, bound of its error).
+  auto offer = [&](int c, uint64_t key, auto&& f) {
     const int w = c / per_row;
     const float cum = s_cum[w];
-    if (isnan(cum)) return false;
-    o->beam = w;
-    double s;
+    if (isnan(cum)) return;
     if (s_done[w]) {
-      if (c != w * per_row) return false;
-      o->key = (uint32_t)~p.a.end_token;
-      s = (double)cum;
-    } else {
-      o->key = key;
-      if (key == 0) return false;
-      const float x = unordered((uint32_t)(key >> 32));
-      s = (double)cum + (((double)x - (double)s_top[w]) + s_off[w]);
-      if ((float)s == -INFINITY) return false;
+      if (c == w * per_row) f(w, (uint64_t)(uint32_t)~p.a.end_token, cum, 0.f);
+    } else if (key != 0) {
+      const float d = unordered((uint32_t)(key >> 32)) - s_top[w], off = (float)s_off[w];
+      f(w, key, cum + (d + off), 0x1p-22f * (fabsf(cum) + fabsf(d) + fabsf(off)));
     }
-    o->score = ordered(s);
-    return true;
+  };
+  auto for_each = [&](auto&& f) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = tid + i * kBeamThreads;
+      if (c < n_all) offer(c, held_key[i], f);
+    }
+    for (int c = tid + kHeld * kBeamThreads; c < n_all; c += kBeamThreads)
+      offer(c, __ldcg(keys + c), f);
+  };
+  // score in 64 bits; false: below fp32's range, none
+  auto scored = [&](int w, uint64_t key, Cand* o) {
+    double s = (double)s_cum[w];
+    if (!s_done[w])
+      s += ((double)unordered((uint32_t)(key >> 32)) - (double)s_top[w]) + s_off[w];
+    *o = Cand{ordered(s), key, w};
+    return (float)s != -INFINITY;
   };
   auto value = [](uint64_t o) {
     return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
   };
   for (int pass = 0;; ++pass) {
-    Cand held[kHeld];
-    bool has[kHeld];
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int c = tid + i * kBeamThreads;
-      has[i] = c < n_all && candidate(c, held_key[i], &held[i]);
-    }
-    auto for_each = [&](auto&& f) {
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (has[i]) f(held[i]);
-      for (int c = tid + kHeld * kBeamThreads; c < n_all; c += kBeamThreads) {
-        Cand o;
-        if (candidate(c, __ldcg(keys + c), &o)) f(o);
-      }
-    };
-    // threshold as in the chunks, on the upper halves of the ordered scores
+    // threshold as in the chunks: what K candidates reach at least
     uint32_t mine = 0;
-    for_each([&](const Cand& o) { mine = max(mine, (uint32_t)(o.score >> 32)); });
+    for_each([&](int, uint64_t, float s, float err) {
+      const float at_least = s - err;
+      if (at_least > -INFINITY) mine = max(mine, ordered(at_least));
+    });
     const uint32_t bar = warp_qth_largest(mine, (K + kWarps - 1) / kWarps);
     if (lane == 0) s_bar[warp] = bar;
     __syncthreads();
     uint32_t least = ~0u;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) least = min(least, s_bar[w]);
-    for_each([&](const Cand& o) {
-      if ((uint32_t)(o.score >> 32) < least) return;
+    // (0: fewer than K anywhere; unordered(0) is a NaN, and everything is taken)
+    float floor_s = unordered(least);
+    floor_s -= 1.25f * (float)kNear + 0x1p-22f * fabsf(floor_s);
+    for_each([&](int w, uint64_t key, float s, float err) {
+      if (s + err < floor_s) return;
       const int at = atomicAdd(&s_count, 1);
-      if (at < kListCap) list[at] = o;
+      if (at < kListCap) list[at] = Cand{0, key, w};
     });
     __syncthreads();
-    const int n = s_count, got = min(n, K);
+    const int n = s_count;
+    int got = 0;
     if (n <= kListCap) {
+      int there = 0;
+      for (int i = tid; i < n; i += kBeamThreads) {
+        Cand o;
+        const bool ok = scored(list[i].beam, list[i].key, &o);
+        list[i].score = ok ? o.score : 0;  // (0: below the score of any candidate)
+        there += ok;
+      }
+      there = (int)__reduce_add_sync(~0u, (unsigned)there);
+      if (lane == 0) s_there[warp] = there;
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w) got += s_there[w];
+      got = min(got, K);
       for (int i = tid; i < n; i += kBeamThreads) {
         int rank = 0;
         const Cand o = list[i];
+        if (o.score == 0) continue;
         for (int j = 0; j < n; ++j) rank += better(list[j], o);
         if (rank < K) picked[rank] = o;
       }
@@ -611,10 +633,11 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
     } else {
       // more candidates than the list holds: the best after the last one, K times
       Cand last{~0ull, ~0ull, -1};
-      for (int k = 0; k < K; ++k) {
+      for (; got < K; ++got) {
         Cand best{0, 0, kMaxBeams};
-        for_each([&](const Cand& o) {
-          if (better(last, o) && better(o, best)) best = o;
+        for_each([&](int w, uint64_t key, float, float) {
+          Cand o;
+          if (scored(w, key, &o) && better(last, o) && better(o, best)) best = o;
         });
 #pragma unroll
         for (int d = 16; d; d >>= 1) {
@@ -628,34 +651,44 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
         __syncthreads();
         for (int w = 0; w < kWarps; ++w)
           if (better(s_best[w], best)) best = s_best[w];
+        if (best.score == 0) break;  // (the same in every thread)
         last = best;
-        if (tid == 0) picked[k] = best;
+        if (tid == 0) picked[got] = best;
         __syncthreads();
       }
+      __syncthreads();
     }
-    if (pass == 1 || got == 0) break;
+    if (pass == 1 || got == 0) {
+      if (tid == 0) s_count = got;
+      break;
+    }
     // ---- scores of two beams too close for the fp32 sums: next to each other, or
     // one left out next to the last one picked
-    for (int i = tid; i + 1 < got; i += kBeamThreads)
-      if (picked[i].beam != picked[i + 1].beam &&
-          value(picked[i].score) - value(picked[i + 1].score) <=
-              kNear + 1e-15 * fabs(value(picked[i].score))) {
-        s_again[picked[i].beam] = s_again[picked[i + 1].beam] = 1;
-        s_near = 1;
-      }
+    auto near = [&](const Cand& a, const Cand& b) {
+      if (a.beam == b.beam ||
+          value(a.score) - value(b.score) > kNear + 1e-15 * fabs(value(a.score)))
+        return;
+      s_again[a.beam] = s_again[b.beam] = 1;
+      s_near = 1;
+    };
+    for (int i = tid; i + 1 < got; i += kBeamThreads) near(picked[i], picked[i + 1]);
     if (got == K) {
       const Cand end = picked[got - 1];
-      const double near = value(end.score) - (kNear + 1e-15 * fabs(value(end.score)));
-      const uint64_t bound = ordered(near);
-      for_each([&](const Cand& o) {
-        if (o.score >= bound && o.beam != end.beam && better(end, o)) {
-          s_again[o.beam] = s_again[end.beam] = 1;
-          s_near = 1;
-        }
-      });
+      if (n <= kListCap) {
+        for (int i = tid; i < n; i += kBeamThreads)
+          if (list[i].score != 0 && better(end, list[i])) near(end, list[i]);
+      } else {
+        for_each([&](int w, uint64_t key, float, float) {
+          Cand o;
+          if (scored(w, key, &o) && better(end, o)) near(end, o);
+        });
+      }
     }
     __syncthreads();
-    if (!s_near) break;
+    if (!s_near) {
+      if (tid == 0) s_count = got;
+      break;
+    }
     if (tid < 64) {
       const double t = exp2((double)tid / 64);
       table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
@@ -686,7 +719,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
       __syncthreads();
     }
   }
-  const int got = min(s_count, K);
+  __syncthreads();
+  const int got = s_count;
   for (int i = tid; i < K; i += kBeamThreads) {
     const int64_t at = (int64_t)blockIdx.x * K + i;
     float score = -INFINITY;
