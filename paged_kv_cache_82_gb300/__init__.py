@@ -1009,14 +1009,16 @@ def _layers(k_cache: torch.Tensor, v_cache: torch.Tensor, cache_dtype: Optional[
     if L < 1:
         raise ValueError("the caches hold no layer")
     NB, Hkv, bs, D = _cache_geometry(k_cache[0], cache_dtype)
-    strides, dev = [], torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t[0].is_contiguous():
-            raise ValueError(f"{n} must be contiguous within a layer")
-        if t.get_device() < 0 or t.get_device() != dev:
-            raise ValueError(f"{n} must be on the current CUDA device")
-        strides.append(t.stride(0) * t.element_size())
-    return (L, *strides, NB, bs, Hkv, D)
+    if not (k_cache.is_contiguous() or k_cache[0].is_contiguous()):
+        raise ValueError("k_cache must be contiguous within a layer")
+    if not (v_cache.is_contiguous() or v_cache[0].is_contiguous()):
+        raise ValueError("v_cache must be contiguous within a layer")
+    dev = k_cache.get_device()
+    if dev < 0 or dev != v_cache.get_device() or dev != torch.cuda.current_device():
+        raise ValueError("the caches must be on the current CUDA device" if dev >= 0 else
+                         "k_cache must be a CUDA tensor")
+    e = k_cache.element_size()
+    return L, k_cache.stride(0) * e, v_cache.stride(0) * e, NB, bs, Hkv, D
 
 
 def pa_copy_blocks_layers(k_cache: torch.Tensor, v_cache: torch.Tensor,

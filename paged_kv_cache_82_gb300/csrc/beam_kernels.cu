@@ -460,15 +460,18 @@ __device__ __forceinline__ void add_exp(Sum2& acc, float x, float mx, const floa
 }
 
 template <typename T>
-__device__ __forceinline__ void precise_sum(Sum2& acc, const T* x, int V, float mx,
-                                            const float2* table) {
+__device__ __noinline__ double precise_sum(const void* logits, int64_t at, int V, float mx,
+                                           const float2* table) {
   using P = Pack<T>;
+  const T* x = static_cast<const T*>(logits) + at;
+  Sum2 acc;
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   for (int i = threadIdx.x * P::kN - off; i < V; i += kBeamThreads * P::kN) {
     const uint4 v = load_vec<T>(x, i, V);
 #pragma unroll
     for (int j = 0; j < P::kN; ++j) add_exp(acc, clean(P::get(v, j)), mx, table);
   }
+  return (double)acc.hi + (double)acc.lo;
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -477,258 +480,341 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-struct Cand {
-  uint64_t score;  // ordered(double)
-  uint64_t key;
-  int beam;
+// A candidate: its score (ordered(double); 0: none), and what decides between equal
+// scores, the larger being better: the lower beam, the larger logit, the lower token (in
+// 6, 32 and 24 bits).
+constexpr int kTokenBits = 24;
+static_assert(kMaxBeams <= 64 && kMaxVocab <= 1 << kTokenBits, "fields of Cand::tie");
+struct __align__(16) Cand {
+  uint64_t score, tie;
+  __device__ __forceinline__ int beam() const { return kMaxBeams - 1 - (int)(tie >> 56); }
+  __device__ __forceinline__ int token() const {
+    return (1 << kTokenBits) - 1 - (int)(tie & ((1 << kTokenBits) - 1));
+  }
+  __device__ __forceinline__ float logit() const {
+    return unordered((uint32_t)(tie >> kTokenBits));
+  }
 };
+__device__ __forceinline__ uint64_t make_tie(int beam, uint64_t key) {
+  return (uint64_t)(kMaxBeams - 1 - beam) << 56 | (key >> 32) << kTokenBits |
+         ((uint32_t)key & ((1 << kTokenBits) - 1));
+}
 __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
-  if (a.score != b.score) return a.score > b.score;
-  if (a.beam != b.beam) return a.beam < b.beam;
-  return a.key > b.key;
+  return a.score > b.score || (a.score == b.score && a.tie > b.tie);
+}
+__device__ __forceinline__ double value(uint64_t o) {
+  return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+
+// One group in shared memory.
+struct Group {
+  Cand list[kListCap];  // candidates that may be among the K best
+  Cand picked[kMaxBeamSelected];
+  Cand best[kWarps];
+  double sum[kMaxBeams];    // of exp(x - top)
+  double off[kMaxBeams];    // -log of it
+  double part[kWarps];
+  uint64_t held[kListCap];  // the first candidates' keys
+  float2 table[64];
+  float off32[kMaxBeams];   // -logf of it
+  float top[kMaxBeams];     // row maximum
+  float cum[kMaxBeams];     // beam score; NaN: the beam offers nothing
+  uint8_t done[kMaxBeams];  // finished: one candidate, the end token
+  uint8_t again[kMaxBeams];
+  uint32_t bar[kWarps];
+  int count, near, ranked;
+};
+
+// A candidate's score in 64 bits (0: below fp32's range, none)
+__device__ __forceinline__ uint64_t score64(const Group& g, int w, float logit) {
+  double s = (double)g.cum[w];
+  if (!g.done[w]) s += ((double)logit - (double)g.top[w]) + g.off[w];
+  return (float)s != -INFINITY ? ordered(s) : 0;
+}
+
+// two picks whose beams' sums have to be taken again to tell their order
+__device__ __forceinline__ void note_near(Group& g, const Cand& a, const Cand& b) {
+  const int x = a.beam(), y = b.beam();
+  const double v = value(a.score);
+  if (x == y || v - value(b.score) > kNear + 1e-15 * fabs(v)) return;
+  g.again[x] = g.again[y] = 1;
+  g.near = 1;
+}
+
+// barrier of the joining kernel's first eight warps
+__device__ __forceinline__ void main_warps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kBeamThreads) : "memory");
+}
+// of how many of their threads p holds
+__device__ __forceinline__ int main_warps_count(bool p) {
+  int n;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %1, 0;\n\tbar.red.popc.u32 %0, 1, %2, q;\n\t}"
+      : "=r"(n)
+      : "r"((int)p), "n"(kBeamThreads)
+      : "memory");
+  return n;
+}
+
+// The rare ways, out of the way of the usual ones' instructions.
+//
+// More candidates than the list holds: the best after the last one, K times; the
+// number picked.  near: notes the candidates close to the last one picked.
+__device__ __noinline__ int pick_from_all(Group& g, const uint64_t* keys, int n_all,
+                                          int per_row, int end_key, int K, bool look_near) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto candidate = [&](int c, Cand* o) {
+    const int w = c / per_row;
+    if (isnan(g.cum[w])) return false;
+    if (g.done[w] && c != w * per_row) return false;
+    const uint64_t key = g.done[w] ? (uint64_t)(uint32_t)end_key : __ldcg(keys + c);
+    if (key == 0) return false;
+    *o = Cand{score64(g, w, unordered((uint32_t)(key >> 32))), make_tie(w, key)};
+    return o->score != 0;
+  };
+  Cand last{~0ull, ~0ull};
+  int got = 0;
+  for (; got < K; ++got) {
+    Cand best{0, 0};
+    for (int c = threadIdx.x; c < n_all; c += kBeamThreads) {
+      Cand o;
+      if (candidate(c, &o) && better(last, o) && better(o, best)) best = o;
+    }
+    for (int d = 16; d; d >>= 1) {
+      Cand o;
+      o.score = __shfl_xor_sync(~0u, best.score, d);
+      o.tie = __shfl_xor_sync(~0u, best.tie, d);
+      if (better(o, best)) best = o;
+    }
+    if (lane == 0) g.best[warp] = best;
+    main_warps_sync();
+    for (int w = 0; w < kWarps; ++w)
+      if (better(g.best[w], best)) best = g.best[w];
+    if (best.score == 0) break;  // (the same in every thread)
+    last = best;
+    if (threadIdx.x == 0) g.picked[got] = best;
+    main_warps_sync();
+  }
+  main_warps_sync();
+  if (look_near && got == K)
+    for (int c = threadIdx.x; c < n_all; c += kBeamThreads) {
+      Cand o;
+      if (candidate(c, &o) && better(last, o)) note_near(g, last, o);
+    }
+  return got;
+}
+
+// The sums of the rows noted, in two fp32 parts.
+__device__ __noinline__ void sum_again(Group& g, const BeamArgs& a, int64_t row0) {
+  const int tid = threadIdx.x;
+  if (tid < 64) {
+    const double t = exp2((double)tid / 64);
+    g.table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
+  }
+  main_warps_sync();
+  for (int w = 0; w < a.beam_width; ++w) {
+    if (!g.again[w] || g.done[w]) continue;
+    const int64_t at = (row0 + w) * a.row_stride;
+    double part = a.dtype == PA_F32
+                      ? precise_sum<float>(a.logits, at, a.vocab_size, g.top[w], g.table)
+                  : a.dtype == PA_F16
+                      ? precise_sum<__half>(a.logits, at, a.vocab_size, g.top[w], g.table)
+                      : precise_sum<__nv_bfloat16>(a.logits, at, a.vocab_size, g.top[w],
+                                                   g.table);
+    part = warp_sum(part);
+    if ((tid & 31) == 0) g.part[tid >> 5] = part;
+    main_warps_sync();
+    if (tid == 0) {
+      double sum = 0.0;
+      for (int i = 0; i < kWarps; ++i) sum += g.part[i];
+      g.off[w] = -log(sum);
+      g.off32[w] = (float)g.off[w];
+    }
+    main_warps_sync();
+  }
 }
 
 // One group: the sums of its rows, then the K best of their candidates.
 //
-// FP64 units are few, so 64-bit scores are computed only where they can decide: an
-// fp32 score and a bound of its error sort out the candidates that reach the K-th
-// best score less kNear (some 20 to 50), and those are scored in 64 bits.  What a
-// thread's first kHeld candidates are is loaded while the sums are, and kept.
-constexpr int kHeld = 4;
-__global__ void __launch_bounds__(kBeamThreads) beam_join_kernel(BeamK p) {
-  __shared__ double s_sum[kMaxBeams];
-  __shared__ double s_off[kMaxBeams];    // -log sum
-  __shared__ float s_top[kMaxBeams];     // row maximum
-  __shared__ float s_cum[kMaxBeams];     // beam score; NaN: the beam offers nothing
-  __shared__ uint8_t s_done[kMaxBeams];  // finished: one candidate, the end token
-  __shared__ uint8_t s_again[kMaxBeams];
-  __shared__ Cand list[kListCap];
-  __shared__ double s_part[kWarps];
-  __shared__ uint32_t s_bar[kWarps];
-  __shared__ Cand s_best[kWarps];
-  __shared__ Cand picked[kMaxBeamSelected];
-  __shared__ float2 table[64];
-  __shared__ int s_count, s_near, s_there[kWarps];
+// Bound by latency: a chain of short steps, each run once, whose instructions come
+// from a cache that the chunk kernel has just filled; so loops are not unrolled, and
+// what is rarely needed lies outside.  FP64 units are few: 64-bit scores are computed
+// only where they can decide.  An fp32 score and a bound of its error sort out the
+// candidates that reach the K-th best score less kNear (some 20 to 50).
+//
+// A ninth warp takes the logs in 64 bits (a long chain of FP64 operations) while the
+// others sort out by fp32 ones.
+constexpr int kJoinThreads = kBeamThreads + 32;
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamK p) {
+  extern __shared__ __align__(16) char shared[];
+  Group& g = *reinterpret_cast<Group*>(shared);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = p.a.beam_width, K = p.a.num_selected, S = p.chunks;
   const int64_t row0 = (int64_t)blockIdx.x * W;
-  for (int w = tid; w < W; w += kBeamThreads) {
-    const float cum = p.a.beam_scores[row0 + w];
-    s_cum[w] = isfinite(cum) ? cum : NAN;
-    s_done[w] = p.a.finished && p.a.finished[row0 + w];
-    s_again[w] = 0;
+  if (tid < W) {
+    const float cum = p.a.beam_scores[row0 + tid];
+    g.cum[tid] = isfinite(cum) ? cum : NAN;
+    g.done[tid] = p.a.finished && p.a.finished[row0 + tid];
+    g.again[tid] = 0;
   }
-  if (tid == 0) s_count = s_near = 0;
-  const int per_row = S * K, n_all = W * per_row;
+  if (tid == 0) g.count = g.near = g.ranked = 0;
+  const int per_row = S * K, n_all = W * per_row, n_held = min(n_all, kListCap);
   const uint64_t* keys = p.keys + row0 * per_row;
+  const int end_key = ~p.a.end_token;
   __syncthreads();
   pdl_wait();
   // (a finished row's keys are not written, and not used)
-  uint64_t held_key[kHeld];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int c = tid + i * kBeamThreads;
-    held_key[i] = c < n_all ? __ldcg(keys + c) : 0;
-  }
-  for (int w = warp; w < W; w += kWarps) {
-    if (s_done[w]) continue;
+  if (warp < kWarps)
+#pragma unroll 4
+    for (int c = tid; c < n_held; c += kBeamThreads) g.held[c] = __ldcg(keys + c);
+#pragma unroll 1
+  for (int w = warp; w < W; w += kWarps + 1) {
+    if (g.done[w]) {
+      if (lane == 0) g.sum[w] = 1.0;
+      continue;
+    }
     const float2* st = p.stats + (row0 + w) * S;
     float m = -INFINITY;
-    for (int i = lane; i < S; i += 32) m = fmaxf(m, __ldcg(&st[i].x));
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
     double sum = 0.0;
-    for (int i = lane; i < S; i += 32) {
-      const float2 v = __ldcg(st + i);
-      if (v.x > -INFINITY) sum += (double)(v.y * expf(v.x - m));
+    if (S <= 32) {
+      const float2 v = lane < S ? __ldcg(st + lane) : make_float2(-INFINITY, 0.f);
+      m = v.x;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+      if (v.x > -INFINITY) sum = (double)(v.y * expf(v.x - m));
+    } else {
+#pragma unroll 1
+      for (int i = lane; i < S; i += 32) m = fmaxf(m, __ldcg(&st[i].x));
+#pragma unroll
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+#pragma unroll 1
+      for (int i = lane; i < S; i += 32) {
+        const float2 v = __ldcg(st + i);
+        if (v.x > -INFINITY) sum += (double)(v.y * expf(v.x - m));
+      }
     }
     sum = warp_sum(sum);
     if (lane == 0) {
-      s_top[w] = m;
-      s_sum[w] = sum;
-      if (m == -INFINITY) s_cum[w] = NAN;
+      g.top[w] = m;
+      g.sum[w] = sum;
+      g.off32[w] = -logf((float)sum);
+      if (m == -INFINITY) g.cum[w] = NAN;
     }
   }
   __syncthreads();
-  for (int w = tid; w < W; w += kBeamThreads) s_off[w] = s_done[w] ? 0.0 : -log(s_sum[w]);
-  __syncthreads();
-  // The c-th candidate, whose key (unless its beam is finished) is `key`: f(beam, key,
-  // fp32 score, bound of its error).
-  auto offer = [&](int c, uint64_t key, auto&& f) {
-    const int w = c / per_row;
-    const float cum = s_cum[w];
-    if (isnan(cum)) return;
-    if (s_done[w]) {
-      if (c == w * per_row) f(w, (uint64_t)(uint32_t)~p.a.end_token, cum, 0.f);
-    } else if (key != 0) {
-      const float d = unordered((uint32_t)(key >> 32)) - s_top[w], off = (float)s_off[w];
-      f(w, key, cum + (d + off), 0x1p-22f * (fabsf(cum) + fabsf(d) + fabsf(off)));
-    }
-  };
-  auto for_each = [&](auto&& f) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int c = tid + i * kBeamThreads;
-      if (c < n_all) offer(c, held_key[i], f);
-    }
-    for (int c = tid + kHeld * kBeamThreads; c < n_all; c += kBeamThreads)
-      offer(c, __ldcg(keys + c), f);
-  };
-  // score in 64 bits; false: below fp32's range, none
-  auto scored = [&](int w, uint64_t key, Cand* o) {
-    double s = (double)s_cum[w];
-    if (!s_done[w])
-      s += ((double)unordered((uint32_t)(key >> 32)) - (double)s_top[w]) + s_off[w];
-    *o = Cand{ordered(s), key, w};
-    return (float)s != -INFINITY;
-  };
-  auto value = [](uint64_t o) {
-    return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
-  };
+  if (warp == kWarps) {
+    for (int w = lane; w < W; w += 32) g.off[w] = -log(g.sum[w]);
+    asm volatile("bar.arrive 2, %0;" ::"n"(kJoinThreads) : "memory");
+    return;
+  }
+  int got;
+#pragma unroll 1
   for (int pass = 0;; ++pass) {
-    // threshold as in the chunks: what K candidates reach at least
-    uint32_t mine = 0;
-    for_each([&](int, uint64_t, float s, float err) {
-      const float at_least = s - err;
-      if (at_least > -INFINITY) mine = max(mine, ordered(at_least));
-    });
-    const uint32_t bar = warp_qth_largest(mine, (K + kWarps - 1) / kWarps);
-    if (lane == 0) s_bar[warp] = bar;
-    __syncthreads();
-    uint32_t least = ~0u;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) least = min(least, s_bar[w]);
-    // (0: fewer than K anywhere; unordered(0) is a NaN, and everything is taken)
-    float floor_s = unordered(least);
+    // Every candidate's beam, key, fp32 score and bound of its error, if it is one.
+    auto offered = [&](int c, int* w, uint64_t* key, float* s, float* err) {
+      *w = c / per_row;
+      const float cum = g.cum[*w];
+      if (isnan(cum)) return false;
+      if (g.done[*w]) {
+        *key = (uint64_t)(uint32_t)end_key;
+        *s = cum;
+        *err = 0.f;
+        return c == *w * per_row;
+      }
+      *key = c < n_held ? g.held[c] : __ldcg(keys + c);
+      const float d = unordered((uint32_t)(*key >> 32)) - g.top[*w], off = g.off32[*w];
+      *s = cum + (d + off);
+      // (logf and its argument: 2^-23 of the log, and 2^-24)
+      *err = 0x1p-21f * (fabsf(cum) + fabsf(d) + fabsf(off)) + 0x1p-23f;
+      return *key != 0;
+    };
+    // a threshold that K threads' best candidates reach at least, and not many more: the
+    // largest score less 1/4, 1/2, 1, ..., then back half of the last step if that was
+    // too far (beams' scores may lie far apart, so that no warp stands for the others)
+    float mine = -INFINITY;
+#pragma unroll 1
+    for (int c = tid; c < n_all; c += kBeamThreads) {
+      int w;
+      uint64_t key;
+      float s, err;
+      if (offered(c, &w, &key, &s, &err)) mine = fmaxf(mine, s - err);
+    }
+    const uint32_t wmax = __reduce_max_sync(~0u, ordered(mine));
+    if (lane == 0) g.bar[warp] = wmax;
+    main_warps_sync();
+    const float top = unordered(__reduce_max_sync(~0u, g.bar[lane & (kWarps - 1)]));
+    float step = 0.25f, floor_s = top - step;
+    int reach = main_warps_count(mine >= floor_s);
+#pragma unroll 1
+    while (reach < K && floor_s > -INFINITY) {
+      step *= 2.f;
+      floor_s = top - step;
+      reach = main_warps_count(mine >= floor_s);
+    }
+    if (reach > K + K / 2 && main_warps_count(mine >= top - 0.75f * step) >= K)
+      floor_s = top - 0.75f * step;
     floor_s -= 1.25f * (float)kNear + 0x1p-22f * fabsf(floor_s);
-    for_each([&](int w, uint64_t key, float s, float err) {
-      if (s + err < floor_s) return;
-      const int at = atomicAdd(&s_count, 1);
-      if (at < kListCap) list[at] = Cand{0, key, w};
-    });
-    __syncthreads();
-    const int n = s_count;
-    int got = 0;
+#pragma unroll 1
+    for (int c = tid; c < n_all; c += kBeamThreads) {
+      int w;
+      uint64_t key;
+      float s, err;
+      if (!offered(c, &w, &key, &s, &err) || s + err < floor_s) continue;
+      const int at = atomicAdd(&g.count, 1);
+      if (at < kListCap) g.list[at].tie = make_tie(w, key);
+    }
+    if (pass == 0)
+      asm volatile("bar.sync 2, %0;" ::"n"(kJoinThreads) : "memory");  // (the logs)
+    else
+      main_warps_sync();
+    const int n = g.count;
     if (n <= kListCap) {
-      int there = 0;
+#pragma unroll 1
+      for (int i = tid; i < n; i += kBeamThreads)
+        g.list[i].score = score64(g, g.list[i].beam(), g.list[i].logit());
+      main_warps_sync();
+#pragma unroll 1
       for (int i = tid; i < n; i += kBeamThreads) {
-        Cand o;
-        const bool ok = scored(list[i].beam, list[i].key, &o);
-        list[i].score = ok ? o.score : 0;  // (0: below the score of any candidate)
-        there += ok;
-      }
-      there = (int)__reduce_add_sync(~0u, (unsigned)there);
-      if (lane == 0) s_there[warp] = there;
-      __syncthreads();
-      for (int w = 0; w < kWarps; ++w) got += s_there[w];
-      got = min(got, K);
-      for (int i = tid; i < n; i += kBeamThreads) {
-        int rank = 0;
-        const Cand o = list[i];
+        const Cand o = g.list[i];
         if (o.score == 0) continue;
-        for (int j = 0; j < n; ++j) rank += better(list[j], o);
-        if (rank < K) picked[rank] = o;
-      }
-      __syncthreads();
-    } else {
-      // more candidates than the list holds: the best after the last one, K times
-      Cand last{~0ull, ~0ull, -1};
-      for (; got < K; ++got) {
-        Cand best{0, 0, kMaxBeams};
-        for_each([&](int w, uint64_t key, float, float) {
-          Cand o;
-          if (scored(w, key, &o) && better(last, o) && better(o, best)) best = o;
-        });
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-          Cand o;
-          o.score = __shfl_xor_sync(~0u, best.score, d);
-          o.key = __shfl_xor_sync(~0u, best.key, d);
-          o.beam = __shfl_xor_sync(~0u, best.beam, d);
-          if (better(o, best)) best = o;
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += better(g.list[j], o);
+        if (rank < K) {
+          g.picked[rank] = o;
+          atomicAdd(&g.ranked, 1);
         }
-        if (lane == 0) s_best[warp] = best;
-        __syncthreads();
-        for (int w = 0; w < kWarps; ++w)
-          if (better(s_best[w], best)) best = s_best[w];
-        if (best.score == 0) break;  // (the same in every thread)
-        last = best;
-        if (tid == 0) picked[got] = best;
-        __syncthreads();
       }
-      __syncthreads();
+      main_warps_sync();
+      got = g.ranked;
+    } else {
+      got = pick_from_all(g, keys, n_all, per_row, end_key, K, pass == 0);
     }
-    if (pass == 1 || got == 0) {
-      if (tid == 0) s_count = got;
-      break;
-    }
+    if (pass == 1 || got == 0) break;
     // ---- scores of two beams too close for the fp32 sums: next to each other, or
     // one left out next to the last one picked
-    auto near = [&](const Cand& a, const Cand& b) {
-      if (a.beam == b.beam ||
-          value(a.score) - value(b.score) > kNear + 1e-15 * fabs(value(a.score)))
-        return;
-      s_again[a.beam] = s_again[b.beam] = 1;
-      s_near = 1;
-    };
-    for (int i = tid; i + 1 < got; i += kBeamThreads) near(picked[i], picked[i + 1]);
-    if (got == K) {
-      const Cand end = picked[got - 1];
-      if (n <= kListCap) {
-        for (int i = tid; i < n; i += kBeamThreads)
-          if (list[i].score != 0 && better(end, list[i])) near(end, list[i]);
-      } else {
-        for_each([&](int w, uint64_t key, float, float) {
-          Cand o;
-          if (scored(w, key, &o) && better(end, o)) near(end, o);
-        });
-      }
+    if (tid + 1 < got) note_near(g, g.picked[tid], g.picked[tid + 1]);
+    if (n <= kListCap && n > got && got == K) {
+      const Cand end = g.picked[K - 1];
+#pragma unroll 1
+      for (int i = tid; i < n; i += kBeamThreads)
+        if (g.list[i].score != 0 && better(end, g.list[i])) note_near(g, end, g.list[i]);
     }
-    __syncthreads();
-    if (!s_near) {
-      if (tid == 0) s_count = got;
-      break;
-    }
-    if (tid < 64) {
-      const double t = exp2((double)tid / 64);
-      table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
-    }
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    for (int w = 0; w < W; ++w) {
-      if (!s_again[w] || s_done[w]) continue;
-      Sum2 acc;
-      const int64_t at = (row0 + w) * p.a.row_stride;
-      if (p.a.dtype == PA_F32)
-        precise_sum(acc, static_cast<const float*>(p.a.logits) + at, p.a.vocab_size, s_top[w],
-                    table);
-      else if (p.a.dtype == PA_F16)
-        precise_sum(acc, static_cast<const __half*>(p.a.logits) + at, p.a.vocab_size, s_top[w],
-                    table);
-      else
-        precise_sum(acc, static_cast<const __nv_bfloat16*>(p.a.logits) + at, p.a.vocab_size,
-                    s_top[w], table);
-      const double part = warp_sum((double)acc.hi + (double)acc.lo);
-      if (lane == 0) s_part[warp] = part;
-      __syncthreads();
-      if (tid == 0) {
-        double sum = 0.0;
-        for (int i = 0; i < kWarps; ++i) sum += s_part[i];
-        s_off[w] = -log(sum);
-      }
-      __syncthreads();
-    }
+    main_warps_sync();
+    if (!g.near) break;
+    sum_again(g, p.a, row0);
+    if (tid == 0) g.count = g.ranked = 0;
+    main_warps_sync();
   }
-  __syncthreads();
-  const int got = s_count;
   for (int i = tid; i < K; i += kBeamThreads) {
     const int64_t at = (int64_t)blockIdx.x * K + i;
     float score = -INFINITY;
     int parent = -1, token = -1;
     if (i < got) {
-      score = (float)value(picked[i].score);
-      parent = (int)row0 + picked[i].beam;
-      token = (int)~(uint32_t)picked[i].key;
+      const Cand o = g.picked[i];
+      score = (float)value(o.score);
+      parent = (int)row0 + o.beam();
+      token = o.token();
     }
     p.a.scores[at] = score;
     p.a.parents[at] = parent;
@@ -782,7 +868,8 @@ cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStre
   count_launch();
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.num_groups);
-  cfg.blockDim = dim3(kBeamThreads);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = sizeof(Group);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -68,8 +68,7 @@ struct Team {
   // global writes before it are seen after it, by all
   __device__ __forceinline__ void sync() const {
     if (cluster) {
-      __threadfence();
-      cg::this_cluster().sync();
+      cg::this_cluster().sync();  // (a release and an acquire of global writes, too)
     } else {
       cg::this_grid().sync();
     }
@@ -106,115 +105,151 @@ __device__ __forceinline__ bool in_pool(const Pool& p, int id) {
   return id >= 0 && (int64_t)id < p.num_blocks;
 }
 
-// Released entries come in pieces: piece i is entries [col0, col0 + kSeg) of the
-// (i / pieces_per_row)-th row that releases any.  load(k, col, &row, &id): whether the
-// call releases that entry, its row, and the block that it names.
-//
-// claim_released: every released entry of a block out of references proposes itself.
-template <class Load>
-__device__ __forceinline__ void claim_released(const Pool& p, const Team& t, int pieces,
-                                               int pieces_per_row, int width,
-                                               const Load& load) {
-  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
-    const int k = i / pieces_per_row, col0 = i % pieces_per_row * kSeg;
-    int ids[kPer], count[kPer], row = 0;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (!load(k, col0 + e * 32 + t.lane, &row, &ids[e])) ids[e] = -1;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) count[e] = ids[e] >= 0 ? __ldcg(p.extra_refs_out + ids[e]) : 0;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (count[e] >= 0) continue;
-      if (count[e] < -1 && count[e] > kClaim) flag_error(p.err, PA_DEV_ERR_METADATA);
-      atomicMin(p.extra_refs_out + ids[e], INT_MIN + row * width + col0 + e * 32 + t.lane);
-    }
-  }
-}
-// owners among a piece's entries: a mask per 32 entries
-template <class Load>
-__device__ __forceinline__ void owners_of(const Pool& p, const Team& t, int k, int col0,
-                                          int width, const Load& load, unsigned (&mask)[kPer],
-                                          int (&ids)[kPer]) {
-  int count[kPer], row = 0;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    if (!load(k, col0 + e * 32 + t.lane, &row, &ids[e])) ids[e] = -1;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) count[e] = ids[e] >= 0 ? __ldcg(p.extra_refs_out + ids[e]) : 0;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    mask[e] = __ballot_sync(~0u, count[e] == INT_MIN + row * width + col0 + e * 32 + t.lane);
-}
-template <class Load>
-__device__ __forceinline__ void count_owners(const Pool& p, const Team& t, int pieces,
-                                             int pieces_per_row, int width, const Load& load,
-                                             int* counts) {
-  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
-    unsigned mask[kPer];
-    int ids[kPer];
-    owners_of(p, t, i / pieces_per_row, i % pieces_per_row * kSeg, width, load, mask, ids);
-    int n = 0;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) n += __popc(mask[e]);
-    if (t.lane == 0) counts[i] = n;
-  }
-}
-
 struct Scan {  // shared memory of the scans
-  long long warp_sums[32];
-  long long total;
+  int warp_sums[32];
+  int total;
   int starts[kThreads];
 };
 
 // f(piece, sum of the counts before it) for each piece whose count is not 0, by the
-// warp of the team that takes it; the sum of all counts, in every thread.  (Every CTA
-// scans all counts, a round of kThreads at a time.)
+// warp that it belongs to; the sum of all counts, in every thread.
 template <class F>
 __device__ __forceinline__ int64_t in_order(const Team& t, int pieces, const int* counts,
                                             Scan& sh, const F& f) {
   int64_t sum = 0;
+#pragma unroll 1
   for (int first = 0; first < pieces; first += kThreads) {
     const int i = first + t.tid;
     const int n = i < pieces ? __ldcg(counts + i) : 0;
-    const int before = (int)block_scan_excl((long long)n, &sh.total, sh.warp_sums);
+    const int before = block_scan_excl(n, &sh.total, sh.warp_sums);
     sh.starts[t.tid] = n ? before : -1;
     const int64_t round = sh.total;
     __syncthreads();
-    for (int j = t.gwarp; j < kThreads; j += t.gwarps)
-      if (sh.starts[j] >= 0) f(first + j, sum + sh.starts[j]);  // (one j to a warp)
+    const int ahead = first % t.gwarps;
+#pragma unroll 1
+    for (int j = t.gwarp >= ahead ? t.gwarp - ahead : t.gwarp - ahead + t.gwarps; j < kThreads;
+         j += t.gwarps)
+      if (sh.starts[j] >= 0) f(first + j, sum + sh.starts[j]);
     sum += round;
     __syncthreads();  // starts and total are written again
   }
   return sum;
 }
 
-// Pushes the freed blocks from stack position `base` on; how many there are.
-template <class Load>
-__device__ __forceinline__ int64_t push_owners(const Pool& p, const Team& t, int pieces,
-                                               int pieces_per_row, int width,
-                                               const Load& load, const int* counts,
-                                               int64_t base, Scan& sh) {
-  return in_order(t, pieces, counts, sh, [&](int piece, int64_t before) {
-    unsigned mask[kPer];
-    int ids[kPer];
-    owners_of(p, t, piece / pieces_per_row, piece % pieces_per_row * kSeg, width, load, mask,
-              ids);
-    int64_t at = base + before;
+// The entries that a call releases, in pieces: piece i is entries [col0, col0 + kSeg) of
+// the (i / per_row)-th row that releases any.  load(k, col0, ids): the blocks that the
+// released entries among them name, -1 elsewhere (entry e of a lane: column col0 + 32 e +
+// lane); row_of(k): the row.  A piece belongs to the same warp in every pass, which keeps
+// its first piece's blocks and, once known, owners in registers: most calls have no more
+// pieces than warps, and then a pass is one load of the counts.
+template <class Load, class RowOf>
+struct Released {
+  const Pool& p;
+  const Team& t;
+  const int pieces, per_row, width;
+  const Load& load;
+  const RowOf& row_of;
+  int first_ids[kPer];
+  unsigned first_owners[kPer];
+
+  __device__ __forceinline__ Released(const Pool& pool, const Team& team, int n_pieces,
+                                      int pieces_per_row, int table_width, const Load& l,
+                                      const RowOf& r)
+      : p(pool), t(team), pieces(n_pieces), per_row(pieces_per_row), width(table_width),
+        load(l), row_of(r) {
+    if (t.gwarp < pieces) fetch(t.gwarp, first_ids);
+  }
+  __device__ __forceinline__ void fetch(int i, int (&ids)[kPer]) const {
+    load(i / per_row, i % per_row * kSeg, ids);
+  }
+  // the claim of a piece's entry 0 of this lane
+  __device__ __forceinline__ int place(int i) const {
+    return INT_MIN + row_of(i / per_row) * width + i % per_row * kSeg + t.lane;
+  }
+  __device__ __forceinline__ void counts_of(const int (&ids)[kPer], int (&count)[kPer]) const {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (mask[e] >> t.lane & 1) {
-        const int64_t pos = at + __popc(mask[e] & ((1u << t.lane) - 1));
-        if (pos < p.free_capacity)
-          p.free_blocks[pos] = ids[e];
-        else
-          flag_error(p.err, PA_DEV_ERR_METADATA);
-        p.extra_refs_out[ids[e]] = 0;
+    for (int e = 0; e < kPer; ++e)
+      count[e] = ids[e] >= 0 ? __ldcg(p.extra_refs_out + ids[e]) : 0;
+  }
+  // every released entry of a block out of references proposes itself
+  __device__ __forceinline__ void claim() {
+#pragma unroll 1
+    for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+      int ids[kPer], count[kPer];
+      get(i, ids);
+      counts_of(ids, count);
+      const int at = place(i);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (count[e] >= 0) continue;
+        if (count[e] < -1 && count[e] > kClaim) flag_error(p.err, PA_DEV_ERR_METADATA);
+        atomicMin(p.extra_refs_out + ids[e], at + 32 * e);
       }
-      at += __popc(mask[e]);
     }
-  });
-}
+  }
+  // the blocks that each piece owns, into counts
+  __device__ __forceinline__ void count(int* counts) {
+#pragma unroll 1
+    for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+      int ids[kPer], n = 0;
+      unsigned owners[kPer];
+      get(i, ids);
+      owners_of(i, ids, owners);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) n += __popc(owners[e]);
+      if (i == t.gwarp)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) first_owners[e] = owners[e];
+      if (t.lane == 0) counts[i] = n;
+    }
+  }
+  // Pushes them from stack position `base` on; how many there are.  (Every CTA scans all
+  // counts, a round of kThreads at a time.)
+  __device__ __forceinline__ int64_t push(const int* counts, int64_t base, Scan& sh) {
+    return in_order(t, pieces, counts, sh, [&](int i, int64_t before) {
+      int ids[kPer];
+      unsigned owners[kPer];
+      get(i, ids);
+      if (i == t.gwarp) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) owners[e] = first_owners[e];
+      } else {
+        owners_of(i, ids, owners);
+      }
+      int64_t at = base + before;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (owners[e] >> t.lane & 1) {
+          const int64_t pos = at + __popc(owners[e] & ((1u << t.lane) - 1));
+          if (pos < p.free_capacity)
+            p.free_blocks[pos] = ids[e];
+          else
+            flag_error(p.err, PA_DEV_ERR_METADATA);
+          p.extra_refs_out[ids[e]] = 0;
+        }
+        at += __popc(owners[e]);
+      }
+    });
+  }
+
+ private:
+  __device__ __forceinline__ void get(int i, int (&ids)[kPer]) const {
+    if (i == t.gwarp) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) ids[e] = first_ids[e];
+    } else {
+      fetch(i, ids);
+    }
+  }
+  __device__ __forceinline__ void owners_of(int i, const int (&ids)[kPer],
+                                            unsigned (&owners)[kPer]) const {
+    int count[kPer];
+    counts_of(ids, count);
+    const int at = place(i);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) owners[e] = __ballot_sync(~0u, count[e] == at + 32 * e);
+  }
+};
 
 // ---- fork --------------------------------------------------------------------------
 struct ForkK {
@@ -228,7 +263,7 @@ struct ForkK {
   Pool pool;
   int64_t* block_mapping;
   int32_t* num_pairs;
-  int cols;      // table columns of one tile
+  int cols_log2;  // table columns of one tile
   bool cluster;
   // workspace
   int32_t* row_need;  // [rows] partly filled shared last block (its id), -1: none
@@ -239,10 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   extern __shared__ int sh[];
   const int R = p.num_rows;
   int* s_src = sh;            // source of each new row (-1: none)
-  int* s_uses = sh + R;       // new rows of each old row
+  int* s_uses = sh + R;       // new rows of each old row; then each new row's place among
+                              // the copies, -1: none
   int* s_len = sh + 2 * R;    // old rows' lengths
-  int* s_part = sh + 3 * R;   // new rows' partly filled last block, -1: none; then the
-                              // fresh block in its place, -1: none
+  int* s_part = sh + 3 * R;   // new rows' partly filled last block, -1: none; then that to
+                              // be copied; then the fresh block in its place
   int* s_gone = sh + 4 * R;   // old rows nobody takes over, in order
   int* s_tile = sh + 5 * R;   // [rows][cols] of the new tables
   __shared__ Scan scan;
@@ -264,36 +300,33 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   __syncthreads();
   for (int r = t.tid; r < R; r += kThreads)
     if (s_src[r] >= 0) atomicAdd(&s_uses[s_src[r]], 1);
-  if (q.extra_refs != q.extra_refs_out) {
-    copy_refs(q, t);
-    t.sync();
-  } else {
-    __syncthreads();
-  }
-  // ---- references: u - 1 for each block of an old row that u new rows take over
+  __syncthreads();
+  // ---- what needs only the inputs is loaded before the counts are settled: this warp's
+  // first pieces of the old rows' tables and of the released ones, and the new rows'
+  // partly filled last blocks (by every CTA for itself)
   const int segs = (p.width + kSeg - 1) / kSeg;
-  for (int i = t.gwarp; i < R * segs; i += t.gwarps) {
-    const int s = i / segs, col0 = i % segs * kSeg;
-    const int change = s_uses[s] - 1;
+  auto entries = [&](int s, int col0, int (&ids)[kPer]) {
     const int nb = (s_len[s] + kBS - 1) / kBS;
-    if (change == 0 || col0 >= nb) continue;
     const int32_t* row = p.tables + (int64_t)s * p.width;
-    int ids[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int col = col0 + e * 32 + t.lane;
-      ids[e] = col < nb ? __ldg(row + col) : INT_MIN;
+      ids[e] = col < nb ? __ldg(row + col) : -1;
     }
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (in_pool(q, ids[e]))
-        atomicAdd(q.extra_refs_out + ids[e], change);
-      else if (ids[e] != INT_MIN || col0 + e * 32 + t.lane < nb)
-        flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
-    }
+    for (int e = 0; e < kPer; ++e)
+      if (!in_pool(q, ids[e])) {
+        if (col0 + e * 32 + t.lane < nb) flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
+        ids[e] = -1;
+      }
+  };
+  int ids[kPer];
+  int i = t.gwarp;
+  for (; i < R * segs; i += t.gwarps) {
+    if (s_uses[i / segs] == 1) continue;
+    entries(i / segs, i % segs * kSeg, ids);
+    break;
   }
-  // ---- the new rows' partly filled last blocks, and the rows nobody takes over (by
-  // every CTA for itself)
   for (int r = t.tid; r < R; r += kThreads) {
     const int s = s_src[r];
     int id = -1;
@@ -306,33 +339,60 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     }
     s_part[r] = id;
   }
+  // ---- the rows nobody takes over, in order
   int gone = 0;
+#pragma unroll 1
   for (int base = 0; base < R; base += kThreads) {
     const int r = base + t.tid;
     const bool g = r < R && s_uses[r] == 0 && s_len[r] > 0;
-    const int at = (int)block_scan_excl((long long)g, &scan.total, scan.warp_sums);
+    const int at = block_scan_excl((int)g, &scan.total, scan.warp_sums);
     if (g) s_gone[gone + at] = r;
-    gone += (int)scan.total;
+    gone += scan.total;
     __syncthreads();
   }
-  t.sync();
-  auto load = [&](int k, int col, int* row, int* id) {
-    const int s = s_gone[k];
-    *row = s;
-    if (col >= (s_len[s] + kBS - 1) / kBS) return false;
-    *id = __ldg(p.tables + (int64_t)s * p.width + col);
-    return in_pool(q, *id);
+  auto load = [&](int k, int col0, int (&out)[kPer]) {
+    const int s = s_gone[k], nb = (s_len[s] + kBS - 1) / kBS;
+    const int32_t* row = p.tables + (int64_t)s * p.width;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int col = col0 + e * 32 + t.lane;
+      out[e] = col < nb ? __ldg(row + col) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (!in_pool(q, out[e])) out[e] = -1;
   };
-  const int pieces = gone * segs;
-  claim_released(q, t, pieces, segs, p.width, load);
+  auto row_of = [&](int k) { return s_gone[k]; };
+  Released<decltype(load), decltype(row_of)> released(q, t, gone * segs, segs, p.width, load,
+                                                      row_of);
+  if (q.extra_refs != q.extra_refs_out) {
+    copy_refs(q, t);
+    t.sync();
+  }
+  // ---- references: u - 1 for each block of an old row that u new rows take over
+#pragma unroll 1
+  while (i < R * segs) {
+    const int change = s_uses[i / segs] - 1;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (ids[e] >= 0) atomicAdd(q.extra_refs_out + ids[e], change);
+    for (i += t.gwarps; i < R * segs; i += t.gwarps) {
+      if (s_uses[i / segs] == 1) continue;
+      entries(i / segs, i % segs * kSeg, ids);
+      break;
+    }
+  }
+  t.sync();
   // ---- which rows need a copy of their last block: all that hold it but the first,
   // and that one too where others outside hold it (a warp per row)
+#pragma unroll 1
   for (int r = t.gwarp; r < R; r += t.gwarps) {
     const int id = s_part[r];
     int need = -1;
     if (id >= 0) {
       const int extra = __ldcg(q.extra_refs_out + id);
       int holders = 0, before = 0;
+#pragma unroll 1
       for (int o = t.lane; o < R; o += 32)
         if (s_part[o] == id) {
           ++holders;
@@ -344,26 +404,37 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     }
     if (t.lane == 0) p.row_need[r] = need;
   }
-  int64_t freed = 0;
+  released.claim();
   t.sync();
-  if (pieces > 0) {  // (the same in every CTA)
-    count_owners(q, t, pieces, segs, p.width, load, p.counts);
+  // the copies' numbers, while the freed blocks are counted
+  int64_t pairs = 0;
+#pragma unroll 1
+  for (int base = 0; base < R; base += kThreads) {
+    const int r = base + t.tid;
+    const int id = r < R ? __ldcg(p.row_need + r) : -1;
+    const int k = (int)pairs + block_scan_excl((int)(id >= 0), &scan.total, scan.warp_sums);
+    if (r < R) {
+      s_part[r] = id;
+      s_uses[r] = id >= 0 ? k : -1;
+    }
+    pairs += scan.total;
+    __syncthreads();
+  }
+  int64_t freed = 0;
+  if (gone > 0) {  // (the same in every CTA)
+    released.count(p.counts);
     t.sync();
-    freed = push_owners(q, t, pieces, segs, p.width, load, p.counts, height, scan);
+    freed = released.push(p.counts, height, scan);
     t.sync();
   }
   // ---- copies, in row order, onto blocks popped from the stack
   const int64_t top = min(height + freed, q.free_capacity);
-  int64_t pairs = 0;
-  for (int base = 0; base < R; base += kThreads) {
-    const int r = base + t.tid;
-    const int id = r < R ? __ldcg(p.row_need + r) : -1;
-    const int64_t k = pairs + block_scan_excl((long long)(id >= 0), &scan.total,
-                                              scan.warp_sums);
+  for (int r = t.tid; r < R; r += kThreads) {
+    const int id = s_part[r], k = s_uses[r];
     int fresh = -1;
-    if (id >= 0 && k < top) fresh = __ldcg(q.free_blocks + (top - 1 - k));
-    if (r < R) s_part[r] = fresh;
-    if (lead && id >= 0) {
+    if (k >= 0 && k < top) fresh = __ldcg(q.free_blocks + (top - 1 - k));
+    s_part[r] = fresh;
+    if (lead && k >= 0) {
       if (k < top) {
         p.block_mapping[2 * k] = id;
         p.block_mapping[2 * k + 1] = fresh;
@@ -373,9 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
         flag_error(q.err, PA_DEV_ERR_NO_BLOCKS);
       }
     }
-    pairs += scan.total;
-    __syncthreads();
   }
+  __syncthreads();
   pairs = min(pairs, top);
   if (lead) {
     if (t.tid == 0) {
@@ -390,11 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   // ---- the new tables.  A CTA takes some columns of all rows: what it will write is
   // read first, so that the tables may be changed in place whatever rows trade places.
   const bool in_place = p.tables == p.tables_out;
-  const int cols = p.cols, items = R * cols;
+  const int cols = 1 << p.cols_log2, items = R << p.cols_log2;
+#pragma unroll 1
   for (int col0 = t.rank * cols; col0 < p.width; col0 += t.ranks * cols) {
 #pragma unroll 4
     for (int i = t.tid; i < items; i += kThreads) {
-      const int r = i / cols, col = col0 + i % cols, s = s_src[r];
+      const int r = i >> p.cols_log2, col = col0 + (i & (cols - 1)), s = s_src[r];
       if (s < 0) continue;
       const int L = s_len[s], fresh = s_part[r];
       if (col < (L + kBS - 1) / kBS)
@@ -402,8 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
                                                   : p.tables[(int64_t)s * p.width + col];
     }
     __syncthreads();
+#pragma unroll 2
     for (int i = t.tid; i < items; i += kThreads) {
-      const int r = i / cols, col = col0 + i % cols, s = s_src[r];
+      const int r = i >> p.cols_log2, col = col0 + (i & (cols - 1)), s = s_src[r];
       if (s < 0 || col >= (s_len[s] + kBS - 1) / kBS) continue;
       if (in_place && s == r && s_part[r] == -1) continue;
       p.tables_out[(int64_t)r * p.width + col] = s_tile[i];
@@ -468,6 +540,22 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
   if (t.tid == 0) s_popped = 0;
   if (q.extra_refs != q.extra_refs_out) copy_refs(q, t);
   __syncthreads();
+  // a piece of a row's table, and its blocks' further holders before the call
+  const int segs = (p.width + kSeg - 1) / kSeg;
+  const int pieces = R * segs;
+  auto look_up = [&](int i, int (&ids)[kPer], int (&extra)[kPer]) {
+    const int r = i / segs, col0 = i % segs * kSeg, had = (s_len[r] + kBS - 1) / kBS;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int col = col0 + e * 32 + t.lane;
+      ids[e] = s_n[r] >= 0 && col < had ? __ldg(p.tables + (int64_t)r * p.width + col) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      extra[e] = in_pool(q, ids[e]) ? __ldcg(q.extra_refs + ids[e]) : 0;
+  };
+  int first_ids[kPer], first_extra[kPer];  // (this warp's first, loaded ahead)
+  if (t.gwarp < pieces) look_up(t.gwarp, first_ids, first_extra);
   // ---- the lists: ascending positions in [start, L); how many stay in place
   const int lsegs = (min(p.max_keep, p.width * kBS) + kSeg - 1) / kSeg;
   for (int i = t.gwarp; i < R * lsegs; i += t.gwarps) {
@@ -518,29 +606,19 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
   if (lead && bad) flag_error(q.err, bad);
   __syncthreads();
   // ---- blocks that change and have other holders: replaced by fresh ones
-  const int segs = (p.width + kSeg - 1) / kSeg;
-  const int pieces = R * segs;
+#pragma unroll 1
   for (int i = t.gwarp; i < pieces; i += t.gwarps) {
     const int r = i / segs, col0 = i % segs * kSeg;
     const int left = (s_n[r] + kBS - 1) / kBS, first = s_first[r];
     int n = 0;
     if (s_n[r] >= 0 && left > col0 && first < col0 + kSeg) {
-      const int32_t* row = p.tables + (int64_t)r * p.width;
-      int ids[kPer], extra[kPer];
+      if (i != t.gwarp) look_up(i, first_ids, first_extra);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         const int col = col0 + e * 32 + t.lane;
-        ids[e] = col >= first && col < left ? __ldg(row + col) : -1;
-      }
-#pragma unroll
-      for (int e = 0; e < kPer; ++e)
-        extra[e] = in_pool(q, ids[e]) ? __ldcg(q.extra_refs + ids[e]) : 0;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int col = col0 + e * 32 + t.lane;
-        if (col >= first && col < left && !in_pool(q, ids[e]))
-          flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
-        const unsigned mask = __ballot_sync(~0u, extra[e] > 0);
+        const bool changes = col >= first && col < left;
+        if (changes && !in_pool(q, first_ids[e])) flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
+        const unsigned mask = __ballot_sync(~0u, changes && first_extra[e] > 0);
         n += __popc(mask);
         if (t.lane == 0) p.masks[i * kPer + e] = mask;
       }
@@ -551,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
   // ---- pops in row order; the rows whose running need fits the stack run
   for (int64_t sum = 0, base = 0; base < pieces; base += kThreads) {
     const int i = (int)base + t.tid;
-    const long long n = i < pieces ? __ldcg(p.counts + i) : 0;
+    const int n = i < pieces ? __ldcg(p.counts + i) : 0;
     const int64_t before = sum + block_scan_excl(n, &scan.total, scan.warp_sums);
     if (i < pieces && i % segs == segs - 1) s_end[i / segs] = (int)(before + n);
     sum += scan.total;
@@ -624,22 +702,29 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
       if (in_pool(q, ids[e])) atomicAdd(q.extra_refs_out + ids[e], -1);
   }
   t.sync();
-  auto load = [&](int r, int col, int* row, int* id) {
-    *row = r;
-    const int n = s_n[r];
-    if (n < 0 || col < s_first[r] || col >= (s_len[r] + kBS - 1) / kBS) return false;
-    if (col < (n + kBS - 1) / kBS &&
-        (popped == 0 || __ldcg(p.fresh + (int64_t)r * p.width + col) == INT_MIN))
-      return false;
-    *id = __ldg(p.tables + (int64_t)r * p.width + col);
-    return in_pool(q, *id);
+  auto load = [&](int r, int col0, int (&out)[kPer]) {
+    const int had = (s_len[r] + kBS - 1) / kBS, n = s_n[r], left = (n + kBS - 1) / kBS;
+    const int64_t at = (int64_t)r * p.width;
+    // (nothing is replaced: only the blocks past the kept ones)
+    const int from = n < 0 ? had : popped > 0 ? s_first[r] : max(s_first[r], left);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int col = col0 + e * 32 + t.lane;
+      out[e] = col >= from && col < had ? __ldg(p.tables + at + col) : -1;
+      if (col >= from && col < left && __ldcg(p.fresh + at + col) == INT_MIN) out[e] = -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (!in_pool(q, out[e])) out[e] = -1;
   };
-  claim_released(q, t, pieces, segs, p.width, load);
+  auto row_of = [](int r) { return r; };
+  Released<decltype(load), decltype(row_of)> released(q, t, pieces, segs, p.width, load,
+                                                      row_of);
+  released.claim();
   t.sync();
-  count_owners(q, t, pieces, segs, p.width, load, p.counts);
+  released.count(p.counts);
   t.sync();
-  const int64_t freed =
-      push_owners(q, t, pieces, segs, p.width, load, p.counts, height - popped, scan);
+  const int64_t freed = released.push(p.counts, height - popped, scan);
   if (lead && t.tid == 0)
     *q.free_count_out = (int)min(height - popped + freed, q.free_capacity);
   // ---- the moves: of a row that only loses its end none, unless its last block is
@@ -790,10 +875,10 @@ cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, cudaStream_t stre
   const int64_t want = ctas_for(R * p.width, 0, a.rows);
   // columns of a tile: a line of 32, fewer (a sector of 8) where that spreads the
   // columns over more CTAs, and what fits at the largest numbers of rows
-  p.cols = 32;
-  while (p.cols > 8 && (int64_t)p.width <= want * (p.cols / 2)) p.cols /= 2;
-  while (p.cols > 1 && (size_t)(p.cols * R * 4) > kTileBytes) p.cols /= 2;
-  return launch_team(fork_kernel, p, want, (size_t)((5 + p.cols) * R * 4),
+  p.cols_log2 = 5;
+  while (p.cols_log2 > 3 && (int64_t)p.width <= want << (p.cols_log2 - 1)) --p.cols_log2;
+  while (p.cols_log2 > 0 && ((size_t)R * 4) << p.cols_log2 > kTileBytes) --p.cols_log2;
+  return launch_team(fork_kernel, p, want, (size_t)(5 + (1 << p.cols_log2)) * R * 4,
                      (size_t)5 * kMaxForkRows * 4 + kTileBytes, num_sms, stream);
 }
 

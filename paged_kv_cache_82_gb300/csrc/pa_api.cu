@@ -1085,7 +1085,7 @@ pa_status beam_size_status(int num_groups, int beam_width, int vocab_size,
   if (num_groups < 0 || beam_width < 1 || vocab_size < 1 || num_selected < 1)
     return PA_ERR_INVALID_ARG;
   if (beam_width > kMaxBeams || num_selected > kMaxBeamSelected ||
-      vocab_size > (1 << 24) || (int64_t)num_groups * beam_width >= (1 << 24))
+      vocab_size > kMaxVocab || (int64_t)num_groups * beam_width >= (1 << 24))
     return PA_ERR_UNSUPPORTED;
   const BeamPlan plan =
       make_beam_plan(PA_F32, num_groups, beam_width, vocab_size, num_selected);

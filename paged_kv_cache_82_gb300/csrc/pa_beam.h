@@ -9,6 +9,7 @@ namespace pa {
 
 // ---- beam selection (beam_kernels.cu) ---------------------------------------
 constexpr int kMaxBeams = 64;          // beams of one group
+constexpr int kMaxVocab = 1 << 24;
 constexpr int kMaxBeamSelected = 128;  // continuations of one group
 constexpr int kBeamThreads = 256;
 constexpr int kBeamAlign = 8;  // a row may start up to 7 elements into 16 bytes

@@ -63,7 +63,7 @@ BAD_ROWS = [
     (dict(tables_out=None), 1), (dict(seq_lens=None), 1), (dict(lens_out=None), 1),
     (dict(refs=None), 1), (dict(refs_out=None), 1), (dict(free_blocks=None), 1),
     (dict(free_count=None), 1), (dict(free_count_out=None), 1), (dict(workspace=None), 1),
-    (dict(workspace=at(12) + 64), 1), (dict(workspace_bytes=63), 1), (dict(tables=at(1) + 2), 1),
+    (dict(workspace=at(12) + 64), 1), (dict(workspace_bytes=31), 1), (dict(tables=at(1) + 2), 1),
     (dict(refs_out=at(6) + 1), 1), (dict(tables_out=at(1) + 4), 1), (dict(lens_out=at(1)), 1),
     (dict(refs_out=at(5) + 4), 1), (dict(refs_out=at(7)), 1), (dict(free_count_out=at(2)), 1),
     (dict(workspace=at(5)), 1), (dict(free_count=at(7)), 1)]
@@ -142,7 +142,7 @@ def test_workspace_sizes():
     # rows enough for chunks of 8192
     assert pa.pa_beam_select_workspace_size(100, 4, 8185, 4) == 400 * 4 * 8 + 400 * 8
     assert pa.pa_fork_blocks_workspace_size(0, 7) == 0
-    assert pa.pa_fork_blocks_workspace_size(5, 257) == 4 * (4 * 5 + 5 * 2)
+    assert pa.pa_fork_blocks_workspace_size(5, 257) == 4 * (5 + 5 * 2)
     assert pa.pa_compact_blocks_workspace_size(5, 257) >= 4 * 5 * 257
     for f, bad in ((pa.pa_beam_select_workspace_size, (1, 65, 100, 1)),
                    (pa.pa_beam_select_workspace_size, (-1, 1, 100, 1)),
