@@ -500,7 +500,7 @@ __device__ __forceinline__ uint64_t make_tie(int beam, uint64_t key) {
          ((uint32_t)key & ((1 << kTokenBits) - 1));
 }
 __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
-  return a.score > b.score || (a.score == b.score && a.tie > b.tie);
+  return (a.score > b.score) | ((a.score == b.score) & (a.tie > b.tie));
 }
 __device__ __forceinline__ double value(uint64_t o) {
   return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
