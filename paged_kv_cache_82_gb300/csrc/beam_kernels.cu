@@ -32,14 +32,12 @@ namespace {
 constexpr int kWarps = kBeamThreads / 32;
 constexpr int kVecCap = 256;    // 16-byte vectors of a chunk that hold a candidate
 constexpr int kListCap = 1024;  // candidates of a group
-// log2(e) in two parts, the first rounded towards zero so that the second is
-// positive (a product with -inf then keeps its sign)
-constexpr float kLog2eHi = 1.44269502162933349609375f;
-constexpr float kLog2eLo = 1.925963033500789e-8f;
+constexpr float kLog2e = 1.44269502162933349609375f;  // off by less than 2^-25 of itself
+constexpr float kMasked = -1e30f;  // the lowest value of a type, or next to it
 // Two scores' difference from which on the fp32 sums decide.  A row's log-sum is
-// off by at most: 2^-22 (the exponential) + ln 2 x 2^-23 x the mean of |log2 p|
-// over the row, below log2 V <= 24 (the exponent's two roundings) + 18 x 2^-24 (8
-// additions in a thread, 10 above) + 2^-22 (chunks joined) = 3.5e-6.
+// off by at most: 2^-22 (the exponential) + ln 2 x 2^-23 x the mean of |log2 p| over
+// the row, below log2 V <= 24 (the exponent's rounding and log2 e's) + 18 x 2^-24 (8
+// additions in a thread, 10 above) + 2 x 2^-22 (warps and chunks joined) = 3.8e-6.
 constexpr double kNear = 1e-5;
 
 // ---- order of logits ---------------------------------------------------------
@@ -233,8 +231,8 @@ __device__ __noinline__ float odd_sum(const T* x, int base, int V, float mx) {
 #pragma unroll
     for (int j = 0; j < P::kN / 2; ++j) {
       const float2 e = P::pair(v, j);
-      acc[j & 3].x += exp2_approx((clean(e.x) - mx) * kLog2eHi);
-      acc[j & 3].y += exp2_approx((clean(e.y) - mx) * kLog2eHi);
+      acc[j & 3].x += exp2_approx((clean(e.x) - mx) * kLog2e);
+      acc[j & 3].y += exp2_approx((clean(e.y) - mx) * kLog2e);
     }
   }
   return ((acc[0].x + acc[1].x) + (acc[2].x + acc[3].x)) +
@@ -315,18 +313,38 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
   const int q = (K + kWarps - 1) / kWarps;
   const uint32_t wmax = __reduce_max_sync(~0u, om);
   const uint32_t bar = q == 1 ? wmax : warp_qth_largest(om, q);
+  // ---- sum of 2^(x h - c), h = fl32(log2 e), c = fl32(m h) for the warp's maximum m.  x h
+  // - c is (x - m) h, one rounding, and m h - c, which is exact in fp32 and comes off at
+  // the end; h's error counts for x - m only.  (No barrier before it: a warp whose logits
+  // are there goes on.  One whose logits are all masked by a type's lowest value sums 0.)
+  const float wm = unordered(wmax);
+  const float c = wm > kMasked ? wm * kLog2e : 0.f;
+  float2 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+  const float2 h2 = make_float2(kLog2e, kLog2e), c2 = make_float2(-c, -c);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int j = 0; j < kN / 2; ++j) {
+      const float2 e = P::pair(v[i], j);
+      const float2 y = __ffma2_rn(e, h2, c2);
+      acc[j & 3] = __fadd2_rn(acc[j & 3], make_float2(exp2_approx(y.x), exp2_approx(y.y)));
+    }
+  const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+  const float2 a03 = __fadd2_rn(a01, a23);
+  float sum = a03.x + a03.y;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   if (lane == 0) {
     s_max[warp] = wmax;
     s_bar[warp] = bar;
+    s_sum[warp] = sum;
   }
   if (tid == 0) s_count = s_vecs = 0;
   __syncthreads();
-  uint32_t omax = 0, least = ~0u;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    omax = max(omax, s_max[w]);
-    least = min(least, s_bar[w]);
-  }
+  const uint32_t omax = __reduce_max_sync(~0u, s_max[lane & (kWarps - 1)]);
+  const uint32_t least = __reduce_min_sync(~0u, s_bar[lane & (kWarps - 1)]);
   const float mx = unordered(omax);
   const int64_t out = row * p.chunks + chunk;
   if (mx == -INFINITY) {  // nothing here (uniform over the CTA)
@@ -351,41 +369,24 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
         ++at;
       }
   }
-  // ---- sum of 2^(x log2 e - c), c = fl32(mx log2 e): c's rounding is put right
-  // at the end, so every exponent is good to 2^-23 of itself
-  const float c = mx * kLog2eHi;
-  float2 acc[4];
+  // ---- the warps' sums, all relative to the largest maximum
+  {
+    const float w = unordered(s_max[lane & (kWarps - 1)]);
+    const float d = fmaf(w, kLog2e, -(w * kLog2e));
+    sum = w > kMasked ? s_sum[lane & (kWarps - 1)] * exp2f((w - mx) * kLog2e - d) : 0.f;
+  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
-  const float2 hi2 = make_float2(kLog2eHi, kLog2eHi), lo2 = make_float2(kLog2eLo, kLog2eLo),
-               c2 = make_float2(-c, -c);
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-    for (int j = 0; j < kN / 2; ++j) {
-      const float2 e = P::pair(v[i], j);
-      const float2 y = __ffma2_rn(e, lo2, __ffma2_rn(e, hi2, c2));
-      acc[j & 3] = __fadd2_rn(acc[j & 3], make_float2(exp2_approx(y.x), exp2_approx(y.y)));
-    }
-  const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-  const float2 a03 = __fadd2_rn(a01, a23);
-  float sum = a03.x + a03.y;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  if (lane == 0) s_sum[warp] = sum;
+  for (int d = kWarps / 2; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   __syncthreads();
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += s_sum[w];
   const int n_vecs = s_vecs;
   if (n_vecs <= kVecCap)  // the logits among theirs
     for (int e = tid; e < n_vecs * kN; e += kBeamThreads) {
+      const int at = vec_at[e / kN] + e % kN;
       const float f = P::get(reinterpret_cast<const T*>(vecs) + e);
-      if (f >= floor_x)
-        list[atomicAdd(&s_count, 1)] = make_key(fminf(f, FLT_MAX), vec_at[e / kN] + e % kN);
+      if (f >= floor_x) list[atomicAdd(&s_count, 1)] = make_key(fminf(f, FLT_MAX), at);
     }
   // NaN, infinite or huge logits: the exponents above overflowed.  (Uniform.)
-  const bool odd = !(sum >= 0.25f && sum < INFINITY) || fabsf(mx) > 1e30f;
+  const bool odd = !(sum >= 0.5f && sum < INFINITY) || fabsf(mx) > 1e6f;
   if (odd) {
     float t = odd_sum<T, kVecs>(x, base, V, mx);
 #pragma unroll
@@ -393,15 +394,11 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     __syncthreads();
     if (lane == 0) s_sum[warp] = t;
     __syncthreads();
-    sum = 0.f;
+    sum = s_sum[lane & (kWarps - 1)];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_sum[w];
+    for (int d = kWarps / 2; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   }
-  if (tid == 0) {
-    // 2^c against exp(mx): d = mx log2 e - c
-    const float d = odd ? 0.f : fmaf(mx, kLog2eLo, fmaf(mx, kLog2eHi, -c));
-    p.stats[out] = make_float2(mx, sum * exp2f(-d));
-  }
+  if (tid == 0) p.stats[out] = make_float2(mx, sum);
   uint64_t* keys = p.keys + out * K;
   if (n_vecs <= kVecCap) {
     __syncthreads();
@@ -409,6 +406,7 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     for (int i = tid; i < n; i += kBeamThreads) {
       const uint64_t mine = list[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) rank += list[j] > mine;
       if (rank < K) keys[rank] = mine;
     }

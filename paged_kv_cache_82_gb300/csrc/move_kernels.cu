@@ -117,17 +117,6 @@ struct MoveRing {  // a warp's steps in flight
   uint32_t dst[kStages][kTokens < 32 ? 32 : kTokens];  // each token's place
 };
 
-__device__ __forceinline__ void copy_async16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kN>
-__device__ __forceinline__ void async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
-}
-
 // The slices [u, u_end) of a row's heads (a layer's K, then its V, head by head), of
 // 2^kLg lanes each.  Few warps share an SM where there are few heads, so that a step's
 // instructions count: places are 32-bit, and the loops' bounds known.

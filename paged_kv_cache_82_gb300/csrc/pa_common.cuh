@@ -200,6 +200,20 @@ __device__ __forceinline__ T block_scan_excl(T v, T* total, T* warp_sums) {
 }
 
 // ----------------------------------------------------------------------------
+// asynchronous copies of 16 bytes, a thread's own, completing group by group
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kN>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+// ----------------------------------------------------------------------------
 // programmatic dependent launch: let the next grid in the stream start its
 // prologue; wait until the previous grid has completed and its writes are
 // visible
