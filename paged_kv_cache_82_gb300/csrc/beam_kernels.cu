@@ -100,7 +100,7 @@ struct Pack;
 template <>
 struct Pack<float> {
   static constexpr int kN = 4;
-  static constexpr uint32_t kNegInf = 0xff800000u;
+  static constexpr uint32_t kNegInf = 0xff800000u, kNegInfs = kNegInf;
   static constexpr float kLowest = -FLT_MAX;
   static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
   static __device__ __forceinline__ float get(const float* p) { return *p; }
@@ -122,7 +122,7 @@ struct Pack<float> {
 template <>
 struct Pack<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static constexpr uint32_t kNegInf = 0xff80u;
+  static constexpr uint32_t kNegInf = 0xff80u, kNegInfs = 0xff80ff80u;
   static constexpr float kLowest = -0x1.fep127f;
   static __device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) {
     return __bfloat16_as_ushort(*p);
@@ -157,7 +157,7 @@ struct Pack<__nv_bfloat16> {
 template <>
 struct Pack<__half> {
   static constexpr int kN = 8;
-  static constexpr uint32_t kNegInf = 0xfc00u;
+  static constexpr uint32_t kNegInf = 0xfc00u, kNegInfs = 0xfc00fc00u;
   static constexpr float kLowest = -65504.f;
   static __device__ __forceinline__ uint32_t bits(const __half* p) { return __half_as_ushort(*p); }
   static __device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
@@ -302,7 +302,16 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
       v[i] = __ldcs(reinterpret_cast<const uint4*>(x + base + i * kStep));
   } else {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = load_vec<T>(x, base + i * kStep, V);
+    for (int i = 0; i < kVecs; ++i) {
+      const int at = base + i * kStep;
+      v[i] = make_uint4(P::kNegInfs, P::kNegInfs, P::kNegInfs, P::kNegInfs);
+      if (at >= 0 && at + kN <= V) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+    }
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {  // the vector that a row's start or end cuts
+      const int at = base + i * kStep;
+      if ((at < 0 && at + kN > 0) || (at < V && at + kN > V)) v[i] = load_edge<T>(x, at, V);
+    }
   }
   typename P::Max tops(v[0]);
 #pragma unroll
