@@ -91,9 +91,8 @@ __device__ __forceinline__ void copy_refs(const Pool& p, const Team& t) {
   for (int64_t i = first; i < p.num_blocks; i += step) p.extra_refs_out[i] = p.extra_refs[i];
 }
 
-// The stack's height, 0 with a flag where it is not one.
-__device__ __forceinline__ int64_t stack_height(const Pool& p, bool lead) {
-  int64_t n = *p.free_count;
+// The stack's height as it was read, 0 with a flag where it is not one.
+__device__ __forceinline__ int64_t stack_height(const Pool& p, int64_t n, bool lead) {
   if (n < 0 || n > p.free_capacity) {
     if (lead) flag_error(p.err, PA_DEV_ERR_METADATA);
     n = 0;
@@ -139,7 +138,7 @@ __device__ __forceinline__ int64_t in_order(const Team& t, int pieces, const int
 // The entries that a call releases, in pieces: piece i is entries [col0, col0 + kSeg) of
 // the (i / per_row)-th row that releases any.  load(k, col0, ids): the blocks that the
 // released entries among them name, -1 elsewhere (entry e of a lane: column col0 + 32 e +
-// lane); row_of(k): the row.  A piece belongs to the same warp in every pass, which keeps
+// lane; any number in a broken table); row_of(k): the row.  A piece belongs to the same warp in every pass, which keeps
 // its first piece's blocks and, once known, owners in registers: most calls have no more
 // pieces than warps, and then a pass is one load of the counts.
 template <class Load, class RowOf>
@@ -149,7 +148,7 @@ struct Released {
   const int pieces, per_row, width;
   const Load& load;
   const RowOf& row_of;
-  int first_ids[kPer];
+  int first_ids[kPer], first_counts[kPer];
   unsigned first_owners[kPer];
 
   __device__ __forceinline__ Released(const Pool& pool, const Team& team, int n_pieces,
@@ -159,25 +158,16 @@ struct Released {
         load(l), row_of(r) {
     if (t.gwarp < pieces) fetch(t.gwarp, first_ids);
   }
-  __device__ __forceinline__ void fetch(int i, int (&ids)[kPer]) const {
-    load(i / per_row, i % per_row * kSeg, ids);
-  }
-  // the claim of a piece's entry 0 of this lane
-  __device__ __forceinline__ int place(int i) const {
-    return INT_MIN + row_of(i / per_row) * width + i % per_row * kSeg + t.lane;
-  }
-  __device__ __forceinline__ void counts_of(const int (&ids)[kPer], int (&count)[kPer]) const {
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      count[e] = ids[e] >= 0 ? __ldcg(p.extra_refs_out + ids[e]) : 0;
+  // the first piece's counts, loaded ahead of claim() or count()
+  __device__ __forceinline__ void look_ahead() {
+    if (t.gwarp < pieces) counts_of(first_ids, first_counts);
   }
   // every released entry of a block out of references proposes itself
-  __device__ __forceinline__ void claim() {
+  __device__ __forceinline__ void claim() const {
 #pragma unroll 1
     for (int i = t.gwarp; i < pieces; i += t.gwarps) {
       int ids[kPer], count[kPer];
-      get(i, ids);
-      counts_of(ids, count);
+      get(i, ids, count);
       const int at = place(i);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
@@ -191,10 +181,10 @@ struct Released {
   __device__ __forceinline__ void count(int* counts) {
 #pragma unroll 1
     for (int i = t.gwarp; i < pieces; i += t.gwarps) {
-      int ids[kPer], n = 0;
+      int ids[kPer], count[kPer], n = 0;
       unsigned owners[kPer];
-      get(i, ids);
-      owners_of(i, ids, owners);
+      get(i, ids, count);
+      owners_of(i, count, owners);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) n += __popc(owners[e]);
       if (i == t.gwarp)
@@ -205,16 +195,19 @@ struct Released {
   }
   // Pushes them from stack position `base` on; how many there are.  (Every CTA scans all
   // counts, a round of kThreads at a time.)
-  __device__ __forceinline__ int64_t push(const int* counts, int64_t base, Scan& sh) {
+  __device__ __forceinline__ int64_t push(const int* counts, int64_t base, Scan& sh) const {
     return in_order(t, pieces, counts, sh, [&](int i, int64_t before) {
-      int ids[kPer];
+      int ids[kPer], count[kPer];
       unsigned owners[kPer];
-      get(i, ids);
       if (i == t.gwarp) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) owners[e] = first_owners[e];
+        for (int e = 0; e < kPer; ++e) {
+          ids[e] = first_ids[e];
+          owners[e] = first_owners[e];
+        }
       } else {
-        owners_of(i, ids, owners);
+        get(i, ids, count);
+        owners_of(i, count, owners);
       }
       int64_t at = base + before;
 #pragma unroll
@@ -233,18 +226,32 @@ struct Released {
   }
 
  private:
-  __device__ __forceinline__ void get(int i, int (&ids)[kPer]) const {
+  __device__ __forceinline__ void fetch(int i, int (&ids)[kPer]) const {
+    load(i / per_row, i % per_row * kSeg, ids);
+  }
+  // the claim of a piece's entry 0 of this lane
+  __device__ __forceinline__ int place(int i) const {
+    return INT_MIN + row_of(i / per_row) * width + i % per_row * kSeg + t.lane;
+  }
+  __device__ __forceinline__ void counts_of(const int (&ids)[kPer], int (&count)[kPer]) const {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      count[e] = in_pool(p, ids[e]) ? __ldcg(p.extra_refs_out + ids[e]) : 0;
+  }
+  __device__ __forceinline__ void get(int i, int (&ids)[kPer], int (&count)[kPer]) const {
     if (i == t.gwarp) {
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) ids[e] = first_ids[e];
+      for (int e = 0; e < kPer; ++e) {
+        ids[e] = first_ids[e];
+        count[e] = first_counts[e];
+      }
     } else {
       fetch(i, ids);
+      counts_of(ids, count);
     }
   }
-  __device__ __forceinline__ void owners_of(int i, const int (&ids)[kPer],
+  __device__ __forceinline__ void owners_of(int i, const int (&count)[kPer],
                                             unsigned (&owners)[kPer]) const {
-    int count[kPer];
-    counts_of(ids, count);
     const int at = place(i);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) owners[e] = __ballot_sync(~0u, count[e] == at + 32 * e);
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   const Team t(p.cluster);
   const bool lead = t.rank == 0;
   const Pool& q = p.pool;
-  const int64_t height = stack_height(q, lead && t.tid == 0);
+  const int counted = *q.free_count;
   unsigned bad = 0;
   for (int r = t.tid; r < R; r += kThreads) {
     const int s = __ldg(p.sources + r);
@@ -301,9 +308,20 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   for (int r = t.tid; r < R; r += kThreads)
     if (s_src[r] >= 0) atomicAdd(&s_uses[s_src[r]], 1);
   __syncthreads();
-  // ---- what needs only the inputs is loaded before the counts are settled: this warp's
-  // first pieces of the old rows' tables and of the released ones, and the new rows'
-  // partly filled last blocks (by every CTA for itself)
+  // ---- the rows nobody takes over, in order
+  int gone = 0;
+#pragma unroll 1
+  for (int base = 0; base < R; base += kThreads) {
+    const int r = base + t.tid;
+    const bool g = r < R && s_uses[r] == 0 && s_len[r] > 0;
+    const int at = block_scan_excl((int)g, &scan.total, scan.warp_sums);
+    if (g) s_gone[gone + at] = r;
+    gone += scan.total;
+    __syncthreads();
+  }
+  // ---- what needs only the inputs is loaded before the counts are settled, all of it
+  // before any of it is looked at: this warp's first pieces of the old rows' tables and of
+  // the released ones, and the new rows' partly filled last blocks (by every CTA for itself)
   const int segs = (p.width + kSeg - 1) / kSeg;
   auto entries = [&](int s, int col0, int (&ids)[kPer]) {
     const int nb = (s_len[s] + kBS - 1) / kBS;
@@ -313,12 +331,6 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
       const int col = col0 + e * 32 + t.lane;
       ids[e] = col < nb ? __ldg(row + col) : -1;
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (!in_pool(q, ids[e])) {
-        if (col0 + e * 32 + t.lane < nb) flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
-        ids[e] = -1;
-      }
   };
   int ids[kPer];
   int i = t.gwarp;
@@ -327,6 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     entries(i / segs, i % segs * kSeg, ids);
     break;
   }
+  auto load = [&](int k, int col0, int (&out)[kPer]) { entries(s_gone[k], col0, out); };
+  auto row_of = [&](int k) { return s_gone[k]; };
+  Released<decltype(load), decltype(row_of)> released(q, t, gone * segs, segs, p.width, load,
+                                                      row_of);
+#pragma unroll 1
   for (int r = t.tid; r < R; r += kThreads) {
     const int s = s_src[r];
     int id = -1;
@@ -339,32 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     }
     s_part[r] = id;
   }
-  // ---- the rows nobody takes over, in order
-  int gone = 0;
-#pragma unroll 1
-  for (int base = 0; base < R; base += kThreads) {
-    const int r = base + t.tid;
-    const bool g = r < R && s_uses[r] == 0 && s_len[r] > 0;
-    const int at = block_scan_excl((int)g, &scan.total, scan.warp_sums);
-    if (g) s_gone[gone + at] = r;
-    gone += scan.total;
-    __syncthreads();
-  }
-  auto load = [&](int k, int col0, int (&out)[kPer]) {
-    const int s = s_gone[k], nb = (s_len[s] + kBS - 1) / kBS;
-    const int32_t* row = p.tables + (int64_t)s * p.width;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int col = col0 + e * 32 + t.lane;
-      out[e] = col < nb ? __ldg(row + col) : -1;
-    }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (!in_pool(q, out[e])) out[e] = -1;
-  };
-  auto row_of = [&](int k) { return s_gone[k]; };
-  Released<decltype(load), decltype(row_of)> released(q, t, gone * segs, segs, p.width, load,
-                                                      row_of);
   if (q.extra_refs != q.extra_refs_out) {
     copy_refs(q, t);
     t.sync();
@@ -372,10 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   // ---- references: u - 1 for each block of an old row that u new rows take over
 #pragma unroll 1
   while (i < R * segs) {
-    const int change = s_uses[i / segs] - 1;
+    const int change = s_uses[i / segs] - 1, nb = (s_len[i / segs] + kBS - 1) / kBS;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (ids[e] >= 0) atomicAdd(q.extra_refs_out + ids[e], change);
+    for (int e = 0; e < kPer; ++e) {
+      if (in_pool(q, ids[e]))
+        atomicAdd(q.extra_refs_out + ids[e], change);
+      else if (i % segs * kSeg + e * 32 + t.lane < nb)
+        flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
+    }
     for (i += t.gwarps; i < R * segs; i += t.gwarps) {
       if (s_uses[i / segs] == 1) continue;
       entries(i / segs, i % segs * kSeg, ids);
@@ -383,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     }
   }
   t.sync();
+  released.look_ahead();
   // ---- which rows need a copy of their last block: all that hold it but the first,
   // and that one too where others outside hold it (a warp per row)
 #pragma unroll 1
@@ -406,7 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   }
   released.claim();
   t.sync();
-  // the copies' numbers, while the freed blocks are counted
+  const int64_t height = stack_height(q, counted, lead && t.tid == 0);
+  released.look_ahead();
+  // ---- the copies' numbers, while the freed blocks are counted
   int64_t pairs = 0;
 #pragma unroll 1
   for (int base = 0; base < R; base += kThreads) {
@@ -420,13 +418,26 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     pairs += scan.total;
     __syncthreads();
   }
+  // ---- the new tables.  A CTA takes some columns of all rows: what it will write is
+  // read first, so that the tables may be changed in place whatever rows trade places.
+  // (The first columns now: nobody writes to the tables before the last barrier.)
+  const int cols = 1 << p.cols_log2, items = R << p.cols_log2;
+  auto read_tile = [&](int col0) {
+#pragma unroll 8
+    for (int i = t.tid; i < items; i += kThreads) {
+      const int r = i >> p.cols_log2, col = col0 + (i & (cols - 1)), s = s_src[r];
+      if (s >= 0 && col < (s_len[s] + kBS - 1) / kBS)
+        s_tile[i] = p.tables[(int64_t)s * p.width + col];
+    }
+  };
+  if (t.rank * cols < p.width) read_tile(t.rank * cols);
   int64_t freed = 0;
   if (gone > 0) {  // (the same in every CTA)
     released.count(p.counts);
     t.sync();
     freed = released.push(p.counts, height, scan);
-    t.sync();
   }
+  t.sync();
   // ---- copies, in row order, onto blocks popped from the stack
   const int64_t top = min(height + freed, q.free_capacity);
   for (int r = t.tid; r < R; r += kThreads) {
@@ -457,30 +468,23 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     for (int r = t.tid; r < R; r += kThreads)
       p.seq_lens_out[r] = s_src[r] >= 0 ? s_len[s_src[r]] : 0;
   }
-  // ---- the new tables.  A CTA takes some columns of all rows: what it will write is
-  // read first, so that the tables may be changed in place whatever rows trade places.
   const bool in_place = p.tables == p.tables_out;
-  const int cols = 1 << p.cols_log2, items = R << p.cols_log2;
 #pragma unroll 1
   for (int col0 = t.rank * cols; col0 < p.width; col0 += t.ranks * cols) {
-#pragma unroll 4
-    for (int i = t.tid; i < items; i += kThreads) {
-      const int r = i >> p.cols_log2, col = col0 + (i & (cols - 1)), s = s_src[r];
-      if (s < 0) continue;
-      const int L = s_len[s], fresh = s_part[r];
-      if (col < (L + kBS - 1) / kBS)
-        s_tile[i] = fresh != -1 && col == L / kBS ? fresh
-                                                  : p.tables[(int64_t)s * p.width + col];
+    if (col0 != t.rank * cols) {
+      __syncthreads();
+      read_tile(col0);
+      __syncthreads();
     }
-    __syncthreads();
 #pragma unroll 2
     for (int i = t.tid; i < items; i += kThreads) {
       const int r = i >> p.cols_log2, col = col0 + (i & (cols - 1)), s = s_src[r];
       if (s < 0 || col >= (s_len[s] + kBS - 1) / kBS) continue;
-      if (in_place && s == r && s_part[r] == -1) continue;
-      p.tables_out[(int64_t)r * p.width + col] = s_tile[i];
+      const int fresh = s_part[r];
+      if (in_place && s == r && fresh == -1) continue;
+      p.tables_out[(int64_t)r * p.width + col] =
+          fresh != -1 && col == s_len[s] / kBS ? fresh : s_tile[i];
     }
-    __syncthreads();
   }
 }
 
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
   const Team t(p.cluster);
   const bool lead = t.rank == 0;
   const Pool& q = p.pool;
-  const int64_t height = stack_height(q, lead && t.tid == 0);
+  const int counted = *q.free_count;
   unsigned bad = 0;
   for (int r = t.tid; r < R; r += kThreads) {
     const int64_t L = p.seq_lens[r];
@@ -635,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
     sum += scan.total;
     __syncthreads();
   }
+  const int64_t height = stack_height(q, counted, lead && t.tid == 0);
   bad = 0;
   for (int r = t.tid; r < R && pieces > 0; r += kThreads) {
     if (s_end[r] > height) {
@@ -713,25 +718,17 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
       out[e] = col >= from && col < had ? __ldg(p.tables + at + col) : -1;
       if (col >= from && col < left && __ldcg(p.fresh + at + col) == INT_MIN) out[e] = -1;
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (!in_pool(q, out[e])) out[e] = -1;
   };
   auto row_of = [](int r) { return r; };
   Released<decltype(load), decltype(row_of)> released(q, t, pieces, segs, p.width, load,
                                                       row_of);
-  released.claim();
-  t.sync();
-  released.count(p.counts);
-  t.sync();
-  const int64_t freed = released.push(p.counts, height - popped, scan);
-  if (lead && t.tid == 0)
-    *q.free_count_out = (int)min(height - popped + freed, q.free_capacity);
+  released.look_ahead();
   // ---- the moves: of a row that only loses its end none, unless its last block is
-  // replaced
+  // replaced.  (From the last warp on: the first ones have the released pieces.)
   const int64_t wide = (int64_t)p.max_keep + kBS;
   const int msegs = (int)((wide + kSeg - 1) / kSeg);
-  for (int64_t i = t.gwarp; i < (int64_t)R * msegs; i += t.gwarps) {
+#pragma unroll 1
+  for (int64_t i = t.gwarps - 1 - t.gwarp; i < (int64_t)R * msegs; i += t.gwarps) {
     const int r = (int)(i / msegs), j0 = (int)(i % msegs) * kSeg;
     const int n = s_n[r], at0 = s_first[r] * kBS, start = s_start[r];
     const int32_t* list = p.keep + (int64_t)r * p.max_keep;
@@ -775,26 +772,44 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
       p.dst_slots[r * wide + j] = ok ? (int64_t)to[e] * kBS + (at0 + j) % kBS : -1;
     }
   }
-  // ---- the tables: in place, only what is replaced, once nobody reads the old ones
+  released.claim();
+  // ---- the tables: out of place, whole
   const bool in_place = p.tables == p.tables_out;
-  if (in_place) {
-    if (popped == 0) return;  // (the same in every CTA)
-    t.sync();
-  }
-  for (int i = t.gwarp; i < pieces; i += t.gwarps) {
-    const int r = i / segs, col0 = i % segs * kSeg;
-    const int n = s_n[r], blocks = ((n >= 0 ? n : s_len[r]) + kBS - 1) / kBS;
+  auto write_tables = [&]() {
+#pragma unroll 1
+    for (int i = t.gwarps - 1 - t.gwarp; i < pieces; i += t.gwarps) {
+      const int r = i / segs, col0 = i % segs * kSeg;
+      const int n = s_n[r], blocks = ((n >= 0 ? n : s_len[r]) + kBS - 1) / kBS;
+      const int64_t at = (int64_t)r * p.width;
+      int now[kPer], was[kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int col = col0 + e * 32 + t.lane;
-      if (col >= blocks) break;
-      const int64_t at = (int64_t)r * p.width + col;
-      const int now = popped > 0 && n >= 0 && col >= s_first[r] ? __ldcg(p.fresh + at) : INT_MIN;
-      if (now != INT_MIN)
-        p.tables_out[at] = now;
-      else if (!in_place)
-        p.tables_out[at] = __ldg(p.tables + at);
+      for (int e = 0; e < kPer; ++e) {
+        const int col = col0 + e * 32 + t.lane;
+        const bool on = col < blocks;
+        now[e] = on && popped > 0 && n >= 0 && col >= s_first[r] ? __ldcg(p.fresh + at + col)
+                                                                 : INT_MIN;
+        was[e] = on && !in_place ? __ldg(p.tables + at + col) : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int col = col0 + e * 32 + t.lane;
+        if (col < blocks && (now[e] != INT_MIN || !in_place))
+          p.tables_out[at + col] = now[e] != INT_MIN ? now[e] : was[e];
+      }
     }
+  };
+  if (!in_place) write_tables();
+  t.sync();
+  released.look_ahead();
+  released.count(p.counts);
+  t.sync();
+  const int64_t freed = released.push(p.counts, height - popped, scan);
+  if (lead && t.tid == 0)
+    *q.free_count_out = (int)min(height - popped + freed, q.free_capacity);
+  // ---- and in place what is replaced, once nobody reads the old ones
+  if (in_place && popped > 0) {  // (the same in every CTA)
+    t.sync();
+    write_tables();
   }
 }
 
