@@ -20,18 +20,22 @@
 // resolve (kNear), the sums of those rows are taken again with exponentials in
 // two fp32 parts and the group is picked again (about one group in 2000 of
 // unlike beams, always for beams that are copies of each other).
+#include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
 
 #include "pa_beam.h"
 #include "pa_common.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace pa {
 namespace {
 
 constexpr int kWarps = kBeamThreads / 32;
-constexpr int kVecCap = 256;    // 16-byte vectors of a chunk that hold a candidate
-constexpr int kListCap = 1024;  // candidates of a group
+constexpr int kVecCap = 512;    // 16-byte vectors of a chunk that hold a candidate
+constexpr int kListCap = 1024;  // candidates of a chunk, and of a group
+constexpr int kMaxJoinCtas = 4;
 constexpr float kLog2e = 1.44269502162933349609375f;  // off by less than 2^-25 of itself
 constexpr float kMasked = -1e30f;  // the lowest value of a type, or next to it
 // Two scores' difference from which on the fp32 sums decide.  A row's log-sum is
@@ -214,6 +218,7 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int i0, int n) {
 struct BeamK {
   BeamArgs a;
   int chunks;
+  unsigned stride;  // through a group's candidates
   uint64_t* keys;  // [rows][chunks][K], best first
   float2* stats;   // [rows][chunks]: maximum, sum of exp(x - maximum)
 };
@@ -239,18 +244,75 @@ __device__ __noinline__ float odd_sum(const T* x, int base, int V, float mx) {
          ((acc[0].y + acc[1].y) + (acc[2].y + acc[3].y));
 }
 
-// More vectors than there is room for hold a candidate (long runs of equal logits): the
-// best key below the last one taken, K times.
+// The K best of a list of n: each counts the better ones, up to K.
+__device__ __forceinline__ void rank_list(const uint64_t* list, int n, int K, uint64_t* keys) {
+  for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+    const uint64_t mine = list[i];
+    int rank = 0;
+    for (int j = 0; j < n && rank < K; j += 4)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rank += j + k < n && list[j + k] > mine;
+    if (rank < K) keys[rank] = mine;
+  }
+  for (int i = n + threadIdx.x; i < K; i += kBeamThreads) keys[i] = 0;
+}
+
+// More logits than there is room for reach the threshold: those of a chunk of equal ones
+// (masked by a type's lowest value, say), as a rule.  The logits above it to the list, and
+// then of the equal ones the first; where even the former are too many (the warps' logits
+// must lie far apart), the best key below the last one taken, K times.
 template <typename T, int kVecs>
-__device__ __noinline__ void pick_one_by_one(const T* x, int base, int V, int K,
-                                             uint64_t* s_best, uint64_t* keys) {
+__device__ __noinline__ void pick_from_many(const T* x, int base, int V, int K, float floor_x,
+                                            uint64_t* list, int* s_count, int* warp_sums,
+                                            uint64_t* s_best, uint64_t* keys) {
   using P = Pack<T>;
+  constexpr int kStep = kBeamThreads * P::kN;
+  __syncthreads();
+  if (threadIdx.x == 0) *s_count = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < kVecs; ++i) {
+    const int at = base + i * kStep;
+    const uint4 v = load_vec<T>(x, at, V);
+#pragma unroll
+    for (int j = 0; j < P::kN; ++j) {
+      const float e = P::get(v, j);
+      if (e > floor_x) {
+        const int n = atomicAdd(s_count, 1);
+        if (n < kListCap) list[n] = make_key(fminf(e, FLT_MAX), at + j);
+      }
+    }
+  }
+  __syncthreads();
+  int n = *s_count;
+  if (n <= kListCap) {
+#pragma unroll 1
+    for (int i = 0; i < kVecs && n < K; ++i) {
+      const int at = base + i * kStep;
+      const uint4 v = load_vec<T>(x, at, V);
+      int equal = 0, total;
+#pragma unroll
+      for (int j = 0; j < P::kN; ++j) equal += P::get(v, j) == floor_x;
+      int place = n + block_scan_excl(equal, warp_sums + kWarps, warp_sums);
+      total = warp_sums[kWarps];
+#pragma unroll
+      for (int j = 0; j < P::kN; ++j)
+        if (P::get(v, j) == floor_x) {
+          if (place < K) list[place] = make_key(fminf(floor_x, FLT_MAX), at + j);
+          ++place;
+        }
+      n = min(n + total, max(n, K));
+      __syncthreads();  // the scan's memory is written again; the list is complete
+    }
+    rank_list(list, n, K, keys);
+    return;
+  }
   uint64_t last = ~0ull;
   for (int k = 0; k < K; ++k) {
     uint64_t best = 0;
 #pragma unroll 1
     for (int i = 0; i < kVecs; ++i) {
-      const int at = base + i * kBeamThreads * P::kN;
+      const int at = base + i * kStep;
       const uint4 v = load_vec<T>(x, at, V);
 #pragma unroll
       for (int j = 0; j < P::kN; ++j) {
@@ -279,11 +341,11 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
   constexpr int kN = P::kN, kStep = kBeamThreads * kN;
   __shared__ uint4 vecs[kVecCap];
   __shared__ int vec_at[kVecCap];
-  __shared__ uint64_t list[kVecCap * kN];
+  __shared__ uint64_t list[kListCap];
   __shared__ uint32_t s_max[kWarps], s_bar[kWarps];
   __shared__ float s_sum[kWarps];
   __shared__ uint64_t s_best[kWarps];
-  __shared__ int s_count, s_vecs;
+  __shared__ int s_count, s_vecs, s_scan[kWarps + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / (unsigned)p.chunks;
   const int chunk = (int)(blockIdx.x - row * p.chunks);
@@ -392,7 +454,10 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     for (int e = tid; e < n_vecs * kN; e += kBeamThreads) {
       const int at = vec_at[e / kN] + e % kN;
       const float f = P::get(reinterpret_cast<const T*>(vecs) + e);
-      if (f >= floor_x) list[atomicAdd(&s_count, 1)] = make_key(fminf(f, FLT_MAX), at);
+      if (f >= floor_x) {
+        const int n = atomicAdd(&s_count, 1);
+        if (n < kListCap) list[n] = make_key(fminf(f, FLT_MAX), at);
+      }
     }
   // NaN, infinite or huge logits: the exponents above overflowed.  (Uniform.)
   const bool odd = !(sum >= 0.5f && sum < INFINITY) || fabsf(mx) > 1e6f;
@@ -409,20 +474,12 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
   }
   if (tid == 0) p.stats[out] = make_float2(mx, sum);
   uint64_t* keys = p.keys + out * K;
-  if (n_vecs <= kVecCap) {
-    __syncthreads();
-    const int n = s_count;
-    for (int i = tid; i < n; i += kBeamThreads) {
-      const uint64_t mine = list[i];
-      int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) rank += list[j] > mine;
-      if (rank < K) keys[rank] = mine;
-    }
-    for (int i = n + tid; i < K; i += kBeamThreads) keys[i] = 0;
-    return;
-  }
-  pick_one_by_one<T, kVecs>(x, base, V, K, s_best, keys);
+  __syncthreads();
+  const int n = n_vecs <= kVecCap ? s_count : kListCap + 1;
+  if (n <= kListCap)
+    rank_list(list, n, K, keys);
+  else
+    pick_from_many<T, kVecs>(x, base, V, K, floor_x, list, &s_count, s_scan, s_best, keys);
 }
 
 // ---- sums again, in two fp32 parts ---------------------------------------------
@@ -466,19 +523,40 @@ __device__ __forceinline__ void add_exp(Sum2& acc, float x, float mx, const floa
   acc.add(s * scale, s_lo * scale);
 }
 
+// A thread's part of a row: vectors first, first + step, ..., four at a time with the next
+// four on their way.  (Words one after another in a loop: few instructions to fetch for
+// code that is rarely run.)
 template <typename T>
 __device__ __noinline__ double precise_sum(const void* logits, int64_t at, int V, float mx,
-                                           const float2* table) {
+                                           const float2* table, int first, int step) {
   using P = Pack<T>;
   const T* x = static_cast<const T*>(logits) + at;
-  Sum2 acc;
-  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  for (int i = threadIdx.x * P::kN - off; i < V; i += kBeamThreads * P::kN) {
-    const uint4 v = load_vec<T>(x, i, V);
+  const uint4 none = make_uint4(P::kNegInfs, P::kNegInfs, P::kNegInfs, P::kNegInfs);
+  Sum2 acc[2];
+  int i = first * P::kN - (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  const int hop = step * P::kN;
+  uint4 next[4];
 #pragma unroll
-    for (int j = 0; j < P::kN; ++j) add_exp(acc, clean(P::get(v, j)), mx, table);
+  for (int u = 0; u < 4; ++u) next[u] = i + u * hop < V ? load_vec<T>(x, i + u * hop, V) : none;
+#pragma unroll 1
+  while (i < V) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = next[u];
+    i += 4 * hop;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) next[u] = i + u * hop < V ? load_vec<T>(x, i + u * hop, V) : none;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int j = 0; j < P::kN / 4; ++j)
+          add_exp(acc[j & 1], clean(P::get(v[u], j)), mx, table);
+        v[u] = make_uint4(v[u].y, v[u].z, v[u].w, v[u].x);
+      }
   }
-  return (double)acc.hi + (double)acc.lo;
+  return ((double)acc[0].hi + (double)acc[1].hi) + ((double)acc[0].lo + (double)acc[1].lo);
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -517,10 +595,10 @@ __device__ __forceinline__ double value(uint64_t o) {
 struct Group {
   Cand list[kListCap];  // candidates that may be among the K best
   Cand picked[kMaxBeamSelected];
-  Cand best[kWarps];
   double sum[kMaxBeams];    // of exp(x - top)
   double off[kMaxBeams];    // -log of it
-  double part[kWarps];
+  double part[kMaxBeams][kWarps];       // sums taken again: this CTA's warps'
+  double parts[kMaxJoinCtas][kMaxBeams];  // and, in the first CTA, all CTAs'
   uint64_t held[kListCap];  // the first candidates' keys
   float2 table[64];
   float off32[kMaxBeams];   // -logf of it
@@ -531,6 +609,8 @@ struct Group {
   uint32_t bar[kWarps];
   int count, near, ranked;
 };
+
+static_assert(sizeof(Group) <= 47 * 1024, "a group in the default shared memory");
 
 // A candidate's score in 64 bits (0: below fp32's range, none)
 __device__ __forceinline__ uint64_t score64(const Group& g, int w, float logit) {
@@ -565,79 +645,104 @@ __device__ __forceinline__ int main_warps_count(bool p) {
 
 // The rare ways, out of the way of the usual ones' instructions.
 //
-// More candidates than the list holds: the best after the last one, K times; the
-// number picked.  near: notes the candidates close to the last one picked.
-__device__ __noinline__ int pick_from_all(Group& g, const uint64_t* keys, int n_all,
-                                          int per_row, int end_key, int K, bool look_near) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto candidate = [&](int c, Cand* o) {
+// f(score, tie) for this thread's share of all candidates.
+template <class F>
+__device__ __forceinline__ void for_all_scored(const Group& g, const uint64_t* keys, int n_all,
+                                               int per_row, int end_key, const F& f) {
+#pragma unroll 1
+  for (int c = threadIdx.x; c < n_all; c += kBeamThreads) {
     const int w = c / per_row;
-    if (isnan(g.cum[w])) return false;
-    if (g.done[w] && c != w * per_row) return false;
+    if (isnan(g.cum[w]) || (g.done[w] && c != w * per_row)) continue;
     const uint64_t key = g.done[w] ? (uint64_t)(uint32_t)end_key : __ldcg(keys + c);
-    if (key == 0) return false;
-    *o = Cand{score64(g, w, unordered((uint32_t)(key >> 32))), make_tie(w, key)};
-    return o->score != 0;
-  };
-  Cand last{~0ull, ~0ull};
-  int got = 0;
-  for (; got < K; ++got) {
-    Cand best{0, 0};
-    for (int c = threadIdx.x; c < n_all; c += kBeamThreads) {
-      Cand o;
-      if (candidate(c, &o) && better(last, o) && better(o, best)) best = o;
-    }
-    for (int d = 16; d; d >>= 1) {
-      Cand o;
-      o.score = __shfl_xor_sync(~0u, best.score, d);
-      o.tie = __shfl_xor_sync(~0u, best.tie, d);
-      if (better(o, best)) best = o;
-    }
-    if (lane == 0) g.best[warp] = best;
-    main_warps_sync();
-    for (int w = 0; w < kWarps; ++w)
-      if (better(g.best[w], best)) best = g.best[w];
-    if (best.score == 0) break;  // (the same in every thread)
-    last = best;
-    if (threadIdx.x == 0) g.picked[got] = best;
-    main_warps_sync();
+    if (key == 0) continue;
+    const Cand o{score64(g, w, unordered((uint32_t)(key >> 32))), make_tie(w, key)};
+    if (o.score != 0) f(o);
   }
+}
+// how many of all candidates are at or above (score, tie), in every thread
+__device__ __forceinline__ int count_from(Group& g, const uint64_t* keys, int n_all,
+                                          int per_row, int end_key, const Cand& from) {
+  int n = 0;
+  for_all_scored(g, keys, n_all, per_row, end_key,
+                 [&](const Cand& o) { n += !better(from, o); });
+  n = (int)__reduce_add_sync(~0u, (unsigned)n);
   main_warps_sync();
-  if (look_near && got == K)
-    for (int c = threadIdx.x; c < n_all; c += kBeamThreads) {
-      Cand o;
-      if (candidate(c, &o) && better(last, o)) note_near(g, last, o);
+  if ((threadIdx.x & 31) == 0) g.bar[threadIdx.x >> 5] = (uint32_t)n;
+  main_warps_sync();
+  return (int)__reduce_add_sync(~0u, (threadIdx.x & 31) < kWarps ? g.bar[threadIdx.x & 31] : 0);
+}
+// More candidates than the list holds reach the threshold (many equal scores): the list
+// from the candidate on which, by halving first the scores' range and then the ties', has
+// at least K of them behind it and not many more.  Returns the list's length.
+__device__ __noinline__ int list_from_all(Group& g, const uint64_t* keys, int n_all,
+                                          int per_row, int end_key, int K) {
+  const int most = min(kListCap, 3 * K + 64);
+  Cand from{1, 0};  // every candidate is above
+  int n = count_from(g, keys, n_all, per_row, end_key, from);
+#pragma unroll 1
+  for (int word = 0; word < 2; ++word) {  // of (score, tie)
+    uint64_t lo = word ? from.tie : from.score, hi = ~0ull;
+#pragma unroll 1
+    for (int i = 0; i < 64 && n > most && hi - lo > 1; ++i) {
+      const uint64_t mid = lo + (hi - lo) / 2;
+      const Cand at = word ? Cand{from.score, mid} : Cand{mid, 0};
+      const int reach = count_from(g, keys, n_all, per_row, end_key, at);
+      if (reach >= K) {
+        lo = mid;
+        n = reach;
+      } else {
+        hi = mid;
+      }
     }
-  return got;
+    (word ? from.tie : from.score) = lo;
+  }
+  if (threadIdx.x == 0) g.count = 0;
+  main_warps_sync();
+  for_all_scored(g, keys, n_all, per_row, end_key, [&](const Cand& o) {
+    if (better(from, o)) return;
+    const int at = atomicAdd(&g.count, 1);
+    if (at < kListCap) g.list[at] = o;
+  });
+  main_warps_sync();
+  return min(g.count, kListCap);
+}
+// and, once they are picked, the candidates left out that are close to the last pick
+__device__ __noinline__ void note_near_from_all(Group& g, const uint64_t* keys, int n_all,
+                                                int per_row, int end_key, const Cand& end) {
+  for_all_scored(g, keys, n_all, per_row, end_key, [&](const Cand& o) {
+    if (better(end, o)) note_near(g, end, o);
+  });
 }
 
-// The sums of the rows noted, in two fp32 parts.
-__device__ __noinline__ void sum_again(Group& g, const BeamArgs& a, int64_t row0) {
+// The sums of the rows noted, in two fp32 parts: CTA `rank` of `ranks` takes its share of
+// every row, to `parts` of the first CTA.
+__device__ __noinline__ void sum_again(Group& g, const BeamArgs& a, int64_t row0, int rank,
+                                       int ranks, double* parts) {
   const int tid = threadIdx.x;
   if (tid < 64) {
     const double t = exp2((double)tid / 64);
     g.table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
   }
   main_warps_sync();
+  const int first = rank * kBeamThreads + tid, step = ranks * kBeamThreads;
   for (int w = 0; w < a.beam_width; ++w) {
     if (!g.again[w] || g.done[w]) continue;
     const int64_t at = (row0 + w) * a.row_stride;
-    double part = a.dtype == PA_F32
-                      ? precise_sum<float>(a.logits, at, a.vocab_size, g.top[w], g.table)
-                  : a.dtype == PA_F16
-                      ? precise_sum<__half>(a.logits, at, a.vocab_size, g.top[w], g.table)
-                      : precise_sum<__nv_bfloat16>(a.logits, at, a.vocab_size, g.top[w],
-                                                   g.table);
+    double part =
+        a.dtype == PA_F32
+            ? precise_sum<float>(a.logits, at, a.vocab_size, g.top[w], g.table, first, step)
+        : a.dtype == PA_F16
+            ? precise_sum<__half>(a.logits, at, a.vocab_size, g.top[w], g.table, first, step)
+            : precise_sum<__nv_bfloat16>(a.logits, at, a.vocab_size, g.top[w], g.table, first,
+                                         step);
     part = warp_sum(part);
-    if ((tid & 31) == 0) g.part[tid >> 5] = part;
-    main_warps_sync();
-    if (tid == 0) {
-      double sum = 0.0;
-      for (int i = 0; i < kWarps; ++i) sum += g.part[i];
-      g.off[w] = -log(sum);
-      g.off32[w] = (float)g.off[w];
-    }
-    main_warps_sync();
+    if ((tid & 31) == 0) g.part[w][tid >> 5] = part;
+  }
+  main_warps_sync();
+  if (tid < a.beam_width && g.again[tid] && !g.done[tid]) {
+    double sum = 0.0;
+    for (int i = 0; i < kWarps; ++i) sum += g.part[tid][i];
+    parts[rank * kMaxBeams + tid] = sum;
   }
 }
 
@@ -651,13 +756,48 @@ __device__ __noinline__ void sum_again(Group& g, const BeamArgs& a, int64_t row0
 //
 // A ninth warp takes the logs in 64 bits (a long chain of FP64 operations) while the
 // others sort out by fp32 ones.
+// Where there are few groups, a cluster of CTAs takes each, all but the first only to
+// help with the sums that have to be taken again (64 groups of 4 beams that are copies of
+// each other, 128256 bf16 logits: 106 us with four CTAs to a group, 179 with two).
 constexpr int kJoinThreads = kBeamThreads + 32;
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamK p) {
   extern __shared__ __align__(16) char shared[];
   Group& g = *reinterpret_cast<Group*>(shared);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = p.a.beam_width, K = p.a.num_selected, S = p.chunks;
-  const int64_t row0 = (int64_t)blockIdx.x * W;
+  cg::cluster_group team = cg::this_cluster();
+  const int rank = (int)team.block_rank(), ranks = (int)team.num_blocks();
+  const int64_t group = blockIdx.x / (unsigned)ranks;
+  const int64_t row0 = group * W;
+  // Barriers of the cluster: 0, all CTAs run; 1, the first one has told the others whether
+  // sums have to be taken again, into their memory; 2, they have been.
+  if (ranks > 1) team.barrier_arrive();
+  if (rank != 0) {
+    if (warp == kWarps) return;
+    team.barrier_wait();
+    team.sync();
+    if (g.near) {
+      sum_again(g, p.a, row0, rank, ranks, &team.map_shared_rank(&g, 0)->parts[0][0]);
+      team.sync();
+    }
+    return;
+  }
+  auto tell = [&](bool near) {
+    if (ranks == 1) return;
+    team.barrier_wait();
+    for (int i = tid; i < (ranks - 1) * W; i += kBeamThreads) {
+      Group& o = *team.map_shared_rank(&g, 1 + i / W);
+      const int w = i % W;
+      if (w == 0) o.near = near;
+      if (near) {
+        o.again[w] = g.again[w];
+        o.done[w] = g.done[w];
+        o.top[w] = g.top[w];
+      }
+    }
+    team.barrier_arrive();
+    if (near) team.barrier_wait();
+  };
   if (tid < W) {
     const float cum = p.a.beam_scores[row0 + tid];
     g.cum[tid] = isfinite(cum) ? cum : NAN;
@@ -668,6 +808,12 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamK p) {
   const int per_row = S * K, n_all = W * per_row, n_held = min(n_all, kListCap);
   const uint64_t* keys = p.keys + row0 * per_row;
   const int end_key = ~p.a.end_token;
+  // A thread's candidates: the i-th is stride x i modulo an odd number that is prime to
+  // the stride, i = tid, tid + 256, ...  Each has some of many pieces and ranks, so that
+  // the best ones are in many threads.
+  const unsigned modulus = (unsigned)n_all | 1;
+  const unsigned c_first = (unsigned)((uint64_t)tid * p.stride % modulus);
+  const unsigned c_step = (unsigned)((uint64_t)kBeamThreads * p.stride % modulus);
   __syncthreads();
   pdl_wait();
   // (a finished row's keys are not written, and not used)
@@ -717,6 +863,15 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamK p) {
   int got;
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
+    auto for_mine = [&](auto&& f) {
+      unsigned c = c_first;
+#pragma unroll 1
+      for (unsigned i = tid; i < modulus; i += kBeamThreads) {
+        if (c < (unsigned)n_all) f((int)c);
+        c += c_step;
+        if (c >= modulus) c -= modulus;
+      }
+    };
     // Every candidate's beam, key, fp32 score and bound of its error, if it is one.
     auto offered = [&](int c, int* w, uint64_t* key, float* s, float* err) {
       *w = c / per_row;
@@ -736,16 +891,15 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamK p) {
       return *key != 0;
     };
     // a threshold that K threads' best candidates reach at least, and not many more: the
-    // largest score less 1/4, 1/2, 1, ..., then back half of the last step if that was
+    // largest score less 1/4, 1/2, 1, ..., then back some of the last step if that was
     // too far (beams' scores may lie far apart, so that no warp stands for the others)
     float mine = -INFINITY;
-#pragma unroll 1
-    for (int c = tid; c < n_all; c += kBeamThreads) {
+    for_mine([&](int c) {
       int w;
       uint64_t key;
       float s, err;
       if (offered(c, &w, &key, &s, &err)) mine = fmaxf(mine, s - err);
-    }
+    });
     const uint32_t wmax = __reduce_max_sync(~0u, ordered(mine));
     if (lane == 0) g.bar[warp] = wmax;
     main_warps_sync();
@@ -753,68 +907,90 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamK p) {
     float step = 0.25f, floor_s = top - step;
     int reach = main_warps_count(mine >= floor_s);
 #pragma unroll 1
-    while (reach < K && floor_s > -INFINITY) {
+    for (int i = 0; i < 140 && reach < K; ++i) {  // (2^130 is the largest step in fp32)
       step *= 2.f;
       floor_s = top - step;
       reach = main_warps_count(mine >= floor_s);
     }
-    if (reach > K + K / 2 && main_warps_count(mine >= top - 0.75f * step) >= K)
-      floor_s = top - 0.75f * step;
-    floor_s -= 1.25f * (float)kNear + 0x1p-22f * fabsf(floor_s);
+    float back = step * 0.25f;
 #pragma unroll 1
-    for (int c = tid; c < n_all; c += kBeamThreads) {
+    for (int i = 0; i < 6 && reach > K + K / 2; ++i, back *= 0.5f) {
+      const int n = main_warps_count(mine >= floor_s + back);
+      if (n < K) continue;
+      floor_s += back;
+      reach = n;
+    }
+    floor_s -= 1.25f * (float)kNear + 0x1p-22f * fabsf(floor_s);
+    for_mine([&](int c) {
       int w;
       uint64_t key;
       float s, err;
-      if (!offered(c, &w, &key, &s, &err) || s + err < floor_s) continue;
+      if (!offered(c, &w, &key, &s, &err) || s + err < floor_s) return;
       const int at = atomicAdd(&g.count, 1);
       if (at < kListCap) g.list[at].tie = make_tie(w, key);
-    }
+    });
     if (pass == 0)
       asm volatile("bar.sync 2, %0;" ::"n"(kJoinThreads) : "memory");  // (the logs)
     else
       main_warps_sync();
-    const int n = g.count;
-    if (n <= kListCap) {
+    int n = g.count;
+    const bool all_listed = n <= kListCap;
+    if (all_listed) {
 #pragma unroll 1
       for (int i = tid; i < n; i += kBeamThreads)
         g.list[i].score = score64(g, g.list[i].beam(), g.list[i].logit());
       main_warps_sync();
-#pragma unroll 1
-      for (int i = tid; i < n; i += kBeamThreads) {
-        const Cand o = g.list[i];
-        if (o.score == 0) continue;
-        int rank = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) rank += better(g.list[j], o);
-        if (rank < K) {
-          g.picked[rank] = o;
-          atomicAdd(&g.ranked, 1);
-        }
-      }
-      main_warps_sync();
-      got = g.ranked;
     } else {
-      got = pick_from_all(g, keys, n_all, per_row, end_key, K, pass == 0);
+      n = list_from_all(g, keys, n_all, per_row, end_key, K);
     }
+#pragma unroll 1
+    for (int i = tid; i < n; i += kBeamThreads) {
+      const Cand o = g.list[i];
+      if (o.score == 0) continue;
+      int rank = 0;
+      for (int j = 0; j < n && rank < K; j += 4)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rank += j + k < n && better(g.list[j + k], o);
+      if (rank < K) {
+        g.picked[rank] = o;
+        atomicAdd(&g.ranked, 1);
+      }
+    }
+    main_warps_sync();
+    got = g.ranked;
     if (pass == 1 || got == 0) break;
     // ---- scores of two beams too close for the fp32 sums: next to each other, or
     // one left out next to the last one picked
     if (tid + 1 < got) note_near(g, g.picked[tid], g.picked[tid + 1]);
-    if (n <= kListCap && n > got && got == K) {
+    if (got == K) {
       const Cand end = g.picked[K - 1];
+      if (!all_listed)
+        note_near_from_all(g, keys, n_all, per_row, end_key, end);
+      else
 #pragma unroll 1
-      for (int i = tid; i < n; i += kBeamThreads)
-        if (g.list[i].score != 0 && better(end, g.list[i])) note_near(g, end, g.list[i]);
+        for (int i = tid; i < n; i += kBeamThreads)
+          if (g.list[i].score != 0 && better(end, g.list[i])) note_near(g, end, g.list[i]);
     }
     main_warps_sync();
     if (!g.near) break;
-    sum_again(g, p.a, row0);
+    tell(true);
+    sum_again(g, p.a, row0, 0, ranks, &g.parts[0][0]);
+    if (ranks > 1)
+      team.sync();
+    else
+      main_warps_sync();
+    if (tid < W && g.again[tid] && !g.done[tid]) {
+      double sum = 0.0;
+      for (int r = 0; r < ranks; ++r) sum += g.parts[r][tid];
+      g.off[tid] = -log(sum);
+      g.off32[tid] = (float)g.off[tid];
+    }
     if (tid == 0) g.count = g.ranked = 0;
     main_warps_sync();
   }
+  if (!g.near) tell(false);
   for (int i = tid; i < K; i += kBeamThreads) {
-    const int64_t at = (int64_t)blockIdx.x * K + i;
+    const int64_t at = group * K + i;
     float score = -INFINITY;
     int parent = -1, token = -1;
     if (i < got) {
@@ -864,7 +1040,9 @@ BeamPlan make_beam_plan(pa_dtype dtype, int num_groups, int beam_width, int voca
 }
 
 cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStream_t stream) {
-  BeamK p{a, plan.chunks, static_cast<uint64_t*>(a.workspace),
+  const int64_t candidates = (int64_t)a.beam_width * plan.chunks * a.num_selected;
+  const unsigned stride = (candidates | 1) % 1000003 ? 1000003u : 1000033u;  // (primes)
+  BeamK p{a, plan.chunks, stride, static_cast<uint64_t*>(a.workspace),
           reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + plan.off_stats)};
   const unsigned grid = (unsigned)((int64_t)a.num_groups * a.beam_width * plan.chunks);
   cudaError_t e = a.dtype == PA_F32   ? launch_chunks<float>(p, plan.per_thread, grid, stream)
@@ -873,16 +1051,25 @@ cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStre
                                                                      stream);
   if (e != cudaSuccess) return e;
   count_launch();
+  // CTAs to a group: one to 16K logits of a row, while all groups' fit the SMs twice (a
+  // cluster costs half a microsecond to launch and tell that there is nothing to do)
+  unsigned ctas = 1;
+  while (ctas < kMaxJoinCtas && (int64_t)a.num_groups * ctas * 2 <= 2 * 152 &&
+         (int64_t)ctas * 2 * 16384 <= a.vocab_size)
+    ctas *= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.num_groups);
+  cfg.gridDim = dim3((unsigned)a.num_groups * ctas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = sizeof(Group);
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, beam_join_kernel, p);
   if (e == cudaSuccess) count_launch();
   return e;

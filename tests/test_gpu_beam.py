@@ -128,6 +128,59 @@ def test_scores_closer_than_fp32_sums_resolve(dtype):
             _check(x, c, 5)
 
 
+@pytest.mark.parametrize("V", [40001, 140003])
+def test_close_scores_of_long_rows(V):
+    """The same where several CTAs share the sums that are taken again; of several
+    groups, some need it."""
+    rng = np.random.default_rng(V)
+    x = _logits(rng, 12, V, "f32")
+    d = x.double().numpy()
+    m = d.max(1)
+    logp = -np.log(np.exp(d - m[:, None]).sum(1))
+    cum = np.zeros((4, 3), np.float32)
+    for g in range(4):
+        cum[g] = (logp[3 * g] - logp[3 * g:3 * g + 3]).astype(np.float32)
+    cum[1] = [-1.0, -2.5, -7.0]
+    for step in (-1, 0, 1):
+        c = cum.copy()
+        c[::2, 1] = np.nextafter(c[::2, 1], np.float32(step * 1e9)) if step else c[::2, 1]
+        _check(x, c, 1)
+        _check(x, c, 6)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_sorted_logits_and_the_largest_lists(dtype):
+    """A vocabulary in the order of its logits (one warp has all the largest), and as
+    many continuations as there may be."""
+    rng = np.random.default_rng(12)
+    x = torch.sort(_logits(rng, 8, 50000, dtype).float(), 1, descending=True)[0].to(DT[dtype])
+    _check(x, _scores(rng, 2, 4), 8)
+    _check(x.flip(1).contiguous(), _scores(rng, 2, 4), 128)
+    x = _logits(rng, 96, 9000, dtype)
+    _check(x, _scores(rng, 24, 4), 128)
+    _check(x, _scores(rng, 3, 32) * 0.01, 128)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_few_tokens_left_by_masks(dtype):
+    """Constrained decoding: a few tokens allowed, the others at -inf or at the type's
+    lowest value; fewer and more of them than continuations."""
+    rng = np.random.default_rng(13)
+    for V, rows in ((9000, 8), (20000, 60)):
+        for left in (1, 3, 300):
+            for mask in (float("-inf"), torch.finfo(DT[dtype]).min):
+                x = _logits(rng, rows, V, dtype)
+                allowed = torch.zeros(V, dtype=torch.bool)
+                allowed[torch.from_numpy(rng.choice(V, left, replace=False))] = True
+                x[:, ~allowed] = mask
+                if mask != float("-inf") and left < 8:
+                    # (masked tokens' scores differ by less than a 64-bit number of their
+                    # size resolves: one beam, so that only tokens decide)
+                    _check(x, _scores(rng, rows, 1), 8)
+                else:
+                    _check(x, _scores(rng, rows // 4, 4), 8)
+
+
 @pytest.mark.parametrize("dtype", sorted(DT))
 def test_masked_infinite_and_nan_logits(dtype):
     rng = np.random.default_rng(4)

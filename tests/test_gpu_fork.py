@@ -106,6 +106,57 @@ def test_beams(in_place, groups, width, hi):
     assert want["flags"] <= {"blocks"}
 
 
+@pytest.mark.parametrize("groups,width,hi", [(8, 4, 300), (150, 8, 3000)])
+def test_captured_calls_on_two_streams(groups, width, hi):
+    """A graph of a fork and one of a compaction, each on buffers of its own, replayed at
+    the same time: one cluster, and a grid of every SM."""
+    rng = np.random.default_rng(groups)
+    c = _tree(rng, groups, width, hi, 9, spare=groups * width * hi // 16)
+    R = groups * width
+    src = np.sort(rng.integers(0, width, (groups, width)), 1) + np.arange(groups)[:, None] * width
+    d = _tree(rng, groups, 1, hi, 40, spare=groups * hi // 16)
+    keep, ks, start = _lists(rng, d, 0.3)
+    fork_in = [_i32(c[k]) for k in ("table", "lens", "refs", "stack")] + [_i32([c["count"]])]
+    comp_in = [_i32(d[k]) for k in ("table", "lens", "refs", "stack")] + [_i32([d["count"]])]
+    sources, kd, kl, st = _i32(src.reshape(-1)), _i32(keep), _i32(ks), _i32(start)
+
+    def outs(t):
+        return dict(block_tables_out=t[0].clone(), seq_lens_out=t[1].clone(),
+                    extra_refs_out=t[2].clone(), free_count_out=t[4].clone())
+
+    fo, co = outs(fork_in), outs(comp_in)
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for which in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if which == 0:
+                got.append(pa.pa_fork_blocks(sources, *fork_in, **fo))
+            else:
+                got.append(pa.pa_compact_blocks(kd, kl, *comp_in, keep_start=st, **co))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    want = ref.fork(src.reshape(-1), c["table"], c["lens"], c["refs"], c["stack"], c["count"])
+    np.testing.assert_array_equal(fo["block_tables_out"].cpu().numpy(), want["table"])
+    np.testing.assert_array_equal(fo["extra_refs_out"].cpu().numpy(), want["refs"])
+    np.testing.assert_array_equal(got[0][0].cpu().numpy(), want["pairs"])
+    assert int(fo["free_count_out"]) == want["count"] and R == len(want["seq_lens"])
+    moves = got[1][2].cpu().numpy()
+    want = ref.compact(keep, ks, start, d["table"], d["lens"], d["refs"], d["stack"], d["count"],
+                       got[1][0].cpu().numpy(), got[1][1].cpu().numpy())
+    np.testing.assert_array_equal(moves, want["moves"])
+    np.testing.assert_array_equal(got[1][0].cpu().numpy(), want["src"])
+    np.testing.assert_array_equal(got[1][1].cpu().numpy(), want["dst"])
+    np.testing.assert_array_equal(co["extra_refs_out"].cpu().numpy(), want["refs"])
+    assert int(co["free_count_out"]) == want["count"]
+
+
 def test_a_step_of_beams_needs_no_spare_block():
     """With no free block at all, the copies go into what the step gives back."""
     rng = np.random.default_rng(3)
