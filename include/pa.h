@@ -657,13 +657,16 @@ pa_status pa_get_device_error(pa_stream_t stream, uint32_t* flags);
  *   pa_compact_blocks      tokens dropped from rows
  *   pa_move_tokens         the moves that close the gaps, in all layers
  *
- * extra_refs : int32 [num_blocks], a block's holders beyond the first: 0 for a block
- * in one row's table (as pa_build_step hands them out) and for a free one.  Holders
- * are the entries of block tables and whatever else keeps a block (a prefix cache).
+ * extra_refs : int32 [num_blocks], a block's holders beyond the first, 0 or more: 0 for
+ * a block in one row's table (as pa_build_step hands them out) and for a free one.
+ * Holders are the entries of block tables and whatever else keeps a block (a prefix
+ * cache).
  *
  * A beam step: pa_beam_select with num_selected = beam_width, whose `parents` are
  * the `sources` of pa_fork_blocks, pa_copy_blocks_layers with the pairs that leaves,
- * then pa_build_step for the new tokens.
+ * then pa_build_step for the new tokens.  None of it needs the host, so the loop can be
+ * captured into a CUDA graph.  Calls that may run at the same time need workspaces of
+ * their own.  All results are bitwise deterministic from run to run.
  */
 
 /*
@@ -697,7 +700,8 @@ pa_status pa_get_device_error(pa_stream_t stream, uint32_t* flags);
  * finished_out : device uint8 [num_groups][K], or NULL: 1 where the token is
  *                end_token, else 0; may be finished if K = W.
  * workspace    : device, pa_beam_select_workspace_size bytes, 256-byte aligned.
- * W <= 64, K <= 128, vocab_size <= 2^24 (else PA_ERR_UNSUPPORTED).
+ * W <= 64, K <= 128, vocab_size <= 2^24, num_groups * W < 2^24 (else
+ * PA_ERR_UNSUPPORTED).
  */
 pa_status pa_beam_select(const void* logits, pa_dtype logits_dtype, int num_groups,
                          int beam_width, int vocab_size, int64_t row_stride,
@@ -734,8 +738,9 @@ pa_status pa_beam_select_workspace_size(int num_groups, int beam_width, int voca
  *                    PA_DEV_ERR_METADATA and counts as r.
  * block_tables     : device int32 [num_rows][max_blocks_per_seq]; _out: the same
  *                    shape, may be block_tables.  Entries past a row's blocks are
- *                    left as they were.  An id outside [0, num_blocks) sets
- *                    PA_DEV_ERR_BLOCK_ID and counts for nothing.
+ *                    left as they were.  An id outside [0, num_blocks) counts for
+ *                    nothing and, where its count would change, sets
+ *                    PA_DEV_ERR_BLOCK_ID.
  * seq_lens, _out   : device int32 [num_rows]; tokens in the cache (one out of range:
  *                    PA_DEV_ERR_METADATA, counts as 0).
  * extra_refs, _out : above; a count that falls below -1 sets PA_DEV_ERR_METADATA.
@@ -770,7 +775,7 @@ pa_status pa_fork_blocks_workspace_size(int num_rows, int max_blocks_per_seq,
  * block_mapping    : device int64 [max_pairs][2], as pa_copy_blocks.
  * num_pairs        : device int32, pairs that there are (outside [0, max_pairs]:
  *                    PA_DEV_ERR_METADATA, clamped); NULL: max_pairs.
- * Of a block's bounds (pa_summarise_blocks), see there.
+ * A layer's bounds records (pa_summarise_blocks) are not copied: see there.
  */
 pa_status pa_copy_blocks_layers(void* k_cache, void* v_cache, pa_dtype cache_dtype,
                                 int num_layers, int64_t k_layer_stride,
@@ -839,6 +844,8 @@ pa_status pa_compact_blocks_workspace_size(int num_rows, int max_blocks_per_seq,
  * src_slots, dst_slots : device int64 [num_rows][max_moves].
  * num_moves            : device int32 [num_rows] (outside [0, max_moves]:
  *                        PA_DEV_ERR_METADATA, the row is not moved).
+ * max_moves < 2^30, a layer's K or V below 2^37 bytes, num_layers * num_kv_heads <=
+ * 2^24 and, times num_rows, <= 2^28 (else PA_ERR_UNSUPPORTED).
  */
 pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype cache_dtype,
                          int num_layers, int64_t k_layer_stride, int64_t v_layer_stride,

@@ -1276,7 +1276,9 @@ pa_status pa_move_tokens(void* k_cache, void* v_cache, pa_dtype cache_dtype,
   // (a warp to each slice of a head's tokens, 17 slices at most; places of 32 bytes in a
   // layer's cache are counted in 32 bits)
   if (max_moves >= (1ll << 30) ||
-      num_blocks * num_kv_heads * page_bytes(cache_dtype, head_dim) >= 32ll * UINT32_MAX || (int64_t)num_layers * num_kv_heads > (1 << 24) ||
+      num_blocks * num_kv_heads * page_bytes(cache_dtype, head_dim) >=
+          32ll * UINT32_MAX ||
+      (int64_t)num_layers * num_kv_heads > (1 << 24) ||
       (int64_t)num_rows * num_layers * num_kv_heads > (1ll << 28))
     return PA_ERR_UNSUPPORTED;
   if (!src_slots || !dst_slots || !num_moves || !aligned(src_slots, 8) ||

@@ -39,12 +39,12 @@ def beam_select(logits, beam_scores, K, finished=None, end_token=-1):
 
 def _free(refs, released, stack, count, flags):
     """Pushes the blocks of the released entries whose count fell below 0."""
-    pushed = []
+    pushed = {}  # (in order)
     for b in released:
         if refs[b] < 0 and b not in pushed:
             if refs[b] < -1:
                 flags.add("metadata")
-            pushed.append(b)
+            pushed[b] = True
     for b in pushed:
         refs[b] = 0
         if count < len(stack):

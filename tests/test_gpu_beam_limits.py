@@ -1,0 +1,136 @@
+"""The largest sizes of the calls for several hypotheses, and calls on other streams."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_82_gb300 as pa
+from tests import _beam_ref as ref
+from tests.test_gpu_beam import DT, _check, _logits, _scores
+from tests.test_gpu_fork import _compact, _fork, _i32, _lists, _tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,B,W,V,K", [
+    ("f16", 1, 1, 1 << 24, 128), ("bf16", 1, 3, (1 << 24) - 1, 5), ("f32", 1, 64, 200001, 128),
+    ("bf16", 2, 64, 128256, 128), ("f32", 3, 5, 128256, 128), ("f16", 1000, 1, 700, 2),
+    ("bf16", 4000, 2, 33, 8)])
+def test_largest_selections(dtype, B, W, V, K):
+    rng = np.random.default_rng(V % 1000 + K)
+    _check(_logits(rng, B * W, V, dtype), _scores(rng, B, W), K)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_equal_logits_of_many_beams(dtype):
+    """Every score of a group is equal but for the beam's: more candidates at the last
+    pick's score than any list holds."""
+    x = torch.zeros(64, 70001).to(DT[dtype])
+    scores = np.zeros((1, 64), np.float32)
+    _check(x, scores, 128)
+    scores[0, 40] = 1.0
+    _check(x, scores, 100)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_one_row_of_a_million_blocks(in_place):
+    rng = np.random.default_rng(1)
+    c = _tree(rng, 1, 2, 0, 0)
+    n = 1 << 20
+    c["table"] = np.full((2, n + 3), -7, np.int32)
+    ids = rng.permutation(n + 9).astype(np.int32)
+    c["table"][0, :n] = ids[:n]
+    c["table"][1, :2] = ids[:2]
+    c["lens"] = np.array([16 * n - 5, 32], np.int32)
+    c["refs"] = np.zeros(n + 9, np.int32)
+    c["refs"][ids[:2]] = 1
+    c["stack"] = np.full(n + 9, -5, np.int32)
+    c["stack"][:9] = ids[n:]
+    c["count"] = 9
+    assert not _fork(c, [0, 0], in_place)["flags"]
+    assert not _fork(c, [1, -1], in_place)["flags"]      # a million blocks onto the stack
+    keep = np.sort(rng.choice(16 * n - 5, 200_000, replace=False)).astype(np.int32)[None]
+    keep = np.repeat(keep, 2, 0)
+    want = _compact(c, keep, np.array([200_000, -1], np.int32), in_place=in_place)
+    assert not want["flags"]
+
+
+def test_caches_and_layers_beyond_32_bits():
+    """Two layers of 5 GB each in K, and in V: places past 2^32 bytes in a layer, and a
+    second layer past 2^32."""
+    L, NB, H, D = 2, 160_000, 8, 128
+    k = torch.empty(L, NB, H, 16, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    assert k[0].numel() * 2 > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    near = [0, 1, 2, 131_071, 131_072, 131_073, NB - 2, NB - 1]
+    for t in (k, v):
+        t[:, near] = torch.randn(L, len(near), H, 16, D, device="cuda", generator=g).bfloat16()
+    k0, v0 = k[:, near].clone(), v[:, near].clone()
+    pairs = torch.tensor([[NB - 1, 1], [0, NB - 2], [131_072, 131_071]], device="cuda")
+    pa.pa_copy_blocks_layers(k, v, pairs)
+    src = torch.tensor([[16 * (NB - 1) + 15, 16 * 131_073 + 7],
+                        [16 * 131_072 + 4, 2 * 16 + 1]], device="cuda")
+    dst = torch.tensor([[16 * 131_073 + 1, 16 * 131_073 + 2],
+                        [5, 16 * (NB - 1) + 3]], device="cuda")
+    pa.pa_move_tokens(k, v, src, dst, torch.tensor([2, 2], dtype=torch.int32, device="cuda"))
+    assert pa.pa_get_device_error() == 0
+    for t, t0 in ((k, k0), (v, v0)):
+        want = t0.clone()
+        want[:, 1], want[:, 6], want[:, 3] = t0[:, 7], t0[:, 0], t0[:, 4]
+        want[:, 5, :, 1], want[:, 5, :, 2] = t0[:, 7, :, 15], t0[:, 5, :, 7]
+        want[:, 0, :, 5], want[:, 7, :, 3] = t0[:, 4, :, 4], t0[:, 2, :, 1]
+        assert torch.equal(t[:, near], want)
+
+
+def test_calls_at_the_same_time():
+    """Each call of a beam step and of dropped tokens on a stream of its own, many times,
+    in buffers of its own: the results of the calls alone."""
+    rng = np.random.default_rng(9)
+    c = _tree(rng, 60, 4, 900, 9, spare=4000)
+    src = np.sort(rng.integers(0, 4, (60, 4)), 1) + np.arange(60)[:, None] * 4
+    d = _tree(rng, 50, 2, 700, 4000, spare=4000)
+    keep, ks, start = _lists(rng, d, 0.4)
+    x = _logits(rng, 32, 50000, "bf16").cuda()
+    scores = torch.from_numpy(_scores(rng, 8, 4)).cuda()
+    fork = [_i32(c[k]) for k in ("table", "lens", "refs", "stack")] + [_i32([c["count"]])]
+    comp = [_i32(d[k]) for k in ("table", "lens", "refs", "stack")] + [_i32([d["count"]])]
+    sources, kd, kl, st = _i32(src.reshape(-1)), _i32(keep), _i32(ks), _i32(start)
+    slots = torch.full((2, len(ks), keep.shape[1] + 16), -1, dtype=torch.int64, device="cuda")
+    NB = len(d["refs"])
+    cache = torch.randn(3, NB, 2, 16, 64, device="cuda").bfloat16()
+
+    def calls():
+        return [[t.clone() for t in fork], [t.clone() for t in comp], slots.clone(),
+                cache.clone(), cache.clone() + 1]
+
+    def select(s):
+        return pa.pa_beam_select(x, scores, 9)
+
+    def forked(s):
+        return (*pa.pa_fork_blocks(sources, *s[0]), *s[0])
+
+    def dropped(s):
+        out = pa.pa_compact_blocks(kd, kl, *s[1], keep_start=st, src_slots=s[2][0],
+                                   dst_slots=s[2][1])
+        pa.pa_move_tokens(s[3], s[4], *out)
+        return (*out, *s[1], s[3], s[4])
+
+    works = (select, forked, dropped, select, dropped, forked)
+    alone = []
+    for w in works:
+        alone.append(w(calls()))
+        torch.cuda.synchronize()
+    states = [[calls() for _ in range(4)] for _ in works]
+    streams = [torch.cuda.Stream() for _ in works]
+    torch.cuda.synchronize()
+    got = [[] for _ in works]
+    for i in range(4):
+        for j, w in enumerate(works):
+            with torch.cuda.stream(streams[j]):
+                got[j].append(w(states[j][i]))
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    for one, many in zip(alone, got):
+        for some in many:
+            for a, b in zip(one, some):
+                assert torch.equal(a, b)
