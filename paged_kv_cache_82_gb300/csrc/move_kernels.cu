@@ -12,10 +12,13 @@ namespace {
 
 // ---- blocks --------------------------------------------------------------------
 // A CTA copies pieces of up to 32 KB, eight 16-byte loads of each thread in flight: 24
-// blocks x 32 layers of bf16 16.6 us, 500 x 80 of E4M3 391 us = 6.7 TB/s (99 % of a plain
-// copy's rate; with four loads and eight CTAs per SM 16.8 and 420).
+// blocks x 32 layers of bf16 16.9 us, 500 x 80 of E4M3 395 us = 6.6 TB/s (98 % of a plain
+// copy's rate; with four loads and eight CTAs per SM 16.8 and 420).  Smaller blocks have
+// fewer threads, not fewer loads of each: 200 blocks x 32 layers of INT4, 8 heads of 64,
+// 18.8 us (floor 17.3; with a thread to a load 40.7, to four 21.1); of 8 heads of 64 E4M3
+// channels 32.4 (30.8; 48.6, 33.6).
 constexpr int kCopyLoads = 8;
-constexpr int kMaxCopyThreads = 256;  // fewer where a block is smaller than 4 KB
+constexpr int kMaxCopyThreads = 256;  // fewer where a block is smaller than 32 KB
 constexpr int kCopyCtasPerSm = 64;    // CTAs of a grid: more than are resident, for a short
                                       // last wave
 
@@ -311,7 +314,7 @@ cudaError_t launch_copy_blocks_layers(const LayerCaches& c, int64_t block_bytes,
   p.v_layer = c.v_layer_bytes;
   p.num_blocks = c.num_blocks;
   p.block_vecs = block_bytes / 16;
-  const int64_t warps = (p.block_vecs + 31) / 32;
+  const int64_t warps = (p.block_vecs + 32 * kCopyLoads - 1) / (32 * kCopyLoads);
   const int threads = warps * 32 < kMaxCopyThreads ? (int)warps * 32 : kMaxCopyThreads;
   p.pieces = (int)((p.block_vecs + threads * kCopyLoads - 1) / (threads * kCopyLoads));
   p.num_layers = c.num_layers;

@@ -134,3 +134,79 @@ def test_calls_at_the_same_time():
         for some in many:
             for a, b in zip(one, some):
                 assert torch.equal(a, b)
+
+
+def test_rows_far_apart():
+    """A row stride past 2^31 elements in all."""
+    rng = np.random.default_rng(12)
+    x = _logits(rng, 4, 3001, "bf16")
+    rows = torch.empty(4, 1 << 30, dtype=torch.bfloat16, device="cuda")[:, 5:3006]
+    rows.copy_(x)
+    _check(x, _scores(rng, 2, 2), 5, rows=rows)
+
+
+@pytest.mark.parametrize("which", range(1, 16))
+def test_some_of_the_state_in_place(which):
+    """Each of tables, lengths, references and count in place or not, from unaligned
+    starts."""
+    rng = np.random.default_rng(which)
+    names = ("block_tables", "seq_lens", "extra_refs", "free_count")
+
+    def offset(x, value=None):  # the same, four bytes behind a 16-byte boundary
+        t = torch.empty(x.numel() + 1, dtype=torch.int32, device="cuda")[1:].view(x.shape)
+        return t.copy_(x) if value is None else t.fill_(value)
+
+    for call in ("fork", "compact"):
+        c = _tree(rng, 20, 3, 300, 500, spare=900)
+        state = [offset(_i32(c[k])) for k in ("table", "lens", "refs", "stack")]
+        state.append(_i32([c["count"]]))
+        ins = dict(zip(names, (state[0], state[1], state[2], state[4])))
+        outs = {n + "_out": offset(ins[n], -9) for i, n in enumerate(names) if which >> i & 1}
+        before = np.full_like(c["table"], -9) if which & 1 else c["table"]
+        if call == "fork":
+            src = rng.integers(-1, 60, 60)
+            mapping, pairs = pa.pa_fork_blocks(_i32(src), *state, **outs)
+            want = ref.fork(src, c["table"], c["lens"], c["refs"], c["stack"], c["count"], before)
+            assert int(pairs) == want["num_pairs"]
+            np.testing.assert_array_equal(mapping.cpu().numpy(), want["pairs"])
+        else:
+            keep, ks, start = _lists(rng, c, 0.3)
+            got = pa.pa_compact_blocks(_i32(keep), _i32(ks), *state, keep_start=_i32(start),
+                                       **outs)
+            want = ref.compact(keep, ks, start, c["table"], c["lens"], c["refs"], c["stack"],
+                               c["count"], got[0].cpu().numpy(), got[1].cpu().numpy(), before)
+            np.testing.assert_array_equal(got[0].cpu().numpy(), want["src"])
+            np.testing.assert_array_equal(got[1].cpu().numpy(), want["dst"])
+            np.testing.assert_array_equal(got[2].cpu().numpy(), want["moves"])
+        assert pa.pa_get_device_error() == 0 and not want["flags"]
+        for n, k in zip(names[:3], ("table", "seq_lens", "refs")):
+            np.testing.assert_array_equal(outs.get(n + "_out", ins[n]).cpu().numpy(), want[k])
+        np.testing.assert_array_equal(state[3].cpu().numpy(), want["stack"])
+        assert int(outs.get("free_count_out", ins["free_count"])) == want["count"]
+
+
+def test_rows_cut_to_their_first_tokens():
+    """No lists at all: keep of no columns."""
+    rng = np.random.default_rng(2)
+    c = _tree(rng, 9, 2, 200, 300, spare=300)
+    start = np.array([int(rng.integers(0, n + 1)) for n in c["lens"]], np.int32)
+    for in_place in (True, False):
+        assert not _compact(c, np.zeros((18, 0), np.int32), np.zeros(18, np.int32), start,
+                            in_place)["flags"]
+
+
+def test_one_token_to_many_slots():
+    k = torch.randn(2, 6, 3, 16, 64, device="cuda").bfloat16()
+    v = torch.randn_like(k)
+    src = torch.tensor([[5, 5, 5, 90, 5, 7]], device="cuda")
+    dst = torch.tensor([[5, 17, 90, 91, 95, 3]], device="cuda")
+    k0, v0 = k.clone(), v.clone()
+    # (90 is a destination before it is a source: not a list of moves, left out)
+    src[0, 3] = -1
+    pa.pa_move_tokens(k, v, src, dst, torch.tensor([6], dtype=torch.int32, device="cuda"))
+    assert pa.pa_get_device_error() == 0
+    for t, t0 in ((k, k0), (v, v0)):
+        want = t0.clone()
+        for s, d in ((5, 17), (5, 90), (5, 95), (7, 3)):
+            want[:, d // 16, :, d % 16] = t0[:, s // 16, :, s % 16]
+        assert torch.equal(t, want)
