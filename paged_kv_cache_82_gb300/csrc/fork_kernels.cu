@@ -22,7 +22,7 @@
 // lengths in shared memory and does the small scans over rows or pieces for itself.
 // What is left is latency: five or six barriers of 1.3 us each, the way of the writes
 // before them to L2 included, and one or two loads of 0.5 us between them.  64 forked
-// rows of up to 258 blocks 14.6 us, 1024 of up to 1026 31 us; 64 requests that keep 6
+// rows of up to 258 blocks 14.4 us, 1024 of up to 1026 29 us; 64 requests that keep 6
 // of their last 32 tokens 17 us, 32 prompts of 2K to 32K that keep a quarter 30 us.
 #include <cooperative_groups.h>
 #include <limits.h>
@@ -108,10 +108,15 @@ __device__ __forceinline__ bool in_pool(const Pool& p, int id) {
   return id >= 0 && (int64_t)id < p.num_blocks;
 }
 
+// Counts of one round of a scan: one to a thread, or four where there are more pieces than
+// threads (1024 rows of up to 1026 blocks, some 2500 released pieces: 31.0 us with one, 29.2
+// with four; 64 rows of up to 258, some 30 pieces: 14.2 and 14.4).
+constexpr int kEach = 4, kScan = kEach * kThreads;
+
 struct Scan {  // shared memory of the scans
   int warp_sums[32];
   int total;
-  int starts[kThreads];
+  int starts[kScan];
 };
 
 // f(piece, sum of the counts before it) for each piece whose count is not 0, by the
@@ -120,17 +125,28 @@ template <class F>
 __device__ __forceinline__ int64_t in_order(const Team& t, int pieces, const int* counts,
                                             Scan& sh, const F& f) {
   int64_t sum = 0;
+  const int each = pieces > kThreads ? kEach : 1;
 #pragma unroll 1
-  for (int first = 0; first < pieces; first += kThreads) {
-    const int i = first + t.tid;
-    const int n = i < pieces ? __ldcg(counts + i) : 0;
-    const int before = block_scan_excl(n, &sh.total, sh.warp_sums);
-    sh.starts[t.tid] = n ? before : -1;
+  for (int first = 0; first < pieces; first += each * kThreads) {
+    int n[kEach], mine = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = first + t.tid * each + e;
+      n[e] = e < each && i < pieces ? __ldcg(counts + i) : 0;
+      mine += n[e];
+    }
+    int before = block_scan_excl(mine, &sh.total, sh.warp_sums);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (e < each) {
+        sh.starts[t.tid * each + e] = n[e] ? before : -1;
+        before += n[e];
+      }
     const int64_t round = sh.total;
     __syncthreads();
-    const int ahead = first % t.gwarps;
+    const int ahead = first % t.gwarps, here = min(each * kThreads, pieces - first);
 #pragma unroll 1
-    for (int j = t.gwarp >= ahead ? t.gwarp - ahead : t.gwarp - ahead + t.gwarps; j < kThreads;
+    for (int j = t.gwarp >= ahead ? t.gwarp - ahead : t.gwarp - ahead + t.gwarps; j < here;
          j += t.gwarps)
       if (sh.starts[j] >= 0) f(first + j, sum + sh.starts[j]);
     sum += round;
@@ -142,9 +158,9 @@ __device__ __forceinline__ int64_t in_order(const Team& t, int pieces, const int
 // The entries that a call releases, in pieces: piece i is entries [col0, col0 + kSeg) of
 // the (i / per_row)-th row that releases any.  load(k, col0, ids): the blocks that the
 // released entries among them name, -1 elsewhere (entry e of a lane: column col0 + 32 e +
-// lane; any number in a broken table); row_of(k): the row.  A piece belongs to the same warp in every pass, which keeps
-// its first piece's blocks and, once known, owners in registers: most calls have no more
-// pieces than warps, and then a pass is one load of the counts.
+// lane; any number in a broken table); row_of(k): the row.  A piece belongs to the same warp
+// in every pass, which keeps its first piece's blocks and, once known, owners in registers:
+// most calls have no more pieces than warps, and then a pass is one load of the counts.
 template <class Load, class RowOf>
 struct Released {
   const Pool& p;
@@ -198,7 +214,7 @@ struct Released {
     }
   }
   // Pushes them from stack position `base` on; how many there are.  (Every CTA scans all
-  // counts, a round of kThreads at a time.)
+  // counts.)
   __device__ __forceinline__ int64_t push(const int* counts, int64_t base, Scan& sh) const {
     return in_order(t, pieces, counts, sh, [&](int i, int64_t before) {
       int ids[kPer], count[kPer];
@@ -823,7 +839,8 @@ template <class P>
 cudaError_t launch_team(void (*kernel)(P), P& p, int64_t want, size_t smem, size_t max_smem,
                         int num_sms, cudaStream_t stream) {
   // (always the largest step's limit: see launch_build_step)
-  if (smem > 40 * 1024) {
+  static_assert(sizeof(Scan) < 20 * 1024, "with dynamic shared memory, 48 KB by default");
+  if (smem > 28 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)max_smem);
     if (e != cudaSuccess) return e;

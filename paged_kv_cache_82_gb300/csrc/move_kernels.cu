@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(kMaxCopyThreads) copy_layers_kernel(CopyK p) {
 // done in order.  Each channel of each head of each layer has an order of its own: a
 // warp takes slices of heads' channels through all moves of a row, and no warp waits
 // for another: 8 prompts cut from 4K-8K to half, 16 layers of bf16, 488 us = 6.4 TB/s
-// (94 % of a plain copy's rate).  Reading ahead is always right (no destination is a later source), so a
-// warp keeps kStages steps of loads in flight, through shared memory, and writes a step
-// once it and those before it have landed.
+// (94 % of a plain copy's rate).  Reading ahead is always right (no destination is a later
+// source), so a warp keeps kStages steps of loads in flight, through shared memory, and
+// writes a step once it and those before it have landed.
 constexpr int kMoveWarps = 4;
 constexpr int kStages = 8;
 constexpr int kStageLoads = 4;    // 16-byte loads of a lane in one step, at most

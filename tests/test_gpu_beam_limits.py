@@ -185,6 +185,20 @@ def test_some_of_the_state_in_place(which):
         assert int(outs.get("free_count_out", ins["free_count"])) == want["count"]
 
 
+@pytest.mark.parametrize("R", [120, 150, 190, 230, 270, 330, 500, 800, 1300, 1900, 2600, 4096])
+def test_wide_tables_of_few_blocks(R):
+    """Rows' state and tiles of tables in shared memory, from little of it to all."""
+    rng = np.random.default_rng(R)
+    c = _tree(rng, R // 2, 2, 70, 9, spare=R * 5)
+    wide = np.full((R, 40_000 if R < 600 else 3000), -7, np.int32)
+    wide[:, :c["table"].shape[1]] = c["table"]
+    c["table"] = wide
+    src = np.sort(rng.integers(0, 2, (R // 2, 2)), 1) + np.arange(R // 2)[:, None] * 2
+    assert not _fork(c, src.reshape(-1))["flags"]
+    keep, ks, start = _lists(rng, c, 0.3)
+    assert _compact(c, keep, ks, start)["flags"] <= {"blocks"}
+
+
 def test_rows_cut_to_their_first_tokens():
     """No lists at all: keep of no columns."""
     rng = np.random.default_rng(2)
