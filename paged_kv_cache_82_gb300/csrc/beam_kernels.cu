@@ -265,34 +265,62 @@ __device__ __forceinline__ void rank_list(const uint64_t* list, int n, int K, ui
   for (int i = n + threadIdx.x; i < K; i += kBeamThreads) keys[i] = 0;
 }
 
+// More vectors reach the threshold than K should leave: the logits of some lanes or warps lie
+// above the others' (a vocabulary sorted by frequency).  The threshold once more, of the
+// vectors kept, dealt out over all warps.
+template <typename T>
+__device__ __noinline__ float tighten(const uint4* vecs, int n, int K, uint32_t* s_bar,
+                                      float floor_x) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int i = lane * kWarps + warp; i < n; i += kBeamThreads)
+    m = fmaxf(m, (typename Pack<T>::Max(vecs[i])).value());
+  const uint32_t bar = warp_qth_largest(ordered(fminf(m, FLT_MAX)), (K + kWarps - 1) / kWarps);
+  __syncthreads();  // (s_bar has been read)
+  if (lane == 0) s_bar[warp] = bar;
+  __syncthreads();
+  return fmaxf(unordered(__reduce_min_sync(~0u, s_bar[lane & (kWarps - 1)])), floor_x);
+}
+
 // More logits than there is room for reach the threshold: those of a chunk of equal ones
 // (masked by a type's lowest value, say), as a rule.  The logits above it to the list, and
-// then of the equal ones the first; where even the former are too many (the warps' logits
-// must lie far apart), the best key below the last one taken, K times.
+// then of the equal ones the first; where even the former are too many, above a threshold
+// of the vectors kept; and where that does not help, the best key below the last one taken,
+// K times.
 template <typename T, int kVecs>
 __device__ __noinline__ void pick_from_many(const T* x, int base, int V, int K, float floor_x,
-                                            uint64_t* list, int* s_count, int* warp_sums,
+                                            const uint4* vecs, int kept, uint64_t* list,
+                                            int* s_count, int* warp_sums, uint32_t* s_bar,
                                             uint64_t* s_best, uint64_t* keys) {
   using P = Pack<T>;
   constexpr int kStep = kBeamThreads * P::kN;
-  __syncthreads();
-  if (threadIdx.x == 0) *s_count = 0;
-  __syncthreads();
+  int n;
 #pragma unroll 1
-  for (int i = 0; i < kVecs; ++i) {
-    const int at = base + i * kStep;
-    const uint4 v = load_vec<T>(x, at, V);
+  for (bool again = true;; again = false) {
+    __syncthreads();
+    if (threadIdx.x == 0) *s_count = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < kVecs; ++i) {
+      const int at = base + i * kStep;
+      const uint4 v = load_vec<T>(x, at, V);
 #pragma unroll
-    for (int j = 0; j < P::kN; ++j) {
-      const float e = P::get(v, j);
-      if (e > floor_x) {
-        const int n = atomicAdd(s_count, 1);
-        if (n < kListCap) list[n] = make_key(fminf(e, FLT_MAX), at + j);
+      for (int j = 0; j < P::kN; ++j) {
+        const float e = clean(P::get(v, j));
+        if (e > floor_x) {
+          const int place = atomicAdd(s_count, 1);
+          if (place < kListCap) list[place] = make_key(e, at + j);
+        }
       }
     }
+    __syncthreads();
+    n = *s_count;
+    if (n <= kListCap || !again) break;
+    const float higher = tighten<T>(vecs, kept, K, s_bar, floor_x);
+    if (higher == floor_x) break;
+    floor_x = higher;
   }
-  __syncthreads();
-  int n = *s_count;
   if (n <= kListCap) {
 #pragma unroll 1
     for (int i = 0; i < kVecs && n < K; ++i) {
@@ -300,13 +328,13 @@ __device__ __noinline__ void pick_from_many(const T* x, int base, int V, int K, 
       const uint4 v = load_vec<T>(x, at, V);
       int equal = 0, total;
 #pragma unroll
-      for (int j = 0; j < P::kN; ++j) equal += P::get(v, j) == floor_x;
+      for (int j = 0; j < P::kN; ++j) equal += clean(P::get(v, j)) == floor_x;
       int place = n + block_scan_excl(equal, warp_sums + kWarps, warp_sums);
       total = warp_sums[kWarps];
 #pragma unroll
       for (int j = 0; j < P::kN; ++j)
-        if (P::get(v, j) == floor_x) {
-          if (place < K) list[place] = make_key(fminf(floor_x, FLT_MAX), at + j);
+        if (clean(P::get(v, j)) == floor_x) {
+          if (place < K) list[place] = make_key(floor_x, at + j);
           ++place;
         }
       n = min(n + total, max(n, K));
@@ -432,7 +460,7 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
     return;
   }
   // ---- the vectors that hold a logit at or above the threshold, to shared memory
-  const float floor_x = fmaxf(unordered(least), P::kLowest);
+  float floor_x = fmaxf(unordered(least), P::kLowest);
   unsigned hits = 0;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) hits |= (typename P::Max(v[i])).reaches(floor_x) ? 1u << i : 0u;
@@ -458,6 +486,8 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
   for (int d = kWarps / 2; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   __syncthreads();
   const int n_vecs = s_vecs;
+  if (n_vecs > 2 * K + 64 && n_vecs <= kVecCap)  // (some K to 2 K are usual)
+    floor_x = tighten<T>(vecs, n_vecs, K, s_bar, floor_x);
   if (n_vecs <= kVecCap)  // the logits among theirs
     for (int e = tid; e < n_vecs * kN; e += kBeamThreads) {
       const int at = vec_at[e / kN] + e % kN;
@@ -487,7 +517,8 @@ __global__ void __launch_bounds__(kBeamThreads, kVecs >= 8 ? 4 : 5)
   if (n <= kListCap)
     rank_list(list, n, K, keys);
   else
-    pick_from_many<T, kVecs>(x, base, V, K, floor_x, list, &s_count, s_scan, s_best, keys);
+    pick_from_many<T, kVecs>(x, base, V, K, floor_x, vecs, min(n_vecs, kVecCap), list, &s_count,
+                             s_scan, s_bar, s_best, keys);
 }
 
 // ---- sums again, in two fp32 parts ---------------------------------------------

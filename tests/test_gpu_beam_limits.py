@@ -31,6 +31,42 @@ def test_equal_logits_of_many_beams(dtype):
     _check(x, scores, 100)
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("allowed", [300, 1500, 6000, 14000])
+def test_few_warps_hold_everything(dtype, allowed):
+    """Allowed tokens next to each other, the others at the type's lowest value or -inf;
+    logits that fall or rise along the vocabulary."""
+    rng = np.random.default_rng(allowed)
+    V = 50_003
+    for rest in (-np.inf, torch.finfo(DT[dtype]).min):
+        x = _logits(rng, 8, V, dtype)
+        for r in range(8):
+            at = int(rng.integers(0, V - allowed))
+            x[r, :at], x[r, at + allowed:] = rest, rest
+        for K in (3, 40, 128):
+            _check(x, _scores(rng, 2, 4), K)
+    x = _logits(rng, 8, V, dtype)
+    for up in (True, False):
+        y = torch.sort(x.float(), 1, descending=not up)[0].to(DT[dtype])
+        y[:, allowed::allowed] = torch.finfo(DT[dtype]).min
+        for K in (5, 100):
+            _check(y, _scores(rng, 2, 4), K)
+    trend = torch.log1p(torch.arange(V) / 50.0) * -2
+    _check((x.float() + trend).to(DT[dtype]), _scores(rng, 4, 2), 16)
+
+
+def test_infinite_among_the_largest():
+    """More largest numbers than a list holds, and +inf, which counts as one of them."""
+    x = torch.zeros(2, 30_000)
+    x[0, 2000:7000] = torch.finfo(torch.float32).max
+    x[0, 6000:6010] = float("inf")
+    x[1, ::3] = float("inf")
+    x[1, 1::3] = torch.finfo(torch.float32).max
+    x[1, 2::9] = float("nan")
+    for K in (1, 8, 100):
+        _check(x, np.array([[0.0, -1.0]], np.float32), K)
+
+
 @pytest.mark.parametrize("in_place", [True, False])
 def test_one_row_of_a_million_blocks(in_place):
     rng = np.random.default_rng(1)
