@@ -6,27 +6,31 @@
 //
 // Each logit is read once.  A CTA takes a chunk of a row into registers and
 // leaves the chunk's maximum m, its sum of exp(x - m) and its K largest logits;
-// a second kernel, one CTA per group, joins the sums of each row (the running
+// a second kernel, a CTA to a group, joins the sums of each row (the running
 // maximum of an online softmax, over chunks) and picks K of the W x chunks x K
 // candidates.
 //
 // The K largest of a chunk without sorting it: eight warps, each with its q-th
 // largest lane maximum, q = ceil(K / 8); the smallest of these eight numbers is
-// a threshold that at least 8 q >= K logits reach, and about 20 of 8192 do for K
+// a threshold that at least 8 q >= K logits reach, and about 20 of 16384 do for K
 // = 8.  Those go to a list in shared memory, where each counts the larger ones.
+// (Where some lanes or warps hold most of the largest logits, as in a vocabulary
+// sorted by frequency, the same again over what reached the threshold: the case
+// below with a falling trend 22 us with it, 33 without, sorted 36 and 243.)
 //
 // Which tokens come back must not depend on the rounding of fp32 sums: scores are
 // compared in 64 bits, and where two beams' scores lie closer than the fp32 sums
 // resolve (kNear), the sums of those rows are taken again with exponentials in
 // two fp32 parts and the group is picked again (about one group in 2000 of
-// unlike beams, always for beams that are copies of each other).
+// unlike beams with K = 4, one in 100 with K = 64, always for beams that are copies of
+// each other; such a call takes 33 to 40 us longer).
 //
 // 64 groups of 4 beams of 128256 bf16 logits, a tenth of them finished, 59 MB: 22.0 us,
 // where reading them at a plain copy's rate takes 8.7.  The chunks take 15 of it: half of
 // the issue slots (nine instructions to a logit), the rest waiting for loads and for the
 // other warps of a CTA, four CTAs to an SM.  The join's chain of short steps takes 5, its
-// launch and end the rest.  32 groups of 8 beams of 50257 fp32 logits 21.8 us; one of 4
-// beams of 32000 8.6 us.
+// launch and end the rest.  32 groups of 8 beams of 50257 fp32 logits 22.0 us; one of 4
+// beams of 32000 8.3 us.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
@@ -684,10 +688,95 @@ __device__ __forceinline__ int main_warps_count(bool p) {
 
 // The rare ways, out of the way of the usual ones' instructions.
 //
-// f(score, tie) for this thread's share of all candidates, kBatch loads at a time.
-template <class F>
-__device__ __forceinline__ void for_all_scored(const Group& g, const uint64_t* keys, int n_all,
-                                               int per_row, int end_key, const F& f) {
+// More candidates than there is room for, or than are soon ranked, reach the threshold
+// (many equal scores): a piece's candidates are in the scores' order, so the best of all
+// pieces' first ones is taken, K times, 2.3 us each (one group of 4 equal rows of 128256
+// logits: 23 us with K = 4, 296 with K = 128).  A thread has the pieces tid, tid + 256, ...
+// and keeps the best of their first ones; `heads` (two words of each piece, those of its
+// maximum and sum) counts the taken ones.  Returns the list's length.
+__device__ __noinline__ int list_in_order(Group& g, const uint64_t* keys, uint32_t* heads,
+                                          int pieces, int S, int end_key, int K) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto first_of = [&](int piece, uint32_t taken, uint64_t key) {
+    const int w = piece / S;
+    if (isnan(g.cum[w])) return Cand{0, 0};
+    if (g.done[w]) {
+      if (piece != w * S || taken != 0) return Cand{0, 0};
+      key = (uint64_t)(uint32_t)end_key;
+    }
+    if (key == 0) return Cand{0, 0};
+    return Cand{score64(g, w, unordered((uint32_t)(key >> 32))), make_tie(w, key)};
+  };
+  for (int piece = tid; piece < pieces; piece += kBeamThreads) heads[2 * piece] = 0;
+  Cand mine;
+  int at;
+  auto look = [&] {
+    mine = Cand{0, 0};
+    at = tid;
+#pragma unroll 1
+    for (int p0 = tid; p0 < pieces; p0 += kBatch * kBeamThreads) {
+      uint32_t taken[kBatch];
+      uint64_t key[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int piece = p0 + i * kBeamThreads;
+        taken[i] = piece < pieces ? heads[2 * piece] : K;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        key[i] = taken[i] < (uint32_t)K
+                     ? __ldcg(keys + (int64_t)(p0 + i * kBeamThreads) * K + taken[i])
+                     : 0;
+#pragma unroll 1
+      for (int i = 0; i < kBatch; ++i) {
+        const int piece = p0 + i * kBeamThreads;
+        if (piece < pieces) {
+          const Cand o = first_of(piece, taken[0], key[0]);
+          if (better(o, mine)) {
+            mine = o;
+            at = piece;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k + 1 < kBatch; ++k) {
+          taken[k] = taken[k + 1];
+          key[k] = key[k + 1];
+        }
+      }
+    }
+  };
+  look();
+  // (the list's last places hold the warps' best, of two rounds in turn)
+  static_assert(kMaxBeamSelected + 2 * kWarps <= kListCap, "room for them");
+  int n = 0;
+#pragma unroll 1
+  for (; n < K; ++n) {
+    Cand best = mine;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const Cand o{__shfl_xor_sync(~0u, best.score, d), __shfl_xor_sync(~0u, best.tie, d)};
+      if (better(o, best)) best = o;
+    }
+    Cand* room = g.list + kListCap - (n & 1 ? 2 : 1) * kWarps;
+    if (lane == 0) room[warp] = best;
+    main_warps_sync();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (better(room[w], best)) best = room[w];
+    if (best.score == 0) break;
+    if (tid == 0) g.list[n] = best;
+    if (mine.score == best.score && mine.tie == best.tie) {
+      ++heads[2 * at];
+      look();
+    }
+  }
+  main_warps_sync();
+  return n;
+}
+// and, once they are picked, the candidates left out that are close to the last pick
+__device__ __noinline__ void note_near_from_all(Group& g, const uint64_t* keys, int n_all,
+                                                int per_row, int end_key, const Cand& end) {
+  const float end_s = (float)value(end.score);
 #pragma unroll 1
   for (int c0 = threadIdx.x; c0 < n_all; c0 += kBatch * kBeamThreads) {
     uint64_t batch[kBatch];
@@ -699,67 +788,18 @@ __device__ __forceinline__ void for_all_scored(const Group& g, const uint64_t* k
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int c = c0 + i * kBeamThreads, w = c / per_row;
-      if (c >= n_all || isnan(g.cum[w]) || (g.done[w] && c != w * per_row)) continue;
+      if (c >= n_all || w == end.beam() || isnan(g.cum[w])) continue;
+      if (g.done[w] && c != w * per_row) continue;
       const uint64_t key = g.done[w] ? (uint64_t)(uint32_t)end_key : batch[i];
       if (key == 0) continue;
-      const Cand o{score64(g, w, unordered((uint32_t)(key >> 32))), make_tie(w, key)};
-      if (o.score != 0) f(o);
+      const float x = unordered((uint32_t)(key >> 32));
+      const float s = g.done[w] ? g.cum[w] : g.cum[w] + ((x - g.top[w]) + g.off32[w]);
+      // (in fp32 first: far more than its error and kNear away, as nearly all are)
+      if (s < end_s - 1e-4f - 0x1p-18f * (fabsf(s) + fabsf(g.cum[w]) + fabsf(g.off32[w]))) continue;
+      const Cand o{score64(g, w, x), make_tie(w, key)};
+      if (o.score != 0 && better(end, o)) note_near(g, end, o);
     }
   }
-}
-// how many of all candidates are at or above (score, tie), in every thread
-__device__ __forceinline__ int count_from(Group& g, const uint64_t* keys, int n_all,
-                                          int per_row, int end_key, const Cand& from) {
-  int n = 0;
-  for_all_scored(g, keys, n_all, per_row, end_key,
-                 [&](const Cand& o) { n += !better(from, o); });
-  n = (int)__reduce_add_sync(~0u, (unsigned)n);
-  main_warps_sync();
-  if ((threadIdx.x & 31) == 0) g.bar[threadIdx.x >> 5] = (uint32_t)n;
-  main_warps_sync();
-  return (int)__reduce_add_sync(~0u, (threadIdx.x & 31) < kWarps ? g.bar[threadIdx.x & 31] : 0);
-}
-// More candidates than the list holds reach the threshold (many equal scores): the list
-// from the candidate on which, by halving first the scores' range and then the ties', has
-// at least K of them behind it and not many more.  Returns the list's length.
-__device__ __noinline__ int list_from_all(Group& g, const uint64_t* keys, int n_all,
-                                          int per_row, int end_key, int K) {
-  const int most = min(kListCap, 3 * K + 64);
-  Cand from{1, 0};  // every candidate is above
-  int n = count_from(g, keys, n_all, per_row, end_key, from);
-#pragma unroll 1
-  for (int word = 0; word < 2; ++word) {  // of (score, tie)
-    uint64_t lo = word ? from.tie : from.score, hi = ~0ull;
-#pragma unroll 1
-    for (int i = 0; i < 64 && n > most && hi - lo > 1; ++i) {
-      const uint64_t mid = lo + (hi - lo) / 2;
-      const Cand at = word ? Cand{from.score, mid} : Cand{mid, 0};
-      const int reach = count_from(g, keys, n_all, per_row, end_key, at);
-      if (reach >= K) {
-        lo = mid;
-        n = reach;
-      } else {
-        hi = mid;
-      }
-    }
-    (word ? from.tie : from.score) = lo;
-  }
-  if (threadIdx.x == 0) g.count = 0;
-  main_warps_sync();
-  for_all_scored(g, keys, n_all, per_row, end_key, [&](const Cand& o) {
-    if (better(from, o)) return;
-    const int at = atomicAdd(&g.count, 1);
-    if (at < kListCap) g.list[at] = o;
-  });
-  main_warps_sync();
-  return min(g.count, kListCap);
-}
-// and, once they are picked, the candidates left out that are close to the last pick
-__device__ __noinline__ void note_near_from_all(Group& g, const uint64_t* keys, int n_all,
-                                                int per_row, int end_key, const Cand& end) {
-  for_all_scored(g, keys, n_all, per_row, end_key, [&](const Cand& o) {
-    if (better(end, o)) note_near(g, end, o);
-  });
 }
 
 // The sums of the rows noted, in two fp32 parts: CTA `rank` of `ranks` takes its share of
@@ -999,14 +1039,15 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(BeamK p) {
     else
       main_warps_sync();
     int n = g.count;
-    const bool all_listed = n <= kListCap;
+    const bool all_listed = n <= min(kListCap, 4 * K + 128);
     if (all_listed) {
 #pragma unroll 1
       for (int i = tid; i < n; i += kBeamThreads)
         g.list[i].score = score64(g, g.list[i].beam(), g.list[i].logit());
       main_warps_sync();
     } else {
-      n = list_from_all(g, keys, n_all, per_row, end_key, K);
+      n = list_in_order(g, keys, reinterpret_cast<uint32_t*>(p.stats + row0 * S), W * S, S,
+                        end_key, K);
     }
 #pragma unroll 1
     for (int i = tid; i < n; i += kBeamThreads) {

@@ -31,6 +31,29 @@ def test_equal_logits_of_many_beams(dtype):
     _check(x, scores, 100)
 
 
+@pytest.mark.parametrize("K", [7, 64, 128])
+def test_more_equal_scores_than_a_list_holds(K):
+    """One group whose candidates come in many pieces: equal rows, rows of two or three
+    values, few allowed tokens, finished beams, beams with nothing to offer, and beams whose
+    scores are a power of two apart, as their logits are."""
+    rng = np.random.default_rng(K)
+    V = 100_001
+    x = torch.zeros(6, V)
+    x[1] = torch.from_numpy(rng.integers(0, 2, V).astype(np.float32))
+    x[2] = torch.from_numpy(rng.integers(0, 3, V).astype(np.float32)) * 0.25
+    x[3, 5:] = torch.finfo(torch.float32).min
+    x[4] = float("-inf")
+    scores = np.array([[-1.0, -1.0, -1.5, -2.0, 0.0, -1.0]], np.float32)
+    finished = np.array([[0, 0, 0, 0, 0, 1]], np.uint8)
+    _check(x, scores, K, finished, 9)
+    _check(x, scores, K)
+    _check(x[:4].repeat(16, 1), -np.arange(64, dtype=np.float32)[None] / 8, K)
+    one = torch.full((4, V), torch.finfo(torch.bfloat16).min, dtype=torch.bfloat16)
+    for r in range(4):
+        one[r, int(rng.integers(0, V))] = 3.0      # one allowed token of each beam
+    _check(one, np.array([[0.0, -1.0, -1.0, -7.5]], np.float32), K)
+
+
 @pytest.mark.parametrize("dtype", sorted(DT))
 @pytest.mark.parametrize("allowed", [300, 1500, 6000, 14000])
 def test_few_warps_hold_everything(dtype, allowed):
