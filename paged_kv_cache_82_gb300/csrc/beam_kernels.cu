@@ -30,7 +30,7 @@
 // the issue slots (nine instructions to a logit), the rest waiting for loads and for the
 // other warps of a CTA, four CTAs to an SM.  The join's chain of short steps takes 5, its
 // launch and end the rest.  32 groups of 8 beams of 50257 fp32 logits 22.0 us; one of 4
-// beams of 32000 8.3 us.
+// beams of 32000 7.5 us.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
@@ -690,8 +690,8 @@ __device__ __forceinline__ int main_warps_count(bool p) {
 //
 // More candidates than there is room for, or than are soon ranked, reach the threshold
 // (many equal scores): a piece's candidates are in the scores' order, so the best of all
-// pieces' first ones is taken, K times, 2.3 us each (one group of 4 equal rows of 128256
-// logits: 23 us with K = 4, 296 with K = 128).  A thread has the pieces tid, tid + 256, ...
+// pieces' first ones is taken, K times, some 1.7 us each (one group of 4 equal rows of
+// 128256 logits: 226 us with K = 128).  A thread has the pieces tid, tid + 256, ...
 // and keeps the best of their first ones; `heads` (two words of each piece, those of its
 // maximum and sum) counts the taken ones.  Returns the list's length.
 __device__ __noinline__ int list_in_order(Group& g, const uint64_t* keys, uint32_t* heads,
@@ -1133,12 +1133,14 @@ BeamPlan make_beam_plan(pa_dtype dtype, int num_groups, int beam_width, int voca
   const int64_t rows = (int64_t)num_groups * beam_width;
   const int64_t span = (int64_t)vocab_size + kBeamAlign - 1;
   auto chunks = [&](int e) { return (span + kBeamThreads * e - 1) / (kBeamThreads * e); };
-  // the longest chunks (32 registers of logits a thread) that give each of the 152 SMs
-  // two CTAs
+  // the longest chunks (32 registers of logits a thread) that make 16 CTAs: fewer pieces are
+  // sooner joined, and a CTA's loads are all in flight at once (one group of 4 beams of
+  // 128256 bf16 logits 14.5 us in chunks of 2048, 10.0 in chunks of 16384; of 32000 9.4 and
+  // 7.7; four groups of 32000 10.0 and 9.0)
   const int longest = dtype == PA_F32 ? 32 : 64;
   b.per_thread = 8;
   for (int e = longest; e > 8 && b.per_thread == 8; e /= 2)
-    if (e != 16 && rows * chunks(e) >= 2 * 152) b.per_thread = e;
+    if (e != 16 && rows * chunks(e) >= 16) b.per_thread = e;
   b.chunks = (int)chunks(b.per_thread);
   b.off_stats = (rows * b.chunks * num_selected * 8 + 255) / 256 * 256;
   b.bytes = b.off_stats + rows * b.chunks * 8;
