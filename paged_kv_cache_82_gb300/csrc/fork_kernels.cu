@@ -20,9 +20,10 @@
 // between the passes: up to eight CTAs as one cluster, where more are needed a
 // cooperative grid (one CTA per SM at most).  Every CTA keeps the rows' sources and
 // lengths in shared memory and does the small scans over rows or pieces for itself.
+// Tables are walked as far as the longest row goes, not as wide as they are.
 // What is left is latency: five or six barriers of 1.3 us each, the way of the writes
 // before them to L2 included, and one or two loads of 0.5 us between them.  64 forked
-// rows of up to 258 blocks 14.4 us, 1024 of up to 1026 29 us; 64 requests that keep 6
+// rows of up to 258 blocks 13 us, 1024 of up to 1026 29 us; 64 requests that keep 6
 // of their last 32 tokens 17 us, 32 prompts of 2K to 32K that keep a quarter 30 us.
 #include <cooperative_groups.h>
 #include <limits.h>
@@ -40,6 +41,7 @@ constexpr int kWarpsPerCta = kThreads / 32;
 constexpr int kMaxCluster = 8;  // the portable size
 constexpr int kSeg = 256;       // table entries (or listed tokens) of one piece: 8 per lane
 constexpr int kPer = kSeg / 32;
+constexpr int kFewPieces = 8;   // that every CTA of a cluster looks through for itself
 // counts below this are claims: INT_MIN + the place of a released entry
 constexpr int kClaim = -(1 << 30);
 
@@ -110,13 +112,25 @@ __device__ __forceinline__ bool in_pool(const Pool& p, int id) {
 
 // Counts of one round of a scan: one to a thread, or four where there are more pieces than
 // threads (1024 rows of up to 1026 blocks, some 2500 released pieces: 31.0 us with one, 29.2
-// with four; 64 rows of up to 258, some 30 pieces: 14.2 and 14.4).
+// with four; 64 rows of up to 258, some 30 pieces: 14.2 and 14.4 then).
 constexpr int kEach = 4, kScan = kEach * kThreads;
 
 struct Scan {  // shared memory of the scans
   int warp_sums[32];
   int total;
   int starts[kScan];
+};
+
+// The CTA's largest v, after the barrier that follows put().
+struct Largest {
+  int* room;  // [32]
+  __device__ __forceinline__ void put(const Team& t, int v) const {
+    v = __reduce_max_sync(~0u, v);
+    if (t.lane == 0) room[t.warp] = v;
+  }
+  __device__ __forceinline__ int get(const Team& t) const {
+    return __reduce_max_sync(~0u, room[t.lane]);
+  }
 };
 
 // f(piece, sum of the counts before it) for each piece whose count is not 0, by the
@@ -165,27 +179,29 @@ template <class Load, class RowOf>
 struct Released {
   const Pool& p;
   const Team& t;
+  const int me, all;  // this warp among those that share the pieces
   const int pieces, per_row, width;
   const Load& load;
   const RowOf& row_of;
   int first_ids[kPer], first_counts[kPer];
   unsigned first_owners[kPer];
 
-  __device__ __forceinline__ Released(const Pool& pool, const Team& team, int n_pieces,
-                                      int pieces_per_row, int table_width, const Load& l,
-                                      const RowOf& r)
-      : p(pool), t(team), pieces(n_pieces), per_row(pieces_per_row), width(table_width),
-        load(l), row_of(r) {
-    if (t.gwarp < pieces) fetch(t.gwarp, first_ids);
+  __device__ __forceinline__ Released(const Pool& pool, const Team& team, bool alone,
+                                      int n_pieces, int pieces_per_row, int table_width,
+                                      const Load& l, const RowOf& r)
+      : p(pool), t(team), me(alone ? team.warp : team.gwarp),
+        all(alone ? kWarpsPerCta : team.gwarps), pieces(n_pieces), per_row(pieces_per_row),
+        width(table_width), load(l), row_of(r) {
+    if (me < pieces) fetch(me, first_ids);
   }
   // the first piece's counts, loaded ahead of claim() or count()
   __device__ __forceinline__ void look_ahead() {
-    if (t.gwarp < pieces) counts_of(first_ids, first_counts);
+    if (me < pieces) counts_of(first_ids, first_counts);
   }
   // every released entry of a block out of references proposes itself
   __device__ __forceinline__ void claim() const {
 #pragma unroll 1
-    for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+    for (int i = me; i < pieces; i += all) {
       int ids[kPer], count[kPer];
       get(i, ids, count);
       const int at = place(i);
@@ -200,17 +216,39 @@ struct Released {
   // the blocks that each piece owns, into counts
   __device__ __forceinline__ void count(int* counts) {
 #pragma unroll 1
-    for (int i = t.gwarp; i < pieces; i += t.gwarps) {
+    for (int i = me; i < pieces; i += all) {
       int ids[kPer], count[kPer], n = 0;
       unsigned owners[kPer];
       get(i, ids, count);
       owners_of(i, count, owners);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) n += __popc(owners[e]);
-      if (i == t.gwarp)
+      if (i == me)
 #pragma unroll
         for (int e = 0; e < kPer; ++e) first_owners[e] = owners[e];
       if (t.lane == 0) counts[i] = n;
+    }
+  }
+  // Where every CTA has all pieces, one to a warp at most: how many blocks this one owns,
+  // and f(which of them, block) for each.
+  __device__ __forceinline__ int own() {
+    int n = 0;
+    if (me < pieces) {
+      owners_of(me, first_counts, first_owners);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) n += __popc(first_owners[e]);
+    }
+    return n;
+  }
+  template <class F>
+  __device__ __forceinline__ void each_owned(const F& f) const {
+    if (me >= pieces) return;
+    int at = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (first_owners[e] >> t.lane & 1)
+        f(at + __popc(first_owners[e] & ((1u << t.lane) - 1)), first_ids[e]);
+      at += __popc(first_owners[e]);
     }
   }
   // Pushes them from stack position `base` on; how many there are.  (Every CTA scans all
@@ -219,7 +257,7 @@ struct Released {
     return in_order(t, pieces, counts, sh, [&](int i, int64_t before) {
       int ids[kPer], count[kPer];
       unsigned owners[kPer];
-      if (i == t.gwarp) {
+      if (i == me) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
           ids[e] = first_ids[e];
@@ -259,7 +297,7 @@ struct Released {
       count[e] = in_pool(p, ids[e]) ? __ldcg(p.extra_refs_out + ids[e]) : 0;
   }
   __device__ __forceinline__ void get(int i, int (&ids)[kPer], int (&count)[kPer]) const {
-    if (i == t.gwarp) {
+    if (i == me) {
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         ids[e] = first_ids[e];
@@ -314,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   const Pool& q = p.pool;
   const int counted = *q.free_count;
   unsigned bad = 0;
+  int longest = 0;
+  const Largest of_lengths{scan.starts};
   for (int r = t.tid; r < R; r += kThreads) {
     const int s = __ldg(p.sources + r);
     const int64_t L = p.seq_lens[r];
@@ -322,9 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     s_src[r] = s < -1 || s >= R ? r : s;
     s_len[r] = fits ? (int)L : 0;
     s_uses[r] = 0;
+    longest = max(longest, s_len[r]);
   }
+  of_lengths.put(t, longest);
   if (lead && bad) flag_error(q.err, bad);
   __syncthreads();
+  const int filled = (of_lengths.get(t) + kBS - 1) / kBS;  // columns of the longest row
   for (int r = t.tid; r < R; r += kThreads)
     if (s_src[r] >= 0) atomicAdd(&s_uses[s_src[r]], 1);
   __syncthreads();
@@ -342,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   // ---- what needs only the inputs is loaded before the counts are settled, all of it
   // before any of it is looked at: this warp's first pieces of the old rows' tables and of
   // the released ones, and the new rows' partly filled last blocks (by every CTA for itself)
-  const int segs = (p.width + kSeg - 1) / kSeg;
+  const int segs = (max(filled, min(p.width, 1)) + kSeg - 1) / kSeg;  // (0: no columns)
   auto entries = [&](int s, int col0, int (&ids)[kPer]) {
     const int nb = (s_len[s] + kBS - 1) / kBS;
     const int32_t* row = p.tables + (int64_t)s * p.width;
@@ -361,8 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   }
   auto load = [&](int k, int col0, int (&out)[kPer]) { entries(s_gone[k], col0, out); };
   auto row_of = [&](int k) { return s_gone[k]; };
-  Released<decltype(load), decltype(row_of)> released(q, t, gone * segs, segs, p.width, load,
-                                                      row_of);
+  // Few pieces, and all CTAs in one cluster: every CTA finds and counts the freed blocks for
+  // itself, which saves two barriers and the ways to memory between them (4 rows of 63 blocks
+  // 13.2 -> 10.9 us; with 23 pieces of 256, 64 rows, it would be 13.9 -> 19.5).
+  const bool alone = p.cluster && gone * segs <= kFewPieces;
+  Released<decltype(load), decltype(row_of)> released(q, t, alone, gone * segs, segs, p.width,
+                                                      load, row_of);
 #pragma unroll 1
   for (int r = t.tid; r < R; r += kThreads) {
     const int s = s_src[r];
@@ -420,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     }
     if (t.lane == 0) p.row_need[r] = need;
   }
-  released.claim();
+  if (!alone || t.warp % t.ranks == t.rank) released.claim();
   t.sync();
   const int64_t height = stack_height(q, counted, lead && t.tid == 0);
   released.look_ahead();
@@ -450,20 +497,47 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
         s_tile[i] = p.tables[(int64_t)s * p.width + col];
     }
   };
-  if (t.rank * cols < p.width) read_tile(t.rank * cols);
-  int64_t freed = 0;
-  if (gone > 0) {  // (the same in every CTA)
-    released.count(p.counts);
+  if (t.rank * cols < filled) read_tile(t.rank * cols);
+  int64_t freed = 0, top;
+  int* s_fresh = s_gone;  // the freed blocks among those to be popped, in their order
+  if (alone) {            // (the same in every CTA)
+    const int mine = released.own();
+    if (t.lane == 0) scan.starts[t.warp] = mine;
+    cg::this_cluster().barrier_arrive();  // (the claims have been read)
+    __syncthreads();
+    const int n = scan.starts[t.lane];
+    freed = __reduce_add_sync(~0u, n);
+    top = min(height + freed, q.free_capacity);
+    const int64_t base = height + __reduce_add_sync(~0u, t.lane < t.warp ? n : 0);
+    released.each_owned([&](int at, int id) {
+      const int64_t pos = base + at;
+      if (pos >= q.free_capacity) {
+        if (lead) flag_error(q.err, PA_DEV_ERR_METADATA);
+        return;
+      }
+      if (lead) q.free_blocks[pos] = id;
+      if (top - 1 - pos < pairs) s_fresh[top - 1 - pos] = id;
+    });
+    __syncthreads();
+  } else {
+    if (gone > 0) {
+      released.count(p.counts);
+      t.sync();
+      freed = released.push(p.counts, height, scan);
+    }
     t.sync();
-    freed = released.push(p.counts, height, scan);
+    top = min(height + freed, q.free_capacity);
   }
-  t.sync();
   // ---- copies, in row order, onto blocks popped from the stack
-  const int64_t top = min(height + freed, q.free_capacity);
   for (int r = t.tid; r < R; r += kThreads) {
     const int id = s_part[r], k = s_uses[r];
     int fresh = -1;
-    if (k >= 0 && k < top) fresh = __ldcg(q.free_blocks + (top - 1 - k));
+    if (k >= 0 && k < top) {
+      if (alone && top - 1 - k >= height)
+        fresh = s_fresh[k];
+      else
+        fresh = __ldcg(q.free_blocks + (top - 1 - k));
+    }
     s_part[r] = fresh;
     if (lead && k >= 0) {
       if (k < top) {
@@ -490,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   }
   const bool in_place = p.tables == p.tables_out;
 #pragma unroll 1
-  for (int col0 = t.rank * cols; col0 < p.width; col0 += t.ranks * cols) {
+  for (int col0 = t.rank * cols; col0 < filled; col0 += t.ranks * cols) {
     if (col0 != t.rank * cols) {
       __syncthreads();
       read_tile(col0);
@@ -505,6 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
       p.tables_out[(int64_t)r * p.width + col] =
           fresh != -1 && col == s_len[s] / kBS ? fresh : s_tile[i];
     }
+  }
+  if (alone && lead) {
+    cg::this_cluster().barrier_wait();
+    released.each_owned([&](int, int id) { q.extra_refs_out[id] = 0; });
   }
 }
 
@@ -550,6 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
   const Pool& q = p.pool;
   const int counted = *q.free_count;
   unsigned bad = 0;
+  int longest = 0;
+  const Largest of_lengths{scan.starts};
   for (int r = t.tid; r < R; r += kThreads) {
     const int64_t L = p.seq_lens[r];
     const int k = __ldg(p.keep_lens + r), start = p.keep_start ? __ldg(p.keep_start + r) : 0;
@@ -560,12 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
     s_n[r] = ok && k >= 0 ? start + k : -1;
     s_start[r] = start;
     s_first[r] = s_end[r] = 0;
+    longest = max(longest, s_len[r]);
   }
+  of_lengths.put(t, longest);
   if (t.tid == 0) s_popped = 0;
   if (q.extra_refs != q.extra_refs_out) copy_refs(q, t);
   __syncthreads();
+  const int filled = (of_lengths.get(t) + kBS - 1) / kBS;  // columns of the longest row
   // a piece of a row's table, and its blocks' further holders before the call
-  const int segs = (p.width + kSeg - 1) / kSeg;
+  const int segs = (max(filled, min(p.width, 1)) + kSeg - 1) / kSeg;  // (0: no columns)
   const int pieces = R * segs;
   auto look_up = [&](int i, int (&ids)[kPer], int (&extra)[kPer]) {
     const int r = i / segs, col0 = i % segs * kSeg, had = (s_len[r] + kBS - 1) / kBS;
@@ -740,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
     }
   };
   auto row_of = [](int r) { return r; };
-  Released<decltype(load), decltype(row_of)> released(q, t, pieces, segs, p.width, load,
+  Released<decltype(load), decltype(row_of)> released(q, t, false, pieces, segs, p.width, load,
                                                       row_of);
   released.look_ahead();
   // ---- the moves: of a row that only loses its end none, unless its last block is
