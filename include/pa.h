@@ -699,7 +699,9 @@ pa_status pa_get_device_error(pa_stream_t stream, uint32_t* flags);
  * tokens       : device int32 [num_groups][K].
  * finished_out : device uint8 [num_groups][K], or NULL: 1 where the token is
  *                end_token, else 0; may be finished if K = W.
- * workspace    : device, pa_beam_select_workspace_size bytes, 256-byte aligned.
+ * workspace    : device, pa_beam_select_workspace_size bytes, 256-byte aligned (never
+ *                less for more groups, beams, tokens or picks: that of the largest step
+ *                serves all smaller ones).
  * W <= 64, K <= 128, vocab_size <= 2^24, num_groups * W < 2^24 (else
  * PA_ERR_UNSUPPORTED).
  */

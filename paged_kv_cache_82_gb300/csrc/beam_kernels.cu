@@ -1127,12 +1127,21 @@ cudaError_t launch_chunks(const BeamK& p, int per_thread, unsigned grid, cudaStr
 
 }  // namespace
 
+namespace {
+// chunks of a row by threads of `e` logits
+int64_t chunks_of(int vocab_size, int e) {
+  return ((int64_t)vocab_size + kBeamAlign - 1 + kBeamThreads * e - 1) / (kBeamThreads * e);
+}
+int64_t keys_bytes(int64_t pieces, int num_selected) {
+  return (pieces * num_selected * 8 + 255) / 256 * 256;
+}
+constexpr int kFewCtas = 16;  // with fewer, chunks are short
+}  // namespace
+
 BeamPlan make_beam_plan(pa_dtype dtype, int num_groups, int beam_width, int vocab_size,
                         int num_selected) {
   BeamPlan b{};
   const int64_t rows = (int64_t)num_groups * beam_width;
-  const int64_t span = (int64_t)vocab_size + kBeamAlign - 1;
-  auto chunks = [&](int e) { return (span + kBeamThreads * e - 1) / (kBeamThreads * e); };
   // the longest chunks (32 registers of logits a thread) that make 16 CTAs: fewer pieces are
   // sooner joined, and a CTA's loads are all in flight at once (one group of 4 beams of
   // 128256 bf16 logits 14.5 us in chunks of 2048, 10.0 in chunks of 16384; of 32000 9.4 and
@@ -1140,11 +1149,22 @@ BeamPlan make_beam_plan(pa_dtype dtype, int num_groups, int beam_width, int voca
   const int longest = dtype == PA_F32 ? 32 : 64;
   b.per_thread = 8;
   for (int e = longest; e > 8 && b.per_thread == 8; e /= 2)
-    if (e != 16 && rows * chunks(e) >= 16) b.per_thread = e;
-  b.chunks = (int)chunks(b.per_thread);
-  b.off_stats = (rows * b.chunks * num_selected * 8 + 255) / 256 * 256;
+    if (e != 16 && rows * chunks_of(vocab_size, e) >= kFewCtas) b.per_thread = e;
+  b.chunks = (int)chunks_of(vocab_size, b.per_thread);
+  b.off_stats = keys_bytes(rows * b.chunks, num_selected);
   b.bytes = b.off_stats + rows * b.chunks * 8;
   return b;
+}
+
+// Room for any type's plan (fp32 logits are cut into the most chunks) and for that of any
+// fewer rows or smaller vocabulary: of the short chunks, four to a long one, there are fewer
+// than 4 x 16.
+int64_t beam_workspace_bytes(int num_groups, int beam_width, int vocab_size, int num_selected) {
+  const int64_t rows = (int64_t)num_groups * beam_width;
+  const int64_t few = rows * chunks_of(vocab_size, 8), many = rows * chunks_of(vocab_size, 32);
+  const int64_t at_most = few < 4 * (kFewCtas - 1) ? few : 4 * (kFewCtas - 1);
+  const int64_t pieces = many > at_most ? many : at_most;
+  return keys_bytes(pieces, num_selected) + pieces * 8;
 }
 
 cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStream_t stream) {

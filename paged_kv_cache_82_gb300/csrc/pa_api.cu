@@ -1103,9 +1103,7 @@ pa_status pa_beam_select_workspace_size(int num_groups, int beam_width, int voca
   if (!bytes) return PA_ERR_INVALID_ARG;
   if (pa_status st = beam_size_status(num_groups, beam_width, vocab_size, num_selected))
     return st;
-  // (fp32 logits are cut into the most chunks)
-  *bytes =
-      (size_t)make_beam_plan(PA_F32, num_groups, beam_width, vocab_size, num_selected).bytes;
+  *bytes = (size_t)beam_workspace_bytes(num_groups, beam_width, vocab_size, num_selected);
   return PA_OK;
 }
 

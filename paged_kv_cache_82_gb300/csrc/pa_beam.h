@@ -20,6 +20,7 @@ struct BeamPlan {
 };
 BeamPlan make_beam_plan(pa_dtype dtype, int num_groups, int beam_width, int vocab_size,
                         int num_selected);
+int64_t beam_workspace_bytes(int num_groups, int beam_width, int vocab_size, int num_selected);
 struct BeamArgs {
   const void* logits;
   pa_dtype dtype;

@@ -152,6 +152,24 @@ def test_workspace_sizes():
             f(*bad)
 
 
+def test_workspace_of_the_largest_step_serves_smaller_ones():
+    """The size never falls as groups, beams, tokens or picks grow: the kernels' plan
+    changes from short chunks to long ones on the way."""
+    size = pa.pa_beam_select_workspace_size
+    for V in (1, 2041, 2042, 8185, 8186, 32000, 100_000, 128_256, 1 << 24):
+        for K in (1, 8, 128):
+            rows = [size(g, 1, V, K) for g in range(0, 70)]
+            assert rows == sorted(rows)
+            assert [size(1, w, V, K) for w in range(1, 65)] == rows[1:65]
+    for g in (1, 2, 3, 5, 15, 16, 40):
+        of_tokens = [size(g, 1, V, 4) for V in range(1, 140_000, 997)]
+        assert of_tokens == sorted(of_tokens)
+    rows = [pa.pa_fork_blocks_workspace_size(r, 300) for r in range(60)]
+    assert rows == sorted(rows)
+    rows = [pa.pa_compact_blocks_workspace_size(7, m) for m in range(0, 3000, 31)]
+    assert rows == sorted(rows)
+
+
 def test_binding_refuses_tensors_the_abi_would_misread():
     """Shapes, types, layouts and places are checked before a pointer is used (CPU
     tensors: the last check)."""
