@@ -20,7 +20,8 @@
 // between the passes: up to eight CTAs as one cluster, where more are needed a
 // cooperative grid (one CTA per SM at most).  Every CTA keeps the rows' sources and
 // lengths in shared memory and does the small scans over rows or pieces for itself.
-// Tables are walked as far as the longest row goes, not as wide as they are.
+// Tables are walked as far as the longest row goes, not as wide as they are.  (They are
+// read by ordinary loads: the call may write them, once nobody reads the old ones.)
 // What is left is latency: five or six barriers of 1.3 us each, the way of the writes
 // before them to L2 included, and one or two loads of 0.5 us between them.  64 forked
 // rows of up to 258 blocks 13 us, 1024 of up to 1026 29 us; 64 requests that keep 6
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int col = col0 + e * 32 + t.lane;
-      ids[e] = col < nb ? __ldg(row + col) : -1;
+      ids[e] = col < nb ? row[col] : -1;
     }
   };
   int ids[kPer];
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     const int s = s_src[r];
     int id = -1;
     if (s >= 0 && s_len[s] % kBS != 0) {
-      id = __ldg(p.tables + (int64_t)s * p.width + s_len[s] / kBS);
+      id = p.tables[(int64_t)s * p.width + s_len[s] / kBS];
       if (!in_pool(q, id)) {
         if (lead) flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
         id = -1;
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int col = col0 + e * 32 + t.lane;
-      ids[e] = s_n[r] >= 0 && col < had ? __ldg(p.tables + (int64_t)r * p.width + col) : -1;
+      ids[e] = s_n[r] >= 0 && col < had ? p.tables[(int64_t)r * p.width + col] : -1;
     }
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
               flag_error(q.err, PA_DEV_ERR_BLOCK_ID);
               fresh = -1;
             }
-            atomicAdd(q.extra_refs_out + __ldg(row + col), -1);
+            atomicAdd(q.extra_refs_out + row[col], -1);
           }
           p.fresh[(int64_t)r * p.width + col] = fresh;
         }
@@ -803,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int col = col0 + e * 32 + t.lane;
-      ids[e] = col >= left && col < had ? __ldg(row + col) : -1;
+      ids[e] = col >= left && col < had ? row[col] : -1;
     }
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
@@ -818,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int col = col0 + e * 32 + t.lane;
-      out[e] = col >= from && col < had ? __ldg(p.tables + at + col) : -1;
+      out[e] = col >= from && col < had ? p.tables[at + col] : -1;
       if (col >= from && col < left && __ldcg(p.fresh + at + col) == INT_MIN) out[e] = -1;
     }
   };
@@ -860,9 +861,9 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
       const int at = (at0 + j0 + e * 32 + t.lane) / kBS;
       from[e] = to[e] = 0;
       if (pos[e] >= 0) {
-        from[e] = __ldg(row + pos[e] / kBS);
+        from[e] = row[pos[e] / kBS];
         const int now = popped > 0 ? __ldcg(fresh + at) : INT_MIN;
-        to[e] = now == INT_MIN ? __ldg(row + at) : now;
+        to[e] = now == INT_MIN ? row[at] : now;
       }
     }
 #pragma unroll
@@ -891,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
         const bool on = col < blocks;
         now[e] = on && popped > 0 && n >= 0 && col >= s_first[r] ? __ldcg(p.fresh + at + col)
                                                                  : INT_MIN;
-        was[e] = on && !in_place ? __ldg(p.tables + at + col) : 0;
+        was[e] = on && !in_place ? p.tables[at + col] : 0;
       }
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
