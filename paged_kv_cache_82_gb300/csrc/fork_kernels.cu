@@ -17,15 +17,15 @@
 // Shape.  A few MB at most are read and written (tables, counts, lists), but by
 // passes that each need all of the one before: references, claims, owners counted,
 // owners pushed, tables.  So a call is one kernel whose CTAs meet at a barrier
-// between the passes: up to eight CTAs as one cluster, where more are needed a
-// cooperative grid (one CTA per SM at most).  Every CTA keeps the rows' sources and
+// between the passes: up to eight or sixteen CTAs as one cluster, where more are needed
+// a cooperative grid (one CTA per SM at most).  Every CTA keeps the rows' sources and
 // lengths in shared memory and does the small scans over rows or pieces for itself.
 // Tables are walked as far as the longest row goes, not as wide as they are.  (They are
 // read by ordinary loads: the call may write them, once nobody reads the old ones.)
 // What is left is latency: five or six barriers of 1.3 us each, the way of the writes
 // before them to L2 included, and one or two loads of 0.5 us between them.  64 forked
 // rows of up to 258 blocks 13 us, 1024 of up to 1026 29 us; 64 requests that keep 6
-// of their last 32 tokens 17 us, 32 prompts of 2K to 32K that keep a quarter 30 us.
+// of their last 32 tokens 15.5 us, 32 prompts of 2K to 32K that keep a quarter 30 us.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -39,7 +39,8 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarpsPerCta = kThreads / 32;
-constexpr int kMaxCluster = 8;  // the portable size
+constexpr int kMaxCluster = 8;   // the portable size
+constexpr int kBigCluster = 16;  // where the device can hold it
 constexpr int kSeg = 256;       // table entries (or listed tokens) of one piece: 8 per lane
 constexpr int kPer = kSeg / 32;
 constexpr int kFewPieces = 8;   // that every CTA of a cluster looks through for itself
@@ -917,11 +918,11 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(CompactK p) {
   }
 }
 
-// One kernel over `want` CTAs: a cluster of up to eight where these are not too few, or a
+// One kernel over `want` CTAs: a cluster of up to `team` where these are not too few, or a
 // cooperative grid of at most one CTA per SM.  p.cluster tells the kernel which.
 template <class P>
 cudaError_t launch_team(void (*kernel)(P), P& p, int64_t want, size_t smem, size_t max_smem,
-                        int num_sms, cudaStream_t stream) {
+                        int num_sms, int team, cudaStream_t stream) {
   // (always the largest step's limit: see launch_build_step)
   static_assert(sizeof(Scan) < 20 * 1024, "with dynamic shared memory, 48 KB by default");
   if (smem > 28 * 1024) {
@@ -930,9 +931,12 @@ cudaError_t launch_team(void (*kernel)(P), P& p, int64_t want, size_t smem, size
     if (e != cudaSuccess) return e;
   }
   // (a cluster's barriers are shorter: 64 rows of 258 entries 14.5 us by 8 CTAs of one,
-  // 18.4 by 9 of a grid; 64 rows of 513, compacted, 17.1 and 21.3 by 17)
+  // 18.4 by 9 of a grid; 64 rows of 513, compacted, 17.1 and 21.3 by 17.  16 CTAs where 9
+  // to 24 are wanted: those two 13.1 -> 12.8 and 16.7 -> 15.4, 2 rows of 8192 entries 25
+  // -> 16 us; where up to 48 or 80 are, a grid is faster, 31.8 against 36.4.)
   unsigned ctas = 1;
-  while (ctas < kMaxCluster && ctas < want) ctas *= 2;
+  const unsigned most = want > kMaxCluster ? team : kMaxCluster;
+  while (ctas < most && ctas < want) ctas *= 2;
   p.cluster = want <= 3 * kMaxCluster;
   if (!p.cluster) ctas = (unsigned)(want < num_sms ? want : num_sms);
   cudaLaunchConfig_t cfg{};
@@ -975,11 +979,41 @@ constexpr size_t kTileBytes = 64 * 1024;  // of a tile of the new tables, at mos
 
 }  // namespace
 
+int largest_team() {
+  int fewest = 1;
+  auto query = [&](auto kernel) {
+    const int smem = (int)(5 * kMaxForkRows * 4 + kTileBytes);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kBigCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kBigCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // (not this device, then)
+      n = 0;
+    }
+    fewest = n < fewest ? n : fewest;
+  };
+  query(fork_kernel);
+  query(compact_kernel);
+  return fewest > 0 ? kBigCluster : kMaxCluster;
+}
+
 int64_t fork_workspace_bytes(int num_rows, int max_blocks_per_seq) {
   return 4 * (num_rows + pieces_of(num_rows, max_blocks_per_seq));
 }
 
-cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, int team, cudaStream_t stream) {
   ForkK p{};
   p.sources = a.sources;
   p.num_rows = a.rows.num_rows;
@@ -1001,7 +1035,7 @@ cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, cudaStream_t stre
   while (p.cols_log2 > 3 && (int64_t)p.width <= want << (p.cols_log2 - 1)) --p.cols_log2;
   while (p.cols_log2 > 0 && ((size_t)R * 4) << p.cols_log2 > kTileBytes) --p.cols_log2;
   return launch_team(fork_kernel, p, want, (size_t)(5 + (1 << p.cols_log2)) * R * 4,
-                     (size_t)5 * kMaxForkRows * 4 + kTileBytes, num_sms, stream);
+                     (size_t)5 * kMaxForkRows * 4 + kTileBytes, num_sms, team, stream);
 }
 
 int64_t compact_workspace_bytes(int num_rows, int max_blocks_per_seq) {
@@ -1010,7 +1044,8 @@ int64_t compact_workspace_bytes(int num_rows, int max_blocks_per_seq) {
               (int64_t)num_rows * max_blocks_per_seq);
 }
 
-cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, int team,
+                                  cudaStream_t stream) {
   CompactK p{};
   p.keep = a.keep;
   p.max_keep = a.max_keep;
@@ -1032,7 +1067,8 @@ cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_
   p.masks = reinterpret_cast<uint32_t*>(p.counts + pieces_of(R, p.width));
   p.fresh = reinterpret_cast<int32_t*>(p.masks) + kPer * pieces_of(R, p.width);
   return launch_team(compact_kernel, p, ctas_for(R * p.width, R * (int64_t)p.max_keep, a.rows),
-                     (size_t)(5 * R * 4), (size_t)5 * kMaxForkRows * 4, num_sms, stream);
+                     (size_t)(5 * R * 4), (size_t)5 * kMaxForkRows * 4 + kTileBytes, num_sms, team,
+                     stream);
 }
 
 }  // namespace pa

@@ -22,6 +22,7 @@ struct DeviceInfo {
   bool ready = false;
   unsigned* err = nullptr;
   int num_sms = 0;
+  int team = 0;  // largest_team(), once it has been asked for
 };
 
 std::mutex g_mutex;
@@ -1004,6 +1005,16 @@ bool has_workspace(const void* workspace, size_t given, int64_t bytes) {
   return given >= (size_t)bytes && (bytes == 0 || (workspace && aligned(workspace, 256)));
 }
 
+// the device of a call on rows, with its largest team
+const DeviceInfo* rows_device_info() {
+  const DeviceInfo* d = device_info();
+  if (!d) return nullptr;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceInfo& known = g_dev[d - g_dev];
+  if (known.team == 0) known.team = largest_team();
+  return d;
+}
+
 // the checks of tables, counts and stack that pa_fork_blocks and pa_compact_blocks
 // share
 pa_status rows_status(const RowState& a, int block_size) {
@@ -1183,10 +1194,11 @@ pa_status pa_fork_blocks(const int32_t* sources, int num_rows,
   const Span outs[] = {{block_mapping, R * 16}, {num_pairs, 4}, {workspace, (size_t)need}};
   const Span ins[] = {{sources, R * 4}};
   if (rows_overlap(rows, outs, 3, ins, 1)) return PA_ERR_INVALID_ARG;
-  const DeviceInfo* di = device_info();
+  const DeviceInfo* di = rows_device_info();
   if (!di) return PA_ERR_CUDA;
   const ForkArgs a{rows, sources, block_mapping, num_pairs, workspace, di->err};
-  const cudaError_t e = launch_fork_blocks(a, di->num_sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_fork_blocks(a, di->num_sms, di->team,
+                                           reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -1251,11 +1263,12 @@ pa_status pa_compact_blocks(const int32_t* keep, int max_keep, const int32_t* ke
       {src_slots, slots}, {dst_slots, slots}, {num_moves, R * 4}, {workspace, (size_t)need}};
   const Span ins[] = {{keep, R * max_keep * 4}, {keep_lens, R * 4}, {keep_start, R * 4}};
   if (rows_overlap(rows, outs, 4, ins, 3)) return PA_ERR_INVALID_ARG;
-  const DeviceInfo* di = device_info();
+  const DeviceInfo* di = rows_device_info();
   if (!di) return PA_ERR_CUDA;
   const CompactArgs a{rows,      keep,      max_keep,  keep_lens, keep_start,
                       src_slots, dst_slots, num_moves, workspace, di->err};
-  const cudaError_t e = launch_compact_blocks(a, di->num_sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_compact_blocks(a, di->num_sms, di->team,
+                                              reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

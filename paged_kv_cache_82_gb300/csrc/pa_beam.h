@@ -68,7 +68,9 @@ struct ForkArgs {
   unsigned* err;
 };
 int64_t fork_workspace_bytes(int num_rows, int max_blocks_per_seq);
-cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, cudaStream_t stream);
+// CTAs of the largest cluster that the current device holds of both calls' kernels
+int largest_team();
+cudaError_t launch_fork_blocks(const ForkArgs& a, int num_sms, int team, cudaStream_t stream);
 
 struct CompactArgs {
   RowState rows;
@@ -83,7 +85,8 @@ struct CompactArgs {
   unsigned* err;
 };
 int64_t compact_workspace_bytes(int num_rows, int max_blocks_per_seq);
-cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, int team,
+                                  cudaStream_t stream);
 
 // ---- copies and moves of all layers (move_kernels.cu) --------------------------
 struct LayerCaches {
