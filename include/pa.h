@@ -677,8 +677,9 @@ pa_status pa_get_device_error(pa_stream_t stream, uint32_t* flags);
  *   score(w, t) = beam_scores[g][w] + x_t - log(sum over u of exp(x_u)),
  *   x = logits[g * W + w]
  * over tokens t < vocab_size.  The K largest scores of a group, largest first;
- * equal scores (to 64 bits): the lower beam first, within a beam the larger logit,
- * then the lower token.  Scores are compared in 64 bits, closer ones than fp32 sums
+ * equal scores (to 64 bits; beams of the same logits and beam score have them, wherever
+ * their rows start): the lower beam first, within a beam the larger logit, then the
+ * lower token.  Scores are compared in 64 bits, closer ones than fp32 sums
  * resolve by sums in two fp32 parts, and rounded to fp32 once.
  *
  * What is no candidate: a logit of -inf (a NaN logit counts as -inf, +inf as the

@@ -566,31 +566,71 @@ __device__ __forceinline__ void add_exp(Sum2& acc, float x, float mx, const floa
   acc.add(s * scale, s_lo * scale);
 }
 
-// A thread's part of a row: vectors first, first + step, ..., four at a time with the next
-// four on their way.  (Words one after another in a loop: few instructions to fetch for
-// code that is rarely run.)
-template <typename T>
-__device__ __noinline__ double precise_sum(const void* logits, int64_t at, int V, float mx,
-                                           const float2* table, int first, int step) {
+// How a row's vectors of kN logits, counted from its first one, can be loaded
+enum RowStart {
+  kOnVectors,  // it starts on 16 bytes: a load to a vector
+  kOnWords,    // on 4: four loads
+  kInWords,    // on 2: five, of which the vector is the inner halves
+};
+
+// The kN logits from i on (i < n) of a row of n, what lies past its end being -inf; kInWords:
+// those from i - 1 on and, in `fifth`, two more.
+template <typename T, int kStart>
+__device__ __forceinline__ uint4 load_from(const T* row, int i, int n, uint32_t& fifth) {
+  constexpr int kN = Pack<T>::kN;
+  if constexpr (kStart == kOnVectors) return load_vec<T>(row, i, n);
+  if constexpr (kStart == kInWords) --i;
+  if (i >= 0 && i + kN + (kStart == kInWords ? 2 : 0) <= n) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row + i);
+    if constexpr (kStart == kInWords) fifth = __ldg(w + 4);
+    return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+  }
+  if constexpr (kStart == kInWords) fifth = load_edge<T>(row, i + kN, n).x;
+  return load_edge<T>(row, i, n);
+}
+
+// A thread's part of a row: vectors first, first + step, ..., kAhead at a time with as many on
+// their way.  They are counted from the row's first logit, wherever in 16 bytes it lies:
+// which logits are added in which order must not depend on that, or beams that are copies
+// of each other would have sums that differ in their last bits.  (Words one after another
+// in a loop: few instructions to fetch for code that is rarely run.)
+template <typename T, int kStart>
+__device__ __noinline__ double sum_from(const T* x, int V, float mx, const float2* table,
+                                        int first, int step) {
   using P = Pack<T>;
-  const T* x = static_cast<const T*>(logits) + at;
+  // (Fewer where a fifth word takes registers: with four the join saves more of its own
+  // around the call, 0.6 us of every selection.  64 groups of 4 copies of 128255 bf16 logits
+  // 106.4 us with two, 108.4 with three; of 128256, all on vectors, 105.7.)
+  constexpr int kAhead = kStart == kInWords ? 2 : 4;
   const uint4 none = make_uint4(P::kNegInfs, P::kNegInfs, P::kNegInfs, P::kNegInfs);
   Sum2 acc[2];
-  int i = first * P::kN - (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  int i = first * P::kN;
   const int hop = step * P::kN;
-  uint4 next[4];
+  uint4 next[kAhead];
+  uint32_t fifth[kAhead];
+  auto fetch = [&] {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) next[u] = i + u * hop < V ? load_vec<T>(x, i + u * hop, V) : none;
+    for (int u = 0; u < kAhead; ++u) {
+      fifth[u] = P::kNegInfs;
+      next[u] = i + u * hop < V ? load_from<T, kStart>(x, i + u * hop, V, fifth[u]) : none;
+    }
+  };
+  fetch();
 #pragma unroll 1
   while (i < V) {
-    uint4 v[4];
+    uint4 v[kAhead];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = next[u];
-    i += 4 * hop;
+    for (int u = 0; u < kAhead; ++u) {
+      v[u] = next[u];
+      if (kStart == kInWords)
+        v[u] = make_uint4(__funnelshift_r(v[u].x, v[u].y, 16), __funnelshift_r(v[u].y, v[u].z, 16),
+                          __funnelshift_r(v[u].z, v[u].w, 16),
+                          __funnelshift_r(v[u].w, fifth[u], 16));
+    }
+    i += kAhead * hop;
+    fetch();
 #pragma unroll
-    for (int u = 0; u < 4; ++u) next[u] = i + u * hop < V ? load_vec<T>(x, i + u * hop, V) : none;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kAhead; ++u)
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -600,6 +640,17 @@ __device__ __noinline__ double precise_sum(const void* logits, int64_t at, int V
       }
   }
   return ((double)acc[0].hi + (double)acc[1].hi) + ((double)acc[0].lo + (double)acc[1].lo);
+}
+
+template <typename T>
+__device__ __forceinline__ double precise_sum(const void* logits, int64_t at, int V, float mx,
+                                              const float2* table, int first, int step) {
+  const T* x = static_cast<const T*>(logits) + at;
+  const unsigned start = (unsigned)(reinterpret_cast<uintptr_t>(x) & 15);
+  if constexpr (sizeof(T) == 2)
+    if (start & 2) return sum_from<T, kInWords>(x, V, mx, table, first, step);
+  return start ? sum_from<T, kOnWords>(x, V, mx, table, first, step)
+               : sum_from<T, kOnVectors>(x, V, mx, table, first, step);
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
