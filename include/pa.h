@@ -735,7 +735,8 @@ pa_status pa_beam_select_workspace_size(int num_groups, int beam_width, int voca
  *               it.  Copy the pairs' blocks (pa_copy_blocks_layers) before the next
  *               write or fork.  If the stack runs out, the remaining rows keep
  *               sharing (PA_DEV_ERR_NO_BLOCKS): do not write; a later call with
- *               s = r finds them again.
+ *               s = r finds them again.  What is popped is entered as it is, an id
+ *               outside [0, num_blocks) with PA_DEV_ERR_BLOCK_ID.
  *
  * sources          : device int32 [num_rows]; a value outside [-1, num_rows) sets
  *                    PA_DEV_ERR_METADATA and counts as r.

@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
   const int R = p.num_rows;
   int* s_src = sh;            // source of each new row (-1: none)
   int* s_uses = sh + R;       // new rows of each old row; then each new row's place among
-                              // the copies, -1: none
+                              // the copies, -1: none; then -1 too where the stack ran out
   int* s_len = sh + 2 * R;    // old rows' lengths
   int* s_part = sh + 3 * R;   // new rows' partly filled last block, -1: none; then that to
-                              // be copied; then the fresh block in its place
+                              // be copied; then what was popped in its place (any number)
   int* s_gone = sh + 4 * R;   // old rows nobody takes over, in order
   int* s_tile = sh + 5 * R;   // [rows][cols] of the new tables
   __shared__ Scan scan;
@@ -551,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
         flag_error(q.err, PA_DEV_ERR_NO_BLOCKS);
       }
     }
+    if (k >= top) s_uses[r] = -1;
   }
   __syncthreads();
   pairs = min(pairs, top);
@@ -576,10 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(ForkK p) {
     for (int i = t.tid; i < items; i += kThreads) {
       const int r = i >> p.cols_log2, col = col0 + (i & (cols - 1)), s = s_src[r];
       if (s < 0 || col >= (s_len[s] + kBS - 1) / kBS) continue;
-      const int fresh = s_part[r];
-      if (in_place && s == r && fresh == -1) continue;
+      const bool swapped = s_uses[r] >= 0;
+      if (in_place && s == r && !swapped) continue;
       p.tables_out[(int64_t)r * p.width + col] =
-          fresh != -1 && col == s_len[s] / kBS ? fresh : s_tile[i];
+          swapped && col == s_len[s] / kBS ? s_part[r] : s_tile[i];
     }
   }
   if (alone && lead) {
