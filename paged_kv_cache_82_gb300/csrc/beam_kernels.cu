@@ -1218,7 +1218,8 @@ int64_t beam_workspace_bytes(int num_groups, int beam_width, int vocab_size, int
   return keys_bytes(pieces, num_selected) + pieces * 8;
 }
 
-cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStream_t stream) {
+cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, int num_sms,
+                               cudaStream_t stream) {
   const int64_t candidates = (int64_t)a.beam_width * plan.chunks * a.num_selected;
   const unsigned stride = (candidates | 1) % 1000003 ? 1000003u : 1000033u;  // (primes)
   BeamK p{a, plan.chunks, stride, static_cast<uint64_t*>(a.workspace),
@@ -1233,7 +1234,7 @@ cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStre
   // CTAs to a group: one to 16K logits of a row, while all groups' fit the SMs twice (a
   // cluster costs half a microsecond to launch and tell that there is nothing to do)
   unsigned ctas = 1;
-  while (ctas < kMaxJoinCtas && (int64_t)a.num_groups * ctas * 2 <= 2 * 152 &&
+  while (ctas < kMaxJoinCtas && (int64_t)a.num_groups * ctas * 2 <= 2 * num_sms &&
          (int64_t)ctas * 2 * 16384 <= a.vocab_size)
     ctas *= 2;
   cudaLaunchConfig_t cfg{};

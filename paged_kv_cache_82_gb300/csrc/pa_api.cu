@@ -1159,8 +1159,10 @@ pa_status pa_beam_select(const void* logits, pa_dtype logits_dtype, int num_grou
   const BeamArgs a{logits,     logits_dtype, num_groups, beam_width,   vocab_size,
                    row_stride, beam_scores,  finished,   end_token,    num_selected,
                    scores,     parents,      tokens,     finished_out, workspace};
+  const DeviceInfo* di = device_info();
+  if (!di) return PA_ERR_CUDA;
   const cudaError_t e =
-      launch_beam_select(a, plan, reinterpret_cast<cudaStream_t>(stream));
+      launch_beam_select(a, plan, di->num_sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

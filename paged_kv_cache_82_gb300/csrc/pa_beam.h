@@ -36,7 +36,8 @@ struct BeamArgs {
   uint8_t* finished_out;
   void* workspace;
 };
-cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, cudaStream_t stream);
+cudaError_t launch_beam_select(const BeamArgs& a, const BeamPlan& plan, int num_sms,
+                               cudaStream_t stream);
 
 // ---- forked and compacted rows (fork_kernels.cu) ------------------------------
 // rows of one call: five ints each in one CTA's shared memory
