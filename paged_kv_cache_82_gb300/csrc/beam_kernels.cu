@@ -706,10 +706,12 @@ struct Group {
 
 static_assert(sizeof(Group) <= 47 * 1024, "a group in the default shared memory");
 
-// A candidate's score in 64 bits (0: below fp32's range, none)
+// A candidate's score in 64 bits (0: below fp32's range, none).  The fp32 numbers first, whose
+// sum is exact as a rule: where beams have the same sum, logits and beam scores that make
+// equal scores make equal numbers.
 __device__ __forceinline__ uint64_t score64(const Group& g, int w, float logit) {
   double s = (double)g.cum[w];
-  if (!g.done[w]) s += ((double)logit - (double)g.top[w]) + g.off[w];
+  if (!g.done[w]) s = (s + ((double)logit - (double)g.top[w])) + g.off[w];
   return (float)s != -INFINITY ? ordered(s) : 0;
 }
 

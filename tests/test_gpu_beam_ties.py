@@ -86,3 +86,24 @@ def test_copies_among_other_beams():
             parents, tokens = _want(x[:1], 2, 5)
             np.testing.assert_array_equal(p.cpu().numpy(), 2 * parents)
             np.testing.assert_array_equal(t.cpu().numpy(), tokens)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_equal_scores_by_logits_and_beam_scores(dtype):
+    """Copies whose beam scores lie as far apart as some of their logits do: a lower logit
+    of a better beam scores as much as a higher one of a worse beam, and the lower beam
+    comes first.  (Logits in steps of 1/4 and beam scores in steps of 1/2, so that their
+    sums are exact.)"""
+    rng = np.random.default_rng(6)
+    for V, W, K, pad in ((37, 4, 30, 1), (701, 5, 64, 0), (20011, 16, 128, 3)):
+        x = torch.from_numpy(np.round(rng.standard_normal((4, V)) * 10) / 4).to(DT[dtype])
+        cum = rng.choice([-0.5, -1.0, -1.5, -3.0], (4, W)).astype(np.float32)
+        s, p, t = pa.pa_beam_select(_copies(x, W, 0, pad), torch.from_numpy(cum).cuda(), K)
+        for g, row in enumerate(x.double().numpy()):
+            best = np.argsort(-row, kind="stable")[:K]
+            beam, tok = np.repeat(np.arange(W), len(best)), np.tile(best, W)
+            # (the row's log-sum is the same for all)
+            order = np.lexsort((tok, -row[tok], beam, -(cum[g][beam] + row[tok])))[:K]
+            np.testing.assert_array_equal(p[g].cpu().numpy(), g * W + beam[order])
+            np.testing.assert_array_equal(t[g].cpu().numpy(), tok[order])
+    assert pa.pa_get_device_error() == 0
