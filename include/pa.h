@@ -679,8 +679,12 @@ pa_status pa_get_device_error(pa_stream_t stream, uint32_t* flags);
  * over tokens t < vocab_size.  The K largest scores of a group, largest first;
  * equal scores (to 64 bits; beams of the same logits and beam score have them, wherever
  * their rows start): the lower beam first, within a beam the larger logit, then the
- * lower token.  Scores are compared in 64 bits, closer ones than fp32 sums
- * resolve by sums in two fp32 parts, and rounded to fp32 once.
+ * lower token.  Scores are 64-bit numbers with sums of fp32 exponentials, whose logs are off
+ * by 3.8e-6 at most.  Where two beams' scores lie too close for these to tell their order,
+ * the two rows' sums are taken again in two fp32 parts (right to about 1e-12), so that the
+ * picks do not depend on how a sum was rounded.  What is returned is rounded to fp32 once:
+ * off by 3.8e-6 and half a step at most, and, of rows not summed again, different
+ * in its last bits with the number of rows in the call and with where they start.
  *
  * What is no candidate: a logit of -inf (a NaN logit counts as -inf, +inf as the
  * largest fp32 number); any token of a beam whose beam_score is not finite (at the

@@ -23,13 +23,15 @@
 // resolve (kNear), the sums of those rows are taken again with exponentials in
 // two fp32 parts and the group is picked again (about one group in 2000 of
 // unlike beams with K = 4, one in 100 with K = 64, always for beams that are copies of
-// each other; such a call takes 33 to 40 us longer).
+// each other).  In 64 groups of 4 beams of 128256 bf16 logits that takes 36 us more
+// for one pair of such beams, 85 where all beams are copies.
 //
 // 64 groups of 4 beams of 128256 bf16 logits, a tenth of them finished, 59 MB: 22.0 us,
-// where reading them at a plain copy's rate takes 8.7.  The chunks take 15 of it: half of
-// the issue slots (nine instructions to a logit), the rest waiting for loads and for the
-// other warps of a CTA, four CTAs to an SM.  The join's chain of short steps takes 5, its
-// launch and end the rest.  32 groups of 8 beams of 50257 fp32 logits 22.0 us; one of 4
+// where reading them at a plain copy's rate takes 8.7 (other logits in each call, more in
+// all than the L2 holds; 20.5 where it holds them).  The chunks alone take 16 (3.7 TB/s):
+// half of the issue slots (nine instructions to a logit), the rest waiting for loads and for
+// the other warps of a CTA, four CTAs to an SM.  The join adds 6, a chain of short steps.
+// 32 groups of 8 beams of 50257 fp32 logits 22.1 us, 15 of them the chunks; one group of 4
 // beams of 32000 7.5 us.
 #include <cooperative_groups.h>
 #include <float.h>
